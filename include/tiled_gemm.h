@@ -330,6 +330,100 @@ int gemm_ex_host_ws(const void* A_host, const void* B_host, void* C_host, int64_
  */
 int64_t gemm_host_panel_rows(int64_t M);
 
+/* ------------------------------------------------- block-scaled 8-bit products
+ *
+ * A matrix in 8-bit floating point with one FP32 scale for each block of
+ * 128: the element (r, c) of the matrix is code(r, c) times the scale of the
+ * block it lies in.  Training and serving products take 8-bit operands this
+ * way; the functions below quantise a matrix and multiply two such
+ * matrices.  The pages have no counterpart.
+ */
+
+/* 8-bit types (one byte each, no infinity in e4m3). */
+typedef enum {
+    GEMM_F8_E4M3 = 0, /* 4 exponent, 3 mantissa bits, largest 448 */
+    GEMM_F8_E5M2 = 1  /* 5 exponent, 2 mantissa bits, largest 57344 */
+} gemm_f8_t;
+
+/* Block shapes, on the matrix as stored (R rows of C elements), and the
+   layout of their scales.  Blocks at the right and lower edge are partial. */
+typedef enum {
+    GEMM_FP8_ROW = 0, /* 1 x 128: scale of (r, c) at S[(c / 128) * lds + r], lds >= R */
+    GEMM_FP8_COL = 1, /* 128 x 1: scale of (r, c) at S[(r / 128) * lds + c], lds >= C */
+    GEMM_FP8_TILE = 2 /* 128 x 128: at S[(r / 128) * lds + c / 128], lds >= ceil(C / 128) */
+} gemm_fp8_block_t;
+
+/* A quantised matrix in device memory.  `data` is 16-byte aligned and its
+   row pitch `ld` (bytes, at least the columns) a multiple of 16; the bytes
+   between a row's end and the next are never used. */
+typedef struct {
+    const void* data;
+    int64_t ld;
+    gemm_f8_t type;
+    gemm_fp8_block_t block;
+    const float* scale;
+    int64_t scale_ld; /* the lds of the block shape */
+    gemm_op_t op;     /* products only: as stored, or its transpose */
+} gemm_fp8_matrix_t;
+
+/*
+ * gemm_fp8_quantize -- quantise X (rows x cols, row pitch ldx elements, F32,
+ * F16 or BF16) into Q (row pitch ldq, see gemm_fp8_matrix_t) and its scales.
+ *
+ * For each block: amax = the largest finite |x|; s = max(amax * (1 / F),
+ * 2^-126) with F the type's largest value, or 1 where amax is 0; each code
+ * is x * (1 / s) rounded to nearest-even.  1 / F, 1 / s and both products
+ * are rounded to FP32, so the result is determined bit for bit.  A NaN or an
+ * infinity becomes the 8-bit NaN and does not affect its block's scale.
+ *
+ * X needs element alignment only (16-byte aligned rows are read faster).
+ * rows == 0 or cols == 0 is a no-op.  Returns GEMM_OK,
+ * GEMM_ERR_INVALID_VALUE (null pointer, negative size or one above
+ * GEMM_MAX_DIM, a pitch below its row, unknown enum), GEMM_ERR_UNSUPPORTED
+ * (Q or ldq not multiples of 16) or GEMM_ERR_CUDA.
+ */
+int gemm_fp8_quantize(const void* X, int64_t ldx, int64_t rows, int64_t cols,
+                      gemm_dtype_t in_dtype, gemm_f8_t f8, gemm_fp8_block_t block, void* Q,
+                      int64_t ldq, float* S, int64_t lds, void* stream);
+
+/*
+ * gemm_fp8_quantize_pair -- gemm_fp8_quantize in both vector shapes from one
+ * read of X: GEMM_FP8_ROW into Q_row, S_row and GEMM_FP8_COL into Q_col,
+ * S_col.  A training step needs both: the forward product and the weight
+ * gradient contract over different axes of a layer's input.
+ */
+int gemm_fp8_quantize_pair(const void* X, int64_t ldx, int64_t rows, int64_t cols,
+                           gemm_dtype_t in_dtype, gemm_f8_t f8, void* Q_row, int64_t ldq_row,
+                           float* S_row, int64_t lds_row, void* Q_col, int64_t ldq_col,
+                           float* S_col, int64_t lds_col, void* stream);
+
+/*
+ * gemm_fp8 -- C = alpha * op(A) @ op(B) + beta * C on quantised matrices.
+ *
+ * op(A) is M x K, op(B) is K x N and C is M x N with row pitch ldc elements,
+ * as gemm_general: A is stored M x K (GEMM_OP_N) or K x M (GEMM_OP_T), B
+ * K x N (GEMM_OP_N) or N x K (GEMM_OP_T).  With W stored out x in and
+ * 128 x 128 blocks, the same bytes serve x @ W^T (op(B) = GEMM_OP_T) and
+ * the input gradient dy @ W (GEMM_OP_N); the weight gradient dy^T @ x takes
+ * both operands with GEMM_FP8_COL blocks, A as GEMM_OP_T.
+ *
+ * Vector blocks must run along K: GEMM_FP8_ROW where the stored rows run
+ * along K (A as GEMM_OP_N, B as GEMM_OP_T), GEMM_FP8_COL otherwise.  The
+ * types of A and B may differ.  Products are accumulated in FP32 within a
+ * block of 128 of K, multiplied by both scales in FP32 and summed in FP32;
+ * alpha and beta are applied in FP32 before the one rounding to out_dtype.
+ * beta == 0 never reads C.  C needs element alignment only and must not
+ * overlap A or B.  K == 0 gives beta * C (zeros for beta == 0).  The result
+ * is identical run to run.
+ *
+ * Returns GEMM_OK, GEMM_ERR_INVALID_VALUE (null pointer where data is
+ * needed, bad size, pitch or enum), GEMM_ERR_UNSUPPORTED (an operand's data
+ * or ld not a multiple of 16, vector blocks across K) or GEMM_ERR_CUDA.
+ */
+int gemm_fp8(const gemm_fp8_matrix_t* A, const gemm_fp8_matrix_t* B, void* C, int64_t ldc,
+             int64_t M, int64_t N, int64_t K, float alpha, float beta, gemm_dtype_t out_dtype,
+             void* stream);
+
 /*
  * gemm_device_status -- synchronize `stream`, then read and clear the status
  * word of the current device.  Returns GEMM_OK, GEMM_ERR_TIMEOUT if a

@@ -6,7 +6,7 @@ its ctypes binding plus the seeded input generator.  The library is loaded
 on first use and there is no CPU fallback.
 """
 from .binding import (  # noqa: F401
-    BF16, F16, F32, KERNEL_NAMES, KERNELS, GemmError, addmm, error_string, gemm, gemm_debug_config,
+    BF16, E4M3, E5M2, F16, F32, Fp8Matrix, KERNEL_NAMES, KERNELS, GemmError, addmm, error_string, gemm, gemm_debug_config,
     gemm_device_status, gemm_error_string, gemm_ex, gemm_ex_host, gemm_ex_host_ws, gemm_ex_kernel,
     gemm_ex_ws, gemm_host_panel_rows,
     gemm_general, gemm_launch_count, gemm_traffic_model, gemm_workspace_size, matmul_ws,
@@ -14,4 +14,6 @@ from .binding import (  # noqa: F401
     gemm_ws_split_count,
     header_functions, library_path,
     load_library, matmul, matmul_splitk,
+    gemm_fp8, gemm_fp8_quantize, gemm_fp8_quantize_pair, matmul_fp8, quantize_fp8,
+    quantize_fp8_pair,
 )

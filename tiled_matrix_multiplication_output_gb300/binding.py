@@ -11,6 +11,7 @@ call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -48,6 +49,13 @@ _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 
+class Fp8Matrix(ctypes.Structure):
+    """gemm_fp8_matrix_t: a quantised matrix in device memory."""
+
+    _fields_ = [("data", _p), ("ld", _i64), ("type", _int), ("block", _int), ("scale", _p),
+                ("scale_ld", _i64), ("op", _int)]
+
+
 _SIGNATURES = {
     "gemm": ([_p, _p, _p, _i64, _i64, _i64, _int, _int, _p], _int),
     "gemm_ex": ([_p, _p, _p, _i64, _i64, _i64, _int, _int, _int, _p], _int),
@@ -67,6 +75,11 @@ _SIGNATURES = {
     "gemm_splitk": ([_p, _p, _p, _i64, _i64, _i64, _int, _int, _int, _int, _p, ctypes.c_size_t,
                      _p], _int),
     "gemm_splitk_noalloc": ([_p, _p, _p, _i64, _i64, _i64, _int, _int, _int, _int, _p], _int),
+    "gemm_fp8_quantize": ([_p, _i64, _i64, _i64, _int, _int, _int, _p, _i64, _p, _i64, _p], _int),
+    "gemm_fp8_quantize_pair": ([_p, _i64, _i64, _i64, _int, _int, _p, _i64, _p, _i64, _p, _i64,
+                                _p, _i64, _p], _int),
+    "gemm_fp8": ([ctypes.POINTER(Fp8Matrix), ctypes.POINTER(Fp8Matrix), _p, _i64, _i64, _i64,
+                  _i64, ctypes.c_float, ctypes.c_float, _int, _p], _int),
     "gemm_device_status": ([_p], _int),
     "gemm_debug_config": ([_i64, _int], _int),
     "gemm_launch_count": ([], ctypes.c_uint64),
@@ -230,6 +243,24 @@ def matmul_splitk(A, B, splits: int, out_dtype=None, workspace=None, stream=None
     return C
 
 
+def gemm_fp8_quantize(X, ldx, rows, cols, in_dtype, f8, block, Q, ldq, S, lds,
+                      stream=None) -> int:
+    return load_library().gemm_fp8_quantize(X, ldx, rows, cols, in_dtype, f8, block, Q, ldq, S,
+                                            lds, stream)
+
+
+def gemm_fp8_quantize_pair(X, ldx, rows, cols, in_dtype, f8, Q_row, ldq_row, S_row, lds_row,
+                           Q_col, ldq_col, S_col, lds_col, stream=None) -> int:
+    return load_library().gemm_fp8_quantize_pair(X, ldx, rows, cols, in_dtype, f8, Q_row, ldq_row,
+                                                 S_row, lds_row, Q_col, ldq_col, S_col, lds_col,
+                                                 stream)
+
+
+def gemm_fp8(A, B, C, ldc, M, N, K, alpha, beta, out_dtype, stream=None) -> int:
+    """A and B are Fp8Matrix structures (or None)."""
+    return load_library().gemm_fp8(A, B, C, ldc, M, N, K, alpha, beta, out_dtype, stream)
+
+
 def gemm_device_status(stream=None) -> int:
     return load_library().gemm_device_status(stream)
 
@@ -360,4 +391,176 @@ def matmul(A, B, out_dtype=None, kernel: str | int = "auto", out=None, stream=No
                         dtype_code(A.dtype), F32, dtype_code(odt), kid, _stream_handle(stream))
     if rc != OK:
         raise GemmError(rc, "gemm_ex_kernel")
+    return out
+
+
+# ------------------------------------------------- block-scaled 8-bit products
+
+E4M3, E5M2 = 0, 1
+F8_CODES = {"e4m3": E4M3, "e5m2": E5M2}
+FP8_BLOCKS = {"row": 0, "col": 1, "tile": 2}
+
+
+def _out_dtype(out_dtype):
+    torch = _torch()
+    if out_dtype is None:
+        return torch.float32
+    return torch_dtype(out_dtype) if isinstance(out_dtype, (str, int)) else out_dtype
+
+
+def _f8_code(dtype) -> int:
+    torch = _torch()
+    if isinstance(dtype, str):
+        if dtype not in F8_CODES:
+            raise ValueError(f"unknown 8-bit type {dtype!r}")
+        return F8_CODES[dtype]
+    if dtype is torch.float8_e4m3fn:
+        return E4M3
+    if dtype is torch.float8_e5m2:
+        return E5M2
+    raise TypeError(f"{dtype} is not an 8-bit floating-point type")
+
+
+def _on_stream(stream):
+    """A context in which PyTorch allocates for `stream` (memory freed later
+    is then reused in that stream's order only)."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _check_matrix(x, what):
+    torch = _torch()
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is not on the current device")
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{what}'s rows must be contiguous")
+    if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+        raise ValueError(f"{what}'s rows must not overlap")
+
+
+def _pitch(x) -> int:
+    """Elements from one row of a 2-D tensor to the next (a single row has none of its own)."""
+    return x.stride(0) if x.shape[0] > 1 else -(-x.shape[1] // 16) * 16
+
+
+def _fp8_empty(rows, cols, f8, block, device):
+    """Uninitialised codes with a row pitch of a multiple of 16, and scales."""
+    torch = _torch()
+    q = torch.empty((rows, -(-cols // 16) * 16), device=device,
+                    dtype=torch.float8_e4m3fn if f8 == E4M3 else torch.float8_e5m2)[:, :cols]
+    rb, cb = -(-rows // 128), -(-cols // 128)
+    shape = ((cb, rows), (rb, cols), (rb, cb))[block]
+    return q, torch.empty(shape, dtype=torch.float32, device=device)
+
+
+def _quantize_input(x):
+    torch = _torch()
+    _check_matrix(x, "x")
+    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise TypeError("x must be FP32, FP16 or BF16")
+
+
+def quantize_fp8(x, block: str = "row", dtype="e4m3", stream=None):
+    """Quantise a 2-D CUDA tensor (FP32, FP16 or BF16; rows contiguous, any
+    row stride) into 8-bit floating point with one FP32 scale for each block
+    of 128.
+
+    block: "row" (1 x 128; scales of shape (ceil(cols / 128), rows)), "col"
+    (128 x 1; (ceil(rows / 128), cols)) or "tile" (128 x 128;
+    (ceil(rows / 128), ceil(cols / 128))).  dtype: "e4m3" or "e5m2".  Returns
+    (codes, scales): an element is its code times its block's scale.  The
+    codes are a (rows, cols) view of rows padded to 16 bytes, the form
+    matmul_fp8 takes.  The exact definition is gemm_fp8_quantize's.
+    """
+    _quantize_input(x)
+    if block not in FP8_BLOCKS:
+        raise ValueError(f"unknown block shape {block!r}")
+    rows, cols = x.shape
+    f8, b = _f8_code(dtype), FP8_BLOCKS[block]
+    with _on_stream(stream):
+        q, s = _fp8_empty(rows, cols, f8, b, x.device)
+    rc = gemm_fp8_quantize(x.data_ptr(), _pitch(x), rows, cols, dtype_code(x.dtype), f8, b,
+                           q.data_ptr(), _pitch(q), s.data_ptr(), s.shape[1],
+                           _stream_handle(stream))
+    if rc != OK:
+        raise GemmError(rc, "gemm_fp8_quantize")
+    return q, s
+
+
+def quantize_fp8_pair(x, dtype="e4m3", stream=None):
+    """quantize_fp8 with "row" and with "col" blocks from one read of x:
+    ((codes, scales), (codes, scales))."""
+    _quantize_input(x)
+    rows, cols = x.shape
+    f8 = _f8_code(dtype)
+    with _on_stream(stream):
+        qr, sr = _fp8_empty(rows, cols, f8, 0, x.device)
+        qc, sc = _fp8_empty(rows, cols, f8, 1, x.device)
+    rc = gemm_fp8_quantize_pair(x.data_ptr(), _pitch(x), rows, cols, dtype_code(x.dtype), f8,
+                                qr.data_ptr(), _pitch(qr), sr.data_ptr(), sr.shape[1],
+                                qc.data_ptr(), _pitch(qc), sc.data_ptr(), sc.shape[1],
+                                _stream_handle(stream))
+    if rc != OK:
+        raise GemmError(rc, "gemm_fp8_quantize_pair")
+    return (qr, sr), (qc, sc)
+
+
+def _fp8_operand(q, s, op, k_rows, what):
+    """The Fp8Matrix of codes q and scales s; k_rows: q's rows run along K."""
+    torch = _torch()
+    _check_matrix(q, what)
+    if s.dtype is not torch.float32 or not s.is_cuda or s.dim() != 2 or not s.is_contiguous():
+        raise ValueError(f"{what}'s scales must be a contiguous 2-D FP32 CUDA tensor")
+    rows, cols = q.shape
+    rb, cb = (rows + 127) // 128, (cols + 127) // 128
+    shape = tuple(s.shape)
+    if shape == ((cb, rows) if k_rows else (rb, cols)):
+        block = 0 if k_rows else 1
+    elif shape == (rb, cb):
+        block = 2
+    else:
+        raise ValueError(f"{what}'s scales have shape {shape}: expected "
+                         f"{(cb, rows) if k_rows else (rb, cols)} (a vector along the "
+                         f"contraction) or {(rb, cb)} (128 x 128 blocks)")
+    return Fp8Matrix(q.data_ptr(), _pitch(q), _f8_code(q.dtype), block, s.data_ptr(), shape[1],
+                     OPS[op])
+
+
+def matmul_fp8(a, a_scale, b, b_scale, op_a="n", op_b="t", out_dtype=None, out=None, alpha=1.0,
+               beta=0.0, stream=None):
+    """C = alpha * op(A) @ op(B) + beta * C on quantised operands, as
+    quantize_fp8 gives them (FP32 accumulation; the scales are applied for
+    each 128 of the contraction).
+
+    op "n" takes an operand as stored, "t" its transpose; the defaults are
+    x @ W^T with W stored out x in.  A scale vector must run along the
+    contraction: "row" blocks where the stored rows do, "col" blocks
+    otherwise; "tile" blocks serve both.  `out` may supply C (rows
+    contiguous, any row stride); beta != 0 needs it.  out_dtype defaults to
+    FP32, or to out's type.  Returns C without synchronizing."""
+    torch = _torch()
+    if op_a not in OPS or op_b not in OPS:
+        raise ValueError("op_a and op_b are \"n\" or \"t\"")
+    A = _fp8_operand(a, a_scale, op_a, op_a == "n", "a")
+    B = _fp8_operand(b, b_scale, op_b, op_b == "t", "b")
+    M, K = (a.shape[1], a.shape[0]) if op_a == "t" else a.shape
+    K2, N = (b.shape[1], b.shape[0]) if op_b == "t" else b.shape
+    if K != K2:
+        raise ValueError("inner dimensions differ")
+    if out is None:
+        if beta != 0.0:
+            raise ValueError("beta != 0 needs out")
+        with _on_stream(stream):
+            out = torch.empty((M, N), dtype=_out_dtype(out_dtype), device=a.device)
+    else:
+        _check_matrix(out, "out")
+        if tuple(out.shape) != (M, N) or (out_dtype is not None and
+                                          out.dtype != _out_dtype(out_dtype)):
+            raise ValueError("out must be an (M, N) tensor of the output dtype")
+    rc = gemm_fp8(ctypes.byref(A), ctypes.byref(B), out.data_ptr(),
+                  out.stride(0) if M > 1 else N, M, N, K, alpha, beta, dtype_code(out.dtype),
+                  _stream_handle(stream))
+    if rc != OK:
+        raise GemmError(rc, "gemm_fp8")
     return out

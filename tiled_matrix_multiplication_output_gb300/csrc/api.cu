@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "device.h"
 #include "launch.h"
 #include "tc_params.h"
 #include "tiled_gemm.h"
@@ -24,15 +25,11 @@ std::atomic<long long> g_wait_budget{kDefaultWaitBudget};
 std::atomic<unsigned long long> g_launches{0};
 std::atomic<int> g_fault_skip_kblock{-1};
 
-struct DeviceInfo {
-    int num_sms = 0;
-    int* status = nullptr;
-    bool ready = false;
-};
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
-// Set-up of the current device, once: SM count and the status word address.
+}  // namespace
+
 cudaError_t device_info(DeviceInfo* out)
 {
     int dev = 0;
@@ -58,9 +55,13 @@ cudaError_t device_info(DeviceInfo* out)
     return cudaSuccess;
 }
 
+long long wait_budget_cycles() { return g_wait_budget.load(); }
+int fault_skip_kblock() { return g_fault_skip_kblock.load(); }
+
+namespace {
+
 bool valid_dtype(int dt) { return dt == GEMM_F32 || dt == GEMM_F16 || dt == GEMM_BF16; }
 int dt_size(int dt) { return dt == GEMM_F32 ? 4 : 2; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Host-side argument check shared by every entry point.
 int validate(const void* A, const void* B, const void* C, int64_t M, int64_t N, int64_t K,

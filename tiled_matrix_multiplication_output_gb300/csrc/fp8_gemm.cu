@@ -1,0 +1,184 @@
+// Host side of the block-scaled 8-bit product: tensor maps, the choice of
+// kernel, and the product over an empty K.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+#include <type_traits>
+
+#include "fp8_gemm.cuh"
+#include "launch.h"
+
+namespace tmmo {
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+// The stored matrix of an operand (outer x K, or K x outer when MN-major) in
+// boxes of 128 x box_rows bytes, 128-byte swizzle.  The row pitch is a
+// multiple of 16 bytes; the matrix itself may end anywhere.
+bool encode_operand(CUtensorMap* map, const Fp8Operand& o, int64_t outer, int64_t K,
+                    uint32_t box_outer)
+{
+    auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+    if (!fn)
+        return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(o.mn_major ? outer : K),
+                                static_cast<cuuint64_t>(o.mn_major ? K : outer)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.ld)};
+    const cuuint32_t box[2] = {128, o.mn_major ? static_cast<cuuint32_t>(F8_BK) : box_outer};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(o.data), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int out_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+template <int CG, int BN, int STAGES, bool COLV>
+cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
+{
+    using L = Fp8Layout<CG, BN, STAGES>;
+    auto kern = fp8_gemm_kernel<CG, BN, STAGES, COLV>;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess)
+        return err;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    static int max_units[kMaxDevices] = {};
+    static std::mutex mu;
+    int units_cap = 0;
+    {
+        std::lock_guard<std::mutex> g(mu);
+        if (max_units[dev] == 0) {
+            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       L::SMEM_ALLOC);
+            if (err != cudaSuccess)
+                return err;
+            int cap = l.num_sms;
+            if (CG == 2) {
+                cudaLaunchConfig_t cfg{};
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = 2;
+                attr[0].val.clusterDim.y = 1;
+                attr[0].val.clusterDim.z = 1;
+                cfg.gridDim = dim3(2 * std::max(1, l.num_sms / 2), 1, 1);
+                cfg.blockDim = dim3(F8_THREADS, 1, 1);
+                cfg.dynamicSmemBytes = L::SMEM_ALLOC;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                int clusters = 0;
+                err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+                if (err != cudaSuccess)
+                    return err;
+                cap = std::max(1, clusters);
+            }
+            max_units[dev] = cap;
+        }
+        units_cap = max_units[dev];
+    }
+    CUtensorMap ta, tb;
+    if (!encode_operand(&ta, l.a, l.M, l.K, 128) || !encode_operand(&tb, l.b, l.N, l.K, 128))
+        return cudaErrorNotSupported;
+    Fp8Params p{};
+    p.M = l.M;
+    p.N = l.N;
+    p.K = l.K;
+    p.tiles_m = (l.M + TC_BM * CG - 1) / (TC_BM * CG);
+    p.tiles_n = (l.N + BN - 1) / BN;
+    const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+    if (tiles > 0x3fffffffLL)
+        return cudaErrorNotSupported;
+    p.num_tiles = static_cast<int>(tiles);
+    p.k_blocks = (l.K + F8_BK - 1) / F8_BK;
+    p.group_m = 8;
+    p.idesc = fp8_idesc(l.a.type, l.b.type, TC_BM * CG, BN, l.a.mn_major, l.b.mn_major);
+    p.a_mn = l.a.mn_major;
+    p.b_mn = l.b.mn_major;
+    p.sa = l.a.scale;
+    p.sa_k = l.a.stride_k;
+    p.sa_o = l.a.stride_o;
+    p.sa_shift = l.a.shift;
+    p.sb = l.b.scale;
+    p.sb_k = l.b.stride_k;
+    p.sb_o = l.b.stride_o;
+    p.sb_shift = l.b.shift;
+    p.C = l.C;
+    p.ldc = l.ldc;
+    p.out_dtype = l.out_dtype;
+    p.vec_out = (reinterpret_cast<uintptr_t>(l.C) & 15u) == 0 &&
+                (l.ldc * out_bytes(l.out_dtype)) % 16 == 0;
+    p.alpha = l.alpha;
+    p.beta = l.beta;
+    p.status = l.status;
+    p.wait_budget = l.wait_budget;
+    p.fault_skip_kblock = l.fault_skip_kblock;
+    const int units = std::max(1, std::min(p.num_tiles, units_cap));
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(units * CG, 1, 1);
+    cfg.blockDim = dim3(F8_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = L::SMEM_ALLOC;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    note_launch();
+    err = cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <int CG, int BN, int STAGES>
+cudaError_t launch_scales(const Fp8Launch& l, cudaStream_t stream)
+{
+    return l.b.shift == 0 ? launch_tiles<CG, BN, STAGES, true>(l, stream)
+                          : launch_tiles<CG, BN, STAGES, false>(l, stream);
+}
+
+template <typename OutT>
+__global__ void scale_rows_kernel(OutT* C, long long ldc, int M, int N, float beta)
+{
+    const long long total = static_cast<long long>(M) * N;
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+        OutT* c = C + (i / N) * ldc + i % N;
+        *c = fp8_to_out<OutT>(beta != 0.0f ? beta * out_to_f32(*c) : 0.0f);
+    }
+}
+
+}  // namespace
+
+cudaError_t fp8_empty_launch(const Fp8Launch& l, cudaStream_t stream)
+{
+    const unsigned grid = static_cast<unsigned>(
+        std::min<long long>((static_cast<long long>(l.M) * l.N + 255) / 256, 8LL * l.num_sms));
+    note_launch();
+    if (l.out_dtype == DT_F32)
+        scale_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<float*>(l.C), l.ldc, l.M, l.N, l.beta);
+    else if (l.out_dtype == DT_F16)
+        scale_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<__half*>(l.C), l.ldc, l.M, l.N, l.beta);
+    else
+        scale_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<__nv_bfloat16*>(l.C), l.ldc, l.M, l.N,
+                                                    l.beta);
+    return cudaGetLastError();
+}
+
+cudaError_t fp8_gemm_launch(const Fp8Launch& l, cudaStream_t stream)
+{
+    // Pair tiles of 256 x 256 once they fill half of the CTA pairs; below
+    // that, four times as many 128 x 128 tiles keep more SMs busy.
+    const long long pair_tiles =
+        static_cast<long long>((l.M + 255) / 256) * ((l.N + 255) / 256);
+    if (pair_tiles * 4 >= l.num_sms)
+        return launch_scales<2, 256, 5>(l, stream);
+    return launch_scales<1, 128, 5>(l, stream);
+}
+
+}  // namespace tmmo

@@ -1,0 +1,505 @@
+// Block-scaled 8-bit matrix product on the 5th-generation tensor cores:
+//
+//   C[m, n] = alpha * sum_kb sA[m, kb] * sB[n, kb] * P_kb[m, n] + beta * C[m, n],
+//   P_kb[m, n] = sum over the 128 k of block kb of a[m, k] * b[n, k],
+//
+// a and b in e4m3 or e5m2, the scales in FP32, one for each outer index (or
+// for 128 of them) and K block.
+//
+// The scales are arbitrary FP32 numbers, so a K block's product has to be
+// scaled before it joins the sum: P_kb is accumulated by the tensor core
+// (FP32, in tensor memory), read back, and added to the running sum in
+// registers, FP32, as acc += (sA * sB) * P_kb.  What bounds the kernel is
+// the tensor pipe as long as that "promotion" keeps up: for a 128 x 256 half
+// of a CTA pair's tile a K block is 512 cycles of MMA, against 128 x 256
+// values that have to cross from tensor memory and one multiply-add each --
+// 256 cycles of the FP32 pipe.  So:
+//
+//   * eight epilogue warps (two per SM partition, so that one's loads from
+//     tensor memory overlap the other's arithmetic) hold the running sums:
+//     128 registers a thread for 256-column tiles.  setmaxnreg moves
+//     registers from the copying and issuing warps to them;
+//   * several partial buffers in tensor memory (512 columns in all), so the
+//     tensor core works on the next K blocks while one is promoted;
+//   * multiply-adds in pairs (fma.rn.f32x2), half the instructions;
+//   * scales are fetched two K blocks ahead into registers; a scale vector
+//     along the columns is staged through a private slice of shared memory
+//     per warp and read back by broadcast.
+//
+// One K step is one 128-byte swizzle row: a 128 x 128 block of either
+// operand is 16 KiB, one TMA box, whether K or the outer axis is contiguous
+// in memory (K-major or MN-major operand), so the same stored bytes serve
+// the forward product and both gradients.  TMA fills what lies outside the
+// matrix with zeros, which add nothing.
+//
+// CG = 2 runs on a CTA pair (M = 256 MMAs, each CTA loading its 128 rows of A
+// and half of B's columns), as tc_gemm_kernel does.  Every wait is bounded in
+// the same way.
+#pragma once
+
+#include <type_traits>
+
+#include "fp8.h"
+#include "launch.h"
+#include "tc_gemm.cuh"
+
+namespace tmmo {
+
+constexpr int F8_BK = 128;       // K per step and per scale block
+constexpr int F8_THREADS = 384;  // warps 0-3: copies, MMA, two idle; 4-11: epilogue
+constexpr int F8_EPI_WARP0 = 4;
+constexpr int F8_EPI_WARPS = 8;
+constexpr int F8_BOX = 128 * F8_BK;  // bytes of one operand box
+// Registers: 384 threads are launched with 168 each (64,512 in all); the
+// first warpgroup keeps 72 and the two epilogue warpgroups get 216 each:
+// 128 * 72 + 256 * 216 = 64,512.
+constexpr int F8_REGS_LAUNCH = 168;
+constexpr int F8_REGS_FEW = 72;
+constexpr int F8_REGS_EPI = 216;
+static_assert(128 * F8_REGS_FEW + 256 * F8_REGS_EPI <= F8_THREADS * F8_REGS_LAUNCH, "register split");
+
+struct Fp8Params {
+    int M, N, K;
+    int tiles_m, tiles_n, num_tiles;
+    int k_blocks;
+    int group_m;
+    uint32_t idesc;
+    bool a_mn, b_mn;               // operands stored with the outer axis contiguous
+    const float *sa, *sb;          // scales, see Fp8Operand
+    long long sa_k, sa_o, sb_k, sb_o;
+    int sa_shift, sb_shift;
+    void* C;
+    long long ldc;
+    int out_dtype;                 // DT_*
+    bool vec_out;                  // C's rows take 16-byte accesses
+    float alpha, beta;
+    int* status;
+    long long wait_budget;
+    int fault_skip_kblock;
+};
+
+template <int CG, int BN, int STAGES>
+struct Fp8Layout {
+    static constexpr int STAGE = 2 * F8_BOX;           // one box of A, one of B per CTA
+    static constexpr int OFF_STAGING = STAGES * STAGE;  // 4 KiB per epilogue warp
+    static constexpr int OFF_SCALE = OFF_STAGING + F8_EPI_WARPS * TC_STAGING_BYTES;
+    static constexpr int SCALE_BYTES = 2 * (BN / 2) * 4;  // two K blocks' column scales per warp
+    static constexpr int NBUF = 512 / BN < 4 ? 512 / BN : 4;
+    static constexpr int OFF_BAR = OFF_SCALE + F8_EPI_WARPS * SCALE_BYTES;
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 1;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
+    static constexpr int BYTES = OFF_MISC + 16;
+    static constexpr int SMEM_ALLOC = BYTES + 1024;
+    static constexpr uint32_t TMEM_COLS = NBUF * BN;
+    static_assert(BN / CG == 128, "each CTA holds one 128-row box of B");
+    static_assert(SMEM_ALLOC <= 232448, "exceeds 227 KiB of dynamic shared memory");
+};
+
+// Instruction descriptor of tcgen05.mma kind::f8f6f4: as kind::f16, with the
+// types e4m3 = 0 and e5m2 = 1.
+__host__ __device__ constexpr uint32_t fp8_idesc(int a_type, int b_type, int m, int n, bool a_mn,
+                                                 bool b_mn)
+{
+    return (1u << 4) | (static_cast<uint32_t>(a_type) << 7) | (static_cast<uint32_t>(b_type) << 10) |
+           ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// Descriptor of the 32-wide K slice `k` of a 16 KiB operand box.  K-major:
+// 128-byte rows, 8-row groups 1024 bytes apart, 32 bytes along the row per
+// slice.  MN-major: 128 outer values per 128-byte row (one swizzle atom, so
+// the leading offset is unused), 8-row K groups 1024 bytes apart, 32 rows
+// (4 KiB) per slice.
+__device__ __forceinline__ uint64_t fp8_desc(uint32_t box, int k, bool mn)
+{
+    return mn ? smem_desc_sw128(box + k * 4096, F8_BOX, 1024) : smem_desc_sw128(box + k * 32, 16, 1024);
+}
+
+// alpha * v + beta * C for a run of `N` values of one row, stored in OutT.
+// in: how many of them lie inside C.  vec: 16-byte accesses are allowed.
+template <typename OutT>
+__device__ __forceinline__ OutT fp8_to_out(float v)
+{
+    if constexpr (sizeof(OutT) == 4)
+        return v;
+    else if constexpr (std::is_same<OutT, __half>::value)
+        return __float2half_rn(v);
+    else
+        return __float2bfloat16_rn(v);
+}
+
+template <typename OutT>
+__device__ __forceinline__ void fp8_axpby(float* v, int n, const OutT* src, float alpha, float beta)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        v[i] *= alpha;
+        if (beta != 0.0f && i < n)
+            v[i] = fmaf(beta, out_to_f32(src[i]), v[i]);
+    }
+}
+
+// 32 values of one row of C straight from registers, `n` of them inside C.
+template <typename OutT>
+__device__ __forceinline__ void fp8_store_row(OutT* dst, float* v, int n, const Fp8Params& p)
+{
+    if (n <= 0)
+        return;
+    if (p.alpha != 1.0f || p.beta != 0.0f)
+        fp8_axpby<OutT>(v, n, dst, p.alpha, p.beta);
+    constexpr int PER = 16 / static_cast<int>(sizeof(OutT));
+#pragma unroll
+    for (int c = 0; c < 32 / PER; ++c) {
+        if (p.vec_out && (c + 1) * PER <= n) {
+            uint4 u;
+            if constexpr (sizeof(OutT) == 4) {
+                u = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                               __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+            } else {
+                OutT* tag = nullptr;
+                u = make_uint4(pack2(v[8 * c], v[8 * c + 1], tag), pack2(v[8 * c + 2], v[8 * c + 3], tag),
+                               pack2(v[8 * c + 4], v[8 * c + 5], tag),
+                               pack2(v[8 * c + 6], v[8 * c + 7], tag));
+            }
+            *reinterpret_cast<uint4*>(dst + c * PER) = u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (c * PER + i < n)
+                    dst[c * PER + i] = fp8_to_out<OutT>(v[c * PER + i]);
+        }
+    }
+}
+
+// COLV: the column operand has a scale for each column (a vector along the
+// tile's columns); otherwise one for 128 columns, the same for all of a
+// thread's columns.
+template <int CG, int BN, int STAGES, bool COLV>
+__global__ void __launch_bounds__(F8_THREADS, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const Fp8Params p)
+{
+    using L = Fp8Layout<CG, BN, STAGES>;
+    constexpr int TILE_M = TC_BM * CG;
+    constexpr int NBUF = L::NBUF;
+    constexpr int COLS = BN / 2;  // columns of the tile per epilogue thread
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + L::OFF_BAR;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + NBUF + b); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t rank = (CG == 2) ? cluster_ctarank() : 0;
+    const bool leader = (rank == 0);
+    const int unit = (CG == 2) ? (blockIdx.x >> 1) : blockIdx.x;
+    const int num_units = (CG == 2) ? (gridDim.x >> 1) : gridDim.x;
+    const TcWatch watch{abort_flag, p.status, p.wait_budget};
+    auto tile_coords = [&](int t, int& mb, int& nb) {
+        const int per_group = p.group_m * p.tiles_n;
+        const int g = t / per_group;
+        const int first_m = g * p.group_m;
+        const int gm = min(p.tiles_m - first_m, p.group_m);
+        const int r = t - g * per_group;
+        mb = first_m + r % gm;
+        nb = r / gm;
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), F8_EPI_WARPS * CG);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(smem_u32(tmem_slot), L::TMEM_COLS);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before();
+    if constexpr (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp < F8_EPI_WARP0) {
+        set_max_regs_dec<F8_REGS_FEW>();
+        if (warp == 0 && lane == 0) {
+            // -------------------------------------------- TMA producer
+            int stage = 0;
+            uint32_t phase = 0;
+            int issued[STAGES];
+#pragma unroll
+            for (int s = 0; s < STAGES; ++s)
+                issued[s] = 0;
+            bool ok = true;
+            for (int t = unit; ok && t < p.num_tiles; t += num_units) {
+                int mb, nb;
+                tile_coords(t, mb, nb);
+                const int a_row = mb * TILE_M + static_cast<int>(rank) * TC_BM;
+                const int b_row = nb * BN + static_cast<int>(rank) * 128;
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (!tc_wait(empty_bar(stage), phase ^ 1, watch)) {
+                        ok = false;
+                        break;
+                    }
+                    if (p.fault_skip_kblock != kb) {  // test hook, -1 in normal use
+                        if (leader)
+                            mbar_arrive_expect_tx(full_bar(stage), CG * L::STAGE);
+                        const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
+                        const uint32_t dA = sbase + stage * L::STAGE;
+                        auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
+                            if constexpr (CG == 2)
+                                tma_load_2d_pair(dst, map, fb, x, y);
+                            else
+                                tma_load_2d(dst, map, fb, x, y);
+                        };
+                        const int k0 = kb * F8_BK;
+                        if (p.a_mn)
+                            load(dA, &tmA, a_row, k0);
+                        else
+                            load(dA, &tmA, k0, a_row);
+                        if (p.b_mn)
+                            load(dA + F8_BOX, &tmB, b_row, k0);
+                        else
+                            load(dA + F8_BOX, &tmB, k0, b_row);
+#pragma unroll
+                        for (int s = 0; s < STAGES; ++s)
+                            issued[s] += (s == stage);
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok && leader) {
+                // Drain (bounded): the copies already issued into each stage
+                // land before shared memory goes away.
+#pragma unroll
+                for (int s = 0; s < STAGES; ++s) {
+                    if (issued[s] == 0)
+                        continue;
+                    const uint32_t par = static_cast<uint32_t>(issued[s] - 1) & 1u;
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait(full_bar(s), par) && clock64() - t0 < p.wait_budget) {
+                    }
+                }
+            }
+        } else if (warp == 1 && leader && lane == 0) {
+            // -------------------------------------------- MMA issuer
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, buf_phase = 0;
+            bool ok = true;
+            for (int t = unit; ok && t < p.num_tiles; t += num_units) {
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (!tc_wait<CG == 2>(tempty_bar(buf), buf_phase ^ 1, watch) ||
+                        !tc_wait(full_bar(stage), phase, watch)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = sbase + stage * L::STAGE;
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+#pragma unroll
+                    for (int k = 0; k < F8_BK / 32; ++k)
+                        tc_mma_f8<CG>(d, fp8_desc(a0, k, p.a_mn), fp8_desc(a0 + F8_BOX, k, p.b_mn),
+                                      p.idesc, k != 0);
+                    if constexpr (CG == 2) {
+                        tc_commit_pair(empty_bar(stage), 0x3);
+                        tc_commit_pair(tfull_bar(buf), 0x3);
+                    } else {
+                        tc_commit(empty_bar(stage));
+                        tc_commit(tfull_bar(buf));
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    if (++buf == NBUF) {
+                        buf = 0;
+                        buf_phase ^= 1;
+                    }
+                }
+            }
+            // every MMA issued has completed before TMEM is released (bounded)
+            tc_commit_self<CG>(drain_bar);
+            const long long t0 = clock64();
+            while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
+            }
+        }
+    } else {
+        // ------------------------------------------------ promotion, epilogue
+        set_max_regs_inc<F8_REGS_EPI>();
+        const int ew = warp - F8_EPI_WARP0;
+        const int q = warp & 3;        // TMEM lane quarter
+        const int half = ew >> 2;      // column half of the tile
+        const uint32_t scol = sbase + L::OFF_SCALE + static_cast<uint32_t>(ew * L::SCALE_BYTES);
+        const uint32_t tempty0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        bool ok = true;
+        for (int t = unit; ok && t < p.num_tiles; t += num_units) {
+            int mb, nb;
+            tile_coords(t, mb, nb);
+            const int row = mb * TILE_M + static_cast<int>(rank) * TC_BM + q * 32 + static_cast<int>(lane);
+            const int col0 = nb * BN + half * COLS;
+            // Scales: rows and columns beyond the matrix take the last one's
+            // (their products are never stored).
+            const float* sa = p.sa + (static_cast<long long>(min(row, p.M - 1)) >> p.sa_shift) * p.sa_o;
+            const float* sb = p.sb;
+            if constexpr (!COLV)
+                sb += (static_cast<long long>(min(col0, p.N - 1)) >> p.sb_shift) * p.sb_o;
+            constexpr int CPL = COLS / 32;  // column scales each lane fetches
+            const int sc = min(col0 + static_cast<int>(lane) * CPL, p.N - 1);
+            float ra[2], cs[2][COLV ? CPL : 1];
+            auto fetch = [&](int kb, int slot) {
+                kb = min(kb, p.k_blocks - 1);
+                const float a = __ldg(sa + kb * p.sa_k);
+                ra[slot] = a;
+                if constexpr (COLV) {
+#pragma unroll
+                    for (int i = 0; i < CPL; ++i)
+                        cs[slot][i] = __ldg(sb + kb * p.sb_k +
+                                            static_cast<long long>(min(sc + i, p.N - 1)) * p.sb_o);
+                } else {
+                    cs[slot][0] = __ldg(sb + kb * p.sb_k);
+                }
+            };
+            fetch(0, 0);
+            fetch(1, 1);
+            uint64_t acc[COLS / 2];
+#pragma unroll
+            for (int i = 0; i < COLS / 2; ++i)
+                acc[i] = 0;
+#pragma unroll 1
+            for (int kb = 0; kb < p.k_blocks; ++kb) {
+                float rs = ra[0];
+                uint32_t slot_addr = scol + static_cast<uint32_t>((kb & 1) * COLS * 4);
+                if constexpr (COLV) {
+#pragma unroll
+                    for (int i = 0; i < CPL; i += 2)
+                        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(
+                                         slot_addr + (lane * CPL + i) * 4),
+                                     "f"(cs[0][i]), "f"(cs[0][i + 1])
+                                     : "memory");
+                    __syncwarp();
+                } else {
+                    rs *= cs[0][0];
+                }
+                ra[0] = ra[1];
+#pragma unroll
+                for (int i = 0; i < (COLV ? CPL : 1); ++i)
+                    cs[0][i] = cs[1][i];
+                fetch(kb + 2, 1);
+                const uint64_t rs2 = pack_f32x2(__float_as_uint(rs), __float_as_uint(rs));
+                int w = 1;
+                if (lane == 0)
+                    w = tc_wait(tfull_bar(buf), buf_phase, watch) ? 1 : 0;
+                if (!__shfl_sync(0xffffffffu, w, 0)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                       static_cast<uint32_t>(buf * BN + half * COLS);
+                uint32_t v[2][32];
+                tmem_ld_32x32b_x32(taddr, v[0]);
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c) {
+                    tmem_wait_ld();
+                    if (c + 1 < COLS / 32) {
+                        tmem_ld_32x32b_x32(taddr + (c + 1) * 32, v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (CG == 2)
+                                mbar_arrive_cluster(tempty0 + 8u * buf);
+                            else
+                                mbar_arrive(tempty0 + 8u * buf);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        uint64_t s0 = rs2, s1 = rs2;
+                        if constexpr (COLV) {
+                            uint32_t f[4];
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                                         : "r"(slot_addr + (c * 32 + 2 * i) * 4));
+                            s0 = fmul2(rs2, pack_f32x2(f[0], f[1]));
+                            s1 = fmul2(rs2, pack_f32x2(f[2], f[3]));
+                        }
+                        ffma2(acc[c * 16 + i], pack_f32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s0);
+                        ffma2(acc[c * 16 + i + 1], pack_f32x2(v[c & 1][2 * i + 2], v[c & 1][2 * i + 3]),
+                              s1);
+                    }
+                }
+                if (++buf == NBUF) {
+                    buf = 0;
+                    buf_phase ^= 1;
+                }
+            }
+            if (!ok)
+                break;
+            // ---- the finished tile: alpha, beta, rounding to the output type
+            if (row < p.M) {
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c) {
+                    float o[32];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        uint32_t lo, hi;
+                        unpack_f32x2(acc[c * 16 + i], lo, hi);
+                        o[2 * i] = __uint_as_float(lo);
+                        o[2 * i + 1] = __uint_as_float(hi);
+                    }
+                    const int col = col0 + c * 32;
+                    const int n = min(p.N - col, 32);
+                    const long long at = static_cast<long long>(row) * p.ldc + col;
+                    if (p.out_dtype == DT_F32)
+                        fp8_store_row(static_cast<float*>(p.C) + at, o, n, p);
+                    else if (p.out_dtype == DT_F16)
+                        fp8_store_row(static_cast<__half*>(p.C) + at, o, n, p);
+                    else
+                        fp8_store_row(static_cast<__nv_bfloat16*>(p.C) + at, o, n, p);
+                }
+            }
+        }
+    }
+
+    // ---------------------------------------------------- teardown
+    __syncwarp();
+    tc_fence_before();
+    if constexpr (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc<CG>(tmem_base, L::TMEM_COLS);
+    }
+}
+
+}  // namespace tmmo
