@@ -22,9 +22,10 @@
 //   * several partial buffers in tensor memory (512 columns in all), so the
 //     tensor core works on the next K blocks while one is promoted;
 //   * multiply-adds in pairs (fma.rn.f32x2), half the instructions;
-//   * scales are fetched two K blocks ahead into registers; a scale vector
-//     along the columns is staged through a private slice of shared memory
-//     per warp and read back by broadcast.
+//   * one warp copies the scales of each K block into a ring in shared
+//     memory, eight K blocks ahead (asynchronous 4-byte copies, which take
+//     any alignment).  Loads by the epilogue warps themselves, two K blocks
+//     ahead, waited for the memory system: 1.2 times the time.
 //
 // One K step is one 128-byte swizzle row: a 128 x 128 block of either
 // operand is 16 KiB, one TMA box, whether K or the outer axis is contiguous
@@ -46,7 +47,7 @@
 namespace tmmo {
 
 constexpr int F8_BK = 128;       // K per step and per scale block
-constexpr int F8_THREADS = 384;  // warps 0-3: copies, MMA, two idle; 4-11: epilogue
+constexpr int F8_THREADS = 384;  // warps 0-3: copies, MMA, scales, one idle; 4-11: epilogue
 constexpr int F8_EPI_WARP0 = 4;
 constexpr int F8_EPI_WARPS = 8;
 constexpr int F8_BOX = 128 * F8_BK;  // bytes of one operand box
@@ -81,12 +82,13 @@ struct Fp8Params {
 template <int CG, int BN, int STAGES>
 struct Fp8Layout {
     static constexpr int STAGE = 2 * F8_BOX;           // one box of A, one of B per CTA
-    static constexpr int OFF_STAGING = STAGES * STAGE;  // 4 KiB per epilogue warp
-    static constexpr int OFF_SCALE = OFF_STAGING + F8_EPI_WARPS * TC_STAGING_BYTES;
-    static constexpr int SCALE_BYTES = 2 * (BN / 2) * 4;  // two K blocks' column scales per warp
     static constexpr int NBUF = 512 / BN < 4 ? 512 / BN : 4;
-    static constexpr int OFF_BAR = OFF_SCALE + F8_EPI_WARPS * SCALE_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 1;
+    // Scale ring: per K block, 128 row scales and BN column scales (or two).
+    static constexpr int SLOTS = 8;
+    static constexpr int SLOT_BYTES = (128 + BN) * 4;
+    static constexpr int OFF_SCALE = STAGES * STAGE;
+    static constexpr int OFF_BAR = OFF_SCALE + SLOTS * SLOT_BYTES;
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 2 * SLOTS + 1;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
     static constexpr int BYTES = OFF_MISC + 16;
     static constexpr int SMEM_ALLOC = BYTES + 1024;
@@ -193,7 +195,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + NBUF + b); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF);
+    auto sfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 * NBUF + i); };
+    auto sempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 * NBUF + L::SLOTS + i); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF + 2 * L::SLOTS);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
 
@@ -222,6 +226,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         for (int b = 0; b < NBUF; ++b) {
             mbar_init(tfull_bar(b), 1);
             mbar_init(tempty_bar(b), F8_EPI_WARPS * CG);
+        }
+        for (int i = 0; i < L::SLOTS; ++i) {
+            mbar_init(sfull_bar(i), 32);
+            mbar_init(sempty_bar(i), F8_EPI_WARPS);
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -346,6 +354,54 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             const long long t0 = clock64();
             while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
             }
+        } else if (warp == 2) {
+            // -------------------------------------------- scales
+            int slot = 0;
+            uint32_t slot_phase = 0;
+            bool ok = true;
+            for (int t = unit; ok && t < p.num_tiles; t += num_units) {
+                int mb, nb;
+                tile_coords(t, mb, nb);
+                // Rows and columns beyond the matrix take the last one's
+                // scale (their products are never stored).
+                const int row0 = mb * TILE_M + static_cast<int>(rank) * TC_BM + static_cast<int>(lane);
+                const int col0 = nb * BN + static_cast<int>(lane) * (COLV ? 1 : COLS);
+                const float* ra[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ra[i] = p.sa + (static_cast<long long>(min(row0 + 32 * i, p.M - 1)) >> p.sa_shift) *
+                                       p.sa_o;
+                constexpr int NC = COLV ? BN / 32 : 1;
+                const float* cb[NC];
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    cb[i] = p.sb + (static_cast<long long>(min(col0 + 32 * i, p.N - 1)) >> p.sb_shift) *
+                                       p.sb_o;
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    int w = 1;
+                    if (lane == 0)
+                        w = tc_wait(sempty_bar(slot), slot_phase ^ 1, watch) ? 1 : 0;
+                    if (!__shfl_sync(0xffffffffu, w, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = sbase + L::OFF_SCALE + slot * L::SLOT_BYTES + lane * 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        cp_async_4(dst + 128 * i, ra[i] + kb * p.sa_k);
+                    if (COLV || lane < 2) {
+#pragma unroll
+                        for (int i = 0; i < NC; ++i)
+                            cp_async_4(dst + 512 + 128 * i, cb[i] + kb * p.sb_k);
+                    }
+                    cp_async_mbar_arrive(sfull_bar(slot));
+                    if (++slot == L::SLOTS) {
+                        slot = 0;
+                        slot_phase ^= 1;
+                    }
+                }
+            }
+            cp_async_wait_all();
         }
     } else {
         // ------------------------------------------------ promotion, epilogue
@@ -353,73 +409,38 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         const int ew = warp - F8_EPI_WARP0;
         const int q = warp & 3;        // TMEM lane quarter
         const int half = ew >> 2;      // column half of the tile
-        const uint32_t scol = sbase + L::OFF_SCALE + static_cast<uint32_t>(ew * L::SCALE_BYTES);
         const uint32_t tempty0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
-        int buf = 0;
-        uint32_t buf_phase = 0;
+        int buf = 0, slot = 0;
+        uint32_t buf_phase = 0, slot_phase = 0;
         bool ok = true;
         for (int t = unit; ok && t < p.num_tiles; t += num_units) {
             int mb, nb;
             tile_coords(t, mb, nb);
             const int row = mb * TILE_M + static_cast<int>(rank) * TC_BM + q * 32 + static_cast<int>(lane);
             const int col0 = nb * BN + half * COLS;
-            // Scales: rows and columns beyond the matrix take the last one's
-            // (their products are never stored).
-            const float* sa = p.sa + (static_cast<long long>(min(row, p.M - 1)) >> p.sa_shift) * p.sa_o;
-            const float* sb = p.sb;
-            if constexpr (!COLV)
-                sb += (static_cast<long long>(min(col0, p.N - 1)) >> p.sb_shift) * p.sb_o;
-            constexpr int CPL = COLS / 32;  // column scales each lane fetches
-            const int sc = min(col0 + static_cast<int>(lane) * CPL, p.N - 1);
-            float ra[2], cs[2][COLV ? CPL : 1];
-            auto fetch = [&](int kb, int slot) {
-                kb = min(kb, p.k_blocks - 1);
-                const float a = __ldg(sa + kb * p.sa_k);
-                ra[slot] = a;
-                if constexpr (COLV) {
-#pragma unroll
-                    for (int i = 0; i < CPL; ++i)
-                        cs[slot][i] = __ldg(sb + kb * p.sb_k +
-                                            static_cast<long long>(min(sc + i, p.N - 1)) * p.sb_o);
-                } else {
-                    cs[slot][0] = __ldg(sb + kb * p.sb_k);
-                }
-            };
-            fetch(0, 0);
-            fetch(1, 1);
             uint64_t acc[COLS / 2];
 #pragma unroll
             for (int i = 0; i < COLS / 2; ++i)
                 acc[i] = 0;
 #pragma unroll 1
             for (int kb = 0; kb < p.k_blocks; ++kb) {
-                float rs = ra[0];
-                uint32_t slot_addr = scol + static_cast<uint32_t>((kb & 1) * COLS * 4);
-                if constexpr (COLV) {
-#pragma unroll
-                    for (int i = 0; i < CPL; i += 2)
-                        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(
-                                         slot_addr + (lane * CPL + i) * 4),
-                                     "f"(cs[0][i]), "f"(cs[0][i + 1])
-                                     : "memory");
-                    __syncwarp();
-                } else {
-                    rs *= cs[0][0];
-                }
-                ra[0] = ra[1];
-#pragma unroll
-                for (int i = 0; i < (COLV ? CPL : 1); ++i)
-                    cs[0][i] = cs[1][i];
-                fetch(kb + 2, 1);
-                const uint64_t rs2 = pack_f32x2(__float_as_uint(rs), __float_as_uint(rs));
                 int w = 1;
                 if (lane == 0)
-                    w = tc_wait(tfull_bar(buf), buf_phase, watch) ? 1 : 0;
+                    w = tc_wait(sfull_bar(slot), slot_phase, watch) &&
+                                tc_wait(tfull_bar(buf), buf_phase, watch)
+                            ? 1
+                            : 0;
                 if (!__shfl_sync(0xffffffffu, w, 0)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                const uint32_t saddr = sbase + L::OFF_SCALE + slot * L::SLOT_BYTES;
+                const uint32_t caddr = saddr + 512 + (COLV ? half * COLS * 4 : half * 4);
+                float rs = ld_shared_f32(saddr + (q * 32 + lane) * 4);
+                if constexpr (!COLV)
+                    rs *= ld_shared_f32(caddr);
+                const uint64_t rs2 = pack_f32x2(__float_as_uint(rs), __float_as_uint(rs));
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                        static_cast<uint32_t>(buf * BN + half * COLS);
                 uint32_t v[2][32];
@@ -434,7 +455,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         __syncwarp();
                         if (lane == 0) {
                             if constexpr (CG == 2)
-                                mbar_arrive_cluster(tempty0 + 8u * buf);
+                                mbar_arrive_cluster_relaxed(tempty0 + 8u * buf);
                             else
                                 mbar_arrive(tempty0 + 8u * buf);
                         }
@@ -446,7 +467,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                             uint32_t f[4];
                             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                          : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-                                         : "r"(slot_addr + (c * 32 + 2 * i) * 4));
+                                         : "r"(caddr + (c * 32 + 2 * i) * 4));
                             s0 = fmul2(rs2, pack_f32x2(f[0], f[1]));
                             s1 = fmul2(rs2, pack_f32x2(f[2], f[3]));
                         }
@@ -454,6 +475,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         ffma2(acc[c * 16 + i + 1], pack_f32x2(v[c & 1][2 * i + 2], v[c & 1][2 * i + 3]),
                               s1);
                     }
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(sempty_bar(slot));
+                if (++slot == L::SLOTS) {
+                    slot = 0;
+                    slot_phase ^= 1;
                 }
                 if (++buf == NBUF) {
                     buf = 0;

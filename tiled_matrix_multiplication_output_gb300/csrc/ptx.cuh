@@ -62,6 +62,17 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 // Callers bound their waits by a clock budget checked between attempts.
 constexpr uint32_t MBAR_SUSPEND_HINT_NS = 1000000;
 
+// The same with no ordering of memory accesses at cluster scope, for a
+// barrier that only reports that tensor memory has been read: the reads have
+// returned (tcgen05.wait::ld) before the arrival is issued, and nothing else
+// is handed over.  The ordered form waits for the thread's outstanding
+// accesses, about a microsecond when it runs once per K block.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+                 : "memory");
+}
+
 // True once the phase with parity `parity` has completed.
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
 {
@@ -197,6 +208,29 @@ __device__ __forceinline__ void grid_dep_wait()
 __device__ __forceinline__ void fence_proxy_async_smem()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Asynchronous 4-byte copy into shared memory (generic proxy), and an
+// arrival on `bar` (counted among its expected ones) once every copy that
+// this thread issued before has landed.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // ------------------------------------------------------------------- tcgen05
