@@ -47,9 +47,10 @@
 namespace tmmo {
 
 constexpr int F8_BK = 128;       // K per step and per scale block
-constexpr int F8_THREADS = 384;  // warps 0-3: copies, MMA, scales, one idle; 4-11: epilogue
+constexpr int F8_THREADS = 384;  // warps 0-3: copies, MMA, scales, herald; 4-11: epilogue
 constexpr int F8_EPI_WARP0 = 4;
 constexpr int F8_EPI_WARPS = 8;
+constexpr int F8_HERALD_BAR = 1;  // hardware barrier of the herald and the epilogue warps
 constexpr int F8_BOX = 128 * F8_BK;  // bytes of one operand box
 // Registers: 384 threads are launched with 168 each (64,512 in all); the
 // first warpgroup keeps 72 and the two epilogue warpgroups get 216 each:
@@ -72,7 +73,7 @@ struct Fp8Params {
     void* C;
     long long ldc;
     int out_dtype;                 // DT_*
-    bool vec_out;                  // C's rows take 16-byte accesses
+    bool vec_out;                  // C's rows take 32-byte accesses
     float alpha, beta;
     int* status;
     long long wait_budget;
@@ -83,12 +84,15 @@ template <int CG, int BN, int STAGES>
 struct Fp8Layout {
     static constexpr int STAGE = 2 * F8_BOX;           // one box of A, one of B per CTA
     static constexpr int NBUF = 512 / BN < 4 ? 512 / BN : 4;
-    // Scale ring: per K block, 128 row scales and BN column scales (or two).
-    static constexpr int SLOTS = 8;
-    static constexpr int SLOT_BYTES = (128 + BN) * 4;
+    // Scale ring: per K block, 128 row scales and BN column scales (or two);
+    // a slot, with one pair of barriers, holds GROUP K blocks.
+    static constexpr int SLOTS = 3;
+    static constexpr int GROUP = 4;
+    static constexpr int BLOCK_BYTES = (128 + BN) * 4;
+    static constexpr int SLOT_BYTES = GROUP * BLOCK_BYTES;
     static constexpr int OFF_SCALE = STAGES * STAGE;
     static constexpr int OFF_BAR = OFF_SCALE + SLOTS * SLOT_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 2 * SLOTS + 1;
+    static constexpr int NUM_BARS = 2 * STAGES + NBUF + 2 * SLOTS + 1;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
     static constexpr int BYTES = OFF_MISC + 16;
     static constexpr int SMEM_ALLOC = BYTES + 1024;
@@ -105,16 +109,6 @@ __host__ __device__ constexpr uint32_t fp8_idesc(int a_type, int b_type, int m, 
     return (1u << 4) | (static_cast<uint32_t>(a_type) << 7) | (static_cast<uint32_t>(b_type) << 10) |
            ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-// Descriptor of the 32-wide K slice `k` of a 16 KiB operand box.  K-major:
-// 128-byte rows, 8-row groups 1024 bytes apart, 32 bytes along the row per
-// slice.  MN-major: 128 outer values per 128-byte row (one swizzle atom, so
-// the leading offset is unused), 8-row K groups 1024 bytes apart, 32 rows
-// (4 KiB) per slice.
-__device__ __forceinline__ uint64_t fp8_desc(uint32_t box, int k, bool mn)
-{
-    return mn ? smem_desc_sw128(box + k * 4096, F8_BOX, 1024) : smem_desc_sw128(box + k * 32, 16, 1024);
 }
 
 // alpha * v + beta * C for a run of `N` values of one row, stored in OutT.
@@ -149,27 +143,50 @@ __device__ __forceinline__ void fp8_store_row(OutT* dst, float* v, int n, const 
         return;
     if (p.alpha != 1.0f || p.beta != 0.0f)
         fp8_axpby<OutT>(v, n, dst, p.alpha, p.beta);
-    constexpr int PER = 16 / static_cast<int>(sizeof(OutT));
+    constexpr int PER = 32 / static_cast<int>(sizeof(OutT));  // values per 32-byte sector
 #pragma unroll
     for (int c = 0; c < 32 / PER; ++c) {
         if (p.vec_out && (c + 1) * PER <= n) {
-            uint4 u;
-            if constexpr (sizeof(OutT) == 4) {
-                u = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                               __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-            } else {
-                OutT* tag = nullptr;
-                u = make_uint4(pack2(v[8 * c], v[8 * c + 1], tag), pack2(v[8 * c + 2], v[8 * c + 3], tag),
-                               pack2(v[8 * c + 4], v[8 * c + 5], tag),
-                               pack2(v[8 * c + 6], v[8 * c + 7], tag));
+            uint32_t u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (sizeof(OutT) == 4)
+                    u[i] = __float_as_uint(v[8 * c + i]);
+                else
+                    u[i] = pack2(v[16 * c + 2 * i], v[16 * c + 2 * i + 1], static_cast<OutT*>(nullptr));
             }
-            *reinterpret_cast<uint4*>(dst + c * PER) = u;
+            st_global_v8(dst + c * PER, u);
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (c * PER + i < n)
                     dst[c * PER + i] = fp8_to_out<OutT>(v[c * PER + i]);
         }
+    }
+}
+
+// Bounded wait of a whole warp on an mbarrier phase: every lane polls, so no
+// branch diverges, and the poll does not suspend the warp.  These waits come
+// once per K block, and one lane waiting for the others with tc_wait (a
+// divergent loop, a suspending poll, a shuffle) cost about 300 cycles of the
+// 512 that a K block has.
+__device__ __forceinline__ bool fp8_wait_warp(uint32_t bar, uint32_t parity, const TcWatch& w)
+{
+    long long t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity)))
+            return true;
+        if ((n & 1023u) != 0)
+            continue;
+        // now and then: has another role given up, or the budget run out?
+        const long long now = clock64();
+        if (t0 == 0)
+            t0 = now;
+        const bool late = now - t0 > w.budget;
+        if (late)
+            tc_raise(w);
+        if (__any_sync(0xffffffffu, late || *w.abort_flag))
+            return false;
     }
 }
 
@@ -192,12 +209,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + L::OFF_BAR;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-    auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
-    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + NBUF + b); };
-    auto sfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 * NBUF + i); };
-    auto sempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 * NBUF + L::SLOTS + i); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF + 2 * L::SLOTS);
+    // The MMAs of the K block in stage s have completed: its operands may be
+    // overwritten and its product read.
+    auto done_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto sfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + NBUF + i); };
+    auto sempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + NBUF + L::SLOTS + i); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + NBUF + 2 * L::SLOTS);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
 
@@ -221,12 +239,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1);
+            mbar_init(done_bar(s), 1);
         }
-        for (int b = 0; b < NBUF; ++b) {
-            mbar_init(tfull_bar(b), 1);
+        for (int b = 0; b < NBUF; ++b)
             mbar_init(tempty_bar(b), F8_EPI_WARPS * CG);
-        }
         for (int i = 0; i < L::SLOTS; ++i) {
             mbar_init(sfull_bar(i), 32);
             mbar_init(sempty_bar(i), F8_EPI_WARPS);
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 const int a_row = mb * TILE_M + static_cast<int>(rank) * TC_BM;
                 const int b_row = nb * BN + static_cast<int>(rank) * 128;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!tc_wait(empty_bar(stage), phase ^ 1, watch)) {
+                    if (!tc_wait(done_bar(stage), phase ^ 1, watch)) {
                         ok = false;
                         break;
                     }
@@ -313,32 +329,46 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     }
                 }
             }
-        } else if (warp == 1 && leader && lane == 0) {
+        } else if (warp == 1 && leader) {
             // -------------------------------------------- MMA issuer
+            // The whole warp runs the loop and one elected lane issues: the
+            // descriptors then live in uniform registers, where the
+            // instruction takes them from.
+            // Descriptor of a 32-wide K slice of a 16 KiB operand box.  K-major:
+            // 128-byte rows, 8-row groups 1024 bytes apart, 32 bytes along
+            // the row per slice.  MN-major: 128 outer values per 128-byte
+            // row (one swizzle atom, so the leading offset is unused), 8-row
+            // K groups 1024 bytes apart, 32 rows (4 KiB) per slice.
+            const uint64_t hi = (1ull << 46) | (2ull << 61) | (static_cast<uint64_t>(1024 >> 4) << 32);
+            const uint64_t a_hi = hi | (static_cast<uint64_t>((p.a_mn ? F8_BOX : 16) >> 4) << 16);
+            const uint64_t b_hi = hi | (static_cast<uint64_t>((p.b_mn ? F8_BOX : 16) >> 4) << 16);
+            const uint32_t a_step = (p.a_mn ? 4096 : 32) >> 4;
+            const uint32_t b_step = (p.b_mn ? 4096 : 32) >> 4;
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
             bool ok = true;
             for (int t = unit; ok && t < p.num_tiles; t += num_units) {
+#pragma unroll 1
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!tc_wait<CG == 2>(tempty_bar(buf), buf_phase ^ 1, watch) ||
-                        !tc_wait(full_bar(stage), phase, watch)) {
-                        ok = false;
+                    ok = fp8_wait_warp(tempty_bar(buf), buf_phase ^ 1, watch) &&
+                         fp8_wait_warp(full_bar(stage), phase, watch);
+                    if (!ok)
                         break;
-                    }
                     tc_fence_after();
-                    const uint32_t a0 = sbase + stage * L::STAGE;
+                    const uint32_t a0 = (sbase + stage * L::STAGE) >> 4;
+                    const uint32_t b0 = a0 + (F8_BOX >> 4);
                     const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < F8_BK / 32; ++k)
-                        tc_mma_f8<CG>(d, fp8_desc(a0, k, p.a_mn), fp8_desc(a0 + F8_BOX, k, p.b_mn),
-                                      p.idesc, k != 0);
-                    if constexpr (CG == 2) {
-                        tc_commit_pair(empty_bar(stage), 0x3);
-                        tc_commit_pair(tfull_bar(buf), 0x3);
-                    } else {
-                        tc_commit(empty_bar(stage));
-                        tc_commit(tfull_bar(buf));
+                        for (int k = 0; k < F8_BK / 32; ++k)
+                            tc_mma_f8<CG>(d, a_hi | ((a0 + k * a_step) & 0x3FFF),
+                                          b_hi | ((b0 + k * b_step) & 0x3FFF), p.idesc, k != 0);
+                        if constexpr (CG == 2)
+                            tc_commit_pair(done_bar(stage), 0x3);
+                        else
+                            tc_commit(done_bar(stage));
                     }
+                    __syncwarp();
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -350,9 +380,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 }
             }
             // every MMA issued has completed before TMEM is released (bounded)
-            tc_commit_self<CG>(drain_bar);
+            if (elect_one())
+                tc_commit_self<CG>(drain_bar);
+            __syncwarp();
             const long long t0 = clock64();
-            while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
+            while (!__all_sync(0xffffffffu, mbar_test_wait(drain_bar, 0))) {
+                if (__any_sync(0xffffffffu, clock64() - t0 > p.wait_budget))
+                    break;
             }
         } else if (warp == 2) {
             // -------------------------------------------- scales
@@ -377,7 +411,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 for (int i = 0; i < NC; ++i)
                     cb[i] = p.sb + (static_cast<long long>(min(col0 + 32 * i, p.N - 1)) >> p.sb_shift) *
                                        p.sb_o;
-                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                for (int kb0 = 0; kb0 < p.k_blocks; kb0 += L::GROUP) {
                     int w = 1;
                     if (lane == 0)
                         w = tc_wait(sempty_bar(slot), slot_phase ^ 1, watch) ? 1 : 0;
@@ -385,14 +419,18 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = sbase + L::OFF_SCALE + slot * L::SLOT_BYTES + lane * 4;
+                    uint32_t dst = sbase + L::OFF_SCALE + slot * L::SLOT_BYTES + lane * 4;
+                    const int kb1 = min(kb0 + L::GROUP, p.k_blocks);
+#pragma unroll 1
+                    for (int kb = kb0; kb < kb1; ++kb, dst += L::BLOCK_BYTES) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        cp_async_4(dst + 128 * i, ra[i] + kb * p.sa_k);
-                    if (COLV || lane < 2) {
+                        for (int i = 0; i < 4; ++i)
+                            cp_async_4(dst + 128 * i, ra[i] + kb * p.sa_k);
+                        if (COLV || lane < 2) {
 #pragma unroll
-                        for (int i = 0; i < NC; ++i)
-                            cp_async_4(dst + 512 + 128 * i, cb[i] + kb * p.sb_k);
+                            for (int i = 0; i < NC; ++i)
+                                cp_async_4(dst + 512 + 128 * i, cb[i] + kb * p.sb_k);
+                        }
                     }
                     cp_async_mbar_arrive(sfull_bar(slot));
                     if (++slot == L::SLOTS) {
@@ -402,6 +440,33 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 }
             }
             cp_async_wait_all();
+        } else if (warp == 3) {
+            // -------------------------------------------- herald
+            // Waits on the barriers of each K block for the epilogue warps and
+            // lets them go on through a hardware barrier.  After a wait that
+            // ran out it goes through the barriers without waiting, so that
+            // every warp reaches the end.
+            int stage = 0, slot = 0;
+            uint32_t phase = 0, slot_phase = 0;
+            bool ok = true;
+            for (int t = unit; t < p.num_tiles; t += num_units) {
+#pragma unroll 1
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (kb % L::GROUP == 0) {
+                        ok = ok && fp8_wait_warp(sfull_bar(slot), slot_phase, watch);
+                        if (++slot == L::SLOTS) {
+                            slot = 0;
+                            slot_phase ^= 1;
+                        }
+                    }
+                    ok = ok && fp8_wait_warp(done_bar(stage), phase, watch);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    bar_sync(F8_HERALD_BAR, 32 * (F8_EPI_WARPS + 1));
+                }
+            }
         }
     } else {
         // ------------------------------------------------ promotion, epilogue
@@ -411,44 +476,49 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         const int half = ew >> 2;      // column half of the tile
         const uint32_t tempty0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
         int buf = 0, slot = 0;
-        uint32_t buf_phase = 0, slot_phase = 0;
-        bool ok = true;
-        for (int t = unit; ok && t < p.num_tiles; t += num_units) {
+        for (int t = unit; t < p.num_tiles; t += num_units) {
             int mb, nb;
             tile_coords(t, mb, nb);
+            const uint32_t t_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                    static_cast<uint32_t>(half * COLS);
             const int row = mb * TILE_M + static_cast<int>(rank) * TC_BM + q * 32 + static_cast<int>(lane);
             const int col0 = nb * BN + half * COLS;
             uint64_t acc[COLS / 2];
 #pragma unroll
             for (int i = 0; i < COLS / 2; ++i)
                 acc[i] = 0;
-#pragma unroll 1
-            for (int kb = 0; kb < p.k_blocks; ++kb) {
-                int w = 1;
-                if (lane == 0)
-                    w = tc_wait(sfull_bar(slot), slot_phase, watch) &&
-                                tc_wait(tfull_bar(buf), buf_phase, watch)
-                            ? 1
-                            : 0;
-                if (!__shfl_sync(0xffffffffu, w, 0)) {
-                    ok = false;
-                    break;
-                }
+            // Tensor memory is read in chunks of 32 columns, each load issued
+            // before the arithmetic of the chunk before it, across K blocks
+            // as well: the next block's first chunk and scales are fetched
+            // before the last chunk's arithmetic.
+            constexpr int NCH = COLS / 32;
+            uint32_t v[2][32];
+            float rs = 0.0f;
+            uint32_t caddr = 0;
+            auto begin = [&](int kb) {
+                bar_sync(F8_HERALD_BAR, 32 * (F8_EPI_WARPS + 1));
                 tc_fence_after();
-                const uint32_t saddr = sbase + L::OFF_SCALE + slot * L::SLOT_BYTES;
-                const uint32_t caddr = saddr + 512 + (COLV ? half * COLS * 4 : half * 4);
-                float rs = ld_shared_f32(saddr + (q * 32 + lane) * 4);
+                tmem_ld_32x32b_x32(t_base + static_cast<uint32_t>(buf * BN), v[0]);
+                const uint32_t saddr =
+                    sbase + L::OFF_SCALE + slot * L::SLOT_BYTES + (kb % L::GROUP) * L::BLOCK_BYTES;
+                caddr = saddr + 512 + (COLV ? half * COLS * 4 : half * 4);
+                rs = ld_shared_f32(saddr + (q * 32 + lane) * 4);
                 if constexpr (!COLV)
                     rs *= ld_shared_f32(caddr);
+            };
+            begin(0);
+#pragma unroll 1
+            for (int kb = 0; kb < p.k_blocks; ++kb) {
                 const uint64_t rs2 = pack_f32x2(__float_as_uint(rs), __float_as_uint(rs));
-                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                       static_cast<uint32_t>(buf * BN + half * COLS);
-                uint32_t v[2][32];
-                tmem_ld_32x32b_x32(taddr, v[0]);
+                const uint32_t taddr = t_base + static_cast<uint32_t>(buf * BN);
+                const uint32_t cols = caddr;
+                const bool more = kb + 1 < p.k_blocks;
+                const bool slot_end = (kb + 1) % L::GROUP == 0 || !more;
+                const uint32_t sempty = sempty_bar(slot);
 #pragma unroll
-                for (int c = 0; c < COLS / 32; ++c) {
+                for (int c = 0; c < NCH; ++c) {
                     tmem_wait_ld();
-                    if (c + 1 < COLS / 32) {
+                    if (c + 1 < NCH) {
                         tmem_ld_32x32b_x32(taddr + (c + 1) * 32, v[(c + 1) & 1]);
                     } else {
                         tc_fence_before();
@@ -459,6 +529,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                             else
                                 mbar_arrive(tempty0 + 8u * buf);
                         }
+                        if (++buf == NBUF)
+                            buf = 0;
+                        if (slot_end && ++slot == L::SLOTS)
+                            slot = 0;
+                        if (more)
+                            begin(kb + 1);
                     }
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
@@ -467,7 +543,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                             uint32_t f[4];
                             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                          : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-                                         : "r"(caddr + (c * 32 + 2 * i) * 4));
+                                         : "r"(cols + (c * 32 + 2 * i) * 4));
                             s0 = fmul2(rs2, pack_f32x2(f[0], f[1]));
                             s1 = fmul2(rs2, pack_f32x2(f[2], f[3]));
                         }
@@ -476,22 +552,15 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                               s1);
                     }
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(sempty_bar(slot));
-                if (++slot == L::SLOTS) {
-                    slot = 0;
-                    slot_phase ^= 1;
-                }
-                if (++buf == NBUF) {
-                    buf = 0;
-                    buf_phase ^= 1;
+                if (slot_end) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(sempty);
                 }
             }
-            if (!ok)
-                break;
+            const bool stored = !*abort_flag;  // an unfinished tile is not written
             // ---- the finished tile: alpha, beta, rounding to the output type
-            if (row < p.M) {
+            if (stored && row < p.M) {
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c) {
                     float o[32];
