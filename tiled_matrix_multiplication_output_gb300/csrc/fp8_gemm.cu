@@ -17,8 +17,8 @@ namespace {
 constexpr int kMaxDevices = 64;
 
 // The stored matrix of an operand (outer x K, or K x outer when MN-major) in
-// boxes of 128 x box_rows bytes, 128-byte swizzle.  The row pitch is a
-// multiple of 16 bytes; the matrix itself may end anywhere.
+// boxes of box_outer x 128 of K, swizzled over the length of a box row.  The
+// row pitch is a multiple of 16 bytes; the matrix itself may end anywhere.
 bool encode_operand(CUtensorMap* map, const Fp8Operand& o, int64_t outer, int64_t K,
                     uint32_t box_outer)
 {
@@ -28,10 +28,11 @@ bool encode_operand(CUtensorMap* map, const Fp8Operand& o, int64_t outer, int64_
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(o.mn_major ? outer : K),
                                 static_cast<cuuint64_t>(o.mn_major ? K : outer)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.ld)};
-    const cuuint32_t box[2] = {128, o.mn_major ? static_cast<cuuint32_t>(F8_BK) : box_outer};
+    const cuuint32_t box[2] = {o.mn_major ? box_outer : F8_BK, o.mn_major ? F8_BK : box_outer};
     const cuuint32_t estr[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(o.data), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -82,7 +83,7 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
         units_cap = max_units[dev];
     }
     CUtensorMap ta, tb;
-    if (!encode_operand(&ta, l.a, l.M, l.K, 128) || !encode_operand(&tb, l.b, l.N, l.K, 128))
+    if (!encode_operand(&ta, l.a, l.M, l.K, 128) || !encode_operand(&tb, l.b, l.N, l.K, 128 / L::SUB))
         return cudaErrorNotSupported;
     Fp8Params p{};
     p.M = l.M;
@@ -96,7 +97,7 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
     p.num_tiles = static_cast<int>(tiles);
     p.k_blocks = (l.K + F8_BK - 1) / F8_BK;
     p.group_m = 8;
-    p.idesc = fp8_idesc(l.a.type, l.b.type, TC_BM * CG, BN, l.a.mn_major, l.b.mn_major);
+    p.idesc = fp8_idesc(l.a.type, l.b.type, TC_BM * CG, BN / L::SUB, l.a.mn_major, l.b.mn_major);
     p.a_mn = l.a.mn_major;
     p.b_mn = l.b.mn_major;
     p.sa = l.a.scale;

@@ -50,7 +50,7 @@ constexpr int F8_BK = 128;       // K per step and per scale block
 constexpr int F8_THREADS = 384;  // warps 0-3: copies, MMA, scales, herald; 4-11: epilogue
 constexpr int F8_EPI_WARP0 = 4;
 constexpr int F8_EPI_WARPS = 8;
-constexpr int F8_HERALD_BAR = 1;  // hardware barrier of the herald and the epilogue warps
+constexpr int F8_HERALD_BAR = 1;  // hardware barriers of the herald and the epilogue warps
 constexpr int F8_BOX = 128 * F8_BK;  // bytes of one operand box
 // Registers: 384 threads are launched with 168 each (64,512 in all); the
 // first warpgroup keeps 72 and the two epilogue warpgroups get 216 each:
@@ -92,12 +92,15 @@ struct Fp8Layout {
     static constexpr int SLOT_BYTES = GROUP * BLOCK_BYTES;
     static constexpr int OFF_SCALE = STAGES * STAGE;
     static constexpr int OFF_BAR = OFF_SCALE + SLOTS * SLOT_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + NBUF + 2 * SLOTS + 1;
+    // A K block's MMAs are issued as SUB groups of BN / SUB columns, each
+    // with its own barriers.
+    static constexpr int SUB = CG;
+    static constexpr int NUM_BARS = STAGES * (1 + SUB) + NBUF * SUB + 2 * SLOTS + 1;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
     static constexpr int BYTES = OFF_MISC + 16;
     static constexpr int SMEM_ALLOC = BYTES + 1024;
     static constexpr uint32_t TMEM_COLS = NBUF * BN;
-    static_assert(BN / CG == 128, "each CTA holds one 128-row box of B");
+    static_assert(BN / CG == 128, "each CTA holds 128 rows of B");
     static_assert(SMEM_ALLOC <= 232448, "exceeds 227 KiB of dynamic shared memory");
 };
 
@@ -109,6 +112,15 @@ __host__ __device__ constexpr uint32_t fp8_idesc(int a_type, int b_type, int m, 
     return (1u << 4) | (static_cast<uint32_t>(a_type) << 7) | (static_cast<uint32_t>(b_type) << 10) |
            ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// The constant part of an operand box's shared-memory descriptor: offsets,
+// version, and the swizzle mode (128 or 64 bytes, the length of a row).
+__device__ __forceinline__ uint64_t fp8_desc_hi(uint32_t row_bytes, bool mn)
+{
+    const uint64_t lbo = mn ? F8_BOX : 16, sbo = 8 * row_bytes;
+    return ((lbo >> 4) << 16) | ((sbo >> 4) << 32) | (1ull << 46) |
+           (static_cast<uint64_t>(row_bytes == 128 ? 2 : 4) << 61);
 }
 
 // alpha * v + beta * C for a run of `N` values of one row, stored in OutT.
@@ -201,7 +213,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     using L = Fp8Layout<CG, BN, STAGES>;
     constexpr int TILE_M = TC_BM * CG;
     constexpr int NBUF = L::NBUF;
+    constexpr int SUB = L::SUB;
     constexpr int COLS = BN / 2;  // columns of the tile per epilogue thread
+    constexpr int HERALD_THREADS = 32 * (F8_EPI_WARPS / SUB + 1);
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -209,13 +223,14 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + L::OFF_BAR;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
-    // The MMAs of the K block in stage s have completed: its operands may be
-    // overwritten and its product read.
-    auto done_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
-    auto sfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + NBUF + i); };
-    auto sempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + NBUF + L::SLOTS + i); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + NBUF + 2 * L::SLOTS);
+    // Group j of the MMAs on stage s has completed (and with the last group
+    // all of them): its product can be read, the stage overwritten.
+    auto done_bar = [&](int s, int j) { return bar0 + 8u * (STAGES + s * SUB + j); };
+    auto tempty_bar = [&](int b, int j) { return bar0 + 8u * (STAGES * (1 + SUB) + b * SUB + j); };
+    const uint32_t sbar0 = bar0 + 8u * (STAGES * (1 + SUB) + NBUF * SUB);
+    auto sfull_bar = [&](int i) { return sbar0 + 8u * i; };
+    auto sempty_bar = [&](int i) { return sbar0 + 8u * (L::SLOTS + i); };
+    const uint32_t drain_bar = sbar0 + 8u * (2 * L::SLOTS);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
 
@@ -239,10 +254,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(done_bar(s), 1);
+            for (int j = 0; j < SUB; ++j)
+                mbar_init(done_bar(s, j), 1);
         }
         for (int b = 0; b < NBUF; ++b)
-            mbar_init(tempty_bar(b), F8_EPI_WARPS * CG);
+            for (int j = 0; j < SUB; ++j)
+                mbar_init(tempty_bar(b, j), F8_EPI_WARPS / SUB * CG);
         for (int i = 0; i < L::SLOTS; ++i) {
             mbar_init(sfull_bar(i), 32);
             mbar_init(sempty_bar(i), F8_EPI_WARPS);
@@ -280,9 +297,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 int mb, nb;
                 tile_coords(t, mb, nb);
                 const int a_row = mb * TILE_M + static_cast<int>(rank) * TC_BM;
-                const int b_row = nb * BN + static_cast<int>(rank) * 128;
+                // Group j of the columns takes 128 / SUB rows of B from each CTA.
+                const int b_row = nb * BN + static_cast<int>(rank) * (128 / SUB);
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!tc_wait(done_bar(stage), phase ^ 1, watch)) {
+                    if (!tc_wait(done_bar(stage, SUB - 1), phase ^ 1, watch)) {
                         ok = false;
                         break;
                     }
@@ -302,10 +320,15 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                             load(dA, &tmA, a_row, k0);
                         else
                             load(dA, &tmA, k0, a_row);
-                        if (p.b_mn)
-                            load(dA + F8_BOX, &tmB, b_row, k0);
-                        else
-                            load(dA + F8_BOX, &tmB, k0, b_row);
+#pragma unroll
+                        for (int j = 0; j < SUB; ++j) {
+                            const uint32_t dB = dA + F8_BOX + j * (F8_BOX / SUB);
+                            const int o = b_row + j * 128;
+                            if (p.b_mn)
+                                load(dB, &tmB, o, k0);
+                            else
+                                load(dB, &tmB, k0, o);
+                        }
 #pragma unroll
                         for (int s = 0; s < STAGES; ++s)
                             issued[s] += (s == stage);
@@ -334,41 +357,48 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             // The whole warp runs the loop and one elected lane issues: the
             // descriptors then live in uniform registers, where the
             // instruction takes them from.
-            // Descriptor of a 32-wide K slice of a 16 KiB operand box.  K-major:
+            // Descriptor of a 32-wide K slice of an operand box.  K-major:
             // 128-byte rows, 8-row groups 1024 bytes apart, 32 bytes along
-            // the row per slice.  MN-major: 128 outer values per 128-byte
-            // row (one swizzle atom, so the leading offset is unused), 8-row
-            // K groups 1024 bytes apart, 32 rows (4 KiB) per slice.
-            const uint64_t hi = (1ull << 46) | (2ull << 61) | (static_cast<uint64_t>(1024 >> 4) << 32);
-            const uint64_t a_hi = hi | (static_cast<uint64_t>((p.a_mn ? F8_BOX : 16) >> 4) << 16);
-            const uint64_t b_hi = hi | (static_cast<uint64_t>((p.b_mn ? F8_BOX : 16) >> 4) << 16);
-            const uint32_t a_step = (p.a_mn ? 4096 : 32) >> 4;
-            const uint32_t b_step = (p.b_mn ? 4096 : 32) >> 4;
+            // the row per slice.  MN-major: a row holds the box's 128 (or,
+            // in groups, 64) outer values, one swizzle atom of as many
+            // bytes, so the leading offset is unused; 8-row K groups follow
+            // each other, 32 rows per slice.
+            constexpr uint32_t B_ROW = 128 / SUB;  // bytes of an MN-major row of B
+            const uint64_t a_hi = fp8_desc_hi(128, p.a_mn);
+            const uint64_t b_hi = fp8_desc_hi(p.b_mn ? B_ROW : 128, p.b_mn);
+            const uint32_t a_step = (p.a_mn ? 32 * 128 : 32) >> 4;
+            const uint32_t b_step = (p.b_mn ? 32 * B_ROW : 32) >> 4;
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
             bool ok = true;
             for (int t = unit; ok && t < p.num_tiles; t += num_units) {
 #pragma unroll 1
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    ok = fp8_wait_warp(tempty_bar(buf), buf_phase ^ 1, watch) &&
-                         fp8_wait_warp(full_bar(stage), phase, watch);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
+                    ok = fp8_wait_warp(full_bar(stage), phase, watch);
                     const uint32_t a0 = (sbase + stage * L::STAGE) >> 4;
                     const uint32_t b0 = a0 + (F8_BOX >> 4);
                     const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
-                    if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < F8_BK / 32; ++k)
-                            tc_mma_f8<CG>(d, a_hi | ((a0 + k * a_step) & 0x3FFF),
-                                          b_hi | ((b0 + k * b_step) & 0x3FFF), p.idesc, k != 0);
-                        if constexpr (CG == 2)
-                            tc_commit_pair(done_bar(stage), 0x3);
-                        else
-                            tc_commit(done_bar(stage));
+                    for (int j = 0; j < SUB; ++j) {
+                        ok = ok && fp8_wait_warp(tempty_bar(buf, j), buf_phase ^ 1, watch);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < F8_BK / 32; ++k)
+                                tc_mma_f8<CG>(d + j * (BN / SUB), a_hi | ((a0 + k * a_step) & 0x3FFF),
+                                              b_hi | ((b0 + j * (F8_BOX / SUB >> 4) + k * b_step) & 0x3FFF),
+                                              p.idesc, k != 0);
+                            if constexpr (CG == 2)
+                                tc_commit_pair(done_bar(stage, j), 0x3);
+                            else
+                                tc_commit(done_bar(stage, j));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok)
+                        break;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -459,12 +489,15 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                             slot_phase ^= 1;
                         }
                     }
-                    ok = ok && fp8_wait_warp(done_bar(stage), phase, watch);
+#pragma unroll
+                    for (int j = 0; j < SUB; ++j) {
+                        ok = ok && fp8_wait_warp(done_bar(stage, j), phase, watch);
+                        bar_sync(F8_HERALD_BAR + j, HERALD_THREADS);
+                    }
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
-                    bar_sync(F8_HERALD_BAR, 32 * (F8_EPI_WARPS + 1));
                 }
             }
         }
@@ -474,7 +507,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         const int ew = warp - F8_EPI_WARP0;
         const int q = warp & 3;        // TMEM lane quarter
         const int half = ew >> 2;      // column half of the tile
-        const uint32_t tempty0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
+        const int group = SUB == 2 ? half : 0;  // the MMA group that fills this warp's columns
+        const uint32_t tempty0 =
+            (CG == 2) ? mapa_shared(tempty_bar(0, group), 0) : tempty_bar(0, group);
         int buf = 0, slot = 0;
         for (int t = unit; t < p.num_tiles; t += num_units) {
             int mb, nb;
@@ -496,7 +531,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             float rs = 0.0f;
             uint32_t caddr = 0;
             auto begin = [&](int kb) {
-                bar_sync(F8_HERALD_BAR, 32 * (F8_EPI_WARPS + 1));
+                bar_sync(F8_HERALD_BAR + group, HERALD_THREADS);
                 tc_fence_after();
                 tmem_ld_32x32b_x32(t_base + static_cast<uint32_t>(buf * BN), v[0]);
                 const uint32_t saddr =
@@ -525,9 +560,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         __syncwarp();
                         if (lane == 0) {
                             if constexpr (CG == 2)
-                                mbar_arrive_cluster_relaxed(tempty0 + 8u * buf);
+                                mbar_arrive_cluster_relaxed(tempty0 + 8u * SUB * buf);
                             else
-                                mbar_arrive(tempty0 + 8u * buf);
+                                mbar_arrive(tempty0 + 8u * SUB * buf);
                         }
                         if (++buf == NBUF)
                             buf = 0;
