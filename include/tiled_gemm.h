@@ -424,6 +424,51 @@ int gemm_fp8(const gemm_fp8_matrix_t* A, const gemm_fp8_matrix_t* B, void* C, in
              int64_t M, int64_t N, int64_t K, float alpha, float beta, gemm_dtype_t out_dtype,
              void* stream);
 
+/* ------------------------------------------------------ orthogonalisation
+ *
+ * gemm_newton_schulz -- the update of the Muon optimiser from a gradient's
+ * running mean: every matrix G of a batch is brought towards the nearest
+ * matrix with orthonormal rows (or columns, where it has more rows) by
+ * matrix products alone.
+ *
+ *     X = G / (|G|_F + eps);   `steps` times, with that step's (a, b, c):
+ *     A = X X^T,  B = b A + c A A,  X = a X + B X;   O = X
+ *
+ * (on the shorter side: A = X^T X and X = a X + X B where rows > cols).
+ * Each singular value s goes to a s + b s^3 + c s^5 a step, the singular
+ * vectors stay.  The pages have no counterpart.
+ *
+ * G and O: `batch` matrices of rows x cols, row pitches ldg and ldo and batch
+ * pitches batch_stride_g and batch_stride_o in elements, element alignment;
+ * F32, F16 or BF16 each.  O may be G itself (same type and pitches); other
+ * overlap is not allowed.  coefficients: host array of steps x (a, b, c),
+ * read during the call; steps 1 to 32.
+ *
+ * Accuracy.  Products take FP16 operands and accumulate in FP32, X is kept
+ * to 22 bits: the result is about 2e-3 (relative, in the 2-norm of all
+ * elements) from the definition in exact arithmetic, before the rounding to
+ * out_dtype.  Singular values must stay below 16 throughout, as they do for
+ * coefficients that converge.  A G whose norm is not finite in FP32 gives
+ * NaN throughout its O.  A zero G gives zeros (NaN for eps == 0).
+ *
+ * workspace: device memory of gemm_newton_schulz_workspace_size(batch, rows,
+ * cols) bytes, 256-byte aligned; scratch, and not shared by calls that
+ * overlap in time.  Empty batches and matrices are no-ops.  The result is
+ * identical run to run, and does not depend on the other matrices of the
+ * batch or on where in it a matrix is, but may depend on the batch's size.
+ *
+ * Returns GEMM_OK, GEMM_ERR_INVALID_VALUE (null pointer, bad size, pitch,
+ * enum, steps or batch above 65535, a coefficient or eps that is not finite,
+ * negative eps, workspace missing, misaligned or too small),
+ * GEMM_ERR_UNSUPPORTED (too many tiles) or GEMM_ERR_CUDA.
+ */
+size_t gemm_newton_schulz_workspace_size(int64_t batch, int64_t rows, int64_t cols);
+int gemm_newton_schulz(const void* G, int64_t ldg, int64_t batch_stride_g, void* O, int64_t ldo,
+                       int64_t batch_stride_o, int64_t batch, int64_t rows, int64_t cols,
+                       gemm_dtype_t in_dtype, gemm_dtype_t out_dtype, int steps,
+                       const float* coefficients, float eps, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /*
  * gemm_device_status -- synchronize `stream`, then read and clear the status
  * word of the current device.  Returns GEMM_OK, GEMM_ERR_TIMEOUT if a

@@ -16,4 +16,6 @@ from .binding import (  # noqa: F401
     load_library, matmul, matmul_splitk,
     gemm_fp8, gemm_fp8_quantize, gemm_fp8_quantize_pair, matmul_fp8, quantize_fp8,
     quantize_fp8_pair,
+    NEWTON_SCHULZ_COEFFICIENTS, gemm_newton_schulz, gemm_newton_schulz_workspace_size,
+    newton_schulz,
 )

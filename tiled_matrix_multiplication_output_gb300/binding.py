@@ -80,6 +80,10 @@ _SIGNATURES = {
                                 _p, _i64, _p], _int),
     "gemm_fp8": ([ctypes.POINTER(Fp8Matrix), ctypes.POINTER(Fp8Matrix), _p, _i64, _i64, _i64,
                   _i64, ctypes.c_float, ctypes.c_float, _int, _p], _int),
+    "gemm_newton_schulz_workspace_size": ([_i64, _i64, _i64], ctypes.c_size_t),
+    "gemm_newton_schulz": ([_p, _i64, _i64, _p, _i64, _i64, _i64, _i64, _i64, _int, _int, _int,
+                            ctypes.POINTER(ctypes.c_float), ctypes.c_float, _p, ctypes.c_size_t,
+                            _p], _int),
     "gemm_device_status": ([_p], _int),
     "gemm_debug_config": ([_i64, _int], _int),
     "gemm_launch_count": ([], ctypes.c_uint64),
@@ -259,6 +263,19 @@ def gemm_fp8_quantize_pair(X, ldx, rows, cols, in_dtype, f8, Q_row, ldq_row, S_r
 def gemm_fp8(A, B, C, ldc, M, N, K, alpha, beta, out_dtype, stream=None) -> int:
     """A and B are Fp8Matrix structures (or None)."""
     return load_library().gemm_fp8(A, B, C, ldc, M, N, K, alpha, beta, out_dtype, stream)
+
+
+def gemm_newton_schulz_workspace_size(batch, rows, cols) -> int:
+    return load_library().gemm_newton_schulz_workspace_size(batch, rows, cols)
+
+
+def gemm_newton_schulz(G, ldg, batch_stride_g, O, ldo, batch_stride_o, batch, rows, cols, in_dtype,
+                       out_dtype, steps, coefficients, eps, workspace, workspace_bytes,
+                       stream=None) -> int:
+    """coefficients: a ctypes array of 3 * steps floats (or None)."""
+    return load_library().gemm_newton_schulz(G, ldg, batch_stride_g, O, ldo, batch_stride_o, batch,
+                                             rows, cols, in_dtype, out_dtype, steps, coefficients,
+                                             eps, workspace, workspace_bytes, stream)
 
 
 def gemm_device_status(stream=None) -> int:
@@ -564,3 +581,73 @@ def matmul_fp8(a, a_scale, b, b_scale, op_a="n", op_b="t", out_dtype=None, out=N
     if rc != OK:
         raise GemmError(rc, "gemm_fp8")
     return out
+
+
+# ------------------------------------------------------------ orthogonalisation
+
+# Coefficients of one step that bring singular values from about 0.01 into
+# [0.7, 1.2] in five steps.
+NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps: float = 1e-7,
+                  out_dtype=None, out=None, workspace=None, stream=None):
+    """Orthogonalise a CUDA matrix (or a batch of them, 3-D) by Newton-Schulz
+    products, as the Muon optimiser does with a gradient's running mean:
+    X = G / (norm + eps), then `steps` times A = X X^T, X = a X + (b A + c A A) X.
+
+    G: FP32, FP16 or BF16, rows contiguous, any row and batch stride.
+    coefficients: one (a, b, c) for every step, or a sequence of `steps` of
+    them.  out_dtype defaults to G's type; `out` may supply the result (it
+    may be G itself).  workspace: a CUDA tensor of at least
+    gemm_newton_schulz_workspace_size(batch, rows, cols) bytes, allocated by
+    PyTorch unless given.  Accuracy: see gemm_newton_schulz in the header.
+    Returns the result without synchronizing."""
+    torch = _torch()
+    _check_batch(G, "G")
+    steps = int(steps)
+    if not 1 <= steps <= 32:
+        raise ValueError("steps must be between 1 and 32")
+    rows_of = list(coefficients)
+    if len(rows_of) == 3 and not hasattr(rows_of[0], "__len__"):
+        rows_of = [rows_of] * steps
+    if len(rows_of) != steps or any(len(r) != 3 for r in rows_of):
+        raise ValueError("coefficients are (a, b, c), or one such triple for each step")
+    coef = (ctypes.c_float * (3 * steps))(*[float(v) for r in rows_of for v in r])
+    rows, cols = G.shape[-2:]
+    batch = G.shape[0] if G.dim() == 3 else 1
+    if out is None:
+        odt = G.dtype if out_dtype is None else _out_dtype(out_dtype)
+        with _on_stream(stream):
+            out = torch.empty(G.shape, dtype=odt, device=G.device)
+    else:
+        _check_batch(out, "out")
+        if out.shape != G.shape or (out_dtype is not None and out.dtype != _out_dtype(out_dtype)):
+            raise ValueError("out must have G's shape and the output dtype")
+    if workspace is None:
+        with _on_stream(stream):
+            workspace = torch.empty(gemm_newton_schulz_workspace_size(batch, rows, cols),
+                                    dtype=torch.uint8, device=G.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    rc = gemm_newton_schulz(G.data_ptr(), _row_pitch(G), G.stride(0) if batch > 1 else 0,
+                            out.data_ptr(), _row_pitch(out), out.stride(0) if batch > 1 else 0,
+                            batch, rows, cols, dtype_code(G.dtype), dtype_code(out.dtype), steps,
+                            coef, eps, workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if rc != OK:
+        raise GemmError(rc, "gemm_newton_schulz")
+    return out
+
+
+def _row_pitch(x) -> int:
+    return x.stride(-2) if x.shape[-2] > 1 else x.shape[-1]
+
+
+def _check_batch(x, what):
+    torch = _torch()
+    if x.dim() not in (2, 3) or not x.is_cuda:
+        raise ValueError(f"{what} must be a 2-D or 3-D CUDA tensor")
+    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise TypeError(f"{what} must be FP32, FP16 or BF16")
+    _check_matrix(x if x.dim() == 2 else x[0] if x.shape[0] else x.new_empty((0, 0)), what)

@@ -177,31 +177,6 @@ __device__ __forceinline__ void fp8_store_row(OutT* dst, float* v, int n, const 
     }
 }
 
-// Bounded wait of a whole warp on an mbarrier phase: every lane polls, so no
-// branch diverges, and the poll does not suspend the warp.  These waits come
-// once per K block, and one lane waiting for the others with tc_wait (a
-// divergent loop, a suspending poll, a shuffle) cost about 300 cycles of the
-// 512 that a K block has.
-__device__ __forceinline__ bool fp8_wait_warp(uint32_t bar, uint32_t parity, const TcWatch& w)
-{
-    long long t0 = 0;
-    for (uint32_t n = 1;; ++n) {
-        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity)))
-            return true;
-        if ((n & 1023u) != 0)
-            continue;
-        // now and then: has another role given up, or the budget run out?
-        const long long now = clock64();
-        if (t0 == 0)
-            t0 = now;
-        const bool late = now - t0 > w.budget;
-        if (late)
-            tc_raise(w);
-        if (__any_sync(0xffffffffu, late || *w.abort_flag))
-            return false;
-    }
-}
-
 // COLV: the column operand has a scale for each column (a vector along the
 // tile's columns); otherwise one for 128 columns, the same for all of a
 // thread's columns.
@@ -374,13 +349,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             for (int t = unit; ok && t < p.num_tiles; t += num_units) {
 #pragma unroll 1
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    ok = fp8_wait_warp(full_bar(stage), phase, watch);
+                    ok = tc_wait_warp(full_bar(stage), phase, watch);
                     const uint32_t a0 = (sbase + stage * L::STAGE) >> 4;
                     const uint32_t b0 = a0 + (F8_BOX >> 4);
                     const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
 #pragma unroll
                     for (int j = 0; j < SUB; ++j) {
-                        ok = ok && fp8_wait_warp(tempty_bar(buf, j), buf_phase ^ 1, watch);
+                        ok = ok && tc_wait_warp(tempty_bar(buf, j), buf_phase ^ 1, watch);
                         if (!ok)
                             break;
                         tc_fence_after();
@@ -483,7 +458,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 #pragma unroll 1
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
                     if (kb % L::GROUP == 0) {
-                        ok = ok && fp8_wait_warp(sfull_bar(slot), slot_phase, watch);
+                        ok = ok && tc_wait_warp(sfull_bar(slot), slot_phase, watch);
                         if (++slot == L::SLOTS) {
                             slot = 0;
                             slot_phase ^= 1;
@@ -491,7 +466,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     }
 #pragma unroll
                     for (int j = 0; j < SUB; ++j) {
-                        ok = ok && fp8_wait_warp(done_bar(stage, j), phase, watch);
+                        ok = ok && tc_wait_warp(done_bar(stage, j), phase, watch);
                         bar_sync(F8_HERALD_BAR + j, HERALD_THREADS);
                     }
                     if (++stage == STAGES) {

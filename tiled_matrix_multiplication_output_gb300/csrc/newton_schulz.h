@@ -1,0 +1,33 @@
+// Internal launcher of the Newton-Schulz orthogonalisation (host side).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace tmmo {
+
+constexpr int NS_MAX_STEPS = 32;
+
+struct NsLaunch {
+    const void* G;
+    int64_t ldg, batch_g;   // elements from one row, one matrix, to the next
+    void* O;
+    int64_t ldo, batch_o;
+    int batch, rows, cols;
+    int in_dtype, out_dtype;
+    int steps;
+    const float* coefficients;  // host: steps x (a, b, c)
+    float eps;
+    void* workspace;        // 256-byte aligned, ns_workspace_bytes()
+    int num_sms;
+    int* status;
+    long long wait_budget;
+    int fault_skip_kblock;
+};
+
+size_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream);
+
+}  // namespace tmmo
