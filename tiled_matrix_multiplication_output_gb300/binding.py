@@ -11,10 +11,10 @@ call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
+import struct
 import threading
 
 from . import build as _build
@@ -56,6 +56,11 @@ class Fp8Matrix(ctypes.Structure):
                 ("scale_ld", _i64), ("op", _int)]
 
 
+# The same layout as bytes, which are quicker to make.
+_FP8_MATRIX = struct.Struct("@PqiiPqi4x")
+assert _FP8_MATRIX.size == ctypes.sizeof(Fp8Matrix)
+
+
 _SIGNATURES = {
     "gemm": ([_p, _p, _p, _i64, _i64, _i64, _int, _int, _p], _int),
     "gemm_ex": ([_p, _p, _p, _i64, _i64, _i64, _int, _int, _int, _p], _int),
@@ -78,8 +83,8 @@ _SIGNATURES = {
     "gemm_fp8_quantize": ([_p, _i64, _i64, _i64, _int, _int, _int, _p, _i64, _p, _i64, _p], _int),
     "gemm_fp8_quantize_pair": ([_p, _i64, _i64, _i64, _int, _int, _p, _i64, _p, _i64, _p, _i64,
                                 _p, _i64, _p], _int),
-    "gemm_fp8": ([ctypes.POINTER(Fp8Matrix), ctypes.POINTER(Fp8Matrix), _p, _i64, _i64, _i64,
-                  _i64, ctypes.c_float, ctypes.c_float, _int, _p], _int),
+    "gemm_fp8": ([_p, _p, _p, _i64, _i64, _i64, _i64, ctypes.c_float, ctypes.c_float, _int, _p],
+                 _int),
     "gemm_newton_schulz_workspace_size": ([_i64, _i64, _i64], ctypes.c_size_t),
     "gemm_newton_schulz": ([_p, _i64, _i64, _p, _i64, _i64, _i64, _i64, _i64, _int, _int, _int,
                             ctypes.POINTER(ctypes.c_float), ctypes.c_float, _p, ctypes.c_size_t,
@@ -261,7 +266,8 @@ def gemm_fp8_quantize_pair(X, ldx, rows, cols, in_dtype, f8, Q_row, ldq_row, S_r
 
 
 def gemm_fp8(A, B, C, ldc, M, N, K, alpha, beta, out_dtype, stream=None) -> int:
-    """A and B are Fp8Matrix structures (or None)."""
+    """A and B: Fp8Matrix structures, or the bytes of such."""
+    A, B = (ctypes.byref(m) if isinstance(m, Fp8Matrix) else m for m in (A, B))
     return load_library().gemm_fp8(A, B, C, ldc, M, N, K, alpha, beta, out_dtype, stream)
 
 
@@ -316,16 +322,32 @@ gemm_error_string = error_string
 
 # ------------------------------------------------------- PyTorch convenience
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_dtype_codes = None
+
+
+def _dtype_codes() -> dict:
+    global _torch_dtype_codes
+    if _torch_dtype_codes is None:
+        torch = _torch()
+        _torch_dtype_codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    return _torch_dtype_codes
 
 
 def dtype_code(dt) -> int:
-    torch = _torch()
     if isinstance(dt, str):
         return DTYPE_CODES[dt]
-    return {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[dt]
+    return _dtype_codes()[dt]
 
 
 def torch_dtype(code_or_name):
@@ -418,6 +440,10 @@ F8_CODES = {"e4m3": E4M3, "e5m2": E5M2}
 FP8_BLOCKS = {"row": 0, "col": 1, "tile": 2}
 
 
+def _empty(shape, dtype, device):
+    return _torch().empty(shape, dtype=dtype, device=device)
+
+
 def _out_dtype(out_dtype):
     torch = _torch()
     if out_dtype is None:
@@ -438,44 +464,61 @@ def _f8_code(dtype) -> int:
     raise TypeError(f"{dtype} is not an 8-bit floating-point type")
 
 
-def _on_stream(stream):
-    """A context in which PyTorch allocates for `stream` (memory freed later
-    is then reused in that stream's order only)."""
-    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+def _allocate(stream, make, *args):
+    """make(*args) with PyTorch allocating for `stream` (memory freed later is
+    then reused in that stream's order only)."""
+    if stream is None:
+        return make(*args)
+    with _torch().cuda.stream(stream):
+        return make(*args)
+
+
+def _stream_ptr(stream, x) -> int:
+    """The stream's address; by default the current one of x's device.  Asked
+    of PyTorch's C layer, 3 us less than building a Stream object: the calls
+    below take about 10 us of host time in all."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(x.get_device())
 
 
 def _check_matrix(x, what):
-    torch = _torch()
+    """Returns (rows, cols, row stride) of a 2-D CUDA tensor with contiguous rows."""
     if x.dim() != 2 or not x.is_cuda:
         raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    if x.device.index != torch.cuda.current_device():
+    if x.get_device() != _torch()._C._cuda_getDevice():
         raise ValueError(f"{what} is not on the current device")
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    rows, cols = x.shape
+    pitch, step = x.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what}'s rows must be contiguous")
-    if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+    if pitch < cols and rows > 1:
         raise ValueError(f"{what}'s rows must not overlap")
-
-
-def _pitch(x) -> int:
-    """Elements from one row of a 2-D tensor to the next (a single row has none of its own)."""
-    return x.stride(0) if x.shape[0] > 1 else -(-x.shape[1] // 16) * 16
+    # a single row has no pitch of its own
+    return rows, cols, pitch if rows > 1 else (cols + 15) // 16 * 16
 
 
 def _fp8_empty(rows, cols, f8, block, device):
-    """Uninitialised codes with a row pitch of a multiple of 16, and scales."""
+    """Uninitialised codes with a row pitch of a multiple of 16, their pitch,
+    scales and their pitch."""
     torch = _torch()
-    q = torch.empty((rows, -(-cols // 16) * 16), device=device,
-                    dtype=torch.float8_e4m3fn if f8 == E4M3 else torch.float8_e5m2)[:, :cols]
-    rb, cb = -(-rows // 128), -(-cols // 128)
-    shape = ((cb, rows), (rb, cols), (rb, cb))[block]
-    return q, torch.empty(shape, dtype=torch.float32, device=device)
+    ld = (cols + 15) // 16 * 16
+    q = torch.empty((rows, ld), device=device,
+                    dtype=torch.float8_e4m3fn if f8 == E4M3 else torch.float8_e5m2)
+    if ld != cols:
+        q = q[:, :cols]
+    rb, cb = (rows + 127) // 128, (cols + 127) // 128
+    n, lds = ((cb, rows), (rb, cols), (rb, cb))[block]
+    return q, ld, torch.empty((n, lds), dtype=torch.float32, device=device), lds
 
 
 def _quantize_input(x):
-    torch = _torch()
-    _check_matrix(x, "x")
-    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+    """(rows, cols, row stride, type code) of a tensor to quantise."""
+    shape = _check_matrix(x, "x")
+    code = _dtype_codes().get(x.dtype)
+    if code is None:
         raise TypeError("x must be FP32, FP16 or BF16")
+    return (*shape, code)
 
 
 def quantize_fp8(x, block: str = "row", dtype="e4m3", stream=None):
@@ -490,16 +533,15 @@ def quantize_fp8(x, block: str = "row", dtype="e4m3", stream=None):
     codes are a (rows, cols) view of rows padded to 16 bytes, the form
     matmul_fp8 takes.  The exact definition is gemm_fp8_quantize's.
     """
-    _quantize_input(x)
-    if block not in FP8_BLOCKS:
+    rows, cols, ldx, code = _quantize_input(x)
+    kind = FP8_BLOCKS.get(block)
+    if kind is None:
         raise ValueError(f"unknown block shape {block!r}")
-    rows, cols = x.shape
-    f8, b = _f8_code(dtype), FP8_BLOCKS[block]
-    with _on_stream(stream):
-        q, s = _fp8_empty(rows, cols, f8, b, x.device)
-    rc = gemm_fp8_quantize(x.data_ptr(), _pitch(x), rows, cols, dtype_code(x.dtype), f8, b,
-                           q.data_ptr(), _pitch(q), s.data_ptr(), s.shape[1],
-                           _stream_handle(stream))
+    f8 = _f8_code(dtype)
+    q, ldq, s, lds = _allocate(stream, _fp8_empty, rows, cols, f8, kind, x.device)
+    rc = (_lib or load_library()).gemm_fp8_quantize(
+        x.data_ptr(), ldx, rows, cols, code, f8, kind, q.data_ptr(), ldq, s.data_ptr(), lds,
+        _stream_ptr(stream, x))
     if rc != OK:
         raise GemmError(rc, "gemm_fp8_quantize")
     return q, s
@@ -508,40 +550,37 @@ def quantize_fp8(x, block: str = "row", dtype="e4m3", stream=None):
 def quantize_fp8_pair(x, dtype="e4m3", stream=None):
     """quantize_fp8 with "row" and with "col" blocks from one read of x:
     ((codes, scales), (codes, scales))."""
-    _quantize_input(x)
-    rows, cols = x.shape
+    rows, cols, ldx, code = _quantize_input(x)
     f8 = _f8_code(dtype)
-    with _on_stream(stream):
-        qr, sr = _fp8_empty(rows, cols, f8, 0, x.device)
-        qc, sc = _fp8_empty(rows, cols, f8, 1, x.device)
-    rc = gemm_fp8_quantize_pair(x.data_ptr(), _pitch(x), rows, cols, dtype_code(x.dtype), f8,
-                                qr.data_ptr(), _pitch(qr), sr.data_ptr(), sr.shape[1],
-                                qc.data_ptr(), _pitch(qc), sc.data_ptr(), sc.shape[1],
-                                _stream_handle(stream))
+    qr, ldr, sr, ldsr = _allocate(stream, _fp8_empty, rows, cols, f8, 0, x.device)
+    qc, ldc, sc, ldsc = _allocate(stream, _fp8_empty, rows, cols, f8, 1, x.device)
+    rc = (_lib or load_library()).gemm_fp8_quantize_pair(
+        x.data_ptr(), ldx, rows, cols, code, f8, qr.data_ptr(), ldr, sr.data_ptr(), ldsr,
+        qc.data_ptr(), ldc, sc.data_ptr(), ldsc, _stream_ptr(stream, x))
     if rc != OK:
         raise GemmError(rc, "gemm_fp8_quantize_pair")
     return (qr, sr), (qc, sc)
 
 
 def _fp8_operand(q, s, op, k_rows, what):
-    """The Fp8Matrix of codes q and scales s; k_rows: q's rows run along K."""
+    """(stored rows, stored columns, the bytes of its gemm_fp8_matrix_t) of
+    codes q and scales s; k_rows: q's rows run along K."""
+    rows, cols, ld = _check_matrix(q, what)
     torch = _torch()
-    _check_matrix(q, what)
     if s.dtype is not torch.float32 or not s.is_cuda or s.dim() != 2 or not s.is_contiguous():
         raise ValueError(f"{what}'s scales must be a contiguous 2-D FP32 CUDA tensor")
-    rows, cols = q.shape
     rb, cb = (rows + 127) // 128, (cols + 127) // 128
-    shape = tuple(s.shape)
-    if shape == ((cb, rows) if k_rows else (rb, cols)):
+    n, lds = s.shape
+    if (n, lds) == ((cb, rows) if k_rows else (rb, cols)):
         block = 0 if k_rows else 1
-    elif shape == (rb, cb):
+    elif (n, lds) == (rb, cb):
         block = 2
     else:
-        raise ValueError(f"{what}'s scales have shape {shape}: expected "
+        raise ValueError(f"{what}'s scales have shape {(n, lds)}: expected "
                          f"{(cb, rows) if k_rows else (rb, cols)} (a vector along the "
                          f"contraction) or {(rb, cb)} (128 x 128 blocks)")
-    return Fp8Matrix(q.data_ptr(), _pitch(q), _f8_code(q.dtype), block, s.data_ptr(), shape[1],
-                     OPS[op])
+    return rows, cols, _FP8_MATRIX.pack(q.data_ptr(), ld, _f8_code(q.dtype), block, s.data_ptr(),
+                                        lds, op)
 
 
 def matmul_fp8(a, a_scale, b, b_scale, op_a="n", op_b="t", out_dtype=None, out=None, alpha=1.0,
@@ -556,28 +595,29 @@ def matmul_fp8(a, a_scale, b, b_scale, op_a="n", op_b="t", out_dtype=None, out=N
     otherwise; "tile" blocks serve both.  `out` may supply C (rows
     contiguous, any row stride); beta != 0 needs it.  out_dtype defaults to
     FP32, or to out's type.  Returns C without synchronizing."""
-    torch = _torch()
-    if op_a not in OPS or op_b not in OPS:
+    ta, tb = OPS.get(op_a), OPS.get(op_b)
+    if ta is None or tb is None:
         raise ValueError("op_a and op_b are \"n\" or \"t\"")
-    A = _fp8_operand(a, a_scale, op_a, op_a == "n", "a")
-    B = _fp8_operand(b, b_scale, op_b, op_b == "t", "b")
-    M, K = (a.shape[1], a.shape[0]) if op_a == "t" else a.shape
-    K2, N = (b.shape[1], b.shape[0]) if op_b == "t" else b.shape
+    M, K, A = _fp8_operand(a, a_scale, ta, not ta, "a")
+    K2, N, B = _fp8_operand(b, b_scale, tb, tb, "b")
+    if ta:
+        M, K = K, M
+    if tb:
+        K2, N = N, K2
     if K != K2:
         raise ValueError("inner dimensions differ")
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out")
-        with _on_stream(stream):
-            out = torch.empty((M, N), dtype=_out_dtype(out_dtype), device=a.device)
+        out = _allocate(stream, _empty, (M, N), _out_dtype(out_dtype), a.device)
+        ldc = N
     else:
-        _check_matrix(out, "out")
-        if tuple(out.shape) != (M, N) or (out_dtype is not None and
-                                          out.dtype != _out_dtype(out_dtype)):
+        rows, cols, ldc = _check_matrix(out, "out")
+        if (rows, cols) != (M, N) or (out_dtype is not None and
+                                      out.dtype != _out_dtype(out_dtype)):
             raise ValueError("out must be an (M, N) tensor of the output dtype")
-    rc = gemm_fp8(ctypes.byref(A), ctypes.byref(B), out.data_ptr(),
-                  out.stride(0) if M > 1 else N, M, N, K, alpha, beta, dtype_code(out.dtype),
-                  _stream_handle(stream))
+    rc = (_lib or load_library()).gemm_fp8(A, B, out.data_ptr(), ldc, M, N, K, alpha, beta,
+                                           dtype_code(out.dtype), _stream_ptr(stream, a))
     if rc != OK:
         raise GemmError(rc, "gemm_fp8")
     return out
@@ -603,51 +643,48 @@ def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, ep
     gemm_newton_schulz_workspace_size(batch, rows, cols) bytes, allocated by
     PyTorch unless given.  Accuracy: see gemm_newton_schulz in the header.
     Returns the result without synchronizing."""
-    torch = _torch()
-    _check_batch(G, "G")
-    steps = int(steps)
+    batch, rows, cols, ldg, stride_g = _check_batch(G, "G")
     if not 1 <= steps <= 32:
         raise ValueError("steps must be between 1 and 32")
-    rows_of = list(coefficients)
-    if len(rows_of) == 3 and not hasattr(rows_of[0], "__len__"):
-        rows_of = [rows_of] * steps
-    if len(rows_of) != steps or any(len(r) != 3 for r in rows_of):
-        raise ValueError("coefficients are (a, b, c), or one such triple for each step")
-    coef = (ctypes.c_float * (3 * steps))(*[float(v) for r in rows_of for v in r])
-    rows, cols = G.shape[-2:]
-    batch = G.shape[0] if G.dim() == 3 else 1
+    if len(coefficients) == 3 and not hasattr(coefficients[0], "__len__"):
+        values = (*coefficients,) * steps
+    else:
+        if len(coefficients) != steps or any(len(r) != 3 for r in coefficients):
+            raise ValueError("coefficients are (a, b, c), or one such triple for each step")
+        values = [v for r in coefficients for v in r]
     if out is None:
         odt = G.dtype if out_dtype is None else _out_dtype(out_dtype)
-        with _on_stream(stream):
-            out = torch.empty(G.shape, dtype=odt, device=G.device)
+        out = _allocate(stream, _empty, G.shape, odt, G.device)
+        ldo, stride_o = cols, rows * cols
     else:
-        _check_batch(out, "out")
+        *_, ldo, stride_o = _check_batch(out, "out")
         if out.shape != G.shape or (out_dtype is not None and out.dtype != _out_dtype(out_dtype)):
             raise ValueError("out must have G's shape and the output dtype")
+    lib = _lib or load_library()
     if workspace is None:
-        with _on_stream(stream):
-            workspace = torch.empty(gemm_newton_schulz_workspace_size(batch, rows, cols),
-                                    dtype=torch.uint8, device=G.device)
+        nbytes = lib.gemm_newton_schulz_workspace_size(batch, rows, cols)
+        workspace = _allocate(stream, _empty, (nbytes,), _torch().uint8, G.device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    rc = gemm_newton_schulz(G.data_ptr(), _row_pitch(G), G.stride(0) if batch > 1 else 0,
-                            out.data_ptr(), _row_pitch(out), out.stride(0) if batch > 1 else 0,
-                            batch, rows, cols, dtype_code(G.dtype), dtype_code(out.dtype), steps,
-                            coef, eps, workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    rc = lib.gemm_newton_schulz(G.data_ptr(), ldg, stride_g, out.data_ptr(), ldo, stride_o, batch,
+                                rows, cols, dtype_code(G.dtype), dtype_code(out.dtype), steps,
+                                (ctypes.c_float * (3 * steps))(*values), eps,
+                                workspace.data_ptr(), nbytes, _stream_ptr(stream, G))
     if rc != OK:
         raise GemmError(rc, "gemm_newton_schulz")
     return out
 
 
-def _row_pitch(x) -> int:
-    return x.stride(-2) if x.shape[-2] > 1 else x.shape[-1]
-
-
 def _check_batch(x, what):
-    torch = _torch()
+    """(batch, rows, cols, row stride, batch stride) of a matrix or a 3-D batch."""
     if x.dim() not in (2, 3) or not x.is_cuda:
         raise ValueError(f"{what} must be a 2-D or 3-D CUDA tensor")
-    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+    if x.dtype not in _dtype_codes():
         raise TypeError(f"{what} must be FP32, FP16 or BF16")
-    _check_matrix(x if x.dim() == 2 else x[0] if x.shape[0] else x.new_empty((0, 0)), what)
+    if x.dim() == 2:
+        return 1, *_check_matrix(x, what), 0
+    if x.shape[0] == 0:
+        return 0, x.shape[1], x.shape[2], x.shape[2], 0
+    return x.shape[0], *_check_matrix(x[0], what), x.stride(0)
