@@ -39,6 +39,11 @@ struct Fp8Launch {
 
 cudaError_t fp8_gemm_launch(const Fp8Launch& l, cudaStream_t stream);
 
+// The kernel for few output tiles (fp8_small.cu), and whether it is the
+// choice for a product.
+bool fp8_small_takes(const Fp8Launch& l);
+cudaError_t fp8_small_launch(const Fp8Launch& l, cudaStream_t stream);
+
 // C = beta * C (zeros for beta = 0): the product over an empty K.
 cudaError_t fp8_empty_launch(const Fp8Launch& l, cudaStream_t stream);
 

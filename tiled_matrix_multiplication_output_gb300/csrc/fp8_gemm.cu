@@ -9,32 +9,10 @@
 #include <type_traits>
 
 #include "fp8_gemm.cuh"
-#include "launch.h"
+#include "fp8_launch.cuh"
 
 namespace tmmo {
 namespace {
-
-constexpr int kMaxDevices = 64;
-
-// The stored matrix of an operand (outer x K, or K x outer when MN-major) in
-// boxes of box_outer x 128 of K, swizzled over the length of a box row.  The
-// row pitch is a multiple of 16 bytes; the matrix itself may end anywhere.
-bool encode_operand(CUtensorMap* map, const Fp8Operand& o, int64_t outer, int64_t K,
-                    uint32_t box_outer)
-{
-    auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
-    if (!fn)
-        return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(o.mn_major ? outer : K),
-                                static_cast<cuuint64_t>(o.mn_major ? K : outer)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.ld)};
-    const cuuint32_t box[2] = {o.mn_major ? box_outer : F8_BK, o.mn_major ? F8_BK : box_outer};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(o.data), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 int out_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
 
@@ -173,6 +151,8 @@ cudaError_t fp8_empty_launch(const Fp8Launch& l, cudaStream_t stream)
 
 cudaError_t fp8_gemm_launch(const Fp8Launch& l, cudaStream_t stream)
 {
+    if (fp8_small_takes(l))
+        return fp8_small_launch(l, stream);
     // Pair tiles of 256 x 256 once they fill half of the CTA pairs; below
     // that, four times as many 128 x 128 tiles keep more SMs busy.
     const long long pair_tiles =

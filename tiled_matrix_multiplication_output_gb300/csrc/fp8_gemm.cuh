@@ -115,12 +115,12 @@ __host__ __device__ constexpr uint32_t fp8_idesc(int a_type, int b_type, int m, 
 }
 
 // The constant part of an operand box's shared-memory descriptor: offsets,
-// version, and the swizzle mode (128 or 64 bytes, the length of a row).
+// version, and the swizzle mode (128, 64 or 32 bytes, the length of a row).
 __device__ __forceinline__ uint64_t fp8_desc_hi(uint32_t row_bytes, bool mn)
 {
     const uint64_t lbo = mn ? F8_BOX : 16, sbo = 8 * row_bytes;
     return ((lbo >> 4) << 16) | ((sbo >> 4) << 32) | (1ull << 46) |
-           (static_cast<uint64_t>(row_bytes == 128 ? 2 : 4) << 61);
+           (static_cast<uint64_t>(row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6) << 61);
 }
 
 // alpha * v + beta * C for a run of `N` values of one row, stored in OutT.
