@@ -28,7 +28,7 @@ STAMP_PATH = LIB_PATH + ".sha256"
 SOURCES = ("api.cu", "tc_gemm.cu", "tc_gemm_nn.cu", "tc_gemm_tn.cu", "tc_gemm_nt.cu",
            "tc_gemm_tt.cu", "tc_gemm_splitk.cu", "tc_small.cu", "simt_gemm.cu", "tile16.cu",
            "model.cu", "api_fp8.cu", "fp8_quantize.cu", "fp8_gemm.cu", "fp8_small.cu",
-           "api_newton_schulz.cu", "newton_schulz.cu")
+           "api_newton_schulz.cu", "newton_schulz.cu", "ns_resident.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "-I" + INCLUDE, "-I" + CSRC]

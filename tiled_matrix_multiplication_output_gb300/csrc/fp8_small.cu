@@ -74,13 +74,6 @@ struct Fp8SmallLayout {
     static_assert(SMEM_ALLOC <= 113 * 1024, "two blocks fit on an SM");
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 template <typename OutT>
 __device__ __forceinline__ void fs_store(const Fp8SmallParams& p, int row, int col, float v)
 {

@@ -41,17 +41,13 @@
 #include <mutex>
 
 #include "launch.h"
+#include "newton_schulz.cuh"
 #include "newton_schulz.h"
-#include "tc_gemm.cuh"
 
 namespace tmmo {
 namespace {
 
 constexpr int kMaxDevices = 64;
-
-// Stored value = scale * value.
-constexpr float NS_SX = 4096.0f, NS_SA = 4096.0f, NS_SB = 2048.0f;
-constexpr float NS_LO = 2048.0f;  // lo holds (X - hi) * NS_LO
 
 constexpr int NS_THREADS = 320;   // warp 0: copies, 1: MMA, 2-9: epilogue
 constexpr int NS_EPI_WARP0 = 2;
@@ -74,12 +70,9 @@ struct NsParams {
     int k_blocks;
     bool a_mn, b_mn;
     uint32_t idesc;
-    float alpha, beta;             // acc * alpha + beta * addend
-    // FP16 addend (and the low half of X), output and mirrored output, all
-    // with one row pitch and one batch pitch each
-    const __half *add_hi, *add_lo;
+    // pitches of the FP16 addend and output; X's low half has X's
     long long ld_add, batch_add;
-    __half *out_hi, *out_lo;
+    __half* lo;                    // X's low half, read as part of the addend and written
     long long ld_out, batch_out;
     void* result;                  // NS_LAST
     long long ld_res, batch_res;
@@ -88,6 +81,35 @@ struct NsParams {
     long long wait_budget;
     int fault_skip_kblock;
 };
+
+// What differs from step to step: acc * alpha + beta * add -> out.
+struct NsOperands {
+    float alpha, beta;
+    const __half* add;
+    __half* out;
+};
+
+// One orthogonalisation: the products' parameters by mode (an update's serve
+// its last step as well) and where the operands are.
+struct NsPlan {
+    NsParams p[3];
+    __half *hi[2], *A, *B;         // X (read from one, written to the other), A, B
+    float coefficients[3 * NS_MAX_STEPS];
+};
+
+__host__ __device__ inline NsOperands ns_operands(const NsPlan& f, int mode, int step)
+{
+    const float a = f.coefficients[3 * step], b = f.coefficients[3 * step + 1],
+                c = f.coefficients[3 * step + 2];
+    switch (mode) {
+    case NS_GRAM:
+        return {NS_SA / (NS_SX * NS_SX), 0.0f, nullptr, f.A};
+    case NS_POLY:
+        return {c * (NS_SB / (NS_SA * NS_SA)), b * (NS_SB / NS_SA), f.A, f.B};
+    default:
+        return {1.0f / NS_SB, a, f.hi[step & 1], f.hi[(step & 1) ^ 1]};
+    }
+}
 
 template <int CG, int BN, int STAGES>
 struct NsLayout {
@@ -176,45 +198,103 @@ __device__ __forceinline__ void ns_store_row(__half* dst, int n, const uint32_t 
     }
 }
 
-__device__ __forceinline__ float2 ns_unpack(uint32_t w)
+// Descriptor constants of an operand box (128 outer x 64 of K).  K-major: one
+// box of 128-byte rows; MN-major: two atoms of 64 outer values, 64 K rows of
+// 128 bytes each.
+__device__ __forceinline__ uint64_t ns_desc_hi(bool mn)
 {
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return (1ull << 46) | (2ull << 61) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+           (static_cast<uint64_t>((mn ? NS_BOX / 2 : 16) >> 4) << 16);
 }
 
-__device__ __forceinline__ uint32_t ns_pack(float lo, float hi)
+// One warp's part of a finished tile: rows `row` (one a lane), COLS columns
+// from col0.  The first addend is fetched before `wait`, which returns once
+// the accumulator at taddr is complete (false: given up).
+template <int MODE, int COLS, typename Wait>
+__device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands& o, int z, bool mirror,
+                                            int row, int col0, uint32_t taddr, Wait&& wait)
 {
-    return pack2(lo, hi, static_cast<__half*>(nullptr));
-}
-
-template <typename OutT>
-__device__ __forceinline__ void ns_store_result(OutT* dst, int n, const float (&v)[32])
-{
-    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
-    constexpr int PER = 16 / static_cast<int>(sizeof(OutT));
+    const bool inside = row < p.M;
+    const long long at_add = z * p.batch_add + row * p.ld_add + col0;
+    uint32_t ah[16], al[16];
+    auto fetch = [&](int c) {  // the addend of chunk c
+        const int n = inside ? p.N - col0 - c * 32 : 0;
+        if constexpr (MODE != NS_GRAM)
+            ns_load_row(o.add + at_add + c * 32, n, ah);
+        if constexpr (MODE >= NS_UPDATE)
+            ns_load_row(p.lo + at_add + c * 32, n, al);
+    };
+    fetch(0);
+    if (!wait())
+        return;
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < COLS / 32; ++c) {
+        const int col = col0 + c * 32;
+        const int n = min(p.N - col, 32);
+        if (n <= 0)
+            break;
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(taddr + c * 32, v);
+        tmem_wait_ld();
+        float f[32];
 #pragma unroll
-    for (int c = 0; c < 32 / PER; ++c) {
-        if (vec && (c + 1) * PER <= n) {
-            uint4 u;
-            if constexpr (sizeof(OutT) == 4) {
-                u = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                               __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-            } else {
-                OutT* tag = nullptr;
-                u = make_uint4(pack2(v[8 * c], v[8 * c + 1], tag), pack2(v[8 * c + 2], v[8 * c + 3], tag),
-                               pack2(v[8 * c + 4], v[8 * c + 5], tag),
-                               pack2(v[8 * c + 6], v[8 * c + 7], tag));
+        for (int i = 0; i < 16; ++i) {
+            f[2 * i] = o.alpha * __uint_as_float(v[2 * i]);
+            f[2 * i + 1] = o.alpha * __uint_as_float(v[2 * i + 1]);
+            if constexpr (MODE != NS_GRAM) {
+                float2 a = ns_unpack(ah[i]);
+                if constexpr (MODE >= NS_UPDATE) {
+                    const float2 l = ns_unpack(al[i]);
+                    a.x = fmaf(l.x, 1.0f / NS_LO, a.x);
+                    a.y = fmaf(l.y, 1.0f / NS_LO, a.y);
+                }
+                f[2 * i] = fmaf(o.beta, a.x, f[2 * i]);
+                f[2 * i + 1] = fmaf(o.beta, a.y, f[2 * i + 1]);
             }
-            *reinterpret_cast<uint4*>(dst + c * PER) = u;
-        } else {
+        }
+        if (c + 1 < COLS / 32)
+            fetch(c + 1);
+        if constexpr (MODE == NS_LAST) {
+            if (inside) {
+                const long long at = z * p.batch_res + row * p.ld_res + col;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (c * PER + i < n) {
-                    if constexpr (sizeof(OutT) == 4) {
-                        dst[c * PER + i] = v[c * PER + i];
-                    } else {
-                        OutT* tag = nullptr;
-                        const uint32_t u = pack2(v[c * PER + i], 0.0f, tag);
-                        dst[c * PER + i] = *reinterpret_cast<const OutT*>(&u);
+                for (int i = 0; i < 32; ++i)
+                    f[i] *= 1.0f / NS_SX;
+                if (p.out_dtype == DT_F32)
+                    ns_store_result(static_cast<float*>(p.result) + at, n, f);
+                else if (p.out_dtype == DT_F16)
+                    ns_store_result(static_cast<__half*>(p.result) + at, n, f);
+                else
+                    ns_store_result(static_cast<__nv_bfloat16*>(p.result) + at, n, f);
+            }
+        } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = ns_pack(f[2 * i], f[2 * i + 1]);
+            const long long at = z * p.batch_out + row * p.ld_out + col;
+            if (inside)
+                ns_store_row(o.out + at, n, w);
+            if constexpr (MODE == NS_UPDATE) {
+                uint32_t lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 h = ns_unpack(w[i]);
+                    lo[i] = ns_pack((f[2 * i] - h.x) * NS_LO, (f[2 * i + 1] - h.y) * NS_LO);
+                }
+                if (inside)
+                    ns_store_row(p.lo + at, n, lo);
+            } else if (mirror) {
+                // the mirrored tile: lane l writes column `row` of the rows
+                // col .. col + 31
+                unsigned short* dst = reinterpret_cast<unsigned short*>(o.out) + z * p.batch_out +
+                                      col * p.ld_out + row;
+                if (inside) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (i < n)
+                            dst[i * p.ld_out] = static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)));
                     }
                 }
             }
@@ -229,7 +309,8 @@ __device__ __forceinline__ void ns_store_result(OutT* dst, int n, const float (&
 template <int CG, int BN, int STAGES, int MODE>
 __global__ void __launch_bounds__(NS_THREADS, 1)
     ns_product_kernel(const __grid_constant__ CUtensorMap tmA,
-                      const __grid_constant__ CUtensorMap tmB, const NsParams p)
+                      const __grid_constant__ CUtensorMap tmB, const NsParams p,
+                      const NsOperands o)
 {
     using L = NsLayout<CG, BN, STAGES>;
     constexpr bool SYMMETRIC = MODE == NS_GRAM || MODE == NS_POLY;
@@ -257,6 +338,10 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
     const int unit = (CG == 2) ? (blockIdx.x >> 1) : blockIdx.x;
     const int num_units = (CG == 2) ? (gridDim.x >> 1) : gridDim.x;
     const TcWatch watch{abort_flag, p.status, p.wait_budget};
+    // The next product's blocks may take the SMs that this one leaves idle
+    // and set themselves up; they wait for this grid to complete before they
+    // touch global memory.
+    grid_dep_launch_dependents();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -284,10 +369,12 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    grid_dep_wait();
 
     if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------ TMA producer
+            fence_proxy_async_all();  // the operands were written by plain stores
             int stage = 0;
             uint32_t phase = 0;
             int issued[STAGES];
@@ -362,9 +449,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
             int stage = 0, local = 0;
             uint32_t phase = 0;
             bool ok = true;
-            const uint64_t hi = (1ull << 46) | (2ull << 61) | (static_cast<uint64_t>(1024 >> 4) << 32);
-            const uint64_t a_hi = hi | (static_cast<uint64_t>((p.a_mn ? NS_BOX / 2 : 16) >> 4) << 16);
-            const uint64_t b_hi = hi | (static_cast<uint64_t>((p.b_mn ? NS_BOX / 2 : 16) >> 4) << 16);
+            const uint64_t a_hi = ns_desc_hi(p.a_mn), b_hi = ns_desc_hi(p.b_mn);
             const uint32_t a_step = (p.a_mn ? 2048 : 32) >> 4;
             const uint32_t b_step = (p.b_mn ? 2048 : 32) >> 4;
             for (int t = unit; ok && t < p.num_tiles; t += num_units, ++local) {
@@ -426,98 +511,16 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
             const int acc = local & 1;
             const int row = mb * TILE_M + static_cast<int>(rank) * TC_BM + q * 32 + static_cast<int>(lane);
             const int col0 = nb * BN + half * COLS;
-            const bool inside = row < p.M;
-            const __half* add_hi = p.add_hi + z * p.batch_add + row * p.ld_add + col0;
-            const __half* add_lo = p.add_lo + z * p.batch_add + row * p.ld_add + col0;
-            uint32_t ah[16], al[16];
-            auto fetch = [&](int c) {  // the addend of chunk c
-                const int n = inside ? p.N - col0 - c * 32 : 0;
-                if constexpr (MODE != NS_GRAM)
-                    ns_load_row(add_hi + c * 32, n, ah);
-                if constexpr (MODE >= NS_UPDATE)
-                    ns_load_row(add_lo + c * 32, n, al);
-            };
-            fetch(0);
-            int ok = 1;
-            if (lane == 0)
-                ok = tc_wait(tfull_bar(acc), (local >> 1) & 1, watch) ? 1 : 0;
-            if (!__shfl_sync(0xffffffffu, ok, 0))
+            bool ok = true;
+            ns_epilogue<MODE, COLS>(p, o, z, mb != nb, row, col0,
+                                    tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                        static_cast<uint32_t>(acc * BN + half * COLS),
+                                    [&]() {
+                                        ok = tc_wait_warp(tfull_bar(acc), (local >> 1) & 1, watch);
+                                        return ok;
+                                    });
+            if (!ok)
                 break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                   static_cast<uint32_t>(acc * BN + half * COLS);
-#pragma unroll 1
-            for (int c = 0; c < COLS / 32; ++c) {
-                const int col = col0 + c * 32;
-                const int n = min(p.N - col, 32);
-                if (n <= 0)
-                    break;
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(taddr + c * 32, v);
-                tmem_wait_ld();
-                float f[32];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    f[2 * i] = p.alpha * __uint_as_float(v[2 * i]);
-                    f[2 * i + 1] = p.alpha * __uint_as_float(v[2 * i + 1]);
-                    if constexpr (MODE != NS_GRAM) {
-                        float2 a = ns_unpack(ah[i]);
-                        if constexpr (MODE >= NS_UPDATE) {
-                            const float2 l = ns_unpack(al[i]);
-                            a.x = fmaf(l.x, 1.0f / NS_LO, a.x);
-                            a.y = fmaf(l.y, 1.0f / NS_LO, a.y);
-                        }
-                        f[2 * i] = fmaf(p.beta, a.x, f[2 * i]);
-                        f[2 * i + 1] = fmaf(p.beta, a.y, f[2 * i + 1]);
-                    }
-                }
-                if (c + 1 < COLS / 32)
-                    fetch(c + 1);
-                if constexpr (MODE == NS_LAST) {
-                    if (inside) {
-                        const long long at = z * p.batch_res + row * p.ld_res + col;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            f[i] *= 1.0f / NS_SX;
-                        if (p.out_dtype == DT_F32)
-                            ns_store_result(static_cast<float*>(p.result) + at, n, f);
-                        else if (p.out_dtype == DT_F16)
-                            ns_store_result(static_cast<__half*>(p.result) + at, n, f);
-                        else
-                            ns_store_result(static_cast<__nv_bfloat16*>(p.result) + at, n, f);
-                    }
-                } else {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = ns_pack(f[2 * i], f[2 * i + 1]);
-                    const long long at = z * p.batch_out + row * p.ld_out + col;
-                    if (inside)
-                        ns_store_row(p.out_hi + at, n, w);
-                    if constexpr (MODE == NS_UPDATE) {
-                        uint32_t lo[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 h = ns_unpack(w[i]);
-                            lo[i] = ns_pack((f[2 * i] - h.x) * NS_LO, (f[2 * i + 1] - h.y) * NS_LO);
-                        }
-                        if (inside)
-                            ns_store_row(p.out_lo + at, n, lo);
-                    } else if (mb != nb) {
-                        // the mirrored tile: lane l writes column `row` of
-                        // the rows col..col + 31
-                        unsigned short* dst = reinterpret_cast<unsigned short*>(p.out_hi) +
-                                              z * p.batch_out + col * p.ld_out + row;
-                        if (inside) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                if (i < n)
-                                    dst[i * p.ld_out] = static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)));
-                            }
-                        }
-                    }
-                }
-            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -544,10 +547,6 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
 }
 
 // ------------------------------------------------------------ normalisation
-
-__device__ __forceinline__ float ns_value(const float* p) { return *p; }
-__device__ __forceinline__ float ns_value(const __half* p) { return __half2float(*p); }
-__device__ __forceinline__ float ns_value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 // Eight consecutive values, `n` of them inside the row.
 template <typename InT>
@@ -580,30 +579,16 @@ struct NsNorm {
     long long ld, batch_x;
 };
 
-__device__ __forceinline__ float ns_block_sum(float s)
-{
-    __shared__ float part[32];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        s += __shfl_xor_sync(0xffffffffu, s, d);
-    if ((threadIdx.x & 31) == 0)
-        part[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = 0.0f;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i)
-        s += part[i];
-    return s;
-}
-
-// Partial sums of squares, a fixed set of elements per block.
+// A thread's sum of squares over the groups first, first + step, ... of
+// matrix z.
 template <typename InT>
-__global__ void __launch_bounds__(512) ns_norm_kernel(const NsNorm p)
+__device__ __forceinline__ float ns_square_sum(const NsNorm& p, long long z, long long first,
+                                               long long step)
 {
-    const InT* g = static_cast<const InT*>(p.G) + blockIdx.y * p.batch_g;
+    const InT* g = static_cast<const InT*>(p.G) + z * p.batch_g;
     const long long total = static_cast<long long>(p.rows) * p.groups;
     float s = 0.0f;
-    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    for (long long i = first; i < total; i += step) {
         const int row = static_cast<int>(i / p.groups), c = static_cast<int>(i % p.groups) * 8;
         float v[8];
         ns_load8(g + row * p.ldg + c, p.cols - c, p.vec, v);
@@ -611,26 +596,21 @@ __global__ void __launch_bounds__(512) ns_norm_kernel(const NsNorm p)
         for (int k = 0; k < 8; ++k)
             s = fmaf(v[k], v[k], s);
     }
-    s = ns_block_sum(s);
-    if (threadIdx.x == 0)
-        p.partial[blockIdx.y * p.blocks + blockIdx.x] = s;
+    return s;
 }
 
-// X = G / (norm + eps) as hi and lo.  Every block adds the partial sums in
-// the same order.  Where the norm is not finite (a NaN or an infinity in G,
-// or squares beyond FP32) the result is NaN throughout.
+// X = G / (norm + eps) as hi and lo over the same groups, from the sum of
+// all squares.  Where the norm is not finite (a NaN or an infinity in G, or
+// squares beyond FP32) the result is NaN throughout.
 template <typename InT>
-__global__ void __launch_bounds__(512) ns_scale_kernel(const NsNorm p)
+__device__ __forceinline__ void ns_scale(const NsNorm& p, long long z, long long first,
+                                         long long step, float sum)
 {
-    float sum = 0.0f;
-    for (int i = 0; i < p.blocks; ++i)
-        sum += p.partial[blockIdx.y * p.blocks + i];
     const float norm = sqrtf(sum);
     const float scale = isfinite(norm) ? NS_SX / (norm + p.eps) : __int_as_float(0x7fffffff);
-    const InT* g = static_cast<const InT*>(p.G) + blockIdx.y * p.batch_g;
+    const InT* g = static_cast<const InT*>(p.G) + z * p.batch_g;
     const long long total = static_cast<long long>(p.rows) * p.groups;
-    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    for (long long i = first; i < total; i += step) {
         const int row = static_cast<int>(i / p.groups), c = static_cast<int>(i % p.groups) * 8;
         float v[8];
         ns_load8(g + row * p.ldg + c, p.cols - c, p.vec, v);
@@ -642,10 +622,36 @@ __global__ void __launch_bounds__(512) ns_scale_kernel(const NsNorm p)
             const float2 r = ns_unpack(h[k]);
             l[k] = ns_pack((x - r.x) * NS_LO, (y - r.y) * NS_LO);
         }
-        const long long at = blockIdx.y * p.batch_x + row * p.ld + c;
+        const long long at = z * p.batch_x + row * p.ld + c;
         *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
     }
+}
+
+// Partial sums of squares, a fixed set of elements per block.
+template <typename InT>
+__global__ void __launch_bounds__(512) ns_norm_kernel(const NsNorm p)
+{
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const long long first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const float s = ns_block_sum(ns_square_sum<InT>(p, blockIdx.y, first,
+                                                    static_cast<long long>(gridDim.x) * blockDim.x));
+    if (threadIdx.x == 0)
+        p.partial[blockIdx.y * p.blocks + blockIdx.x] = s;
+}
+
+// Every block adds the partial sums in the same order.
+template <typename InT>
+__global__ void __launch_bounds__(512) ns_scale_kernel(const NsNorm p)
+{
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    float sum = 0.0f;
+    for (int i = 0; i < p.blocks; ++i)
+        sum += p.partial[blockIdx.y * p.blocks + i];
+    const long long first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    ns_scale<InT>(p, blockIdx.y, first, static_cast<long long>(gridDim.x) * blockDim.x, sum);
 }
 
 // ------------------------------------------------------------------- host
@@ -703,8 +709,8 @@ bool ns_encode(CUtensorMap* map, const __half* base, int64_t rows, int64_t cols,
 }
 
 template <int CG, int BN, int STAGES, int MODE>
-cudaError_t ns_run(const CUtensorMap& ta, const CUtensorMap& tb, NsParams p, int num_sms,
-                   cudaStream_t stream)
+cudaError_t ns_run(const CUtensorMap& ta, const CUtensorMap& tb, NsParams p, const NsOperands& o,
+                   int num_sms, cudaStream_t stream)
 {
     using L = NsLayout<CG, BN, STAGES>;
     auto kern = ns_product_kernel<CG, BN, STAGES, MODE>;
@@ -760,45 +766,57 @@ cudaError_t ns_run(const CUtensorMap& ta, const CUtensorMap& tb, NsParams p, int
     p.idesc = tc_idesc(false, TC_BM * CG, BN, p.a_mn, p.b_mn);
     const int units = std::max(1, std::min(p.num_tiles, units_cap));
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(units * CG, 1, 1);
     cfg.blockDim = dim3(NS_THREADS, 1, 1);
     cfg.dynamicSmemBytes = L::SMEM_ALLOC;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
     note_launch();
-    err = cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
+    err = cudaLaunchKernelEx(&cfg, kern, ta, tb, p, o);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 // 256 x 256 pair tiles once they fill half of the CTA pairs, 128 x 128 tiles
 // otherwise.
 template <int MODE>
-cudaError_t ns_product(const CUtensorMap& ta, const CUtensorMap& tb, const NsParams& p, int num_sms,
-                       cudaStream_t stream)
+cudaError_t ns_product(const CUtensorMap& ta, const CUtensorMap& tb, const NsParams& p,
+                       const NsOperands& o, int num_sms, cudaStream_t stream)
 {
     const long long tm = (p.M + 255) / 256, tn = (p.N + 255) / 256;
     const bool symmetric = MODE == NS_GRAM || MODE == NS_POLY;
     const long long pairs = p.batch * (symmetric ? tn * (tn + 1) / 2 : tm * tn);
     if (pairs * 4 >= num_sms)
-        return ns_run<2, 256, 6, MODE>(ta, tb, p, num_sms, stream);
-    return ns_run<1, 128, 6, MODE>(ta, tb, p, num_sms, stream);
+        return ns_run<2, 256, 6, MODE>(ta, tb, p, o, num_sms, stream);
+    return ns_run<1, 128, 6, MODE>(ta, tb, p, o, num_sms, stream);
 }
 
 template <typename InT>
 cudaError_t ns_normalise(const NsNorm& n, int batch, cudaStream_t stream)
 {
-    const dim3 grid(n.blocks, batch);
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(n.blocks, batch);
+    cfg.blockDim = dim3(512, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     note_launch();
-    ns_norm_kernel<InT><<<grid, 512, 0, stream>>>(n);
+    cudaError_t err = cudaLaunchKernelEx(&cfg, ns_norm_kernel<InT>, n);
+    if (err != cudaSuccess)
+        return err;
     note_launch();
-    ns_scale_kernel<InT><<<grid, 512, 0, stream>>>(n);
-    return cudaGetLastError();
+    err = cudaLaunchKernelEx(&cfg, ns_scale_kernel<InT>, n);
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace
@@ -810,13 +828,38 @@ size_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols)
 
 cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
 {
+    if (ns_resident_takes(l))
+        return ns_resident_launch(l, stream);
     const NsSpace s = ns_space(l.batch, l.rows, l.cols);
     char* ws = static_cast<char*>(l.workspace);
-    __half* hi[2] = {reinterpret_cast<__half*>(ws + s.off_hi[0]),
-                     reinterpret_cast<__half*>(ws + s.off_hi[1])};
-    __half* lo = reinterpret_cast<__half*>(ws + s.off_lo);
-    __half* A = reinterpret_cast<__half*>(ws + s.off_a);
-    __half* B = reinterpret_cast<__half*>(ws + s.off_b);
+    const bool tall = l.rows > l.cols;
+    const int m = static_cast<int>(s.m), wide = std::max(l.rows, l.cols);
+    NsPlan plan{};
+    plan.hi[0] = reinterpret_cast<__half*>(ws + s.off_hi[0]);
+    plan.hi[1] = reinterpret_cast<__half*>(ws + s.off_hi[1]);
+    plan.A = reinterpret_cast<__half*>(ws + s.off_a);
+    plan.B = reinterpret_cast<__half*>(ws + s.off_b);
+    std::copy(l.coefficients, l.coefficients + 3 * l.steps, plan.coefficients);
+    for (int mode = 0; mode < 3; ++mode) {
+        NsParams& p = plan.p[mode];
+        const bool update = mode == NS_UPDATE;
+        p.batch = l.batch;
+        p.M = update ? l.rows : m;
+        p.N = update ? l.cols : m;
+        p.K = mode == NS_GRAM ? wide : m;
+        p.a_mn = mode == NS_GRAM && tall;
+        p.b_mn = mode == NS_GRAM ? tall : update && !tall;
+        p.ld_add = p.ld_out = update ? s.ld_x : s.ld_a;
+        p.batch_add = p.batch_out = update ? s.x : s.a;
+        p.lo = reinterpret_cast<__half*>(ws + s.off_lo);
+        p.result = l.O;
+        p.ld_res = l.ldo;
+        p.batch_res = l.batch_o;
+        p.out_dtype = l.out_dtype;
+        p.status = l.status;
+        p.wait_budget = l.wait_budget;
+        p.fault_skip_kblock = l.fault_skip_kblock;
+    }
 
     const int es = l.in_dtype == DT_F32 ? 4 : 2;
     NsNorm n{};
@@ -834,84 +877,40 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
     n.blocks = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(NS_NORM_BLOCKS, (groups + 4 * 512 - 1) / (4 * 512))));
     n.eps = l.eps;
-    n.hi = hi[0];
-    n.lo = lo;
+    n.hi = plan.hi[0];
+    n.lo = reinterpret_cast<__half*>(ws + s.off_lo);
     n.ld = s.ld_x;
     n.batch_x = s.x;
-    cudaError_t err = l.in_dtype == DT_F32   ? ns_normalise<float>(n, l.batch, stream)
-                      : l.in_dtype == DT_F16 ? ns_normalise<__half>(n, l.batch, stream)
-                                             : ns_normalise<__nv_bfloat16>(n, l.batch, stream);
-    if (err != cudaSuccess)
-        return err;
 
     // Tensor maps: X with K (128-row boxes) or the outer axis (64-row boxes)
     // contiguous, A and B.
     CUtensorMap x_rows[2], x_cols[2], ta, tb;
     for (int i = 0; i < 2; ++i)
-        if (!ns_encode(&x_rows[i], hi[i], l.rows, l.cols, s.ld_x, l.batch, s.x, 128) ||
-            !ns_encode(&x_cols[i], hi[i], l.rows, l.cols, s.ld_x, l.batch, s.x, 64))
+        if (!ns_encode(&x_rows[i], plan.hi[i], l.rows, l.cols, s.ld_x, l.batch, s.x, 128) ||
+            !ns_encode(&x_cols[i], plan.hi[i], l.rows, l.cols, s.ld_x, l.batch, s.x, 64))
             return cudaErrorNotSupported;
-    if (!ns_encode(&ta, A, s.m, s.m, s.ld_a, l.batch, s.a, 128) ||
-        !ns_encode(&tb, B, s.m, s.m, s.ld_a, l.batch, s.a, 128))
+    if (!ns_encode(&ta, plan.A, m, m, s.ld_a, l.batch, s.a, 128) ||
+        !ns_encode(&tb, plan.B, m, m, s.ld_a, l.batch, s.a, 128))
         return cudaErrorNotSupported;
 
-    const bool tall = l.rows > l.cols;
-    const int m = static_cast<int>(s.m), wide = std::max(l.rows, l.cols);
-    NsParams base{};
-    base.batch = l.batch;
-    base.status = l.status;
-    base.wait_budget = l.wait_budget;
-    base.fault_skip_kblock = l.fault_skip_kblock;
+    cudaError_t err = l.in_dtype == DT_F32   ? ns_normalise<float>(n, l.batch, stream)
+                      : l.in_dtype == DT_F16 ? ns_normalise<__half>(n, l.batch, stream)
+                                             : ns_normalise<__nv_bfloat16>(n, l.batch, stream);
+    if (err != cudaSuccess)
+        return err;
     for (int i = 0; i < l.steps; ++i) {
-        const float a = l.coefficients[3 * i], b = l.coefficients[3 * i + 1],
-                    c = l.coefficients[3 * i + 2];
         const int cur = i & 1;
-        NsParams p = base;  // A = X X^T or X^T X
-        p.M = p.N = m;
-        p.K = wide;
-        p.a_mn = p.b_mn = tall;
-        p.alpha = NS_SA / (NS_SX * NS_SX);
-        p.out_hi = A;
-        p.ld_out = s.ld_a;
-        p.batch_out = s.a;
+        const NsOperands gram = ns_operands(plan, NS_GRAM, i), poly = ns_operands(plan, NS_POLY, i),
+                         update = ns_operands(plan, NS_UPDATE, i);
         const CUtensorMap& tx = tall ? x_cols[cur] : x_rows[cur];
-        if ((err = ns_product<NS_GRAM>(tx, tx, p, l.num_sms, stream)) != cudaSuccess)
-            return err;
-        p = base;  // B = b A + c A A
-        p.M = p.N = p.K = m;
-        p.alpha = c * (NS_SB / (NS_SA * NS_SA));
-        p.beta = b * (NS_SB / NS_SA);
-        p.add_hi = A;
-        p.ld_add = s.ld_a;
-        p.batch_add = s.a;
-        p.out_hi = B;
-        p.ld_out = s.ld_a;
-        p.batch_out = s.a;
-        if ((err = ns_product<NS_POLY>(ta, ta, p, l.num_sms, stream)) != cudaSuccess)
-            return err;
-        p = base;  // X = a X + B X or a X + X B
-        p.M = l.rows;
-        p.N = l.cols;
-        p.K = m;
-        p.b_mn = !tall;
-        p.alpha = 1.0f / NS_SB;
-        p.beta = a;
-        p.add_hi = hi[cur];
-        p.add_lo = lo;
-        p.ld_add = s.ld_x;
-        p.batch_add = s.x;
-        p.out_hi = hi[cur ^ 1];
-        p.out_lo = lo;
-        p.ld_out = s.ld_x;
-        p.batch_out = s.x;
-        p.result = l.O;
-        p.ld_res = l.ldo;
-        p.batch_res = l.batch_o;
-        p.out_dtype = l.out_dtype;
         const CUtensorMap& t1 = tall ? x_rows[cur] : tb;
         const CUtensorMap& t2 = tall ? tb : x_cols[cur];
-        err = i + 1 < l.steps ? ns_product<NS_UPDATE>(t1, t2, p, l.num_sms, stream)
-                              : ns_product<NS_LAST>(t1, t2, p, l.num_sms, stream);
+        if ((err = ns_product<NS_GRAM>(tx, tx, plan.p[NS_GRAM], gram, l.num_sms, stream)) != cudaSuccess ||
+            (err = ns_product<NS_POLY>(ta, ta, plan.p[NS_POLY], poly, l.num_sms, stream)) != cudaSuccess)
+            return err;
+        err = i + 1 < l.steps
+                  ? ns_product<NS_UPDATE>(t1, t2, plan.p[NS_UPDATE], update, l.num_sms, stream)
+                  : ns_product<NS_LAST>(t1, t2, plan.p[NS_UPDATE], update, l.num_sms, stream);
         if (err != cudaSuccess)
             return err;
     }

@@ -28,6 +28,12 @@ struct NsLaunch {
 };
 
 size_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+
+// The one-launch form for matrices that a cluster holds on chip
+// (ns_resident.cu), and whether it takes a matrix.
+bool ns_resident_takes(const NsLaunch& l);
+cudaError_t ns_resident_launch(const NsLaunch& l, cudaStream_t stream);
+
 cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream);
 
 }  // namespace tmmo

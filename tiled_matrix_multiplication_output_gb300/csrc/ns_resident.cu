@@ -1,0 +1,569 @@
+// Newton-Schulz orthogonalisation of matrices with a short side of up to 128,
+// in one launch: a cluster of blocks holds one matrix on chip from the first
+// read of G to the write of the result.
+//
+// Such matrices are bound by latency: fifteen dependent products of a
+// microsecond or two of tensor work each for five steps.  As separate
+// launches a product costs 5 to 7 us whatever its size (set-up, copies from
+// L2, stores back, the fences and barriers between grids).  Here
+//
+//   * X (m x n, m <= n; G transposed while it is read where it has more rows
+//     than columns) is divided by columns over the blocks of the cluster.
+//     Then the update X <- a X + B X is local to a block, and only
+//     A = X X^T, a sum over the blocks, crosses between them;
+//   * a thread keeps its 128 values of X in registers, in FP32, and writes
+//     their FP16 operand form to shared memory, in the 128-byte-swizzled
+//     layout of a tensor-core operand.  One copy serves both products: rows
+//     of 64 columns are a K-major operand of X X^T and an MN-major one of
+//     B X;
+//   * A and B share one buffer: each thread replaces its elements of A by
+//     those of B once the product A A is complete, and every block computes
+//     all of B for itself;
+//   * the sum over blocks goes through distributed shared memory in FP32:
+//     a block adds up 1 / SIZE of the rows, in rank order, and writes the
+//     FP16 result to all of them;
+//   * G is read once: the norm is taken from the registers.
+//
+// Eight warps; one of them issues the MMAs, all of them wait for a product's
+// completion (bounded) and read it from tensor memory.  A wait that runs out
+// is reported as everywhere, and the block then only takes part in barriers.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "newton_schulz.cuh"
+#include "newton_schulz.h"
+
+namespace tmmo {
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int NR_THREADS = 256;
+constexpr int NR_MAX_SIZE = 16;  // blocks of a cluster
+
+struct NsResident {
+    const void* G;
+    void* O;
+    // element (i, j) of X at G[z * batch_g + i * row_g + j * col_g], and so in O
+    long long batch_g, row_g, col_g, batch_o, row_o, col_o;
+    int m, n;
+    int share;                     // columns of X per block
+    int in_dtype, out_dtype;
+    int steps;
+    float eps;
+    float coefficients[3 * NS_MAX_STEPS];
+    int* status;
+    long long wait_budget;
+    int fault_skip;                // test hook: the product whose completion is not signalled
+};
+
+constexpr int NR_CHUNK = 128 * 128;  // bytes of 64 columns (of 128 rows) of an operand
+constexpr int NR_COLS = 256;         // columns of X a block can hold
+constexpr uint32_t NR_TMEM_COLS = 256;
+
+template <int SIZE>
+struct NrLayout {
+    static constexpr int OFF_A = 0;                               // 128 x 128
+    static constexpr int OFF_X = OFF_A + 2 * NR_CHUNK;            // 128 x NR_COLS
+    static constexpr int OFF_STAGING = OFF_X + NR_COLS / 64 * NR_CHUNK;
+    // 128 FP32 rows from all blocks, to be added up here
+    static constexpr int OFF_BAR = OFF_STAGING + (SIZE > 1 ? 128 * 128 * 4 : 0);
+    static constexpr int SMEM_ALLOC = OFF_BAR + 64 + 1024;
+    static_assert(SMEM_ALLOC <= 232448, "exceeds 227 KiB of dynamic shared memory");
+};
+
+// Shared-memory address of 8 columns (16 bytes) of an operand: 64-column
+// chunks of 128 rows of 128 bytes, 128-byte swizzle.
+__device__ __forceinline__ uint32_t nr_addr(uint32_t base, int row, int col)
+{
+    return base + (col >> 6) * NR_CHUNK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t (&w)[4])
+{
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&w)[4])
+{
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// 32 consecutive columns of one row of X from G, `cnt` of them inside.
+template <typename InT>
+__device__ __forceinline__ void nr_load(const InT* g, long long step, int cnt, float (&v)[32])
+{
+    constexpr int PER = 16 / static_cast<int>(sizeof(InT));
+    if (step == 1 && cnt == 32 && (reinterpret_cast<uintptr_t>(g) & 15u) == 0) {
+#pragma unroll
+        for (int i = 0; i < 32 / PER; ++i) {
+            const uint4 u = reinterpret_cast<const uint4*>(g)[i];
+            const InT* e = reinterpret_cast<const InT*>(&u);
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+                v[i * PER + k] = ns_value(e + k);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = i < cnt ? ns_value(g + i * step) : 0.0f;
+    }
+}
+
+template <typename OutT>
+__device__ __forceinline__ void nr_store(OutT* o, long long step, int cnt, const float (&v)[32])
+{
+    if (step == 1) {
+        ns_store_result(o, cnt, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (i < cnt) {
+            if constexpr (sizeof(OutT) == 4) {
+                o[i * step] = v[i];
+            } else {
+                const uint32_t u = pack2(v[i], 0.0f, static_cast<OutT*>(nullptr));
+                o[i * step] = *reinterpret_cast<const OutT*>(&u);
+            }
+        }
+    }
+}
+
+template <int SIZE>
+__global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid_constant__ NsResident p)
+{
+    using L = NrLayout<SIZE>;
+    constexpr int XCH = NR_COLS / 64;  // 32-column chunks of X per thread
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t sA = sbase + L::OFF_A, sX = sbase + L::OFF_X;
+    const uint32_t done_bar = sbase + L::OFF_BAR;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + 8);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + 12);
+    float* sum_slot = reinterpret_cast<float*>(smem + L::OFF_BAR + 16);
+
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+    const uint32_t lane = tid & 31;
+    const int q = warp & 3, g = warp >> 2;  // TMEM lane quarter; which of two column chunks
+    const int rank = SIZE > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const long long z = blockIdx.x / SIZE;
+    const int col0 = rank * p.share;                             // this block's columns of X
+    const int ncol = min(max(p.n - col0, 0), p.share);
+    const TcWatch watch{abort_flag, p.status, p.wait_budget};
+
+    if (tid == 0) {
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc<1>(smem_u32(tmem_slot), NR_TMEM_COLS);
+        tmem_relinquish<1>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot + (static_cast<uint32_t>(q * 32) << 16);
+
+    // ---- X in registers: row q * 32 + lane, columns in chunks of 32 taken by
+    // the two column groups in turn.  Zero outside the matrix; chunks wholly
+    // outside are left out everywhere.
+    const int row = q * 32 + static_cast<int>(lane);
+    float x[XCH][32];
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < XCH; ++c) {
+        const int col = (2 * c + g) * 32;
+        const int cnt = row < p.m ? min(ncol - col, 32) : 0;
+        const long long at = z * p.batch_g + row * p.row_g + (col0 + col) * p.col_g;
+        if (p.in_dtype == DT_F32)
+            nr_load(static_cast<const float*>(p.G) + at, p.col_g, cnt, x[c]);
+        else if (p.in_dtype == DT_F16)
+            nr_load(static_cast<const __half*>(p.G) + at, p.col_g, cnt, x[c]);
+        else
+            nr_load(static_cast<const __nv_bfloat16*>(p.G) + at, p.col_g, cnt, x[c]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            s = fmaf(x[c][i], x[c][i], s);
+    }
+    s = ns_block_sum(s);
+    if constexpr (SIZE > 1) {
+        if (tid == 0)
+            *sum_slot = s;
+        __syncwarp();
+        cluster_sync();
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < SIZE; ++k)
+            s += ld_cluster_f32(mapa_shared(smem_u32(sum_slot), k));
+    }
+    // Where the norm is not finite the result is NaN throughout.
+    const float norm = sqrtf(s);
+    const float scale = isfinite(norm) ? NS_SX / (norm + p.eps) : __int_as_float(0x7fffffff);
+#pragma unroll
+    for (int c = 0; c < XCH; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            x[c][i] *= scale;
+
+    auto put_x = [&]() {  // the operand form of X
+#pragma unroll
+        for (int c = 0; c < XCH; ++c) {
+            const float(&v)[32] = x[c];
+            if ((2 * c + g) * 32 < ncol) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    st_shared_v4(nr_addr(sX, row, (2 * c + g) * 32 + 8 * k),
+                                 ns_pack(v[8 * k], v[8 * k + 1]), ns_pack(v[8 * k + 2], v[8 * k + 3]),
+                                 ns_pack(v[8 * k + 4], v[8 * k + 5]), ns_pack(v[8 * k + 6], v[8 * k + 7]));
+            }
+        }
+    };
+    put_x();
+
+    // Descriptor constants.  K-major: 8-row groups 1024 bytes apart.
+    // MN-major (X in the update): 64-column atoms a chunk apart.
+    const uint64_t k_hi = (1ull << 46) | (2ull << 61) | (64ull << 32) | (1ull << 16);
+    const uint64_t n_hi = (1ull << 46) | (2ull << 61) | (64ull << 32) |
+                          (static_cast<uint64_t>(NR_CHUNK >> 4) << 16);
+    const int m_steps = (p.m + 15) / 16;   // K steps over rows; all further rows are zero
+    const int n_steps = (ncol + 15) / 16;  // over this block's columns
+    const int width = (ncol + 31) / 32 * 32;
+    int product = 0;
+    bool ok = true;
+    // Issues a product of 128 rows (K-major from `a`; `b` K-major as well, or
+    // X MN-major) and waits for it.
+    auto multiply = [&](uint32_t a, uint32_t b, bool b_mn, int steps, int n) {
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (ok && warp == 0) {
+            tc_fence_after();
+            const uint32_t idesc = tc_idesc(false, 128, n, false, b_mn);
+            const uint32_t d = *tmem_slot;
+            if (elect_one()) {
+                for (int k = 0; k < steps; ++k) {
+                    const uint32_t off = (k >> 2) * NR_CHUNK + (k & 3) * 32;
+                    const uint32_t ka = (a + off) >> 4, kb = (b + (b_mn ? k * 2048 : off)) >> 4;
+                    tc_mma_f16<1>(d, k_hi | (ka & 0x3FFF), (b_mn ? n_hi : k_hi) | (kb & 0x3FFF), idesc,
+                                  k != 0);
+                }
+                if (p.fault_skip != product)  // test hook, -1 in normal use
+                    tc_commit(done_bar);
+            }
+            __syncwarp();
+        }
+        ok = ok && tc_wait_warp(done_bar, static_cast<uint32_t>(product & 1), watch);
+        tc_fence_after();
+        ++product;
+    };
+
+    // The loops over A's elements are kept rolled: unrolled, a step is long
+    // straight-line code that is fetched anew every time.
+#pragma unroll 1
+    for (int step = 0; step < p.steps; ++step) {
+        const float ca = p.coefficients[3 * step], cb = p.coefficients[3 * step + 1],
+                    cc = p.coefficients[3 * step + 2];
+        // ---- A = X X^T
+        constexpr float alpha_a = NS_SA / (NS_SX * NS_SX);
+        multiply(sX, sX, false, n_steps, 128);
+        if constexpr (SIZE == 1) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                const int col = (2 * g + c) * 32;
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + col, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = ns_pack(alpha_a * __uint_as_float(v[8 * k + 2 * i]),
+                                       alpha_a * __uint_as_float(v[8 * k + 2 * i + 1]));
+                    st_shared_v4(nr_addr(sA, row, col + 8 * k), w[0], w[1], w[2], w[3]);
+                }
+            }
+        } else {
+            // Every row goes to the block that adds it up, into its staging
+            // buffer ([sender][row], 16-byte units swizzled against bank
+            // conflicts), and that block adds the senders' rows in rank
+            // order.  Rows are pushed, as remote stores do not wait.
+            constexpr int SHARE = 128 / SIZE;            // rows that this block adds up
+            constexpr int ITEMS = SHARE * 16;            // in units of 8 columns
+            constexpr int MINE = (ITEMS + NR_THREADS - 1) / NR_THREADS;
+            const uint32_t staging = sbase + L::OFF_STAGING;
+            const int to = rank * SHARE + row % SHARE;
+            const uint32_t dst =
+                mapa_shared(staging + to * 512, static_cast<uint32_t>(row / SHARE));
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                const int col = (2 * g + c) * 32;
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + col, v);
+                tmem_wait_ld();
+                if (n_steps == 0) {  // a block without columns adds nothing
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = 0;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t w[4] = {v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+                    st_cluster_v4(dst + (((col / 4 + k) ^ (to & 7)) << 4), w);
+                }
+            }
+            __syncwarp();
+            cluster_sync();
+#pragma unroll
+            for (int j = 0; j < MINE; ++j) {
+                const int item = j * NR_THREADS + tid;
+                if (item < ITEMS) {
+                    const int r = item / 16, u = 2 * (item % 16);
+                    float a[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        a[i] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < SIZE; ++k) {
+                        const int from = k * SHARE + r;
+                        uint32_t t[4], w[4];
+                        ld_shared_v4(staging + from * 512 + ((u ^ (from & 7)) << 4), t);
+                        ld_shared_v4(staging + from * 512 + (((u + 1) ^ (from & 7)) << 4), w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            a[i] += __uint_as_float(t[i]);
+                            a[4 + i] += __uint_as_float(w[i]);
+                        }
+                    }
+                    uint32_t sum[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sum[i] = ns_pack(alpha_a * a[2 * i], alpha_a * a[2 * i + 1]);
+                    const uint32_t at = nr_addr(sA, rank * SHARE + r, 8 * (item % 16));
+#pragma unroll
+                    for (int k = 0; k < SIZE; ++k)
+                        st_cluster_v4(mapa_shared(at, k), sum);
+                }
+            }
+            fence_proxy_async_cluster();
+            __syncwarp();
+            cluster_sync();
+        }
+        // ---- B = b A + c A A, in A's place
+        const float alpha_b = cc * (NS_SB / (NS_SA * NS_SA)), beta_b = cb * (NS_SB / NS_SA);
+        multiply(sA, sA, false, m_steps, 128);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+            const int col = (2 * g + c) * 32;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tmem + col, v);
+            uint32_t w[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                ld_shared_v4(nr_addr(sA, row, col + 8 * k), w[k]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = ns_unpack(w[k][i]);
+                    w[k][i] = ns_pack(fmaf(beta_b, a.x, alpha_b * __uint_as_float(v[8 * k + 2 * i])),
+                                      fmaf(beta_b, a.y, alpha_b * __uint_as_float(v[8 * k + 2 * i + 1])));
+                }
+                st_shared_v4(nr_addr(sA, row, col + 8 * k), w[k][0], w[k][1], w[k][2], w[k][3]);
+            }
+        }
+        // ---- X = a X + B X
+        multiply(sA, sX, true, width > 0 ? m_steps : 0, width > 0 ? width : 32);
+#pragma unroll
+        for (int c = 0; c < XCH; ++c) {
+            if ((2 * c + g) * 32 < ncol) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + (2 * c + g) * 32, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    x[c][i] = fmaf(ca, x[c][i], (1.0f / NS_SB) * __uint_as_float(v[i]));
+            }
+        }
+        if (step + 1 < p.steps)
+            put_x();
+    }
+
+    // ---- the result
+    if (!*abort_flag) {
+#pragma unroll
+        for (int c = 0; c < XCH; ++c) {
+            const int col = (2 * c + g) * 32;
+            const int cnt = row < p.m ? min(ncol - col, 32) : 0;
+            if (cnt <= 0)
+                continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                x[c][i] *= 1.0f / NS_SX;
+            const long long at = z * p.batch_o + row * p.row_o + (col0 + col) * p.col_o;
+            if (p.out_dtype == DT_F32)
+                nr_store(static_cast<float*>(p.O) + at, p.col_o, cnt, x[c]);
+            else if (p.out_dtype == DT_F16)
+                nr_store(static_cast<__half*>(p.O) + at, p.col_o, cnt, x[c]);
+            else
+                nr_store(static_cast<__nv_bfloat16*>(p.O) + at, p.col_o, cnt, x[c]);
+        }
+    }
+
+    // ---- teardown.  After a wait that ran out the MMAs issued may still be
+    // running: one commit more, waited for (bounded), before TMEM is released.
+    if (warp == 0 && !ok) {
+        const uint32_t drain_bar = sbase + L::OFF_BAR + 24;
+        if (elect_one()) {
+            mbar_init(drain_bar, 1);
+            fence_mbar_init();
+            tc_commit(drain_bar);
+        }
+        __syncwarp();
+        const long long t0 = clock64();
+        while (!__all_sync(0xffffffffu, mbar_test_wait(drain_bar, 0))) {
+            if (__any_sync(0xffffffffu, clock64() - t0 > p.wait_budget))
+                break;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        __syncwarp();
+        tmem_dealloc<1>(*tmem_slot, NR_TMEM_COLS);
+    }
+    if constexpr (SIZE > 1) {  // no block leaves while its shared memory may be read
+        __syncwarp();
+        cluster_sync();
+    }
+}
+
+template <int SIZE>
+cudaError_t launch_resident(const NsResident& p, int batch, cudaStream_t stream, bool probe)
+{
+    using L = NrLayout<SIZE>;
+    auto kern = ns_resident_kernel<SIZE>;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess)
+        return err;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = SIZE;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(batch) * SIZE, 1, 1);
+    cfg.blockDim = dim3(NR_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = L::SMEM_ALLOC;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = SIZE > 1 ? 1 : 0;
+    // Per device: 1 once prepared, -1 where no cluster of this size fits.
+    static int state[kMaxDevices] = {};
+    static std::mutex mu;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (state[dev] == 0) {
+            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_ALLOC);
+            if (err != cudaSuccess)
+                return err;
+            int clusters = 1;
+            if (SIZE > 8)
+                err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (err == cudaSuccess && SIZE > 1)
+                err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+            if (err != cudaSuccess)
+                return err;
+            state[dev] = clusters > 0 ? 1 : -1;
+        }
+        if (state[dev] < 0)
+            return cudaErrorNotSupported;
+    }
+    if (probe)
+        return cudaSuccess;
+    note_launch();
+    err = cudaLaunchKernelEx(&cfg, kern, p);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+cudaError_t launch_size(const NsResident& p, int size, int batch, cudaStream_t stream, bool probe)
+{
+    switch (size) {
+    case 1:
+        return launch_resident<1>(p, batch, stream, probe);
+    case 2:
+        return launch_resident<2>(p, batch, stream, probe);
+    case 4:
+        return launch_resident<4>(p, batch, stream, probe);
+    case 8:
+        return launch_resident<8>(p, batch, stream, probe);
+    default:
+        return launch_resident<16>(p, batch, stream, probe);
+    }
+}
+
+// Blocks for one matrix, 0 where it does not fit a cluster.
+int resident_size(int rows, int cols)
+{
+    if (std::min(rows, cols) > 128)
+        return 0;
+    int size = 1;
+    while (size * NR_COLS < std::max(rows, cols) && size <= NR_MAX_SIZE)
+        size *= 2;
+    return size <= NR_MAX_SIZE ? size : 0;
+}
+
+}  // namespace
+
+bool ns_resident_takes(const NsLaunch& l)
+{
+    const int size = resident_size(l.rows, l.cols);
+    if (size == 0 || static_cast<long long>(l.batch) * size > 0x7fffffffLL)
+        return false;
+    return launch_size(NsResident{}, size, 1, nullptr, true) == cudaSuccess;
+}
+
+cudaError_t ns_resident_launch(const NsLaunch& l, cudaStream_t stream)
+{
+    const int size = resident_size(l.rows, l.cols);
+    const bool tall = l.rows > l.cols;
+    NsResident p{};
+    p.G = l.G;
+    p.O = l.O;
+    p.batch_g = l.batch_g;
+    p.batch_o = l.batch_o;
+    p.row_g = tall ? 1 : l.ldg;
+    p.col_g = tall ? l.ldg : 1;
+    p.row_o = tall ? 1 : l.ldo;
+    p.col_o = tall ? l.ldo : 1;
+    p.m = std::min(l.rows, l.cols);
+    p.n = std::max(l.rows, l.cols);
+    p.share = ((p.n + size - 1) / size + 15) / 16 * 16;
+    p.in_dtype = l.in_dtype;
+    p.out_dtype = l.out_dtype;
+    p.steps = l.steps;
+    p.eps = l.eps;
+    std::copy(l.coefficients, l.coefficients + 3 * l.steps, p.coefficients);
+    p.status = l.status;
+    p.wait_budget = l.wait_budget;
+    p.fault_skip = l.fault_skip_kblock;
+    return launch_size(p, size, l.batch, stream, false);
+}
+
+}  // namespace tmmo
