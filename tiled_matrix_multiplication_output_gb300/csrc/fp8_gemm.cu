@@ -8,6 +8,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "device.h"
 #include "fp8_gemm.cuh"
 #include "fp8_launch.cuh"
 
@@ -15,6 +16,25 @@ namespace tmmo {
 namespace {
 
 int out_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+// C in boxes of 32 rows x 128 bytes, 128-byte swizzle.
+bool encode_output(CUtensorMap* map, const Fp8Launch& l)
+{
+    auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+    if (!fn)
+        return false;
+    const int es = out_bytes(l.out_dtype);
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(l.N), static_cast<cuuint64_t>(l.M)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(l.ldc) * es};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), 32};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUtensorMapDataType type = l.out_dtype == DT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : l.out_dtype == DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return fn(map, type, 2, l.C, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int CG, int BN, int STAGES, bool COLV>
 cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
@@ -96,6 +116,10 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
     p.status = l.status;
     p.wait_budget = l.wait_budget;
     p.fault_skip_kblock = l.fault_skip_kblock;
+    CUtensorMap tc = ta;  // unused without tma_out
+    p.tma_out = l.beta == 0.0f && aligned16(l.C) && (l.ldc * out_bytes(l.out_dtype)) % 16 == 0;
+    if (p.tma_out && !encode_output(&tc, l))
+        return cudaErrorNotSupported;
     const int units = std::max(1, std::min(p.num_tiles, units_cap));
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
@@ -110,7 +134,7 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     note_launch();
-    err = cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
+    err = cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, p);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -158,7 +182,7 @@ cudaError_t fp8_gemm_launch(const Fp8Launch& l, cudaStream_t stream)
     const long long pair_tiles =
         static_cast<long long>((l.M + 255) / 256) * ((l.N + 255) / 256);
     if (pair_tiles * 4 >= l.num_sms)
-        return launch_scales<2, 256, 5>(l, stream);
+        return launch_scales<2, 256, 4>(l, stream);
     return launch_scales<1, 128, 5>(l, stream);
 }
 

@@ -73,6 +73,7 @@ struct Fp8Params {
     void* C;
     long long ldc;
     int out_dtype;                 // DT_*
+    bool tma_out;                  // the output goes through a tensor map (beta == 0)
     bool vec_out;                  // C's rows take 32-byte accesses
     float alpha, beta;
     int* status;
@@ -90,7 +91,8 @@ struct Fp8Layout {
     static constexpr int GROUP = 4;
     static constexpr int BLOCK_BYTES = (128 + BN) * 4;
     static constexpr int SLOT_BYTES = GROUP * BLOCK_BYTES;
-    static constexpr int OFF_SCALE = STAGES * STAGE;
+    static constexpr int OFF_STAGING = STAGES * STAGE;  // 4 KiB of output per epilogue warp
+    static constexpr int OFF_SCALE = OFF_STAGING + F8_EPI_WARPS * TC_STAGING_BYTES;
     static constexpr int OFF_BAR = OFF_SCALE + SLOTS * SLOT_BYTES;
     // A K block's MMAs are issued as SUB groups of BN / SUB columns, each
     // with its own barriers.
@@ -177,13 +179,63 @@ __device__ __forceinline__ void fp8_store_row(OutT* dst, float* v, int n, const 
     }
 }
 
+// A warp's 32 x COLS part of a finished tile through its staging buffer, in
+// strips of 32 rows x 128 bytes: swizzled, conflict-free stores to shared
+// memory and one TMA store each, which clips at C's edges.  Straight from
+// registers, a thread holding a row, the stores scatter over 32 lines each.
+template <typename OutT, int COLS>
+__device__ __forceinline__ void fp8_store_tile(const uint64_t (&acc)[COLS / 2], uint32_t stg,
+                                               const CUtensorMap* map, int row0, int col0, uint32_t lane,
+                                               const Fp8Params& p)
+{
+    constexpr int STRIP = TcOut<OutT>::STRIP;
+    const uint32_t base = stg + lane * 128, sw = lane & 7;
+#pragma unroll
+    for (int s = 0; s < COLS / STRIP; ++s) {
+        if (row0 >= p.M || col0 + s * STRIP >= p.N)
+            break;
+        if (lane == 0)
+            bulk_wait_group_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {  // 16-byte chunks
+            uint32_t w[4];
+            if constexpr (sizeof(OutT) == 4) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    unpack_f32x2(acc[s * 16 + c * 2 + i], w[2 * i], w[2 * i + 1]);
+                if (p.alpha != 1.0f) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = __float_as_uint(p.alpha * __uint_as_float(w[i]));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t lo, hi;
+                    unpack_f32x2(acc[s * 32 + c * 4 + i], lo, hi);
+                    w[i] = pack2(p.alpha * __uint_as_float(lo), p.alpha * __uint_as_float(hi),
+                                 static_cast<OutT*>(nullptr));
+                }
+            }
+            st_shared_v4(base + ((c ^ sw) << 4), w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, stg, col0 + s * STRIP, row0);
+            bulk_commit_group();
+        }
+    }
+}
+
 // COLV: the column operand has a scale for each column (a vector along the
 // tile's columns); otherwise one for 128 columns, the same for all of a
 // thread's columns.
 template <int CG, int BN, int STAGES, bool COLV>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const Fp8Params p)
+                    const __grid_constant__ CUtensorMap tmC, const Fp8Params p)
 {
     using L = Fp8Layout<CG, BN, STAGES>;
     constexpr int TILE_M = TC_BM * CG;
@@ -244,6 +296,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
+        if (p.tma_out)
+            tma_prefetch_desc(&tmC);
     }
     if (warp == 1) {
         tmem_alloc<CG>(smem_u32(tmem_slot), L::TMEM_COLS);
@@ -570,7 +624,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             }
             const bool stored = !*abort_flag;  // an unfinished tile is not written
             // ---- the finished tile: alpha, beta, rounding to the output type
-            if (stored && row < p.M) {
+            if (stored && p.tma_out) {
+                const int row0 = row - static_cast<int>(lane);
+                const uint32_t stg = sbase + L::OFF_STAGING + ew * TC_STAGING_BYTES;
+                if (p.out_dtype == DT_F32)
+                    fp8_store_tile<float, COLS>(acc, stg, &tmC, row0, col0, lane, p);
+                else if (p.out_dtype == DT_F16)
+                    fp8_store_tile<__half, COLS>(acc, stg, &tmC, row0, col0, lane, p);
+                else
+                    fp8_store_tile<__nv_bfloat16, COLS>(acc, stg, &tmC, row0, col0, lane, p);
+            } else if (stored && row < p.M) {
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c) {
                     float o[32];
@@ -596,6 +659,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     }
 
     // ---------------------------------------------------- teardown
+    if (warp >= F8_EPI_WARP0 && lane == 0)
+        bulk_wait_group_read<0>();  // the output copies have read shared memory
     __syncwarp();
     tc_fence_before();
     if constexpr (CG == 2)
