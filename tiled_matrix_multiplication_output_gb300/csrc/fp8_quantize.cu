@@ -38,20 +38,26 @@ constexpr int Q_COLS = 8;      // columns per thread
 
 enum { Q_ROW = 1, Q_COL = 2, Q_TILE = 4 };
 
-// Magnitudes are compared as integers: with the sign bit cleared, IEEE
-// values order like their bits.  Adding one exponent step to the bits makes
-// the non-finite ones wrap past the sign bit, which is cleared, so they end
-// below every finite value and drop out of a maximum.
+// Magnitudes are compared as integers: with the sign bit cleared, IEEE values
+// order like their bits, non-finite ones above all others.  A maximum at or
+// above LIMIT (the bits of infinity) therefore says that a block holds a
+// value that is not finite, and only then is it taken again over magnitudes
+// that leave those out (`finite`).
 template <typename T>
 struct QIn;
 template <>
 struct QIn<float> {
     static constexpr int WORDS = 8;   // 32-bit words of 8 elements
-    static constexpr uint32_t BIAS = 0x00800000u;
-    static __device__ uint32_t mag(uint32_t w) { return ((w & 0x7fffffffu) + BIAS) & 0x7fffffffu; }
+    static constexpr uint32_t LIMIT = 0x7f800000u;
+    static __device__ uint32_t mag(uint32_t w) { return w & 0x7fffffffu; }
+    static __device__ uint32_t finite(uint32_t w)
+    {
+        const uint32_t m = mag(w);
+        return m < LIMIT ? m : 0u;
+    }
     static __device__ uint32_t vmax(uint32_t a, uint32_t b) { return max(a, b); }
     static __device__ uint32_t combine(uint32_t m) { return m; }
-    static __device__ float value(uint32_t m) { return m >= BIAS ? __uint_as_float(m - BIAS) : 0.0f; }
+    static __device__ float value(uint32_t m) { return __uint_as_float(m); }
     static __device__ void unpack(const uint32_t (&w)[8], float (&v)[8])
     {
 #pragma unroll
@@ -59,17 +65,23 @@ struct QIn<float> {
             v[i] = __uint_as_float(w[i]);
     }
 };
-template <>
-struct QIn<__nv_bfloat16> {
+// Two 16-bit values a word.
+template <uint32_t INF>
+struct QIn16 {
     static constexpr int WORDS = 4;
-    static constexpr uint32_t BIAS = 0x0080u;
-    static __device__ uint32_t mag(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x7fff7fffu; }
+    static constexpr uint32_t LIMIT = INF;
+    static __device__ uint32_t mag(uint32_t w) { return w & 0x7fff7fffu; }
+    static __device__ uint32_t finite(uint32_t w)
+    {
+        const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+        return (lo < INF ? lo : 0u) | ((hi < INF ? hi : 0u) << 16);
+    }
     static __device__ uint32_t vmax(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
     static __device__ uint32_t combine(uint32_t m) { return max(m & 0xffffu, m >> 16); }
-    static __device__ float value(uint32_t m)
-    {
-        return m >= BIAS ? __uint_as_float((m - BIAS) << 16) : 0.0f;
-    }
+};
+template <>
+struct QIn<__nv_bfloat16> : QIn16<0x7f80u> {
+    static __device__ float value(uint32_t m) { return __uint_as_float(m << 16); }
     static __device__ void unpack(const uint32_t (&w)[4], float (&v)[8])
     {
 #pragma unroll
@@ -80,15 +92,10 @@ struct QIn<__nv_bfloat16> {
     }
 };
 template <>
-struct QIn<__half> {
-    static constexpr int WORDS = 4;
-    static constexpr uint32_t BIAS = 0x0400u;
-    static __device__ uint32_t mag(uint32_t w) { return ((w & 0x7fff7fffu) + 0x04000400u) & 0x7fff7fffu; }
-    static __device__ uint32_t vmax(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-    static __device__ uint32_t combine(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+struct QIn<__half> : QIn16<0x7c00u> {
     static __device__ float value(uint32_t m)
     {
-        return m >= BIAS ? __half2float(__ushort_as_half(static_cast<unsigned short>(m - BIAS))) : 0.0f;
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(m)));
     }
     static __device__ void unpack(const uint32_t (&w)[4], float (&v)[8])
     {
@@ -112,15 +119,9 @@ __device__ __forceinline__ float q_scale(float amax, float inv_max)
     return amax > 0.0f ? fmaxf(__fmul_rn(amax, inv_max), 0x1p-126f) : 1.0f;
 }
 
-// Eight codes of v * r.  x * r + x * 0 is x * r for finite x (the added zero
-// changes nothing but a zero's sign where x * r is itself zero) and NaN
-// otherwise, where the saturating conversion alone would give +-F for an
-// infinity.
-__device__ __forceinline__ uint32_t q_pair(float lo, float hi, int f8)
+__device__ __forceinline__ uint32_t q_pair(float lo, float hi, __nv_fp8_interpretation_t kind)
 {
-    const __nv_fp8x2_storage_t s = __nv_cvt_float2_to_fp8x2(
-        make_float2(lo, hi), __NV_SATFINITE, f8 == F8_E4M3 ? __NV_E4M3 : __NV_E5M2);
-    return static_cast<uint32_t>(s);
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, kind);
 }
 
 struct QParams {
@@ -135,21 +136,25 @@ struct QParams {
     int64_t lds_row, lds_col, lds_tile;
 };
 
-// One thread's 8 codes of one row; `n` of them lie inside the matrix.
+// One thread's 8 codes x * r of one row; `n` of them lie inside the matrix.
+// EXACT: some of them may be infinite.  Then x * r + x * 0 makes those NaN,
+// where the saturating conversion alone would give +-F, and is x * r for the
+// finite ones.  (A NaN stays one either way.)
+template <bool EXACT>
 __device__ __forceinline__ void q_store(uint8_t* dst, const float (&v)[8], const float (&r)[8],
                                         int n, int f8)
 {
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        t[i] = fmaf(v[i], r[i], __fmul_rn(v[i], 0.0f));
+        t[i] = EXACT ? fmaf(v[i], r[i], __fmul_rn(v[i], 0.0f)) : __fmul_rn(v[i], r[i]);
     uint32_t lo, hi;
     if (f8 == F8_E4M3) {
-        lo = q_pair(t[0], t[1], F8_E4M3) | (q_pair(t[2], t[3], F8_E4M3) << 16);
-        hi = q_pair(t[4], t[5], F8_E4M3) | (q_pair(t[6], t[7], F8_E4M3) << 16);
+        lo = q_pair(t[0], t[1], __NV_E4M3) | (q_pair(t[2], t[3], __NV_E4M3) << 16);
+        hi = q_pair(t[4], t[5], __NV_E4M3) | (q_pair(t[6], t[7], __NV_E4M3) << 16);
     } else {
-        lo = q_pair(t[0], t[1], F8_E5M2) | (q_pair(t[2], t[3], F8_E5M2) << 16);
-        hi = q_pair(t[4], t[5], F8_E5M2) | (q_pair(t[6], t[7], F8_E5M2) << 16);
+        lo = q_pair(t[0], t[1], __NV_E5M2) | (q_pair(t[2], t[3], __NV_E5M2) << 16);
+        hi = q_pair(t[4], t[5], __NV_E5M2) | (q_pair(t[6], t[7], __NV_E5M2) << 16);
     }
     if (n == 8) {
         *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
@@ -159,23 +164,172 @@ __device__ __forceinline__ void q_store(uint8_t* dst, const float (&v)[8], const
     }
 }
 
-template <typename InT, int FORMS, bool VEC>
-__global__ void __launch_bounds__(Q_THREADS) fp8_quantize_kernel(const QParams p)
+// The largest magnitude of a thread's 8 elements of a row (a word, to be
+// combined) and of its 8 columns over its rows.
+template <typename In, bool EXACT>
+__device__ __forceinline__ uint32_t q_mag(uint32_t w)
+{
+    return EXACT ? In::finite(w) : In::mag(w);
+}
+
+// The tile in registers: maxima, scales, codes.  EXACT as in q_store; without
+// it, returns false as soon as a maximum shows a value that is not finite,
+// for the whole block alike and before anything is written.
+template <typename InT, int FORMS, bool EXACT>
+__device__ __forceinline__ bool q_tile(const QParams& p, const uint32_t (&w)[Q_ROWS][QIn<InT>::WORDS],
+                                       uint32_t (&s_max)[Q_THREADS / 32][16 * QIn<InT>::WORDS], int rb,
+                                       int cb, int row0, int col0, int nrow, int ncol)
 {
     using In = QIn<InT>;
     constexpr int W = In::WORDS;
-    __shared__ uint32_t s_max[(FORMS & (Q_COL | Q_TILE)) ? Q_THREADS / 32 : 1][16 * W];
-
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
     const int cg = tid & 15, rg = tid >> 4;
+    const float inv_max = q_inverse_max(p.f8);
+
+    // a maximum for each column of the thread over its rows, then over the
+    // warp's two row groups and (through shared memory) the warps
+    uint32_t m[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        m[j] = q_mag<In, EXACT>(w[0][j]);
+#pragma unroll
+        for (int i = 1; i < Q_ROWS; ++i)
+            m[j] = In::vmax(m[j], q_mag<In, EXACT>(w[i][j]));
+    }
+    uint32_t all = m[0];
+#pragma unroll
+    for (int j = 1; j < W; ++j)
+        all = In::vmax(all, m[j]);
+    all = In::combine(all);
+    if constexpr ((FORMS & Q_COL) != 0) {
+        if (!EXACT && __syncthreads_or(all >= In::LIMIT))
+            return false;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            m[j] = In::vmax(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+        if (lane < 16) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                s_max[warp][cg * W + j] = m[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < Q_THREADS / 32; ++k) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                m[j] = In::vmax(m[j], s_max[k][cg * W + j]);
+        }
+    } else if constexpr ((FORMS & Q_TILE) != 0) {
+        all = __reduce_max_sync(0xffffffffu, all);
+        if (lane == 0)
+            s_max[warp][0] = all;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < Q_THREADS / 32; ++k)
+            all = max(all, s_max[k][0]);
+        if (!EXACT && all >= In::LIMIT)
+            return false;
+    } else {
+        if (!EXACT && __any_sync(0xffffffffu, all >= In::LIMIT))
+            return false;  // (a warp's rows are its own)
+    }
+
+    float rc[8];  // the factors of the column or tile form
+    if constexpr ((FORMS & Q_COL) != 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = W == 8 ? m[j % W] : (m[j >> 1] >> (16 * (j & 1))) & 0xffffu;
+            const float s = q_scale(In::value(b), inv_max);
+            rc[j] = __frcp_rn(s);
+            if (rg == 0 && j < ncol)
+                p.s_col[rb * p.lds_col + col0 + j] = s;
+        }
+    } else if constexpr ((FORMS & Q_TILE) != 0) {
+        const float s = q_scale(In::value(all), inv_max);
+        if (tid == 0)
+            p.s_tile[rb * p.lds_tile + cb] = s;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            rc[j] = __frcp_rn(s);
+    }
+    // The factors of the thread's rows: maxima over the 16 lanes that share
+    // them (two 16-bit ones a shuffle), then each lane takes one row's scale
+    // and inverse, and the inverses go round.
+    float rr[Q_ROWS];
+    if constexpr ((FORMS & Q_ROW) != 0) {
+        constexpr int PER = W == 8 ? 1 : 2;  // rows per word
+        uint32_t t[Q_ROWS / PER];
+#pragma unroll
+        for (int i = 0; i < Q_ROWS; ++i) {
+            uint32_t u = q_mag<In, EXACT>(w[i][0]);
+#pragma unroll
+            for (int j = 1; j < W; ++j)
+                u = In::vmax(u, q_mag<In, EXACT>(w[i][j]));
+            u = In::combine(u);
+            t[i / PER] = i % PER ? t[i / PER] | (u << 16) : u;
+        }
+#pragma unroll
+        for (int i = 0; i < Q_ROWS / PER; ++i) {
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1)
+                t[i] = In::vmax(t[i], __shfl_xor_sync(0xffffffffu, t[i], d));
+        }
+        const int own = cg & 7;
+        uint32_t u = t[0];
+#pragma unroll
+        for (int i = 1; i < Q_ROWS / PER; ++i)
+            u = own / PER == i ? t[i] : u;
+        if (PER == 2)
+            u = (u >> (16 * (own & 1))) & 0xffffu;
+        const float s = q_scale(In::value(u), inv_max);
+        if (cg < nrow)
+            p.s_row[cb * p.lds_row + row0 + cg] = s;
+        const float r = __frcp_rn(s);
+#pragma unroll
+        for (int i = 0; i < Q_ROWS; ++i)
+            rr[i] = __shfl_sync(0xffffffffu, r, i, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < Q_ROWS; ++i) {
+        float v[8];
+        In::unpack(w[i], v);
+        if constexpr ((FORMS & Q_ROW) != 0) {
+            float r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                r[j] = rr[i];
+            if (i < nrow)
+                q_store<EXACT>(p.q_row + static_cast<int64_t>(row0 + i) * p.ld_row + col0, v, r, ncol, p.f8);
+        }
+        if constexpr ((FORMS & Q_COL) != 0) {
+            if (i < nrow)
+                q_store<EXACT>(p.q_col + static_cast<int64_t>(row0 + i) * p.ld_col + col0, v, rc, ncol, p.f8);
+        }
+        if constexpr ((FORMS & Q_TILE) != 0) {
+            if (i < nrow)
+                q_store<EXACT>(p.q_tile + static_cast<int64_t>(row0 + i) * p.ld_tile + col0, v, rc, ncol,
+                               p.f8);
+        }
+    }
+    return true;
+}
+
+// Blocks on an SM: each holds 32 KiB (16-bit X) or 64 KiB in flight.
+template <typename InT, int FORMS, bool VEC>
+__global__ void __launch_bounds__(Q_THREADS, sizeof(InT) == 4 ? 2 : FORMS == (Q_ROW | Q_COL) ? 3 : 4)
+    fp8_quantize_kernel(const QParams p)
+{
+    constexpr int W = QIn<InT>::WORDS;
+    __shared__ uint32_t s_max[Q_THREADS / 32][16 * W];
+
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int cb = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.col_blocks));
     const int rb = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.col_blocks));
     const int row0 = rb * QT + rg * Q_ROWS;
     const int col0 = cb * QT + cg * Q_COLS;
     const int ncol = min(max(p.cols - col0, 0), Q_COLS);   // columns of this thread inside X
     const int nrow = min(max(p.rows - row0, 0), Q_ROWS);
-    const float inv_max = q_inverse_max(p.f8);
 
     // ---- load: zeros outside X, which change no maximum
     uint32_t w[Q_ROWS][W];
@@ -211,118 +365,10 @@ __global__ void __launch_bounds__(Q_THREADS) fp8_quantize_kernel(const QParams p
         }
     }
 
-    // ---- 1 x 128: a maximum over the 16 lanes that share a row
-    if constexpr ((FORMS & Q_ROW) != 0) {
-        float mine = 0.0f;  // the scale of row row0 + cg, kept for a coalesced store
-#pragma unroll
-        for (int i = 0; i < Q_ROWS; ++i) {
-            uint32_t m = In::mag(w[i][0]);
-#pragma unroll
-            for (int j = 1; j < W; ++j)
-                m = In::vmax(m, In::mag(w[i][j]));
-            m = In::combine(m);
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1)
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-            const float s = q_scale(In::value(m), inv_max);
-            if (cg == i)
-                mine = s;
-            const float r = __frcp_rn(s);
-            if (i < nrow) {
-                float v[8], rr[8];
-                In::unpack(w[i], v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    rr[j] = r;
-                q_store(p.q_row + static_cast<int64_t>(row0 + i) * p.ld_row + col0, v, rr, ncol, p.f8);
-            }
-        }
-        if (cg < nrow)
-            p.s_row[cb * p.lds_row + row0 + cg] = mine;
-    }
-
-    if constexpr ((FORMS & (Q_COL | Q_TILE)) != 0) {
-        // this thread's columns over its rows, then over the warp's two row groups
-        uint32_t m[W];
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            m[j] = In::mag(w[0][j]);
-#pragma unroll
-            for (int i = 1; i < Q_ROWS; ++i)
-                m[j] = In::vmax(m[j], In::mag(w[i][j]));
-            m[j] = In::vmax(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
-        }
-        if constexpr ((FORMS & Q_TILE) != 0) {
-            uint32_t t = m[0];
-#pragma unroll
-            for (int j = 1; j < W; ++j)
-                t = In::vmax(t, m[j]);
-            t = In::combine(t);
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1)
-                t = max(t, __shfl_xor_sync(0xffffffffu, t, d));
-            if (lane == 0)
-                s_max[warp][0] = t;
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < Q_THREADS / 32; ++k)
-                t = max(t, s_max[k][0]);
-            const float s = q_scale(In::value(t), inv_max);
-            if (tid == 0)
-                p.s_tile[rb * p.lds_tile + cb] = s;
-            const float r = __frcp_rn(s);
-#pragma unroll
-            for (int i = 0; i < Q_ROWS; ++i) {
-                if (i < nrow) {
-                    float v[8], rr[8];
-                    In::unpack(w[i], v);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        rr[j] = r;
-                    q_store(p.q_tile + static_cast<int64_t>(row0 + i) * p.ld_tile + col0, v, rr, ncol,
-                            p.f8);
-                }
-            }
-        } else {
-            if (lane < 16) {
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    s_max[warp][cg * W + j] = m[j];
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < Q_THREADS / 32; ++k) {
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    m[j] = In::vmax(m[j], s_max[k][cg * W + j]);
-            }
-            float s[8], r[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t b;
-                if constexpr (W == 8)
-                    b = m[j];
-                else
-                    b = (m[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-                s[j] = q_scale(In::value(b), inv_max);
-                r[j] = __frcp_rn(s[j]);
-            }
-            if (rg == 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < ncol)
-                        p.s_col[rb * p.lds_col + col0 + j] = s[j];
-            }
-#pragma unroll
-            for (int i = 0; i < Q_ROWS; ++i) {
-                if (i < nrow) {
-                    float v[8];
-                    In::unpack(w[i], v);
-                    q_store(p.q_col + static_cast<int64_t>(row0 + i) * p.ld_col + col0, v, r, ncol,
-                            p.f8);
-                }
-            }
-        }
+    if (!q_tile<InT, FORMS, false>(p, w, s_max, rb, cb, row0, col0, nrow, ncol)) {
+        if (FORMS != Q_ROW)
+            __syncthreads();  // the maxima in shared memory have been read
+        q_tile<InT, FORMS, true>(p, w, s_max, rb, cb, row0, col0, nrow, ncol);
     }
 }
 
