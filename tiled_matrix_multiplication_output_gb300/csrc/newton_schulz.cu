@@ -208,28 +208,33 @@ __device__ __forceinline__ uint64_t ns_desc_hi(bool mn)
 }
 
 // One warp's part of a finished tile: rows `row` (one a lane), COLS columns
-// from col0.  The first addend is fetched before `wait`, which returns once
-// the accumulator at taddr is complete (false: given up).
+// from col0 in chunks of 32.  The addend is fetched two chunks ahead, the
+// first two before `wait`, which returns once the accumulator at taddr is
+// complete (false: given up).
 template <int MODE, int COLS, typename Wait>
 __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands& o, int z, bool mirror,
                                             int row, int col0, uint32_t taddr, Wait&& wait)
 {
     const bool inside = row < p.M;
     const long long at_add = z * p.batch_add + row * p.ld_add + col0;
-    uint32_t ah[16], al[16];
-    auto fetch = [&](int c) {  // the addend of chunk c
+    uint32_t ah[2][16], al[2][16];
+    auto fetch = [&](int c, int b) {  // the addend of chunk c
         const int n = inside ? p.N - col0 - c * 32 : 0;
         if constexpr (MODE != NS_GRAM)
-            ns_load_row(o.add + at_add + c * 32, n, ah);
+            ns_load_row(o.add + at_add + c * 32, n, ah[b]);
         if constexpr (MODE >= NS_UPDATE)
-            ns_load_row(p.lo + at_add + c * 32, n, al);
+            ns_load_row(p.lo + at_add + c * 32, n, al[b]);
     };
-    fetch(0);
+    fetch(0, 0);
+    fetch(1, 1);
     if (!wait())
         return;
     tc_fence_after();
 #pragma unroll 1
-    for (int c = 0; c < COLS / 32; ++c) {
+    for (int c0 = 0; c0 < COLS / 32; c0 += 2)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int c = c0 + b;
         const int col = col0 + c * 32;
         const int n = min(p.N - col, 32);
         if (n <= 0)
@@ -243,9 +248,9 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands&
             f[2 * i] = o.alpha * __uint_as_float(v[2 * i]);
             f[2 * i + 1] = o.alpha * __uint_as_float(v[2 * i + 1]);
             if constexpr (MODE != NS_GRAM) {
-                float2 a = ns_unpack(ah[i]);
+                float2 a = ns_unpack(ah[b][i]);
                 if constexpr (MODE >= NS_UPDATE) {
-                    const float2 l = ns_unpack(al[i]);
+                    const float2 l = ns_unpack(al[b][i]);
                     a.x = fmaf(l.x, 1.0f / NS_LO, a.x);
                     a.y = fmaf(l.y, 1.0f / NS_LO, a.y);
                 }
@@ -253,8 +258,8 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands&
                 f[2 * i + 1] = fmaf(o.beta, a.y, f[2 * i + 1]);
             }
         }
-        if (c + 1 < COLS / 32)
-            fetch(c + 1);
+        if (c + 2 < COLS / 32)
+            fetch(c + 2, b);
         if constexpr (MODE == NS_LAST) {
             if (inside) {
                 const long long at = z * p.batch_res + row * p.ld_res + col;
@@ -374,7 +379,6 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------ TMA producer
-            fence_proxy_async_all();  // the operands were written by plain stores
             int stage = 0;
             uint32_t phase = 0;
             int issued[STAGES];
