@@ -356,3 +356,35 @@ def test_a_wait_that_runs_out_is_reported(M, N, K):
     C = tg.matmul_fp8(*a[:2], *b[:2])
     _status()
     _expect(C, a, "n", b, "t", K)
+
+
+def test_offsets_beyond_32_bits():
+    """Inputs, codes and outputs of more than 2^31 elements: the last rows
+    are as exact as the first."""
+    rows, cols = 36000, 60000
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    some = [0, 17, rows // 2, rows - 1]
+    x[some] = _draw(4, cols, "bf16", seed=80).cuda()
+    q, s = tg.quantize_fp8(x)
+    want_q, want_s = ref.quantize(x[some].float().cpu().numpy(), "row", "e4m3")
+    np.testing.assert_array_equal(s[:, some].cpu().numpy(), want_s)
+    np.testing.assert_array_equal(q[some].float().cpu().numpy(), want_q)
+    del x
+    # the contraction over the rows of the first: 36000 x 60000, as a K x M operand
+    w, ws, _ = _operand(24, rows, True, "vector", "e4m3", 81, True)
+    sc = torch.ones(-(-rows // 128), cols, device="cuda")
+    C = tg.matmul_fp8(w, ws, q, sc, op_a="n", op_b="n")
+    _status()
+    b = q[some].double().cpu().numpy()
+    a = w[:, some].double().cpu().numpy() * ws.t()[:, [r // 128 for r in some]].double().cpu().numpy()
+    np.testing.assert_allclose(C.double().cpu().numpy(), a @ b, rtol=1e-6, atol=1e-6 * np.abs(a @ b).max())
+    del C, q, sc
+    # an output beyond 2^31 elements
+    a, sa, na = _operand(rows, 64, True, "vector", "e4m3", 82, True)
+    b, sb, nb = _operand(cols, 64, True, "tile", "e4m3", 83, True)
+    C = tg.matmul_fp8(a, sa, b, sb, out_dtype="bf16")
+    _status()
+    pick = a[some], sa[:, some].contiguous()
+    cref, _ = _reference(*pick, na, "n", b, sb, nb, "t")
+    np.testing.assert_array_equal(C[some].double().cpu().numpy(),
+                                  torch.from_numpy(cref).to(torch.bfloat16).double().numpy())

@@ -14,8 +14,9 @@ ABC = tg.NEWTON_SCHULZ_COEFFICIENTS
 
 # The result is stated to be within 2e-3 of exact arithmetic (relative, 2-norm
 # of all elements) before it is rounded to the output type; FP16 storage of
-# A and B alone moves it by about 1e-3.  4e-3 leaves a factor of two, and the
-# output's rounding adds at most half an ulp, 2^-9 for BF16, to every element.
+# A and B alone moves it by about 1e-3.  4e-3 leaves a factor of two.  The
+# output's rounding, half an ulp (2^-8 of an element for BF16) at worst and
+# evenly spread, adds less than half of that over all elements.
 STATED = 4e-3
 ROUNDING = {"f32": 0.0, "f16": 2.0 ** -12, "bf16": 2.0 ** -9}
 
