@@ -59,6 +59,7 @@ class Fp8Matrix(ctypes.Structure):
 # The same layout as bytes, which are quicker to make.
 _FP8_MATRIX = struct.Struct("@PqiiPqi4x")
 assert _FP8_MATRIX.size == ctypes.sizeof(Fp8Matrix)
+_pack_matrix = _FP8_MATRIX.pack
 
 
 _SIGNATURES = {
@@ -452,16 +453,24 @@ def _out_dtype(out_dtype):
 
 
 def _f8_code(dtype) -> int:
-    torch = _torch()
     if isinstance(dtype, str):
         if dtype not in F8_CODES:
             raise ValueError(f"unknown 8-bit type {dtype!r}")
         return F8_CODES[dtype]
-    if dtype is torch.float8_e4m3fn:
-        return E4M3
-    if dtype is torch.float8_e5m2:
-        return E5M2
-    raise TypeError(f"{dtype} is not an 8-bit floating-point type")
+    code = _f8_dtypes()[1].get(dtype)
+    if code is None:
+        raise TypeError(f"{dtype} is not an 8-bit floating-point type")
+    return code
+
+
+_torch_c_module = None
+
+
+def _torch_c():
+    global _torch_c_module
+    if _torch_c_module is None:
+        _torch_c_module = _torch()._C
+    return _torch_c_module
 
 
 def _allocate(stream, make, *args):
@@ -479,46 +488,63 @@ def _stream_ptr(stream, x) -> int:
     below take about 10 us of host time in all."""
     if stream is not None:
         return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(x.get_device())
+    return _torch_c()._cuda_getCurrentRawStream(x.get_device())
 
 
 def _check_matrix(x, what):
-    """Returns (rows, cols, row stride) of a 2-D CUDA tensor with contiguous rows."""
-    if x.dim() != 2 or not x.is_cuda:
+    """Returns (rows, cols, row stride) of a 2-D tensor with contiguous rows on
+    the current CUDA device."""
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 2 or not x.is_cuda:
         raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    if x.get_device() != _torch()._C._cuda_getDevice():
+    if x.get_device() != _torch_c()._cuda_getDevice():
         raise ValueError(f"{what} is not on the current device")
-    rows, cols = x.shape
-    pitch, step = x.stride()
+    rows, cols = shape
+    pitch, step = strides
     if step != 1 and cols > 1:
         raise ValueError(f"{what}'s rows must be contiguous")
-    if pitch < cols and rows > 1:
+    if rows <= 1:  # a single row has no pitch of its own
+        return rows, cols, (cols + 15) // 16 * 16
+    if pitch < cols:
         raise ValueError(f"{what}'s rows must not overlap")
-    # a single row has no pitch of its own
-    return rows, cols, pitch if rows > 1 else (cols + 15) // 16 * 16
+    return rows, cols, pitch
+
+
+_f8_types = None
+
+
+def _f8_dtypes() -> tuple:
+    """PyTorch's types by code, and the codes by type."""
+    global _f8_types
+    if _f8_types is None:
+        torch = _torch()
+        types = (torch.float8_e4m3fn, torch.float8_e5m2)
+        _f8_types = types, {types[E4M3]: E4M3, types[E5M2]: E5M2}
+    return _f8_types
 
 
 def _fp8_empty(rows, cols, f8, block, device):
     """Uninitialised codes with a row pitch of a multiple of 16, their pitch,
     scales and their pitch."""
-    torch = _torch()
+    empty = _torch().empty
     ld = (cols + 15) // 16 * 16
-    q = torch.empty((rows, ld), device=device,
-                    dtype=torch.float8_e4m3fn if f8 == E4M3 else torch.float8_e5m2)
+    q = empty((rows, ld), device=device, dtype=_f8_dtypes()[0][f8])
     if ld != cols:
         q = q[:, :cols]
-    rb, cb = (rows + 127) // 128, (cols + 127) // 128
-    n, lds = ((cb, rows), (rb, cols), (rb, cb))[block]
-    return q, ld, torch.empty((n, lds), dtype=torch.float32, device=device), lds
+    if block == 0:
+        n, lds = (cols + 127) // 128, rows
+    else:
+        n, lds = (rows + 127) // 128, cols if block == 1 else (cols + 127) // 128
+    return q, ld, empty((n, lds), dtype=_torch().float32, device=device), lds
 
 
 def _quantize_input(x):
     """(rows, cols, row stride, type code) of a tensor to quantise."""
-    shape = _check_matrix(x, "x")
+    rows, cols, ldx = _check_matrix(x, "x")
     code = _dtype_codes().get(x.dtype)
     if code is None:
         raise TypeError("x must be FP32, FP16 or BF16")
-    return (*shape, code)
+    return rows, cols, ldx, code
 
 
 def quantize_fp8(x, block: str = "row", dtype="e4m3", stream=None):
@@ -566,21 +592,22 @@ def _fp8_operand(q, s, op, k_rows, what):
     """(stored rows, stored columns, the bytes of its gemm_fp8_matrix_t) of
     codes q and scales s; k_rows: q's rows run along K."""
     rows, cols, ld = _check_matrix(q, what)
-    torch = _torch()
-    if s.dtype is not torch.float32 or not s.is_cuda or s.dim() != 2 or not s.is_contiguous():
+    if s.dtype is not _torch().float32 or s.dim() != 2 or not (s.is_cuda and s.is_contiguous()):
         raise ValueError(f"{what}'s scales must be a contiguous 2-D FP32 CUDA tensor")
     rb, cb = (rows + 127) // 128, (cols + 127) // 128
     n, lds = s.shape
-    if (n, lds) == ((cb, rows) if k_rows else (rb, cols)):
-        block = 0 if k_rows else 1
-    elif (n, lds) == (rb, cb):
+    if k_rows and n == cb and lds == rows:
+        block = 0
+    elif not k_rows and n == rb and lds == cols:
+        block = 1
+    elif n == rb and lds == cb:
         block = 2
     else:
         raise ValueError(f"{what}'s scales have shape {(n, lds)}: expected "
                          f"{(cb, rows) if k_rows else (rb, cols)} (a vector along the "
                          f"contraction) or {(rb, cb)} (128 x 128 blocks)")
-    return rows, cols, _FP8_MATRIX.pack(q.data_ptr(), ld, _f8_code(q.dtype), block, s.data_ptr(),
-                                        lds, op)
+    return rows, cols, _pack_matrix(q.data_ptr(), ld, _f8_code(q.dtype), block, s.data_ptr(), lds,
+                                    op)
 
 
 def matmul_fp8(a, a_scale, b, b_scale, op_a="n", op_b="t", out_dtype=None, out=None, alpha=1.0,
