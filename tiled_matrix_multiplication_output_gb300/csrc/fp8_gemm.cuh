@@ -42,7 +42,7 @@
 
 #include "fp8.h"
 #include "launch.h"
-#include "tc_gemm.cuh"
+#include "ops.cuh"
 
 namespace tmmo {
 
@@ -579,41 +579,62 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 const bool more = kb + 1 < p.k_blocks;
                 const bool slot_end = (kb + 1) % L::GROUP == 0 || !more;
                 const uint32_t sempty = sempty_bar(slot);
+                // the block has been read: its partial buffer may be refilled
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2)
+                            mbar_arrive_cluster_relaxed(tempty0 + 8u * SUB * buf);
+                        else
+                            mbar_arrive(tempty0 + 8u * SUB * buf);
+                    }
+                    if (++buf == NBUF)
+                        buf = 0;
+                    if (slot_end && ++slot == L::SLOTS)
+                        slot = 0;
+                };
+                if constexpr (COLV) {
+                    // The products of the scales are formed while the chunk
+                    // is on its way from tensor memory, in the registers of a
+                    // second chunk.
 #pragma unroll
-                for (int c = 0; c < NCH; ++c) {
-                    tmem_wait_ld();
-                    if (c + 1 < NCH) {
-                        tmem_ld_32x32b_x32(taddr + (c + 1) * 32, v[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if constexpr (CG == 2)
-                                mbar_arrive_cluster_relaxed(tempty0 + 8u * SUB * buf);
-                            else
-                                mbar_arrive(tempty0 + 8u * SUB * buf);
+                    for (int c = 0; c < NCH; ++c) {
+                        uint64_t f[16];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            uint32_t w[4];
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                         : "r"(cols + (c * 32 + 2 * i) * 4));
+                            f[i] = fmul2(rs2, pack_f32x2(w[0], w[1]));
+                            f[i + 1] = fmul2(rs2, pack_f32x2(w[2], w[3]));
                         }
-                        if (++buf == NBUF)
-                            buf = 0;
-                        if (slot_end && ++slot == L::SLOTS)
-                            slot = 0;
-                        if (more)
+                        tmem_wait_ld(v[0]);
+                        if (c + 1 == NCH)
+                            release();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            ffma2(acc[c * 16 + i], pack_f32x2(v[0][2 * i], v[0][2 * i + 1]), f[i]);
+                        if (c + 1 < NCH)
+                            tmem_ld_32x32b_x32(taddr + (c + 1) * 32, v[0]);
+                        else if (more)
                             begin(kb + 1);
                     }
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        uint64_t s0 = rs2, s1 = rs2;
-                        if constexpr (COLV) {
-                            uint32_t f[4];
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-                                         : "r"(cols + (c * 32 + 2 * i) * 4));
-                            s0 = fmul2(rs2, pack_f32x2(f[0], f[1]));
-                            s1 = fmul2(rs2, pack_f32x2(f[2], f[3]));
+                    for (int c = 0; c < NCH; ++c) {
+                        tmem_wait_ld(v[c & 1]);
+                        if (c + 1 < NCH) {
+                            tmem_ld_32x32b_x32(taddr + (c + 1) * 32, v[(c + 1) & 1]);
+                        } else {
+                            release();
+                            if (more)
+                                begin(kb + 1);
                         }
-                        ffma2(acc[c * 16 + i], pack_f32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s0);
-                        ffma2(acc[c * 16 + i + 1], pack_f32x2(v[c & 1][2 * i + 2], v[c & 1][2 * i + 3]),
-                              s1);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            ffma2(acc[c * 16 + i], pack_f32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), rs2);
                     }
                 }
                 if (slot_end) {

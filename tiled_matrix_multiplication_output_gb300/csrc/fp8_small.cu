@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(FS_THREADS, 2)
                     tmem_ld_32x32b_x16(taddr, v);
                 else
                     tmem_ld_32x32b_x32(taddr + c * 32, v);
-                tmem_wait_ld();
+                tmem_wait_ld(v);
                 if (c + 1 == BN / CH) {
                     tc_fence_before();
                     __syncwarp();

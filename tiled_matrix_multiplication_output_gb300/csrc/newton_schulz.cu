@@ -241,7 +241,7 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands&
             break;
         uint32_t v[32];
         tmem_ld_32x32b_x32(taddr + c * 32, v);
-        tmem_wait_ld();
+        tmem_wait_ld(v);
         float f[32];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {

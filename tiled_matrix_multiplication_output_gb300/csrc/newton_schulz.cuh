@@ -6,7 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "launch.h"
-#include "tc_gemm.cuh"
+#include "ops.cuh"
 
 namespace tmmo {
 

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
                 const int col = (2 * g + c) * 32;
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tmem + col, v);
-                tmem_wait_ld();
+                tmem_wait_ld(v);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t w[4];
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
                 const int col = (2 * g + c) * 32;
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tmem + col, v);
-                tmem_wait_ld();
+                tmem_wait_ld(v);
                 if (n_steps == 0) {  // a block without columns adds nothing
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 ld_shared_v4(nr_addr(sA, row, col + 8 * k), w[k]);
-            tmem_wait_ld();
+            tmem_wait_ld(v);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
             if ((2 * c + g) * 32 < ncol) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tmem + (2 * c + g) * 32, v);
-                tmem_wait_ld();
+                tmem_wait_ld(v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     x[c][i] = fmaf(ca, x[c][i], (1.0f / NS_SB) * __uint_as_float(v[i]));

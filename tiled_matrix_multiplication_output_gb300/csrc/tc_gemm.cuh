@@ -208,31 +208,6 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const TcW
     }
 }
 
-// Bounded wait of a whole warp on an mbarrier phase: every lane polls, so no
-// branch diverges, and the poll does not suspend the warp.  For waits
-// on the critical path of a K step: one lane waiting for the others with
-// tc_wait (a divergent loop, a suspending poll, a shuffle) costs about 300
-// cycles more.
-__device__ __forceinline__ bool tc_wait_warp(uint32_t bar, uint32_t parity, const TcWatch& w)
-{
-    long long t0 = 0;
-    for (uint32_t n = 1;; ++n) {
-        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity)))
-            return true;
-        if ((n & 1023u) != 0)
-            continue;
-        // now and then: has another role given up, or the budget run out?
-        const long long now = clock64();
-        if (t0 == 0)
-            t0 = now;
-        const bool late = now - t0 > w.budget;
-        if (late)
-            tc_raise(w);
-        if (__any_sync(0xffffffffu, late || *w.abort_flag))
-            return false;
-    }
-}
-
 template <typename OutT>
 struct TcOut;
 template <>
