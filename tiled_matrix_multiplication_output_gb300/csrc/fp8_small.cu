@@ -31,7 +31,7 @@
 namespace tmmo {
 namespace {
 
-constexpr int FS_THREADS = 256;  // warps 0: copies, 1: MMA, 2: scales, 4-7: epilogue
+constexpr int FS_THREADS = 256;  // warps 0: copies, 1: MMA, 2: scales, 3: herald, 4-7: epilogue
 constexpr int FS_EPI_WARP0 = 4;
 constexpr int FS_MAX_SPLITS = 8;
 
@@ -264,7 +264,20 @@ __global__ void __launch_bounds__(FS_THREADS, 2)
             cp_async_mbar_arrive(sfull_bar(slot));
         }
         cp_async_wait_all();
-    } else if (warp >= FS_EPI_WARP0) {
+    } else if (warp == 3) {
+        // ------------------------------------------------ herald, as in
+        // fp8_gemm_kernel: a poll of an mbarrier takes about 300 cycles even
+        // when it succeeds, a hardware barrier that the herald has already
+        // reached about 40
+        for (int i = 0; i < nkb; ++i) {
+            const int g = i / L::GROUP;
+            if (i % L::GROUP == 0)
+                ok = ok && tc_wait_warp(sfull_bar(g % L::SLOTS),
+                                        static_cast<uint32_t>((g / L::SLOTS) & 1), watch);
+            ok = ok && tc_wait_warp(done_bar(i % STAGES), static_cast<uint32_t>((i / STAGES) & 1), watch);
+            bar_sync(F8_HERALD_BAR, 160);
+        }
+    } else {
         // ------------------------------------------------ promotion
         const int q = warp & 3;
 #pragma unroll
@@ -272,12 +285,8 @@ __global__ void __launch_bounds__(FS_THREADS, 2)
             acc[j] = 0;
 #pragma unroll 1
         for (int i = 0; i < nkb; ++i) {
-            const int s = i % STAGES, b = i % NBUF, g = i / L::GROUP, slot = g % L::SLOTS;
-            if (i % L::GROUP == 0)
-                ok = tc_wait_warp(sfull_bar(slot), static_cast<uint32_t>((g / L::SLOTS) & 1), watch);
-            ok = ok && tc_wait_warp(done_bar(s), static_cast<uint32_t>((i / STAGES) & 1), watch);
-            if (!ok)
-                break;
+            const int b = i % NBUF, slot = i / L::GROUP % L::SLOTS;
+            bar_sync(F8_HERALD_BAR, 160);
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(b * BN);
@@ -317,7 +326,7 @@ __global__ void __launch_bounds__(FS_THREADS, 2)
                     mbar_arrive(sempty_bar(slot));
             }
         }
-        ok = ok && !*abort_flag;
+        ok = !*abort_flag;  // an unfinished sum is not used
     }
 
     // ------------------------------------------------ sums of the cluster, output
