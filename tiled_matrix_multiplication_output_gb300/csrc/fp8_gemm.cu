@@ -109,8 +109,6 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
     p.C = l.C;
     p.ldc = l.ldc;
     p.out_dtype = l.out_dtype;
-    p.vec_out = (reinterpret_cast<uintptr_t>(l.C) & 31u) == 0 &&
-                (l.ldc * out_bytes(l.out_dtype)) % 32 == 0;
     p.alpha = l.alpha;
     p.beta = l.beta;
     p.status = l.status;

@@ -74,7 +74,6 @@ struct Fp8Params {
     long long ldc;
     int out_dtype;                 // DT_*
     bool tma_out;                  // the output goes through a tensor map (beta == 0)
-    bool vec_out;                  // C's rows take 32-byte accesses
     float alpha, beta;
     int* status;
     long long wait_budget;
@@ -125,8 +124,6 @@ __device__ __forceinline__ uint64_t fp8_desc_hi(uint32_t row_bytes, bool mn)
            (static_cast<uint64_t>(row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6) << 61);
 }
 
-// alpha * v + beta * C for a run of `N` values of one row, stored in OutT.
-// in: how many of them lie inside C.  vec: 16-byte accesses are allowed.
 template <typename OutT>
 __device__ __forceinline__ OutT fp8_to_out(float v)
 {
@@ -136,47 +133,6 @@ __device__ __forceinline__ OutT fp8_to_out(float v)
         return __float2half_rn(v);
     else
         return __float2bfloat16_rn(v);
-}
-
-template <typename OutT>
-__device__ __forceinline__ void fp8_axpby(float* v, int n, const OutT* src, float alpha, float beta)
-{
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        v[i] *= alpha;
-        if (beta != 0.0f && i < n)
-            v[i] = fmaf(beta, out_to_f32(src[i]), v[i]);
-    }
-}
-
-// 32 values of one row of C straight from registers, `n` of them inside C.
-template <typename OutT>
-__device__ __forceinline__ void fp8_store_row(OutT* dst, float* v, int n, const Fp8Params& p)
-{
-    if (n <= 0)
-        return;
-    if (p.alpha != 1.0f || p.beta != 0.0f)
-        fp8_axpby<OutT>(v, n, dst, p.alpha, p.beta);
-    constexpr int PER = 32 / static_cast<int>(sizeof(OutT));  // values per 32-byte sector
-#pragma unroll
-    for (int c = 0; c < 32 / PER; ++c) {
-        if (p.vec_out && (c + 1) * PER <= n) {
-            uint32_t u[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if constexpr (sizeof(OutT) == 4)
-                    u[i] = __float_as_uint(v[8 * c + i]);
-                else
-                    u[i] = pack2(v[16 * c + 2 * i], v[16 * c + 2 * i + 1], static_cast<OutT*>(nullptr));
-            }
-            st_global_v8(dst + c * PER, u);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (c * PER + i < n)
-                    dst[c * PER + i] = fp8_to_out<OutT>(v[c * PER + i]);
-        }
-    }
 }
 
 // A warp's 32 x COLS part of a finished tile through its staging buffer, in
@@ -225,6 +181,44 @@ __device__ __forceinline__ void fp8_store_tile(const uint64_t (&acc)[COLS / 2], 
         if (lane == 0) {
             tma_store_2d(map, stg, col0 + s * STRIP, row0);
             bulk_commit_group();
+        }
+    }
+}
+
+// The same for an output without a tensor map (rows that are not 16-byte
+// aligned, or beta != 0): strips of 32 FP32 columns, stored and, for beta,
+// read a row at a time, a column a lane.  A thread writing its own row
+// element by element took ten times as long.
+template <typename OutT, int COLS>
+__device__ __forceinline__ void fp8_store_rows(const uint64_t (&acc)[COLS / 2], uint32_t stg, int row0,
+                                               int col0, uint32_t lane, const Fp8Params& p)
+{
+    const uint32_t base = stg + lane * 128, sw = lane & 7;
+    const int rows = min(p.M - row0, 32);
+#pragma unroll
+    for (int s = 0; s < COLS / 32; ++s) {
+        if (rows <= 0 || col0 + s * 32 >= p.N)
+            break;
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
+            unpack_f32x2(acc[s * 16 + 2 * c], w[0], w[1]);
+            unpack_f32x2(acc[s * 16 + 2 * c + 1], w[2], w[3]);
+            st_shared_v4(base + ((c ^ sw) << 4), w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        const int col = col0 + s * 32 + static_cast<int>(lane);
+        if (col < p.N) {
+            OutT* c = static_cast<OutT*>(p.C) + static_cast<long long>(row0) * p.ldc + col;
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r, c += p.ldc) {
+                float v = p.alpha * ld_shared_f32(stg + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) |
+                                                                  ((lane & 3) << 2)));
+                if (p.beta != 0.0f)
+                    v = fmaf(p.beta, out_to_f32(*c), v);
+                *c = fp8_to_out<OutT>(v);
+            }
         }
     }
 }
@@ -645,36 +639,22 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             }
             const bool stored = !*abort_flag;  // an unfinished tile is not written
             // ---- the finished tile: alpha, beta, rounding to the output type
+            const int row0 = row - static_cast<int>(lane);
+            const uint32_t stg = sbase + L::OFF_STAGING + ew * TC_STAGING_BYTES;
             if (stored && p.tma_out) {
-                const int row0 = row - static_cast<int>(lane);
-                const uint32_t stg = sbase + L::OFF_STAGING + ew * TC_STAGING_BYTES;
                 if (p.out_dtype == DT_F32)
                     fp8_store_tile<float, COLS>(acc, stg, &tmC, row0, col0, lane, p);
                 else if (p.out_dtype == DT_F16)
                     fp8_store_tile<__half, COLS>(acc, stg, &tmC, row0, col0, lane, p);
                 else
                     fp8_store_tile<__nv_bfloat16, COLS>(acc, stg, &tmC, row0, col0, lane, p);
-            } else if (stored && row < p.M) {
-#pragma unroll
-                for (int c = 0; c < COLS / 32; ++c) {
-                    float o[32];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        uint32_t lo, hi;
-                        unpack_f32x2(acc[c * 16 + i], lo, hi);
-                        o[2 * i] = __uint_as_float(lo);
-                        o[2 * i + 1] = __uint_as_float(hi);
-                    }
-                    const int col = col0 + c * 32;
-                    const int n = min(p.N - col, 32);
-                    const long long at = static_cast<long long>(row) * p.ldc + col;
-                    if (p.out_dtype == DT_F32)
-                        fp8_store_row(static_cast<float*>(p.C) + at, o, n, p);
-                    else if (p.out_dtype == DT_F16)
-                        fp8_store_row(static_cast<__half*>(p.C) + at, o, n, p);
-                    else
-                        fp8_store_row(static_cast<__nv_bfloat16*>(p.C) + at, o, n, p);
-                }
+            } else if (stored) {
+                if (p.out_dtype == DT_F32)
+                    fp8_store_rows<float, COLS>(acc, stg, row0, col0, lane, p);
+                else if (p.out_dtype == DT_F16)
+                    fp8_store_rows<__half, COLS>(acc, stg, row0, col0, lane, p);
+                else
+                    fp8_store_rows<__nv_bfloat16, COLS>(acc, stg, row0, col0, lane, p);
             }
         }
     }
