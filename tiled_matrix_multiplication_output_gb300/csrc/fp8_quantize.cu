@@ -27,6 +27,7 @@
 
 #include "fp8.h"
 #include "launch.h"
+#include "load8.cuh"
 
 namespace tmmo {
 namespace {
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(Q_THREADS, sizeof(InT) == 4 ? 2 : FORMS == (Q_
     const InT* src = static_cast<const InT*>(p.X) + static_cast<int64_t>(row0) * p.ldx + col0;
 #pragma unroll
     for (int i = 0; i < Q_ROWS; ++i) {
-        if (VEC && i < nrow && ncol == Q_COLS) {
+        if (VEC && i < nrow && ncol == Q_COLS) {  // whole, on a 16-byte boundary
 #pragma unroll
             for (int j = 0; j < W / 4; ++j) {
                 const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src + i * p.ldx) + j);
@@ -346,22 +347,7 @@ __global__ void __launch_bounds__(Q_THREADS, sizeof(InT) == 4 ? 2 : FORMS == (Q_
                 w[i][4 * j + 3] = u.w;
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                w[i][j] = 0;
-            if (i < nrow) {
-#pragma unroll
-                for (int j = 0; j < Q_COLS; ++j) {
-                    if (j < ncol) {
-                        if constexpr (W == 8)
-                            w[i][j] = reinterpret_cast<const uint32_t*>(src + i * p.ldx)[j];
-                        else
-                            w[i][j >> 1] |= static_cast<uint32_t>(
-                                                reinterpret_cast<const uint16_t*>(src + i * p.ldx)[j])
-                                            << (16 * (j & 1));
-                    }
-                }
-            }
+            load8(src + i * p.ldx, i < nrow ? ncol : 0, w[i]);
         }
     }
 

@@ -552,30 +552,10 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
 
 // ------------------------------------------------------------ normalisation
 
-// Eight consecutive values, `n` of them inside the row.
-template <typename InT>
-__device__ __forceinline__ void ns_load8(const InT* src, int n, bool vec, float (&v)[8])
-{
-    if (vec && n >= 8) {
-        alignas(16) InT e[8];
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(InT)) / 2; ++i)
-            reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(src)[i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = ns_value(&e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = i < n ? ns_value(src + i) : 0.0f;
-    }
-}
-
 struct NsNorm {
     const void* G;
     long long ldg, batch_g;
     int rows, cols, groups;        // groups of 8 columns per row
-    bool vec;
     float* partial;                // [batch][blocks]
     int blocks;
     float eps;
@@ -595,7 +575,7 @@ __device__ __forceinline__ float ns_square_sum(const NsNorm& p, long long z, lon
     for (long long i = first; i < total; i += step) {
         const int row = static_cast<int>(i / p.groups), c = static_cast<int>(i % p.groups) * 8;
         float v[8];
-        ns_load8(g + row * p.ldg + c, p.cols - c, p.vec, v);
+        ns_load8(g + row * p.ldg + c, min(p.cols - c, 8), v);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             s = fmaf(v[k], v[k], s);
@@ -617,7 +597,7 @@ __device__ __forceinline__ void ns_scale(const NsNorm& p, long long z, long long
     for (long long i = first; i < total; i += step) {
         const int row = static_cast<int>(i / p.groups), c = static_cast<int>(i % p.groups) * 8;
         float v[8];
-        ns_load8(g + row * p.ldg + c, p.cols - c, p.vec, v);
+        ns_load8(g + row * p.ldg + c, min(p.cols - c, 8), v);
         uint32_t h[4], l[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -865,7 +845,6 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
         p.fault_skip_kblock = l.fault_skip_kblock;
     }
 
-    const int es = l.in_dtype == DT_F32 ? 4 : 2;
     NsNorm n{};
     n.G = l.G;
     n.ldg = l.ldg;
@@ -873,8 +852,6 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
     n.rows = l.rows;
     n.cols = l.cols;
     n.groups = (l.cols + 7) / 8;
-    n.vec = (reinterpret_cast<uintptr_t>(l.G) & 15u) == 0 && (l.ldg * es) % 16 == 0 &&
-            (l.batch == 1 || (l.batch_g * es) % 16 == 0);
     n.partial = reinterpret_cast<float*>(ws + s.off_partial);
     // about four groups of 8 values a thread, up to NS_NORM_BLOCKS blocks
     const int64_t groups = static_cast<int64_t>(l.rows) * n.groups;

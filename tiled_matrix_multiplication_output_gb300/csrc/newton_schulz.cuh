@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "launch.h"
+#include "load8.cuh"
 #include "ops.cuh"
 
 namespace tmmo {
@@ -62,6 +63,18 @@ __device__ __forceinline__ void ns_store_result(OutT* dst, int n, const float (&
             }
         }
     }
+}
+
+// Eight consecutive values of a row, `n` of them inside it (zeros beyond).
+template <typename InT>
+__device__ __forceinline__ void ns_load8(const InT* src, int n, float (&v)[8])
+{
+    uint32_t w[2 * sizeof(InT)];
+    load8(src, n, w);
+    const InT* e = reinterpret_cast<const InT*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = ns_value(e + i);
 }
 
 __device__ __forceinline__ float ns_block_sum(float s)

@@ -99,15 +99,14 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&w)[4])
 template <typename InT>
 __device__ __forceinline__ void nr_load(const InT* g, long long step, int cnt, float (&v)[32])
 {
-    constexpr int PER = 16 / static_cast<int>(sizeof(InT));
-    if (step == 1 && cnt == 32 && (reinterpret_cast<uintptr_t>(g) & 15u) == 0) {
+    if (step == 1) {
 #pragma unroll
-        for (int i = 0; i < 32 / PER; ++i) {
-            const uint4 u = reinterpret_cast<const uint4*>(g)[i];
-            const InT* e = reinterpret_cast<const InT*>(&u);
+        for (int i = 0; i < 32; i += 8) {
+            float e[8];
+            ns_load8(g + i, min(cnt - i, 8), e);
 #pragma unroll
-            for (int k = 0; k < PER; ++k)
-                v[i * PER + k] = ns_value(e + k);
+            for (int k = 0; k < 8; ++k)
+                v[i + k] = e[k];
         }
     } else {
 #pragma unroll
