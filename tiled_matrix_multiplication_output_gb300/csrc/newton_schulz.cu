@@ -76,6 +76,7 @@ struct NsParams {
     long long ld_out, batch_out;
     void* result;                  // NS_LAST
     long long ld_res, batch_res;
+    bool vec_res;                  // its rows are on 16-byte boundaries
     int out_dtype;
     int* status;
     long long wait_budget;
@@ -111,10 +112,14 @@ __host__ __device__ inline NsOperands ns_operands(const NsPlan& f, int mode, int
     }
 }
 
-template <int CG, int BN, int STAGES>
+// The last product of a call stages its output, which need not be aligned; the
+// others leave that shared memory to the L1 cache, through which the addends
+// come (with it, 8 x 545 x 552 took 178 us instead of 162).
+template <int CG, int BN, int STAGES, bool STAGED>
 struct NsLayout {
     static constexpr int STAGE = 2 * NS_BOX;
-    static constexpr int OFF_BAR = STAGES * STAGE;
+    static constexpr int OFF_STAGING = STAGES * STAGE;  // 4 KiB of output per epilogue warp
+    static constexpr int OFF_BAR = OFF_STAGING + (STAGED ? NS_EPI_WARPS * TC_STAGING_BYTES : 0);
     static constexpr int NUM_BARS = 2 * STAGES + 5;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
     static constexpr int BYTES = OFF_MISC + 16;
@@ -213,7 +218,7 @@ __device__ __forceinline__ uint64_t ns_desc_hi(bool mn)
 // complete (false: given up).
 template <int MODE, int COLS, typename Wait>
 __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands& o, int z, bool mirror,
-                                            int row, int col0, uint32_t taddr, Wait&& wait)
+                                            int row, int col0, uint32_t taddr, uint32_t stg, Wait&& wait)
 {
     const bool inside = row < p.M;
     const long long at_add = z * p.batch_add + row * p.ld_add + col0;
@@ -261,18 +266,19 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands&
         if (c + 2 < COLS / 32)
             fetch(c + 2, b);
         if constexpr (MODE == NS_LAST) {
-            if (inside) {
-                const long long at = z * p.batch_res + row * p.ld_res + col;
+            const uint32_t lane = threadIdx.x & 31;
+            const int row0 = row - static_cast<int>(lane), rows = min(p.M - row0, 32);
+            const long long at = z * p.batch_res + row0 * p.ld_res + col;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    f[i] *= 1.0f / NS_SX;
-                if (p.out_dtype == DT_F32)
-                    ns_store_result(static_cast<float*>(p.result) + at, n, f);
-                else if (p.out_dtype == DT_F16)
-                    ns_store_result(static_cast<__half*>(p.result) + at, n, f);
-                else
-                    ns_store_result(static_cast<__nv_bfloat16*>(p.result) + at, n, f);
-            }
+            for (int i = 0; i < 32; ++i)
+                f[i] *= 1.0f / NS_SX;
+            if (p.out_dtype == DT_F32)
+                ns_store_result(static_cast<float*>(p.result) + at, p.ld_res, rows, n, p.vec_res, stg, lane, f);
+            else if (p.out_dtype == DT_F16)
+                ns_store_result(static_cast<__half*>(p.result) + at, p.ld_res, rows, n, p.vec_res, stg, lane, f);
+            else
+                ns_store_result(static_cast<__nv_bfloat16*>(p.result) + at, p.ld_res, rows, n, p.vec_res, stg,
+                                lane, f);
         } else {
             uint32_t w[16];
 #pragma unroll
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
                       const __grid_constant__ CUtensorMap tmB, const NsParams p,
                       const NsOperands o)
 {
-    using L = NsLayout<CG, BN, STAGES>;
+    using L = NsLayout<CG, BN, STAGES, MODE == NS_LAST>;
     constexpr bool SYMMETRIC = MODE == NS_GRAM || MODE == NS_POLY;
     constexpr int TILE_M = TC_BM * CG;
     constexpr int COLS = BN / 2;  // columns of the tile per epilogue warp
@@ -519,6 +525,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
             ns_epilogue<MODE, COLS>(p, o, z, mb != nb, row, col0,
                                     tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                         static_cast<uint32_t>(acc * BN + half * COLS),
+                                    sbase + L::OFF_STAGING + (warp - NS_EPI_WARP0) * TC_STAGING_BYTES,
                                     [&]() {
                                         ok = tc_wait_warp(tfull_bar(acc), (local >> 1) & 1, watch);
                                         return ok;
@@ -696,7 +703,7 @@ template <int CG, int BN, int STAGES, int MODE>
 cudaError_t ns_run(const CUtensorMap& ta, const CUtensorMap& tb, NsParams p, const NsOperands& o,
                    int num_sms, cudaStream_t stream)
 {
-    using L = NsLayout<CG, BN, STAGES>;
+    using L = NsLayout<CG, BN, STAGES, MODE == NS_LAST>;
     auto kern = ns_product_kernel<CG, BN, STAGES, MODE>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -777,9 +784,10 @@ cudaError_t ns_product(const CUtensorMap& ta, const CUtensorMap& tb, const NsPar
     const long long tm = (p.M + 255) / 256, tn = (p.N + 255) / 256;
     const bool symmetric = MODE == NS_GRAM || MODE == NS_POLY;
     const long long pairs = p.batch * (symmetric ? tn * (tn + 1) / 2 : tm * tn);
+    constexpr int STAGES = MODE == NS_LAST ? 5 : 6;
     if (pairs * 4 >= num_sms)
-        return ns_run<2, 256, 6, MODE>(ta, tb, p, o, num_sms, stream);
-    return ns_run<1, 128, 6, MODE>(ta, tb, p, o, num_sms, stream);
+        return ns_run<2, 256, STAGES, MODE>(ta, tb, p, o, num_sms, stream);
+    return ns_run<1, 128, STAGES, MODE>(ta, tb, p, o, num_sms, stream);
 }
 
 template <typename InT>
@@ -839,6 +847,7 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
         p.result = l.O;
         p.ld_res = l.ldo;
         p.batch_res = l.batch_o;
+        p.vec_res = ns_vec_rows(l);
         p.out_dtype = l.out_dtype;
         p.status = l.status;
         p.wait_budget = l.wait_budget;

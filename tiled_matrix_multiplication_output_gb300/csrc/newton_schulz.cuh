@@ -30,13 +30,32 @@ __device__ __forceinline__ uint32_t ns_pack(float lo, float hi)
 }
 
 template <typename OutT>
-__device__ __forceinline__ void ns_store_result(OutT* dst, int n, const float (&v)[32])
+__device__ __forceinline__ OutT ns_to_out(float v)
 {
-    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
-    constexpr int PER = 16 / static_cast<int>(sizeof(OutT));
+    if constexpr (sizeof(OutT) == 4) {
+        return v;
+    } else {
+        const uint32_t u = pack2(v, 0.0f, static_cast<OutT*>(nullptr));
+        return *reinterpret_cast<const OutT*>(&u);
+    }
+}
+
+// A warp's 32 rows x 32 columns of the result, a row a lane, at `o` with row
+// pitch ld; `rows` and `n` columns of them lie inside.  vec: rows are on
+// 16-byte boundaries and a thread stores its own; otherwise the values go
+// through 4 KiB of shared memory and are stored a row at a time, a column a
+// lane.  Called by the whole warp.
+template <typename OutT>
+__device__ __forceinline__ void ns_store_result(OutT* o, long long ld, int rows, int n, bool vec,
+                                                uint32_t stg, uint32_t lane, const float (&v)[32])
+{
+    if (vec && n == 32) {
+        if (static_cast<int>(lane) >= rows)
+            return;
+        OutT* dst = o + static_cast<long long>(lane) * ld;
+        constexpr int PER = 16 / static_cast<int>(sizeof(OutT));
 #pragma unroll
-    for (int c = 0; c < 32 / PER; ++c) {
-        if (vec && (c + 1) * PER <= n) {
+        for (int c = 0; c < 32 / PER; ++c) {
             uint4 u;
             if constexpr (sizeof(OutT) == 4) {
                 u = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
@@ -48,20 +67,22 @@ __device__ __forceinline__ void ns_store_result(OutT* dst, int n, const float (&
                                pack2(v[8 * c + 6], v[8 * c + 7], tag));
             }
             *reinterpret_cast<uint4*>(dst + c * PER) = u;
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (c * PER + i < n) {
-                    if constexpr (sizeof(OutT) == 4) {
-                        dst[c * PER + i] = v[c * PER + i];
-                    } else {
-                        OutT* tag = nullptr;
-                        const uint32_t u = pack2(v[c * PER + i], 0.0f, tag);
-                        dst[c * PER + i] = *reinterpret_cast<const OutT*>(&u);
-                    }
-                }
-            }
         }
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        st_shared_v4(stg + lane * 128 + ((c ^ (lane & 7)) << 4), __float_as_uint(v[4 * c]),
+                     __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                     __float_as_uint(v[4 * c + 3]));
+    __syncwarp();
+    if (static_cast<int>(lane) < n) {
+        o += lane;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, o += ld)
+            *o = ns_to_out<OutT>(ld_shared_f32(
+                stg + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2))));
     }
 }
 

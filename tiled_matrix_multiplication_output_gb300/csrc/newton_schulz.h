@@ -6,6 +6,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "launch.h"
+
 namespace tmmo {
 
 constexpr int NS_MAX_STEPS = 32;
@@ -26,6 +28,14 @@ struct NsLaunch {
     long long wait_budget;
     int fault_skip_kblock;
 };
+
+// Whether the rows of the result are on 16-byte boundaries.
+inline bool ns_vec_rows(const NsLaunch& l)
+{
+    const int64_t es = l.out_dtype == DT_F32 ? 4 : 2;
+    return (reinterpret_cast<uintptr_t>(l.O) & 15u) == 0 && l.ldo * es % 16 == 0 &&
+           (l.batch == 1 || l.batch_o * es % 16 == 0);
+}
 
 size_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
 

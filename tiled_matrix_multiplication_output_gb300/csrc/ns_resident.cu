@@ -49,6 +49,7 @@ struct NsResident {
     long long batch_g, row_g, col_g, batch_o, row_o, col_o;
     int m, n;
     int share;                     // columns of X per block
+    bool vec_o;                    // O's rows are on 16-byte boundaries
     int in_dtype, out_dtype;
     int steps;
     float eps;
@@ -115,23 +116,20 @@ __device__ __forceinline__ void nr_load(const InT* g, long long step, int cnt, f
     }
 }
 
+// A warp's 32 rows x 32 columns of the result; tall: the matrix lies
+// transposed in O, so a column of X is contiguous over the lanes.
 template <typename OutT>
-__device__ __forceinline__ void nr_store(OutT* o, long long step, int cnt, const float (&v)[32])
+__device__ __forceinline__ void nr_store(OutT* o, const NsResident& p, int row0, int cnt, uint32_t stg,
+                                         uint32_t lane, const float (&v)[32])
 {
-    if (step == 1) {
-        ns_store_result(o, cnt, v);
-        return;
-    }
+    const int rows = min(p.m - row0, 32);
+    if (p.col_o == 1) {
+        ns_store_result(o, p.row_o, rows, cnt, p.vec_o, stg, lane, v);
+    } else if (static_cast<int>(lane) < rows) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        if (i < cnt) {
-            if constexpr (sizeof(OutT) == 4) {
-                o[i * step] = v[i];
-            } else {
-                const uint32_t u = pack2(v[i], 0.0f, static_cast<OutT*>(nullptr));
-                o[i * step] = *reinterpret_cast<const OutT*>(&u);
-            }
-        }
+        for (int i = 0; i < 32; ++i)
+            if (i < cnt)
+                o[lane * p.row_o + i * p.col_o] = ns_to_out<OutT>(v[i]);
     }
 }
 
@@ -405,19 +403,22 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
 #pragma unroll
         for (int c = 0; c < XCH; ++c) {
             const int col = (2 * c + g) * 32;
-            const int cnt = row < p.m ? min(ncol - col, 32) : 0;
+            const int cnt = min(ncol - col, 32), row0 = q * 32;
             if (cnt <= 0)
                 continue;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 x[c][i] *= 1.0f / NS_SX;
-            const long long at = z * p.batch_o + row * p.row_o + (col0 + col) * p.col_o;
+            // (no MMA reads the operands any more: A's buffer, 4 KiB a warp,
+            // serves as staging)
+            const uint32_t stg = sA + warp * TC_STAGING_BYTES;
+            const long long at = z * p.batch_o + row0 * p.row_o + (col0 + col) * p.col_o;
             if (p.out_dtype == DT_F32)
-                nr_store(static_cast<float*>(p.O) + at, p.col_o, cnt, x[c]);
+                nr_store(static_cast<float*>(p.O) + at, p, row0, cnt, stg, lane, x[c]);
             else if (p.out_dtype == DT_F16)
-                nr_store(static_cast<__half*>(p.O) + at, p.col_o, cnt, x[c]);
+                nr_store(static_cast<__half*>(p.O) + at, p, row0, cnt, stg, lane, x[c]);
             else
-                nr_store(static_cast<__nv_bfloat16*>(p.O) + at, p.col_o, cnt, x[c]);
+                nr_store(static_cast<__nv_bfloat16*>(p.O) + at, p, row0, cnt, stg, lane, x[c]);
         }
     }
 
@@ -554,6 +555,7 @@ cudaError_t ns_resident_launch(const NsLaunch& l, cudaStream_t stream)
     p.m = std::min(l.rows, l.cols);
     p.n = std::max(l.rows, l.cols);
     p.share = ((p.n + size - 1) / size + 15) / 16 * 16;
+    p.vec_o = ns_vec_rows(l);
     p.in_dtype = l.in_dtype;
     p.out_dtype = l.out_dtype;
     p.steps = l.steps;
