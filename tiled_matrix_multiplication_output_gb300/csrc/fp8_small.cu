@@ -46,6 +46,7 @@ struct Fp8SmallParams {
     int sp_shift, sq_shift;
     void* C;
     long long c_row, c_col;        // elements from one row / column of the tile to the next in C
+    bool by_row;                   // rows of the tile are rows of C
     int out_dtype;
     float alpha, beta;
     int* status;
@@ -70,7 +71,7 @@ struct Fp8SmallLayout {
     static constexpr int SMEM_ALLOC = BYTES + 1024;
     static constexpr uint32_t TMEM_COLS = NBUF * BN;
     static_assert(STAGE % 1024 == 0, "boxes start on whole swizzle atoms");
-    static_assert(BN * 512 <= STAGES * STAGE, "the partial sums fit into the ring");
+    static_assert(128 * (BN + 1) * 4 <= STAGES * STAGE, "the partial sums fit into the ring");
     static_assert(SMEM_ALLOC <= 113 * 1024, "two blocks fit on an SM");
 };
 
@@ -92,6 +93,73 @@ __device__ __forceinline__ void fs_store_any(const Fp8SmallParams& p, int row, i
         fs_store<__half>(p, row, col, v);
     else
         fs_store<__nv_bfloat16>(p, row, col, v);
+}
+
+// The end of a tile: the blocks' sums through shared memory (at `base`, whose
+// ring holds nothing any more), added up over the cluster in rank order and
+// stored, with rows (BY_ROW) or columns of the tile contiguous as they are in
+// C.  `full`: this thread holds a row of sums.  Each block adds up a share,
+// 128 / SPLITS rows or BN / SPLITS columns, with all its threads.
+template <int BN, int SPLITS, bool BY_ROW>
+__device__ __forceinline__ void fs_finish(const Fp8SmallParams& p, const uint64_t (&acc)[BN / 2], bool full,
+                                          uint32_t base, int split, int row0, int col0,
+                                          volatile int* abort_flag)
+{
+    // rows with a word between them, against bank conflicts
+    constexpr int STEP_R = BY_ROW ? BN + 1 : 1, STEP_C = BY_ROW ? 1 : 128;
+    const int t = static_cast<int>(threadIdx.x);
+    if (full) {
+        const uint32_t at = base + (t & 127) * STEP_R * 4;
+#pragma unroll
+        for (int j = 0; j < BN; ++j) {
+            uint32_t w[2];
+            unpack_f32x2(acc[j / 2], w[0], w[1]);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + j * STEP_C * 4), "r"(w[j & 1]) : "memory");
+        }
+    }
+    __syncwarp();
+    if constexpr (SPLITS > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    constexpr int MINE = 128 * BN / SPLITS / FS_THREADS;
+    constexpr int BATCH = MINE * SPLITS > 64 ? 64 / SPLITS : MINE;  // loads in flight
+    // this thread's first element; the next ones are FS_THREADS / BN rows, or
+    // two columns, further
+    const int r0 = BY_ROW ? split * (128 / SPLITS) + t / BN : t & 127;
+    const int c0 = BY_ROW ? t % BN : split * (BN / SPLITS) + (t >> 7);
+    constexpr int DR = BY_ROW ? FS_THREADS / BN : 0, DC = BY_ROW ? 0 : 2;
+    const uint32_t at = base + (r0 * STEP_R + c0 * STEP_C) * 4;
+    uint32_t peer[SPLITS];
+#pragma unroll
+    for (int k = 0; k < SPLITS; ++k)
+        peer[k] = SPLITS > 1 ? mapa_shared(at, k) : at;
+    const bool store = !*abort_flag;
+#pragma unroll
+    for (int j0 = 0; j0 < MINE; j0 += BATCH) {
+        float v[BATCH][SPLITS];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+            for (int k = 0; k < SPLITS; ++k) {
+                const uint32_t from = peer[k] + (j0 + j) * (DR * STEP_R + DC * STEP_C) * 4;
+                v[j][k] = SPLITS > 1 ? ld_cluster_f32(from) : ld_shared_f32(from);
+            }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            float sum = v[j][0];
+#pragma unroll
+            for (int k = 1; k < SPLITS; ++k)
+                sum += v[j][k];
+            const int row = row0 + r0 + (j0 + j) * DR, col = col0 + c0 + (j0 + j) * DC;
+            if (store && row < p.rows && col < p.cols)
+                fs_store_any(p, row, col, sum);
+        }
+    }
+    if constexpr (SPLITS > 1) {
+        __syncwarp();
+        cluster_sync();
+    }
 }
 
 template <int BN, int SPLITS>
@@ -330,8 +398,9 @@ __global__ void __launch_bounds__(FS_THREADS, 2)
     }
 
     // ------------------------------------------------ sums of the cluster, output
-    if constexpr (SPLITS == 1) {
-        const int r = static_cast<int>(threadIdx.x) - FS_EPI_WARP0 * 32;  // tile row
+    if (SPLITS == 1 && !p.by_row) {
+        // a thread's values lie next to its neighbours' in C
+        const int r = static_cast<int>(threadIdx.x) & 127;
         if (warp >= FS_EPI_WARP0 && ok && row0 + r < p.rows) {
 #pragma unroll
             for (int j = 0; j < BN; ++j) {
@@ -341,50 +410,10 @@ __global__ void __launch_bounds__(FS_THREADS, 2)
                     fs_store_any(p, row0 + r, col0 + j, __uint_as_float(w[j & 1]));
             }
         }
+    } else if (p.by_row) {
+        fs_finish<BN, SPLITS, true>(p, acc, warp >= FS_EPI_WARP0 && ok, sbase, split, row0, col0, abort_flag);
     } else {
-        // Every K block of this block has been consumed, so the ring holds
-        // nothing; the sums go there as [column][row].
-        if (warp >= FS_EPI_WARP0 && ok) {
-            const int r = static_cast<int>(threadIdx.x) - FS_EPI_WARP0 * 32;
-#pragma unroll
-            for (int j = 0; j < BN; ++j) {
-                uint32_t w[2];
-                unpack_f32x2(acc[j / 2], w[0], w[1]);
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + (j * 128 + r) * 4), "r"(w[j & 1])
-                             : "memory");
-            }
-        }
-        __syncwarp();
-        cluster_sync();
-        // This block adds up BN / SPLITS columns, all its threads taking
-        // part: thread t has tile row t % 128 and every other column.
-        constexpr int PART = BN / SPLITS;
-        constexpr int MINE = PART / 2;
-        const int r = static_cast<int>(threadIdx.x) & 127;
-        const int c0 = split * PART + static_cast<int>(threadIdx.x >> 7);
-        float v[MINE][SPLITS];
-        uint32_t peer[SPLITS];
-#pragma unroll
-        for (int k = 0; k < SPLITS; ++k)
-            peer[k] = mapa_shared(sbase + (c0 * 128 + r) * 4, k);
-#pragma unroll
-        for (int j = 0; j < MINE; ++j)
-#pragma unroll
-            for (int k = 0; k < SPLITS; ++k)
-                v[j][k] = ld_cluster_f32(peer[k] + j * 2 * 128 * 4);
-        const bool store = !*abort_flag && row0 + r < p.rows;
-#pragma unroll
-        for (int j = 0; j < MINE; ++j) {
-            float sum = v[j][0];
-#pragma unroll
-            for (int k = 1; k < SPLITS; ++k)
-                sum += v[j][k];
-            const int col = col0 + c0 + 2 * j;
-            if (store && col < p.cols)
-                fs_store_any(p, row0 + r, col, sum);
-        }
-        __syncwarp();
-        cluster_sync();
+        fs_finish<BN, SPLITS, false>(p, acc, warp >= FS_EPI_WARP0 && ok, sbase, split, row0, col0, abort_flag);
     }
 
     // ---------------------------------------------------- teardown
@@ -445,6 +474,7 @@ cudaError_t launch_small(const Fp8Launch& l, bool swapped, cudaStream_t stream)
     p.C = l.C;
     p.c_row = swapped ? 1 : l.ldc;
     p.c_col = swapped ? l.ldc : 1;
+    p.by_row = !swapped;
     p.out_dtype = l.out_dtype;
     p.alpha = l.alpha;
     p.beta = l.beta;
