@@ -83,6 +83,10 @@ def parse_args():
     ap.add_argument("--simt", action="store_true",
                     help="instead of the benchmark line: time the SIMT kernel on FP32 and "
                          "unaligned 16-bit products in every operand layout, one JSON line each")
+    ap.add_argument("--operators", action="store_true",
+                    help="instead of the benchmark line: time the 8-bit products, their "
+                         "quantisation and the orthogonalisation on the cases of "
+                         "perf/operators.py, one JSON line each")
     ap.add_argument("--kernel-only", action="store_true",
                     help="time only the GEMM launches (no e2e, cuBLAS context or CPU "
                          "baseline); used for profiler captures")
@@ -971,8 +975,69 @@ def run_rows():
             emit(k, m, m, m, statistics.median(rounds[k]))
 
 
+def operator_floor_us(op, work, peaks):
+    """The least time of a case at the measured rates: its compulsory bytes at
+    the copy bandwidth or its operations at the burst rate of 16-bit products
+    (twice that for 8-bit ones), whichever is longer."""
+    rate = {"quant": math.inf, "product": 2.0, "orth": 1.0}[op] * peaks["bf16_tflops"] * 1e12
+    return 1e6 * max(work["bytes"] / (peaks["hbm_gbs"] * 1e9), work["flops"] / rate)
+
+
+def run_operators(passes=60):
+    """Times the listed cases of perf/operators.py through the package: on the
+    device alone (a CUDA graph of the calls, over three sets of inputs in
+    turn) and as Python calls one after another."""
+    import importlib.util
+    import torch
+    import tiled_matrix_multiplication_output_gb300 as tg
+    tg.load_library(build_if_missing=True)
+    torch.cuda.set_device(0)
+    spec = importlib.util.spec_from_file_location("operators",
+                                                  os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    peaks, _ = load_peaks()
+    for case in ops.listed():
+        states = [ops.prepare(case, seed) for seed in range(3)]
+        for state in states * 2:
+            ops.run(state)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(passes):
+                ops.run(states[i % 3])
+
+        def timed(f):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            f()
+            b.record()
+            torch.cuda.synchronize()
+            return a.elapsed_time(b) * 1e3 / passes
+
+        timed(graph.replay)
+        device = statistics.median(timed(graph.replay) for _ in range(5))
+        calls = statistics.median(
+            timed(lambda: [ops.run(states[i % 3]) for i in range(passes)]) for _ in range(5))
+        work = ops.work(case)
+        floor = operator_floor_us(case["op"], work, peaks)
+        print(json.dumps({
+            "case": case["name"], "device_us": round(device, 2), "call_us": round(calls, 2),
+            "floor_us": round(floor, 2), "times_floor": round(device / floor, 2),
+            "gb_per_s": round(work["bytes"] / device / 1e3, 1),
+            "tflop_per_s": round(work["flops"] / device / 1e6, 2)}), flush=True)
+        del graph, states
+    rc = tg.gemm_device_status(torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise RuntimeError(tg.error_string(rc))
+
+
 def main():
     args = parse_args()
+    if args.operators:
+        run_operators()
+        return
     if args.sweep:
         run_sweep()
         return

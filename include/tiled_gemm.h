@@ -447,8 +447,9 @@ int gemm_fp8(const gemm_fp8_matrix_t* A, const gemm_fp8_matrix_t* B, void* C, in
  * Accuracy.  Products take FP16 operands and accumulate in FP32, X is kept
  * to 22 bits: the result is about 2e-3 (relative, in the 2-norm of all
  * elements) from the definition in exact arithmetic, before the rounding to
- * out_dtype.  Singular values must stay below 16 throughout, as they do for
- * coefficients that converge.  A G whose norm is not finite in FP32 gives
+ * out_dtype.  Singular values must stay below 4 and |b s^2 + c s^4| below 32
+ * throughout, the range of the FP16 operands, as they do for coefficients
+ * that converge; beyond it the result is not finite.  A G whose norm is not finite in FP32 gives
  * NaN throughout its O.  A zero G gives zeros (NaN for eps == 0).
  *
  * workspace: device memory of gemm_newton_schulz_workspace_size(batch, rows,

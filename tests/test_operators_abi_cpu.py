@@ -97,3 +97,13 @@ def test_cpu_tensors_are_rejected():
                  lambda: tg.newton_schulz(x), lambda: tg.matmul_fp8(x, x, x, x)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_bench_floor_of_an_operator():
+    import bench
+    peaks = {"hbm_gbs": 6800.0, "bf16_tflops": 1876.6}
+    work = {"bytes": 6.8e9, "flops": 1.8766e12}
+    assert bench.operator_floor_us("quant", work, peaks) == pytest.approx(1000.0)
+    assert bench.operator_floor_us("orth", work, peaks) == pytest.approx(1000.0)
+    assert bench.operator_floor_us("orth", {"bytes": 1, "flops": 1.8766e12}, peaks) == pytest.approx(1000.0)
+    assert bench.operator_floor_us("product", {"bytes": 1, "flops": 1.8766e12}, peaks) == pytest.approx(500.0)

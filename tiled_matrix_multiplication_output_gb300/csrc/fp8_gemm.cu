@@ -176,7 +176,10 @@ cudaError_t fp8_gemm_launch(const Fp8Launch& l, cudaStream_t stream)
     if (fp8_small_takes(l))
         return fp8_small_launch(l, stream);
     // Pair tiles of 256 x 256 once they fill half of the CTA pairs; below
-    // that, four times as many 128 x 128 tiles keep more SMs busy.
+    // that, four times as many 128 x 128 tiles keep more SMs busy.  Measured
+    // on GB300, us, with the limit at half the pairs / a quarter of them:
+    // 2048 x 1024 x 1024 (32 pair tiles) 6.8 / 8.7, 1500 x 1500 x 1000 (36)
+    // 9.5 / 12.5, 300 x 4319 x 564 (34) 7.7 / 11.1.
     const long long pair_tiles =
         static_cast<long long>((l.M + 255) / 256) * ((l.N + 255) / 256);
     if (pair_tiles * 4 >= l.num_sms)

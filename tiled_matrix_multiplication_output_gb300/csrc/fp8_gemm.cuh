@@ -9,23 +9,43 @@
 // The scales are arbitrary FP32 numbers, so a K block's product has to be
 // scaled before it joins the sum: P_kb is accumulated by the tensor core
 // (FP32, in tensor memory), read back, and added to the running sum in
-// registers, FP32, as acc += (sA * sB) * P_kb.  What bounds the kernel is
-// the tensor pipe as long as that "promotion" keeps up: for a 128 x 256 half
-// of a CTA pair's tile a K block is 512 cycles of MMA, against 128 x 256
-// values that have to cross from tensor memory and one multiply-add each --
-// 256 cycles of the FP32 pipe.  So:
+// registers, FP32, as acc += (sA * sB) * P_kb.  For a CTA pair's 256 x 256
+// tile a K block is 512 cycles of MMA, against 128 x 256 values a CTA that
+// have to cross from tensor memory and one multiply-add each, 256 cycles of
+// the FP32 pipe.  So:
 //
-//   * eight epilogue warps (two per SM partition, so that one's loads from
-//     tensor memory overlap the other's arithmetic) hold the running sums:
-//     128 registers a thread for 256-column tiles.  setmaxnreg moves
-//     registers from the copying and issuing warps to them;
+//   * eight epilogue warps, two per SM partition, hold the running sums: 128
+//     registers a thread for 256-column tiles.  setmaxnreg moves registers
+//     from the copying and issuing warps to them.  (Sixteen warps with half
+//     the columns took 1.16 times the time.);
 //   * several partial buffers in tensor memory (512 columns in all), so the
-//     tensor core works on the next K blocks while one is promoted;
+//     tensor core works on the next K blocks while one is promoted; a pair's
+//     K block is issued as two groups of 128 columns with barriers of their
+//     own, so that its first half is promoted during the second's MMAs;
 //   * multiply-adds in pairs (fma.rn.f32x2), half the instructions;
+//   * little synchronisation on the critical path, where every K block waits
+//     on it twice.  A herald warp polls the mbarriers for the epilogue and
+//     releases it through a hardware barrier (a poll costs some 300 cycles,
+//     a barrier that the herald has reached about 40); the arrivals that
+//     free a buffer carry no memory ordering; the MMA warp runs a uniform
+//     loop with an elected issuer, which keeps descriptors in uniform
+//     registers; one commit a group serves copies and epilogue.  Together
+//     these took 8192 x 8192 x 16384 from 2055 us to 780;
 //   * one warp copies the scales of each K block into a ring in shared
-//     memory, eight K blocks ahead (asynchronous 4-byte copies, which take
+//     memory, twelve K blocks ahead (asynchronous 4-byte copies, which take
 //     any alignment).  Loads by the epilogue warps themselves, two K blocks
 //     ahead, waited for the memory system: 1.2 times the time.
+//
+// What bounds it.  Measured on GB300, BF16 out, one vector of scales and one
+// of tiles: 8192 x 8192 x 4096 204 us (2.7 PFLOP/s, 0.72 of twice the
+// measured 16-bit burst rate), x 16384 760 us (2.9).  A K block takes 714
+// cycles at the 1.8 GHz that the chip holds at this power: the shared memory
+// of an SM moves 80 KiB for it (32 written by TMA, A read once a group, B
+// once), 640 cycles.  A tile's end, when the sums go out and the MMAs wait
+// for free buffers, adds about 3000.  With two vectors of scales a thread
+// needs the scales of all its columns, 256 broadcast loads a K block and one
+// multiplication more a value: 1250 cycles, bound by latency and shared
+// memory together (4096 x 4096 x 8192 164 us against 113).
 //
 // One K step is one 128-byte swizzle row: a 128 x 128 block of either
 // operand is 16 KiB, one TMA box, whether K or the outer axis is contiguous

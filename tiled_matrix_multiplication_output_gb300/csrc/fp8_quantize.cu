@@ -20,6 +20,12 @@
 // 1 x 128, over the threads of a column for 128 x 1, over all for 128 x 128
 // -- so the two vector forms that training needs (the forward product and
 // the weight gradient contract over different axes) come from one read.
+// Besides the bytes the arithmetic counts, as 13 elements pass an SM a cycle
+// at the full rate: maxima are taken on packed 16-bit integers, values that
+// are not finite are looked for in the maxima only, a row's scale is worked
+// out by one lane.  Measured on GB300, 8192 x 8192 BF16: 128 x 128 32 us
+// (6.3 TB/s, 0.93 of the measured copy bandwidth), 1 x 128 33, 128 x 1 35,
+// both vectors 55 (4.8); FP32, 1 x 128, 55 (6.1).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -17,7 +17,10 @@
 //   * a block's first copies are issued before anything else is set up, and
 //     its ring holds 80 to 100 KiB, so that two blocks fit on an SM.
 //
-// The scaling of each K block's product is fp8_gemm_kernel's.
+// The scaling of each K block's product is fp8_gemm_kernel's.  Measured on
+// GB300, BF16 out: one token against 8192 x 8192 weights 14.0 us (4.8 TB/s
+// with the launch, 0.71 of the measured copy bandwidth), 64 tokens 18.2; one
+// against 4096 x 4096 6.5, of which a launch alone is about 4.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
