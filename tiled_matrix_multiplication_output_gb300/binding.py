@@ -442,7 +442,7 @@ FP8_BLOCKS = {"row": 0, "col": 1, "tile": 2}
 
 
 def _empty(shape, dtype, device):
-    return _torch().empty(shape, dtype=dtype, device=device)
+    return (_cached or _cache()).empty(shape, dtype=dtype, device=device)
 
 
 def _out_dtype(out_dtype):
@@ -457,20 +457,36 @@ def _f8_code(dtype) -> int:
         if dtype not in F8_CODES:
             raise ValueError(f"unknown 8-bit type {dtype!r}")
         return F8_CODES[dtype]
-    code = _f8_dtypes()[1].get(dtype)
+    code = _cache().f8_codes.get(dtype)
     if code is None:
         raise TypeError(f"{dtype} is not an 8-bit floating-point type")
     return code
 
 
-_torch_c_module = None
+class _Torch:
+    """What the calls below take from PyTorch, looked up once: they spend
+    about 10 us of host time in all, so that every look-up shows."""
+
+    def __init__(self):
+        torch = _torch()
+        self.current_device = torch._C._cuda_getDevice
+        # the address of the current stream, 3 us less than building a Stream object
+        self.current_stream = torch._C._cuda_getCurrentRawStream
+        self.empty = torch.empty
+        self.float32 = torch.float32
+        self.f8_types = (torch.float8_e4m3fn, torch.float8_e5m2)
+        self.f8_codes = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
+        self.codes = _dtype_codes()
 
 
-def _torch_c():
-    global _torch_c_module
-    if _torch_c_module is None:
-        _torch_c_module = _torch()._C
-    return _torch_c_module
+_cached = None
+
+
+def _cache() -> _Torch:
+    global _cached
+    if _cached is None:
+        _cached = _Torch()
+    return _cached
 
 
 def _allocate(stream, make, *args):
@@ -483,24 +499,23 @@ def _allocate(stream, make, *args):
 
 
 def _stream_ptr(stream, x) -> int:
-    """The stream's address; by default the current one of x's device.  Asked
-    of PyTorch's C layer, 3 us less than building a Stream object: the calls
-    below take about 10 us of host time in all."""
+    """The stream's address; by default the current one of x's device."""
     if stream is not None:
         return stream.cuda_stream
-    return _torch_c()._cuda_getCurrentRawStream(x.get_device())
+    return (_cached or _cache()).current_stream(x.get_device())
 
 
 def _check_matrix(x, what):
     """Returns (rows, cols, row stride) of a 2-D tensor with contiguous rows on
     the current CUDA device."""
-    shape, strides = x.shape, x.stride()
-    if len(shape) != 2 or not x.is_cuda:
+    device = x.get_device()
+    shape = x.shape
+    if device < 0 or len(shape) != 2:
         raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    if x.get_device() != _torch_c()._cuda_getDevice():
+    if device != (_cached or _cache()).current_device():
         raise ValueError(f"{what} is not on the current device")
     rows, cols = shape
-    pitch, step = strides
+    pitch, step = x.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what}'s rows must be contiguous")
     if rows <= 1:  # a single row has no pitch of its own
@@ -510,38 +525,25 @@ def _check_matrix(x, what):
     return rows, cols, pitch
 
 
-_f8_types = None
-
-
-def _f8_dtypes() -> tuple:
-    """PyTorch's types by code, and the codes by type."""
-    global _f8_types
-    if _f8_types is None:
-        torch = _torch()
-        types = (torch.float8_e4m3fn, torch.float8_e5m2)
-        _f8_types = types, {types[E4M3]: E4M3, types[E5M2]: E5M2}
-    return _f8_types
-
-
 def _fp8_empty(rows, cols, f8, block, device):
     """Uninitialised codes with a row pitch of a multiple of 16, their pitch,
     scales and their pitch."""
-    empty = _torch().empty
+    t = _cached or _cache()
     ld = (cols + 15) // 16 * 16
-    q = empty((rows, ld), device=device, dtype=_f8_dtypes()[0][f8])
+    q = t.empty((rows, ld), device=device, dtype=t.f8_types[f8])
     if ld != cols:
         q = q[:, :cols]
     if block == 0:
         n, lds = (cols + 127) // 128, rows
     else:
         n, lds = (rows + 127) // 128, cols if block == 1 else (cols + 127) // 128
-    return q, ld, empty((n, lds), dtype=_torch().float32, device=device), lds
+    return q, ld, t.empty((n, lds), device=device, dtype=t.float32), lds
 
 
 def _quantize_input(x):
     """(rows, cols, row stride, type code) of a tensor to quantise."""
     rows, cols, ldx = _check_matrix(x, "x")
-    code = _dtype_codes().get(x.dtype)
+    code = (_cached or _cache()).codes.get(x.dtype)
     if code is None:
         raise TypeError("x must be FP32, FP16 or BF16")
     return rows, cols, ldx, code
@@ -592,8 +594,10 @@ def _fp8_operand(q, s, op, k_rows, what):
     """(stored rows, stored columns, the bytes of its gemm_fp8_matrix_t) of
     codes q and scales s; k_rows: q's rows run along K."""
     rows, cols, ld = _check_matrix(q, what)
-    if s.dtype is not _torch().float32 or s.dim() != 2 or not (s.is_cuda and s.is_contiguous()):
-        raise ValueError(f"{what}'s scales must be a contiguous 2-D FP32 CUDA tensor")
+    t = _cached or _cache()
+    if s.dtype is not t.float32 or s.dim() != 2 or not s.is_contiguous() \
+            or s.get_device() != q.get_device():
+        raise ValueError(f"{what}'s scales must be a contiguous 2-D FP32 tensor on its device")
     rb, cb = (rows + 127) // 128, (cols + 127) // 128
     n, lds = s.shape
     if k_rows and n == cb and lds == rows:
@@ -606,8 +610,10 @@ def _fp8_operand(q, s, op, k_rows, what):
         raise ValueError(f"{what}'s scales have shape {(n, lds)}: expected "
                          f"{(cb, rows) if k_rows else (rb, cols)} (a vector along the "
                          f"contraction) or {(rb, cb)} (128 x 128 blocks)")
-    return rows, cols, _pack_matrix(q.data_ptr(), ld, _f8_code(q.dtype), block, s.data_ptr(), lds,
-                                    op)
+    f8 = t.f8_codes.get(q.dtype)
+    if f8 is None:
+        raise TypeError(f"{what} must have an 8-bit floating-point type")
+    return rows, cols, _pack_matrix(q.data_ptr(), ld, f8, block, s.data_ptr(), lds, op)
 
 
 def matmul_fp8(a, a_scale, b, b_scale, op_a="n", op_b="t", out_dtype=None, out=None, alpha=1.0,
@@ -691,8 +697,8 @@ def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, ep
     if workspace is None:
         nbytes = lib.gemm_newton_schulz_workspace_size(batch, rows, cols)
         workspace = _allocate(stream, _empty, (nbytes,), _torch().uint8, G.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif workspace.get_device() != G.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on G's device")
     else:
         nbytes = workspace.numel() * workspace.element_size()
     rc = lib.gemm_newton_schulz(G.data_ptr(), ldg, stride_g, out.data_ptr(), ldo, stride_o, batch,
@@ -708,7 +714,7 @@ def _check_batch(x, what):
     """(batch, rows, cols, row stride, batch stride) of a matrix or a 3-D batch."""
     if x.dim() not in (2, 3) or not x.is_cuda:
         raise ValueError(f"{what} must be a 2-D or 3-D CUDA tensor")
-    if x.dtype not in _dtype_codes():
+    if x.dtype not in (_cached or _cache()).codes:
         raise TypeError(f"{what} must be FP32, FP16 or BF16")
     if x.dim() == 2:
         return 1, *_check_matrix(x, what), 0
