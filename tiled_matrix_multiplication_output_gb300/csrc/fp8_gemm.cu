@@ -184,7 +184,7 @@ cudaError_t fp8_gemm_launch(const Fp8Launch& l, cudaStream_t stream)
         static_cast<long long>((l.M + 255) / 256) * ((l.N + 255) / 256);
     if (pair_tiles * 4 >= l.num_sms)
         return launch_scales<2, 256, 4>(l, stream);
-    return launch_scales<1, 128, 5>(l, stream);
+    return launch_scales<1, 128, 4>(l, stream);
 }
 
 }  // namespace tmmo

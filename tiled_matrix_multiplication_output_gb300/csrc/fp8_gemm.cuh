@@ -110,8 +110,9 @@ struct Fp8Layout {
     static constexpr int GROUP = 4;
     static constexpr int BLOCK_BYTES = (128 + BN) * 4;
     static constexpr int SLOT_BYTES = GROUP * BLOCK_BYTES;
-    static constexpr int OFF_STAGING = STAGES * STAGE;  // 4 KiB of output per epilogue warp
-    static constexpr int OFF_SCALE = OFF_STAGING + F8_EPI_WARPS * TC_STAGING_BYTES;
+    // Two output buffers of 4 KiB per epilogue warp.
+    static constexpr int OFF_STAGING = STAGES * STAGE;
+    static constexpr int OFF_SCALE = OFF_STAGING + F8_EPI_WARPS * 2 * TC_STAGING_BYTES;
     static constexpr int OFF_BAR = OFF_SCALE + SLOTS * SLOT_BYTES;
     // A K block's MMAs are issued as SUB groups of BN / SUB columns, each
     // with its own barriers.
@@ -165,14 +166,22 @@ __device__ __forceinline__ void fp8_store_tile(const uint64_t (&acc)[COLS / 2], 
                                                const Fp8Params& p)
 {
     constexpr int STRIP = TcOut<OutT>::STRIP;
-    const uint32_t base = stg + lane * 128, sw = lane & 7;
+    const uint32_t sw = lane & 7;
 #pragma unroll
     for (int s = 0; s < COLS / STRIP; ++s) {
         if (row0 >= p.M || col0 + s * STRIP >= p.N)
             break;
-        if (lane == 0)
-            bulk_wait_group_read<0>();
+        // Two buffers in turn.  Both are free at a tile's first strip (the
+        // last tile's left long before); later the strip before the last has
+        // to have left this one.
+        if (lane == 0) {
+            if (s == 0)
+                bulk_wait_group_read<0>();
+            else
+                bulk_wait_group_read<1>();
+        }
         __syncwarp();
+        const uint32_t buf = stg + (s & 1) * TC_STAGING_BYTES, base = buf + lane * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {  // 16-byte chunks
             uint32_t w[4];
@@ -199,7 +208,7 @@ __device__ __forceinline__ void fp8_store_tile(const uint64_t (&acc)[COLS / 2], 
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            tma_store_2d(map, stg, col0 + s * STRIP, row0);
+            tma_store_2d(map, buf, col0 + s * STRIP, row0);
             bulk_commit_group();
         }
     }
@@ -660,7 +669,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             const bool stored = !*abort_flag;  // an unfinished tile is not written
             // ---- the finished tile: alpha, beta, rounding to the output type
             const int row0 = row - static_cast<int>(lane);
-            const uint32_t stg = sbase + L::OFF_STAGING + ew * TC_STAGING_BYTES;
+            const uint32_t stg = sbase + L::OFF_STAGING + ew * 2 * TC_STAGING_BYTES;
             if (stored && p.tma_out) {
                 if (p.out_dtype == DT_F32)
                     fp8_store_tile<float, COLS>(acc, stg, &tmC, row0, col0, lane, p);
