@@ -211,6 +211,27 @@ def test_many_tiles(M, N, K, op_a, op_b, block_b):
     _expect(C, a, op_a, b, op_b, K)
 
 
+@pytest.mark.parametrize("M,N,K", [(500, 4850, 300), (2300, 2290, 1160), (2500, 2100, 64)])
+@pytest.mark.parametrize("op_a,op_b,block_b", [("n", "t", "tile"), ("n", "n", "vector"),
+                                               ("t", "t", "vector"), ("t", "n", "tile")])
+def test_last_tiles_shared_by_two_pairs(M, N, K, op_a, op_b, block_b):
+    """A last wave of at most half as many tiles as there are CTA pairs (all
+    of them, or 5 and 14 beyond a whole one): their columns are split."""
+    a, b = _product(M, N, K, op_a, op_b, "vector", block_b, seed=13)
+    kw = dict(op_a=op_a, op_b=op_b)
+    C = tg.matmul_fp8(*a[:2], *b[:2], out_dtype="bf16", **kw)
+    wide = torch.empty(M, N + 5, device="cuda")[:, :N].copy_(C)  # rows not on 16-byte boundaries
+    C0 = wide.double().cpu().numpy()
+    tg.matmul_fp8(*a[:2], *b[:2], out=wide, alpha=0.5, beta=-0.75, **kw)
+    F = tg.matmul_fp8(*a[:2], *b[:2], **kw)
+    F2 = tg.matmul_fp8(*a[:2], *b[:2], **kw)
+    _status()
+    assert torch.equal(F, F2)
+    _expect(C, a, op_a, b, op_b, K)
+    _expect(F, a, op_a, b, op_b, K)
+    _expect(wide, a, op_a, b, op_b, K, 0.5, -0.75, C0)
+
+
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(3, 77, 300), (520, 512, 256), (520, 511, 256)])
 def test_alpha_beta_into_a_strided_output(M, N, K, out):

@@ -92,7 +92,6 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
     const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
     if (tiles > 0x3fffffffLL)
         return cudaErrorNotSupported;
-    p.num_tiles = static_cast<int>(tiles);
     p.k_blocks = (l.K + F8_BK - 1) / F8_BK;
     p.group_m = 8;
     p.idesc = fp8_idesc(l.a.type, l.b.type, TC_BM * CG, BN / L::SUB, l.a.mn_major, l.b.mn_major);
@@ -118,7 +117,16 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
     p.tma_out = l.beta == 0.0f && aligned16(l.C) && (l.ldc * out_bytes(l.out_dtype)) % 16 == 0;
     if (p.tma_out && !encode_output(&tc, l))
         return cudaErrorNotSupported;
-    const int units = std::max(1, std::min(p.num_tiles, units_cap));
+    // Waves of whole tiles; where the last one would fill at most half of the
+    // CTA pairs, its tiles go to two pairs each.  Measured on GB300, us,
+    // whole / in parts: 4096 x 4096 x 8192 (28 tiles of 76 in the last wave)
+    // 112 / 106, with two scale vectors 155 / 141; 8192 x 8192 x 4096 (36)
+    // 200 / 197; 512 x 4864 x 4096 (38, the only wave) 18.4 / 15.2.
+    const int last = static_cast<int>(tiles % units_cap);
+    const bool split = CG == 2 && last > 0 && 2 * last <= units_cap;
+    p.whole = static_cast<int>(split ? tiles - last : tiles);
+    p.items = static_cast<int>(split ? tiles + last : tiles);
+    const int units = std::min(p.items, units_cap);
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -37,15 +37,22 @@
 //     ahead, waited for the memory system: 1.2 times the time.
 //
 // What bounds it.  Measured on GB300, BF16 out, one vector of scales and one
-// of tiles: 8192 x 8192 x 4096 204 us (2.7 PFLOP/s, 0.72 of twice the
+// of tiles: 8192 x 8192 x 4096 197 us (2.8 PFLOP/s, 0.74 of twice the
 // measured 16-bit burst rate), x 16384 760 us (2.9).  A K block takes 714
 // cycles at the 1.8 GHz that the chip holds at this power: the shared memory
 // of an SM moves 80 KiB for it (32 written by TMA, A read once a group, B
 // once), 640 cycles.  A tile's end, when the sums go out and the MMAs wait
 // for free buffers, adds about 3000.  With two vectors of scales a thread
 // needs the scales of all its columns, 256 broadcast loads a K block and one
-// multiplication more a value: 1250 cycles, bound by latency and shared
-// memory together (4096 x 4096 x 8192 164 us against 113).
+// multiplication more a value: 1200 cycles (4096 x 4096 x 8192 141 us
+// against 106).  There the FP32 pipe and the registers' read ports count for
+// most: a packed multiplication and a multiply-add of three different
+// operands take 5.3 cycles (one with a shared factor 2.7), 680 a K block and
+// partition; without any load of scales it would still be 1130.
+//
+// Waves.  A last wave that would fill at most half of the CTA pairs has its
+// tiles split into parts of 128 columns, one group of MMAs a K block, which
+// all epilogue warps share; a pair has at most one, after its whole tiles.
 //
 // One K step is one 128-byte swizzle row: a 128 x 128 block of either
 // operand is 16 KiB, one TMA box, whether K or the outer axis is contiguous
@@ -82,7 +89,9 @@ static_assert(128 * F8_REGS_FEW + 256 * F8_REGS_EPI <= F8_THREADS * F8_REGS_LAUN
 
 struct Fp8Params {
     int M, N, K;
-    int tiles_m, tiles_n, num_tiles;
+    int tiles_m, tiles_n;
+    int whole;                     // tiles computed whole, an item each
+    int items;                     // those and the parts: two for each further tile
     int k_blocks;
     int group_m;
     uint32_t idesc;
@@ -291,7 +300,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const int unit = (CG == 2) ? (blockIdx.x >> 1) : blockIdx.x;
     const int num_units = (CG == 2) ? (gridDim.x >> 1) : gridDim.x;
     const TcWatch watch{abort_flag, p.status, p.wait_budget};
-    auto tile_coords = [&](int t, int& mb, int& nb) {
+    // Item t: its tile, whether it is a part of one only, and the first of its
+    // columns in the tile.  A unit has at most one part, its last item.
+    auto item_coords = [&](int t, int& mb, int& nb, bool& part, int& first) {
+        part = false;
+        first = 0;
+        if (SUB == 2 && t >= p.whole) {
+            part = true;
+            first = ((t - p.whole) & 1) * (BN / 2);
+            t = p.whole + ((t - p.whole) >> 1);
+        }
         const int per_group = p.group_m * p.tiles_n;
         const int g = t / per_group;
         const int first_m = g * p.group_m;
@@ -345,12 +363,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             for (int s = 0; s < STAGES; ++s)
                 issued[s] = 0;
             bool ok = true;
-            for (int t = unit; ok && t < p.num_tiles; t += num_units) {
-                int mb, nb;
-                tile_coords(t, mb, nb);
+            for (int t = unit; ok && t < p.items; t += num_units) {
+                int mb, nb, first;
+                bool part;
+                item_coords(t, mb, nb, part, first);
                 const int a_row = mb * TILE_M + static_cast<int>(rank) * TC_BM;
                 // Group j of the columns takes 128 / SUB rows of B from each CTA.
-                const int b_row = nb * BN + static_cast<int>(rank) * (128 / SUB);
+                const int b_row = nb * BN + first + static_cast<int>(rank) * (128 / SUB);
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
                     if (!tc_wait(done_bar(stage, SUB - 1), phase ^ 1, watch)) {
                         ok = false;
@@ -358,7 +377,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     }
                     if (p.fault_skip_kblock != kb) {  // test hook, -1 in normal use
                         if (leader)
-                            mbar_arrive_expect_tx(full_bar(stage), CG * L::STAGE);
+                            mbar_arrive_expect_tx(full_bar(stage),
+                                                  CG * (part ? F8_BOX + F8_BOX / SUB : L::STAGE));
                         const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
                         const uint32_t dA = sbase + stage * L::STAGE;
                         auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
@@ -374,6 +394,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                             load(dA, &tmA, k0, a_row);
 #pragma unroll
                         for (int j = 0; j < SUB; ++j) {
+                            if (part && j > 0)
+                                break;
                             const uint32_t dB = dA + F8_BOX + j * (F8_BOX / SUB);
                             const int o = b_row + j * 128;
                             if (p.b_mn)
@@ -423,7 +445,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
             bool ok = true;
-            for (int t = unit; ok && t < p.num_tiles; t += num_units) {
+            // The K loop of an item.  PART: one group, issued when both halves of
+            // the buffer are free, and shared by all epilogue warps.
+            auto issue_item = [&](auto is_part) {
+                constexpr bool PART = decltype(is_part)::value;
 #pragma unroll 1
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
                     ok = tc_wait_warp(full_bar(stage), phase, watch);
@@ -435,17 +460,23 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         ok = ok && tc_wait_warp(tempty_bar(buf, j), buf_phase ^ 1, watch);
                         if (!ok)
                             break;
+                        if (PART && j + 1 < SUB)
+                            continue;
+                        const int g = PART ? 0 : j;
                         tc_fence_after();
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < F8_BK / 32; ++k)
-                                tc_mma_f8<CG>(d + j * (BN / SUB), a_hi | ((a0 + k * a_step) & 0x3FFF),
-                                              b_hi | ((b0 + j * (F8_BOX / SUB >> 4) + k * b_step) & 0x3FFF),
+                                tc_mma_f8<CG>(d + g * (BN / SUB), a_hi | ((a0 + k * a_step) & 0x3FFF),
+                                              b_hi | ((b0 + g * (F8_BOX / SUB >> 4) + k * b_step) & 0x3FFF),
                                               p.idesc, k != 0);
-                            if constexpr (CG == 2)
-                                tc_commit_pair(done_bar(stage, j), 0x3);
-                            else
-                                tc_commit(done_bar(stage, j));
+#pragma unroll
+                            for (int i = g; i <= j; ++i) {
+                                if constexpr (CG == 2)
+                                    tc_commit_pair(done_bar(stage, i), 0x3);
+                                else
+                                    tc_commit(done_bar(stage, i));
+                            }
                         }
                         __syncwarp();
                     }
@@ -460,6 +491,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         buf_phase ^= 1;
                     }
                 }
+            };
+            for (int t = unit; ok && t < p.items; t += num_units) {
+                if (SUB == 2 && t >= p.whole)
+                    issue_item(std::true_type{});
+                else
+                    issue_item(std::false_type{});
             }
             // every MMA issued has completed before TMEM is released (bounded)
             if (elect_one())
@@ -475,9 +512,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             int slot = 0;
             uint32_t slot_phase = 0;
             bool ok = true;
-            for (int t = unit; ok && t < p.num_tiles; t += num_units) {
-                int mb, nb;
-                tile_coords(t, mb, nb);
+            for (int t = unit; ok && t < p.items; t += num_units) {
+                int mb, nb, first;
+                bool part;
+                item_coords(t, mb, nb, part, first);
                 // Rows and columns beyond the matrix take the last one's
                 // scale (their products are never stored).
                 const int row0 = mb * TILE_M + static_cast<int>(rank) * TC_BM + static_cast<int>(lane);
@@ -531,7 +569,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             int stage = 0, slot = 0;
             uint32_t phase = 0, slot_phase = 0;
             bool ok = true;
-            for (int t = unit; t < p.num_tiles; t += num_units) {
+            for (int t = unit; t < p.items; t += num_units) {
 #pragma unroll 1
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
                     if (kb % L::GROUP == 0) {
@@ -563,22 +601,28 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         const uint32_t tempty0 =
             (CG == 2) ? mapa_shared(tempty_bar(0, group), 0) : tempty_bar(0, group);
         int buf = 0, slot = 0;
-        for (int t = unit; t < p.num_tiles; t += num_units) {
-            int mb, nb;
-            tile_coords(t, mb, nb);
+        // Item t, WIDTH columns a warp.  (Whole tiles have a loop of their own,
+        // which a choice in it makes 1 to 3 % slower; so has the MMA warp, 5 %.)
+        auto run_item = [&](auto width, int t) {
+            constexpr int WIDTH = decltype(width)::value;
             const uint32_t t_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                    static_cast<uint32_t>(half * COLS);
-            const int row = mb * TILE_M + static_cast<int>(rank) * TC_BM + q * 32 + static_cast<int>(lane);
-            const int col0 = nb * BN + half * COLS;
-            uint64_t acc[COLS / 2];
+                                    static_cast<uint32_t>(half * WIDTH);
+            // the warp's first column in the tile
+            const int cfirst = half * WIDTH + (WIDTH < COLS ? ((t - p.whole) & 1) * (BN / 2) : 0);
+            int mb, nb, first;
+            bool part;
+            item_coords(t, mb, nb, part, first);
+            const int row0 = mb * TILE_M + static_cast<int>(rank) * TC_BM + q * 32;
+            const int col0 = nb * BN + first + half * WIDTH;
+            uint64_t acc[WIDTH / 2];
 #pragma unroll
-            for (int i = 0; i < COLS / 2; ++i)
+            for (int i = 0; i < WIDTH / 2; ++i)
                 acc[i] = 0;
             // Tensor memory is read in chunks of 32 columns, each load issued
             // before the arithmetic of the chunk before it, across K blocks
             // as well: the next block's first chunk and scales are fetched
             // before the last chunk's arithmetic.
-            constexpr int NCH = COLS / 32;
+            constexpr int NCH = WIDTH / 32;
             uint32_t v[2][32];
             float rs = 0.0f;
             uint32_t caddr = 0;
@@ -588,7 +632,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 tmem_ld_32x32b_x32(t_base + static_cast<uint32_t>(buf * BN), v[0]);
                 const uint32_t saddr =
                     sbase + L::OFF_SCALE + slot * L::SLOT_BYTES + (kb % L::GROUP) * L::BLOCK_BYTES;
-                caddr = saddr + 512 + (COLV ? half * COLS * 4 : half * 4);
+                caddr = saddr + 512 + (COLV ? cfirst : cfirst / COLS) * 4;
                 rs = ld_shared_f32(saddr + (q * 32 + lane) * 4);
                 if constexpr (!COLV)
                     rs *= ld_shared_f32(caddr);
@@ -598,7 +642,6 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             for (int kb = 0; kb < p.k_blocks; ++kb) {
                 const uint64_t rs2 = pack_f32x2(__float_as_uint(rs), __float_as_uint(rs));
                 const uint32_t taddr = t_base + static_cast<uint32_t>(buf * BN);
-                const uint32_t cols = caddr;
                 const bool more = kb + 1 < p.k_blocks;
                 const bool slot_end = (kb + 1) % L::GROUP == 0 || !more;
                 const uint32_t sempty = sempty_bar(slot);
@@ -618,6 +661,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         slot = 0;
                 };
                 if constexpr (COLV) {
+                    const uint32_t cols = caddr;
                     // The products of the scales are formed while the chunk
                     // is on its way from tensor memory, in the registers of a
                     // second chunk.
@@ -668,24 +712,28 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             }
             const bool stored = !*abort_flag;  // an unfinished tile is not written
             // ---- the finished tile: alpha, beta, rounding to the output type
-            const int row0 = row - static_cast<int>(lane);
             const uint32_t stg = sbase + L::OFF_STAGING + ew * 2 * TC_STAGING_BYTES;
             if (stored && p.tma_out) {
                 if (p.out_dtype == DT_F32)
-                    fp8_store_tile<float, COLS>(acc, stg, &tmC, row0, col0, lane, p);
+                    fp8_store_tile<float, WIDTH>(acc, stg, &tmC, row0, col0, lane, p);
                 else if (p.out_dtype == DT_F16)
-                    fp8_store_tile<__half, COLS>(acc, stg, &tmC, row0, col0, lane, p);
+                    fp8_store_tile<__half, WIDTH>(acc, stg, &tmC, row0, col0, lane, p);
                 else
-                    fp8_store_tile<__nv_bfloat16, COLS>(acc, stg, &tmC, row0, col0, lane, p);
+                    fp8_store_tile<__nv_bfloat16, WIDTH>(acc, stg, &tmC, row0, col0, lane, p);
             } else if (stored) {
                 if (p.out_dtype == DT_F32)
-                    fp8_store_rows<float, COLS>(acc, stg, row0, col0, lane, p);
+                    fp8_store_rows<float, WIDTH>(acc, stg, row0, col0, lane, p);
                 else if (p.out_dtype == DT_F16)
-                    fp8_store_rows<__half, COLS>(acc, stg, row0, col0, lane, p);
+                    fp8_store_rows<__half, WIDTH>(acc, stg, row0, col0, lane, p);
                 else
-                    fp8_store_rows<__nv_bfloat16, COLS>(acc, stg, row0, col0, lane, p);
+                    fp8_store_rows<__nv_bfloat16, WIDTH>(acc, stg, row0, col0, lane, p);
             }
-        }
+        };
+        int t = unit;
+        for (; t < p.whole; t += num_units)
+            run_item(std::integral_constant<int, COLS>{}, t);
+        if (SUB == 2 && t < p.items)
+            run_item(std::integral_constant<int, COLS / SUB>{}, t);
     }
 
     // ---------------------------------------------------- teardown
