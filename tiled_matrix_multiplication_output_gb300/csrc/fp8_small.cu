@@ -18,9 +18,10 @@
 //     its ring holds 80 to 100 KiB, so that two blocks fit on an SM.
 //
 // The scaling of each K block's product is fp8_gemm_kernel's.  Measured on
-// GB300, BF16 out: one token against 8192 x 8192 weights 14.0 us (4.8 TB/s
-// with the launch, 0.71 of the measured copy bandwidth), 64 tokens 18.2; one
-// against 4096 x 4096 6.5, of which a launch alone is about 4.
+// GB300, BF16 out: one token against 8192 x 8192 weights 13.7 us (4.9 TB/s
+// with the launch, 0.72 of the measured copy bandwidth), 64 tokens 17.8; one
+// against 4096 x 4096 5.9 (6.8 with weights that are not in L2), of which a
+// launch alone is about 4.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -531,8 +532,8 @@ int tile_cols(int cols, bool mn_major)
 // Up to 64 columns the long operand is read once, in one column of tiles.
 // Beyond that this kernel pays while the persistent kernels' 128 x 128 tiles
 // would leave three SMs in four idle.  Measured on GB300, BF16 out, us, this
-// kernel / the persistent ones: 1 x 4096 x 4096 6.6 / 13.6, 64 x 8192 x 8192
-// 18.4 / 22.9, 96 x 200 x 1000 6.0 / 18.3, 128 x 4096 x 4096 (32 tiles) 12.2 /
+// kernel / the persistent ones: 1 x 4096 x 4096 5.9 / 13.6, 64 x 8192 x 8192
+// 18.0 / 22.9, 96 x 200 x 1000 6.0 / 18.3, 128 x 4096 x 4096 (32 tiles) 12.2 /
 // 13.2, 512 x 512 x 4096 (16) 9.7 / 12.7; not taken: 256 x 4096 x 4096 (64)
 // 17.3 / 13.3, 1024^3 (64) 8.9 / 6.7.
 bool fp8_small_takes(const Fp8Launch& l)
@@ -550,11 +551,15 @@ cudaError_t fp8_small_launch(const Fp8Launch& l, cudaStream_t stream)
     const int cols = std::min(l.M, l.N), rows = std::max(l.M, l.N);
     const int bn = tile_cols(cols, swapped ? l.a.mn_major : l.b.mn_major);
     const long long tiles = static_cast<long long>((rows + 127) / 128) * ((cols + bn - 1) / bn);
-    // Splits of K: up to two blocks an SM, each with at least two K blocks.
+    // Splits of K: up to one block an SM, each with at least two K blocks, or
+    // up to two with eight or more each.  (With two of fewer the exchange
+    // costs more than the overlap gives: 64 x 4096 x 4096 10.3 us instead of
+    // 9.4, 1 x 4096 x 4096 7.3 instead of 6.8, 16 x 4096 x 2048 6.2 instead of
+    // 5.6.  With one of more, 16 x 5120 x 5120 takes 10.0 instead of 9.4.)
     const int k_blocks = (l.K + F8_BK - 1) / F8_BK;
     int splits = 1;
-    while (splits < FS_MAX_SPLITS && tiles * splits * 2 <= 2LL * l.num_sms &&
-           k_blocks >= 2 * splits * 2)
+    while (splits < FS_MAX_SPLITS && k_blocks >= 4 * splits &&
+           tiles * splits * 2 <= (k_blocks >= 16 * splits ? 2LL : 1LL) * l.num_sms)
         splits *= 2;
     if (bn == 16)
         return launch_splits<16>(l, swapped, splits, stream);
