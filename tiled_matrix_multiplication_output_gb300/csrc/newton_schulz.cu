@@ -123,7 +123,7 @@ __host__ __device__ inline NsOperands ns_operands(const NsPlan& f, int mode, int
 
 // The last product of a call stages its output, which need not be aligned; the
 // others leave that shared memory to the L1 cache, through which the addends
-// come (with it, 8 x 545 x 552 took 178 us instead of 162).
+// come (with it, 8 x 545 x 552 took 1.1 times as long).
 template <int CG, int BN, int STAGES, bool STAGED>
 struct NsLayout {
     static constexpr int STAGE = 2 * NS_BOX;
@@ -785,7 +785,12 @@ cudaError_t ns_run(const CUtensorMap& ta, const CUtensorMap& tb, NsParams p, con
 }
 
 // 256 x 256 pair tiles once they fill half of the CTA pairs, 128 x 128 tiles
-// otherwise.
+// below that and where the pairs' last wave would be so empty that the smaller
+// tiles need clearly fewer waves, a wave of pairs counted as two: by a factor
+// of 1.4, or of 1.2 for a K of up to 512, where a tile's fixed costs outweigh
+// its operands' traffic.  Measured on GB300, us, pairs / 128 x 128:
+// 8 x 256 x 2400 193 / 158, 8 x 545 x 552 163 / 139, 8 x 300 x 1800 187 / 163,
+// 3000 x 3000 598 / 552; not taken: 2300 x 2300 (a factor of 1.33) 375 / 390.
 template <int MODE>
 cudaError_t ns_product(const CUtensorMap& ta, const CUtensorMap& tb, const NsParams& p,
                        const NsOperands& o, int num_sms, cudaStream_t stream)
@@ -794,7 +799,12 @@ cudaError_t ns_product(const CUtensorMap& ta, const CUtensorMap& tb, const NsPar
     const bool symmetric = MODE == NS_GRAM || MODE == NS_POLY;
     const long long pairs = p.batch * (symmetric ? tn * (tn + 1) / 2 : tm * tn);
     constexpr int STAGES = MODE == NS_LAST ? 5 : 6;
-    if (pairs * 4 >= num_sms)
+    const long long m1 = (p.M + 127) / 128, n1 = (p.N + 127) / 128;
+    const long long singles = p.batch * (symmetric ? n1 * (n1 + 1) / 2 : m1 * n1);
+    const long long pair_waves = 2 * ((2 * pairs + num_sms - 1) / num_sms);
+    const long long single_waves = (singles + num_sms - 1) / num_sms;
+    const bool empty = single_waves * (p.K <= 512 ? 12 : 14) <= pair_waves * 10;
+    if (pairs * 4 >= num_sms && !empty)
         return ns_run<2, 256, STAGES, MODE>(ta, tb, p, o, num_sms, stream);
     return ns_run<1, 128, STAGES, MODE>(ta, tb, p, o, num_sms, stream);
 }
