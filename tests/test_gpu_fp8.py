@@ -215,8 +215,9 @@ def test_many_tiles(M, N, K, op_a, op_b, block_b):
 @pytest.mark.parametrize("op_a,op_b,block_b", [("n", "t", "tile"), ("n", "n", "vector"),
                                                ("t", "t", "vector"), ("t", "n", "tile")])
 def test_last_tiles_shared_by_two_pairs(M, N, K, op_a, op_b, block_b):
-    """A last wave of at most half as many tiles as there are CTA pairs (all
-    of them, or 5 and 14 beyond a whole one): their columns are split."""
+    """A last wave of at most half as many tiles as there are CTA pairs (5 and
+    14 beyond a whole one): their columns are split.  The first shape is one
+    full wave of the smaller tiles."""
     a, b = _product(M, N, K, op_a, op_b, "vector", block_b, seed=13)
     kw = dict(op_a=op_a, op_b=op_b)
     C = tg.matmul_fp8(*a[:2], *b[:2], out_dtype="bf16", **kw)

@@ -15,8 +15,6 @@
 namespace tmmo {
 namespace {
 
-int out_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
-
 // C in boxes of 32 rows x 128 bytes, 128-byte swizzle.
 bool encode_output(CUtensorMap* map, const Fp8Launch& l)
 {
@@ -114,14 +112,14 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
     p.wait_budget = l.wait_budget;
     p.fault_skip_kblock = l.fault_skip_kblock;
     CUtensorMap tc = ta;  // unused without tma_out
-    p.tma_out = l.beta == 0.0f && aligned16(l.C) && (l.ldc * out_bytes(l.out_dtype)) % 16 == 0;
+    p.tma_out = tma_output(l);
     if (p.tma_out && !encode_output(&tc, l))
         return cudaErrorNotSupported;
     // Waves of whole tiles; where the last one would fill at most half of the
     // CTA pairs, its tiles go to two pairs each.  Measured on GB300, us,
     // whole / in parts: 4096 x 4096 x 8192 (28 tiles of 76 in the last wave)
     // 112 / 106, with two scale vectors 155 / 141; 8192 x 8192 x 4096 (36)
-    // 200 / 197; 512 x 4864 x 4096 (38, the only wave) 18.4 / 15.2.
+    // 200 / 197.
     const int last = static_cast<int>(tiles % units_cap);
     const bool split = CG == 2 && last > 0 && 2 * last <= units_cap;
     p.whole = static_cast<int>(split ? tiles - last : tiles);
@@ -183,16 +181,20 @@ cudaError_t fp8_gemm_launch(const Fp8Launch& l, cudaStream_t stream)
 {
     if (fp8_small_takes(l))
         return fp8_small_launch(l, stream);
-    // Pair tiles of 256 x 256 once they fill half of the CTA pairs; below
-    // that, four times as many 128 x 128 tiles keep more SMs busy.  Measured
-    // on GB300, us, with the limit at half the pairs / a quarter of them:
-    // 2048 x 1024 x 1024 (32 pair tiles) 6.8 / 8.7, 1500 x 1500 x 1000 (36)
-    // 9.5 / 12.5, 300 x 4319 x 564 (34) 7.7 / 11.1.
+    // Pair tiles of 256 x 256 take less from shared memory for a value, but a
+    // tile's end costs more, and four times as many 128 x 128 tiles keep more
+    // SMs busy.  So the smaller ones where they are one wave, or up to two (one
+    // of pairs) of at most two K blocks.  Measured on GB300, us, pairs /
+    // 128 x 128: 2400 x 900 (152 tiles) x 128 9.3 / 6.3, x 1024 12.2 / 8.4;
+    // 1024 x 2432 x 4096 (152) 18.3 / 14.0, with two scale vectors 23.9 / 15.9;
+    // 1300 x 2600 (231) x 256 6.9 / 6.3, x 512 7.8 / 7.7, x 1024 9.5 / 10.1.
+    const long long tiles =
+        static_cast<long long>((l.M + 127) / 128) * ((l.N + 127) / 128);
     const long long pair_tiles =
         static_cast<long long>((l.M + 255) / 256) * ((l.N + 255) / 256);
-    if (pair_tiles * 4 >= l.num_sms)
-        return launch_scales<2, 256, 4>(l, stream);
-    return launch_scales<1, 128, 4>(l, stream);
+    if (tiles <= l.num_sms || (2 * pair_tiles <= l.num_sms && l.K <= 2 * F8_BK))
+        return launch_scales<1, 128, 4>(l, stream);
+    return launch_scales<2, 256, 4>(l, stream);
 }
 
 }  // namespace tmmo

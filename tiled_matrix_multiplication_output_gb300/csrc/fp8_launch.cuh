@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include "device.h"
 #include "fp8.h"
 #include "fp8_gemm.cuh"
 #include "launch.h"
@@ -13,6 +14,15 @@ namespace tmmo {
 namespace {
 
 constexpr int kMaxDevices = 64;
+
+inline int out_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+// Whether the product can be stored by TMA: nothing to add to, rows on
+// 16-byte boundaries.
+inline bool tma_output(const Fp8Launch& l)
+{
+    return l.beta == 0.0f && aligned16(l.C) && (l.ldc * out_bytes(l.out_dtype)) % 16 == 0;
+}
 
 // The stored matrix of an operand (outer x K, or K x outer when MN-major) in
 // boxes of box_outer x 128 of K, swizzled over the length of a box row.  The

@@ -80,23 +80,24 @@ struct Fp8SmallLayout {
 };
 
 template <typename OutT>
-__device__ __forceinline__ void fs_store(const Fp8SmallParams& p, int row, int col, float v)
+__device__ __forceinline__ void fs_store(const Fp8SmallParams& p, OutT* c, float v)
 {
-    OutT* c = static_cast<OutT*>(p.C) + row * p.c_row + col * p.c_col;
     v *= p.alpha;
     if (p.beta != 0.0f)
         v = fmaf(p.beta, out_to_f32(*c), v);
     *c = fp8_to_out<OutT>(v);
 }
 
-__device__ __forceinline__ void fs_store_any(const Fp8SmallParams& p, int row, int col, float v)
+// store(C) with C as a pointer to the output's type.
+template <typename Store>
+__device__ __forceinline__ void fs_with_output(const Fp8SmallParams& p, Store&& store)
 {
     if (p.out_dtype == DT_F32)
-        fs_store<float>(p, row, col, v);
+        store(static_cast<float*>(p.C));
     else if (p.out_dtype == DT_F16)
-        fs_store<__half>(p, row, col, v);
+        store(static_cast<__half*>(p.C));
     else
-        fs_store<__nv_bfloat16>(p, row, col, v);
+        store(static_cast<__nv_bfloat16*>(p.C));
 }
 
 // The end of a tile: the blocks' sums through shared memory (at `base`, whose
@@ -139,27 +140,30 @@ __device__ __forceinline__ void fs_finish(const Fp8SmallParams& p, const uint64_
     for (int k = 0; k < SPLITS; ++k)
         peer[k] = SPLITS > 1 ? mapa_shared(at, k) : at;
     const bool store = !*abort_flag;
+    fs_with_output(p, [&](auto* out) {
+        auto* c = out + (row0 + r0) * p.c_row + (col0 + c0) * p.c_col;
+        const long long step = DR * p.c_row + DC * p.c_col;
 #pragma unroll
-    for (int j0 = 0; j0 < MINE; j0 += BATCH) {
-        float v[BATCH][SPLITS];
+        for (int j0 = 0; j0 < MINE; j0 += BATCH) {
+            float v[BATCH][SPLITS];
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j)
+            for (int j = 0; j < BATCH; ++j)
 #pragma unroll
-            for (int k = 0; k < SPLITS; ++k) {
-                const uint32_t from = peer[k] + (j0 + j) * (DR * STEP_R + DC * STEP_C) * 4;
-                v[j][k] = SPLITS > 1 ? ld_cluster_f32(from) : ld_shared_f32(from);
+                for (int k = 0; k < SPLITS; ++k) {
+                    const uint32_t from = peer[k] + (j0 + j) * (DR * STEP_R + DC * STEP_C) * 4;
+                    v[j][k] = SPLITS > 1 ? ld_cluster_f32(from) : ld_shared_f32(from);
+                }
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j, c += step) {
+                float sum = v[j][0];
+#pragma unroll
+                for (int k = 1; k < SPLITS; ++k)
+                    sum += v[j][k];
+                if (store && row0 + r0 + (j0 + j) * DR < p.rows && col0 + c0 + (j0 + j) * DC < p.cols)
+                    fs_store(p, c, sum);
             }
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            float sum = v[j][0];
-#pragma unroll
-            for (int k = 1; k < SPLITS; ++k)
-                sum += v[j][k];
-            const int row = row0 + r0 + (j0 + j) * DR, col = col0 + c0 + (j0 + j) * DC;
-            if (store && row < p.rows && col < p.cols)
-                fs_store_any(p, row, col, sum);
         }
-    }
+    });
     if constexpr (SPLITS > 1) {
         __syncwarp();
         cluster_sync();
@@ -406,13 +410,16 @@ __global__ void __launch_bounds__(FS_THREADS, 2)
         // a thread's values lie next to its neighbours' in C
         const int r = static_cast<int>(threadIdx.x) & 127;
         if (warp >= FS_EPI_WARP0 && ok && row0 + r < p.rows) {
+            fs_with_output(p, [&](auto* out) {
+                auto* c = out + (row0 + r) * p.c_row + col0 * p.c_col;
 #pragma unroll
-            for (int j = 0; j < BN; ++j) {
-                uint32_t w[2];
-                unpack_f32x2(acc[j / 2], w[0], w[1]);
-                if (col0 + j < p.cols)
-                    fs_store_any(p, row0 + r, col0 + j, __uint_as_float(w[j & 1]));
-            }
+                for (int j = 0; j < BN; ++j, c += p.c_col) {
+                    uint32_t w[2];
+                    unpack_f32x2(acc[j / 2], w[0], w[1]);
+                    if (col0 + j < p.cols)
+                        fs_store(p, c, __uint_as_float(w[j & 1]));
+                }
+            });
         }
     } else if (p.by_row) {
         fs_finish<BN, SPLITS, true>(p, acc, warp >= FS_EPI_WARP0 && ok, sbase, split, row0, col0, abort_flag);
@@ -536,9 +543,19 @@ int tile_cols(int cols, bool mn_major)
 // 18.0 / 22.9, 96 x 200 x 1000 6.0 / 18.3, 128 x 4096 x 4096 (32 tiles) 12.2 /
 // 13.2, 512 x 512 x 4096 (16) 9.7 / 12.7; not taken: 256 x 4096 x 4096 (64)
 // 17.3 / 13.3, 1024^3 (64) 8.9 / 6.7.
+//
+// With few K blocks there is nothing to divide over a cluster, and the
+// persistent kernels' stores by TMA are the faster end: 64 x 4096 x 256 6.5 /
+// 4.4, 256 x 2048 x 512 6.4 / 5.3, 64 x 8192 x 768 6.9 / 5.7, 24 x 4096 x 256
+// 4.7 / 4.3, 32 x 8192 x 768 5.5 / 5.6, 16 x 4096 x 256 3.9 / 4.0; without
+// them 100 x 300 x 500 6.0 / 6.8.
 bool fp8_small_takes(const Fp8Launch& l)
 {
-    if (std::min(l.M, l.N) <= 64)
+    const int least = std::min(l.M, l.N);
+    const int k_blocks = (l.K + F8_BK - 1) / F8_BK;
+    if (least > 16 && k_blocks <= (least > 32 ? 6 : 4) && tma_output(l))
+        return false;
+    if (least <= 64)
         return true;
     const long long tiles =
         static_cast<long long>((l.M + 127) / 128) * ((l.N + 127) / 128);
