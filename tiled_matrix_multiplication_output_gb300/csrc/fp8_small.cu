@@ -140,30 +140,30 @@ __device__ __forceinline__ void fs_finish(const Fp8SmallParams& p, const uint64_
     for (int k = 0; k < SPLITS; ++k)
         peer[k] = SPLITS > 1 ? mapa_shared(at, k) : at;
     const bool store = !*abort_flag;
-    fs_with_output(p, [&](auto* out) {
-        auto* c = out + (row0 + r0) * p.c_row + (col0 + c0) * p.c_col;
-        const long long step = DR * p.c_row + DC * p.c_col;
 #pragma unroll
-        for (int j0 = 0; j0 < MINE; j0 += BATCH) {
-            float v[BATCH][SPLITS];
+    for (int j0 = 0; j0 < MINE; j0 += BATCH) {
+        float v[BATCH][SPLITS];
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j)
+        for (int j = 0; j < BATCH; ++j)
 #pragma unroll
-                for (int k = 0; k < SPLITS; ++k) {
-                    const uint32_t from = peer[k] + (j0 + j) * (DR * STEP_R + DC * STEP_C) * 4;
-                    v[j][k] = SPLITS > 1 ? ld_cluster_f32(from) : ld_shared_f32(from);
-                }
+            for (int k = 0; k < SPLITS; ++k) {
+                const uint32_t from = peer[k] + (j0 + j) * (DR * STEP_R + DC * STEP_C) * 4;
+                v[j][k] = SPLITS > 1 ? ld_cluster_f32(from) : ld_shared_f32(from);
+            }
+        const int row = row0 + r0 + j0 * DR, col = col0 + c0 + j0 * DC;
+        fs_with_output(p, [&](auto* out) {
+            auto* c = out + row * p.c_row + col * p.c_col;
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j, c += step) {
+            for (int j = 0; j < BATCH; ++j, c += DR * p.c_row + DC * p.c_col) {
                 float sum = v[j][0];
 #pragma unroll
                 for (int k = 1; k < SPLITS; ++k)
                     sum += v[j][k];
-                if (store && row0 + r0 + (j0 + j) * DR < p.rows && col0 + c0 + (j0 + j) * DC < p.cols)
+                if (store && row + j * DR < p.rows && col + j * DC < p.cols)
                     fs_store(p, c, sum);
             }
-        }
-    });
+        });
+    }
     if constexpr (SPLITS > 1) {
         __syncwarp();
         cluster_sync();
