@@ -37,7 +37,7 @@
 //     ahead, waited for the memory system: 1.2 times the time.
 //
 // What bounds it.  Measured on GB300, BF16 out, one vector of scales and one
-// of tiles: 8192 x 8192 x 4096 197 us (2.8 PFLOP/s, 0.74 of twice the
+// of tiles: 8192 x 8192 x 4096 197 us (2.8 PFLOP/s, 0.73 of twice the
 // measured 16-bit burst rate), x 16384 760 us (2.9).  A K block takes 714
 // cycles at the 1.8 GHz that the chip holds at this power: the shared memory
 // of an SM moves 80 KiB for it (32 written by TMA, A read once a group, B

@@ -20,7 +20,7 @@
 // The scaling of each K block's product is fp8_gemm_kernel's.  Measured on
 // GB300, BF16 out: one token against 8192 x 8192 weights 13.7 us (4.9 TB/s
 // with the launch, 0.72 of the measured copy bandwidth), 64 tokens 17.8; one
-// against 4096 x 4096 5.9 (6.8 with weights that are not in L2), of which a
+// against 4096 x 4096 6.1 (7.0 with weights that are not in L2), of which a
 // launch alone is about 4.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -539,8 +539,8 @@ int tile_cols(int cols, bool mn_major)
 // Up to 64 columns the long operand is read once, in one column of tiles.
 // Beyond that this kernel pays while the persistent kernels' 128 x 128 tiles
 // would leave three SMs in four idle.  Measured on GB300, BF16 out, us, this
-// kernel / the persistent ones: 1 x 4096 x 4096 5.9 / 13.6, 64 x 8192 x 8192
-// 18.0 / 22.9, 96 x 200 x 1000 6.0 / 18.3, 128 x 4096 x 4096 (32 tiles) 12.2 /
+// kernel / the persistent ones: 1 x 4096 x 4096 6.1 / 13.6, 64 x 8192 x 8192
+// 17.7 / 22.9, 96 x 200 x 1000 6.0 / 18.3, 128 x 4096 x 4096 (32 tiles) 12.2 /
 // 13.2, 512 x 512 x 4096 (16) 9.7 / 12.7; not taken: 256 x 4096 x 4096 (64)
 // 17.3 / 13.3, 1024^3 (64) 8.9 / 6.7.
 //
