@@ -63,7 +63,7 @@ constexpr int NS_EPI_WARP0 = 2;
 constexpr int NS_EPI_WARPS = 8;
 constexpr int NS_BK = 64;
 constexpr int NS_BOX = 128 * NS_BK * 2;  // bytes of one operand box per CTA
-constexpr int NS_NORM_BLOCKS = 64;       // partial sums of squares per matrix, at most
+constexpr int NS_NORM_BLOCKS = 512;      // partial sums of squares per matrix, at most: one a thread
 
 enum NsMode {
     NS_GRAM = 0,    // A = X X^T: symmetric
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(512) ns_norm_kernel(const NsNorm p)
     const float s = ns_block_sum(ns_square_sum<InT>(p, blockIdx.y, first,
                                                     static_cast<long long>(gridDim.x) * blockDim.x));
     if (threadIdx.x == 0)
-        p.partial[blockIdx.y * p.blocks + blockIdx.x] = s;
+        p.partial[static_cast<long long>(blockIdx.y) * p.blocks + blockIdx.x] = s;
 }
 
 // Every block adds the partial sums in the same order.
@@ -647,9 +647,9 @@ __global__ void __launch_bounds__(512) ns_scale_kernel(const NsNorm p)
 {
     grid_dep_launch_dependents();
     grid_dep_wait();
-    float sum = 0.0f;
-    for (int i = 0; i < p.blocks; ++i)
-        sum += p.partial[blockIdx.y * p.blocks + i];
+    const int i = static_cast<int>(threadIdx.x);
+    const float sum =
+        ns_block_sum(i < p.blocks ? p.partial[static_cast<long long>(blockIdx.y) * p.blocks + i] : 0.0f);
     const long long first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
     ns_scale<InT>(p, blockIdx.y, first, static_cast<long long>(gridDim.x) * blockDim.x, sum);
 }
