@@ -559,7 +559,8 @@ def quantize_fp8(x, block: str = "row", dtype="e4m3", stream=None):
     (ceil(rows / 128), ceil(cols / 128))).  dtype: "e4m3" or "e5m2".  Returns
     (codes, scales): an element is its code times its block's scale.  The
     codes are a (rows, cols) view of rows padded to 16 bytes, the form
-    matmul_fp8 takes.  The exact definition is gemm_fp8_quantize's.
+    matmul_fp8 takes.  The scales' attribute `fp8_block` says the block shape.
+    The exact definition is gemm_fp8_quantize's.
     """
     rows, cols, ldx, code = _quantize_input(x)
     kind = FP8_BLOCKS.get(block)
@@ -572,6 +573,7 @@ def quantize_fp8(x, block: str = "row", dtype="e4m3", stream=None):
         _stream_ptr(stream, x))
     if rc != OK:
         raise GemmError(rc, "gemm_fp8_quantize")
+    s.fp8_block = block
     return q, s
 
 
@@ -587,12 +589,14 @@ def quantize_fp8_pair(x, dtype="e4m3", stream=None):
         qc.data_ptr(), ldc, sc.data_ptr(), ldsc, _stream_ptr(stream, x))
     if rc != OK:
         raise GemmError(rc, "gemm_fp8_quantize_pair")
+    sr.fp8_block, sc.fp8_block = "row", "col"
     return (qr, sr), (qc, sc)
 
 
-def _fp8_operand(q, s, op, k_rows, what):
+def _fp8_operand(q, s, op, k_rows, kind, what):
     """(stored rows, stored columns, the bytes of its gemm_fp8_matrix_t) of
-    codes q and scales s; k_rows: q's rows run along K."""
+    codes q and scales s; k_rows: q's rows run along K.  kind: the scales'
+    block shape, where the caller says it."""
     rows, cols, ld = _check_matrix(q, what)
     t = _cached or _cache()
     if s.dtype is not t.float32 or s.dim() != 2 or not s.is_contiguous() \
@@ -600,6 +604,8 @@ def _fp8_operand(q, s, op, k_rows, what):
         raise ValueError(f"{what}'s scales must be a contiguous 2-D FP32 tensor on its device")
     rb, cb = (rows + 127) // 128, (cols + 127) // 128
     n, lds = s.shape
+    if kind is not None and kind not in FP8_BLOCKS:
+        raise ValueError(f"unknown block shape {kind!r}")
     if k_rows and n == cb and lds == rows:
         block = 0
     elif not k_rows and n == rb and lds == cols:
@@ -610,6 +616,14 @@ def _fp8_operand(q, s, op, k_rows, what):
         raise ValueError(f"{what}'s scales have shape {(n, lds)}: expected "
                          f"{(cb, rows) if k_rows else (rb, cols)} (a vector along the "
                          f"contraction) or {(rb, cb)} (128 x 128 blocks)")
+    # A square matrix's two vector shapes have scales of the same shape: what
+    # quantised it (or the caller) says which one it is.  (Of one element, all
+    # shapes are the same.)
+    if rows == cols and rows > 1:
+        kind = kind or getattr(s, "fp8_block", None)
+        if FP8_BLOCKS.get(kind, block) != block:
+            raise ValueError(f"{what} has {kind!r} blocks: a scale vector must run along the "
+                             "contraction")
     f8 = t.f8_codes.get(q.dtype)
     if f8 is None:
         raise TypeError(f"{what} must have an 8-bit floating-point type")
@@ -617,7 +631,7 @@ def _fp8_operand(q, s, op, k_rows, what):
 
 
 def matmul_fp8(a, a_scale, b, b_scale, op_a="n", op_b="t", out_dtype=None, out=None, alpha=1.0,
-               beta=0.0, stream=None):
+               beta=0.0, stream=None, block_a=None, block_b=None):
     """C = alpha * op(A) @ op(B) + beta * C on quantised operands, as
     quantize_fp8 gives them (FP32 accumulation; the scales are applied for
     each 128 of the contraction).
@@ -625,14 +639,18 @@ def matmul_fp8(a, a_scale, b, b_scale, op_a="n", op_b="t", out_dtype=None, out=N
     op "n" takes an operand as stored, "t" its transpose; the defaults are
     x @ W^T with W stored out x in.  A scale vector must run along the
     contraction: "row" blocks where the stored rows do, "col" blocks
-    otherwise; "tile" blocks serve both.  `out` may supply C (rows
+    otherwise; "tile" blocks serve both.  The scales' shape tells the block
+    shape, but for a square matrix's two vectors: those are told apart by
+    block_a and block_b ("row", "col" or "tile"), else by the `fp8_block`
+    that quantize_fp8 sets on its scales, and are taken to run along the
+    contraction where neither is there.  `out` may supply C (rows
     contiguous, any row stride); beta != 0 needs it.  out_dtype defaults to
     FP32, or to out's type.  Returns C without synchronizing."""
     ta, tb = OPS.get(op_a), OPS.get(op_b)
     if ta is None or tb is None:
         raise ValueError("op_a and op_b are \"n\" or \"t\"")
-    M, K, A = _fp8_operand(a, a_scale, ta, not ta, "a")
-    K2, N, B = _fp8_operand(b, b_scale, tb, tb, "b")
+    M, K, A = _fp8_operand(a, a_scale, ta, not ta, block_a, "a")
+    K2, N, B = _fp8_operand(b, b_scale, tb, tb, block_b, "b")
     if ta:
         M, K = K, M
     if tb:
