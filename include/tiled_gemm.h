@@ -440,9 +440,11 @@ int gemm_fp8(const gemm_fp8_matrix_t* A, const gemm_fp8_matrix_t* B, void* C, in
  *
  * G and O: `batch` matrices of rows x cols, row pitches ldg and ldo and batch
  * pitches batch_stride_g and batch_stride_o in elements, element alignment;
- * F32, F16 or BF16 each.  O may be G itself (same type and pitches); other
- * overlap is not allowed.  coefficients: host array of steps x (a, b, c),
- * read during the call; steps 1 to 32.
+ * F32, F16 or BF16 each.  Matrices of a batch follow each other or are
+ * interleaved row by row (ld >= (batch - 1) * batch_stride + cols); with
+ * batch_stride_g == 0 every one of them is G.  O may be G itself (same type
+ * and pitches); other overlap is not allowed.  coefficients: host array of
+ * steps x (a, b, c), read during the call; steps 1 to 32.
  *
  * Accuracy.  Products take FP16 operands and accumulate in FP32, X is kept
  * to 22 bits: the result is about 2e-3 (relative, in the 2-norm of all

@@ -107,3 +107,18 @@ def test_bench_floor_of_an_operator():
     assert bench.operator_floor_us("orth", work, peaks) == pytest.approx(1000.0)
     assert bench.operator_floor_us("orth", {"bytes": 1, "flops": 1.8766e12}, peaks) == pytest.approx(1000.0)
     assert bench.operator_floor_us("product", {"bytes": 1, "flops": 1.8766e12}, peaks) == pytest.approx(500.0)
+
+
+def test_orthogonalisation_rejects_batches_that_overlap():
+    """Strides up to the ends of 64 bits, too."""
+    abc = (ctypes.c_float * 3)(3.0, -3.0, 1.0)
+    big = 2 ** 63 - 1
+
+    def call(ldg=48, sg=1536, ldo=48, so=1536, batch=3, rows=32, cols=48):
+        return tg.gemm_newton_schulz(P, ldg, sg, P, ldo, so, batch, rows, cols, tg.F32, tg.F32, 1,
+                                     abc, 1e-7, P, 1 << 30)
+
+    for bad in (dict(so=0), dict(so=1535), dict(so=-1), dict(so=-big), dict(sg=1535), dict(sg=-1536),
+                dict(ldo=143, so=48), dict(ldg=143, sg=48), dict(ldo=big, so=47),
+                dict(ldo=big // 8, so=big // 2), dict(ldg=big // 8, sg=big // 2)):
+        assert call(**bad) == INV, bad

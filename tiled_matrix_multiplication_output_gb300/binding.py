@@ -687,7 +687,9 @@ def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, ep
     products, as the Muon optimiser does with a gradient's running mean:
     X = G / (norm + eps), then `steps` times A = X X^T, X = a X + (b A + c A A) X.
 
-    G: FP32, FP16 or BF16, rows contiguous, any row and batch stride.
+    G: FP32, FP16 or BF16, rows contiguous, any row and batch stride that
+    keeps the matrices apart (also row by row, as t.transpose(0, 1) does), or
+    one matrix expanded over the batch.
     coefficients: one (a, b, c) for every step, or a sequence of `steps` of
     them.  out_dtype defaults to G's type; `out` may supply the result (it
     may be G itself).  workspace: a CUDA tensor of at least

@@ -17,6 +17,14 @@ bool valid_size(int64_t n) { return n >= 0 && n <= GEMM_MAX_DIM; }
 
 constexpr int64_t kMaxBatch = 65535;
 
+// Whether no two matrices of a batch share an element: each lies beyond the
+// one before it, or each of its rows does (interleaved matrices).
+bool apart(int64_t batch, int64_t rows, int64_t cols, int64_t ld, int64_t stride)
+{
+    return batch == 1 || (stride >= cols && (rows == 1 || (stride - cols) / (rows - 1) >= ld)) ||
+           (stride >= cols && (ld - cols) / (batch - 1) >= stride);
+}
+
 }  // namespace
 
 extern "C" size_t gemm_newton_schulz_workspace_size(int64_t batch, int64_t rows, int64_t cols)
@@ -45,8 +53,9 @@ extern "C" int gemm_newton_schulz(const void* G, int64_t ldg, int64_t batch_stri
         return GEMM_OK;
     if (!G || !O || ldg < cols || ldo < cols)
         return GEMM_ERR_INVALID_VALUE;
-    // a matrix's extent in its storage; matrices of a batch do not overlap
-    if (batch > 1 && (batch_stride_g < (rows - 1) * ldg + cols || batch_stride_o < (rows - 1) * ldo + cols))
+    // G is only read, so that one matrix may serve the whole batch
+    if (!apart(batch, rows, cols, ldo, batch_stride_o) ||
+        (batch_stride_g != 0 && !apart(batch, rows, cols, ldg, batch_stride_g)))
         return GEMM_ERR_INVALID_VALUE;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
         workspace_bytes < ns_workspace_bytes(batch, rows, cols))
