@@ -60,3 +60,31 @@ def test_block_shapes_of_one_element_and_of_rows_are_one():
     q, s = tg.quantize_fp8(row, block="tile")      # one block: the scales are a row form's
     assert abs(float(tg.matmul_fp8(q, s, q, s)) - 100.0) <= 2 * 100.0 * 2.0 ** -4
     _status()
+
+
+# ------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("M,N,K", [
+    (8, 512, 4096), (40, 512, 2048), (24, 384, 1024),     # C's columns along the tile's rows
+    (512, 8, 4096), (512, 60, 2048), (384, 24, 1024),     # C's rows along them
+    (120, 1000, 384), (2048, 2048, 1024)])                # one block a tile; CTA pairs
+def test_nothing_is_stored_after_a_wait_that_runs_out(M, N, K):
+    """One K step's copies are left out.  Where K is divided over a cluster, only
+    the block that holds the step gives up: the others' sums are whole, but none of
+    them makes a result."""
+    x, w = torch.randn(M, K, device="cuda"), torch.randn(N, K, device="cuda")
+    a, b = tg.quantize_fp8(x), tg.quantize_fp8(w, block="tile")
+    C = torch.full((M, N), 5.0, device="cuda")
+    tg.gemm_debug_config(20_000_000, 2)
+    try:
+        tg.matmul_fp8(*a, *b, out=C)
+        sh = torch.cuda.current_stream().cuda_stream
+        assert tg.gemm_device_status(sh) == tg.binding.ERR_TIMEOUT
+    finally:
+        tg.gemm_debug_config(0, -1)
+    assert torch.all(C == 5.0)
+    tg.matmul_fp8(*a, *b, out=C)
+    _status()
+    want = x.double() @ w.double().t()
+    # both operands are rounded to four bits: half an ulp is 2^-4 of an element at worst
+    assert ((C.double() - want).abs() <= 2 * 2.0 ** -4 * 1.1 * (x.abs().double() @ w.abs().double().t())).all()

@@ -139,7 +139,17 @@ __device__ __forceinline__ void fs_finish(const Fp8SmallParams& p, const uint64_
 #pragma unroll
     for (int k = 0; k < SPLITS; ++k)
         peer[k] = SPLITS > 1 ? mapa_shared(at, k) : at;
-    const bool store = !*abort_flag;
+    // A block that gave up has no sum: then no block of the cluster stores.
+    // (The question costs 0.1 us; asked after the first sums are on their way,
+    // the same.)
+    int gave_up = *abort_flag;
+    if constexpr (SPLITS > 1) {
+        const uint32_t flag = smem_u32(const_cast<int*>(abort_flag));
+        const int lane = t & 31;
+        if (lane < SPLITS)
+            gave_up |= __float_as_int(ld_cluster_f32(mapa_shared(flag, lane)));
+    }
+    const bool store = !__any_sync(0xffffffffu, gave_up);
 #pragma unroll
     for (int j0 = 0; j0 < MINE; j0 += BATCH) {
         float v[BATCH][SPLITS];
