@@ -54,3 +54,32 @@ def test_results_that_share_elements_are_refused():
         with pytest.raises(tg.GemmError):
             tg.newton_schulz(g, out=store.as_strided((3, 16, 24), (stride, store.shape[1], 1)))
     _status()
+
+
+# ------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("product", [0, 1, 2, 4])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 128, 128), (1, 64, 400), (3, 64, 1000), (1, 1000, 64),
+                                             (1, 100, 2500)])
+def test_nothing_is_stored_after_a_wait_that_runs_out(batch, rows, cols, product):
+    """One-launch form: the completion of one product (of six) is not signalled in
+    the first block of each cluster.  The other blocks' columns would be made of
+    that block's unfinished sums: nobody stores.  The next call is right."""
+    g = torch.stack([draw(rows, cols, "f32", "flat", seed=41 + i) for i in range(batch)]).cuda()
+    out = torch.full_like(g, 5.0)
+    tg.gemm_debug_config(20_000_000, product)
+    try:
+        tg.newton_schulz(g, steps=2, out=out)
+        sh = torch.cuda.current_stream().cuda_stream
+        assert tg.gemm_device_status(sh) == tg.binding.ERR_TIMEOUT
+    finally:
+        tg.gemm_debug_config(0, -1)
+    if product == 4:       # the last step's B: only the columns of the first blocks come of it
+        tg.newton_schulz(g, steps=2, out=(want := torch.empty_like(g)))
+        assert ((out == 5.0) | (out == want)).all() and (out == 5.0).any()
+    else:
+        assert torch.all(out == 5.0)
+    tg.newton_schulz(g, steps=2, out=out)
+    _status()
+    for i in range(batch):
+        expect(out[i], g[i], "f32", steps=2)

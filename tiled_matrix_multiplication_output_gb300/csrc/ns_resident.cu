@@ -35,7 +35,8 @@
 //
 // Eight warps; one of them issues the MMAs, all of them wait for a product's
 // completion (bounded) and read it from tensor memory.  A wait that runs out
-// is reported as everywhere, and the block then only takes part in barriers.
+// is reported as everywhere, the block then only takes part in barriers, and
+// no block of its cluster stores what came of its unfinished sums.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -65,7 +66,8 @@ struct NsResident {
     float coefficients[3 * NS_MAX_STEPS];
     int* status;
     long long wait_budget;
-    int fault_skip;                // test hook: the product whose completion is not signalled
+    int fault_skip;                // test hook: the product whose completion a cluster's first block
+                                   // does not signal
 };
 
 constexpr int NR_CHUNK = 128 * 128;  // bytes of 64 columns (of 128 rows) of an operand
@@ -88,6 +90,11 @@ struct NrLayout {
 __device__ __forceinline__ uint32_t nr_addr(uint32_t base, int row, int col)
 {
     return base + (col >> 6) * NR_CHUNK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ void st_cluster_b32(uint32_t addr, uint32_t w)
+{
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
 }
 
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t (&w)[4])
@@ -264,12 +271,21 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
                     tc_mma_f16<1>(d, k_hi | (ka & 0x3FFF), (b_mn ? n_hi : k_hi) | (kb & 0x3FFF), idesc,
                                   k != 0);
                 }
-                if (p.fault_skip != product)  // test hook, -1 in normal use
+                if (p.fault_skip != product || rank != 0)  // test hook, -1 in normal use
                     tc_commit(done_bar);
             }
             __syncwarp();
         }
-        ok = ok && tc_wait_warp(done_bar, static_cast<uint32_t>(product & 1), watch);
+        if (ok && !tc_wait_warp(done_bar, static_cast<uint32_t>(product & 1), watch)) {
+            ok = false;
+            // What this block hands to the others from here on is no sum: with
+            // its flag in all of them, none stores.  (They see it behind the
+            // barriers of the exchange.)
+            if constexpr (SIZE > 1) {
+                if (lane < SIZE)
+                    st_cluster_b32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), lane), 1);
+            }
+        }
         tc_fence_after();
         ++product;
     };
