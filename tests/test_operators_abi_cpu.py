@@ -2,6 +2,8 @@
 no GPU: bad arguments are rejected before a device is touched, empty problems
 are no-ops."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -122,3 +124,16 @@ def test_orthogonalisation_rejects_batches_that_overlap():
                 dict(ldo=143, so=48), dict(ldg=143, sg=48), dict(ldo=big, so=47),
                 dict(ldo=big // 8, so=big // 2), dict(ldg=big // 8, sg=big // 2)):
         assert call(**bad) == INV, bad
+
+
+def test_a_failed_occupancy_query_is_no_launch_error(tmp_path):
+    """ns_resident.cu linked against a stand-in for the CUDA runtime."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path / "fake_occupancy")
+    cmd = [tgbuild.nvcc_path(), *tgbuild.ARCH, *tgbuild.NVCC_FLAGS, "-O1", "-Xptxas", "-O0", "-cudart", "none",
+           "-o", exe, os.path.join(here, "c", "fake_occupancy.cpp"),
+           os.path.join(tgbuild.CSRC, "ns_resident.cu")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout == "ok\n", r.stdout

@@ -561,7 +561,10 @@ bool ns_resident_takes(const NsLaunch& l)
     const int size = resident_size(l.rows, l.cols);
     if (size == 0 || static_cast<long long>(l.batch) * size > 0x7fffffffLL)
         return false;
-    return launch_size(NsResident{}, size, 1, nullptr, true) == cudaSuccess;
+    if (launch_size(NsResident{}, size, 1, nullptr, true) == cudaSuccess)
+        return true;
+    cudaGetLastError();  // a query that failed is not the separate launches' error
+    return false;
 }
 
 cudaError_t ns_resident_launch(const NsLaunch& l, cudaStream_t stream)
