@@ -83,3 +83,39 @@ def test_nothing_is_stored_after_a_wait_that_runs_out(batch, rows, cols, product
     _status()
     for i in range(batch):
         expect(out[i], g[i], "f32", steps=2)
+
+
+# ------------------------------------------------------------ extreme norms
+
+# one-launch form on one block and on clusters, separate launches
+@pytest.mark.parametrize("rows,cols", [(40, 70), (100, 900), (150, 270), (700, 520)])
+@pytest.mark.parametrize("dtype,scale", [("f32", 1e21), ("f32", 1e39), ("bf16", 3e38), ("f32", 1e-21),
+                                         ("f32", 1e-24), ("bf16", 1e-32), ("f32", 1e-35), ("f32", 1e-38)])
+def test_norms_whose_squares_leave_fp32(rows, cols, dtype, scale):
+    """Entries of about 1e-2 times the scale: up to a norm near the end of FP32,
+    down to values with a few bits left (the definition is of the values given)."""
+    g = draw(rows, cols, "f32", "low rank", seed=rows).double()
+    norm = float(g.norm())
+    g = (g * min(scale, 3.0e38 / norm)).to(torch.float32 if dtype == "f32" else torch.bfloat16).cuda()
+    assert torch.isfinite(g).all() and (g != 0).any()
+    got = tg.newton_schulz(g, eps=0.0, out_dtype="f32")
+    _status()
+    expect(got, g, "f32", eps=0.0)
+    if scale > 1:                        # eps does not matter, nor do zeros
+        g[: rows // 2] = 0
+        g[rows // 2 + 1 :] *= 2.0 ** -90
+        expect(tg.newton_schulz(g, out_dtype="f32"), g, "f32")
+    else:                                # a result that eps makes small
+        tiny = tg.newton_schulz(g, eps=1e-7, out_dtype="f32")
+        assert torch.isfinite(tiny).all() and float(tiny.abs().max()) < 1e-10
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 70), (100, 900), (150, 270)])
+def test_norms_beyond_fp32_and_one_large_value(rows, cols):
+    g = torch.full((2, rows, cols), 3.3e38, device="cuda")
+    g[1] = 1e-3
+    g[1, rows - 1, cols - 1] = 3.3e38    # the norm is this value
+    got = tg.newton_schulz(g)
+    _status()
+    assert torch.isnan(got[0]).all()     # the norm is infinite in FP32
+    expect(got[1], g[1], "f32")

@@ -573,41 +573,40 @@ struct NsNorm {
     long long ldg, batch_g;
     int rows, cols, groups;        // groups of 8 columns per row
     float* partial;                // [batch][blocks]
+    double* wide;                  // the same, for the sums that FP32 does not hold
     int blocks;
     float eps;
     __half *hi, *lo;
     long long ld, batch_x;
 };
 
-// A thread's sum of squares over the groups first, first + step, ... of
-// matrix z.
-template <typename InT>
-__device__ __forceinline__ float ns_square_sum(const NsNorm& p, long long z, long long first,
+// A thread's sum of squares, in FP32 or FP64, over the groups first, first +
+// step, ... of matrix z.
+template <typename InT, typename SumT>
+__device__ __forceinline__ SumT ns_square_sum(const NsNorm& p, long long z, long long first,
                                                long long step)
 {
     const InT* g = static_cast<const InT*>(p.G) + z * p.batch_g;
     const long long total = static_cast<long long>(p.rows) * p.groups;
-    float s = 0.0f;
+    SumT s = 0;
     for (long long i = first; i < total; i += step) {
         const int row = static_cast<int>(i / p.groups), c = static_cast<int>(i % p.groups) * 8;
         float v[8];
         ns_load8(g + row * p.ldg + c, min(p.cols - c, 8), v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            s = fmaf(v[k], v[k], s);
+        for (int k = 0; k < 8; ++k) {
+            const SumT x = v[k];
+            s = fma(x, x, s);
+        }
     }
     return s;
 }
 
-// X = G / (norm + eps) as hi and lo over the same groups, from the sum of
-// all squares.  Where the norm is not finite (a NaN or an infinity in G, or
-// squares beyond FP32) the result is NaN throughout.
+// X = G / (norm + eps) as hi and lo over the same groups.
 template <typename InT>
 __device__ __forceinline__ void ns_scale(const NsNorm& p, long long z, long long first,
-                                         long long step, float sum)
+                                         long long step, float2 factors)
 {
-    const float norm = sqrtf(sum);
-    const float scale = isfinite(norm) ? NS_SX / (norm + p.eps) : __int_as_float(0x7fffffff);
     const InT* g = static_cast<const InT*>(p.G) + z * p.batch_g;
     const long long total = static_cast<long long>(p.rows) * p.groups;
     for (long long i = first; i < total; i += step) {
@@ -617,7 +616,7 @@ __device__ __forceinline__ void ns_scale(const NsNorm& p, long long z, long long
         uint32_t h[4], l[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float x = v[2 * k] * scale, y = v[2 * k + 1] * scale;
+            const float x = v[2 * k] * factors.x * factors.y, y = v[2 * k + 1] * factors.x * factors.y;
             h[k] = ns_pack(x, y);
             const float2 r = ns_unpack(h[k]);
             l[k] = ns_pack((x - r.x) * NS_LO, (y - r.y) * NS_LO);
@@ -635,10 +634,16 @@ __global__ void __launch_bounds__(512) ns_norm_kernel(const NsNorm p)
     grid_dep_launch_dependents();
     grid_dep_wait();
     const long long first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const float s = ns_block_sum(ns_square_sum<InT>(p, blockIdx.y, first,
-                                                    static_cast<long long>(gridDim.x) * blockDim.x));
+    const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+    const long long at = static_cast<long long>(blockIdx.y) * p.blocks + blockIdx.x;
+    const float s = ns_block_sum(ns_square_sum<InT, float>(p, blockIdx.y, first, step));
     if (threadIdx.x == 0)
-        p.partial[static_cast<long long>(blockIdx.y) * p.blocks + blockIdx.x] = s;
+        p.partial[at] = s;
+    if (!ns_squares_fit(s)) {  // (the same for the whole block)
+        const double wide = ns_block_sum(ns_square_sum<InT, double>(p, blockIdx.y, first, step));
+        if (threadIdx.x == 0)
+            p.wide[at] = wide;
+    }
 }
 
 // Every block adds the partial sums in the same order.
@@ -648,10 +653,20 @@ __global__ void __launch_bounds__(512) ns_scale_kernel(const NsNorm p)
     grid_dep_launch_dependents();
     grid_dep_wait();
     const int i = static_cast<int>(threadIdx.x);
-    const float sum =
-        ns_block_sum(i < p.blocks ? p.partial[static_cast<long long>(blockIdx.y) * p.blocks + i] : 0.0f);
+    const long long at = static_cast<long long>(blockIdx.y) * p.blocks + i;
+    const float part = i < p.blocks ? p.partial[at] : 0.0f;
+    const float sum = ns_block_sum(part);
+    float2 factors;
+    if (ns_squares_fit(sum)) {
+        factors = ns_factors(sum, p.eps);
+    } else {
+        double wide = part;
+        if (i < p.blocks && !ns_squares_fit(part))
+            wide = p.wide[at];
+        factors = ns_factors_wide(ns_block_sum(wide), p.eps);
+    }
     const long long first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    ns_scale<InT>(p, blockIdx.y, first, static_cast<long long>(gridDim.x) * blockDim.x, sum);
+    ns_scale<InT>(p, blockIdx.y, first, static_cast<long long>(gridDim.x) * blockDim.x, factors);
 }
 
 // ------------------------------------------------------------------- host
@@ -663,7 +678,7 @@ int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 struct NsSpace {
     int64_t m, ld_x, ld_a;
     int64_t x, a;                   // elements of one matrix
-    size_t off_hi[2], off_lo, off_a, off_b, off_partial, bytes;
+    size_t off_hi[2], off_lo, off_a, off_b, off_partial, off_wide, bytes;
 };
 
 NsSpace ns_space(int64_t batch, int64_t rows, int64_t cols)
@@ -686,6 +701,7 @@ NsSpace ns_space(int64_t batch, int64_t rows, int64_t cols)
     s.off_a = take(batch * s.a * 2);
     s.off_b = take(batch * s.a * 2);
     s.off_partial = take(batch * NS_NORM_BLOCKS * 4);
+    s.off_wide = take(batch * NS_NORM_BLOCKS * 8);
     s.bytes = at;
     return s;
 }
@@ -881,6 +897,7 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
     n.cols = l.cols;
     n.groups = (l.cols + 7) / 8;
     n.partial = reinterpret_cast<float*>(ws + s.off_partial);
+    n.wide = reinterpret_cast<double*>(ws + s.off_wide);
     // one group of 8 values a thread, more from NS_NORM_BLOCKS blocks on (with
     // four: 1024^2 151 us in all instead of 143; with at most 64 blocks 4096^2
     // 1059 instead of 969)

@@ -98,19 +98,44 @@ __device__ __forceinline__ void ns_load8(const InT* src, int n, float (&v)[8])
         v[i] = ns_value(e + i);
 }
 
-__device__ __forceinline__ float ns_block_sum(float s)
+template <typename T>
+__device__ __forceinline__ T ns_block_sum(T s)
 {
-    __shared__ float part[32];
+    __shared__ T part[32];
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         s += __shfl_xor_sync(0xffffffffu, s, d);
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = s;
     __syncthreads();
-    s = 0.0f;
+    s = 0;
     for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i)
         s += part[i];
     return s;
+}
+
+// Squares are summed in FP32.  Below 2^-90 a sum may have lost squares to
+// underflow (each loses at most 2^-150), above FP32 it is infinite: then it is
+// taken again in FP64, which holds every square of an FP32 value.  (FP64 is two
+// operations a cycle and SM here, too few for every call.)
+__device__ __forceinline__ bool ns_squares_fit(float s) { return s >= 0x1p-90f && s <= 3.402823466e38f; }
+
+// What the values of G are multiplied by, NS_SX / (norm + eps), from the sum of
+// squares where that fits FP32 -- the first factor -- and otherwise in two
+// factors, as their product may not fit.
+__device__ __forceinline__ float2 ns_factors(float sum, float eps)
+{
+    return make_float2(NS_SX / (sqrtf(sum) + eps), 1.0f);
+}
+// Where the norm is not finite in FP32 the result is NaN throughout.
+static __device__ __noinline__ float2 ns_factors_wide(double sum, float eps)
+{
+    const double norm = sqrt(sum);
+    if (!(norm <= 3.402823466e38))
+        return make_float2(__int_as_float(0x7fffffff), 1.0f);
+    const double d = norm + eps;
+    const double first = d < 0x1p-100 ? 0x1p100 : 1.0;
+    return make_float2(static_cast<float>(first), static_cast<float>(NS_SX / (d * first)));
 }
 
 }  // namespace tmmo

@@ -92,6 +92,13 @@ __device__ __forceinline__ uint32_t nr_addr(uint32_t base, int row, int col)
     return base + (col >> 6) * NR_CHUNK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
 }
 
+__device__ __forceinline__ double ld_cluster_f64(uint32_t addr)
+{
+    double v;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void st_cluster_b32(uint32_t addr, uint32_t w)
 {
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
@@ -163,6 +170,7 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + 12);
     float* sum_slot = reinterpret_cast<float*>(smem + L::OFF_BAR + 16);
+    double* wide_slot = reinterpret_cast<double*>(smem + L::OFF_BAR + 32);
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -210,6 +218,20 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
             s = fmaf(x[c][i], x[c][i], s);
     }
     s = ns_block_sum(s);
+    if (!ns_squares_fit(s)) {  // (the same for the whole block)
+        double wide = 0.0;
+#pragma unroll
+        for (int c = 0; c < XCH; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                wide = fma(static_cast<double>(x[c][i]), static_cast<double>(x[c][i]), wide);
+        wide = ns_block_sum(wide);
+        if (tid == 0)
+            *wide_slot = wide;
+        if constexpr (SIZE == 1)
+            __syncthreads();
+    }
+    float part[SIZE] = {s};
     if constexpr (SIZE > 1) {
         if (tid == 0)
             *sum_slot = s;
@@ -217,17 +239,30 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
         cluster_sync();
         s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < SIZE; ++k)
-            s += ld_cluster_f32(mapa_shared(smem_u32(sum_slot), k));
+        for (int k = 0; k < SIZE; ++k) {
+            part[k] = ld_cluster_f32(mapa_shared(smem_u32(sum_slot), k));
+            s += part[k];
+        }
     }
-    // Where the norm is not finite the result is NaN throughout.
-    const float norm = sqrtf(s);
-    const float scale = isfinite(norm) ? NS_SX / (norm + p.eps) : __int_as_float(0x7fffffff);
+    float2 factors;
+    if (ns_squares_fit(s)) {
+        factors = ns_factors(s, p.eps);
+    } else {
+        double sum = 0.0;
+#pragma unroll
+        for (int k = 0; k < SIZE; ++k) {
+            if (ns_squares_fit(part[k]))
+                sum += part[k];
+            else
+                sum += SIZE > 1 ? ld_cluster_f64(mapa_shared(smem_u32(wide_slot), k)) : *wide_slot;
+        }
+        factors = ns_factors_wide(sum, p.eps);
+    }
 #pragma unroll
     for (int c = 0; c < XCH; ++c)
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            x[c][i] *= scale;
+            x[c][i] = x[c][i] * factors.x * factors.y;
 
     auto put_x = [&]() {  // the operand form of X
 #pragma unroll
