@@ -446,13 +446,16 @@ int gemm_fp8(const gemm_fp8_matrix_t* A, const gemm_fp8_matrix_t* B, void* C, in
  * and pitches); other overlap is not allowed.  coefficients: host array of
  * steps x (a, b, c), read during the call; steps 1 to 32.
  *
- * Accuracy.  Products take FP16 operands and accumulate in FP32, X is kept
- * to 22 bits: the result is about 2e-3 (relative, in the 2-norm of all
- * elements) from the definition in exact arithmetic, before the rounding to
- * out_dtype.  Singular values must stay below 4 and |b s^2 + c s^4| below 32
- * throughout, the range of the FP16 operands, as they do for coefficients
- * that converge; beyond it the result is not finite.  A G whose norm is not finite in FP32 gives
- * NaN throughout its O.  A zero G gives zeros (NaN for eps == 0).
+ * Accuracy.  X, norms and sums are FP32; operands of products are rounded,
+ * and how far goes by out_dtype.  BF16: one FP16 value an element; the result
+ * is within 2e-3 (relative, in the 2-norm of all elements) of the definition
+ * in exact arithmetic, before its own rounding, which is 1.7e-3.  F32 and F16,
+ * and every type where a side is at most 128: two FP16 values, 22 bits; within
+ * 1e-5 + max(rows, cols) * 2^-25, for up to three times the time.
+ * Singular values must stay below 4 and |b s^2 + c s^4| below 32 throughout,
+ * the range of the FP16 operands, as they do for coefficients that converge;
+ * beyond it the result is not finite.  A G whose norm is not finite in FP32
+ * gives NaN throughout its O.  A zero G gives zeros (NaN for eps == 0).
  *
  * workspace: device memory of gemm_newton_schulz_workspace_size(batch, rows,
  * cols) bytes, 256-byte aligned; scratch, and not shared by calls that

@@ -1,11 +1,12 @@
 """Newton-Schulz orthogonalisation, further forms: batches that are not
 stacked, every size of the one-launch form, extreme norms, precision by the
 result's type, and waits that run out."""
+import numpy as np
 import pytest
 import torch
 
 import tiled_matrix_multiplication_output_gb300 as tg
-from tests.test_gpu_newton_schulz import draw, expect
+from tests.test_gpu_newton_schulz import DT, draw, expect, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +120,58 @@ def test_norms_beyond_fp32_and_one_large_value(rows, cols):
     _status()
     assert torch.isnan(got[0]).all()     # the norm is infinite in FP32
     expect(got[1], g[1], "f32")
+
+
+# -------------------------------------------------- precision by the result's type
+
+KINDS = ["flat", "low rank", "decaying"]
+
+
+def bound(rows, cols, out):
+    """What the header states, before the result's own rounding."""
+    if out == "bf16" and min(rows, cols) > 128:
+        return 2e-3
+    return 1e-5 + max(rows, cols) * 2.0 ** -25
+
+
+def expect_stated(got, g, out, **kw):
+    """Within the stated error, and the rounding of the exact result to the type
+    (independent of it, so that the two add as squares)."""
+    want = reference(g.double().cpu().numpy(), **kw)
+    size = np.linalg.norm(want)
+    rounding = np.linalg.norm(torch.from_numpy(want).to(DT[out]).double().numpy() - want) / size
+    off = np.linalg.norm(got.double().cpu().numpy() - want) / size
+    assert off <= np.hypot(bound(*g.shape, out), rounding), f"{off:.2e}, rounding {rounding:.2e}"
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (5, 300), (32, 33), (63, 64), (64, 64), (100, 100), (128, 128),
+                                       (129, 129), (200, 1000), (1000, 200), (333, 334), (640, 512)])
+def test_results_are_as_exact_as_stated(rows, cols, out, kind):
+    g = draw(rows, cols, "f32", kind, seed=rows + 3 * cols).cuda()
+    got = tg.newton_schulz(g, out_dtype=out)
+    _status()
+    expect_stated(got, g, out)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(2048, 700), (1500, 1500), (300, 3001)])
+def test_large_results_are_as_exact_as_stated(rows, cols, out):
+    """CTA pairs, with one and with two halves an operand."""
+    g = draw(rows, cols, "bf16", "flat", seed=51).cuda()
+    got = tg.newton_schulz(g, out_dtype=out)
+    again = tg.newton_schulz(g, out_dtype=out)
+    _status()
+    assert torch.equal(got, again)
+    expect_stated(got, g, out)
+
+
+def test_more_steps_and_other_coefficients_in_fp32():
+    g = draw(150, 270, "f32", "decaying", seed=52).cuda()
+    expect_stated(tg.newton_schulz(g, steps=12, coefficients=(2.0, -1.5, 0.5)), g, "f32", steps=12,
+                  abc=(2.0, -1.5, 0.5))
+    expect_stated(tg.newton_schulz(g, steps=1), g, "f32", steps=1)
+    g = draw(90, 700, "f32", "low rank", seed=53).cuda()
+    expect_stated(tg.newton_schulz(g, steps=2), g, "f32", steps=2)
+    _status()

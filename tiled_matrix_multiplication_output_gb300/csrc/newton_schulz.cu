@@ -31,15 +31,26 @@
 // plain 16-bit storage loses the small directions: against 64 bits, BF16
 // throughout is off by 1-3 % for matrices with a flat spectrum and up to
 // 18 % for a few strong directions over a noise floor, FP16 by 0.2-2 %.
-// Here X is kept as a pair of FP16 values (hi + lo, 22 bits) along the path
-// a X, which is where small directions grow, and the products take FP16
-// operands: B acts only on directions in which A = X X^T is not small, so
-// the operand's rounding is not amplified.  Simulated, 0.2 % or less for
-// every spectrum tried, about BF16's own rounding.  FP16 rather than BF16
-// for its three more bits at the same rate; power-of-two scales (NS_SX,
-// NS_SA, NS_SB) keep its range away from subnormals: entries of X up to
-// 16 in magnitude, A up to 16, B up to 32, with 24 binary orders below.
-// All sums (norm, products, a X + B X) are FP32.
+// Here X is kept in FP32, which is where small directions grow (along a X),
+// and only the products' operands are FP16: B acts only on directions in which
+// A = X X^T is not small, so an operand's rounding is not amplified.  How many
+// bits the operands have goes by what the result can show:
+//
+//   * BF16 results: one FP16 value an element (A, which is also added, B, and
+//     X as an operand).  At most 2e-3 off exact arithmetic for every spectrum
+//     tried, 1.3e-3 for a few strong directions over a noise floor, before the
+//     result's own rounding, which is 1.66e-3 over all elements;
+//   * FP32 and FP16 results, and those with a short side of up to 128, where
+//     one value would be up to 2.3e-3 off: two FP16 values, hi + lo, 22 bits, and
+//     three products (hi hi + hi lo + lo hi) in one accumulator, for three
+//     times the MMAs.  1e-6 to 5e-5 off, growing with the length of the
+//     contractions, whose sums the tensor core truncates to FP32 every 16 of K.
+//     The next rounding down, TF32, has FP16's ten bits at half its rate.
+//
+// FP16 rather than BF16 for its three more bits at the same rate;
+// power-of-two scales (NS_SX, NS_SA, NS_SB) keep its range away from
+// subnormals: entries of X up to 16 in magnitude, A up to 16, B up to 32, with
+// 24 binary orders below.  All sums (norm, products, a X + B X) are FP32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -79,10 +90,8 @@ struct NsParams {
     int k_blocks;
     bool a_mn, b_mn;
     uint32_t idesc;
-    // pitches of the FP16 addend and output; X's low half has X's
-    long long ld_add, batch_add;
-    __half* lo;                    // X's low half, read as part of the addend and written
-    long long ld_out, batch_out;
+    long long ld, batch_pitch;     // of the addend and of the output in the workspace
+    float* x;                      // X in FP32, read as the addend and written (updates)
     void* result;                  // NS_LAST
     long long ld_res, batch_res;
     bool vec_res;                  // its rows are on 16-byte boundaries
@@ -92,18 +101,23 @@ struct NsParams {
     int fault_skip_kblock;
 };
 
-// What differs from step to step: acc * alpha + beta * add -> out.
+// An operand of a product, in one or two FP16 halves.
+struct NsOperand {
+    __half *hi, *lo;               // lo: the rest hi leaves (two halves)
+};
+
+// What differs from step to step: acc * alpha + beta * addend -> out.
 struct NsOperands {
     float alpha, beta;
-    const __half* add;
-    __half* out;
+    NsOperand add;                 // of B = b A + c A A
+    NsOperand out;
 };
 
 // One orthogonalisation: the products' parameters by mode (an update's serve
 // its last step as well) and where the operands are.
 struct NsPlan {
     NsParams p[3];
-    __half *hi[2], *A, *B;         // X (read from one, written to the other), A, B
+    NsOperand X[2], A, B;          // X: read from one, written to the other
     float coefficients[3 * NS_MAX_STEPS];
 };
 
@@ -113,20 +127,21 @@ __host__ __device__ inline NsOperands ns_operands(const NsPlan& f, int mode, int
                 c = f.coefficients[3 * step + 2];
     switch (mode) {
     case NS_GRAM:
-        return {NS_SA / (NS_SX * NS_SX), 0.0f, nullptr, f.A};
+        return {NS_SA / (NS_SX * NS_SX), 0.0f, {}, f.A};
     case NS_POLY:
         return {c * (NS_SB / (NS_SA * NS_SA)), b * (NS_SB / NS_SA), f.A, f.B};
     default:
-        return {1.0f / NS_SB, a, f.hi[step & 1], f.hi[(step & 1) ^ 1]};
+        return {1.0f / NS_SB, a, {}, f.X[(step & 1) ^ 1]};
     }
 }
 
 // The last product of a call stages its output, which need not be aligned; the
 // others leave that shared memory to the L1 cache, through which the addends
 // come (with it, 8 x 545 x 552 took 1.1 times as long).
-template <int CG, int BN, int STAGES, bool STAGED>
+template <int CG, int BN, bool SPLIT, bool STAGED>
 struct NsLayout {
-    static constexpr int STAGE = 2 * NS_BOX;
+    static constexpr int STAGE = (SPLIT ? 4 : 2) * NS_BOX;  // A, B and with two halves A lo, B lo
+    static constexpr int STAGES = SPLIT ? 3 : STAGED ? 5 : 6;
     static constexpr int OFF_STAGING = STAGES * STAGE;  // 4 KiB of output per epilogue warp
     static constexpr int OFF_BAR = OFF_STAGING + (STAGED ? NS_EPI_WARPS * TC_STAGING_BYTES : 0);
     static constexpr int NUM_BARS = 2 * STAGES + 5;
@@ -182,15 +197,16 @@ __device__ __forceinline__ void ns_tile(int t, const NsParams& p, bool symmetric
     }
 }
 
-// 32 FP16 values of one row, `n` of them inside the matrix.  Rows start on
-// 32-byte boundaries and are padded to whole 16-value groups.
-__device__ __forceinline__ void ns_load_row(const __half* src, int n, uint32_t (&w)[16])
+// 32 values of one row, FP16 (16 words) or FP32, `n` of them inside the matrix.
+// Rows start on 32-byte boundaries and are padded to whole 16-value groups.
+template <int WORDS>
+__device__ __forceinline__ void ns_load_row(const void* src, int n, uint32_t (&w)[WORDS])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < WORDS / 4; ++i) {
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (8 * i < n)
-            u = *reinterpret_cast<const uint4*>(src + 8 * i);
+        if (i * (128 / WORDS) < n)
+            u = static_cast<const uint4*>(src)[i];
         w[4 * i] = u.x;
         w[4 * i + 1] = u.y;
         w[4 * i + 2] = u.z;
@@ -198,17 +214,30 @@ __device__ __forceinline__ void ns_load_row(const __half* src, int n, uint32_t (
     }
 }
 
-__device__ __forceinline__ void ns_store_row(__half* dst, int n, const uint32_t (&w)[16])
+template <int WORDS>
+__device__ __forceinline__ void ns_store_row(void* dst, int n, const uint32_t (&w)[WORDS])
 {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (16 * i < n) {
+    for (int i = 0; i < WORDS / 8; ++i) {
+        if (i * (256 / WORDS) < n) {
             uint32_t u[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 u[k] = w[8 * i + k];
-            st_global_v8(dst + 16 * i, u);
+            st_global_v8(static_cast<uint32_t*>(dst) + 8 * i, u);
         }
+    }
+}
+
+// Column `at` of `n` rows (pitch ld) from a row of FP16 values: the mirrored
+// part of a symmetric product.
+__device__ __forceinline__ void ns_store_column(__half* at, long long ld, int n, const uint32_t (&w)[16])
+{
+    unsigned short* dst = reinterpret_cast<unsigned short*>(at);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (i < n)
+            dst[i * ld] = static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)));
     }
 }
 
@@ -225,19 +254,31 @@ __device__ __forceinline__ uint64_t ns_desc_hi(bool mn)
 // from col0 in chunks of 32.  The addend is fetched two chunks ahead, the
 // first two before `wait`, which returns once the accumulator at taddr is
 // complete (false: given up).
-template <int MODE, int COLS, typename Wait>
+template <int MODE, int COLS, bool SPLIT, typename Wait>
 __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands& o, int z, bool mirror,
                                             int row, int col0, uint32_t taddr, uint32_t stg, Wait&& wait)
 {
     const bool inside = row < p.M;
-    const long long at_add = z * p.batch_add + row * p.ld_add + col0;
-    uint32_t ah[2][16], al[2][16];
+    const long long at0 = z * p.batch_pitch + row * p.ld + col0;
+    uint32_t add[2][32];  // FP32; of A 16 words of hi, then of lo
     auto fetch = [&](int c, int b) {  // the addend of chunk c
         const int n = inside ? p.N - col0 - c * 32 : 0;
-        if constexpr (MODE != NS_GRAM)
-            ns_load_row(o.add + at_add + c * 32, n, ah[b]);
-        if constexpr (MODE >= NS_UPDATE)
-            ns_load_row(p.lo + at_add + c * 32, n, al[b]);
+        const long long at = at0 + c * 32;
+        if constexpr (MODE == NS_POLY) {
+            uint32_t w[16];
+            ns_load_row(o.add.hi + at, n, w);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                add[b][i] = w[i];
+            if constexpr (SPLIT) {
+                ns_load_row(o.add.lo + at, n, w);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    add[b][16 + i] = w[i];
+            }
+        } else if constexpr (MODE >= NS_UPDATE) {
+            ns_load_row(p.x + at, n, add[b]);
+        }
     };
     fetch(0, 0);
     fetch(1, 1);
@@ -258,15 +299,19 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands&
         tmem_wait_ld(v);
         float f[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            f[2 * i] = o.alpha * __uint_as_float(v[2 * i]);
-            f[2 * i + 1] = o.alpha * __uint_as_float(v[2 * i + 1]);
-            if constexpr (MODE != NS_GRAM) {
-                float2 a = ns_unpack(ah[b][i]);
-                if constexpr (MODE >= NS_UPDATE) {
-                    const float2 l = ns_unpack(al[b][i]);
-                    a.x = fmaf(l.x, 1.0f / NS_LO, a.x);
-                    a.y = fmaf(l.y, 1.0f / NS_LO, a.y);
+        for (int i = 0; i < 32; ++i) {
+            f[i] = o.alpha * __uint_as_float(v[i]);
+            if constexpr (MODE >= NS_UPDATE)
+                f[i] = fmaf(o.beta, __uint_as_float(add[b][i]), f[i]);
+        }
+        if constexpr (MODE == NS_POLY) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float2 a = ns_unpack(add[b][i]);
+                if constexpr (SPLIT) {
+                    const float2 l = ns_unpack(add[b][16 + i]);
+                    a.x += l.x;
+                    a.y += l.y;
                 }
                 f[2 * i] = fmaf(o.beta, a.x, f[2 * i]);
                 f[2 * i + 1] = fmaf(o.beta, a.y, f[2 * i + 1]);
@@ -288,35 +333,32 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands&
             else
                 ns_store_result(static_cast<__nv_bfloat16*>(p.result) + at, p.ld_res, rows, n, p.vec_res, stg,
                                 lane, f);
-        } else {
+        } else if (inside) {
+            const long long at = at0 + c * 32;
+            // the mirrored tile: lane l writes column `row` of the rows col .. col + 31
+            const long long at_mirror = z * p.batch_pitch + col * p.ld + row;
+            if constexpr (MODE == NS_UPDATE) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] = __float_as_uint(f[i]);
+                ns_store_row(p.x + at, n, v);
+            }
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 w[i] = ns_pack(f[2 * i], f[2 * i + 1]);
-            const long long at = z * p.batch_out + row * p.ld_out + col;
-            if (inside)
-                ns_store_row(o.out + at, n, w);
-            if constexpr (MODE == NS_UPDATE) {
-                uint32_t lo[16];
+            ns_store_row(o.out.hi + at, n, w);
+            if (MODE != NS_UPDATE && mirror)
+                ns_store_column(o.out.hi + at_mirror, p.ld, n, w);
+            if constexpr (SPLIT) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 h = ns_unpack(w[i]);
-                    lo[i] = ns_pack((f[2 * i] - h.x) * NS_LO, (f[2 * i + 1] - h.y) * NS_LO);
+                    w[i] = ns_pack(f[2 * i] - h.x, f[2 * i + 1] - h.y);
                 }
-                if (inside)
-                    ns_store_row(p.lo + at, n, lo);
-            } else if (mirror) {
-                // the mirrored tile: lane l writes column `row` of the rows
-                // col .. col + 31
-                unsigned short* dst = reinterpret_cast<unsigned short*>(o.out) + z * p.batch_out +
-                                      col * p.ld_out + row;
-                if (inside) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (i < n)
-                            dst[i * p.ld_out] = static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)));
-                    }
-                }
+                ns_store_row(o.out.lo + at, n, w);
+                if (MODE != NS_UPDATE && mirror)
+                    ns_store_column(o.out.lo + at_mirror, p.ld, n, w);
             }
         }
     }
@@ -326,13 +368,16 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands&
 // tc_gemm_kernel: a persistent grid, TMA into a ring of 128-byte-swizzled
 // boxes, tcgen05 into two accumulators in tensor memory so that a tile's
 // epilogue overlaps the next tile's main loop, every wait bounded.
-template <int CG, int BN, int STAGES, int MODE>
+// SPLIT: operands of two halves, three products of halves into one
+// accumulator (lo lo, 2^-22 of the whole, is left out).
+template <int CG, int BN, int MODE, bool SPLIT>
 __global__ void __launch_bounds__(NS_THREADS, 1)
-    ns_product_kernel(const __grid_constant__ CUtensorMap tmA,
-                      const __grid_constant__ CUtensorMap tmB, const NsParams p,
-                      const NsOperands o)
+    ns_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmAlo, const __grid_constant__ CUtensorMap tmBlo,
+                      const NsParams p, const NsOperands o)
 {
-    using L = NsLayout<CG, BN, STAGES, MODE == NS_LAST>;
+    using L = NsLayout<CG, BN, SPLIT, MODE == NS_LAST>;
+    constexpr int STAGES = L::STAGES;
     constexpr bool SYMMETRIC = MODE == NS_GRAM || MODE == NS_POLY;
     constexpr int TILE_M = TC_BM * CG;
     constexpr int COLS = BN / 2;  // columns of the tile per epilogue warp
@@ -377,6 +422,10 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
+        if constexpr (SPLIT) {
+            tma_prefetch_desc(&tmAlo);
+            tma_prefetch_desc(&tmBlo);
+        }
     }
     if (warp == 1) {
         tmem_alloc<CG>(smem_u32(tmem_slot), L::TMEM_COLS);
@@ -415,27 +464,29 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
                         if (leader)
                             mbar_arrive_expect_tx(full_bar(stage), CG * L::STAGE);
                         const uint32_t fb = (CG == 2) ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
-                        const uint32_t dA = sbase + stage * L::STAGE, dB = dA + NS_BOX;
+                        const uint32_t dst = sbase + stage * L::STAGE;
                         const int k0 = kb * NS_BK;
+                        auto load = [&](uint32_t to, const CUtensorMap* map, int x, int y) {
+                            if constexpr (CG == 2)
+                                tma_load_3d_pair(to, map, fb, x, y, z);
+                            else
+                                tma_load_3d(to, map, fb, x, y, z);
+                        };
                         // K-major: one box of 128 rows x 64 of K; MN-major:
                         // two boxes of 64 of K x 64 outer values.
-                        auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
-                            if constexpr (CG == 2)
-                                tma_load_3d_pair(dst, map, fb, x, y, z);
-                            else
-                                tma_load_3d(dst, map, fb, x, y, z);
+                        auto load_box = [&](uint32_t to, const CUtensorMap* map, bool mn, int outer) {
+                            if (mn) {
+                                load(to, map, outer, k0);
+                                load(to + NS_BOX / 2, map, outer + 64, k0);
+                            } else {
+                                load(to, map, k0, outer);
+                            }
                         };
-                        if (p.a_mn) {
-                            load(dA, &tmA, a_row, k0);
-                            load(dA + NS_BOX / 2, &tmA, a_row + 64, k0);
-                        } else {
-                            load(dA, &tmA, k0, a_row);
-                        }
-                        if (p.b_mn) {
-                            load(dB, &tmB, b_row, k0);
-                            load(dB + NS_BOX / 2, &tmB, b_row + 64, k0);
-                        } else {
-                            load(dB, &tmB, k0, b_row);
+                        load_box(dst, &tmA, p.a_mn, a_row);
+                        load_box(dst + NS_BOX, &tmB, p.b_mn, b_row);
+                        if constexpr (SPLIT) {
+                            load_box(dst + 2 * NS_BOX, &tmAlo, p.a_mn, a_row);
+                            load_box(dst + 3 * NS_BOX, &tmBlo, p.b_mn, b_row);
                         }
 #pragma unroll
                         for (int s = 0; s < STAGES; ++s)
@@ -487,9 +538,15 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
                     const uint32_t b0 = a0 + (NS_BOX >> 4);
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < NS_BK / TC_UMMA_K; ++k)
-                            tc_mma_f16<CG>(d, a_hi | ((a0 + k * a_step) & 0x3FFF),
-                                           b_hi | ((b0 + k * b_step) & 0x3FFF), p.idesc, kb != 0 || k != 0);
+                        for (int part = 0; part < (SPLIT ? 3 : 1); ++part) {  // hi hi, hi lo, lo hi
+                            const uint32_t a = a0 + (part == 2 ? 2 * NS_BOX >> 4 : 0);
+                            const uint32_t b = b0 + (part == 1 ? 2 * NS_BOX >> 4 : 0);
+#pragma unroll
+                            for (int k = 0; k < NS_BK / TC_UMMA_K; ++k)
+                                tc_mma_f16<CG>(d, a_hi | ((a + k * a_step) & 0x3FFF),
+                                               b_hi | ((b + k * b_step) & 0x3FFF), p.idesc,
+                                               kb != 0 || part != 0 || k != 0);
+                        }
                         if constexpr (CG == 2)
                             tc_commit_pair(empty_bar(stage), 0x3);
                         else
@@ -531,7 +588,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
             const int row = mb * TILE_M + static_cast<int>(rank) * TC_BM + q * 32 + static_cast<int>(lane);
             const int col0 = nb * BN + half * COLS;
             bool ok = true;
-            ns_epilogue<MODE, COLS>(p, o, z, mb != nb, row, col0,
+            ns_epilogue<MODE, COLS, SPLIT>(p, o, z, mb != nb, row, col0,
                                     tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                         static_cast<uint32_t>(acc * BN + half * COLS),
                                     sbase + L::OFF_STAGING + (warp - NS_EPI_WARP0) * TC_STAGING_BYTES,
@@ -576,7 +633,8 @@ struct NsNorm {
     double* wide;                  // the same, for the sums that FP32 does not hold
     int blocks;
     float eps;
-    __half *hi, *lo;
+    float* x;
+    __half *hi, *lo;               // lo: null without split operands
     long long ld, batch_x;
 };
 
@@ -602,7 +660,7 @@ __device__ __forceinline__ SumT ns_square_sum(const NsNorm& p, long long z, long
     return s;
 }
 
-// X = G / (norm + eps) as hi and lo over the same groups.
+// X = G / (norm + eps) over the same groups, in FP32 and as an operand.
 template <typename InT>
 __device__ __forceinline__ void ns_scale(const NsNorm& p, long long z, long long first,
                                          long long step, float2 factors)
@@ -615,15 +673,21 @@ __device__ __forceinline__ void ns_scale(const NsNorm& p, long long z, long long
         ns_load8(g + row * p.ldg + c, min(p.cols - c, 8), v);
         uint32_t h[4], l[4];
 #pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = v[k] * factors.x * factors.y;
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float x = v[2 * k] * factors.x * factors.y, y = v[2 * k + 1] * factors.x * factors.y;
-            h[k] = ns_pack(x, y);
+            h[k] = ns_pack(v[2 * k], v[2 * k + 1]);
             const float2 r = ns_unpack(h[k]);
-            l[k] = ns_pack((x - r.x) * NS_LO, (y - r.y) * NS_LO);
+            l[k] = ns_pack(v[2 * k] - r.x, v[2 * k + 1] - r.y);
         }
         const long long at = z * p.batch_x + row * p.ld + c;
+        float4* x = reinterpret_cast<float4*>(p.x + at);
+        x[0] = make_float4(v[0], v[1], v[2], v[3]);
+        x[1] = make_float4(v[4], v[5], v[6], v[7]);
         *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        if (p.lo)
+            *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
     }
 }
 
@@ -673,12 +737,13 @@ __global__ void __launch_bounds__(512) ns_scale_kernel(const NsNorm p)
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// Workspace: X hi twice (a product reads one and writes the other), X lo, A,
-// B, partial sums.  Rows are padded to 16 values (32 bytes).
+// Workspace: X in FP32, X as an operand twice (a product reads one and writes
+// the other), A, B, each in two halves, and partial sums.  Rows are padded to
+// 16 values (32 bytes of FP16).
 struct NsSpace {
     int64_t m, ld_x, ld_a;
     int64_t x, a;                   // elements of one matrix
-    size_t off_hi[2], off_lo, off_a, off_b, off_partial, off_wide, bytes;
+    size_t off_x, off_hi[2], off_lo[2], off_a[2], off_b[2], off_partial, off_wide, bytes;
 };
 
 NsSpace ns_space(int64_t batch, int64_t rows, int64_t cols)
@@ -695,11 +760,13 @@ NsSpace ns_space(int64_t batch, int64_t rows, int64_t cols)
         at += static_cast<size_t>(round_up(bytes, 256));
         return here;
     };
-    s.off_hi[0] = take(batch * s.x * 2);
-    s.off_hi[1] = take(batch * s.x * 2);
-    s.off_lo = take(batch * s.x * 2);
-    s.off_a = take(batch * s.a * 2);
-    s.off_b = take(batch * s.a * 2);
+    s.off_x = take(batch * s.x * 4);
+    for (int i = 0; i < 2; ++i) {
+        s.off_hi[i] = take(batch * s.x * 2);
+        s.off_lo[i] = take(batch * s.x * 2);
+        s.off_a[i] = take(batch * s.a * 2);
+        s.off_b[i] = take(batch * s.a * 2);
+    }
     s.off_partial = take(batch * NS_NORM_BLOCKS * 4);
     s.off_wide = take(batch * NS_NORM_BLOCKS * 8);
     s.bytes = at;
@@ -724,12 +791,17 @@ bool ns_encode(CUtensorMap* map, const __half* base, int64_t rows, int64_t cols,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, int BN, int STAGES, int MODE>
-cudaError_t ns_run(const CUtensorMap& ta, const CUtensorMap& tb, NsParams p, const NsOperands& o,
-                   int num_sms, cudaStream_t stream)
+// The tensor maps of an operand's halves.
+struct NsMaps {
+    CUtensorMap hi, lo;
+};
+
+template <int CG, int BN, int MODE, bool SPLIT>
+cudaError_t ns_run(const NsMaps& a, const NsMaps& b, NsParams p, const NsOperands& o, int num_sms,
+                   cudaStream_t stream)
 {
-    using L = NsLayout<CG, BN, STAGES, MODE == NS_LAST>;
-    auto kern = ns_product_kernel<CG, BN, STAGES, MODE>;
+    using L = NsLayout<CG, BN, SPLIT, MODE == NS_LAST>;
+    auto kern = ns_product_kernel<CG, BN, MODE, SPLIT>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess)
@@ -796,7 +868,7 @@ cudaError_t ns_run(const CUtensorMap& ta, const CUtensorMap& tb, NsParams p, con
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
     note_launch();
-    err = cudaLaunchKernelEx(&cfg, kern, ta, tb, p, o);
+    err = cudaLaunchKernelEx(&cfg, kern, a.hi, b.hi, a.lo, b.lo, p, o);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -807,22 +879,29 @@ cudaError_t ns_run(const CUtensorMap& ta, const CUtensorMap& tb, NsParams p, con
 // its operands' traffic.  Measured on GB300, us, pairs / 128 x 128:
 // 8 x 256 x 2400 193 / 158, 8 x 545 x 552 163 / 139, 8 x 300 x 1800 187 / 163,
 // 3000 x 3000 598 / 552; not taken: 2300 x 2300 (a factor of 1.33) 375 / 390.
-template <int MODE>
-cudaError_t ns_product(const CUtensorMap& ta, const CUtensorMap& tb, const NsParams& p,
-                       const NsOperands& o, int num_sms, cudaStream_t stream)
+template <int MODE, bool SPLIT>
+cudaError_t ns_product_tiles(const NsMaps& a, const NsMaps& b, const NsParams& p, const NsOperands& o,
+                             int num_sms, cudaStream_t stream)
 {
     const long long tm = (p.M + 255) / 256, tn = (p.N + 255) / 256;
     const bool symmetric = MODE == NS_GRAM || MODE == NS_POLY;
     const long long pairs = p.batch * (symmetric ? tn * (tn + 1) / 2 : tm * tn);
-    constexpr int STAGES = MODE == NS_LAST ? 5 : 6;
     const long long m1 = (p.M + 127) / 128, n1 = (p.N + 127) / 128;
     const long long singles = p.batch * (symmetric ? n1 * (n1 + 1) / 2 : m1 * n1);
     const long long pair_waves = 2 * ((2 * pairs + num_sms - 1) / num_sms);
     const long long single_waves = (singles + num_sms - 1) / num_sms;
     const bool empty = single_waves * (p.K <= 512 ? 12 : 14) <= pair_waves * 10;
     if (pairs * 4 >= num_sms && !empty)
-        return ns_run<2, 256, STAGES, MODE>(ta, tb, p, o, num_sms, stream);
-    return ns_run<1, 128, STAGES, MODE>(ta, tb, p, o, num_sms, stream);
+        return ns_run<2, 256, MODE, SPLIT>(a, b, p, o, num_sms, stream);
+    return ns_run<1, 128, MODE, SPLIT>(a, b, p, o, num_sms, stream);
+}
+
+template <int MODE>
+cudaError_t ns_product(const NsMaps& a, const NsMaps& b, const NsParams& p, const NsOperands& o, bool split,
+                       int num_sms, cudaStream_t stream)
+{
+    return split ? ns_product_tiles<MODE, true>(a, b, p, o, num_sms, stream)
+                 : ns_product_tiles<MODE, false>(a, b, p, o, num_sms, stream);
 }
 
 template <typename InT>
@@ -861,11 +940,13 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
     char* ws = static_cast<char*>(l.workspace);
     const bool tall = l.rows > l.cols;
     const int m = static_cast<int>(s.m), wide = std::max(l.rows, l.cols);
+    const bool split = ns_split(l);
+    auto half = [&](size_t offset) { return reinterpret_cast<__half*>(ws + offset); };
     NsPlan plan{};
-    plan.hi[0] = reinterpret_cast<__half*>(ws + s.off_hi[0]);
-    plan.hi[1] = reinterpret_cast<__half*>(ws + s.off_hi[1]);
-    plan.A = reinterpret_cast<__half*>(ws + s.off_a);
-    plan.B = reinterpret_cast<__half*>(ws + s.off_b);
+    for (int i = 0; i < 2; ++i)
+        plan.X[i] = {half(s.off_hi[i]), half(s.off_lo[i])};
+    plan.A = {half(s.off_a[0]), half(s.off_a[1])};
+    plan.B = {half(s.off_b[0]), half(s.off_b[1])};
     std::copy(l.coefficients, l.coefficients + 3 * l.steps, plan.coefficients);
     for (int mode = 0; mode < 3; ++mode) {
         NsParams& p = plan.p[mode];
@@ -876,9 +957,9 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
         p.K = mode == NS_GRAM ? wide : m;
         p.a_mn = mode == NS_GRAM && tall;
         p.b_mn = mode == NS_GRAM ? tall : update && !tall;
-        p.ld_add = p.ld_out = update ? s.ld_x : s.ld_a;
-        p.batch_add = p.batch_out = update ? s.x : s.a;
-        p.lo = reinterpret_cast<__half*>(ws + s.off_lo);
+        p.ld = update ? s.ld_x : s.ld_a;
+        p.batch_pitch = update ? s.x : s.a;
+        p.x = reinterpret_cast<float*>(ws + s.off_x);
         p.result = l.O;
         p.ld_res = l.ldo;
         p.batch_res = l.batch_o;
@@ -905,20 +986,25 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
     n.blocks = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(NS_NORM_BLOCKS, (groups + 511) / 512)));
     n.eps = l.eps;
-    n.hi = plan.hi[0];
-    n.lo = reinterpret_cast<__half*>(ws + s.off_lo);
+    n.x = reinterpret_cast<float*>(ws + s.off_x);
+    n.hi = plan.X[0].hi;
+    n.lo = split ? plan.X[0].lo : nullptr;
     n.ld = s.ld_x;
     n.batch_x = s.x;
 
     // Tensor maps: X with K (128-row boxes) or the outer axis (64-row boxes)
     // contiguous, A and B.
-    CUtensorMap x_rows[2], x_cols[2], ta, tb;
+    NsMaps x_rows[2], x_cols[2], ta, tb;
+    auto encode = [&](NsMaps* maps, const NsOperand& o, int64_t rows, int64_t cols, int64_t ld, int64_t pitch,
+                      uint32_t box_rows) {
+        return ns_encode(&maps->hi, o.hi, rows, cols, ld, l.batch, pitch, box_rows) &&
+               ns_encode(&maps->lo, o.lo, rows, cols, ld, l.batch, pitch, box_rows);
+    };
     for (int i = 0; i < 2; ++i)
-        if (!ns_encode(&x_rows[i], plan.hi[i], l.rows, l.cols, s.ld_x, l.batch, s.x, 128) ||
-            !ns_encode(&x_cols[i], plan.hi[i], l.rows, l.cols, s.ld_x, l.batch, s.x, 64))
+        if (!encode(&x_rows[i], plan.X[i], l.rows, l.cols, s.ld_x, s.x, 128) ||
+            !encode(&x_cols[i], plan.X[i], l.rows, l.cols, s.ld_x, s.x, 64))
             return cudaErrorNotSupported;
-    if (!ns_encode(&ta, plan.A, m, m, s.ld_a, l.batch, s.a, 128) ||
-        !ns_encode(&tb, plan.B, m, m, s.ld_a, l.batch, s.a, 128))
+    if (!encode(&ta, plan.A, m, m, s.ld_a, s.a, 128) || !encode(&tb, plan.B, m, m, s.ld_a, s.a, 128))
         return cudaErrorNotSupported;
 
     cudaError_t err = l.in_dtype == DT_F32   ? ns_normalise<float>(n, l.batch, stream)
@@ -930,15 +1016,15 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
         const int cur = i & 1;
         const NsOperands gram = ns_operands(plan, NS_GRAM, i), poly = ns_operands(plan, NS_POLY, i),
                          update = ns_operands(plan, NS_UPDATE, i);
-        const CUtensorMap& tx = tall ? x_cols[cur] : x_rows[cur];
-        const CUtensorMap& t1 = tall ? x_rows[cur] : tb;
-        const CUtensorMap& t2 = tall ? tb : x_cols[cur];
-        if ((err = ns_product<NS_GRAM>(tx, tx, plan.p[NS_GRAM], gram, l.num_sms, stream)) != cudaSuccess ||
-            (err = ns_product<NS_POLY>(ta, ta, plan.p[NS_POLY], poly, l.num_sms, stream)) != cudaSuccess)
+        const NsMaps& tx = tall ? x_cols[cur] : x_rows[cur];
+        const NsMaps& t1 = tall ? x_rows[cur] : tb;
+        const NsMaps& t2 = tall ? tb : x_cols[cur];
+        const int sms = l.num_sms;
+        if ((err = ns_product<NS_GRAM>(tx, tx, plan.p[NS_GRAM], gram, split, sms, stream)) != cudaSuccess ||
+            (err = ns_product<NS_POLY>(ta, ta, plan.p[NS_POLY], poly, split, sms, stream)) != cudaSuccess)
             return err;
-        err = i + 1 < l.steps
-                  ? ns_product<NS_UPDATE>(t1, t2, plan.p[NS_UPDATE], update, l.num_sms, stream)
-                  : ns_product<NS_LAST>(t1, t2, plan.p[NS_UPDATE], update, l.num_sms, stream);
+        err = i + 1 < l.steps ? ns_product<NS_UPDATE>(t1, t2, plan.p[NS_UPDATE], update, split, sms, stream)
+                              : ns_product<NS_LAST>(t1, t2, plan.p[NS_UPDATE], update, split, sms, stream);
         if (err != cudaSuccess)
             return err;
     }

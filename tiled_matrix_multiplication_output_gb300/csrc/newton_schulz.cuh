@@ -13,7 +13,6 @@ namespace tmmo {
 
 // Stored value = scale * value.
 constexpr float NS_SX = 4096.0f, NS_SA = 4096.0f, NS_SB = 2048.0f;
-constexpr float NS_LO = 2048.0f;  // lo holds (X - hi) * NS_LO
 
 __device__ __forceinline__ float ns_value(const float* p) { return *p; }
 __device__ __forceinline__ float ns_value(const __half* p) { return __half2float(*p); }

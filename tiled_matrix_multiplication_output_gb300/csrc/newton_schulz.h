@@ -37,6 +37,17 @@ inline bool ns_vec_rows(const NsLaunch& l)
            (l.batch == 1 || l.batch_o * es % 16 == 0);
 }
 
+// Whether the products' operands are two FP16 values an element instead of one.
+// With one the result is up to 2e-3 off exact arithmetic (relative, over all
+// elements), about what rounding it to BF16 does (1.66e-3), for a third of the
+// MMAs.  So: two where the result has more bits, and for a short side of up to
+// 128, where one would be up to 2.3e-3 off (and the one-launch form is bound by
+// latency).
+inline bool ns_split(const NsLaunch& l)
+{
+    return l.out_dtype != DT_BF16 || l.rows <= 128 || l.cols <= 128;
+}
+
 size_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
 
 // The one-launch form for matrices that a cluster holds on chip

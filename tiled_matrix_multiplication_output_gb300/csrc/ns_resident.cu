@@ -11,24 +11,27 @@
 //     than columns) is divided by columns over the blocks of the cluster.
 //     Then the update X <- a X + B X is local to a block, and only
 //     A = X X^T, a sum over the blocks, crosses between them;
-//   * a thread keeps its 128 values of X in registers, in FP32, and writes
-//     their FP16 operand form to shared memory, in the 128-byte-swizzled
-//     layout of a tensor-core operand.  One copy serves both products: rows
-//     of 64 columns are a K-major operand of X X^T and an MN-major one of
-//     B X;
+//   * a thread keeps its values of X (96 or 128) in registers, in FP32, and
+//     writes their operand form to shared memory, in the
+//     128-byte-swizzled layout of a tensor-core operand.  One copy serves both
+//     products: rows of 64 columns are a K-major operand of X X^T and an
+//     MN-major one of B X;
+//   * operands are two FP16 values an element, hi + lo, and a product is
+//     hi hi + hi lo + lo hi in one accumulator, whatever the result's type:
+//     with one value matrices as narrow as these would be up to 2.3e-3 off,
+//     more than a BF16 result's own rounding (1.66e-3).  It costs 15 us a call
+//     (128 x 128 36 us instead of 21);
 //   * A and B share one buffer: each thread replaces its elements of A by
 //     those of B once the product A A is complete, and every block computes
 //     all of B for itself;
 //   * the sum over blocks goes through distributed shared memory in FP32:
 //     a block adds up 1 / SIZE of the rows, in rank order, and writes the
-//     FP16 result to all of them;
+//     operand form to all of them;
 //   * G is read once: the norm is taken from the registers.
 //
-// A step of a 128 x 128 matrix takes about 3.3 us (6200 cycles: three
-// products of 1000 to 1500 with their latency, four passes over registers
-// and shared memory of about 500), five steps with the launch 20 us against
-// 77 as separate launches; with several blocks the exchange adds 3.5 us a
-// step, most of it in two cluster barriers: 64 x 512 37 us, 128 x 4000 57.
+// Five steps of a 128 x 128 matrix take 36 us with the launch; with several
+// blocks the exchange adds about 3 us a step, most of it in two cluster
+// barriers: 64 x 512 51 us, 128 x 2000 74, 128 x 4000 92.
 // Matrices with a short side of up to 256 were tried in the same way and were
 // slower than separate launches: the exchange of 256 x 256 FP32 sums took
 // 12 us a step.
@@ -71,18 +74,22 @@ struct NsResident {
 };
 
 constexpr int NR_CHUNK = 128 * 128;  // bytes of 64 columns (of 128 rows) of an operand
-constexpr int NR_COLS = 256;         // columns of X a block can hold
 constexpr uint32_t NR_TMEM_COLS = 256;
 
-template <int SIZE>
+// COLS: columns of X a block can hold.
+template <int SIZE, int COLS>
 struct NrLayout {
-    static constexpr int OFF_A = 0;                               // 128 x 128
-    static constexpr int OFF_X = OFF_A + 2 * NR_CHUNK;            // 128 x NR_COLS
-    static constexpr int OFF_STAGING = OFF_X + NR_COLS / 64 * NR_CHUNK;
-    // 128 FP32 rows from all blocks, to be added up here
-    static constexpr int OFF_BAR = OFF_STAGING + (SIZE > 1 ? 128 * 128 * 4 : 0);
+    static constexpr int A_LO = 2 * NR_CHUNK, X_LO = COLS / 64 * NR_CHUNK;  // from hi to lo
+    static constexpr int OFF_A = 0;                               // 128 x 128, hi and lo
+    static constexpr int OFF_X = OFF_A + 2 * A_LO;                // 128 x COLS, hi and lo
+    static constexpr int OFF_STAGING = OFF_X + 2 * X_LO;
+    // 128 FP32 rows from all blocks, to be added up here: whole, or in halves
+    static constexpr int HALVES = COLS == 256 ? 2 : 1;
+    static constexpr int STAGING_ROW = 512 / HALVES;
+    static constexpr int OFF_BAR = OFF_STAGING + (SIZE > 1 ? 128 * STAGING_ROW : 0);
     static constexpr int SMEM_ALLOC = OFF_BAR + 64 + 1024;
-    static_assert(SMEM_ALLOC <= 232448, "exceeds 227 KiB of dynamic shared memory");
+    // (static shared memory: the sums of ns_block_sum)
+    static_assert(SMEM_ALLOC + 512 <= 232448, "exceeds 227 KiB of shared memory");
 };
 
 // Shared-memory address of 8 columns (16 bytes) of an operand: 64-column
@@ -156,11 +163,11 @@ __device__ __forceinline__ void nr_store(OutT* o, const NsResident& p, int row0,
     }
 }
 
-template <int SIZE>
+template <int SIZE, int COLS>
 __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid_constant__ NsResident p)
 {
-    using L = NrLayout<SIZE>;
-    constexpr int XCH = NR_COLS / 64;  // 32-column chunks of X per thread
+    using L = NrLayout<SIZE, COLS>;
+    constexpr int XCH = COLS / 64;  // 32-column chunks of X per thread
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -264,16 +271,28 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
         for (int i = 0; i < 32; ++i)
             x[c][i] = x[c][i] * factors.x * factors.y;
 
-    auto put_x = [&]() {  // the operand form of X
+    // Eight values as an operand: hi, and what it leaves.
+    auto halves = [](const float* v, uint32_t (&h)[4], uint32_t (&l)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = ns_pack(v[2 * i], v[2 * i + 1]);
+            const float2 r = ns_unpack(h[i]);
+            l[i] = ns_pack(v[2 * i] - r.x, v[2 * i + 1] - r.y);
+        }
+    };
+    auto put = [&](uint32_t at, uint32_t to_lo, const float* v) {
+        uint32_t h[4], l[4];
+        halves(v, h, l);
+        st_shared_v4(at, h[0], h[1], h[2], h[3]);
+        st_shared_v4(at + to_lo, l[0], l[1], l[2], l[3]);
+    };
+    auto put_x = [&]() {
 #pragma unroll
         for (int c = 0; c < XCH; ++c) {
-            const float(&v)[32] = x[c];
             if ((2 * c + g) * 32 < ncol) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    st_shared_v4(nr_addr(sX, row, (2 * c + g) * 32 + 8 * k),
-                                 ns_pack(v[8 * k], v[8 * k + 1]), ns_pack(v[8 * k + 2], v[8 * k + 3]),
-                                 ns_pack(v[8 * k + 4], v[8 * k + 5]), ns_pack(v[8 * k + 6], v[8 * k + 7]));
+                    put(nr_addr(sX, row, (2 * c + g) * 32 + 8 * k), L::X_LO, x[c] + 8 * k);
             }
         }
     };
@@ -290,8 +309,8 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
     int product = 0;
     bool ok = true;
     // Issues a product of 128 rows (K-major from `a`; `b` K-major as well, or
-    // X MN-major) and waits for it.
-    auto multiply = [&](uint32_t a, uint32_t b, bool b_mn, int steps, int n) {
+    // X MN-major; their lo halves a_lo and b_lo further) and waits for it.
+    auto multiply = [&](uint32_t a, uint32_t a_lo, uint32_t b, uint32_t b_lo, bool b_mn, int steps, int n) {
         fence_proxy_async_smem();
         tc_fence_before();
         __syncthreads();
@@ -300,11 +319,14 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
             const uint32_t idesc = tc_idesc(false, 128, n, false, b_mn);
             const uint32_t d = *tmem_slot;
             if (elect_one()) {
-                for (int k = 0; k < steps; ++k) {
-                    const uint32_t off = (k >> 2) * NR_CHUNK + (k & 3) * 32;
-                    const uint32_t ka = (a + off) >> 4, kb = (b + (b_mn ? k * 2048 : off)) >> 4;
-                    tc_mma_f16<1>(d, k_hi | (ka & 0x3FFF), (b_mn ? n_hi : k_hi) | (kb & 0x3FFF), idesc,
-                                  k != 0);
+                for (int part = 0; part < 3; ++part) {  // hi hi, hi lo, lo hi
+                    const uint32_t pa = a + (part == 2 ? a_lo : 0), pb = b + (part == 1 ? b_lo : 0);
+                    for (int k = 0; k < steps; ++k) {
+                        const uint32_t off = (k >> 2) * NR_CHUNK + (k & 3) * 32;
+                        const uint32_t ka = (pa + off) >> 4, kb = (pb + (b_mn ? k * 2048 : off)) >> 4;
+                        tc_mma_f16<1>(d, k_hi | (ka & 0x3FFF), (b_mn ? n_hi : k_hi) | (kb & 0x3FFF), idesc,
+                                      part != 0 || k != 0);
+                    }
                 }
                 if (p.fault_skip != product || rank != 0)  // test hook, -1 in normal use
                     tc_commit(done_bar);
@@ -333,7 +355,7 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
                     cc = p.coefficients[3 * step + 2];
         // ---- A = X X^T
         constexpr float alpha_a = NS_SA / (NS_SX * NS_SX);
-        multiply(sX, sX, false, n_steps, 128);
+        multiply(sX, L::X_LO, sX, L::X_LO, false, n_steps, 128);
         if constexpr (SIZE == 1) {
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
@@ -343,12 +365,11 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
                 tmem_wait_ld(v);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint32_t w[4];
+                    float f[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] = ns_pack(alpha_a * __uint_as_float(v[8 * k + 2 * i]),
-                                       alpha_a * __uint_as_float(v[8 * k + 2 * i + 1]));
-                    st_shared_v4(nr_addr(sA, row, col + 8 * k), w[0], w[1], w[2], w[3]);
+                    for (int i = 0; i < 8; ++i)
+                        f[i] = alpha_a * __uint_as_float(v[8 * k + i]);
+                    put(nr_addr(sA, row, col + 8 * k), L::A_LO, f);
                 }
             }
         } else {
@@ -356,93 +377,111 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
             // buffer ([sender][row], 16-byte units swizzled against bank
             // conflicts), and that block adds the senders' rows in rank
             // order.  Rows are pushed, as remote stores do not wait.
+            constexpr int HALVES = L::HALVES;            // 128 or 64 columns at a time
+            constexpr int UNITS = 16 / HALVES;           // of 8 columns
             constexpr int SHARE = 128 / SIZE;            // rows that this block adds up
-            constexpr int ITEMS = SHARE * 16;            // in units of 8 columns
+            constexpr int ITEMS = SHARE * UNITS;
             constexpr int MINE = (ITEMS + NR_THREADS - 1) / NR_THREADS;
             const uint32_t staging = sbase + L::OFF_STAGING;
             const int to = rank * SHARE + row % SHARE;
             const uint32_t dst =
-                mapa_shared(staging + to * 512, static_cast<uint32_t>(row / SHARE));
+                mapa_shared(staging + to * L::STAGING_ROW, static_cast<uint32_t>(row / SHARE));
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                const int col = (2 * g + c) * 32;
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem + col, v);
-                tmem_wait_ld(v);
-                if (n_steps == 0) {  // a block without columns adds nothing
+            for (int h = 0; h < HALVES; ++h) {
+                if (HALVES == 1 || g == h) {
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        const int col = (2 * g + c) * 32;
+                        const int unit = HALVES == 1 ? col / 4 : c * 8;  // of 4 columns
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(tmem + col, v);
+                        tmem_wait_ld(v);
+                        if (n_steps == 0) {  // a block without columns adds nothing
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = 0;
-                }
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = 0;
+                        }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t w[4] = {v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
-                    st_cluster_v4(dst + (((col / 4 + k) ^ (to & 7)) << 4), w);
-                }
-            }
-            __syncwarp();
-            cluster_sync();
-#pragma unroll
-            for (int j = 0; j < MINE; ++j) {
-                const int item = j * NR_THREADS + tid;
-                if (item < ITEMS) {
-                    const int r = item / 16, u = 2 * (item % 16);
-                    float a[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        a[i] = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < SIZE; ++k) {
-                        const int from = k * SHARE + r;
-                        uint32_t t[4], w[4];
-                        ld_shared_v4(staging + from * 512 + ((u ^ (from & 7)) << 4), t);
-                        ld_shared_v4(staging + from * 512 + (((u + 1) ^ (from & 7)) << 4), w);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            a[i] += __uint_as_float(t[i]);
-                            a[4 + i] += __uint_as_float(w[i]);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t w[4] = {v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+                            st_cluster_v4(dst + (((unit + k) ^ (to & 7)) << 4), w);
                         }
                     }
-                    uint32_t sum[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sum[i] = ns_pack(alpha_a * a[2 * i], alpha_a * a[2 * i + 1]);
-                    const uint32_t at = nr_addr(sA, rank * SHARE + r, 8 * (item % 16));
-#pragma unroll
-                    for (int k = 0; k < SIZE; ++k)
-                        st_cluster_v4(mapa_shared(at, k), sum);
                 }
+                __syncwarp();
+                cluster_sync();
+#pragma unroll
+                for (int j = 0; j < MINE; ++j) {
+                    const int item = j * NR_THREADS + tid;
+                    if (item < ITEMS) {
+                        const int r = item / UNITS, u = 2 * (item % UNITS);
+                        float a[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            a[i] = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < SIZE; ++k) {
+                            const int from = k * SHARE + r;
+                            const uint32_t at = staging + from * L::STAGING_ROW;
+                            uint32_t t[4], w[4];
+                            ld_shared_v4(at + ((u ^ (from & 7)) << 4), t);
+                            ld_shared_v4(at + (((u + 1) ^ (from & 7)) << 4), w);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                a[i] += __uint_as_float(t[i]);
+                                a[4 + i] += __uint_as_float(w[i]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            a[i] *= alpha_a;
+                        uint32_t hi[4], lo[4];
+                        halves(a, hi, lo);
+                        const uint32_t at = nr_addr(sA, rank * SHARE + r, 64 * h + 8 * (item % UNITS));
+#pragma unroll
+                        for (int k = 0; k < SIZE; ++k) {
+                            const uint32_t peer = mapa_shared(at, k);
+                            st_cluster_v4(peer, hi);
+                            st_cluster_v4(peer + L::A_LO, lo);
+                        }
+                    }
+                }
+                // the sums are in every block, and the buffer is free for the
+                // next half
+                fence_proxy_async_cluster();
+                __syncwarp();
+                cluster_sync();
             }
-            fence_proxy_async_cluster();
-            __syncwarp();
-            cluster_sync();
         }
         // ---- B = b A + c A A, in A's place
         const float alpha_b = cc * (NS_SB / (NS_SA * NS_SA)), beta_b = cb * (NS_SB / NS_SA);
-        multiply(sA, sA, false, m_steps, 128);
+        multiply(sA, L::A_LO, sA, L::A_LO, false, m_steps, 128);
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
             const int col = (2 * g + c) * 32;
             uint32_t v[32];
             tmem_ld_32x32b_x32(tmem + col, v);
-            uint32_t w[4][4];
+            uint32_t w[4][4], l[4][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k) {
                 ld_shared_v4(nr_addr(sA, row, col + 8 * k), w[k]);
+                ld_shared_v4(nr_addr(sA, row, col + 8 * k) + L::A_LO, l[k]);
+            }
             tmem_wait_ld(v);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+                float f[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 a = ns_unpack(w[k][i]);
-                    w[k][i] = ns_pack(fmaf(beta_b, a.x, alpha_b * __uint_as_float(v[8 * k + 2 * i])),
-                                      fmaf(beta_b, a.y, alpha_b * __uint_as_float(v[8 * k + 2 * i + 1])));
+                    const float2 a = ns_unpack(w[k][i]), r = ns_unpack(l[k][i]);
+                    f[2 * i] = fmaf(beta_b, a.x + r.x, alpha_b * __uint_as_float(v[8 * k + 2 * i]));
+                    f[2 * i + 1] = fmaf(beta_b, a.y + r.y, alpha_b * __uint_as_float(v[8 * k + 2 * i + 1]));
                 }
-                st_shared_v4(nr_addr(sA, row, col + 8 * k), w[k][0], w[k][1], w[k][2], w[k][3]);
+                put(nr_addr(sA, row, col + 8 * k), L::A_LO, f);
             }
         }
         // ---- X = a X + B X
-        multiply(sA, sX, true, width > 0 ? m_steps : 0, width > 0 ? width : 32);
+        multiply(sA, L::A_LO, sX, L::X_LO, true, width > 0 ? m_steps : 0, width > 0 ? width : 32);
 #pragma unroll
         for (int c = 0; c < XCH; ++c) {
             if ((2 * c + g) * 32 < ncol) {
@@ -511,11 +550,11 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
     }
 }
 
-template <int SIZE>
+template <int SIZE, int COLS>
 cudaError_t launch_resident(const NsResident& p, int batch, cudaStream_t stream, bool probe)
 {
-    using L = NrLayout<SIZE>;
-    auto kern = ns_resident_kernel<SIZE>;
+    using L = NrLayout<SIZE, COLS>;
+    auto kern = ns_resident_kernel<SIZE, COLS>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess)
@@ -562,31 +601,41 @@ cudaError_t launch_resident(const NsResident& p, int batch, cudaStream_t stream,
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
+// Columns of X for a block of a cluster: 192, what shared memory has room for
+// beside A and the staging buffer, as long as 16 blocks hold the matrix; beyond
+// that 256 with an exchange in halves, which costs two cluster barriers a step
+// more (128 x 4000 92 us; as separate launches 267).
+constexpr int NR_COLS = 192, NR_MAX_COLS = 256;
+
 cudaError_t launch_size(const NsResident& p, int size, int batch, cudaStream_t stream, bool probe)
 {
     switch (size) {
     case 1:
-        return launch_resident<1>(p, batch, stream, probe);
+        return launch_resident<1, NR_MAX_COLS>(p, batch, stream, probe);
     case 2:
-        return launch_resident<2>(p, batch, stream, probe);
+        return launch_resident<2, NR_COLS>(p, batch, stream, probe);
     case 4:
-        return launch_resident<4>(p, batch, stream, probe);
+        return launch_resident<4, NR_COLS>(p, batch, stream, probe);
     case 8:
-        return launch_resident<8>(p, batch, stream, probe);
+        return launch_resident<8, NR_COLS>(p, batch, stream, probe);
     default:
-        return launch_resident<16>(p, batch, stream, probe);
+        return p.n > 16 * NR_COLS ? launch_resident<16, NR_MAX_COLS>(p, batch, stream, probe)
+                                  : launch_resident<16, NR_COLS>(p, batch, stream, probe);
     }
 }
 
 // Blocks for one matrix, 0 where it does not fit a cluster.
 int resident_size(int rows, int cols)
 {
-    if (std::min(rows, cols) > 128)
+    const int m = std::min(rows, cols), n = std::max(rows, cols);
+    if (m > 128 || n > NR_MAX_SIZE * NR_MAX_COLS)
         return 0;
-    int size = 1;
-    while (size * NR_COLS < std::max(rows, cols) && size <= NR_MAX_SIZE)
+    if (n <= NR_MAX_COLS)
+        return 1;
+    int size = 2;
+    while (size < NR_MAX_SIZE && size * NR_COLS < n)
         size *= 2;
-    return size <= NR_MAX_SIZE ? size : 0;
+    return size;
 }
 
 }  // namespace
@@ -596,7 +645,9 @@ bool ns_resident_takes(const NsLaunch& l)
     const int size = resident_size(l.rows, l.cols);
     if (size == 0 || static_cast<long long>(l.batch) * size > 0x7fffffffLL)
         return false;
-    if (launch_size(NsResident{}, size, 1, nullptr, true) == cudaSuccess)
+    NsResident p{};
+    p.n = std::max(l.rows, l.cols);
+    if (launch_size(p, size, 1, nullptr, true) == cudaSuccess)
         return true;
     cudaGetLastError();  // a query that failed is not the separate launches' error
     return false;
