@@ -175,3 +175,46 @@ def test_more_steps_and_other_coefficients_in_fp32():
     g = draw(90, 700, "f32", "low rank", seed=53).cuda()
     expect_stated(tg.newton_schulz(g, steps=2), g, "f32", steps=2)
     _status()
+
+
+# --------------------------------------------- every size of the one-launch form
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [
+    (100, 256), (100, 257), (384, 65), (128, 500), (100, 1000), (1000, 100), (128, 2048), (2049, 65),
+    (37, 4096),           # 1, 2, 2, 4, 8, 8, 16, 16 and 16 blocks, the last in halves
+    (128, 3000), (3500, 128), (4096, 128),
+    (90, 1537), (1, 4000),    # 16 blocks of 112 columns, 2 of them without any; a single row
+    (4097, 128), (60, 5000)])  # no cluster holds these: separate launches
+def test_every_cluster_size(rows, cols, kind):
+    g = draw(rows, cols, "f32", kind, seed=rows + cols).cuda()
+    got = tg.newton_schulz(g)
+    again = tg.newton_schulz(g)
+    _status()
+    assert torch.equal(got, again)
+    expect_stated(got, g, "f32")
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(9, 64, 2500), (40, 1000, 50), (300, 90, 70), (3, 128, 3900)])
+def test_batches_of_clusters(batch, rows, cols):
+    """More clusters than fit at a time, and each matrix as if it were alone."""
+    g = torch.stack([draw(rows, cols, "f32", KINDS[i % 3], seed=i) for i in range(batch)]).cuda()
+    got = tg.newton_schulz(g, out_dtype="bf16")
+    _status()
+    for i in sorted({0, 1, batch // 2, batch - 1}):
+        assert torch.equal(got[i], tg.newton_schulz(g[i], out_dtype="bf16"))
+        expect_stated(got[i], g[i], "bf16")
+    x = g.clone()
+    assert torch.equal(tg.newton_schulz(x, out=x), tg.newton_schulz(g))     # in place
+    _status()
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 1000), (2049, 65), (128, 3900)])
+def test_clusters_with_unaligned_rows(rows, cols):
+    store = draw(rows + 2, cols + 5, "bf16", "flat", seed=61).cuda()
+    g = store[1:-1, 3:3 + cols]
+    out = torch.full((rows, cols + 3), 7.0, device="cuda")
+    tg.newton_schulz(g, out=out[:, 1:1 + cols])
+    _status()
+    expect_stated(out[:, 1:1 + cols], g, "f32")
+    assert torch.all(out[:, 0] == 7.0) and torch.all(out[:, 1 + cols:] == 7.0)
