@@ -1,9 +1,11 @@
 """Block-scaled 8-bit products, further forms: the block shapes of square
 operands, and every form of the kernel for few output tiles."""
+import numpy as np
 import pytest
 import torch
 
 import tiled_matrix_multiplication_output_gb300 as tg
+from tests.test_gpu_fp8 import DT, _expect, _product, _reference
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +90,83 @@ def test_nothing_is_stored_after_a_wait_that_runs_out(M, N, K):
     want = x.double() @ w.double().t()
     # both operands are rounded to four bits: half an ulp is 2^-4 of an element at worst
     assert ((C.double() - want).abs() <= 2 * 2.0 ** -4 * 1.1 * (x.abs().double() @ w.abs().double().t())).all()
+
+
+# ------------------------------------------- every form of the few-tiles kernel
+
+# (columns of a tile, blocks a tile's K is divided over, whether C's rows lie
+# along the tile's columns): the shorter side gives the columns, K the blocks
+FEW = [(1, 1024, 4096),      # 16, 8, no
+       (1, 4096, 4096),      # 16, 4, no
+       (16, 9000, 1000),     # 16, 2, no
+       (13, 18000, 600),     # 16, 1, no
+       (24, 512, 4096),      # 32, 8, no
+       (32, 1000, 1200),     # 32, 4, no
+       (20, 300, 600),       # 32, 2, no
+       (64, 512, 4096),      # 64, 8, no
+       (64, 2500, 2500),     # 64, 4, no
+       (50, 700, 1000),      # 64, 4, no
+       (60, 9001, 1000),     # 64, 2, no
+       (200, 257, 1100)]     # 64, 4, no; several columns of tiles
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("op_a,op_b,block_b", [("n", "t", "tile"), ("n", "n", "tile"), ("t", "n", "vector"),
+                                               ("t", "t", "vector")])
+@pytest.mark.parametrize("M,N,K", FEW + [(n, m, k) for m, n, k in FEW])
+def test_few_tiles_in_every_form(M, N, K, op_a, op_b, block_b, out):
+    """Integers (exact in FP32), then values of any size, with alpha alone and with beta."""
+    a, b = _product(M, N, K, op_a, op_b, "vector", block_b, integers=True, seed=M + K)
+    C = tg.matmul_fp8(*a[:2], *b[:2], op_a=op_a, op_b=op_b)
+    again = tg.matmul_fp8(*a[:2], *b[:2], op_a=op_a, op_b=op_b)
+    cref, _ = _reference(*a, op_a, *b, op_b)
+    np.testing.assert_array_equal(C.double().cpu().numpy(), cref)
+    assert torch.equal(C, again)
+    a, b = _product(M, N, K, op_a, op_b, "vector", block_b, "e5m2", seed=M + K + 1)
+    D = tg.matmul_fp8(*a[:2], *b[:2], op_a=op_a, op_b=op_b, out_dtype=out, alpha=0.5)
+    _expect(D, a, op_a, b, op_b, K, 0.5)
+    E = D.clone()
+    tg.matmul_fp8(*a[:2], *b[:2], op_a=op_a, op_b=op_b, out=E, alpha=-2.0, beta=0.25)
+    _status()
+    _expect(E, a, op_a, b, op_b, K, -2.0, 0.25, D.double().cpu().numpy())
+
+
+# ------------------------------------------------------------- alpha without beta
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(40, 512, 2000),        # few tiles
+                                   (300, 520, 640),        # 128 x 128 tiles
+                                   (2048, 4096, 512),      # CTA pairs
+                                   (2300, 2296, 640)])     # a last wave in parts
+@pytest.mark.parametrize("op_a,op_b,block_b", [("n", "t", "tile"), ("t", "n", "vector")])
+def test_alpha_into_aligned_outputs(M, N, K, op_a, op_b, block_b, out):
+    """Stored by TMA (but for few tiles), where alpha is the only factor."""
+    a, b = _product(M, N, K, op_a, op_b, "vector", block_b, seed=M)
+    if out == "f16":  # keep the results in its range
+        a = (a[0], a[1] * 2.0 ** -24, a[2])
+    C = torch.full((M, N), float("nan"), device="cuda", dtype=DT[out])
+    tg.matmul_fp8(*a[:2], *b[:2], op_a=op_a, op_b=op_b, out=C, alpha=0.375)
+    _status()
+    _expect(C, a, op_a, b, op_b, K, 0.375)
+
+
+# ------------------------------------------------------------------ in a graph
+
+def test_few_tiles_inside_a_cuda_graph():
+    """K of more than six blocks: the cluster kernel."""
+    def draws(seed):
+        g = torch.Generator().manual_seed(seed)
+        return torch.randn(48, 1500, generator=g).to(torch.bfloat16).cuda()
+
+    x, w = draws(1), torch.randn(264, 1500, device="cuda")
+    wq, ws = tg.quantize_fp8(w, block="tile")
+    tg.matmul_fp8(*tg.quantize_fp8(x), wq, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        xq, xs = tg.quantize_fp8(x)
+        C = tg.matmul_fp8(xq, xs, wq, ws)
+    x.copy_(draws(2))
+    g.replay()
+    torch.cuda.synchronize()
+    _expect(C, (xq, xs, "row"), "n", (wq, ws, "tile"), "t", 1500)
