@@ -84,7 +84,6 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
     Fp8Params p{};
     p.M = l.M;
     p.N = l.N;
-    p.K = l.K;
     p.tiles_m = (l.M + TC_BM * CG - 1) / (TC_BM * CG);
     p.tiles_n = (l.N + BN - 1) / BN;
     const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;

@@ -88,7 +88,7 @@ constexpr int F8_REGS_EPI = 216;
 static_assert(128 * F8_REGS_FEW + 256 * F8_REGS_EPI <= F8_THREADS * F8_REGS_LAUNCH, "register split");
 
 struct Fp8Params {
-    int M, N, K;
+    int M, N;
     int tiles_m, tiles_n;
     int whole;                     // tiles computed whole, an item each
     int items;                     // those and the parts: two for each further tile

@@ -40,7 +40,7 @@ constexpr int FS_EPI_WARP0 = 4;
 constexpr int FS_MAX_SPLITS = 8;
 
 struct Fp8SmallParams {
-    int rows, cols, K;             // of the tile's axes: rows of P, rows of Q
+    int rows, cols;                // of the tile's axes: rows of P, rows of Q
     int tiles_c;
     int k_blocks;
     uint32_t idesc;
@@ -475,12 +475,11 @@ cudaError_t launch_small(const Fp8Launch& l, bool swapped, cudaStream_t stream)
     Fp8SmallParams p{};
     p.rows = swapped ? l.N : l.M;
     p.cols = swapped ? l.M : l.N;
-    p.K = l.K;
     CUtensorMap tp, tq;
-    if (!encode_operand(&tp, P, p.rows, p.K, 128) || !encode_operand(&tq, Q, p.cols, p.K, BN))
+    if (!encode_operand(&tp, P, p.rows, l.K, 128) || !encode_operand(&tq, Q, p.cols, l.K, BN))
         return cudaErrorNotSupported;
     p.tiles_c = (p.cols + BN - 1) / BN;
-    p.k_blocks = (p.K + F8_BK - 1) / F8_BK;
+    p.k_blocks = (l.K + F8_BK - 1) / F8_BK;
     p.idesc = fp8_idesc(P.type, Q.type, 128, BN, P.mn_major, Q.mn_major);
     p.p_mn = P.mn_major;
     p.q_mn = Q.mn_major;

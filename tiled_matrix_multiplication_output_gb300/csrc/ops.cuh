@@ -96,13 +96,6 @@ __device__ __forceinline__ void fence_proxy_async_cluster()
     asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
 }
 
-// Order this thread's generic-proxy accesses, global memory included, with
-// async-proxy ones (TMA) on either side of a barrier.
-__device__ __forceinline__ void fence_proxy_async_all()
-{
-    asm volatile("fence.proxy.async;" ::: "memory");
-}
-
 // D[tmem] (+)= A[smem desc] * B[smem desc], kind::f8f6f4 (8-bit floating point in, F32 acc; K = 32 per
 // instruction).  The operands' types are in the instruction descriptor and
 // may differ.
