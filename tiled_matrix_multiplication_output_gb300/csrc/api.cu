@@ -18,7 +18,6 @@ namespace {
 // One status word per device (the watchdog of the tensor-core kernel).
 __device__ int g_status_word;
 
-constexpr int kMaxDevices = 64;
 constexpr long long kDefaultWaitBudget = 2000000000LL;  // ~1 s of SM clock
 
 std::atomic<long long> g_wait_budget{kDefaultWaitBudget};

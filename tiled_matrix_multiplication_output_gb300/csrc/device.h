@@ -8,6 +8,8 @@
 
 namespace tmmo {
 
+constexpr int kMaxDevices = 64;
+
 struct DeviceInfo {
     int num_sms = 0;
     int* status = nullptr;  // the device status word of the bounded waits

@@ -5,12 +5,12 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "device.h"
 #include "fp8_gemm.cuh"
 #include "fp8_launch.cuh"
+#include "persistent.cuh"
 
 namespace tmmo {
 namespace {
@@ -39,45 +39,12 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
 {
     using L = Fp8Layout<CG, BN, STAGES>;
     auto kern = fp8_gemm_kernel<CG, BN, STAGES, COLV>;
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    static ClusterCaps caps;
+    int units_cap = 0;
+    cudaError_t err = cluster_cap(kern, caps, CG, F8_THREADS, L::SMEM_ALLOC, l.num_sms, &units_cap);
     if (err != cudaSuccess)
         return err;
-    if (dev < 0 || dev >= kMaxDevices)
-        return cudaErrorInvalidDevice;
-    static int max_units[kMaxDevices] = {};
-    static std::mutex mu;
-    int units_cap = 0;
-    {
-        std::lock_guard<std::mutex> g(mu);
-        if (max_units[dev] == 0) {
-            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       L::SMEM_ALLOC);
-            if (err != cudaSuccess)
-                return err;
-            int cap = l.num_sms;
-            if (CG == 2) {
-                cudaLaunchConfig_t cfg{};
-                cudaLaunchAttribute attr[1];
-                attr[0].id = cudaLaunchAttributeClusterDimension;
-                attr[0].val.clusterDim.x = 2;
-                attr[0].val.clusterDim.y = 1;
-                attr[0].val.clusterDim.z = 1;
-                cfg.gridDim = dim3(2 * std::max(1, l.num_sms / 2), 1, 1);
-                cfg.blockDim = dim3(F8_THREADS, 1, 1);
-                cfg.dynamicSmemBytes = L::SMEM_ALLOC;
-                cfg.attrs = attr;
-                cfg.numAttrs = 1;
-                int clusters = 0;
-                err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-                if (err != cudaSuccess)
-                    return err;
-                cap = std::max(1, clusters);
-            }
-            max_units[dev] = cap;
-        }
-        units_cap = max_units[dev];
-    }
+    units_cap = std::max(1, units_cap);
     CUtensorMap ta, tb;
     if (!encode_operand(&ta, l.a, l.M, l.K, 128) || !encode_operand(&tb, l.b, l.N, l.K, 128 / L::SUB))
         return cudaErrorNotSupported;
@@ -124,21 +91,8 @@ cudaError_t launch_tiles(const Fp8Launch& l, cudaStream_t stream)
     p.whole = static_cast<int>(split ? tiles - last : tiles);
     p.items = static_cast<int>(split ? tiles + last : tiles);
     const int units = std::min(p.items, units_cap);
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(units * CG, 1, 1);
-    cfg.blockDim = dim3(F8_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = L::SMEM_ALLOC;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    note_launch();
-    err = cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, p);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    ClusterLaunch launch(static_cast<unsigned>(units * CG), CG, F8_THREADS, L::SMEM_ALLOC, stream);
+    return launch.run(kern, ta, tb, tc, p);
 }
 
 template <int CG, int BN, int STAGES>

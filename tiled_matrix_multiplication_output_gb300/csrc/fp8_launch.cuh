@@ -13,8 +13,6 @@
 namespace tmmo {
 namespace {
 
-constexpr int kMaxDevices = 64;
-
 inline int out_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
 
 // Whether the product can be stored by TMA: nothing to add to, rows on

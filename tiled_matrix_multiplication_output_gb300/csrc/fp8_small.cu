@@ -27,10 +27,10 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "fp8_gemm.cuh"
 #include "fp8_launch.cuh"
+#include "persistent.cuh"
 
 namespace tmmo {
 namespace {
@@ -452,24 +452,11 @@ cudaError_t launch_small(const Fp8Launch& l, bool swapped, cudaStream_t stream)
 {
     using L = Fp8SmallLayout<BN>;
     auto kern = fp8_small_kernel<BN, SPLITS>;
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    static ClusterCaps caps;
+    int cap = 0;
+    const cudaError_t err = cluster_cap(kern, caps, SPLITS, FS_THREADS, L::SMEM_ALLOC, l.num_sms, &cap);
     if (err != cudaSuccess)
         return err;
-    if (dev < 0 || dev >= kMaxDevices)
-        return cudaErrorInvalidDevice;
-    static bool prepared[kMaxDevices] = {};
-    static std::mutex mu;
-    {
-        std::lock_guard<std::mutex> g(mu);
-        if (!prepared[dev]) {
-            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       L::SMEM_ALLOC);
-            if (err != cudaSuccess)
-                return err;
-            prepared[dev] = true;
-        }
-    }
     const Fp8Operand& P = swapped ? l.b : l.a;
     const Fp8Operand& Q = swapped ? l.a : l.b;
     Fp8SmallParams p{};
@@ -504,21 +491,8 @@ cudaError_t launch_small(const Fp8Launch& l, bool swapped, cudaStream_t stream)
     const long long tiles = static_cast<long long>((p.rows + 127) / 128) * p.tiles_c;
     if (tiles * SPLITS > 0x7fffffffLL)
         return cudaErrorNotSupported;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = SPLITS;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * SPLITS), 1, 1);
-    cfg.blockDim = dim3(FS_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = L::SMEM_ALLOC;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = SPLITS > 1 ? 1 : 0;
-    note_launch();
-    err = cudaLaunchKernelEx(&cfg, kern, tp, tq, p);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    ClusterLaunch launch(static_cast<unsigned>(tiles * SPLITS), SPLITS, FS_THREADS, L::SMEM_ALLOC, stream);
+    return launch.run(kern, tp, tq, p);
 }
 
 template <int BN>

@@ -58,16 +58,14 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "launch.h"
 #include "newton_schulz.cuh"
 #include "newton_schulz.h"
+#include "persistent.cuh"
 
 namespace tmmo {
 namespace {
-
-constexpr int kMaxDevices = 64;
 
 constexpr int NS_THREADS = 320;   // warp 0: copies, 1: MMA, 2-9: epilogue
 constexpr int NS_EPI_WARP0 = 2;
@@ -802,45 +800,11 @@ cudaError_t ns_run(const NsMaps& a, const NsMaps& b, NsParams p, const NsOperand
 {
     using L = NsLayout<CG, BN, SPLIT, MODE == NS_LAST>;
     auto kern = ns_product_kernel<CG, BN, MODE, SPLIT>;
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    static ClusterCaps caps;
+    int units_cap = 0;
+    const cudaError_t err = cluster_cap(kern, caps, CG, NS_THREADS, L::SMEM_ALLOC, num_sms, &units_cap);
     if (err != cudaSuccess)
         return err;
-    if (dev < 0 || dev >= kMaxDevices)
-        return cudaErrorInvalidDevice;
-    static int max_units[kMaxDevices] = {};
-    static std::mutex mu;
-    int units_cap = 0;
-    {
-        std::lock_guard<std::mutex> g(mu);
-        if (max_units[dev] == 0) {
-            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       L::SMEM_ALLOC);
-            if (err != cudaSuccess)
-                return err;
-            int cap = num_sms;
-            if (CG == 2) {
-                cudaLaunchConfig_t cfg{};
-                cudaLaunchAttribute attr[1];
-                attr[0].id = cudaLaunchAttributeClusterDimension;
-                attr[0].val.clusterDim.x = 2;
-                attr[0].val.clusterDim.y = 1;
-                attr[0].val.clusterDim.z = 1;
-                cfg.gridDim = dim3(2 * std::max(1, num_sms / 2), 1, 1);
-                cfg.blockDim = dim3(NS_THREADS, 1, 1);
-                cfg.dynamicSmemBytes = L::SMEM_ALLOC;
-                cfg.attrs = attr;
-                cfg.numAttrs = 1;
-                int clusters = 0;
-                err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-                if (err != cudaSuccess)
-                    return err;
-                cap = std::max(1, clusters);
-            }
-            max_units[dev] = cap;
-        }
-        units_cap = max_units[dev];
-    }
     p.tiles_m = (p.M + TC_BM * CG - 1) / (TC_BM * CG);
     p.tiles_n = (p.N + BN - 1) / BN;
     const bool symmetric = MODE == NS_GRAM || MODE == NS_POLY;
@@ -853,23 +817,8 @@ cudaError_t ns_run(const NsMaps& a, const NsMaps& b, NsParams p, const NsOperand
     p.k_blocks = (p.K + NS_BK - 1) / NS_BK;
     p.idesc = tc_idesc(false, TC_BM * CG, BN, p.a_mn, p.b_mn);
     const int units = std::max(1, std::min(p.num_tiles, units_cap));
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(units * CG, 1, 1);
-    cfg.blockDim = dim3(NS_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = L::SMEM_ALLOC;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 2 : 1;
-    note_launch();
-    err = cudaLaunchKernelEx(&cfg, kern, a.hi, b.hi, a.lo, b.lo, p, o);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    ClusterLaunch launch(static_cast<unsigned>(units * CG), CG, NS_THREADS, L::SMEM_ALLOC, stream, true);
+    return launch.run(kern, a.hi, b.hi, a.lo, b.lo, p, o);
 }
 
 // 256 x 256 pair tiles once they fill half of the CTA pairs, 128 x 128 tiles

@@ -43,15 +43,14 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "newton_schulz.cuh"
 #include "newton_schulz.h"
+#include "persistent.cuh"
 
 namespace tmmo {
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int NR_THREADS = 256;
 constexpr int NR_MAX_SIZE = 16;  // blocks of a cluster
 
@@ -555,50 +554,17 @@ cudaError_t launch_resident(const NsResident& p, int batch, cudaStream_t stream,
 {
     using L = NrLayout<SIZE, COLS>;
     auto kern = ns_resident_kernel<SIZE, COLS>;
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    static ClusterCaps caps;
+    int cap = 0;
+    const cudaError_t err = cluster_cap(kern, caps, SIZE, NR_THREADS, L::SMEM_ALLOC, SIZE, &cap);
     if (err != cudaSuccess)
         return err;
-    if (dev < 0 || dev >= kMaxDevices)
-        return cudaErrorInvalidDevice;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = SIZE;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(batch) * SIZE, 1, 1);
-    cfg.blockDim = dim3(NR_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = L::SMEM_ALLOC;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = SIZE > 1 ? 1 : 0;
-    // Per device: 1 once prepared, -1 where no cluster of this size fits.
-    static int state[kMaxDevices] = {};
-    static std::mutex mu;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (state[dev] == 0) {
-            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_ALLOC);
-            if (err != cudaSuccess)
-                return err;
-            int clusters = 1;
-            if (SIZE > 8)
-                err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (err == cudaSuccess && SIZE > 1)
-                err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-            if (err != cudaSuccess)
-                return err;
-            state[dev] = clusters > 0 ? 1 : -1;
-        }
-        if (state[dev] < 0)
-            return cudaErrorNotSupported;
-    }
+    if (cap < 0)
+        return cudaErrorNotSupported;
     if (probe)
         return cudaSuccess;
-    note_launch();
-    err = cudaLaunchKernelEx(&cfg, kern, p);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    ClusterLaunch launch(static_cast<unsigned>(batch) * SIZE, SIZE, NR_THREADS, L::SMEM_ALLOC, stream);
+    return launch.run(kern, p);
 }
 
 // Columns of X for a block of a cluster: 192, what shared memory has room for
