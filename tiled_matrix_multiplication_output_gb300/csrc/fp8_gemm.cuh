@@ -37,15 +37,15 @@
 //     ahead, waited for the memory system: 1.2 times the time.
 //
 // What bounds it.  Measured on GB300, BF16 out, one vector of scales and one
-// of tiles: 8192 x 8192 x 4096 197 us (2.8 PFLOP/s, 0.73 of twice the
-// measured 16-bit burst rate), x 16384 760 us (2.9).  A K block takes 714
+// of tiles: 8192 x 8192 x 4096 200 us (198 to 214 by card; 2.7 PFLOP/s, 0.72 of
+// twice the measured 16-bit burst rate), x 16384 771 us (2.9).  A K block takes 714
 // cycles at the 1.8 GHz that the chip holds at this power: the shared memory
 // of an SM moves 80 KiB for it (32 written by TMA, A read once a group, B
 // once), 640 cycles.  A tile's end, when the sums go out and the MMAs wait
 // for free buffers, adds about 3000.  With two vectors of scales a thread
 // needs the scales of all its columns, 256 broadcast loads a K block and one
-// multiplication more a value: 1200 cycles (4096 x 4096 x 8192 141 us
-// against 106).  There the FP32 pipe and the registers' read ports count for
+// multiplication more a value: 1200 cycles (4096 x 4096 x 8192 141 to
+// 156 us against 106 to 113).  There the FP32 pipe and the registers' read ports count for
 // most: a packed multiplication and a multiply-add of three different
 // operands take 5.3 cycles (one with a shared factor 2.7), 680 a K block and
 // partition; without any load of scales it would still be 1130.

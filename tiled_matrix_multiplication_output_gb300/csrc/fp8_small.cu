@@ -18,10 +18,10 @@
 //     its ring holds 80 to 100 KiB, so that two blocks fit on an SM.
 //
 // The scaling of each K block's product is fp8_gemm_kernel's.  Measured on
-// GB300, BF16 out: one token against 8192 x 8192 weights 13.7 us (4.9 TB/s
-// with the launch, 0.72 of the measured copy bandwidth), 64 tokens 17.8; one
-// against 4096 x 4096 6.1 (7.0 with weights that are not in L2), of which a
-// launch alone is about 4.
+// GB300, BF16 out: one token against 8192 x 8192 weights 14.0 us (4.8 TB/s
+// with the launch, 0.71 of the measured copy bandwidth), 64 tokens 17.9; one
+// against 4096 x 4096 6.0 to 6.3 (7.1 to 7.4 with weights that are not in L2),
+// of which a launch alone is about 4.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>

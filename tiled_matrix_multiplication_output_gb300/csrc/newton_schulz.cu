@@ -18,13 +18,15 @@
 // Matrices with a short side of up to 128 are held on chip by a cluster, in
 // one launch (ns_resident.cu).  For the others every product is a launch,
 // and the launches are programmatic dependents of each other.  Large ones are
-// bound by the tensor pipe: 4096 x 4096 BF16 takes 1.01 ms for five steps,
-// 1360 TFLOP/s, where whole waves of tiles would take 0.73 (the two symmetric
+// bound by the tensor pipe: 4096 x 4096 BF16 takes 1.09 ms for five steps (1.04
+// in shorter runs, before the power cap sets in), 1260 TFLOP/s, where whole
+// waves of tiles would take 0.73 (the two symmetric
 // products run 136 tiles of 256 x 256 in two waves of 76 pairs, the update
 // 256 in four).  Small ones are bound by the latency of a product, about
 // 5.5 us whatever its size (0.95 from the end of one grid to the start of
 // the next, 1.45 to the first operands, 1 to 2 of MMAs, 0.6 to 1.1 of
-// epilogue): 8 x 1000 x 200 takes 104 us.
+// epilogue): 8 x 1000 x 200 takes 104 us.  With operands of two halves (FP32
+// results) 4096 x 4096 takes 2.8 ms, 8 x 1000 x 200 163 us.
 //
 // Numbers.  A singular value may start at 1e-4 of the norm and grow by
 // a factor of 3.4 a step, and so do rounding errors in its direction, so
@@ -930,7 +932,7 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
     n.wide = reinterpret_cast<double*>(ws + s.off_wide);
     // one group of 8 values a thread, more from NS_NORM_BLOCKS blocks on (with
     // four: 1024^2 151 us in all instead of 143; with at most 64 blocks 4096^2
-    // 1059 instead of 969)
+    // 1059 instead of 969; measured with X in two FP16 values)
     const int64_t groups = static_cast<int64_t>(l.rows) * n.groups;
     n.blocks = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(NS_NORM_BLOCKS, (groups + 511) / 512)));
