@@ -86,6 +86,27 @@ def test_nothing_is_stored_after_a_wait_that_runs_out(batch, rows, cols, product
         expect(out[i], g[i], "f32", steps=2)
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 200, 1000), (2, 700, 150), (1, 1900, 2300), (1, 256, 256)])
+def test_nothing_is_stored_after_a_product_that_did_not_finish(batch, rows, cols, out):
+    """Separate launches: the copies of one K step are left out, one that only the
+    products over the longer side have (the last: every product)."""
+    g = torch.stack([draw(rows, cols, "f32", "flat", seed=45 + i) for i in range(batch)]).cuda()
+    res = torch.full_like(g, 5.0, dtype=DT[out])
+    tg.gemm_debug_config(20_000_000, (max(rows, cols) - 1) // 64)
+    try:
+        tg.newton_schulz(g, steps=2, out=res)
+        sh = torch.cuda.current_stream().cuda_stream
+        assert tg.gemm_device_status(sh) == tg.binding.ERR_TIMEOUT
+    finally:
+        tg.gemm_debug_config(0, -1)
+    assert torch.all(res == 5.0)
+    tg.newton_schulz(g, steps=2, out=res)
+    _status()
+    for i in range(batch):
+        expect_stated(res[i], g[i], out, steps=2)
+
+
 # ------------------------------------------------------------ extreme norms
 
 # one-launch form on one block and on clusters, separate launches

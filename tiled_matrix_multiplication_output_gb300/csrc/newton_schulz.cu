@@ -96,6 +96,7 @@ struct NsParams {
     long long ld_res, batch_res;
     bool vec_res;                  // its rows are on 16-byte boundaries
     int out_dtype;
+    int* gave_up;                  // set by a product that did not finish; then no result is stored
     int* status;
     long long wait_budget;
     int fault_skip_kblock;
@@ -259,6 +260,7 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands&
                                             int row, int col0, uint32_t taddr, uint32_t stg, Wait&& wait)
 {
     const bool inside = row < p.M;
+    const bool stored = MODE != NS_LAST || *p.gave_up == 0;  // (asked for ahead of the wait)
     const long long at0 = z * p.batch_pitch + row * p.ld + col0;
     uint32_t add[2][32];  // FP32; of A 16 words of hi, then of lo
     auto fetch = [&](int c, int b) {  // the addend of chunk c
@@ -282,7 +284,7 @@ __device__ __forceinline__ void ns_epilogue(const NsParams& p, const NsOperands&
     };
     fetch(0, 0);
     fetch(1, 1);
-    if (!wait())
+    if (!wait() || !stored)
         return;
     tc_fence_after();
 #pragma unroll 1
@@ -621,6 +623,8 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
         __syncwarp();
         tmem_dealloc<CG>(tmem_base, L::TMEM_COLS);
     }
+    if (threadIdx.x == 0 && *abort_flag)
+        *p.gave_up = 1;
 }
 
 // ------------------------------------------------------------ normalisation
@@ -631,6 +635,7 @@ struct NsNorm {
     int rows, cols, groups;        // groups of 8 columns per row
     float* partial;                // [batch][blocks]
     double* wide;                  // the same, for the sums that FP32 does not hold
+    int* gave_up;                  // cleared here
     int blocks;
     float eps;
     float* x;
@@ -701,8 +706,11 @@ __global__ void __launch_bounds__(512) ns_norm_kernel(const NsNorm p)
     const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
     const long long at = static_cast<long long>(blockIdx.y) * p.blocks + blockIdx.x;
     const float s = ns_block_sum(ns_square_sum<InT, float>(p, blockIdx.y, first, step));
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
         p.partial[at] = s;
+        if (at == 0)
+            *p.gave_up = 0;
+    }
     if (!ns_squares_fit(s)) {  // (the same for the whole block)
         const double wide = ns_block_sum(ns_square_sum<InT, double>(p, blockIdx.y, first, step));
         if (threadIdx.x == 0)
@@ -743,7 +751,7 @@ int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 struct NsSpace {
     int64_t m, ld_x, ld_a;
     int64_t x, a;                   // elements of one matrix
-    size_t off_x, off_hi[2], off_lo[2], off_a[2], off_b[2], off_partial, off_wide, bytes;
+    size_t off_x, off_hi[2], off_lo[2], off_a[2], off_b[2], off_partial, off_wide, off_gave_up, bytes;
 };
 
 NsSpace ns_space(int64_t batch, int64_t rows, int64_t cols)
@@ -769,6 +777,7 @@ NsSpace ns_space(int64_t batch, int64_t rows, int64_t cols)
     }
     s.off_partial = take(batch * NS_NORM_BLOCKS * 4);
     s.off_wide = take(batch * NS_NORM_BLOCKS * 8);
+    s.off_gave_up = take(4);
     s.bytes = at;
     return s;
 }
@@ -916,6 +925,7 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
         p.batch_res = l.batch_o;
         p.vec_res = ns_vec_rows(l);
         p.out_dtype = l.out_dtype;
+        p.gave_up = reinterpret_cast<int*>(ws + s.off_gave_up);
         p.status = l.status;
         p.wait_budget = l.wait_budget;
         p.fault_skip_kblock = l.fault_skip_kblock;
@@ -930,6 +940,7 @@ cudaError_t ns_launch(const NsLaunch& l, cudaStream_t stream)
     n.groups = (l.cols + 7) / 8;
     n.partial = reinterpret_cast<float*>(ws + s.off_partial);
     n.wide = reinterpret_cast<double*>(ws + s.off_wide);
+    n.gave_up = reinterpret_cast<int*>(ws + s.off_gave_up);
     // one group of 8 values a thread, more from NS_NORM_BLOCKS blocks on (with
     // four: 1024^2 151 us in all instead of 143; with at most 64 blocks 4096^2
     // 1059 instead of 969; measured with X in two FP16 values)
