@@ -11,6 +11,7 @@ namespace {
 cudaError_t g_last = cudaSuccess;
 cudaError_t g_query = cudaSuccess;
 int g_clusters = 1;
+int g_failures = 1 << 30;  // the queries that fail before they work again
 
 cudaError_t note(cudaError_t err)
 {
@@ -30,7 +31,7 @@ cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) { return c
 cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunchConfig_t*)
 {
     *n = g_clusters;
-    return note(g_query);
+    return g_failures-- > 0 ? note(g_query) : cudaSuccess;
 }
 cudaError_t cudaGetLastError()
 {
@@ -77,6 +78,14 @@ int main()
     if (tmmo::ns_resident_takes(l) || tmmo::ns_resident_takes(l) || g_last != cudaSuccess) {
         std::printf("no cluster fits: last error %d\n", static_cast<int>(g_last));
         return 3;
+    }
+    l.cols = 1000;          // two forms to choose from: the first query fails, then all work
+    g_clusters = 1;
+    g_query = cudaErrorInvalidValue;
+    g_failures = 1;
+    if (!tmmo::ns_resident_takes(l) || g_last != cudaSuccess) {
+        std::printf("one of two queries failed: last error %d\n", static_cast<int>(g_last));
+        return 4;
     }
     std::printf("ok\n");
     return 0;

@@ -216,14 +216,16 @@ def test_every_cluster_size(rows, cols, kind):
     expect_stated(got, g, "f32")
 
 
-@pytest.mark.parametrize("batch,rows,cols", [(9, 64, 2500), (40, 1000, 50), (300, 90, 70), (3, 128, 3900)])
+@pytest.mark.parametrize("batch,rows,cols", [(9, 64, 2500), (40, 1000, 50), (300, 90, 70), (16, 128, 1024),
+                                             (64, 400, 16), (24, 16, 2000), (3, 128, 3900)])
 def test_batches_of_clusters(batch, rows, cols):
-    """More clusters than fit at a time, and each matrix as if it were alone."""
+    """More clusters than fit at a time, some with 256 columns a block, which alone
+    they would not have, and the same result wherever in the batch a matrix is."""
     g = torch.stack([draw(rows, cols, "f32", KINDS[i % 3], seed=i) for i in range(batch)]).cuda()
     got = tg.newton_schulz(g, out_dtype="bf16")
     _status()
+    assert torch.equal(tg.newton_schulz(g.roll(1, 0), out_dtype="bf16").roll(-1, 0), got)
     for i in sorted({0, 1, batch // 2, batch - 1}):
-        assert torch.equal(got[i], tg.newton_schulz(g[i], out_dtype="bf16"))
         expect_stated(got[i], g[i], "bf16")
     x = g.clone()
     assert torch.equal(tg.newton_schulz(x, out=x), tg.newton_schulz(g))     # in place

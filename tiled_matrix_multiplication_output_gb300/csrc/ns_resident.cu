@@ -60,6 +60,7 @@ struct NsResident {
     // element (i, j) of X at G[z * batch_g + i * row_g + j * col_g], and so in O
     long long batch_g, row_g, col_g, batch_o, row_o, col_o;
     int m, n;
+    int num_sms;
     int share;                     // columns of X per block
     bool vec_o;                    // O's rows are on 16-byte boundaries
     int in_dtype, out_dtype;
@@ -549,71 +550,110 @@ __global__ void __launch_bounds__(NR_THREADS, 1) ns_resident_kernel(const __grid
     }
 }
 
+// Launches a batch; with `clusters` only says how many of them run at a time.
 template <int SIZE, int COLS>
-cudaError_t launch_resident(const NsResident& p, int batch, cudaStream_t stream, bool probe)
+cudaError_t launch_resident(const NsResident& p, int batch, cudaStream_t stream, int* clusters)
 {
     using L = NrLayout<SIZE, COLS>;
     auto kern = ns_resident_kernel<SIZE, COLS>;
     static ClusterCaps caps;
     int cap = 0;
-    const cudaError_t err = cluster_cap(kern, caps, SIZE, NR_THREADS, L::SMEM_ALLOC, SIZE, &cap);
+    const cudaError_t err = cluster_cap(kern, caps, SIZE, NR_THREADS, L::SMEM_ALLOC, p.num_sms, &cap);
     if (err != cudaSuccess)
         return err;
     if (cap < 0)
         return cudaErrorNotSupported;
-    if (probe)
+    if (clusters) {
+        *clusters = cap;
         return cudaSuccess;
+    }
     ClusterLaunch launch(static_cast<unsigned>(batch) * SIZE, SIZE, NR_THREADS, L::SMEM_ALLOC, stream);
     return launch.run(kern, p);
 }
 
 // Columns of X for a block of a cluster: 192, what shared memory has room for
-// beside A and the staging buffer, as long as 16 blocks hold the matrix; beyond
-// that 256 with an exchange in halves, which costs two cluster barriers a step
-// more (128 x 4000 92 us; as separate launches 267).
+// beside A and the staging buffer, or 256 with an exchange in halves, which
+// costs two cluster barriers a step more.
 constexpr int NR_COLS = 192, NR_MAX_COLS = 256;
 
-cudaError_t launch_size(const NsResident& p, int size, int batch, cudaStream_t stream, bool probe)
+struct NrForm {
+    int size = 0, cols = 0;  // blocks for one matrix (0: no cluster holds it), columns for a block
+};
+
+template <int COLS>
+cudaError_t launch_cluster(const NsResident& p, int size, int batch, cudaStream_t stream, int* clusters)
 {
     switch (size) {
-    case 1:
-        return launch_resident<1, NR_MAX_COLS>(p, batch, stream, probe);
     case 2:
-        return launch_resident<2, NR_COLS>(p, batch, stream, probe);
+        return launch_resident<2, COLS>(p, batch, stream, clusters);
     case 4:
-        return launch_resident<4, NR_COLS>(p, batch, stream, probe);
+        return launch_resident<4, COLS>(p, batch, stream, clusters);
     case 8:
-        return launch_resident<8, NR_COLS>(p, batch, stream, probe);
+        return launch_resident<8, COLS>(p, batch, stream, clusters);
     default:
-        return p.n > 16 * NR_COLS ? launch_resident<16, NR_MAX_COLS>(p, batch, stream, probe)
-                                  : launch_resident<16, NR_COLS>(p, batch, stream, probe);
+        return launch_resident<16, COLS>(p, batch, stream, clusters);
     }
 }
 
-// Blocks for one matrix, 0 where it does not fit a cluster.
-int resident_size(int rows, int cols)
+cudaError_t launch_form(const NsResident& p, NrForm f, int batch, cudaStream_t stream, int* clusters)
 {
-    const int m = std::min(rows, cols), n = std::max(rows, cols);
-    if (m > 128 || n > NR_MAX_SIZE * NR_MAX_COLS)
-        return 0;
-    if (n <= NR_MAX_COLS)
-        return 1;
-    int size = 2;
-    while (size < NR_MAX_SIZE && size * NR_COLS < n)
-        size *= 2;
-    return size;
+    if (f.size == 1)
+        return launch_resident<1, NR_MAX_COLS>(p, batch, stream, clusters);
+    return f.cols == NR_COLS ? launch_cluster<NR_COLS>(p, f.size, batch, stream, clusters)
+                             : launch_cluster<NR_MAX_COLS>(p, f.size, batch, stream, clusters);
+}
+
+// The form for a batch.  One matrix alone takes 1.1 to 1.25 times as long with
+// 256 columns a block as with twice the blocks (64 x 512 61 us / 51, 64 x 1000
+// 70 / 57, 128 x 2000 82 / 74), but of those fewer run at a time: 16 x 128 x
+// 1024 78 / 122, 64 x 16 x 2000 344 / 607.  So: 256 where it takes at most four
+// fifths of the waves, or where 16 blocks of 192 do not hold the matrix
+// (128 x 4000 92 us; as separate launches 267).
+NrForm resident_form(const NsResident& p, int batch)
+{
+    if (p.m > 128 || p.n > NR_MAX_SIZE * NR_MAX_COLS)
+        return {};
+    if (p.n <= NR_MAX_COLS)
+        return {1, NR_MAX_COLS};
+    auto with = [&](int cols) {
+        NrForm f{2, cols};
+        while (f.size * cols < p.n)
+            f.size *= 2;
+        return f;
+    };
+    const NrForm narrow = with(NR_COLS), wide = with(NR_MAX_COLS);
+    if (narrow.size > NR_MAX_SIZE)
+        return wide;
+    if (narrow.size == wide.size)
+        return narrow;
+    int few = 0, many = 0;
+    if (launch_form(p, wide, batch, nullptr, &few) != cudaSuccess ||
+        launch_form(p, narrow, batch, nullptr, &many) != cudaSuccess) {
+        cudaGetLastError();  // whether the form chosen fits is asked once more
+        return narrow;
+    }
+    const long long wide_waves = (batch + few - 1) / few, narrow_waves = (batch + many - 1) / many;
+    return 5 * wide_waves <= 4 * narrow_waves ? wide : narrow;
+}
+
+NsResident resident_params(const NsLaunch& l)
+{
+    NsResident p{};
+    p.m = std::min(l.rows, l.cols);
+    p.n = std::max(l.rows, l.cols);
+    p.num_sms = l.num_sms;
+    return p;
 }
 
 }  // namespace
 
 bool ns_resident_takes(const NsLaunch& l)
 {
-    const int size = resident_size(l.rows, l.cols);
-    if (size == 0 || static_cast<long long>(l.batch) * size > 0x7fffffffLL)
-        return false;
-    NsResident p{};
-    p.n = std::max(l.rows, l.cols);
-    if (launch_size(p, size, 1, nullptr, true) == cudaSuccess)
+    const NsResident p = resident_params(l);
+    const NrForm form = resident_form(p, l.batch);
+    int clusters = 0;
+    if (form.size > 0 && static_cast<long long>(l.batch) * form.size <= 0x7fffffffLL &&
+        launch_form(p, form, l.batch, nullptr, &clusters) == cudaSuccess)
         return true;
     cudaGetLastError();  // a query that failed is not the separate launches' error
     return false;
@@ -621,9 +661,9 @@ bool ns_resident_takes(const NsLaunch& l)
 
 cudaError_t ns_resident_launch(const NsLaunch& l, cudaStream_t stream)
 {
-    const int size = resident_size(l.rows, l.cols);
     const bool tall = l.rows > l.cols;
-    NsResident p{};
+    NsResident p = resident_params(l);
+    const NrForm form = resident_form(p, l.batch);
     p.G = l.G;
     p.O = l.O;
     p.batch_g = l.batch_g;
@@ -632,9 +672,7 @@ cudaError_t ns_resident_launch(const NsLaunch& l, cudaStream_t stream)
     p.col_g = tall ? l.ldg : 1;
     p.row_o = tall ? 1 : l.ldo;
     p.col_o = tall ? l.ldo : 1;
-    p.m = std::min(l.rows, l.cols);
-    p.n = std::max(l.rows, l.cols);
-    p.share = ((p.n + size - 1) / size + 15) / 16 * 16;
+    p.share = ((p.n + form.size - 1) / form.size + 15) / 16 * 16;
     p.vec_o = ns_vec_rows(l);
     p.in_dtype = l.in_dtype;
     p.out_dtype = l.out_dtype;
@@ -644,7 +682,7 @@ cudaError_t ns_resident_launch(const NsLaunch& l, cudaStream_t stream)
     p.status = l.status;
     p.wait_budget = l.wait_budget;
     p.fault_skip = l.fault_skip_kblock;
-    return launch_size(p, size, l.batch, stream, false);
+    return launch_form(p, form, l.batch, stream, nullptr);
 }
 
 }  // namespace tmmo
