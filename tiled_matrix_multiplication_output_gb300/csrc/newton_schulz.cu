@@ -20,13 +20,13 @@
 // and the launches are programmatic dependents of each other.  Large ones are
 // bound by the tensor pipe: 4096 x 4096 BF16 takes 1.09 ms for five steps (1.04
 // in shorter runs, before the power cap sets in), 1260 TFLOP/s, where whole
-// waves of tiles would take 0.73 (the two symmetric
-// products run 136 tiles of 256 x 256 in two waves of 76 pairs, the update
-// 256 in four).  Small ones are bound by the latency of a product, about
-// 5.5 us whatever its size (0.95 from the end of one grid to the start of
-// the next, 1.45 to the first operands, 1 to 2 of MMAs, 0.6 to 1.1 of
-// epilogue): 8 x 1000 x 200 takes 104 us.  With operands of two halves (FP32
-// results) 4096 x 4096 takes 2.8 ms, 8 x 1000 x 200 163 us.
+// waves of tiles would take 0.73 (the two symmetric products run 136 tiles of
+// 256 x 256 in two waves of 76 pairs, the update 256 in four).  Small ones are
+// bound by the latency of a product, about 5.5 us whatever its size (0.95 from
+// the end of one grid to the start of the next, 1.45 to the first operands, 1
+// to 2 of MMAs, 0.6 to 1.1 of epilogue): 8 x 1000 x 200 takes 104 us.  With
+// operands of two halves (FP32 results) 4096 x 4096 takes 2.8 ms,
+// 8 x 1000 x 200 163 us.
 //
 // Numbers.  A singular value may start at 1e-4 of the norm and grow by
 // a factor of 3.4 a step, and so do rounding errors in its direction, so
@@ -43,10 +43,11 @@
 //     tried, 1.3e-3 for a few strong directions over a noise floor, before the
 //     result's own rounding, which is 1.66e-3 over all elements;
 //   * FP32 and FP16 results, and those with a short side of up to 128, where
-//     one value would be up to 2.3e-3 off: two FP16 values, hi + lo, 22 bits, and
+//     one value would be up to 7e-3 off: two FP16 values, hi + lo, 22 bits, and
 //     three products (hi hi + hi lo + lo hi) in one accumulator, for three
-//     times the MMAs.  1e-6 to 5e-5 off, growing with the length of the
-//     contractions, whose sums the tensor core truncates to FP32 every 16 of K.
+//     times the MMAs.  1e-6 to 5e-5 off for sides of up to 4096, growing with
+//     the length of the contractions, whose sums the tensor core truncates to
+//     FP32 every 16 of K.
 //     The next rounding down, TF32, has FP16's ten bits at half its rate.
 //
 // FP16 rather than BF16 for its three more bits at the same rate;

@@ -41,8 +41,8 @@ inline bool ns_vec_rows(const NsLaunch& l)
 // With one the result is up to 2e-3 off exact arithmetic (relative, over all
 // elements), about what rounding it to BF16 does (1.66e-3), for a third of the
 // MMAs.  So: two where the result has more bits, and for a short side of up to
-// 128, where one would be up to 2.3e-3 off (and the one-launch form is bound by
-// latency).
+// 128, where one would be 2e-3 off and for the narrowest up to 7e-3 (and the
+// one-launch form is bound by latency).
 inline bool ns_split(const NsLaunch& l)
 {
     return l.out_dtype != DT_BF16 || l.rows <= 128 || l.cols <= 128;

@@ -18,9 +18,9 @@
 //     MN-major one of B X;
 //   * operands are two FP16 values an element, hi + lo, and a product is
 //     hi hi + hi lo + lo hi in one accumulator, whatever the result's type:
-//     with one value matrices as narrow as these would be up to 2.3e-3 off,
-//     more than a BF16 result's own rounding (1.66e-3).  It costs 15 us a call
-//     (128 x 128 36 us instead of 21);
+//     with one value matrices as narrow as these would be 2e-3 off and the
+//     narrowest up to 7e-3, more than a BF16 result's own rounding (1.66e-3).
+//     It costs 15 us a call (128 x 128 36 us instead of 21);
 //   * A and B share one buffer: each thread replaces its elements of A by
 //     those of B once the product A A is complete, and every block computes
 //     all of B for itself;
