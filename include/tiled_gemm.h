@@ -451,7 +451,11 @@ int gemm_fp8(const gemm_fp8_matrix_t* A, const gemm_fp8_matrix_t* B, void* C, in
  * is within 2e-3 (relative, in the 2-norm of all elements) of the definition
  * in exact arithmetic, before its own rounding, which is 1.7e-3.  F32 and F16,
  * and every type where a side is at most 128: two FP16 values, 22 bits; within
- * 1e-5 + max(rows, cols) * 2^-25, for up to three times the time.
+ * 1e-5 + max(rows, cols) * 2^-25, for up to three times the time.  Both
+ * figures are for up to five steps of (3.4445, -4.7750, 2.0315), whose singular
+ * values keep moving, so that every further step adds to the error (twelve
+ * steps: 4.5e-3 and 1.5 times the second figure); coefficients that converge
+ * stay within them.
  * Singular values must stay below 4 and |b s^2 + c s^4| below 32 throughout,
  * the range of the FP16 operands, as they do for coefficients that converge;
  * beyond it the result is not finite.  A G whose norm is not finite in FP32

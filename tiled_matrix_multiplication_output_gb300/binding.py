@@ -697,7 +697,8 @@ def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, ep
     PyTorch unless given.  Accuracy goes by the result's type: BF16 results are
     within 2e-3 of exact arithmetic before they are rounded (1.7e-3), FP32 and
     FP16 ones (and all with a side of up to 128) within about 1e-5, for up to
-    three times the time; see gemm_newton_schulz in the header.
+    three times the time, for five steps of the default coefficients; see
+    gemm_newton_schulz in the header.
     Returns the result without synchronizing."""
     batch, rows, cols, ldg, stride_g = _check_batch(G, "G")
     if not 1 <= steps <= 32:
