@@ -479,6 +479,144 @@ int gemm_newton_schulz(const void* G, int64_t ldg, int64_t batch_stride_g, void*
                        const float* coefficients, float eps, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* --------------------------------------------- products grouped by rows
+ *
+ * Rows that choose their weight: the rows of X are sorted by group, and group
+ * g, the rows [offsets[g], offsets[g + 1]), is multiplied by its own matrix
+ * W[g] -- the experts of a mixture, with any number of rows each.  The
+ * offsets lie in device memory (a router makes them there), so the host
+ * never learns a group's size.  The pages have no counterpart.
+ *
+ * `offsets`: groups + 1 values, ascending, within [0, rows].  Whatever they
+ * hold, no group reads or writes beyond `rows`, and groups do not overlap: a
+ * value counts as the largest of those up to it.  At most GEMM_MAX_GROUPS
+ * groups.  Products are accumulated in FP32; alpha and beta are applied
+ * in FP32 before the one rounding to out_dtype, beta == 0 never reads the
+ * output.  Rows of no group are not read.  F16, BF16 (tensor cores) and F32
+ * operands; any out_dtype.  Results are identical run to run.
+ */
+#define GEMM_MAX_GROUPS 1024
+
+/*
+ * gemm_grouped -- Y = alpha * X op(W[g]) + beta * Y, for the rows of each g.
+ *
+ * X is rows x K (row pitch ldx elements), Y rows x N (pitch ldy), op(W[g])
+ * K x N: W[g] starts stride_w elements behind W[g - 1] and is stored K x N
+ * (GEMM_OP_N) or N x K (GEMM_OP_T) with row pitch ldw.  With W stored
+ * out x in, GEMM_OP_T is the layer and GEMM_OP_N the gradient of its input.
+ * stride_w == 0 uses one matrix throughout.  Rows of no group (before the
+ * first offset, behind the last) are left as they were, or with zero_rest
+ * != 0 set to zero.  K == 0 gives beta * Y.  Y must not overlap X or W.
+ *
+ * Element alignment is enough.  16-bit operands whose pointer, pitch or
+ * stride is not a multiple of 16 bytes are copied to aligned rows first, into
+ * `workspace`: gemm_grouped_workspace_size() bytes of device memory for these
+ * very operands, 0 where none is needed; 256-byte aligned, and not shared
+ * by calls that overlap in time.
+ *
+ * Returns GEMM_OK, GEMM_ERR_INVALID_VALUE (null pointer where data is
+ * needed, bad size, pitch, stride or enum, workspace missing, misaligned or
+ * too small), GEMM_ERR_UNSUPPORTED (more than GEMM_MAX_GROUPS groups) or
+ * GEMM_ERR_CUDA.
+ */
+size_t gemm_grouped_workspace_size(const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                   int64_t stride_w, int64_t rows, int64_t groups, int64_t N,
+                                   int64_t K, gemm_op_t op_w, gemm_dtype_t in_dtype);
+int gemm_grouped(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t stride_w,
+                 gemm_op_t op_w, const int32_t* offsets, void* Y, int64_t ldy, int64_t rows,
+                 int64_t groups, int64_t N, int64_t K, float alpha, float beta, int zero_rest,
+                 gemm_dtype_t in_dtype, gemm_dtype_t out_dtype, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/*
+ * gemm_grouped_wgrad -- C[g] = alpha * D_g^T X_g + beta * C[g], D_g and X_g
+ * the rows of group g: the gradient of W[g] (stored out x in) from the
+ * output's gradient D and the input X.
+ *
+ * D is rows x N (pitch ldd), X rows x K (pitch ldx), C[g] N x K (pitch ldc)
+ * and stride_c elements behind C[g - 1] (matrices must not overlap).  A group
+ * without rows gives beta * C[g] (zeros for beta == 0).  Workspace, alignment
+ * and errors as gemm_grouped.
+ */
+size_t gemm_grouped_wgrad_workspace_size(const void* D, int64_t ldd, const void* X, int64_t ldx,
+                                         int64_t rows, int64_t N, int64_t K,
+                                         gemm_dtype_t in_dtype);
+int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int64_t ldx,
+                       const int32_t* offsets, void* C, int64_t ldc, int64_t stride_c,
+                       int64_t rows, int64_t groups, int64_t N, int64_t K, float alpha, float beta,
+                       gemm_dtype_t in_dtype, gemm_dtype_t out_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------ low-rank adapters
+ *
+ * One weight W (N x K, out x in) shared by all rows, and beside it for each
+ * row i, if adapter[i] = g is one of the `adapters`, a change of low rank:
+ *
+ *     Y_i = X_i W^T + scale[g] (X_i A[g]^T) B[g]^T
+ *
+ * A[g] is rank x K and B[g] N x rank (pitches lda and ldb, strides from one
+ * adapter to the next, in elements).  The rows of different adapters may come
+ * in any order; a row whose adapter[i] lies outside [0, adapters) has none.  No
+ * row sees anything of another row's adapter, not even of one that is not
+ * finite.  scale: device memory, one for each adapter, or null for 1.  rank
+ * at most GEMM_MAX_RANK.  The pages have no counterpart.
+ *
+ * The rank values scale * X_i A^T are FP32 sums.  On the tensor cores they
+ * enter the second product in parts of the operands' type that together hold
+ * at least 16 bits of them (24 for BF16, 22 for FP16 where the result is
+ * F32); with FP16 operands they must stay within FP16's range.  All sums are
+ * FP32, with one rounding to the output's type.  Results are identical run
+ * to run.  Types, alignment and pitches as gemm_grouped.
+ */
+#define GEMM_MAX_RANK 256
+
+typedef struct {
+    const void* A;     /* adapters of rank x K */
+    int64_t lda, stride_a;
+    const void* B;     /* adapters of N x rank */
+    int64_t ldb, stride_b;
+    const float* scale;
+    int64_t adapters, rank;
+} gemm_lora_t;
+
+/*
+ * gemm_lora -- the forward product above.  X is rows x K, Y rows x N.
+ *
+ * workspace: device memory of gemm_lora_workspace_size() bytes, which serves
+ * any operands of these sizes; 256-byte aligned, not shared by calls that
+ * overlap in time.  Returns GEMM_OK, GEMM_ERR_INVALID_VALUE (null pointer
+ * where data is needed, bad size, pitch, stride or enum, workspace missing,
+ * misaligned or too small), GEMM_ERR_UNSUPPORTED (rank above GEMM_MAX_RANK)
+ * or GEMM_ERR_CUDA.
+ */
+size_t gemm_lora_workspace_size(int64_t rows, int64_t N, int64_t K, int64_t adapters,
+                                int64_t rank);
+int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw, const gemm_lora_t* lora,
+              const int32_t* adapter, void* Y, int64_t ldy, int64_t rows, int64_t N, int64_t K,
+              gemm_dtype_t in_dtype, gemm_dtype_t out_dtype, void* workspace,
+              size_t workspace_bytes, void* stream);
+
+/*
+ * gemm_lora_backward -- the gradients of gemm_lora from D = dY (rows x N),
+ * with u_i = scale[g] D_i B[g] and t_i = scale[g] X_i A[g]^T:
+ *
+ *     DX_i = D_i W + u_i A[g]        (rows x K, out_dtype)
+ *     DA[g] = sum of u_i^T X_i       (rank x K, grad_dtype)   over the rows
+ *     DB[g] = sum of D_i^T t_i       (N x rank, grad_dtype)   of adapter g
+ *
+ * W is frozen.  DX, DA or DB null: not computed (X is needed for DA and DB
+ * only, W for DX only).  Adapters without rows get zeros.  workspace of
+ * gemm_lora_backward_workspace_size() bytes.  Errors as gemm_lora.
+ */
+size_t gemm_lora_backward_workspace_size(int64_t rows, int64_t N, int64_t K, int64_t adapters,
+                                         int64_t rank);
+int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int64_t ldx, const void* W,
+                       int64_t ldw, const gemm_lora_t* lora, const int32_t* adapter, void* DX,
+                       int64_t lddx, void* DA, int64_t ldda, int64_t stride_da, void* DB,
+                       int64_t lddb, int64_t stride_db, int64_t rows, int64_t N, int64_t K,
+                       gemm_dtype_t in_dtype, gemm_dtype_t out_dtype, gemm_dtype_t grad_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * gemm_device_status -- synchronize `stream`, then read and clear the status
  * word of the current device.  Returns GEMM_OK, GEMM_ERR_TIMEOUT if a

@@ -1,0 +1,109 @@
+"""Host-side checks of the grouped products and the adapters that need no GPU:
+bad arguments are rejected before a device is touched, empty problems are
+no-ops."""
+import pytest
+import torch
+
+import tiled_matrix_multiplication_output_gb300 as tg
+from tiled_matrix_multiplication_output_gb300 import build as tgbuild
+
+INV, UNS = tg.binding.ERR_INVALID_VALUE, tg.binding.ERR_UNSUPPORTED
+BIG = tg.binding.MAX_DIM
+P = 4096  # a dummy aligned address; never dereferenced on these paths
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if tgbuild.nvcc_path() is None:
+        pytest.skip("nvcc not available")
+    tgbuild.build()
+    return tg.load_library()
+
+
+def _grouped(X=P, ldx=64, W=P, ldw=64, stride=64 * 32, op=1, off=P, Y=P, ldy=32, rows=10, groups=3,
+             N=32, K=64, dt=tg.BF16, out=tg.F32, ws=None, nbytes=0):
+    return tg.gemm_grouped(X, ldx, W, ldw, stride, op, off, Y, ldy, rows, groups, N, K, 1.0, 0.0, 0,
+                           dt, out, ws, nbytes)
+
+
+def test_grouped_rejects_bad_arguments():
+    for bad in (dict(X=None), dict(W=None), dict(off=None), dict(Y=None), dict(ldx=63), dict(ldw=63),
+                dict(op=0, ldw=31), dict(op=2), dict(op=-1), dict(ldy=31), dict(stride=-1),
+                dict(rows=-1), dict(rows=BIG + 1), dict(groups=-1), dict(N=-1), dict(K=-1),
+                dict(N=BIG + 1), dict(K=BIG + 1), dict(dt=3), dict(out=3)):
+        assert _grouped(**bad) == INV, bad
+    assert _grouped(groups=1025) == UNS
+    assert _grouped(rows=0, X=None, Y=None, off=None) == 0
+    assert _grouped(N=0, W=None, Y=None, ldy=0) == 0
+
+
+def _wgrad(D=P, ldd=32, X=P, ldx=64, off=P, C=P, ldc=64, stride=64 * 32, rows=10, groups=3, N=32,
+           K=64, dt=tg.BF16, out=tg.F32):
+    return tg.gemm_grouped_wgrad(D, ldd, X, ldx, off, C, ldc, stride, rows, groups, N, K, 1.0, 0.0,
+                                 dt, out)
+
+
+def test_wgrad_rejects_bad_arguments():
+    for bad in (dict(D=None), dict(X=None), dict(off=None), dict(C=None), dict(ldd=31), dict(ldx=63),
+                dict(ldc=63), dict(stride=64 * 32 - 1), dict(stride=-1), dict(rows=-1),
+                dict(rows=BIG + 1), dict(groups=-1), dict(N=-1), dict(K=BIG + 1), dict(dt=-1),
+                dict(out=9)):
+        assert _wgrad(**bad) == INV, bad
+    assert _wgrad(ldc=2 ** 62, stride=2 ** 62) == INV  # rows of one result reach into the next
+    assert _wgrad(groups=1025) == UNS
+    assert _wgrad(groups=0, off=None, C=None) == 0
+    assert _wgrad(N=0, C=None) == _wgrad(K=0, C=None, ldc=0) == 0
+
+
+def _adapters(A=P, lda=64, sa=64 * 8, B=P, ldb=8, sb=32 * 8, scale=None, G=3, r=8):
+    return tg.LoraAdapters(A, lda, sa, B, ldb, sb, scale, G, r)
+
+
+def _lora(X=P, ldx=64, W=P, ldw=64, lora=None, of=P, Y=P, ldy=32, rows=10, N=32, K=64, dt=tg.BF16,
+          out=tg.F32, ws=P, nbytes=1 << 30):
+    return tg.gemm_lora(X, ldx, W, ldw, lora or _adapters(), of, Y, ldy, rows, N, K, dt, out, ws,
+                        nbytes)
+
+
+def test_lora_rejects_bad_arguments():
+    size = tg.gemm_lora_workspace_size
+    assert 0 < size(10, 32, 64, 3, 8) < size(1000, 32, 64, 3, 8)
+    assert size(-1, 32, 64, 3, 8) == size(10, 32, 64, 3, 257) == size(10, 32, 64, -1, 8) == 0
+    for bad in (dict(X=None), dict(W=None), dict(Y=None), dict(of=None), dict(ldx=63), dict(ldw=63),
+                dict(ldy=31), dict(rows=-1), dict(N=BIG + 1), dict(K=-1), dict(dt=3), dict(out=-1),
+                dict(ws=None), dict(ws=P + 16), dict(nbytes=size(10, 32, 64, 3, 8) - 1)):
+        assert _lora(**bad) == INV, bad
+    for bad in (dict(A=None), dict(B=None), dict(lda=63), dict(ldb=7), dict(sa=-1), dict(sb=-1),
+                dict(G=-1), dict(G=65536), dict(r=-1)):
+        assert _lora(lora=_adapters(**bad)) == INV, bad
+    assert _lora(lora=_adapters(r=257, ldb=300)) == UNS
+    assert _lora(rows=0, X=None, Y=None, of=None, ws=None) == 0
+    assert _lora(N=0, W=None, Y=None, ws=None) == 0
+
+
+def _backward(D=P, ldd=32, X=P, ldx=64, W=P, ldw=64, lora=None, of=P, DX=P, lddx=64, DA=P, ldda=64,
+              sda=64 * 8, DB=P, lddb=8, sdb=32 * 8, rows=10, N=32, K=64, dt=tg.BF16, out=tg.F32,
+              grad=tg.F32, ws=P, nbytes=1 << 30):
+    return tg.gemm_lora_backward(D, ldd, X, ldx, W, ldw, lora or _adapters(), of, DX, lddx, DA, ldda,
+                                 sda, DB, lddb, sdb, rows, N, K, dt, out, grad, ws, nbytes)
+
+
+def test_lora_backward_rejects_bad_arguments():
+    size = tg.gemm_lora_backward_workspace_size
+    for bad in (dict(D=None), dict(X=None), dict(W=None), dict(of=None), dict(ldd=31), dict(ldx=63),
+                dict(ldw=63), dict(lddx=63), dict(ldda=63), dict(sda=64 * 8 - 1), dict(lddb=7),
+                dict(sdb=32 * 8 - 1), dict(rows=-1), dict(grad=3), dict(out=3), dict(dt=3),
+                dict(ws=None), dict(ws=P + 128), dict(nbytes=size(10, 32, 64, 3, 8) - 1)):
+        assert _backward(**bad) == INV, bad
+    assert _backward(lora=_adapters(r=257, ldb=300)) == UNS
+    assert _backward(DX=None, DA=None, DB=None, X=None, W=None, ws=None) == 0
+
+
+def test_cpu_tensors_are_rejected():
+    x, w, o = torch.zeros(4, 4), torch.zeros(2, 4, 4), torch.zeros(3, dtype=torch.int32)
+    of = torch.zeros(4, dtype=torch.int32)
+    for call in (lambda: tg.matmul_grouped(x, w, o), lambda: tg.matmul_grouped_wgrad(x, x, o),
+                 lambda: tg.matmul_lora(x, x, w, w, of),
+                 lambda: tg.matmul_lora_backward(x, x, x, w, w, of)):
+        with pytest.raises(ValueError):
+            call()

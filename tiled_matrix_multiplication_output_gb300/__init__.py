@@ -1,7 +1,8 @@
 """GB300-native output-stationary tiled matrix multiply, C = A @ B.
 
 Beside it, products of 8-bit matrices with a scale for each block of 128, their
-quantisation, and orthogonalisation by Newton-Schulz products.
+quantisation, orthogonalisation by Newton-Schulz products, products whose rows
+are grouped by expert, and low-rank adapters beside a shared projection.
 
 The products run in the CUDA library `_build/libtiled_gemm.so` (hand-written
 sm_103a kernels behind the C ABI of include/tiled_gemm.h); this package is
@@ -21,4 +22,8 @@ from .binding import (  # noqa: F401
     quantize_fp8_pair,
     NEWTON_SCHULZ_COEFFICIENTS, gemm_newton_schulz, gemm_newton_schulz_workspace_size,
     newton_schulz,
+    gemm_grouped, gemm_grouped_wgrad, gemm_grouped_wgrad_workspace_size,
+    gemm_grouped_workspace_size, matmul_grouped, matmul_grouped_wgrad,
+    LoraAdapters, gemm_lora, gemm_lora_backward, gemm_lora_backward_workspace_size,
+    gemm_lora_workspace_size, matmul_lora, matmul_lora_backward,
 )

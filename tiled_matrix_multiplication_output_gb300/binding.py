@@ -62,6 +62,17 @@ assert _FP8_MATRIX.size == ctypes.sizeof(Fp8Matrix)
 _pack_matrix = _FP8_MATRIX.pack
 
 
+class LoraAdapters(ctypes.Structure):
+    """gemm_lora_t: a set of low-rank adapters in device memory."""
+
+    _fields_ = [("A", _p), ("lda", _i64), ("stride_a", _i64), ("B", _p), ("ldb", _i64),
+                ("stride_b", _i64), ("scale", _p), ("adapters", _i64), ("rank", _i64)]
+
+
+_LORA = struct.Struct("@PqqPqqPqq")
+assert _LORA.size == ctypes.sizeof(LoraAdapters)
+
+
 _SIGNATURES = {
     "gemm": ([_p, _p, _p, _i64, _i64, _i64, _int, _int, _p], _int),
     "gemm_ex": ([_p, _p, _p, _i64, _i64, _i64, _int, _int, _int, _p], _int),
@@ -89,6 +100,23 @@ _SIGNATURES = {
     "gemm_newton_schulz_workspace_size": ([_i64, _i64, _i64], ctypes.c_size_t),
     "gemm_newton_schulz": ([_p, _i64, _i64, _p, _i64, _i64, _i64, _i64, _i64, _int, _int, _int,
                             ctypes.POINTER(ctypes.c_float), ctypes.c_float, _p, ctypes.c_size_t,
+                            _p], _int),
+    "gemm_grouped_workspace_size": ([_p, _i64, _p, _i64, _i64, _i64, _i64, _i64, _i64, _int, _int],
+                                    ctypes.c_size_t),
+    "gemm_grouped": ([_p, _i64, _p, _i64, _i64, _int, _p, _p, _i64, _i64, _i64, _i64, _i64,
+                      ctypes.c_float, ctypes.c_float, _int, _int, _int, _p, ctypes.c_size_t, _p],
+                     _int),
+    "gemm_grouped_wgrad_workspace_size": ([_p, _i64, _p, _i64, _i64, _i64, _i64, _int],
+                                          ctypes.c_size_t),
+    "gemm_grouped_wgrad": ([_p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64,
+                            ctypes.c_float, ctypes.c_float, _int, _int, _p, ctypes.c_size_t, _p],
+                           _int),
+    "gemm_lora_workspace_size": ([_i64] * 5, ctypes.c_size_t),
+    "gemm_lora": ([_p, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i64, _i64, _int, _int, _p,
+                   ctypes.c_size_t, _p], _int),
+    "gemm_lora_backward_workspace_size": ([_i64] * 5, ctypes.c_size_t),
+    "gemm_lora_backward": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _i64, _i64, _p,
+                            _i64, _i64, _i64, _i64, _i64, _int, _int, _int, _p, ctypes.c_size_t,
                             _p], _int),
     "gemm_device_status": ([_p], _int),
     "gemm_debug_config": ([_i64, _int], _int),
@@ -283,6 +311,57 @@ def gemm_newton_schulz(G, ldg, batch_stride_g, O, ldo, batch_stride_o, batch, ro
     return load_library().gemm_newton_schulz(G, ldg, batch_stride_g, O, ldo, batch_stride_o, batch,
                                              rows, cols, in_dtype, out_dtype, steps, coefficients,
                                              eps, workspace, workspace_bytes, stream)
+
+
+def gemm_grouped_workspace_size(X, ldx, W, ldw, stride_w, rows, groups, N, K, op_w,
+                                in_dtype) -> int:
+    return load_library().gemm_grouped_workspace_size(X, ldx, W, ldw, stride_w, rows, groups, N, K,
+                                                      op_w, in_dtype)
+
+
+def gemm_grouped(X, ldx, W, ldw, stride_w, op_w, offsets, Y, ldy, rows, groups, N, K, alpha, beta,
+                 zero_rest, in_dtype, out_dtype, workspace=None, workspace_bytes=0,
+                 stream=None) -> int:
+    return load_library().gemm_grouped(X, ldx, W, ldw, stride_w, op_w, offsets, Y, ldy, rows,
+                                       groups, N, K, alpha, beta, zero_rest, in_dtype, out_dtype,
+                                       workspace, workspace_bytes, stream)
+
+
+def gemm_grouped_wgrad_workspace_size(D, ldd, X, ldx, rows, N, K, in_dtype) -> int:
+    return load_library().gemm_grouped_wgrad_workspace_size(D, ldd, X, ldx, rows, N, K, in_dtype)
+
+
+def gemm_grouped_wgrad(D, ldd, X, ldx, offsets, C, ldc, stride_c, rows, groups, N, K, alpha, beta,
+                       in_dtype, out_dtype, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load_library().gemm_grouped_wgrad(D, ldd, X, ldx, offsets, C, ldc, stride_c, rows,
+                                             groups, N, K, alpha, beta, in_dtype, out_dtype,
+                                             workspace, workspace_bytes, stream)
+
+
+def gemm_lora_workspace_size(rows, N, K, adapters, rank) -> int:
+    return load_library().gemm_lora_workspace_size(rows, N, K, adapters, rank)
+
+
+def gemm_lora(X, ldx, W, ldw, lora, adapter, Y, ldy, rows, N, K, in_dtype, out_dtype, workspace,
+              workspace_bytes, stream=None) -> int:
+    """lora: a LoraAdapters structure, or the bytes of one."""
+    lora = ctypes.byref(lora) if isinstance(lora, LoraAdapters) else lora
+    return load_library().gemm_lora(X, ldx, W, ldw, lora, adapter, Y, ldy, rows, N, K, in_dtype,
+                                    out_dtype, workspace, workspace_bytes, stream)
+
+
+def gemm_lora_backward_workspace_size(rows, N, K, adapters, rank) -> int:
+    return load_library().gemm_lora_backward_workspace_size(rows, N, K, adapters, rank)
+
+
+def gemm_lora_backward(D, ldd, X, ldx, W, ldw, lora, adapter, DX, lddx, DA, ldda, stride_da, DB,
+                       lddb, stride_db, rows, N, K, in_dtype, out_dtype, grad_dtype, workspace,
+                       workspace_bytes, stream=None) -> int:
+    lora = ctypes.byref(lora) if isinstance(lora, LoraAdapters) else lora
+    return load_library().gemm_lora_backward(D, ldd, X, ldx, W, ldw, lora, adapter, DX, lddx, DA,
+                                             ldda, stride_da, DB, lddb, stride_db, rows, N, K,
+                                             in_dtype, out_dtype, grad_dtype, workspace,
+                                             workspace_bytes, stream)
 
 
 def gemm_device_status(stream=None) -> int:
@@ -745,3 +824,245 @@ def _check_batch(x, what):
     if x.shape[0] == 0:
         return 0, x.shape[1], x.shape[2], x.shape[2], 0
     return x.shape[0], *_check_matrix(x[0], what), x.stride(0)
+
+
+# ------------------------------------------------------ products grouped by rows
+
+def _check_typed(x, code, what):
+    """_check_matrix of an operand of the type `code`."""
+    if _cache().codes.get(x.dtype) != code:
+        raise TypeError(f"{what}'s type differs from that of the other operands")
+    return _check_matrix(x, what)
+
+
+def _check_stack(x, what):
+    """(matrices, rows, cols, row stride, matrix stride) of a 3-D tensor with
+    contiguous rows on the current CUDA device."""
+    device = x.get_device()
+    if device < 0 or x.dim() != 3:
+        raise ValueError(f"{what} must be a 3-D CUDA tensor")
+    if device != (_cached or _cache()).current_device():
+        raise ValueError(f"{what} is not on the current device")
+    n, rows, cols = x.shape
+    stride, pitch, step = x.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what}'s rows must be contiguous")
+    if rows <= 1:
+        pitch = (cols + 15) // 16 * 16
+    elif pitch < cols:
+        raise ValueError(f"{what}'s rows must not overlap")
+    if n <= 1:  # a single matrix has no stride of its own
+        stride = rows * pitch
+    return n, rows, cols, pitch, stride
+
+
+def _check_index(x, like, n, what):
+    """A contiguous int32 vector (of n values, unless None) on `like`'s device."""
+    if x.dim() != 1 or not x.is_contiguous() or x.get_device() != like.get_device():
+        raise ValueError(f"{what} must be a contiguous 1-D tensor on the operands' device")
+    if x.dtype is not _torch().int32:
+        raise TypeError(f"{what} must be int32")
+    if n is not None and x.shape[0] != n:
+        raise ValueError(f"{what} must have {n} values")
+    return x.data_ptr()
+
+
+def _in_code(x, what):
+    code = (_cached or _cache()).codes.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be FP32, FP16 or BF16")
+    return code
+
+
+def _check_out(out, shape, out_dtype, what="out"):
+    if tuple(out.shape) != shape or (out_dtype is not None and out.dtype != _out_dtype(out_dtype)):
+        raise ValueError(f"{what} must be a {shape} tensor of the output dtype")
+    _in_code(out, what)
+
+
+def _workspace(nbytes, x, stream):
+    """(address, the tensor that holds it) of device scratch, allocated by PyTorch."""
+    if nbytes == 0:
+        return None, None
+    w = _allocate(stream, _empty, (nbytes,), _torch().uint8, x.device)
+    return w.data_ptr(), w
+
+
+def matmul_grouped(x, w, offsets, op_b="t", out_dtype=None, out=None, alpha=1.0, beta=0.0,
+                   stream=None):
+    """Y = alpha * x @ op(w[g]) + beta * Y, with a matrix of its own for each
+    group of rows: the experts of a mixture, and their input's gradient.
+
+    x: 2-D CUDA tensor (FP16, BF16 or FP32; rows contiguous, any row stride)
+    whose rows are sorted by group; w: 3-D, one matrix for each group; offsets:
+    int32 CUDA tensor of len(w) + 1 values, group g being the rows
+    [offsets[g], offsets[g + 1]).  op "t" (the default) takes w[g] stored
+    out x in, x @ w[g]^T; "n" as stored, x @ w[g]: with x the gradient of the
+    output, the gradient of the input.  Groups may be empty.  Rows of no group are
+    left as they were in `out`, and are zero where out is not given.
+    out_dtype defaults to FP32, or to out's type; beta != 0 needs out.  At most
+    GEMM_MAX_GROUPS (1024) groups.  Returns Y without synchronizing."""
+    tb = OPS.get(op_b)
+    if tb is None:
+        raise ValueError("op_b is \"n\" or \"t\"")
+    code = _in_code(x, "x")
+    rows, K, ldx = _check_matrix(x, "x")
+    groups, N, K2, ldw, stride = _check_stack(w, "w")
+    if w.dtype is not x.dtype:
+        raise TypeError("x and w must have the same dtype")
+    if not tb:
+        N, K2 = K2, N
+    if K != K2:
+        raise ValueError("inner dimensions differ")
+    off = _check_index(offsets, x, groups + 1, "offsets")
+    given = out is not None
+    if not given:
+        if beta != 0.0:
+            raise ValueError("beta != 0 needs out")
+        out = _allocate(stream, _empty, (rows, N), _out_dtype(out_dtype), x.device)
+        ldy = N
+    else:
+        _check_out(out, (rows, N), out_dtype)
+        ldy = _check_matrix(out, "out")[2]
+    lib = _lib or load_library()
+    px, pw = x.data_ptr(), w.data_ptr()
+    nbytes = lib.gemm_grouped_workspace_size(px, ldx, pw, ldw, stride, rows, groups, N, K, tb, code)
+    ws, _held = _workspace(nbytes, x, stream)
+    rc = lib.gemm_grouped(px, ldx, pw, ldw, stride, tb, off, out.data_ptr(), ldy, rows, groups, N,
+                          K, alpha, beta, not given, code, dtype_code(out.dtype), ws, nbytes,
+                          _stream_ptr(stream, x))
+    if rc != OK:
+        raise GemmError(rc, "gemm_grouped")
+    return out
+
+
+def matmul_grouped_wgrad(dy, x, offsets, out_dtype=None, out=None, alpha=1.0, beta=0.0,
+                         stream=None):
+    """C[g] = alpha * dy_g^T @ x_g + beta * C[g], dy_g and x_g the rows
+    [offsets[g], offsets[g + 1]) of both: the gradient of matmul_grouped's
+    w (stored out x in).
+
+    dy: rows x out, x: rows x in, as matmul_grouped's x; offsets: int32 CUDA
+    tensor of groups + 1 values.  `out` may supply C (groups, out, in), with
+    beta = 1 to add to it.  out_dtype defaults to FP32, or to out's type.
+    Groups without rows give zeros (beta * C).  Returns C without
+    synchronizing."""
+    code = _in_code(x, "x")
+    rows, K, ldx = _check_matrix(x, "x")
+    rows2, N, ldd = _check_typed(dy, code, "dy")
+    if rows != rows2:
+        raise ValueError("dy and x must have the same number of rows")
+    off = _check_index(offsets, x, None, "offsets")
+    groups = offsets.shape[0] - 1
+    if groups < 0:
+        raise ValueError("offsets must have at least one value")
+    if out is None:
+        if beta != 0.0:
+            raise ValueError("beta != 0 needs out")
+        out = _allocate(stream, _empty, (groups, N, K), _out_dtype(out_dtype), x.device)
+        ldc, stride = K, N * K
+    else:
+        _check_out(out, (groups, N, K), out_dtype)
+        *_, ldc, stride = _check_stack(out, "out")
+    lib = _lib or load_library()
+    px, pd = x.data_ptr(), dy.data_ptr()
+    nbytes = lib.gemm_grouped_wgrad_workspace_size(pd, ldd, px, ldx, rows, N, K, code)
+    ws, _held = _workspace(nbytes, x, stream)
+    rc = lib.gemm_grouped_wgrad(pd, ldd, px, ldx, off, out.data_ptr(), ldc, stride, rows, groups,
+                                N, K, alpha, beta, code, dtype_code(out.dtype), ws, nbytes,
+                                _stream_ptr(stream, x))
+    if rc != OK:
+        raise GemmError(rc, "gemm_grouped_wgrad")
+    return out
+
+
+# --------------------------------------------------------- low-rank adapters
+
+def _lora_operands(a, b, adapter, scale, rows, N, K, code, like):
+    """(the bytes of gemm_lora_t, adapters, rank, the address of the rows' adapters)."""
+    G, r, Ka, lda, stride_a = _check_stack(a, "a")
+    Gb, Nb, rb, ldb, stride_b = _check_stack(b, "b")
+    if a.dtype is not like.dtype or b.dtype is not like.dtype:
+        raise TypeError("a and b must have the other operands' dtype")
+    if (G, r) != (Gb, rb) or Ka != K or Nb != N:
+        raise ValueError(f"a must be (adapters, rank, {K}) and b (adapters, {N}, rank)")
+    index = _check_index(adapter, like, rows, "adapter")
+    ps = None
+    if scale is not None:
+        if scale.dim() != 1 or scale.shape[0] != G or not scale.is_contiguous() \
+                or scale.get_device() != like.get_device():
+            raise ValueError("scale must be a contiguous vector, one value for each adapter, on "
+                             "the operands' device")
+        if scale.dtype is not (_cached or _cache()).float32:
+            raise TypeError("scale must be FP32")
+        ps = scale.data_ptr()
+    return _LORA.pack(a.data_ptr(), lda, stride_a, b.data_ptr(), ldb, stride_b, ps or 0, G,
+                      r), G, r, index
+
+
+def matmul_lora(x, w, a, b, adapter, scale=None, out_dtype=None, out=None, stream=None):
+    """y_i = x_i @ w^T + scale[g] * (x_i @ a[g]^T) @ b[g]^T with g = adapter[i]:
+    a shared projection with a low-rank adapter of its own for every row, in one
+    pass over the rows.
+
+    x: rows x in (FP16, BF16 or FP32; rows contiguous, any row stride); w: out x in;
+    a: (adapters, rank, in) and b: (adapters, out, rank); adapter: int32 CUDA
+    tensor, one value for each row, in any order; a value outside
+    [0, adapters) means none.  scale: FP32, one for each adapter (None: 1).
+    rank at most GEMM_MAX_RANK (256).  A row sees nothing of other rows'
+    adapters.  out_dtype defaults to FP32, or to out's type.  Returns y
+    without synchronizing."""
+    code = _in_code(x, "x")
+    rows, K, ldx = _check_matrix(x, "x")
+    N, K2, ldw = _check_typed(w, code, "w")
+    if K != K2:
+        raise ValueError("inner dimensions differ")
+    lora, G, r, index = _lora_operands(a, b, adapter, scale, rows, N, K, code, x)
+    if out is None:
+        out = _allocate(stream, _empty, (rows, N), _out_dtype(out_dtype), x.device)
+        ldy = N
+    else:
+        _check_out(out, (rows, N), out_dtype)
+        ldy = _check_matrix(out, "out")[2]
+    lib = _lib or load_library()
+    nbytes = lib.gemm_lora_workspace_size(rows, N, K, G, r)
+    ws, _held = _workspace(nbytes, x, stream)
+    rc = lib.gemm_lora(x.data_ptr(), ldx, w.data_ptr(), ldw, lora, index, out.data_ptr(), ldy,
+                       rows, N, K, code, dtype_code(out.dtype), ws, nbytes,
+                       _stream_ptr(stream, x))
+    if rc != OK:
+        raise GemmError(rc, "gemm_lora")
+    return out
+
+
+def matmul_lora_backward(dy, x, w, a, b, adapter, scale=None, out_dtype=None, grad_dtype=None,
+                         stream=None):
+    """(dx, da, db): the gradients of matmul_lora from dy, the gradient of its
+    output.  w is frozen and has none.
+
+    dx_i = dy_i @ w + u_i @ a[g], da[g] = sum of u_i^T x_i, db[g] = sum of
+    dy_i^T t_i over the rows of adapter g, with u_i = scale[g] dy_i @ b[g] and
+    t_i = scale[g] x_i @ a[g]^T.  Adapters without rows get zeros.  out_dtype is
+    dx's type (default FP32), grad_dtype that of da and db (default FP32).
+    Returns without synchronizing."""
+    code = _in_code(x, "x")
+    rows, K, ldx = _check_matrix(x, "x")
+    rows2, N, ldd = _check_typed(dy, code, "dy")
+    N2, K2, ldw = _check_typed(w, code, "w")
+    if rows != rows2 or N != N2 or K != K2:
+        raise ValueError("dy must be rows x out, x rows x in and w out x in")
+    lora, G, r, index = _lora_operands(a, b, adapter, scale, rows, N, K, code, x)
+    odt, gdt = _out_dtype(out_dtype), _out_dtype(grad_dtype)
+    dx = _allocate(stream, _empty, (rows, K), odt, x.device)
+    da = _allocate(stream, _empty, (G, r, K), gdt, x.device)
+    db = _allocate(stream, _empty, (G, N, r), gdt, x.device)
+    lib = _lib or load_library()
+    nbytes = lib.gemm_lora_backward_workspace_size(rows, N, K, G, r)
+    ws, _held = _workspace(nbytes, x, stream)
+    rc = lib.gemm_lora_backward(dy.data_ptr(), ldd, x.data_ptr(), ldx, w.data_ptr(), ldw, lora,
+                                index, dx.data_ptr(), K, da.data_ptr(), K, r * K, db.data_ptr(), r,
+                                N * r, rows, N, K, code, dtype_code(odt), dtype_code(gdt), ws,
+                                nbytes, _stream_ptr(stream, x))
+    if rc != OK:
+        raise GemmError(rc, "gemm_lora_backward")
+    return dx, da, db

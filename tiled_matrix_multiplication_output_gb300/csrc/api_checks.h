@@ -1,0 +1,30 @@
+// Argument checks shared by the entry points of the grouped products and the
+// adapters.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "tiled_gemm.h"
+
+namespace tmmo {
+
+inline bool valid_size(int64_t n) { return n >= 0 && n <= GEMM_MAX_DIM; }
+inline bool valid_dtype(int t) { return t == GEMM_F32 || t == GEMM_F16 || t == GEMM_BF16; }
+
+// Whether matrices of rows x cols (pitch ld >= cols), `stride` elements after
+// each other, do not overlap.
+inline bool apart(int64_t stride, int64_t rows, int64_t ld, int64_t cols)
+{
+    return stride >= 0 && static_cast<__int128>(stride) >= static_cast<__int128>(rows - 1) * ld + cols;
+}
+
+inline int status_of(cudaError_t err)
+{
+    if (err == cudaErrorNotSupported)
+        return GEMM_ERR_UNSUPPORTED;
+    return err == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+}  // namespace tmmo

@@ -1,0 +1,65 @@
+// Internal launchers of low-rank adapters beside a shared projection (host
+// side).
+//
+// One form serves both directions.  A row i of X with adapter g is multiplied
+// by the shared weight and, through the adapter's two factors, by a low-rank
+// one:
+//     t_i = scale_g * X_i F_g^T          (rank values)
+//     Y_i = X_i W^T + t_i E_g^T
+// Forward: X is the input, F = A (rank x K), E = B (N x rank), W as stored
+// (N x K).  Towards the input's gradient: X is the output's gradient, F = B^T,
+// E = A^T and W^T; every matrix is then read across its stored rows.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace tmmo {
+
+constexpr int kMaxRank = 256;
+
+struct LoraLaunch {
+    const void* X;        // rows x K
+    int64_t ldx;
+    const void* W;        // N x K, or (across) K x N
+    int64_t ldw;
+    const void* F;        // adapters of rank x K, or (across) K x rank
+    int64_t ldf, stride_f;
+    const void* E;        // adapters of N x rank, or (across) rank x N
+    int64_t lde, stride_e;
+    bool across;
+    const float* scale;   // one for each adapter, or null: 1
+    const int32_t* adapter;  // one for each row; outside [0, adapters): none
+    void* Y;              // rows x N
+    int64_t ldy;
+    int rows, N, K, adapters, rank;
+    int in_dtype, out_dtype;  // DT_*
+    float* t;             // rows x rank
+    int num_sms;
+    int* status;
+    long long wait_budget;
+    int fault_skip_kblock;
+};
+
+// G_g(c, j) = sum over the rows i of adapter g of P[i, c] t[i, j].
+struct LoraGradLaunch {
+    const void* P;        // rows x cols
+    int64_t ldp;
+    const float* t;       // rows x rank
+    void* G;              // adapters; element (c, j) at c * step_c + j * step_j
+    int64_t step_c, step_j, stride_g;
+    const int32_t* adapter;
+    int rows, cols, adapters, rank;
+    int in_dtype, out_dtype;
+    int num_sms;
+    int* status;
+    long long wait_budget;
+};
+
+cudaError_t lora_simt_shrink(const LoraLaunch& l, cudaStream_t stream);
+cudaError_t lora_simt_expand(const LoraLaunch& l, cudaStream_t stream);
+cudaError_t lora_simt_grad(const LoraGradLaunch& l, cudaStream_t stream);
+
+}  // namespace tmmo

@@ -1,0 +1,173 @@
+// Low-rank adapters on the FP32 units: 64 x 64 tiles of the shared product,
+// and of each adapter's among the tile's rows.
+#include "launch.h"
+#include "lora.h"
+#include "simt_tile.cuh"
+#include "simt_types.h"
+
+namespace tmmo {
+namespace {
+
+// The adapters of a tile's rows (-1: none, or behind the last row).
+__device__ __forceinline__ void load_adapters(int (&s)[ST], const int32_t* adapter, int row0, int rows,
+                                              int adapters)
+{
+    __syncthreads();
+    if (threadIdx.x < ST) {
+        const int i = row0 + threadIdx.x;
+        const int g = i < rows ? adapter[i] : -1;
+        s[threadIdx.x] = g >= 0 && g < adapters ? g : -1;
+    }
+    __syncthreads();
+}
+
+// Calls f(g) once for each adapter among the tile's rows.
+template <typename F>
+__device__ __forceinline__ void each_adapter(const int (&s)[ST], F f)
+{
+    for (int i = 0; i < ST; ++i) {
+        const int g = s[i];
+        bool seen = g < 0;
+        for (int j = 0; j < i && !seen; ++j)
+            seen = s[j] == g;
+        if (!seen)
+            f(g);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(ST_THREADS) lora_shrink_kernel(const LoraLaunch l)
+{
+    __shared__ SimtSmem s;
+    __shared__ int of[ST];
+    const int tiles_r = (l.rank + ST - 1) / ST;
+    const int64_t total = static_cast<int64_t>((l.rows + ST - 1) / ST) * tiles_r;
+    const int r0 = 4 * (threadIdx.x / 16), c0 = 4 * (threadIdx.x % 16);
+    for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
+        const int row0 = static_cast<int>(tile / tiles_r) * ST, j0 = static_cast<int>(tile % tiles_r) * ST;
+        const int cols = min(l.rank - j0, ST);
+        load_adapters(of, l.adapter, row0, l.rows, l.adapters);
+        const View<T> x{static_cast<const T*>(l.X) + row0 * l.ldx, l.ldx, 1};
+        each_adapter(of, [&](int g) {
+            const T* f = static_cast<const T*>(l.F) + g * l.stride_f;
+            const View<T> v = l.across ? View<T>{f + j0, 1, l.ldf} : View<T>{f + j0 * l.ldf, l.ldf, 1};
+            float acc[4][4] = {};
+            simt_accumulate(acc, s, x, v, 0, l.K, [&](int i, int) { return of[i] == g; },
+                            [&](int j, int) { return j < cols; });
+            const float scale = l.scale ? l.scale[g] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (of[r0 + i] == g && c0 + j < cols)
+                        l.t[static_cast<int64_t>(row0 + r0 + i) * l.rank + j0 + c0 + j] =
+                            scale * acc[i][j];
+        });
+    }
+}
+
+template <typename T, typename OutT>
+__global__ void __launch_bounds__(ST_THREADS) lora_expand_kernel(const LoraLaunch l)
+{
+    __shared__ SimtSmem s;
+    __shared__ int of[ST];
+    const int tiles_n = (l.N + ST - 1) / ST;
+    const int64_t total = static_cast<int64_t>((l.rows + ST - 1) / ST) * tiles_n;
+    const int r0 = 4 * (threadIdx.x / 16);
+    for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
+        const int row0 = static_cast<int>(tile / tiles_n) * ST, n0 = static_cast<int>(tile % tiles_n) * ST;
+        const int rows = min(l.rows - row0, ST), cols = min(l.N - n0, ST);
+        load_adapters(of, l.adapter, row0, l.rows, l.adapters);
+        const View<T> x{static_cast<const T*>(l.X) + row0 * l.ldx, l.ldx, 1};
+        auto columns = [&](const void* base, int64_t off, int64_t ld) {
+            const T* p = static_cast<const T*>(base) + off;
+            return l.across ? View<T>{p + n0, 1, ld} : View<T>{p + n0 * ld, ld, 1};
+        };
+        auto in_cols = [&](int j, int) { return j < cols; };
+        float acc[4][4] = {};
+        simt_accumulate(acc, s, x, columns(l.W, 0, l.ldw), 0, l.K, [&](int i, int) { return i < rows; },
+                        in_cols);
+        const View<float> t{l.t + static_cast<int64_t>(row0) * l.rank, l.rank, 1};
+        each_adapter(of, [&](int g) {
+            float add[4][4] = {};
+            simt_accumulate(add, s, t, columns(l.E, g * l.stride_e, l.lde), 0, l.rank,
+                            [&](int i, int) { return of[i] == g; }, in_cols);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (of[r0 + i] == g)  // rows of other adapters see nothing of this one
+                        acc[i][j] += add[i][j];
+        });
+        simt_store(acc, static_cast<OutT*>(l.Y) + row0 * l.ldy + n0, l.ldy, rows, cols, 1.0f, 0.0f);
+    }
+}
+
+template <typename T, typename OutT>
+__global__ void __launch_bounds__(ST_THREADS) lora_grad_kernel(const LoraGradLaunch l)
+{
+    __shared__ SimtSmem s;
+    const int tiles_c = (l.cols + ST - 1) / ST, tiles_r = (l.rank + ST - 1) / ST;
+    const int64_t per = static_cast<int64_t>(tiles_c) * tiles_r;
+    const int r0 = 4 * (threadIdx.x / 16), c0 = 4 * (threadIdx.x % 16);
+    for (int64_t tile = blockIdx.x; tile < per * l.adapters; tile += gridDim.x) {
+        const int g = static_cast<int>(tile / per), u = static_cast<int>(tile % per);
+        const int p0 = u / tiles_r * ST, j0 = u % tiles_r * ST;
+        const int rows = min(l.cols - p0, ST), cols = min(l.rank - j0, ST);
+        const View<T> p{static_cast<const T*>(l.P) + p0, 1, l.ldp};
+        const View<float> t{l.t + j0, 1, l.rank};
+        float acc[4][4] = {};
+        for (int k = 0; k < l.rows; k += ST_K) {
+            const int i = k + static_cast<int>(threadIdx.x);
+            if (!__syncthreads_or(threadIdx.x < ST_K && i < l.rows && l.adapter[i] == g))
+                continue;
+            simt_accumulate(acc, s, p, t, k, min(k + ST_K, l.rows),
+                            [&](int c, int row) { return c < rows && l.adapter[row] == g; },
+                            [&](int j, int row) { return j < cols && l.adapter[row] == g; });
+        }
+        OutT* out = static_cast<OutT*>(l.G) + g * l.stride_g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r0 + i < rows && c0 + j < cols)
+                    put(out + (p0 + r0 + i) * l.step_c + (j0 + c0 + j) * l.step_j, acc[i][j]);
+    }
+}
+
+}  // namespace
+
+cudaError_t lora_simt_shrink(const LoraLaunch& l, cudaStream_t stream)
+{
+    const int64_t tiles = static_cast<int64_t>((l.rows + ST - 1) / ST) * ((l.rank + ST - 1) / ST);
+    return with_in_type(l.in_dtype, [&](auto in) {
+        note_launch();
+        lora_shrink_kernel<decltype(in)><<<simt_blocks(tiles, l.num_sms), ST_THREADS, 0, stream>>>(l);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t lora_simt_expand(const LoraLaunch& l, cudaStream_t stream)
+{
+    const int64_t tiles = static_cast<int64_t>((l.rows + ST - 1) / ST) * ((l.N + ST - 1) / ST);
+    return with_types(l.in_dtype, l.out_dtype, [&](auto in, auto out) {
+        note_launch();
+        lora_expand_kernel<decltype(in), decltype(out)>
+            <<<simt_blocks(tiles, l.num_sms), ST_THREADS, 0, stream>>>(l);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t lora_simt_grad(const LoraGradLaunch& l, cudaStream_t stream)
+{
+    const int64_t tiles = static_cast<int64_t>(l.adapters) * ((l.cols + ST - 1) / ST) *
+                          ((l.rank + ST - 1) / ST);
+    return with_types(l.in_dtype, l.out_dtype, [&](auto in, auto out) {
+        note_launch();
+        lora_grad_kernel<decltype(in), decltype(out)>
+            <<<simt_blocks(tiles, l.num_sms), ST_THREADS, 0, stream>>>(l);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace tmmo
