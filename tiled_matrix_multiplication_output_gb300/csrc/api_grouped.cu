@@ -77,7 +77,8 @@ extern "C" int gemm_grouped(const void* X, int64_t ldx, const void* W, int64_t l
     l.status = d.status;
     l.wait_budget = wait_budget_cycles();
     l.fault_skip_kblock = fault_skip_kblock();
-    return status_of(grouped_simt_launch(l, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return status_of(grouped_tc_takes(l) ? grouped_tc_launch(l, s) : grouped_simt_launch(l, s));
 }
 
 extern "C" size_t gemm_grouped_wgrad_workspace_size(const void*, int64_t, const void*, int64_t,
@@ -121,5 +122,7 @@ extern "C" int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int
     l.status = d.status;
     l.wait_budget = wait_budget_cycles();
     l.fault_skip_kblock = fault_skip_kblock();
-    return status_of(grouped_wgrad_simt_launch(l, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return status_of(grouped_wgrad_tc_takes(l) ? grouped_wgrad_tc_launch(l, s)
+                                               : grouped_wgrad_simt_launch(l, s));
 }

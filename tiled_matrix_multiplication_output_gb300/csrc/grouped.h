@@ -56,6 +56,13 @@ struct GroupedWgradLaunch {
     int fault_skip_kblock;
 };
 
+// The tensor-core kernels, and whether they take the operands (16-bit, rows on
+// 16-byte boundaries).
+bool grouped_tc_takes(const GroupedLaunch& l);
+cudaError_t grouped_tc_launch(const GroupedLaunch& l, cudaStream_t stream);
+bool grouped_wgrad_tc_takes(const GroupedWgradLaunch& l);
+cudaError_t grouped_wgrad_tc_launch(const GroupedWgradLaunch& l, cudaStream_t stream);
+
 // FP32 and every other operand the tensor-core kernels do not take.
 cudaError_t grouped_simt_launch(const GroupedLaunch& l, cudaStream_t stream);
 cudaError_t grouped_wgrad_simt_launch(const GroupedWgradLaunch& l, cudaStream_t stream);

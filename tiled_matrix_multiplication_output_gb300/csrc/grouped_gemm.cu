@@ -1,0 +1,50 @@
+// Launch of the row-grouped products on the tensor cores (grouped_tc.cuh).
+#include "grouped_launch.cuh"
+
+namespace tmmo {
+
+bool grouped_tc_takes(const GroupedLaunch& l)
+{
+    return l.in_dtype != DT_F32 && l.K > 0 && l.by.groups > 0 && aligned_rows(l.X, l.ldx, l.in_dtype) &&
+           aligned_rows(l.W, l.ldw, l.in_dtype) &&
+           (l.by.groups == 1 || (l.stride_w * type_bytes(l.in_dtype)) % 16 == 0);
+}
+
+cudaError_t grouped_tc_launch(const GroupedLaunch& l, cudaStream_t stream)
+{
+    GroupedTcParams p{};
+    p.by = l.by;
+    p.C = l.Y;
+    p.ldc = l.ldy;
+    p.N = l.N;
+    p.K = l.K;
+    p.tiles_f = (l.N + 255) / 256;
+    p.alpha = l.alpha;
+    p.beta = l.beta;
+    p.zero_rest = l.zero_rest;
+    p.one_weight = l.by.groups == 1 || l.stride_w == 0;
+    p.swap = !p.one_weight && l.stride_w < l.ldw;  // matrices interleaved row by row
+    p.idesc = tc_idesc(l.in_dtype == DT_BF16, 256, 0, !l.w_t, false);
+    p.status = l.status;
+    p.wait_budget = l.wait_budget;
+    p.fault_skip_kblock = l.fault_skip_kblock;
+
+    const int64_t inner = l.w_t ? l.K : l.N, outer = l.w_t ? l.N : l.K;
+    const int64_t groups = p.one_weight ? 1 : l.by.groups;
+    const int64_t stride = p.one_weight ? l.ldw : l.stride_w;
+    const uint32_t deep = l.w_t ? TC_BM : TC_BK;
+    CUtensorMap m[4];
+    const bool ok =
+        (p.swap ? encode_map(&m[0], l.in_dtype, l.W, 3, {inner, groups, outer}, {stride, l.ldw}, {64, 1, deep})
+                : encode_map(&m[0], l.in_dtype, l.W, 3, {inner, outer, groups}, {l.ldw, stride}, {64, deep, 1})) &&
+        encode_map(&m[1], l.in_dtype, l.X, 2, {l.K, l.by.rows, 1}, {l.ldx, 0}, {64, TC_BM, 1}) &&
+        encode_map(&m[2], l.in_dtype, l.X, 2, {l.K, l.by.rows, 1}, {l.ldx, 0}, {64, 16, 1});
+    if (!ok)
+        return cudaErrorNotSupported;
+    m[3] = m[2];
+    const int64_t most = (l.by.rows / GT_N + static_cast<int64_t>(std::min(l.by.groups, l.by.rows))) * p.tiles_f;
+    return l.w_t ? launch_grouped_tc<GROUPED_T>(l.out_dtype, m, p, most, l.num_sms, stream)
+                 : launch_grouped_tc<GROUPED_N>(l.out_dtype, m, p, most, l.num_sms, stream);
+}
+
+}  // namespace tmmo

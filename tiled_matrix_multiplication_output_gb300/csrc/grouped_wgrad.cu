@@ -1,0 +1,44 @@
+// Launch of the grouped weight gradient on the tensor cores (grouped_tc.cuh).
+#include "grouped_launch.cuh"
+
+namespace tmmo {
+
+bool grouped_wgrad_tc_takes(const GroupedWgradLaunch& l)
+{
+    return l.in_dtype != DT_F32 && l.by.rows > 0 && aligned_rows(l.D, l.ldd, l.in_dtype) &&
+           aligned_rows(l.X, l.ldx, l.in_dtype);
+}
+
+cudaError_t grouped_wgrad_tc_launch(const GroupedWgradLaunch& l, cudaStream_t stream)
+{
+    GroupedTcParams p{};
+    p.by = l.by;
+    p.C = l.C;
+    p.ldc = l.ldc;
+    p.stride_c = l.stride_c;
+    p.N = l.N;
+    p.K = l.K;
+    p.tiles_f = (l.N + 255) / 256;
+    p.tiles_c = (l.K + GT_N - 1) / GT_N;
+    p.alpha = l.alpha;
+    p.beta = l.beta;
+    p.idesc = tc_idesc(l.in_dtype == DT_BF16, 256, 0, true, true);
+    p.status = l.status;
+    p.wait_budget = l.wait_budget;
+    p.fault_skip_kblock = l.fault_skip_kblock;
+    const int64_t rows = l.by.rows, groups = l.by.groups;
+    CUtensorMap m[4];
+    if (!encode_map(&m[0], l.in_dtype, l.D, 2, {l.N, rows, 1}, {l.ldd, 0}, {64, TC_BK, 1}) ||
+        !encode_map(&m[1], l.in_dtype, l.X, 2, {l.K, rows, 1}, {l.ldx, 0}, {64, TC_BK, 1}))
+        return cudaErrorNotSupported;
+    m[2] = m[3] = m[1];
+    const int64_t stride = groups > 1 ? l.stride_c : l.N * l.ldc;
+    p.tma_out = l.beta == 0.0f && aligned_rows(l.C, l.ldc, l.out_dtype) &&
+                (groups == 1 || (stride * type_bytes(l.out_dtype)) % 16 == 0) &&
+                encode_map(&m[3], l.out_dtype, l.C, 3, {l.K, l.N, groups}, {l.ldc, stride},
+                           {128u / type_bytes(l.out_dtype), 32, 1});
+    const int64_t most = groups * p.tiles_f * p.tiles_c;
+    return launch_grouped_tc<GROUPED_WGRAD>(l.out_dtype, m, p, most, l.num_sms, stream);
+}
+
+}  // namespace tmmo
