@@ -2,6 +2,7 @@
 // translation to the internal launchers.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "api_checks.h"
@@ -26,8 +27,15 @@ bool valid_sizes(int64_t rows, int64_t N, int64_t K, int64_t adapters, int64_t r
            adapters <= kMaxAdapters;
 }
 
-// The rank values of all rows.
-int64_t values_bytes(int64_t rows, int64_t rank) { return round256(rows * rank * 4); }
+// The rank values of all rows: FP32, or in up to three parts.
+int64_t values_bytes(int64_t rows, int64_t rank)
+{
+    return round256(rows * std::max<int64_t>(rank * 4, lora_parts_bytes(static_cast<int>(rank), 3)));
+}
+int64_t plan_bytes(int64_t rows) { return round256((rows + 127) / 128 * LORA_PLAN_BYTES); }
+
+// How many parts hold a rank value: all bits of an FP32 value for an FP32 result.
+int parts_for(int in_dtype, bool f32_result) { return in_dtype == DT_BF16 && f32_result ? 3 : 2; }
 
 // Whether there is an adapter that can change anything.
 bool has_adapters(const gemm_lora_t& a) { return a.adapters > 0 && a.rank > 0; }
@@ -72,7 +80,7 @@ extern "C" size_t gemm_lora_workspace_size(int64_t rows, int64_t N, int64_t K, i
 {
     if (!valid_sizes(rows, N, K, adapters, rank) || rank > GEMM_MAX_RANK)
         return 0;
-    return static_cast<size_t>(values_bytes(rows, rank));
+    return static_cast<size_t>(values_bytes(rows, rank) + plan_bytes(rows));
 }
 
 extern "C" int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw,
@@ -117,11 +125,15 @@ extern "C" int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw,
     d.fill(&l);
     l.fault_skip_kblock = fault_skip_kblock();
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    l.t16 = workspace;
+    l.plan = static_cast<char*>(workspace) + values_bytes(rows, lora->rank);
+    l.parts = parts_for(in_dtype, out_dtype == GEMM_F32);
+    const bool tc = lora_tc_takes(l);
     cudaError_t err = cudaSuccess;
     if (l.adapters > 0)
-        err = lora_simt_shrink(l, s);
+        err = tc ? lora_shrink_tc_launch(l, nullptr, s) : lora_simt_shrink(l, s);
     if (err == cudaSuccess)
-        err = lora_simt_expand(l, s);
+        err = tc ? lora_expand_tc_launch(l, s) : lora_simt_expand(l, s);
     return status_of(err);
 }
 

@@ -1,48 +1,16 @@
-// Host side of the row-grouped tensor-core kernel: tensor maps and the launch.
+// Host side of the row-grouped tensor-core kernel: its launch.
 #pragma once
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
-#include "device.h"
+#include "grouped_maps.h"
 #include "grouped_tc.cuh"
 #include "launch.h"
 #include "persistent.cuh"
 
 namespace tmmo {
-
-inline int type_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
-
-// A tensor of up to three dimensions, innermost first, in boxes whose rows are
-// 128 bytes, swizzled; strides in elements.
-inline bool encode_map(CUtensorMap* map, int dt, const void* base, int rank, const int64_t (&dims)[3],
-                       const int64_t (&strides)[2], const uint32_t (&box)[3])
-{
-    auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
-    if (!fn)
-        return false;
-    const CUtensorMapDataType type = dt == DT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                     : dt == DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    cuuint64_t d[3], s[2];
-    for (int i = 0; i < 3; ++i)
-        d[i] = static_cast<cuuint64_t>(dims[i]);
-    for (int i = 0; i < 2; ++i)
-        s[i] = static_cast<cuuint64_t>(strides[i]) * type_bytes(dt);
-    const cuuint32_t step[3] = {1, 1, 1};
-    return fn(map, type, rank, const_cast<void*>(base), d, s, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Whether TMA can address rows of this pitch (elements).
-inline bool aligned_rows(const void* p, int64_t ld, int dt)
-{
-    return aligned16(p) && (ld * type_bytes(dt)) % 16 == 0;
-}
 
 template <int MODE, typename OutT>
 cudaError_t launch_grouped_tc(const CUtensorMap (&maps)[4], const GroupedTcParams& p, int64_t most_work,

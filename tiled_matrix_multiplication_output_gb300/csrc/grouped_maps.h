@@ -1,0 +1,45 @@
+// Tensor maps of the row-grouped products and the adapters (host side).
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "device.h"
+#include "launch.h"
+
+namespace tmmo {
+
+inline int type_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+// A tensor of up to three dimensions, innermost first, in boxes whose rows are
+// 128 bytes, swizzled; strides in elements.
+inline bool encode_map(CUtensorMap* map, int dt, const void* base, int rank, const int64_t (&dims)[3],
+                       const int64_t (&strides)[2], const uint32_t (&box)[3])
+{
+    auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+    if (!fn)
+        return false;
+    const CUtensorMapDataType type = dt == DT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dt == DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    cuuint64_t d[3], s[2];
+    for (int i = 0; i < 3; ++i)
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+    for (int i = 0; i < 2; ++i)
+        s[i] = static_cast<cuuint64_t>(strides[i]) * type_bytes(dt);
+    const cuuint32_t step[3] = {1, 1, 1};
+    return fn(map, type, rank, const_cast<void*>(base), d, s, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether TMA can address rows of this pitch (elements).
+inline bool aligned_rows(const void* p, int64_t ld, int dt)
+{
+    return aligned16(p) && (ld * type_bytes(dt)) % 16 == 0;
+}
+
+}  // namespace tmmo

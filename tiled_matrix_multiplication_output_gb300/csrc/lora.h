@@ -36,7 +36,10 @@ struct LoraLaunch {
     int64_t ldy;
     int rows, N, K, adapters, rank;
     int in_dtype, out_dtype;  // DT_*
-    float* t;             // rows x rank
+    float* t;             // FP32 units: rows x rank
+    void* t16;            // tensor cores: the same in parts (lora_tc.cuh)
+    int parts;
+    void* plan;           // one for each 128 rows
     int num_sms;
     int* status;
     long long wait_budget;
@@ -58,6 +61,19 @@ struct LoraGradLaunch {
     long long wait_budget;
 };
 
+// Bytes of a row tile's plan, and of rank values in parts for a row.
+constexpr int LORA_PLAN_BYTES = 2576;
+int lora_parts_bytes(int rank, int parts);
+
+// The tensor-core kernels, for 16-bit operands with rows on 16-byte boundaries.
+// Shrink makes the plans and the rank values; of two products, whose rows have the
+// same adapters, in one launch.  Expand may start while a shrink runs.
+bool lora_tc_takes(const LoraLaunch& l);
+cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* second, cudaStream_t stream);
+cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream);
+cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream);
+
+// The FP32 units, for every operand.
 cudaError_t lora_simt_shrink(const LoraLaunch& l, cudaStream_t stream);
 cudaError_t lora_simt_expand(const LoraLaunch& l, cudaStream_t stream);
 cudaError_t lora_simt_grad(const LoraGradLaunch& l, cudaStream_t stream);

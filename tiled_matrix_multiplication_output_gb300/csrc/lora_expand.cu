@@ -1,0 +1,488 @@
+// Y = X W^T + t E^T on the tensor cores, for products with many output tiles: the
+// shared product and every adapter's in one accumulator.
+//
+// The kernel is the CTA-pair GEMM (256 x 256 tiles, two 64-deep K steps per
+// stage) whose contraction goes on, for each adapter among the tile's rows, over
+// its rank values: A is then t in parts, B the adapter's factor, and the lanes
+// of other adapters' rows are masked out.  An adapter of rank 64 costs two more
+// K steps (of 64 at K = 4096) in the tiles that have it, and Y is written
+// once.  Bound by the tensor cores as the shared product alone.
+//
+// Launched as a programmatic dependent of the kernel that makes the rank values: it
+// waits for them only when the first tile's shared product has been issued.
+#include <algorithm>
+
+#include "grouped_launch.cuh"
+#include "lora_tc.cuh"
+
+namespace tmmo {
+namespace {
+
+constexpr int LE_STAGES = 3;
+constexpr int LE_KSUB = 2;
+
+struct ExpandParams {
+    int M, N, k_blocks, rank;
+    int tiles_m, tiles_n;
+    bool adapters;        // there are any: plans and rank values are made
+    bool one;             // one factor for every adapter
+    LoraParts lay;
+    const LoraPlan* plan;
+    void* C;
+    int64_t ldc;
+    bool tma_out;
+    uint32_t idesc, idesc_e;
+    int* status;
+    long long wait_budget;
+    int fault_skip_kblock;
+};
+
+struct ExpandLayout {
+    static constexpr int SUB = 16384;
+    static constexpr int STEPS = LE_STAGES * LE_KSUB;
+    static constexpr int OFF_A = 0;
+    static constexpr int OFF_B = STEPS * SUB;
+    static constexpr int OFF_STAGING = OFF_B + STEPS * SUB;
+    static constexpr int OFF_BAR = OFF_STAGING + 4 * 2 * TC_STAGING_BYTES;
+    static constexpr int NUM_BARS = STEPS + LE_STAGES + 5;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
+    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
+    static_assert(SMEM_ALLOC <= 232448, "exceeds 227 KiB of dynamic shared memory");
+};
+
+// The adapters of a pair's 256 rows, ascending, from the plans of its halves.
+struct PairAdapters {
+    const LoraPlan* half[2];
+    int count[2], at[2];
+
+    __device__ PairAdapters(const ExpandParams& p, int mb)
+    {
+        const int plans = (p.M + LT_ROWS - 1) / LT_ROWS;
+        for (int h = 0; h < 2; ++h) {
+            half[h] = p.plan + 2 * mb + h;
+            count[h] = 2 * mb + h < plans ? half[h]->count : 0;
+            at[h] = 0;
+        }
+    }
+    // The next adapter, or -1, and (off) the lanes that do not have it.
+    __device__ int next(uint32_t (&off)[8])
+    {
+        int g[2];
+        for (int h = 0; h < 2; ++h)
+            g[h] = at[h] < count[h] ? half[h]->ids[at[h]] : 0x7fffffff;
+        const int least = min(g[0], g[1]);
+        if (least == 0x7fffffff)
+            return -1;
+        for (int h = 0; h < 2; ++h) {
+            const bool has = g[h] == least;
+            for (int w = 0; w < 4; ++w)
+                off[4 * h + w] = has ? ~half[h]->rows[at[h]][w] : ~0u;
+            at[h] += has;
+        }
+        return least;
+    }
+};
+
+template <bool ACROSS, typename OutT>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    lora_expand_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmE,
+                       const __grid_constant__ CUtensorMap tmC, const ExpandParams p)
+{
+    using L = ExpandLayout;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + L::OFF_BAR;
+    auto full_bar = [&](int s, int j) { return bar0 + 8u * (s * LE_KSUB + j); };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (L::STEPS + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (L::STEPS + LE_STAGES + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (L::STEPS + LE_STAGES + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (L::STEPS + LE_STAGES + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int unit = blockIdx.x >> 1, num_units = gridDim.x >> 1;
+    const int num_tiles = p.tiles_m * p.tiles_n;
+    const TcWatch watch{abort_flag, p.status, p.wait_budget};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < LE_STAGES; ++s) {
+            for (int j = 0; j < LE_KSUB; ++j)
+                mbar_init(full_bar(s, j), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), 8);  // every epilogue warp of the pair
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmT);
+        tma_prefetch_desc(&tmE);
+        tma_prefetch_desc(&tmC);
+    }
+    if (warp == 1) {
+        tmem_alloc<2>(smem_u32(tmem_slot), 512);
+        tmem_relinquish<2>();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    // row tiles eight at a time, and within those down the rows first
+    auto coords = [&](int t, int& mb, int& nb) {
+        const int band = t / (8 * p.tiles_n) * 8;
+        const int high = min(p.tiles_m - band, 8);
+        const int u = t - band * p.tiles_n;
+        mb = band + u % high;
+        nb = u / high;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const uint32_t sA = sbase + L::OFF_A, sB = sbase + L::OFF_B;
+            int stage = 0, sub = 0;
+            uint32_t phase = 0;
+            int issued[L::STEPS];
+#pragma unroll
+            for (int s = 0; s < L::STEPS; ++s)
+                issued[s] = 0;
+            bool ok = true, waited = false;
+            auto next_stage = [&] {
+                sub = 0;
+                if (++stage == LE_STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            };
+            // One K step: load(A's place, B's place, barrier).
+            auto step = [&](bool skip, auto load) {
+                if (sub == 0 && !tc_wait(empty_bar(stage), phase ^ 1, watch))
+                    return false;
+                if (!skip) {
+                    const int at = stage * LE_KSUB + sub;
+                    if (leader)
+                        mbar_arrive_expect_tx(full_bar(stage, sub), 4 * L::SUB);
+                    for (int s = 0; s < L::STEPS; ++s)  // (registers: no indexing)
+                        issued[s] += s == at;
+                    load(sA + at * L::SUB, sB + at * L::SUB, mapa_shared(full_bar(stage, sub), 0));
+                }
+                if (++sub == LE_KSUB)
+                    next_stage();
+                return true;
+            };
+            for (int t = unit; ok && t < num_tiles; t += num_units) {
+                int mb, nb;
+                coords(t, mb, nb);
+                const int row = mb * 256 + static_cast<int>(rank) * TC_BM;
+                const int col = nb * 256 + static_cast<int>(rank) * TC_BM;
+                for (int kb = 0; ok && kb < p.k_blocks; ++kb) {
+                    const int k = kb * TC_BK;
+                    ok = step(kb == p.fault_skip_kblock, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                        tma_load_2d_pair(dA, &tmX, bar, k, row);
+                        if (ACROSS) {
+                            tma_load_2d_pair(dB, &tmW, bar, col, k);
+                            tma_load_2d_pair(dB + 8192, &tmW, bar, col + 64, k);
+                        } else {
+                            tma_load_2d_pair(dB, &tmW, bar, k, col);
+                        }
+                    });
+                }
+                if (!ok)
+                    break;
+                if (p.adapters) {
+                    if (!waited)
+                        grid_dep_wait();
+                    waited = true;
+                    PairAdapters list(p, mb);
+                    uint32_t off[8];
+                    for (int g = list.next(off); ok && g >= 0; g = list.next(off)) {
+                        const int z = p.one ? 0 : g;
+                        for (int c = 0; ok && c < p.lay.chunks; ++c) {
+                            const int j = c * p.lay.chunk;
+                            ok = step(false, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                                tma_load_2d_pair(dA, &tmT, bar, c * 64, row);
+                                if (ACROSS) {
+                                    tma_load_3d_pair(dB, &tmE, bar, col, j, z);
+                                    tma_load_3d_pair(dB + 8192, &tmE, bar, col + 64, j, z);
+                                } else {
+                                    tma_load_3d_pair(dB, &tmE, bar, j, col, z);
+                                }
+                            });
+                        }
+                    }
+                }
+                if (ok && sub != 0) {
+                    if (leader)
+                        mbar_arrive(full_bar(stage, 1));  // the stage's unused step
+                    issued[1] += stage == 0;
+                    issued[3] += stage == 1;
+                    issued[5] += stage == 2;
+                    next_stage();
+                }
+            }
+            if (!ok && leader) {
+                // wait (bounded) for the loads already issued, of both CTAs,
+                // before shared memory goes away
+                for (int s = 0; s < L::STEPS; ++s) {
+                    const long long t0 = clock64();
+                    while (issued[s] > 0 && !mbar_try_wait(bar0 + 8u * s, (issued[s] - 1) & 1) &&
+                           clock64() - t0 < p.wait_budget) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (leader && lane == 0) {
+            const uint32_t sA = sbase + L::OFF_A, sB = sbase + L::OFF_B;
+            int stage = 0, sub = 0, local = 0;
+            uint32_t phase = 0;
+            bool ok = true, waited = false;
+            auto next_stage = [&] {
+                tc_commit_pair(empty_bar(stage), 0x3);
+                sub = 0;
+                if (++stage == LE_STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            };
+            auto step = [&](auto multiply) {
+                if (!tc_wait(full_bar(stage, sub), phase, watch))
+                    return false;
+                tc_fence_after();
+                const int at = stage * LE_KSUB + sub;
+                multiply(sA + at * L::SUB, sB + at * L::SUB);
+                if (++sub == LE_KSUB)
+                    next_stage();
+                return true;
+            };
+            for (int t = unit; ok && t < num_tiles; t += num_units, ++local) {
+                int mb, nb;
+                coords(t, mb, nb);
+                const int acc = local & 1;
+                if (!tc_wait<true>(tempty_bar(acc), ((local >> 1) & 1) ^ 1, watch)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+                for (int kb = 0; ok && kb < p.k_blocks; ++kb)
+                    ok = step([&](uint32_t a0, uint32_t b0) {
+#pragma unroll
+                        for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
+                            tc_mma_f16<2>(d_tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
+                                          ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                 : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                          p.idesc, kb != 0 || k != 0);
+                    });
+                if (!ok)
+                    break;
+                if (p.adapters) {
+                    if (!waited)
+                        grid_dep_wait();
+                    waited = true;
+                    PairAdapters list(p, mb);
+                    uint32_t off[8];
+                    for (int g = list.next(off); ok && g >= 0; g = list.next(off))
+                        for (int c = 0; ok && c < p.lay.chunks; ++c)
+                            ok = step([&](uint32_t a0, uint32_t b0) {
+                                const int deep = p.lay.deep(c, p.rank);
+                                for (int part = 0; part < p.lay.parts; ++part)
+                                    for (int k = 0; k < deep; ++k)
+                                        tc_mma_f16_lanes(
+                                            d_tmem,
+                                            smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
+                                            ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                   : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                            p.idesc, 1, off);
+                            });
+                }
+                if (!ok)
+                    break;
+                if (sub != 0)
+                    next_stage();
+                tc_commit_pair(tfull_bar(acc), 0x3);
+            }
+            // Wait (bounded) until every MMA issued so far has completed, so
+            // TMEM and the input stages are no longer in use.
+            tc_commit_self<2>(drain_bar);
+            const long long t0 = clock64();
+            while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue
+        const int q = warp & 3;  // TMEM lane quarter this warp may access
+        const uint32_t staging0 = sbase + L::OFF_STAGING + q * 2 * TC_STAGING_BYTES;
+        const uint32_t leader_tempty0 = mapa_shared(tempty_bar(0), 0);
+        const uint32_t leader_tempty1 = mapa_shared(tempty_bar(1), 0);
+        OutT* const out = static_cast<OutT*>(p.C);
+        TcParams plain{};
+        plain.alpha = 1.0f;
+        GroupedTcParams store{};
+        store.alpha = 1.0f;
+        int local = 0;
+        uint32_t buf = 0;
+        for (int t = unit; t < num_tiles; t += num_units, ++local) {
+            int mb, nb;
+            coords(t, mb, nb);
+            const int acc = local & 1;
+            int ok = 1;
+            if (lane == 0)
+                ok = tc_wait(tfull_bar(acc), (local >> 1) & 1, watch) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok)
+                break;
+            tc_fence_after();
+            const int row = mb * 256 + static_cast<int>(rank) * TC_BM + q * 32;
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                   static_cast<uint32_t>(acc * 256);
+            const int cols = min(256, p.N - nb * 256);
+            if (row < p.M && p.tma_out) {
+                constexpr int STRIP = TcOut<OutT>::STRIP;
+#pragma unroll 1
+                for (int s = 0; s < cols; s += STRIP) {
+                    const uint32_t stg = staging0 + buf * TC_STAGING_BYTES;
+                    if (lane == 0)
+                        bulk_wait_group_read<1>();
+                    __syncwarp();
+                    tc_strip_to_smem<OutT>(t_row + s, stg, lane, plain, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tmC, stg, nb * 256 + s, row);
+                        bulk_commit_group();
+                    }
+                    buf ^= 1;
+                }
+            } else if (row < p.M) {
+#pragma unroll 1
+                for (int s = 0; s < cols; s += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(t_row + s, v);
+                    tmem_wait_ld(v);
+                    grouped_strip(v, staging0, lane, out + row * p.ldc + nb * 256 + s, p.ldc,
+                                  min(32, p.M - row), cols - s, store);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(acc ? leader_tempty1 : leader_tempty0);
+        }
+        if (lane == 0)
+            bulk_wait_group_read<0>();
+        __syncwarp();
+    }
+
+    // ---------------------------------------------------- teardown
+    __syncwarp();  // reconverge each warp after its role's divergent loop
+    if (p.adapters)
+        grid_dep_wait();  // this grid must not end before the one it depends on
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc<2>(tmem_base, 512);
+    }
+}
+
+template <bool ACROSS, typename OutT>
+cudaError_t launch(const CUtensorMap (&m)[5], const ExpandParams& p, int num_sms, cudaStream_t stream)
+{
+    using L = ExpandLayout;
+    static ClusterCaps caps;
+    int cap = 0;
+    const cudaError_t err =
+        cluster_cap(lora_expand_kernel<ACROSS, OutT>, caps, 2, TC_THREADS, L::SMEM_ALLOC, num_sms, &cap);
+    if (err != cudaSuccess)
+        return err;
+    const int64_t units = std::min<int64_t>(std::max(cap, 1), static_cast<int64_t>(p.tiles_m) * p.tiles_n);
+    ClusterLaunch l(static_cast<unsigned>(2 * units), 2, TC_THREADS, L::SMEM_ALLOC, stream, p.adapters);
+    return l.run(lora_expand_kernel<ACROSS, OutT>, m[0], m[1], m[2], m[3], m[4], p);
+}
+
+template <bool ACROSS>
+cudaError_t launch(int out_dtype, const CUtensorMap (&m)[5], const ExpandParams& p, int num_sms,
+                   cudaStream_t stream)
+{
+    switch (out_dtype) {
+    case DT_F32:
+        return launch<ACROSS, float>(m, p, num_sms, stream);
+    case DT_F16:
+        return launch<ACROSS, __half>(m, p, num_sms, stream);
+    default:
+        return launch<ACROSS, __nv_bfloat16>(m, p, num_sms, stream);
+    }
+}
+
+}  // namespace
+
+int lora_parts_bytes(int rank, int parts) { return 2 * lora_parts(rank, parts).columns(); }
+
+bool lora_tc_takes(const LoraLaunch& l)
+{
+    if (l.in_dtype == DT_F32 || l.K == 0)
+        return false;
+    const int dt = l.in_dtype;
+    auto stack = [&](const void* p, int64_t ld, int64_t stride) {
+        return aligned_rows(p, ld, dt) &&
+               (l.adapters == 1 || stride == 0 || (stride >= ld && (stride * type_bytes(dt)) % 16 == 0));
+    };
+    return aligned_rows(l.X, l.ldx, dt) && (!l.W || aligned_rows(l.W, l.ldw, dt)) &&
+           (l.adapters == 0 || (stack(l.F, l.ldf, l.stride_f) && stack(l.E, l.lde, l.stride_e)));
+}
+
+cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
+{
+    ExpandParams p{};
+    p.M = l.rows;
+    p.N = l.N;
+    p.k_blocks = (l.K + TC_BK - 1) / TC_BK;
+    p.rank = l.rank;
+    p.tiles_m = (l.rows + 255) / 256;
+    p.tiles_n = (l.N + 255) / 256;
+    p.adapters = l.adapters > 0;
+    p.one = l.adapters == 1 || l.stride_e == 0;
+    p.lay = lora_parts(l.rank, l.parts);
+    p.plan = static_cast<const LoraPlan*>(l.plan);
+    p.C = l.Y;
+    p.ldc = l.ldy;
+    p.idesc = tc_idesc(l.in_dtype == DT_BF16, 256, 256, false, l.across);
+    p.status = l.status;
+    p.wait_budget = l.wait_budget;
+    p.fault_skip_kblock = l.fault_skip_kblock;
+    CUtensorMap m[5];
+    const int dt = l.in_dtype;
+    bool ok = encode_map(&m[0], dt, l.X, 2, {l.K, l.rows, 1}, {l.ldx, 0}, {64, TC_BM, 1}) &&
+              (l.across ? encode_map(&m[1], dt, l.W, 2, {l.N, l.K, 1}, {l.ldw, 0}, {64, TC_BK, 1})
+                        : encode_map(&m[1], dt, l.W, 2, {l.K, l.N, 1}, {l.ldw, 0}, {64, TC_BM, 1}));
+    m[2] = m[3] = m[4] = m[0];
+    if (ok && p.adapters) {
+        const int64_t stacked = p.one ? 1 : l.adapters, stride = p.one ? l.lde : l.stride_e;
+        ok = encode_map(&m[2], dt, l.t16, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, TC_BM, 1}) &&
+             (l.across ? encode_map(&m[3], dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
+                       : encode_map(&m[3], dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride}, {64, TC_BM, 1}));
+    }
+    if (!ok)
+        return cudaErrorNotSupported;
+    p.tma_out = aligned_rows(l.Y, l.ldy, l.out_dtype) &&
+                encode_map(&m[4], l.out_dtype, l.Y, 2, {l.N, l.rows, 1}, {l.ldy, 0},
+                           {128u / type_bytes(l.out_dtype), 32, 1});
+    return l.across ? launch<true>(l.out_dtype, m, p, l.num_sms, stream)
+                    : launch<false>(l.out_dtype, m, p, l.num_sms, stream);
+}
+
+}  // namespace tmmo

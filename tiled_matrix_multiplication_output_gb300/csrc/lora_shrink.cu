@@ -1,0 +1,379 @@
+// Rank values t = scale * X F^T of every row's adapter on the tensor cores, and
+// the plans of the row tiles.
+//
+// With rank r, a row tile of X (128 rows) is read once for 2 * 128 * r
+// operations a column: the bound is reading X from HBM, and for few rows the
+// adapters' factors.  So a tile's contraction is split over a cluster of up to
+// eight CTAs, and where that still leaves SMs idle its adapters are dealt out to
+// several clusters (their rows are disjoint): 8192 rows are 64 tiles on 2
+// CTAs each, 64 rows of 64 adapters one tile on 8 x 16.  The FP32 sums of a
+// cluster are added through distributed shared memory in rank order.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "grouped_maps.h"
+#include "lora_tc.cuh"
+#include "persistent.cuh"
+
+namespace tmmo {
+namespace {
+
+constexpr int LS_THREADS = 256;  // warps 0: copies, 1: MMA, 4-7: accumulator
+constexpr int LS_MAX_STAGES = 8;
+constexpr int LS_RING = 192 * 1024;
+
+struct ShrinkSide {
+    int k_blocks;
+    int across;
+    int one;  // one factor for every adapter
+    uint32_t idesc;
+    void* t;  // parts, rows x columns()
+};
+
+struct ShrinkParams {
+    ShrinkSide side[2];
+    const int32_t* adapter;
+    const float* scale;
+    LoraPlan* plan;
+    int rows, adapters, rank, cols;  // cols: rank rounded up to 16
+    LoraParts lay;
+    int tiles, deal;                 // row tiles; clusters that share a tile's adapters
+    int stages, stage_bytes, b_bytes[2];
+    uint32_t tmem_cols;
+    int* status;
+    long long wait_budget;
+};
+
+struct ShrinkSmem {
+    uint64_t full[LS_MAX_STAGES], empty[LS_MAX_STAGES], done;
+    uint32_t tmem;
+    int abort_flag;
+    int of[LT_ROWS];   // each row's adapter, then its place in the plan
+    int first[LT_ROWS];  // whether the row is the first of its adapter
+    LoraPlan plan;
+};
+
+// The plan of 128 rows from their adapters s.of; every thread calls it.
+__device__ __forceinline__ void make_plan(ShrinkSmem& s, const int32_t* adapter, int row0, int rows, int adapters)
+{
+    const int i = threadIdx.x;
+    if (i < LT_ROWS) {
+        const int g = row0 + i < rows ? adapter[row0 + i] : -1;
+        s.of[i] = g >= 0 && g < adapters ? g : -1;
+        for (int w = 0; w < 4; ++w)
+            s.plan.rows[i][w] = 0;
+    }
+    if (i == 0)
+        s.plan.count = 0;
+    __syncthreads();
+    const int g = i < LT_ROWS ? s.of[i] : -1;
+    if (i < LT_ROWS) {
+        bool first = g >= 0;
+        for (int j = 0; j < i; ++j)
+            first = first && s.of[j] != g;
+        s.first[i] = first;
+    }
+    __syncthreads();
+    int place = -1;
+    if (g >= 0) {
+        place = 0;
+        for (int j = 0; j < LT_ROWS; ++j)
+            place += s.first[j] && s.of[j] < g;
+        if (s.first[i]) {
+            s.plan.ids[place] = g;
+            atomicAdd(&s.plan.count, 1);
+        }
+        atomicOr(&s.plan.rows[place][i >> 5], 1u << (i & 31));
+    }
+    __syncthreads();
+    if (i < LT_ROWS)
+        s.of[i] = place;
+    __syncthreads();
+}
+
+template <typename T>
+__device__ __forceinline__ void store_parts(T* t, float v, const LoraParts& lay, int j)
+{
+    t += j / lay.chunk * 64 + j % lay.chunk;
+    float left = v;
+    for (int p = 0; p < lay.parts; ++p) {
+        T h;
+        put(&h, left);
+        t[p * lay.chunk] = h;
+        const float f = to_f32(h);
+        left = isfinite(f) ? left - f : 0.0f;  // an infinity has no remainder
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(LS_THREADS, 1)
+    lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX0, const __grid_constant__ CUtensorMap tmF0,
+                          const __grid_constant__ CUtensorMap tmX1, const __grid_constant__ CUtensorMap tmF1,
+                          const ShrinkParams p, int splits)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    __shared__ ShrinkSmem s;
+    grid_dep_launch_dependents();  // the product that uses t may start with what it has
+
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31;
+    const int split = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    int id = blockIdx.x / splits;
+    const int tile = id % p.tiles;
+    id /= p.tiles;
+    const int deal = id % p.deal, which = id / p.deal;
+    const ShrinkSide side = p.side[which];
+    const CUtensorMap* tmX = which ? &tmX1 : &tmX0;
+    const CUtensorMap* tmF = which ? &tmF1 : &tmF0;
+    const int b_bytes = p.b_bytes[which];
+    const int row0 = tile * LT_ROWS;
+    const TcWatch watch{&s.abort_flag, p.status, p.wait_budget};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.empty[i]), 1);
+        }
+        mbar_init(smem_u32(&s.done), 1);
+        s.abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(tmX);
+        tma_prefetch_desc(tmF);
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(smem_u32(&s.tmem), p.tmem_cols);
+        tmem_relinquish<1>();
+    }
+    make_plan(s, p.adapter, row0, p.rows, p.adapters);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    if (which == 0 && deal == 0 && split == 0) {
+        const int* from = reinterpret_cast<const int*>(&s.plan);
+        int* to = reinterpret_cast<int*>(p.plan + tile);
+        const int words = 1 + LT_ROWS + 4 * s.plan.count;  // the rows of absent adapters are not read
+        for (int i = threadIdx.x; i < words; i += LS_THREADS)
+            to[i] = from[i];
+    }
+    const int per = (side.k_blocks + splits - 1) / splits;
+    const int kb0 = min(split * per, side.k_blocks), kb1 = min(kb0 + per, side.k_blocks);
+    const int mine = s.plan.count > deal ? (s.plan.count - deal + p.deal - 1) / p.deal : 0;
+    const int steps = mine * (kb1 - kb0);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, n = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int a = deal; ok && a < s.plan.count; a += p.deal) {
+                const int g = side.one ? 0 : s.plan.ids[a];
+                for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                    if (!tc_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&s.full[stage]);
+                    const uint32_t dA = smem_u32(ring) + stage * p.stage_bytes, dB = dA + 16384;
+                    mbar_arrive_expect_tx(bar, 16384 + b_bytes);
+                    tma_load_2d(dA, tmX, bar, kb * TC_BK, row0);
+                    if (side.across) {
+                        for (int b = 0; b * 8192 < b_bytes; ++b)
+                            tma_load_3d(dB + b * 8192, tmF, bar, b * 64, kb * TC_BK, g);
+                    } else {
+                        tma_load_3d(dB, tmF, bar, kb * TC_BK, 0, g);
+                    }
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {  // wait (bounded) for the copies in flight before shared memory goes away
+                for (int i = 0; i < p.stages; ++i) {
+                    const int uses = n / p.stages + (i < n % p.stages);
+                    const long long t0 = clock64();
+                    while (uses > 0 && !mbar_try_wait(smem_u32(&s.full[i]), (uses - 1) & 1) &&
+                           clock64() - t0 < p.wait_budget) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && steps > 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int a = deal; ok && a < s.plan.count; a += p.deal) {
+                uint32_t off[4];
+                for (int w = 0; w < 4; ++w)
+                    off[w] = ~s.plan.rows[a][w];
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!tc_wait(smem_u32(&s.full[stage]), phase, watch)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(ring) + stage * p.stage_bytes, b0 = a0 + 16384;
+#pragma unroll
+                    for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
+                        tc_mma_f16_lanes(tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
+                                         side.across ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                     : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                         side.idesc, kb != kb0 || k != 0, off);
+                    tc_commit(smem_u32(&s.empty[stage]));
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            tc_commit(smem_u32(&s.done));  // also after giving up: nothing may run on
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(&s.done), 0) && clock64() - t0 < p.wait_budget) {
+            }
+        }
+    }
+    // The sums to shared memory; the ring holds nothing any more.
+    __syncwarp();
+    const int pitch = p.cols + 1;
+    float* sums = reinterpret_cast<float*>(ring);
+    if (warp >= 4) {
+        const int row = (warp & 3) * 32 + lane;
+        if (steps > 0) {
+            int ok = 1;
+            if (lane == 0)
+                ok = tc_wait(smem_u32(&s.done), 0, watch) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (ok) {
+                tc_fence_after();
+                for (int j = 0; j < p.cols; j += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j, v);
+                    tmem_wait_ld(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sums[row * pitch + j + i] = __uint_as_float(v[i]);
+                }
+            }
+        } else {
+            for (int j = 0; j < p.cols; ++j)
+                sums[row * pitch + j] = 0.0f;
+        }
+        tc_fence_before();
+    }
+    if (splits > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc<1>(tmem, p.tmem_cols);
+    // Each CTA adds up and stores its share of the rows.
+    int gave_up = s.abort_flag;
+    for (int k = 0; k < splits && splits > 1; ++k)
+        gave_up |= __float_as_int(ld_cluster_f32(mapa_shared(smem_u32(&s.abort_flag), k)));
+    const int share = LT_ROWS / splits;
+    const int columns = p.lay.columns();
+    T* t = static_cast<T*>(side.t);
+    for (int i = threadIdx.x; i < share * p.cols && !gave_up; i += LS_THREADS) {
+        const int row = split * share + i / p.cols, j = i % p.cols;
+        const int place = s.of[row];
+        if (row0 + row >= p.rows || (place < 0 ? deal != 0 : place % p.deal != deal))
+            continue;
+        float sum = 0.0f;
+        if (place >= 0 && j < p.rank) {
+            if (splits == 1) {
+                sum = sums[row * pitch + j];
+            } else {
+                const uint32_t at = smem_u32(&sums[row * pitch + j]);
+                for (int k = 0; k < splits; ++k)
+                    sum += ld_cluster_f32(mapa_shared(at, k));
+            }
+            if (p.scale)
+                sum *= p.scale[s.plan.ids[place]];
+        }
+        store_parts(t + static_cast<int64_t>(row0 + row) * columns, sum, p.lay, j);
+    }
+    if (splits > 1) {
+        __syncwarp();
+        cluster_sync();  // nobody leaves while others read its sums
+    }
+}
+
+template <typename T>
+cudaError_t launch(const CUtensorMap (&m)[4], const ShrinkParams& p, unsigned blocks, int splits, int smem,
+                   cudaStream_t stream)
+{
+    static ClusterCaps caps;
+    int cap = 0;
+    const cudaError_t err = cluster_cap(lora_shrink_tc_kernel<T>, caps, 1, LS_THREADS, LS_RING + 1024, 1, &cap);
+    if (err != cudaSuccess)
+        return err;
+    ClusterLaunch l(blocks, splits, LS_THREADS, smem, stream);
+    return l.run(lora_shrink_tc_kernel<T>, m[0], m[1], m[2], m[3], p, splits);
+}
+
+}  // namespace
+
+cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* second, cudaStream_t stream)
+{
+    const LoraLaunch& l = first;
+    ShrinkParams p{};
+    p.adapter = l.adapter;
+    p.scale = l.scale;
+    p.plan = static_cast<LoraPlan*>(l.plan);
+    p.rows = l.rows;
+    p.adapters = l.adapters;
+    p.rank = l.rank;
+    p.cols = (l.rank + 15) / 16 * 16;
+    p.lay = lora_parts(l.rank, l.parts);
+    p.tiles = (l.rows + LT_ROWS - 1) / LT_ROWS;
+    p.tmem_cols = 32;
+    while (p.tmem_cols < static_cast<uint32_t>(p.cols))
+        p.tmem_cols *= 2;
+    p.status = l.status;
+    p.wait_budget = l.wait_budget;
+    CUtensorMap m[4];
+    const int sides = second ? 2 : 1;
+    int most_k = 1;
+    for (int i = 0; i < sides; ++i) {
+        const LoraLaunch& s = i ? *second : first;
+        const uint32_t cols = static_cast<uint32_t>(p.cols);
+        p.side[i] = {(s.K + TC_BK - 1) / TC_BK, s.across, s.adapters == 1 || s.stride_f == 0, tc_idesc(s.in_dtype == DT_BF16, LT_ROWS, p.cols, false, s.across),
+                     s.t16};
+        p.b_bytes[i] = (s.across ? (p.cols + 63) / 64 * 64 : p.cols) * 128;
+        most_k = std::max(most_k, p.side[i].k_blocks);
+        const int64_t stride = p.side[i].one ? s.ldf : s.stride_f;
+        const int64_t stacked = p.side[i].one ? 1 : s.adapters;
+        if (!encode_map(&m[2 * i], s.in_dtype, s.X, 2, {s.K, s.rows, 1}, {s.ldx, 0}, {64, LT_ROWS, 1}) ||
+            !(s.across ? encode_map(&m[2 * i + 1], s.in_dtype, s.F, 3, {s.rank, s.K, stacked}, {s.ldf, stride},
+                                    {64, TC_BK, 1})
+                       : encode_map(&m[2 * i + 1], s.in_dtype, s.F, 3, {s.K, s.rank, stacked}, {s.ldf, stride},
+                                    {64, cols, 1})))
+            return cudaErrorNotSupported;
+    }
+    if (sides == 1) {
+        m[2] = m[0];
+        m[3] = m[1];
+    }
+    p.stage_bytes = 16384 + std::max(p.b_bytes[0], p.b_bytes[1]);
+    p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
+    p.stages = std::min(LS_MAX_STAGES, LS_RING / p.stage_bytes);
+    // CTAs for every SM: first the contraction is split, then the adapters
+    // dealt out.
+    int splits = 1;
+    while (splits < 8 && 2 * splits <= most_k && p.tiles * sides * splits * 2 <= l.num_sms)
+        splits *= 2;
+    const int most_adapters = std::min(std::min(l.adapters, LT_ROWS), l.rows);
+    p.deal = std::max(1, std::min(most_adapters, l.num_sms / (p.tiles * sides * splits)));
+    const int64_t blocks = static_cast<int64_t>(p.tiles) * sides * splits * p.deal;
+    return l.in_dtype == DT_BF16
+               ? launch<__nv_bfloat16>(m, p, static_cast<unsigned>(blocks), splits, LS_RING + 1024, stream)
+               : launch<__half>(m, p, static_cast<unsigned>(blocks), splits, LS_RING + 1024, stream);
+}
+
+}  // namespace tmmo

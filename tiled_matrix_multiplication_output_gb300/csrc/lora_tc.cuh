@@ -1,0 +1,92 @@
+// Low-rank adapters on the tensor cores: what the kernels share.
+//
+// The rows of a 128-row tile may have different adapters.  One matrix
+// instruction multiplies all 128 rows by one adapter's factor, and its mask of
+// lanes keeps the result away from the rows of others: their accumulators are
+// not touched, whatever the factor holds.  A tile's plan lists its adapters,
+// ascending, with the rows of each.
+//
+// The rank values t are FP32 sums that enter a second product as operands of 16
+// bits, in parts: t = p0 + p1 (+ p2), each the rounding of what the ones before
+// leave, multiplied by the same factor.  Two parts hold 16 bits of a BF16 value
+// and 22 of an FP16 one, three hold 24.  They lie in chunks of `chunk` rank
+// values, 64 columns (128 bytes, a swizzle row) a chunk: part p of value j at
+// column (j / chunk) * 64 + p * chunk + j % chunk.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "lora.h"
+#include "ops.cuh"
+#include "simt_tile.cuh"
+
+namespace tmmo {
+
+constexpr int LT_ROWS = 128;  // rows of a tile, the lanes of a CTA
+
+struct LoraPlan {
+    int count;                  // adapters among the tile's rows
+    int ids[LT_ROWS];           // ascending
+    uint32_t rows[LT_ROWS][4];  // bit i of the i-th: row i has this adapter
+    int pad[3];
+};
+static_assert(sizeof(LoraPlan) == LORA_PLAN_BYTES, "size of a plan in the workspace");
+
+// D[tmem] (+)= A B for the lanes whose bit of `off` is clear.
+__device__ __forceinline__ void tc_mma_f16_lanes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate,
+                                                 const uint32_t (&off)[4])
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(off[0]), "r"(off[1]), "r"(off[2]),
+        "r"(off[3])
+        : "memory");
+}
+// The same on a CTA pair: the leader's lanes, then its peer's.
+__device__ __forceinline__ void tc_mma_f16_lanes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate,
+                                                 const uint32_t (&off)[8])
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8, %9, %10, %11, %12}, "
+        "p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(off[0]), "r"(off[1]), "r"(off[2]),
+        "r"(off[3]), "r"(off[4]), "r"(off[5]), "r"(off[6]), "r"(off[7])
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                            int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// How the rank values are laid out.
+struct LoraParts {
+    int parts, chunk, chunks;
+    __host__ __device__ int columns() const { return 64 * chunks; }
+    // 16-deep instructions of each part in chunk c
+    __host__ __device__ int deep(int c, int rank) const
+    {
+        const int left = rank - c * chunk;
+        return ((left < chunk ? left : chunk) + 15) / 16;
+    }
+};
+inline LoraParts lora_parts(int rank, int parts)
+{
+    const int chunk = rank <= 16 || parts == 3 ? 16 : 32;
+    return {parts, chunk, (rank + chunk - 1) / chunk};
+}
+
+}  // namespace tmmo
