@@ -142,7 +142,7 @@ extern "C" size_t gemm_lora_backward_workspace_size(int64_t rows, int64_t N, int
 {
     if (!valid_sizes(rows, N, K, adapters, rank) || rank > GEMM_MAX_RANK)
         return 0;
-    return static_cast<size_t>(2 * values_bytes(rows, rank));
+    return static_cast<size_t>(2 * values_bytes(rows, rank) + plan_bytes(rows));
 }
 
 extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int64_t ldx,
@@ -185,7 +185,7 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
     LoraLaunch l{};  // towards dX: rank values u = scale * D B
     l.X = D;
     l.ldx = ldd;
-    l.W = W;
+    l.W = dx ? W : nullptr;
     l.ldw = ldw;
     l.F = lora->B;
     l.ldf = lora->ldb;
@@ -216,48 +216,67 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
     f.ldf = lora->lda;
     f.stride_f = lora->stride_a;
     f.across = false;
+    f.W = nullptr;
+    f.E = lora->B;
+    f.lde = lora->ldb;
+    f.stride_e = lora->stride_b;
     f.N = static_cast<int>(N);
     f.K = static_cast<int>(K);
     f.t = reinterpret_cast<float*>(static_cast<char*>(workspace) + values_bytes(rows, lora->rank));
+
+    l.t16 = l.t;
+    f.t16 = f.t;
+    l.plan = f.plan = static_cast<char*>(workspace) + 2 * values_bytes(rows, lora->rank);
+    l.parts = f.parts = parts_for(in_dtype, out_dtype == GEMM_F32 || grad_dtype == GEMM_F32);
+
+    LoraGradLaunch a{};  // dA from X and u
+    a.P = X;
+    a.ldp = ldx;
+    a.t = l.t;
+    a.t16 = l.t16;
+    a.parts = l.parts;
+    a.plan = l.plan;
+    a.G = DA;
+    a.step_c = 1;
+    a.step_j = ldda;
+    a.stride_g = stride_da;
+    a.adapter = adapter;
+    a.rows = l.rows;
+    a.cols = static_cast<int>(K);
+    a.adapters = l.adapters;
+    a.rank = l.rank;
+    a.in_dtype = in_dtype;
+    a.out_dtype = grad_dtype;
+    d.fill(&a);
+    LoraGradLaunch b = a;  // dB from D and t
+    b.P = D;
+    b.ldp = ldd;
+    b.t = f.t;
+    b.t16 = f.t16;
+    b.G = DB;
+    b.step_c = lddb;
+    b.step_j = 1;
+    b.stride_g = stride_db;
+    b.cols = static_cast<int>(N);
 
     cudaError_t err = cudaSuccess;
     auto step = [&](bool wanted, auto launch) {
         if (wanted && err == cudaSuccess)
             err = launch();
     };
-    step(adapters && (dx || da), [&] { return lora_simt_shrink(l, s); });
+    const bool need_u = adapters && (dx || da);
+    if (rows > 0 && N > 0 && lora_tc_takes(l) && (!adapters || lora_tc_takes(f))) {
+        step(need_u || db, [&] {
+            return need_u ? lora_shrink_tc_launch(l, db ? &f : nullptr, s) : lora_shrink_tc_launch(f, nullptr, s);
+        });
+        step(dx, [&] { return lora_expand_tc_launch(l, s); });
+        step(da || db, [&] { return lora_grad_tc_launch({da ? &a : nullptr, db ? &b : nullptr}, s); });
+        return status_of(err);
+    }
+    step(need_u, [&] { return lora_simt_shrink(l, s); });
     step(dx, [&] { return lora_simt_expand(l, s); });
     step(db, [&] { return lora_simt_shrink(f, s); });
-
-    LoraGradLaunch g{};
-    g.adapter = adapter;
-    g.rows = static_cast<int>(rows);
-    g.adapters = l.adapters;
-    g.rank = l.rank;
-    g.in_dtype = in_dtype;
-    g.out_dtype = grad_dtype;
-    d.fill(&g);
-    step(da, [&] {
-        g.P = X;
-        g.ldp = ldx;
-        g.t = l.t;
-        g.cols = static_cast<int>(K);
-        g.G = DA;
-        g.step_c = 1;
-        g.step_j = ldda;
-        g.stride_g = stride_da;
-        return lora_simt_grad(g, s);
-    });
-    step(db, [&] {
-        g.P = D;
-        g.ldp = ldd;
-        g.t = f.t;
-        g.cols = static_cast<int>(N);
-        g.G = DB;
-        g.step_c = lddb;
-        g.step_j = 1;
-        g.stride_g = stride_db;
-        return lora_simt_grad(g, s);
-    });
+    step(da, [&] { return lora_simt_grad(a, s); });
+    step(db, [&] { return lora_simt_grad(b, s); });
     return status_of(err);
 }

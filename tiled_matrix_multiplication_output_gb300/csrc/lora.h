@@ -50,7 +50,10 @@ struct LoraLaunch {
 struct LoraGradLaunch {
     const void* P;        // rows x cols
     int64_t ldp;
-    const float* t;       // rows x rank
+    const float* t;       // FP32 units: rows x rank
+    const void* t16;      // tensor cores: in parts
+    int parts;
+    const void* plan;
     void* G;              // adapters; element (c, j) at c * step_c + j * step_j
     int64_t step_c, step_j, stride_g;
     const int32_t* adapter;
@@ -71,7 +74,8 @@ int lora_parts_bytes(int rank, int parts);
 bool lora_tc_takes(const LoraLaunch& l);
 cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* second, cudaStream_t stream);
 cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream);
-cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream);
+// Two gradients of the same rows in one launch (either may be null).
+cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStream_t stream);
 
 // The FP32 units, for every operand.
 cudaError_t lora_simt_shrink(const LoraLaunch& l, cudaStream_t stream);

@@ -1,0 +1,453 @@
+// The adapters' gradients on the tensor cores: for each adapter, P^T t over its
+// rows, P the layer's input or its output's gradient and t rank values.
+//
+// One tile is 128 columns of P (the lanes) by up to 256 columns of rank values in
+// parts, whose sums are added at the end.  Both operands lie across the
+// contraction, and an adapter's rows lie anywhere: the tile goes through the
+// 64-row blocks that hold any of them, found from the plans.  In a block that
+// holds other rows as well, a warp zeroes those in shared memory, in both
+// operands, before the block counts as loaded; 16-row slices without a row of
+// the adapter are skipped.  Bound: reading P once for each adapter in a block
+// (once in all where sequences are long), the rank values and the launch.
+#include <algorithm>
+
+#include "grouped_maps.h"
+#include "lora_tc.cuh"
+#include "persistent.cuh"
+#include "simt_types.h"
+
+namespace tmmo {
+namespace {
+
+constexpr int LG_THREADS = 256;  // warps 0: copies, 1: MMA, 2: zeros, 4-7: epilogue
+constexpr int LG_MAX_STAGES = 8;
+constexpr int LG_RING = 192 * 1024;
+constexpr int LG_CHUNKS = 4;     // chunks of rank values in a tile
+
+struct GradSide {
+    int tiles_c;       // tiles of P's columns
+    int cols;
+    void* G;
+    int64_t step_c, step_j, stride_g;
+};
+
+struct GradParams {
+    GradSide side[2];
+    int items0, items;   // of the first side, of both
+    int adapters, rank;
+    int plans;
+    const LoraPlan* plan;
+    LoraParts lay;
+    int groups_j;        // tiles of rank values
+    int stages, stage_bytes;
+    uint32_t idesc;      // with N = 0
+    int* status;
+    long long wait_budget;
+};
+
+struct GradItem {
+    int which, g, c0, chunk0, chunks;
+    int n;  // columns of rank values that the tensor core reads
+};
+
+__device__ __forceinline__ GradItem grad_item(int t, const GradParams& p)
+{
+    GradItem w;
+    w.which = t >= p.items0;
+    t -= w.which ? p.items0 : 0;
+    const int per = p.side[w.which].tiles_c * p.groups_j;
+    w.g = t / per;
+    t -= w.g * per;
+    w.c0 = t / p.groups_j * 128;
+    w.chunk0 = t % p.groups_j * LG_CHUNKS;
+    w.chunks = min(LG_CHUNKS, p.lay.chunks - w.chunk0);
+    w.n = (w.chunks - 1) * 64 + p.lay.parts * p.lay.chunk;
+    return w;
+}
+
+// The 64-row blocks that hold rows of adapter g, in order; a whole warp steps
+// through them together.
+class RowBlocks {
+public:
+    __device__ RowBlocks(const GradParams& p, int g) : p_(p), g_(g) {}
+    // The next block and its rows of g (a bit each); false at the end.
+    __device__ bool next(int& block, uint64_t& rows)
+    {
+        for (;;) {
+            while (half_ < 2) {
+                const uint64_t m = half_ == 0 ? lo_ : hi_;
+                block = 2 * tile_ + half_++;
+                if (m != 0) {
+                    rows = m;
+                    return true;
+                }
+            }
+            while (hits_ == 0) {
+                base_ += 32;
+                if (base_ >= p_.plans)
+                    return false;
+                look();
+            }
+            const int src = __ffs(hits_) - 1;
+            hits_ &= hits_ - 1;
+            tile_ = base_ + src;
+            uint32_t w[4];
+            for (int i = 0; i < 4; ++i)
+                w[i] = __shfl_sync(0xffffffffu, mine_[i], src);
+            lo_ = w[0] | static_cast<uint64_t>(w[1]) << 32;
+            hi_ = w[2] | static_cast<uint64_t>(w[3]) << 32;
+            half_ = 0;
+        }
+    }
+
+private:
+    // Each lane looks for g in one of 32 plans.
+    __device__ void look()
+    {
+        const int i = base_ + static_cast<int>(lane_id());
+        bool found = false;
+        if (i < p_.plans) {
+            const LoraPlan& plan = p_.plan[i];
+            int lo = 0, hi = plan.count;  // the first place whose id is not below g
+            const int count = hi;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (plan.ids[mid] < g_)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            found = lo < count && plan.ids[lo] == g_;
+            if (found) {
+                const uint4 v = *reinterpret_cast<const uint4*>(plan.rows[lo]);
+                mine_[0] = v.x;
+                mine_[1] = v.y;
+                mine_[2] = v.z;
+                mine_[3] = v.w;
+            }
+        }
+        hits_ = __ballot_sync(0xffffffffu, found);
+    }
+
+    const GradParams& p_;
+    const int g_;
+    int base_ = -32, tile_ = 0, half_ = 2;
+    uint32_t hits_ = 0;
+    uint32_t mine_[4] = {};
+    uint64_t lo_ = 0, hi_ = 0;
+};
+
+struct GradSmem {
+    uint64_t full[LG_MAX_STAGES], landed[LG_MAX_STAGES], empty[LG_MAX_STAGES], tfull[2], tempty[2], drain;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+template <typename OutT>
+__global__ void __launch_bounds__(LG_THREADS, 1)
+    lora_grad_tc_kernel(const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmT0,
+                        const __grid_constant__ CUtensorMap tmP1, const __grid_constant__ CUtensorMap tmT1,
+                        const __grid_constant__ GradParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = smem_u32(reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023)));
+    __shared__ GradSmem s;
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31;
+    const TcWatch watch{&s.abort_flag, p.status, p.wait_budget};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.landed[i]), 1);
+            mbar_init(smem_u32(&s.empty[i]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&s.tfull[a]), 1);
+            mbar_init(smem_u32(&s.tempty[a]), 4);
+        }
+        mbar_init(smem_u32(&s.drain), 1);
+        s.abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmP0);
+        tma_prefetch_desc(&tmT0);
+        tma_prefetch_desc(&tmP1);
+        tma_prefetch_desc(&tmT1);
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(smem_u32(&s.tmem), 512);
+        tmem_relinquish<1>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+
+    // Roles of whole warps: one lane waits and issues, and the others learn
+    // whether it gave up.
+    auto together = [&](auto f) {
+        int ok = 1;
+        if (lane == 0)
+            ok = f() ? 1 : 0;
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t n_full[LG_MAX_STAGES] = {}, n_landed[LG_MAX_STAGES] = {};
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
+            const GradItem w = grad_item(t, p);
+            RowBlocks blocks(p, w.g);
+            int block;
+            uint64_t rows;
+            while (ok && blocks.next(block, rows)) {
+                const bool whole = rows == ~0ull;
+                ok = together([&] {
+                    if (!tc_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch))
+                        return false;
+                    const uint32_t bar = smem_u32(whole ? &s.full[stage] : &s.landed[stage]);
+                    const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 16384;
+                    const CUtensorMap* tmP = w.which ? &tmP1 : &tmP0;
+                    const CUtensorMap* tmT = w.which ? &tmT1 : &tmT0;
+                    mbar_arrive_expect_tx(bar, 16384 + w.chunks * 8192);
+                    tma_load_2d(a0, tmP, bar, w.c0, block * 64);
+                    tma_load_2d(a0 + 8192, tmP, bar, w.c0 + 64, block * 64);
+                    for (int c = 0; c < w.chunks; ++c)
+                        tma_load_2d(b0 + c * 8192, tmT, bar, (w.chunk0 + c) * 64, block * 64);
+                    return true;
+                });
+                if (ok) {
+                    ++n_full[stage];  // whichever barrier: full completes once a use
+                    n_landed[stage] += !whole;
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before shared memory goes away
+            auto drain = [&](uint64_t* bar, uint32_t uses) {
+                const long long t0 = clock64();
+                while (uses > 0 && !mbar_try_wait(smem_u32(bar), (uses - 1) & 1) &&
+                       clock64() - t0 < p.wait_budget) {
+                }
+            };
+            for (int i = 0; i < p.stages; ++i) {
+                drain(&s.full[i], n_full[i]);
+                drain(&s.landed[i], n_landed[i]);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        int stage = 0, local = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
+            const GradItem w = grad_item(t, p);
+            RowBlocks blocks(p, w.g);
+            int block;
+            uint64_t rows;
+            const int acc = local & 1;
+            const uint32_t d = tmem + acc * 256;
+            const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
+            bool any = false;
+            while (ok && blocks.next(block, rows)) {
+                ok = together([&] {
+                    if (!any && !tc_wait(smem_u32(&s.tempty[acc]), ((local >> 1) & 1) ^ 1, watch))
+                        return false;
+                    if (!tc_wait(smem_u32(&s.full[stage]), phase, watch))
+                        return false;
+                    tc_fence_after();
+                    const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 16384;
+                    bool first = !any;
+                    for (int k = 0; k < 4; ++k) {
+                        if (((rows >> (16 * k)) & 0xffff) == 0)
+                            continue;
+                        tc_mma_f16<1>(d, smem_desc_sw128(a0 + k * 2048, 8192, 1024),
+                                      smem_desc_sw128(b0 + k * 2048, 8192, 1024), idesc, !first);
+                        first = false;
+                    }
+                    tc_commit(smem_u32(&s.empty[stage]));
+                    return true;
+                });
+                any = true;
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok && any) {
+                if (lane == 0)
+                    tc_commit(smem_u32(&s.tfull[acc]));
+                ++local;
+            }
+        }
+        if (lane == 0) {
+            // Wait (bounded) until every MMA issued so far has completed.
+            tc_commit(smem_u32(&s.drain));
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(&s.drain), 0) && clock64() - t0 < p.wait_budget) {
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------ rows of other adapters
+        int stage = 0;
+        uint32_t parity = 0;  // a bit for each stage
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
+            const GradItem w = grad_item(t, p);
+            RowBlocks blocks(p, w.g);
+            int block;
+            uint64_t rows;
+            while (ok && blocks.next(block, rows)) {
+                if (rows != ~0ull) {
+                    ok = together([&] {
+                        return tc_wait(smem_u32(&s.landed[stage]), (parity >> stage) & 1, watch);
+                    });
+                    if (!ok)
+                        break;
+                    parity ^= 1u << stage;
+                    // a row is 128 contiguous bytes of each box (its swizzle stays within)
+                    const uint32_t a0 = ring + stage * p.stage_bytes;
+                    for (int i = lane; i < 512; i += 32) {
+                        const int r = i >> 3;
+                        if (((rows >> r) & 1) || ((rows >> (r & 48)) & 0xffff) == 0)
+                            continue;
+                        for (int b = 0; b < 2 + w.chunks; ++b)
+                            st_shared_v4(a0 + b * 8192 + i * 16, 0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&s.full[stage]));
+                }
+                if (++stage == p.stages)
+                    stage = 0;
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------ epilogue
+        const int q = warp & 3;
+        int local = 0;
+        for (int t = blockIdx.x; t < p.items; t += gridDim.x) {
+            const GradItem w = grad_item(t, p);
+            const GradSide& side = p.side[w.which];
+            RowBlocks blocks(p, w.g);
+            int block;
+            uint64_t rows;
+            const bool any = blocks.next(block, rows);
+            const int acc = local & 1;
+            if (any) {
+                if (!together([&] { return tc_wait(smem_u32(&s.tfull[acc]), (local >> 1) & 1, watch); }))
+                    break;
+                ++local;
+                tc_fence_after();
+            }
+            const int c = w.c0 + q * 32 + static_cast<int>(lane);
+            OutT* out = static_cast<OutT*>(side.G) + w.g * side.stride_g + c * side.step_c;
+            const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+#pragma unroll 1
+            for (int k = 0; k < w.chunks; ++k)
+#pragma unroll 1
+                for (int j0 = 0; j0 < p.lay.chunk; j0 += 16) {
+                    const int j = (w.chunk0 + k) * p.lay.chunk + j0;
+                    if (j >= p.rank)
+                        break;
+                    float sum[16] = {};
+                    if (any)
+                        for (int part = 0; part < p.lay.parts; ++part) {
+                            uint32_t v[16];
+                            tmem_ld_32x32b_x16(from + k * 64 + part * p.lay.chunk + j0, v);
+                            tmem_wait_ld(v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                sum[i] += __uint_as_float(v[i]);
+                        }
+                    if (c < side.cols) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (j + i < p.rank)
+                                put(out + (j + i) * side.step_j, sum[i]);
+                    }
+                }
+            if (any) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&s.tempty[acc]));
+            }
+        }
+    }
+
+    // ---------------------------------------------------- teardown
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc<1>(tmem, 512);
+}
+
+template <typename OutT>
+cudaError_t launch(const CUtensorMap (&m)[4], const GradParams& p, int num_sms, cudaStream_t stream)
+{
+    static ClusterCaps caps;
+    int cap = 0;
+    const cudaError_t err =
+        cluster_cap(lora_grad_tc_kernel<OutT>, caps, 1, LG_THREADS, LG_RING + 1024, num_sms, &cap);
+    if (err != cudaSuccess)
+        return err;
+    ClusterLaunch l(static_cast<unsigned>(std::min(p.items, num_sms)), 1, LG_THREADS, LG_RING + 1024, stream);
+    return l.run(lora_grad_tc_kernel<OutT>, m[0], m[1], m[2], m[3], p);
+}
+
+}  // namespace
+
+cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStream_t stream)
+{
+    const LoraGradLaunch& l = sides[0] ? *sides[0] : *sides[1];
+    GradParams p{};
+    p.adapters = l.adapters;
+    p.rank = l.rank;
+    p.plans = (l.rows + LT_ROWS - 1) / LT_ROWS;
+    p.plan = static_cast<const LoraPlan*>(l.plan);
+    p.lay = lora_parts(l.rank, l.parts);
+    p.groups_j = (p.lay.chunks + LG_CHUNKS - 1) / LG_CHUNKS;
+    p.stage_bytes = 16384 + 8192 * std::min(p.lay.chunks, LG_CHUNKS);
+    p.stages = std::min(LG_MAX_STAGES, LG_RING / p.stage_bytes);
+    p.idesc = tc_idesc(l.in_dtype == DT_BF16, 128, 0, true, true);
+    p.status = l.status;
+    p.wait_budget = l.wait_budget;
+    CUtensorMap m[4];
+    int64_t items[2] = {0, 0};
+    for (int i = 0; i < 2; ++i) {
+        if (!sides[i])
+            continue;
+        const LoraGradLaunch& s = *sides[i];
+        p.side[i] = {(s.cols + 127) / 128, s.cols, s.G, s.step_c, s.step_j, s.stride_g};
+        items[i] = static_cast<int64_t>(p.side[i].tiles_c) * p.groups_j * s.adapters;
+        if (!encode_map(&m[2 * i], s.in_dtype, s.P, 2, {s.cols, s.rows, 1}, {s.ldp, 0}, {64, 64, 1}) ||
+            !encode_map(&m[2 * i + 1], s.in_dtype, s.t16, 2, {p.lay.columns(), s.rows, 1},
+                        {p.lay.columns(), 0}, {64, 64, 1}))
+            return cudaErrorNotSupported;
+    }
+    for (int i = 0; i < 2; ++i)
+        if (!sides[i]) {
+            m[2 * i] = m[2 - 2 * i];
+            m[2 * i + 1] = m[3 - 2 * i];
+        }
+    if (items[0] + items[1] > 0x7fffffff)
+        return cudaErrorNotSupported;
+    p.items0 = static_cast<int>(items[0]);
+    p.items = static_cast<int>(items[0] + items[1]);
+    return with_in_type(l.out_dtype, [&](auto out) {
+        return launch<decltype(out)>(m, p, l.num_sms, stream);
+    });
+}
+
+}  // namespace tmmo

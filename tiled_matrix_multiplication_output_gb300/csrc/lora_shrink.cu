@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     if (which == 0 && deal == 0 && split == 0) {
         const int* from = reinterpret_cast<const int*>(&s.plan);
         int* to = reinterpret_cast<int*>(p.plan + tile);
-        const int words = 1 + LT_ROWS + 4 * s.plan.count;  // the rows of absent adapters are not read
+        const int words = 4 + LT_ROWS + 4 * s.plan.count;  // the rows of absent adapters are not read
         for (int i = threadIdx.x; i < words; i += LS_THREADS)
             to[i] = from[i];
     }

@@ -28,9 +28,9 @@ constexpr int LT_ROWS = 128;  // rows of a tile, the lanes of a CTA
 
 struct LoraPlan {
     int count;                  // adapters among the tile's rows
+    int pad[3];
     int ids[LT_ROWS];           // ascending
     uint32_t rows[LT_ROWS][4];  // bit i of the i-th: row i has this adapter
-    int pad[3];
 };
 static_assert(sizeof(LoraPlan) == LORA_PLAN_BYTES, "size of a plan in the workspace");
 
