@@ -582,15 +582,15 @@ typedef struct {
 /*
  * gemm_lora -- the forward product above.  X is rows x K, Y rows x N.
  *
- * workspace: device memory of gemm_lora_workspace_size() bytes, which serves
- * any operands of these sizes; 256-byte aligned, not shared by calls that
- * overlap in time.  Returns GEMM_OK, GEMM_ERR_INVALID_VALUE (null pointer
+ * workspace: gemm_lora_workspace_size() bytes of device memory for these very
+ * operands; 256-byte aligned, not shared by calls that overlap in time.  Returns GEMM_OK, GEMM_ERR_INVALID_VALUE (null pointer
  * where data is needed, bad size, pitch, stride or enum, workspace missing,
  * misaligned or too small), GEMM_ERR_UNSUPPORTED (rank above GEMM_MAX_RANK)
  * or GEMM_ERR_CUDA.
  */
-size_t gemm_lora_workspace_size(int64_t rows, int64_t N, int64_t K, int64_t adapters,
-                                int64_t rank);
+size_t gemm_lora_workspace_size(const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                const gemm_lora_t* lora, int64_t rows, int64_t N, int64_t K,
+                                gemm_dtype_t in_dtype, gemm_dtype_t out_dtype);
 int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw, const gemm_lora_t* lora,
               const int32_t* adapter, void* Y, int64_t ldy, int64_t rows, int64_t N, int64_t K,
               gemm_dtype_t in_dtype, gemm_dtype_t out_dtype, void* workspace,
@@ -608,8 +608,10 @@ int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw, const gemm
  * only, W for DX only).  Adapters without rows get zeros.  workspace of
  * gemm_lora_backward_workspace_size() bytes.  Errors as gemm_lora.
  */
-size_t gemm_lora_backward_workspace_size(int64_t rows, int64_t N, int64_t K, int64_t adapters,
-                                         int64_t rank);
+size_t gemm_lora_backward_workspace_size(const void* D, int64_t ldd, const void* X, int64_t ldx,
+                                         const void* W, int64_t ldw, const gemm_lora_t* lora,
+                                         int64_t rows, int64_t N, int64_t K, gemm_dtype_t in_dtype,
+                                         gemm_dtype_t out_dtype, gemm_dtype_t grad_dtype);
 int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int64_t ldx, const void* W,
                        int64_t ldw, const gemm_lora_t* lora, const int32_t* adapter, void* DX,
                        int64_t lddx, void* DA, int64_t ldda, int64_t stride_da, void* DB,

@@ -33,6 +33,14 @@ def test_grouped_rejects_bad_arguments():
                 dict(N=BIG + 1), dict(K=BIG + 1), dict(dt=3), dict(out=3)):
         assert _grouped(**bad) == INV, bad
     assert _grouped(groups=1025) == UNS
+    size = tg.gemm_grouped_workspace_size
+    assert size(P, 64, P, 64, 64 * 32, 10, 3, 32, 64, 1, tg.BF16) == 0
+    assert size(P, 65, P, 65, 65 * 32, 10, 3, 32, 64, 1, tg.F32) == 0
+    assert size(P + 2, 64, P, 64, 64 * 32, 10, 3, 32, 64, 1, tg.BF16) >= 10 * 64 * 2
+    need = size(P, 64, P, 65, 65 * 32, 10, 3, 32, 64, 1, tg.BF16)
+    assert need >= 3 * 64 * 32 * 2  # copies to aligned rows
+    for bad in (dict(ws=None, nbytes=need), dict(ws=P + 16, nbytes=need), dict(ws=P, nbytes=need - 1)):
+        assert _grouped(ldw=65, stride=65 * 32, **bad) == INV, bad
     assert _grouped(rows=0, X=None, Y=None, off=None) == 0
     assert _grouped(N=0, W=None, Y=None, ldy=0) == 0
 
@@ -51,6 +59,9 @@ def test_wgrad_rejects_bad_arguments():
         assert _wgrad(**bad) == INV, bad
     assert _wgrad(ldc=2 ** 62, stride=2 ** 62) == INV  # rows of one result reach into the next
     assert _wgrad(groups=1025) == UNS
+    assert tg.gemm_grouped_wgrad_workspace_size(P, 32, P, 64, 10, 32, 64, tg.F16) == 0
+    assert tg.gemm_grouped_wgrad_workspace_size(P, 33, P, 64, 10, 32, 64, tg.F16) >= 10 * 32 * 2
+    assert _wgrad(ldd=33) == INV  # no workspace for the copy
     assert _wgrad(groups=0, off=None, C=None) == 0
     assert _wgrad(N=0, C=None) == _wgrad(K=0, C=None, ldc=0) == 0
 
@@ -66,12 +77,16 @@ def _lora(X=P, ldx=64, W=P, ldw=64, lora=None, of=P, Y=P, ldy=32, rows=10, N=32,
 
 
 def test_lora_rejects_bad_arguments():
-    size = tg.gemm_lora_workspace_size
-    assert 0 < size(10, 32, 64, 3, 8) < size(1000, 32, 64, 3, 8)
-    assert size(-1, 32, 64, 3, 8) == size(10, 32, 64, 3, 257) == size(10, 32, 64, -1, 8) == 0
+    def size(rows, r=8, G=3, dt=tg.BF16, ldx=64):
+        return tg.gemm_lora_workspace_size(P, ldx, P, 64, _adapters(G=G, r=r), rows, 32, 64, dt, tg.F32)
+
+    assert 0 < size(10) < size(1000) < size(1000, r=200)
+    assert size(10, ldx=67) >= size(10) + 10 * 64 * 2  # room for a copy
+    assert size(-1) == size(10, r=257) == size(10, G=-1) == size(10, dt=5) == 0
+    need = size(10)
     for bad in (dict(X=None), dict(W=None), dict(Y=None), dict(of=None), dict(ldx=63), dict(ldw=63),
                 dict(ldy=31), dict(rows=-1), dict(N=BIG + 1), dict(K=-1), dict(dt=3), dict(out=-1),
-                dict(ws=None), dict(ws=P + 16), dict(nbytes=size(10, 32, 64, 3, 8) - 1)):
+                dict(ws=None), dict(ws=P + 16), dict(nbytes=need - 1)):
         assert _lora(**bad) == INV, bad
     for bad in (dict(A=None), dict(B=None), dict(lda=63), dict(ldb=7), dict(sa=-1), dict(sb=-1),
                 dict(G=-1), dict(G=65536), dict(r=-1)):
@@ -89,11 +104,12 @@ def _backward(D=P, ldd=32, X=P, ldx=64, W=P, ldw=64, lora=None, of=P, DX=P, lddx
 
 
 def test_lora_backward_rejects_bad_arguments():
-    size = tg.gemm_lora_backward_workspace_size
+    need = tg.gemm_lora_backward_workspace_size(P, 32, P, 64, P, 64, _adapters(), 10, 32, 64, tg.BF16,
+                                                tg.F32, tg.F32)
     for bad in (dict(D=None), dict(X=None), dict(W=None), dict(of=None), dict(ldd=31), dict(ldx=63),
                 dict(ldw=63), dict(lddx=63), dict(ldda=63), dict(sda=64 * 8 - 1), dict(lddb=7),
                 dict(sdb=32 * 8 - 1), dict(rows=-1), dict(grad=3), dict(out=3), dict(dt=3),
-                dict(ws=None), dict(ws=P + 128), dict(nbytes=size(10, 32, 64, 3, 8) - 1)):
+                dict(ws=None), dict(ws=P + 128), dict(nbytes=need - 1)):
         assert _backward(**bad) == INV, bad
     assert _backward(lora=_adapters(r=257, ldb=300)) == UNS
     assert _backward(DX=None, DA=None, DB=None, X=None, W=None, ws=None) == 0

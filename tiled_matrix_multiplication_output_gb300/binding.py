@@ -111,10 +111,12 @@ _SIGNATURES = {
     "gemm_grouped_wgrad": ([_p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64,
                             ctypes.c_float, ctypes.c_float, _int, _int, _p, ctypes.c_size_t, _p],
                            _int),
-    "gemm_lora_workspace_size": ([_i64] * 5, ctypes.c_size_t),
+    "gemm_lora_workspace_size": ([_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _int, _int],
+                                 ctypes.c_size_t),
     "gemm_lora": ([_p, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i64, _i64, _int, _int, _p,
                    ctypes.c_size_t, _p], _int),
-    "gemm_lora_backward_workspace_size": ([_i64] * 5, ctypes.c_size_t),
+    "gemm_lora_backward_workspace_size": ([_p, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _int,
+                                           _int, _int], ctypes.c_size_t),
     "gemm_lora_backward": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _i64, _i64, _p,
                             _i64, _i64, _i64, _i64, _i64, _int, _int, _int, _p, ctypes.c_size_t,
                             _p], _int),
@@ -338,29 +340,35 @@ def gemm_grouped_wgrad(D, ldd, X, ldx, offsets, C, ldc, stride_c, rows, groups, 
                                              workspace, workspace_bytes, stream)
 
 
-def gemm_lora_workspace_size(rows, N, K, adapters, rank) -> int:
-    return load_library().gemm_lora_workspace_size(rows, N, K, adapters, rank)
+def _lora_struct(lora):
+    """gemm_lora_t from a LoraAdapters structure, or the bytes of one."""
+    return ctypes.byref(lora) if isinstance(lora, LoraAdapters) else lora
+
+
+def gemm_lora_workspace_size(X, ldx, W, ldw, lora, rows, N, K, in_dtype, out_dtype) -> int:
+    return load_library().gemm_lora_workspace_size(X, ldx, W, ldw, _lora_struct(lora), rows, N, K,
+                                                   in_dtype, out_dtype)
 
 
 def gemm_lora(X, ldx, W, ldw, lora, adapter, Y, ldy, rows, N, K, in_dtype, out_dtype, workspace,
               workspace_bytes, stream=None) -> int:
-    """lora: a LoraAdapters structure, or the bytes of one."""
-    lora = ctypes.byref(lora) if isinstance(lora, LoraAdapters) else lora
-    return load_library().gemm_lora(X, ldx, W, ldw, lora, adapter, Y, ldy, rows, N, K, in_dtype,
-                                    out_dtype, workspace, workspace_bytes, stream)
+    return load_library().gemm_lora(X, ldx, W, ldw, _lora_struct(lora), adapter, Y, ldy, rows, N, K,
+                                    in_dtype, out_dtype, workspace, workspace_bytes, stream)
 
 
-def gemm_lora_backward_workspace_size(rows, N, K, adapters, rank) -> int:
-    return load_library().gemm_lora_backward_workspace_size(rows, N, K, adapters, rank)
+def gemm_lora_backward_workspace_size(D, ldd, X, ldx, W, ldw, lora, rows, N, K, in_dtype, out_dtype,
+                                      grad_dtype) -> int:
+    return load_library().gemm_lora_backward_workspace_size(D, ldd, X, ldx, W, ldw,
+                                                            _lora_struct(lora), rows, N, K,
+                                                            in_dtype, out_dtype, grad_dtype)
 
 
 def gemm_lora_backward(D, ldd, X, ldx, W, ldw, lora, adapter, DX, lddx, DA, ldda, stride_da, DB,
                        lddb, stride_db, rows, N, K, in_dtype, out_dtype, grad_dtype, workspace,
                        workspace_bytes, stream=None) -> int:
-    lora = ctypes.byref(lora) if isinstance(lora, LoraAdapters) else lora
-    return load_library().gemm_lora_backward(D, ldd, X, ldx, W, ldw, lora, adapter, DX, lddx, DA,
-                                             ldda, stride_da, DB, lddb, stride_db, rows, N, K,
-                                             in_dtype, out_dtype, grad_dtype, workspace,
+    return load_library().gemm_lora_backward(D, ldd, X, ldx, W, ldw, _lora_struct(lora), adapter, DX,
+                                             lddx, DA, ldda, stride_da, DB, lddb, stride_db, rows,
+                                             N, K, in_dtype, out_dtype, grad_dtype, workspace,
                                              workspace_bytes, stream)
 
 
@@ -1025,11 +1033,11 @@ def matmul_lora(x, w, a, b, adapter, scale=None, out_dtype=None, out=None, strea
         _check_out(out, (rows, N), out_dtype)
         ldy = _check_matrix(out, "out")[2]
     lib = _lib or load_library()
-    nbytes = lib.gemm_lora_workspace_size(rows, N, K, G, r)
+    px, pw, ocode = x.data_ptr(), w.data_ptr(), dtype_code(out.dtype)
+    nbytes = lib.gemm_lora_workspace_size(px, ldx, pw, ldw, lora, rows, N, K, code, ocode)
     ws, _held = _workspace(nbytes, x, stream)
-    rc = lib.gemm_lora(x.data_ptr(), ldx, w.data_ptr(), ldw, lora, index, out.data_ptr(), ldy,
-                       rows, N, K, code, dtype_code(out.dtype), ws, nbytes,
-                       _stream_ptr(stream, x))
+    rc = lib.gemm_lora(px, ldx, pw, ldw, lora, index, out.data_ptr(), ldy, rows, N, K, code, ocode,
+                       ws, nbytes, _stream_ptr(stream, x))
     if rc != OK:
         raise GemmError(rc, "gemm_lora")
     return out
@@ -1057,12 +1065,14 @@ def matmul_lora_backward(dy, x, w, a, b, adapter, scale=None, out_dtype=None, gr
     da = _allocate(stream, _empty, (G, r, K), gdt, x.device)
     db = _allocate(stream, _empty, (G, N, r), gdt, x.device)
     lib = _lib or load_library()
-    nbytes = lib.gemm_lora_backward_workspace_size(rows, N, K, G, r)
+    pd, px, pw = dy.data_ptr(), x.data_ptr(), w.data_ptr()
+    ocode, gcode = dtype_code(odt), dtype_code(gdt)
+    nbytes = lib.gemm_lora_backward_workspace_size(pd, ldd, px, ldx, pw, ldw, lora, rows, N, K, code,
+                                                   ocode, gcode)
     ws, _held = _workspace(nbytes, x, stream)
-    rc = lib.gemm_lora_backward(dy.data_ptr(), ldd, x.data_ptr(), ldx, w.data_ptr(), ldw, lora,
-                                index, dx.data_ptr(), K, da.data_ptr(), K, r * K, db.data_ptr(), r,
-                                N * r, rows, N, K, code, dtype_code(odt), dtype_code(gdt), ws,
-                                nbytes, _stream_ptr(stream, x))
+    rc = lib.gemm_lora_backward(pd, ldd, px, ldx, pw, ldw, lora, index, dx.data_ptr(), K,
+                                da.data_ptr(), K, r * K, db.data_ptr(), r, N * r, rows, N, K, code,
+                                ocode, gcode, ws, nbytes, _stream_ptr(stream, x))
     if rc != OK:
         raise GemmError(rc, "gemm_lora_backward")
     return dx, da, db

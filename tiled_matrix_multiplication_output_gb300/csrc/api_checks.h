@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
 #include "tiled_gemm.h"
@@ -18,6 +19,12 @@ inline bool valid_dtype(int t) { return t == GEMM_F32 || t == GEMM_F16 || t == G
 inline bool apart(int64_t stride, int64_t rows, int64_t ld, int64_t cols)
 {
     return stride >= 0 && static_cast<__int128>(stride) >= static_cast<__int128>(rows - 1) * ld + cols;
+}
+
+// Whether `need` bytes of workspace are not there.
+inline bool bad_workspace(const void* ws, size_t have, size_t need)
+{
+    return need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || have < need);
 }
 
 inline int status_of(cudaError_t err)

@@ -8,6 +8,7 @@
 #include "device.h"
 #include "grouped.h"
 #include "launch.h"
+#include "pack.h"
 #include "tiled_gemm.h"
 
 using namespace tmmo;
@@ -16,7 +17,7 @@ static_assert(kMaxGroups == GEMM_MAX_GROUPS, "the table's size");
 
 namespace {
 
-int check_grouping(const int32_t* offsets, int64_t rows, int64_t groups, int64_t N, int64_t K,
+int check_grouping(int64_t rows, int64_t groups, int64_t N, int64_t K,
                    int in_dtype, int out_dtype)
 {
     if (!valid_size(rows) || !valid_size(N) || !valid_size(K) || groups < 0 ||
@@ -27,13 +28,27 @@ int check_grouping(const int32_t* offsets, int64_t rows, int64_t groups, int64_t
     return GEMM_OK;
 }
 
+// The weights as a stack of stored matrices.
+PackMatrix weights(const void* W, int64_t ldw, int64_t stride, int64_t groups, int64_t N, int64_t K,
+                   int op)
+{
+    return {W, ldw, stride, groups, op == GEMM_OP_T ? N : K, op == GEMM_OP_T ? K : N};
+}
+
 }  // namespace
 
-extern "C" size_t gemm_grouped_workspace_size(const void*, int64_t, const void*, int64_t, int64_t,
-                                              int64_t, int64_t, int64_t, int64_t, gemm_op_t,
-                                              gemm_dtype_t)
+extern "C" size_t gemm_grouped_workspace_size(const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                              int64_t stride_w, int64_t rows, int64_t groups,
+                                              int64_t N, int64_t K, gemm_op_t op_w,
+                                              gemm_dtype_t in_dtype)
 {
-    return 0;
+    if (in_dtype == GEMM_F32 || check_grouping(rows, groups, N, K, in_dtype, GEMM_F32) != GEMM_OK)
+        return 0;
+    PackMatrix x{X, ldx, 0, 1, rows, K}, w = weights(W, ldw, stride_w, groups, N, K, op_w);
+    Packing packing;
+    packing.add(&x);
+    packing.add(&w, true);
+    return packing.bytes();
 }
 
 extern "C" int gemm_grouped(const void* X, int64_t ldx, const void* W, int64_t ldw,
@@ -43,7 +58,7 @@ extern "C" int gemm_grouped(const void* X, int64_t ldx, const void* W, int64_t l
                             gemm_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
                             void* stream)
 {
-    int rc = check_grouping(offsets, rows, groups, N, K, in_dtype, out_dtype);
+    int rc = check_grouping(rows, groups, N, K, in_dtype, out_dtype);
     if (rc == GEMM_OK && op_w != GEMM_OP_N && op_w != GEMM_OP_T)
         rc = GEMM_ERR_INVALID_VALUE;
     if (rc != GEMM_OK || rows == 0 || N == 0)
@@ -52,6 +67,14 @@ extern "C" int gemm_grouped(const void* X, int64_t ldx, const void* W, int64_t l
         return GEMM_ERR_INVALID_VALUE;
     if (K > 0 && groups > 0 &&
         (!X || !W || ldx < K || ldw < (op_w == GEMM_OP_T ? K : N) || stride_w < 0))
+        return GEMM_ERR_INVALID_VALUE;
+    PackMatrix x{X, ldx, 0, 1, rows, K}, w = weights(W, ldw, stride_w, groups, N, K, op_w);
+    Packing packing;
+    if (in_dtype != GEMM_F32) {
+        packing.add(&x);
+        packing.add(&w, true);
+    }
+    if (bad_workspace(workspace, workspace_bytes, packing.bytes()))
         return GEMM_ERR_INVALID_VALUE;
     DeviceInfo d;
     if (device_info(&d) != cudaSuccess)
@@ -78,13 +101,30 @@ extern "C" int gemm_grouped(const void* X, int64_t ldx, const void* W, int64_t l
     l.wait_budget = wait_budget_cycles();
     l.fault_skip_kblock = fault_skip_kblock();
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return status_of(grouped_tc_takes(l) ? grouped_tc_launch(l, s) : grouped_simt_launch(l, s));
+    if (in_dtype == GEMM_F32 || K == 0 || groups == 0)
+        return status_of(grouped_simt_launch(l, s));
+    cudaError_t err = packing.run(workspace, d.num_sms, s);
+    l.X = x.p;
+    l.ldx = x.ld;
+    l.W = w.p;
+    l.ldw = w.ld;
+    l.stride_w = w.stride;
+    if (err == cudaSuccess)
+        err = grouped_tc_launch(l, s);
+    return status_of(err);
 }
 
-extern "C" size_t gemm_grouped_wgrad_workspace_size(const void*, int64_t, const void*, int64_t,
-                                                    int64_t, int64_t, int64_t, gemm_dtype_t)
+extern "C" size_t gemm_grouped_wgrad_workspace_size(const void* D, int64_t ldd, const void* X,
+                                                    int64_t ldx, int64_t rows, int64_t N, int64_t K,
+                                                    gemm_dtype_t in_dtype)
 {
-    return 0;
+    if (in_dtype == GEMM_F32 || check_grouping(rows, 0, N, K, in_dtype, GEMM_F32) != GEMM_OK)
+        return 0;
+    PackMatrix m{D, ldd, 0, 1, rows, N}, x{X, ldx, 0, 1, rows, K};
+    Packing packing;
+    packing.add(&m);
+    packing.add(&x);
+    return packing.bytes();
 }
 
 extern "C" int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int64_t ldx,
@@ -93,12 +133,20 @@ extern "C" int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int
                                   float beta, gemm_dtype_t in_dtype, gemm_dtype_t out_dtype,
                                   void* workspace, size_t workspace_bytes, void* stream)
 {
-    const int rc = check_grouping(offsets, rows, groups, N, K, in_dtype, out_dtype);
+    const int rc = check_grouping(rows, groups, N, K, in_dtype, out_dtype);
     if (rc != GEMM_OK || groups == 0 || N == 0 || K == 0)
         return rc;
     if (!offsets || !C || ldc < K || (groups > 1 && !apart(stride_c, N, ldc, K)))
         return GEMM_ERR_INVALID_VALUE;
     if (rows > 0 && (!D || !X || ldd < N || ldx < K))
+        return GEMM_ERR_INVALID_VALUE;
+    PackMatrix m{D, ldd, 0, 1, rows, N}, x{X, ldx, 0, 1, rows, K};
+    Packing packing;
+    if (in_dtype != GEMM_F32) {
+        packing.add(&m);
+        packing.add(&x);
+    }
+    if (bad_workspace(workspace, workspace_bytes, packing.bytes()))
         return GEMM_ERR_INVALID_VALUE;
     DeviceInfo d;
     if (device_info(&d) != cudaSuccess)
@@ -123,6 +171,14 @@ extern "C" int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int
     l.wait_budget = wait_budget_cycles();
     l.fault_skip_kblock = fault_skip_kblock();
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return status_of(grouped_wgrad_tc_takes(l) ? grouped_wgrad_tc_launch(l, s)
-                                               : grouped_wgrad_simt_launch(l, s));
+    if (in_dtype == GEMM_F32 || rows == 0)
+        return status_of(grouped_wgrad_simt_launch(l, s));
+    cudaError_t err = packing.run(workspace, d.num_sms, s);
+    l.D = m.p;
+    l.ldd = m.ld;
+    l.X = x.p;
+    l.ldx = x.ld;
+    if (err == cudaSuccess)
+        err = grouped_wgrad_tc_launch(l, s);
+    return status_of(err);
 }

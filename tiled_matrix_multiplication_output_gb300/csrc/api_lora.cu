@@ -1,5 +1,5 @@
-// C entry points of the low-rank adapters: argument checks and the
-// translation to the internal launchers.
+// C entry points of the low-rank adapters: argument checks, the workspace, and
+// the order of the launches.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -9,6 +9,7 @@
 #include "device.h"
 #include "launch.h"
 #include "lora.h"
+#include "pack.h"
 #include "tiled_gemm.h"
 
 using namespace tmmo;
@@ -19,68 +20,125 @@ namespace {
 
 constexpr int64_t kMaxAdapters = 65535;
 
-int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
-
-bool valid_sizes(int64_t rows, int64_t N, int64_t K, int64_t adapters, int64_t rank)
-{
-    return valid_size(rows) && valid_size(N) && valid_size(K) && adapters >= 0 && rank >= 0 &&
-           adapters <= kMaxAdapters;
-}
-
-// The rank values of all rows: FP32, or in up to three parts.
-int64_t values_bytes(int64_t rows, int64_t rank)
-{
-    return round256(rows * std::max<int64_t>(rank * 4, lora_parts_bytes(static_cast<int>(rank), 3)));
-}
-int64_t plan_bytes(int64_t rows) { return round256((rows + 127) / 128 * LORA_PLAN_BYTES); }
-
-// How many parts hold a rank value: all bits of an FP32 value for an FP32 result.
-int parts_for(int in_dtype, bool f32_result) { return in_dtype == DT_BF16 && f32_result ? 3 : 2; }
+size_t round256(int64_t n) { return static_cast<size_t>((n + 255) / 256 * 256); }
 
 // Whether there is an adapter that can change anything.
 bool has_adapters(const gemm_lora_t& a) { return a.adapters > 0 && a.rank > 0; }
 
+int check_sizes(const gemm_lora_t* a, int64_t rows, int64_t N, int64_t K, int in_dtype, int out_dtype)
+{
+    if (!a || !valid_size(rows) || !valid_size(N) || !valid_size(K) || a->adapters < 0 || a->rank < 0 ||
+        a->adapters > kMaxAdapters || !valid_dtype(in_dtype) || !valid_dtype(out_dtype))
+        return GEMM_ERR_INVALID_VALUE;
+    return a->rank > GEMM_MAX_RANK ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
+}
+
 int check(const gemm_lora_t* a, const int32_t* adapter, int64_t rows, int64_t N, int64_t K,
           int in_dtype, int out_dtype)
 {
-    if (!a || !valid_sizes(rows, N, K, a->adapters, a->rank) || !valid_dtype(in_dtype) ||
-        !valid_dtype(out_dtype))
+    const int rc = check_sizes(a, rows, N, K, in_dtype, out_dtype);
+    if (rc != GEMM_OK || !has_adapters(*a))
+        return rc;
+    if ((rows > 0 && !adapter) || a->stride_a < 0 || a->stride_b < 0)
         return GEMM_ERR_INVALID_VALUE;
-    if (a->rank > GEMM_MAX_RANK)
-        return GEMM_ERR_UNSUPPORTED;
-    if (has_adapters(*a)) {
-        if ((rows > 0 && !adapter) || a->stride_a < 0 || a->stride_b < 0)
-            return GEMM_ERR_INVALID_VALUE;
-        if ((K > 0 && (!a->A || a->lda < K)) || (N > 0 && (!a->B || a->ldb < a->rank)))
-            return GEMM_ERR_INVALID_VALUE;
-    }
+    if ((K > 0 && (!a->A || a->lda < K)) || (N > 0 && (!a->B || a->ldb < a->rank)))
+        return GEMM_ERR_INVALID_VALUE;
     return GEMM_OK;
 }
 
-bool bad_workspace(const void* ws, size_t have, size_t need)
-{
-    return need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || have < need);
-}
+// The operands as they lie, and the copies that the tensor-core kernels need of
+// them (the input X and the output's gradient D: null where a call has none).
+struct Operands {
+    PackMatrix x, d, w, a, b;
+    Packing packing;
+    bool tc;  // on the tensor cores; else on the FP32 units, or nothing to sum
 
-struct Device {
-    DeviceInfo info;
-    template <typename L>
-    void fill(L* l) const
+    Operands(const void* X, int64_t ldx, const void* D, int64_t ldd, const void* W, int64_t ldw,
+             const gemm_lora_t& l, int64_t rows, int64_t N, int64_t K, int in_dtype)
+        : x{X, ldx, 0, 1, rows, K}, d{D, ldd, 0, 1, rows, N}, w{W, ldw, 0, 1, N, K},
+          a{l.A, l.lda, l.stride_a, l.adapters, l.rank, K},
+          b{l.B, l.ldb, l.stride_b, l.adapters, N, l.rank},
+          tc(in_dtype != GEMM_F32 && rows > 0 && N > 0 && K > 0)
     {
-        l->num_sms = info.num_sms;
-        l->status = info.status;
-        l->wait_budget = wait_budget_cycles();
+        if (!tc)
+            return;
+        for (PackMatrix* m : {&x, &d, &w})
+            if (m->p)
+                packing.add(m);
+        if (has_adapters(l)) {
+            packing.add(&a);
+            packing.add(&b);
+        }
     }
 };
 
+// The workspace: `sides` sets of rank values (FP32, or in parts), the plans of
+// the row tiles, and the copies.
+struct Workspace {
+    size_t values, plans, copies;
+    int sides;
+    Workspace(int sides_, const gemm_lora_t& l, int64_t rows, int parts, const Operands& o)
+        : values(0), plans(0), copies(o.packing.bytes()), sides(sides_)
+    {
+        if (!has_adapters(l))
+            return;
+        values = round256(rows * (o.tc ? lora_parts_bytes(static_cast<int>(l.rank), parts) : l.rank * 4));
+        plans = o.tc ? round256((rows + 127) / 128 * LORA_PLAN_BYTES) : 0;
+    }
+    size_t bytes() const { return sides * values + plans + copies; }
+    void* side(void* p, int i) const { return static_cast<char*>(p) + i * values; }
+    void* plan(void* p) const { return static_cast<char*>(p) + sides * values; }
+    void* copy(void* p) const { return static_cast<char*>(plan(p)) + plans; }
+};
+
+// How many parts hold a rank value: all bits of an FP32 sum for an FP32 result.
+int parts_for(int in_dtype, bool f32_result)
+{
+    return in_dtype == GEMM_BF16 && f32_result ? 3 : 2;
+}
+
+// The input's direction: rank values from X and A, or (across) from D and B.
+LoraLaunch make_launch(const Operands& o, bool across, const gemm_lora_t& lora, const int32_t* adapter,
+                       int64_t rows, int64_t N, int64_t K, int in_dtype, const DeviceInfo& d)
+{
+    const PackMatrix &in = across ? o.d : o.x, &f = across ? o.b : o.a, &e = across ? o.a : o.b;
+    LoraLaunch l{};
+    l.X = in.p;
+    l.ldx = in.ld;
+    l.W = o.w.p;
+    l.ldw = o.w.ld;
+    l.F = f.p;
+    l.ldf = f.ld;
+    l.stride_f = f.stride;
+    l.E = e.p;
+    l.lde = e.ld;
+    l.stride_e = e.stride;
+    l.across = across;
+    l.scale = lora.scale;
+    l.adapter = adapter;
+    l.rows = static_cast<int>(rows);
+    l.N = static_cast<int>(across ? K : N);
+    l.K = static_cast<int>(across ? N : K);
+    l.adapters = has_adapters(lora) ? static_cast<int>(lora.adapters) : 0;
+    l.rank = static_cast<int>(lora.rank);
+    l.in_dtype = in_dtype;
+    l.num_sms = d.num_sms;
+    l.status = d.status;
+    l.wait_budget = wait_budget_cycles();
+    l.fault_skip_kblock = fault_skip_kblock();
+    return l;
+}
+
 }  // namespace
 
-extern "C" size_t gemm_lora_workspace_size(int64_t rows, int64_t N, int64_t K, int64_t adapters,
-                                           int64_t rank)
+extern "C" size_t gemm_lora_workspace_size(const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                           const gemm_lora_t* lora, int64_t rows, int64_t N,
+                                           int64_t K, gemm_dtype_t in_dtype, gemm_dtype_t out_dtype)
 {
-    if (!valid_sizes(rows, N, K, adapters, rank) || rank > GEMM_MAX_RANK)
+    if (check_sizes(lora, rows, N, K, in_dtype, out_dtype) != GEMM_OK || rows == 0 || N == 0)
         return 0;
-    return static_cast<size_t>(values_bytes(rows, rank) + plan_bytes(rows));
+    const Operands o(X, ldx, nullptr, 0, W, ldw, *lora, rows, N, K, in_dtype);
+    return Workspace(1, *lora, rows, parts_for(in_dtype, out_dtype == GEMM_F32), o).bytes();
 }
 
 extern "C" int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw,
@@ -92,57 +150,46 @@ extern "C" int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw,
     const int rc = check(lora, adapter, rows, N, K, in_dtype, out_dtype);
     if (rc != GEMM_OK || rows == 0 || N == 0)
         return rc;
-    if (!Y || ldy < N || (K > 0 && (!X || !W || ldx < K || ldw < K)) ||
-        bad_workspace(workspace, workspace_bytes,
-                      gemm_lora_workspace_size(rows, N, K, lora->adapters, lora->rank)))
+    if (!Y || ldy < N || (K > 0 && (!X || !W || ldx < K || ldw < K)))
         return GEMM_ERR_INVALID_VALUE;
-    Device d;
-    if (device_info(&d.info) != cudaSuccess)
+    Operands o(X, ldx, nullptr, 0, W, ldw, *lora, rows, N, K, in_dtype);
+    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32);
+    const Workspace ws(1, *lora, rows, parts, o);
+    if (bad_workspace(workspace, workspace_bytes, ws.bytes()))
+        return GEMM_ERR_INVALID_VALUE;
+    DeviceInfo d;
+    if (device_info(&d) != cudaSuccess)
         return GEMM_ERR_CUDA;
-    LoraLaunch l{};
-    l.X = X;
-    l.ldx = ldx;
-    l.W = W;
-    l.ldw = ldw;
-    l.F = lora->A;
-    l.ldf = lora->lda;
-    l.stride_f = lora->stride_a;
-    l.E = lora->B;
-    l.lde = lora->ldb;
-    l.stride_e = lora->stride_b;
-    l.scale = lora->scale;
-    l.adapter = adapter;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err = o.packing.run(ws.copy(workspace), d.num_sms, s);
+    LoraLaunch l = make_launch(o, false, *lora, adapter, rows, N, K, in_dtype, d);
     l.Y = Y;
     l.ldy = ldy;
-    l.rows = static_cast<int>(rows);
-    l.N = static_cast<int>(N);
-    l.K = static_cast<int>(K);
-    l.adapters = has_adapters(*lora) ? static_cast<int>(lora->adapters) : 0;
-    l.rank = static_cast<int>(lora->rank);
-    l.in_dtype = in_dtype;
     l.out_dtype = out_dtype;
-    l.t = static_cast<float*>(workspace);
-    d.fill(&l);
-    l.fault_skip_kblock = fault_skip_kblock();
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    l.t16 = workspace;
-    l.plan = static_cast<char*>(workspace) + values_bytes(rows, lora->rank);
-    l.parts = parts_for(in_dtype, out_dtype == GEMM_F32);
-    const bool tc = lora_tc_takes(l);
-    cudaError_t err = cudaSuccess;
-    if (l.adapters > 0)
-        err = tc ? lora_shrink_tc_launch(l, nullptr, s) : lora_simt_shrink(l, s);
+    l.parts = parts;
+    l.t = ws.side(workspace, 0);
+    l.plan = ws.plan(workspace);
+    if (!o.tc && K == 0)
+        l.adapters = 0;
+    if (err == cudaSuccess && l.adapters > 0)
+        err = o.tc ? lora_shrink_tc_launch(l, nullptr, s) : lora_simt_shrink(l, s);
     if (err == cudaSuccess)
-        err = tc ? lora_expand_tc_launch(l, s) : lora_simt_expand(l, s);
+        err = o.tc ? lora_expand_tc_launch(l, s) : lora_simt_expand(l, s);
     return status_of(err);
 }
 
-extern "C" size_t gemm_lora_backward_workspace_size(int64_t rows, int64_t N, int64_t K,
-                                                    int64_t adapters, int64_t rank)
+extern "C" size_t gemm_lora_backward_workspace_size(const void* D, int64_t ldd, const void* X,
+                                                    int64_t ldx, const void* W, int64_t ldw,
+                                                    const gemm_lora_t* lora, int64_t rows,
+                                                    int64_t N, int64_t K, gemm_dtype_t in_dtype,
+                                                    gemm_dtype_t out_dtype,
+                                                    gemm_dtype_t grad_dtype)
 {
-    if (!valid_sizes(rows, N, K, adapters, rank) || rank > GEMM_MAX_RANK)
+    if (check_sizes(lora, rows, N, K, in_dtype, out_dtype) != GEMM_OK || !valid_dtype(grad_dtype))
         return 0;
-    return static_cast<size_t>(2 * values_bytes(rows, rank) + plan_bytes(rows));
+    const Operands o(X, ldx, D, ldd, W, ldw, *lora, rows, N, K, in_dtype);
+    const bool f32 = out_dtype == GEMM_F32 || grad_dtype == GEMM_F32;
+    return Workspace(2, *lora, rows, parts_for(in_dtype, f32), o).bytes();
 }
 
 extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int64_t ldx,
@@ -174,108 +221,79 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
         return GEMM_ERR_INVALID_VALUE;
     if (db && (lddb < lora->rank || (lora->adapters > 1 && !apart(stride_db, N, lddb, lora->rank))))
         return GEMM_ERR_INVALID_VALUE;
-    if (bad_workspace(workspace, workspace_bytes,
-                      gemm_lora_backward_workspace_size(rows, N, K, lora->adapters, lora->rank)))
+    Operands o(X, ldx, D, ldd, W, ldw, *lora, rows, N, K, in_dtype);
+    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32 || grad_dtype == GEMM_F32);
+    const Workspace ws(2, *lora, rows, parts, o);
+    if (bad_workspace(workspace, workspace_bytes, ws.bytes()))
         return GEMM_ERR_INVALID_VALUE;
-    Device d;
-    if (device_info(&d.info) != cudaSuccess)
+    DeviceInfo dev;
+    if (device_info(&dev) != cudaSuccess)
         return GEMM_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err = o.packing.run(ws.copy(workspace), dev.num_sms, s);
 
-    LoraLaunch l{};  // towards dX: rank values u = scale * D B
-    l.X = D;
-    l.ldx = ldd;
-    l.W = dx ? W : nullptr;
-    l.ldw = ldw;
-    l.F = lora->B;
-    l.ldf = lora->ldb;
-    l.stride_f = lora->stride_b;
-    l.E = lora->A;
-    l.lde = lora->lda;
-    l.stride_e = lora->stride_a;
-    l.across = true;
-    l.scale = lora->scale;
-    l.adapter = adapter;
-    l.Y = DX;
-    l.ldy = lddx;
-    l.rows = static_cast<int>(rows);
-    l.N = static_cast<int>(K);
-    l.K = static_cast<int>(N);
-    l.adapters = adapters ? static_cast<int>(lora->adapters) : 0;
-    l.rank = static_cast<int>(lora->rank);
-    l.in_dtype = in_dtype;
-    l.out_dtype = out_dtype;
-    l.t = static_cast<float*>(workspace);
-    d.fill(&l);
-    l.fault_skip_kblock = fault_skip_kblock();
-
-    LoraLaunch f = l;  // forward: rank values t = scale * X A^T
-    f.X = X;
-    f.ldx = ldx;
-    f.F = lora->A;
-    f.ldf = lora->lda;
-    f.stride_f = lora->stride_a;
-    f.across = false;
-    f.W = nullptr;
-    f.E = lora->B;
-    f.lde = lora->ldb;
-    f.stride_e = lora->stride_b;
-    f.N = static_cast<int>(N);
-    f.K = static_cast<int>(K);
-    f.t = reinterpret_cast<float*>(static_cast<char*>(workspace) + values_bytes(rows, lora->rank));
-
-    l.t16 = l.t;
-    f.t16 = f.t;
-    l.plan = f.plan = static_cast<char*>(workspace) + 2 * values_bytes(rows, lora->rank);
-    l.parts = f.parts = parts_for(in_dtype, out_dtype == GEMM_F32 || grad_dtype == GEMM_F32);
+    LoraLaunch u = make_launch(o, true, *lora, adapter, rows, N, K, in_dtype, dev);  // scale * D B
+    u.Y = DX;
+    u.ldy = lddx;
+    u.out_dtype = out_dtype;
+    u.parts = parts;
+    u.t = ws.side(workspace, 0);
+    u.plan = ws.plan(workspace);
+    LoraLaunch t = make_launch(o, false, *lora, adapter, rows, N, K, in_dtype, dev);  // scale * X A^T
+    t.parts = parts;
+    t.t = ws.side(workspace, 1);
+    t.plan = u.plan;
 
     LoraGradLaunch a{};  // dA from X and u
-    a.P = X;
-    a.ldp = ldx;
-    a.t = l.t;
-    a.t16 = l.t16;
-    a.parts = l.parts;
-    a.plan = l.plan;
+    a.P = o.x.p;
+    a.ldp = o.x.ld;
+    a.t = u.t;
+    a.parts = parts;
+    a.plan = u.plan;
     a.G = DA;
     a.step_c = 1;
     a.step_j = ldda;
     a.stride_g = stride_da;
     a.adapter = adapter;
-    a.rows = l.rows;
+    a.rows = u.rows;
     a.cols = static_cast<int>(K);
-    a.adapters = l.adapters;
-    a.rank = l.rank;
+    a.adapters = u.adapters;
+    a.rank = u.rank;
     a.in_dtype = in_dtype;
     a.out_dtype = grad_dtype;
-    d.fill(&a);
+    a.num_sms = u.num_sms;
+    a.status = u.status;
+    a.wait_budget = u.wait_budget;
     LoraGradLaunch b = a;  // dB from D and t
-    b.P = D;
-    b.ldp = ldd;
-    b.t = f.t;
-    b.t16 = f.t16;
+    b.P = o.d.p;
+    b.ldp = o.d.ld;
+    b.t = t.t;
     b.G = DB;
     b.step_c = lddb;
     b.step_j = 1;
     b.stride_g = stride_db;
     b.cols = static_cast<int>(N);
 
-    cudaError_t err = cudaSuccess;
     auto step = [&](bool wanted, auto launch) {
         if (wanted && err == cudaSuccess)
             err = launch();
     };
     const bool need_u = adapters && (dx || da);
-    if (rows > 0 && N > 0 && lora_tc_takes(l) && (!adapters || lora_tc_takes(f))) {
-        step(need_u || db, [&] {
-            return need_u ? lora_shrink_tc_launch(l, db ? &f : nullptr, s) : lora_shrink_tc_launch(f, nullptr, s);
-        });
-        step(dx, [&] { return lora_expand_tc_launch(l, s); });
+    if (o.tc) {
+        step(need_u, [&] { return lora_shrink_tc_launch(u, db ? &t : nullptr, s); });
+        step(!need_u && db, [&] { return lora_shrink_tc_launch(t, nullptr, s); });
+        step(dx, [&] { return lora_expand_tc_launch(u, s); });
         step(da || db, [&] { return lora_grad_tc_launch({da ? &a : nullptr, db ? &b : nullptr}, s); });
         return status_of(err);
     }
-    step(need_u, [&] { return lora_simt_shrink(l, s); });
-    step(dx, [&] { return lora_simt_expand(l, s); });
-    step(db, [&] { return lora_simt_shrink(f, s); });
+    if (in_dtype != GEMM_F32) {  // sums of nothing: no operand is read
+        u.adapters = 0;
+        u.K = 0;
+        a.rows = b.rows = 0;
+    }
+    step(u.adapters > 0 && need_u, [&] { return lora_simt_shrink(u, s); });
+    step(dx, [&] { return lora_simt_expand(u, s); });
+    step(in_dtype == GEMM_F32 && db, [&] { return lora_simt_shrink(t, s); });
     step(da, [&] { return lora_simt_grad(a, s); });
     step(db, [&] { return lora_simt_grad(b, s); });
     return status_of(err);

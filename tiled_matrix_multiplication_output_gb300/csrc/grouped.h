@@ -56,14 +56,12 @@ struct GroupedWgradLaunch {
     int fault_skip_kblock;
 };
 
-// The tensor-core kernels, and whether they take the operands (16-bit, rows on
-// 16-byte boundaries).
-bool grouped_tc_takes(const GroupedLaunch& l);
+// On the tensor cores: 16-bit operands with rows on 16-byte boundaries (pack.h),
+// some groups, rows and K > 0.
 cudaError_t grouped_tc_launch(const GroupedLaunch& l, cudaStream_t stream);
-bool grouped_wgrad_tc_takes(const GroupedWgradLaunch& l);
 cudaError_t grouped_wgrad_tc_launch(const GroupedWgradLaunch& l, cudaStream_t stream);
 
-// FP32 and every other operand the tensor-core kernels do not take.
+// On the FP32 units: FP32 operands, and no operands at all (K == 0, no groups; no rows).
 cudaError_t grouped_simt_launch(const GroupedLaunch& l, cudaStream_t stream);
 cudaError_t grouped_wgrad_simt_launch(const GroupedWgradLaunch& l, cudaStream_t stream);
 

@@ -3,13 +3,6 @@
 
 namespace tmmo {
 
-bool grouped_tc_takes(const GroupedLaunch& l)
-{
-    return l.in_dtype != DT_F32 && l.K > 0 && l.by.groups > 0 && aligned_rows(l.X, l.ldx, l.in_dtype) &&
-           aligned_rows(l.W, l.ldw, l.in_dtype) &&
-           (l.by.groups == 1 || (l.stride_w * type_bytes(l.in_dtype)) % 16 == 0);
-}
-
 cudaError_t grouped_tc_launch(const GroupedLaunch& l, cudaStream_t stream)
 {
     GroupedTcParams p{};

@@ -1,5 +1,5 @@
-// The row-grouped products on the FP32 units: 64 x 64 tiles, each of one
-// group.
+// The row-grouped products on the FP32 units, of FP32 operands: 64 x 64 tiles,
+// each of one group.
 #include "grouped.cuh"
 #include "launch.h"
 #include "simt_tile.cuh"
@@ -8,7 +8,7 @@
 namespace tmmo {
 namespace {
 
-template <typename T, typename OutT>
+template <typename OutT>
 __global__ void __launch_bounds__(ST_THREADS) grouped_simt_kernel(const GroupedLaunch l)
 {
     __shared__ int table[GroupTable::BYTES / sizeof(int)];
@@ -26,9 +26,9 @@ __global__ void __launch_bounds__(ST_THREADS) grouped_simt_kernel(const GroupedL
         const int g = groups.group_of(rt, l.by.groups);
         const int row0 = groups.first[g] + (rt - groups.tile[g]) * ST;
         const int rows = min(groups.first[g + 1] - row0, ST), cols = min(l.N - n0, ST);
-        const View<T> x{static_cast<const T*>(l.X) + row0 * l.ldx, l.ldx, 1};
-        const T* w = static_cast<const T*>(l.W) + g * l.stride_w;
-        const View<T> v = l.w_t ? View<T>{w + n0 * l.ldw, l.ldw, 1} : View<T>{w + n0, 1, l.ldw};
+        const View x{static_cast<const float*>(l.X) + row0 * l.ldx, l.ldx, 1};
+        const float* w = static_cast<const float*>(l.W) + g * l.stride_w;
+        const View v = l.w_t ? View{w + n0 * l.ldw, l.ldw, 1} : View{w + n0, 1, l.ldw};
         float acc[4][4] = {};
         simt_accumulate(acc, s, x, v, 0, l.K, [&](int i, int) { return i < rows; },
                         [&](int j, int) { return j < cols; });
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(ST_THREADS) grouped_simt_kernel(const GroupedL
     }
 }
 
-template <typename T, typename OutT>
+template <typename OutT>
 __global__ void __launch_bounds__(ST_THREADS) grouped_wgrad_simt_kernel(const GroupedWgradLaunch l)
 {
     __shared__ int table[GroupTable::BYTES / sizeof(int)];
@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(ST_THREADS) grouped_wgrad_simt_kernel(const Gr
         const int g = static_cast<int>(t / per_group), u = static_cast<int>(t % per_group);
         const int n0 = u / tiles_k * ST, k0 = u % tiles_k * ST;
         const int rows = min(l.N - n0, ST), cols = min(l.K - k0, ST);
-        const View<T> d{static_cast<const T*>(l.D) + n0, 1, l.ldd};
-        const View<T> x{static_cast<const T*>(l.X) + k0, 1, l.ldx};
+        const View d{static_cast<const float*>(l.D) + n0, 1, l.ldd};
+        const View x{static_cast<const float*>(l.X) + k0, 1, l.ldx};
         float acc[4][4] = {};
         simt_accumulate(acc, s, d, x, groups.first[g], groups.first[g + 1],
                         [&](int i, int) { return i < rows; }, [&](int j, int) { return j < cols; });
@@ -63,9 +63,9 @@ __global__ void __launch_bounds__(ST_THREADS) grouped_wgrad_simt_kernel(const Gr
 cudaError_t grouped_simt_launch(const GroupedLaunch& l, cudaStream_t stream)
 {
     const int64_t tiles = (l.by.rows / ST + static_cast<int64_t>(l.by.groups)) * ((l.N + ST - 1) / ST);
-    return with_types(l.in_dtype, l.out_dtype, [&](auto in, auto out) {
+    return with_type(l.out_dtype, [&](auto out) {
         note_launch();
-        grouped_simt_kernel<decltype(in), decltype(out)>
+        grouped_simt_kernel<decltype(out)>
             <<<simt_blocks(tiles, l.num_sms), ST_THREADS, 0, stream>>>(l);
         return cudaGetLastError();
     });
@@ -74,9 +74,9 @@ cudaError_t grouped_simt_launch(const GroupedLaunch& l, cudaStream_t stream)
 cudaError_t grouped_wgrad_simt_launch(const GroupedWgradLaunch& l, cudaStream_t stream)
 {
     const int64_t tiles = static_cast<int64_t>(l.by.groups) * ((l.N + ST - 1) / ST) * ((l.K + ST - 1) / ST);
-    return with_types(l.in_dtype, l.out_dtype, [&](auto in, auto out) {
+    return with_type(l.out_dtype, [&](auto out) {
         note_launch();
-        grouped_wgrad_simt_kernel<decltype(in), decltype(out)>
+        grouped_wgrad_simt_kernel<decltype(out)>
             <<<simt_blocks(tiles, l.num_sms), ST_THREADS, 0, stream>>>(l);
         return cudaGetLastError();
     });

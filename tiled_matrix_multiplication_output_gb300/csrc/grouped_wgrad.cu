@@ -3,12 +3,6 @@
 
 namespace tmmo {
 
-bool grouped_wgrad_tc_takes(const GroupedWgradLaunch& l)
-{
-    return l.in_dtype != DT_F32 && l.by.rows > 0 && aligned_rows(l.D, l.ldd, l.in_dtype) &&
-           aligned_rows(l.X, l.ldx, l.in_dtype);
-}
-
 cudaError_t grouped_wgrad_tc_launch(const GroupedWgradLaunch& l, cudaStream_t stream)
 {
     GroupedTcParams p{};

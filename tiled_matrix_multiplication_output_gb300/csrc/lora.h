@@ -36,8 +36,7 @@ struct LoraLaunch {
     int64_t ldy;
     int rows, N, K, adapters, rank;
     int in_dtype, out_dtype;  // DT_*
-    float* t;             // FP32 units: rows x rank
-    void* t16;            // tensor cores: the same in parts (lora_tc.cuh)
+    void* t;              // the rank values: FP32, rows x rank, or in parts (lora_tc.cuh)
     int parts;
     void* plan;           // one for each 128 rows
     int num_sms;
@@ -50,8 +49,7 @@ struct LoraLaunch {
 struct LoraGradLaunch {
     const void* P;        // rows x cols
     int64_t ldp;
-    const float* t;       // FP32 units: rows x rank
-    const void* t16;      // tensor cores: in parts
+    const void* t;        // as LoraLaunch has them
     int parts;
     const void* plan;
     void* G;              // adapters; element (c, j) at c * step_c + j * step_j
@@ -68,16 +66,15 @@ struct LoraGradLaunch {
 constexpr int LORA_PLAN_BYTES = 2576;
 int lora_parts_bytes(int rank, int parts);
 
-// The tensor-core kernels, for 16-bit operands with rows on 16-byte boundaries.
-// Shrink makes the plans and the rank values; of two products, whose rows have the
+// On the tensor cores: 16-bit operands with rows on 16-byte boundaries (pack.h),
+// no size of zero.  Shrink makes the plans and the rank values; of two products, whose rows have the
 // same adapters, in one launch.  Expand may start while a shrink runs.
-bool lora_tc_takes(const LoraLaunch& l);
 cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* second, cudaStream_t stream);
 cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream);
 // Two gradients of the same rows in one launch (either may be null).
 cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStream_t stream);
 
-// The FP32 units, for every operand.
+// On the FP32 units: FP32 operands, and sums of nothing.
 cudaError_t lora_simt_shrink(const LoraLaunch& l, cudaStream_t stream);
 cudaError_t lora_simt_expand(const LoraLaunch& l, cudaStream_t stream);
 cudaError_t lora_simt_grad(const LoraGradLaunch& l, cudaStream_t stream);

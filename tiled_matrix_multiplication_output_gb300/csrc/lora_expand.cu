@@ -432,19 +432,6 @@ cudaError_t launch(int out_dtype, const CUtensorMap (&m)[5], const ExpandParams&
 
 int lora_parts_bytes(int rank, int parts) { return 2 * lora_parts(rank, parts).columns(); }
 
-bool lora_tc_takes(const LoraLaunch& l)
-{
-    if (l.in_dtype == DT_F32 || l.K == 0)
-        return false;
-    const int dt = l.in_dtype;
-    auto stack = [&](const void* p, int64_t ld, int64_t stride) {
-        return aligned_rows(p, ld, dt) &&
-               (l.adapters == 1 || stride == 0 || (stride >= ld && (stride * type_bytes(dt)) % 16 == 0));
-    };
-    return aligned_rows(l.X, l.ldx, dt) && (!l.W || aligned_rows(l.W, l.ldw, dt)) &&
-           (l.adapters == 0 || (stack(l.F, l.ldf, l.stride_f) && stack(l.E, l.lde, l.stride_e)));
-}
-
 cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
 {
     ExpandParams p{};
@@ -472,7 +459,7 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     m[2] = m[3] = m[4] = m[0];
     if (ok && p.adapters) {
         const int64_t stacked = p.one ? 1 : l.adapters, stride = p.one ? l.lde : l.stride_e;
-        ok = encode_map(&m[2], dt, l.t16, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, TC_BM, 1}) &&
+        ok = encode_map(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, TC_BM, 1}) &&
              (l.across ? encode_map(&m[3], dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
                        : encode_map(&m[3], dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride}, {64, TC_BM, 1}));
     }

@@ -432,7 +432,7 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStr
         p.side[i] = {(s.cols + 127) / 128, s.cols, s.G, s.step_c, s.step_j, s.stride_g};
         items[i] = static_cast<int64_t>(p.side[i].tiles_c) * p.groups_j * s.adapters;
         if (!encode_map(&m[2 * i], s.in_dtype, s.P, 2, {s.cols, s.rows, 1}, {s.ldp, 0}, {64, 64, 1}) ||
-            !encode_map(&m[2 * i + 1], s.in_dtype, s.t16, 2, {p.lay.columns(), s.rows, 1},
+            !encode_map(&m[2 * i + 1], s.in_dtype, s.t, 2, {p.lay.columns(), s.rows, 1},
                         {p.lay.columns(), 0}, {64, 64, 1}))
             return cudaErrorNotSupported;
     }
@@ -445,7 +445,7 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStr
         return cudaErrorNotSupported;
     p.items0 = static_cast<int>(items[0]);
     p.items = static_cast<int>(items[0] + items[1]);
-    return with_in_type(l.out_dtype, [&](auto out) {
+    return with_type(l.out_dtype, [&](auto out) {
         return launch<decltype(out)>(m, p, l.num_sms, stream);
     });
 }

@@ -344,7 +344,7 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
         const LoraLaunch& s = i ? *second : first;
         const uint32_t cols = static_cast<uint32_t>(p.cols);
         p.side[i] = {(s.K + TC_BK - 1) / TC_BK, s.across, s.adapters == 1 || s.stride_f == 0, tc_idesc(s.in_dtype == DT_BF16, LT_ROWS, p.cols, false, s.across),
-                     s.t16};
+                     s.t};
         p.b_bytes[i] = (s.across ? (p.cols + 63) / 64 * 64 : p.cols) * 128;
         most_k = std::max(most_k, p.side[i].k_blocks);
         const int64_t stride = p.side[i].one ? s.ldf : s.stride_f;

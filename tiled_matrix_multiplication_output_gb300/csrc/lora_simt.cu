@@ -1,4 +1,4 @@
-// Low-rank adapters on the FP32 units: 64 x 64 tiles of the shared product,
+// Low-rank adapters on the FP32 units, of FP32 operands: 64 x 64 tiles of the shared product,
 // and of each adapter's among the tile's rows.
 #include "launch.h"
 #include "lora.h"
@@ -35,7 +35,6 @@ __device__ __forceinline__ void each_adapter(const int (&s)[ST], F f)
     }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(ST_THREADS) lora_shrink_kernel(const LoraLaunch l)
 {
     __shared__ SimtSmem s;
@@ -47,10 +46,10 @@ __global__ void __launch_bounds__(ST_THREADS) lora_shrink_kernel(const LoraLaunc
         const int row0 = static_cast<int>(tile / tiles_r) * ST, j0 = static_cast<int>(tile % tiles_r) * ST;
         const int cols = min(l.rank - j0, ST);
         load_adapters(of, l.adapter, row0, l.rows, l.adapters);
-        const View<T> x{static_cast<const T*>(l.X) + row0 * l.ldx, l.ldx, 1};
+        const View x{static_cast<const float*>(l.X) + row0 * l.ldx, l.ldx, 1};
         each_adapter(of, [&](int g) {
-            const T* f = static_cast<const T*>(l.F) + g * l.stride_f;
-            const View<T> v = l.across ? View<T>{f + j0, 1, l.ldf} : View<T>{f + j0 * l.ldf, l.ldf, 1};
+            const float* f = static_cast<const float*>(l.F) + g * l.stride_f;
+            const View v = l.across ? View{f + j0, 1, l.ldf} : View{f + j0 * l.ldf, l.ldf, 1};
             float acc[4][4] = {};
             simt_accumulate(acc, s, x, v, 0, l.K, [&](int i, int) { return of[i] == g; },
                             [&](int j, int) { return j < cols; });
@@ -60,13 +59,13 @@ __global__ void __launch_bounds__(ST_THREADS) lora_shrink_kernel(const LoraLaunc
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (of[r0 + i] == g && c0 + j < cols)
-                        l.t[static_cast<int64_t>(row0 + r0 + i) * l.rank + j0 + c0 + j] =
+                        static_cast<float*>(l.t)[static_cast<int64_t>(row0 + r0 + i) * l.rank + j0 + c0 + j] =
                             scale * acc[i][j];
         });
     }
 }
 
-template <typename T, typename OutT>
+template <typename OutT>
 __global__ void __launch_bounds__(ST_THREADS) lora_expand_kernel(const LoraLaunch l)
 {
     __shared__ SimtSmem s;
@@ -78,16 +77,16 @@ __global__ void __launch_bounds__(ST_THREADS) lora_expand_kernel(const LoraLaunc
         const int row0 = static_cast<int>(tile / tiles_n) * ST, n0 = static_cast<int>(tile % tiles_n) * ST;
         const int rows = min(l.rows - row0, ST), cols = min(l.N - n0, ST);
         load_adapters(of, l.adapter, row0, l.rows, l.adapters);
-        const View<T> x{static_cast<const T*>(l.X) + row0 * l.ldx, l.ldx, 1};
+        const View x{static_cast<const float*>(l.X) + row0 * l.ldx, l.ldx, 1};
         auto columns = [&](const void* base, int64_t off, int64_t ld) {
-            const T* p = static_cast<const T*>(base) + off;
-            return l.across ? View<T>{p + n0, 1, ld} : View<T>{p + n0 * ld, ld, 1};
+            const float* p = static_cast<const float*>(base) + off;
+            return l.across ? View{p + n0, 1, ld} : View{p + n0 * ld, ld, 1};
         };
         auto in_cols = [&](int j, int) { return j < cols; };
         float acc[4][4] = {};
         simt_accumulate(acc, s, x, columns(l.W, 0, l.ldw), 0, l.K, [&](int i, int) { return i < rows; },
                         in_cols);
-        const View<float> t{l.t + static_cast<int64_t>(row0) * l.rank, l.rank, 1};
+        const View t{static_cast<const float*>(l.t) + static_cast<int64_t>(row0) * l.rank, l.rank, 1};
         each_adapter(of, [&](int g) {
             float add[4][4] = {};
             simt_accumulate(add, s, t, columns(l.E, g * l.stride_e, l.lde), 0, l.rank,
@@ -103,7 +102,7 @@ __global__ void __launch_bounds__(ST_THREADS) lora_expand_kernel(const LoraLaunc
     }
 }
 
-template <typename T, typename OutT>
+template <typename OutT>
 __global__ void __launch_bounds__(ST_THREADS) lora_grad_kernel(const LoraGradLaunch l)
 {
     __shared__ SimtSmem s;
@@ -114,8 +113,8 @@ __global__ void __launch_bounds__(ST_THREADS) lora_grad_kernel(const LoraGradLau
         const int g = static_cast<int>(tile / per), u = static_cast<int>(tile % per);
         const int p0 = u / tiles_r * ST, j0 = u % tiles_r * ST;
         const int rows = min(l.cols - p0, ST), cols = min(l.rank - j0, ST);
-        const View<T> p{static_cast<const T*>(l.P) + p0, 1, l.ldp};
-        const View<float> t{l.t + j0, 1, l.rank};
+        const View p{static_cast<const float*>(l.P) + p0, 1, l.ldp};
+        const View t{static_cast<const float*>(l.t) + j0, 1, l.rank};
         float acc[4][4] = {};
         for (int k = 0; k < l.rows; k += ST_K) {
             const int i = k + static_cast<int>(threadIdx.x);
@@ -140,19 +139,17 @@ __global__ void __launch_bounds__(ST_THREADS) lora_grad_kernel(const LoraGradLau
 cudaError_t lora_simt_shrink(const LoraLaunch& l, cudaStream_t stream)
 {
     const int64_t tiles = static_cast<int64_t>((l.rows + ST - 1) / ST) * ((l.rank + ST - 1) / ST);
-    return with_in_type(l.in_dtype, [&](auto in) {
-        note_launch();
-        lora_shrink_kernel<decltype(in)><<<simt_blocks(tiles, l.num_sms), ST_THREADS, 0, stream>>>(l);
-        return cudaGetLastError();
-    });
+    note_launch();
+    lora_shrink_kernel<<<simt_blocks(tiles, l.num_sms), ST_THREADS, 0, stream>>>(l);
+    return cudaGetLastError();
 }
 
 cudaError_t lora_simt_expand(const LoraLaunch& l, cudaStream_t stream)
 {
     const int64_t tiles = static_cast<int64_t>((l.rows + ST - 1) / ST) * ((l.N + ST - 1) / ST);
-    return with_types(l.in_dtype, l.out_dtype, [&](auto in, auto out) {
+    return with_type(l.out_dtype, [&](auto out) {
         note_launch();
-        lora_expand_kernel<decltype(in), decltype(out)>
+        lora_expand_kernel<decltype(out)>
             <<<simt_blocks(tiles, l.num_sms), ST_THREADS, 0, stream>>>(l);
         return cudaGetLastError();
     });
@@ -162,9 +159,9 @@ cudaError_t lora_simt_grad(const LoraGradLaunch& l, cudaStream_t stream)
 {
     const int64_t tiles = static_cast<int64_t>(l.adapters) * ((l.cols + ST - 1) / ST) *
                           ((l.rank + ST - 1) / ST);
-    return with_types(l.in_dtype, l.out_dtype, [&](auto in, auto out) {
+    return with_type(l.out_dtype, [&](auto out) {
         note_launch();
-        lora_grad_kernel<decltype(in), decltype(out)>
+        lora_grad_kernel<decltype(out)>
             <<<simt_blocks(tiles, l.num_sms), ST_THREADS, 0, stream>>>(l);
         return cudaGetLastError();
     });

@@ -21,11 +21,10 @@ __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // Element (i, k) of an operand at p[i * outer + k * inner].
-template <typename T>
 struct View {
-    const T* p;
+    const float* p;
     int64_t outer, inner;
-    __device__ float at(int i, int k) const { return to_f32(p[i * outer + k * inner]); }
+    __device__ float at(int i, int k) const { return p[i * outer + k * inner]; }
 };
 
 struct alignas(16) SimtSmem {  // read as float4
@@ -35,8 +34,8 @@ struct alignas(16) SimtSmem {  // read as float4
 
 // Fills one operand's step: keep(i, k) says which elements exist; others are
 // zero.  Threads run along whichever axis is contiguous.
-template <typename T, typename Keep>
-__device__ __forceinline__ void simt_fill(float (&s)[ST_K][ST + 4], const View<T>& v, int k0, Keep keep)
+template <typename Keep>
+__device__ __forceinline__ void simt_fill(float (&s)[ST_K][ST + 4], const View& v, int k0, Keep keep)
 {
     const int tid = threadIdx.x;
 #pragma unroll
@@ -49,9 +48,9 @@ __device__ __forceinline__ void simt_fill(float (&s)[ST_K][ST + 4], const View<T
 
 // acc += A B^T over [k0, k1) of the operands' inner axis, this thread's
 // values: rows 4 * (tid / 16) + i, columns 4 * (tid % 16) + j.
-template <typename TA, typename TB, typename KeepA, typename KeepB>
-__device__ __forceinline__ void simt_accumulate(float (&acc)[4][4], SimtSmem& s, const View<TA>& a,
-                                                const View<TB>& b, int k0, int k1, KeepA keep_a,
+template <typename KeepA, typename KeepB>
+__device__ __forceinline__ void simt_accumulate(float (&acc)[4][4], SimtSmem& s, const View& a,
+                                                const View& b, int k0, int k1, KeepA keep_a,
                                                 KeepB keep_b)
 {
     const int r0 = 4 * (threadIdx.x / 16), c0 = 4 * (threadIdx.x % 16);

@@ -14,7 +14,7 @@ namespace tmmo {
 
 // Calls f with a value of the type a DT_* code names.
 template <typename F>
-cudaError_t with_in_type(int dtype, F f)
+cudaError_t with_type(int dtype, F f)
 {
     switch (dtype) {
     case DT_F32:
@@ -24,13 +24,6 @@ cudaError_t with_in_type(int dtype, F f)
     default:
         return f(__nv_bfloat16{});
     }
-}
-template <typename F>
-cudaError_t with_types(int in_dtype, int out_dtype, F f)
-{
-    return with_in_type(in_dtype, [&](auto in) {
-        return with_in_type(out_dtype, [&](auto out) { return f(in, out); });
-    });
 }
 
 inline unsigned simt_blocks(int64_t tiles, int num_sms)
