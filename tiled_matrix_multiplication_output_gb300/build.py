@@ -30,7 +30,8 @@ SOURCES = ("api.cu", "tc_gemm.cu", "tc_gemm_nn.cu", "tc_gemm_tn.cu", "tc_gemm_nt
            "model.cu", "api_fp8.cu", "fp8_quantize.cu", "fp8_gemm.cu", "fp8_small.cu",
            "api_newton_schulz.cu", "newton_schulz.cu", "ns_resident.cu",
            "api_grouped.cu", "grouped_simt.cu", "grouped_gemm.cu", "grouped_wgrad.cu",
-           "api_lora.cu", "lora_simt.cu", "lora_shrink.cu", "lora_expand.cu", "lora_grad.cu", "pack.cu")
+           "api_lora.cu", "lora_simt.cu", "lora_shrink.cu", "lora_expand.cu", "lora_small.cu",
+           "lora_grad.cu", "pack.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "-I" + INCLUDE, "-I" + CSRC]

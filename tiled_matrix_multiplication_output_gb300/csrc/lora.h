@@ -71,6 +71,9 @@ int lora_parts_bytes(int rank, int parts);
 // same adapters, in one launch.  Expand may start while a shrink runs.
 cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* second, cudaStream_t stream);
 cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream);
+// The kernel for few output tiles, and whether it is the choice.
+bool lora_small_takes(const LoraLaunch& l);
+cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream);
 // Two gradients of the same rows in one launch (either may be null).
 cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStream_t stream);
 

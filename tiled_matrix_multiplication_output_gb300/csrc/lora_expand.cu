@@ -434,6 +434,8 @@ int lora_parts_bytes(int rank, int parts) { return 2 * lora_parts(rank, parts).c
 
 cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
 {
+    if (lora_small_takes(l))
+        return lora_small_tc_launch(l, stream);
     ExpandParams p{};
     p.M = l.rows;
     p.N = l.N;

@@ -22,6 +22,7 @@ namespace {
 constexpr int LS_THREADS = 256;  // warps 0: copies, 1: MMA, 4-7: accumulator
 constexpr int LS_MAX_STAGES = 8;
 constexpr int LS_RING = 192 * 1024;
+constexpr int LS_RING_SHARED = 100 * 1024;  // leaves room for the product's kernel on the SM
 
 struct ShrinkSide {
     int k_blocks;
@@ -362,7 +363,11 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
     }
     p.stage_bytes = 16384 + std::max(p.b_bytes[0], p.b_bytes[1]);
     p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
-    p.stages = std::min(LS_MAX_STAGES, LS_RING / p.stage_bytes);
+    // the sums of a tile lie in the ring at the end
+    const int ring = p.stage_bytes * 4 <= LS_RING_SHARED && LT_ROWS * (p.cols + 1) * 4 <= LS_RING_SHARED
+                         ? LS_RING_SHARED
+                         : LS_RING;
+    p.stages = std::min(LS_MAX_STAGES, ring / p.stage_bytes);
     // CTAs for every SM: first the contraction is split, then the adapters
     // dealt out.
     int splits = 1;
@@ -372,8 +377,8 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
     p.deal = std::max(1, std::min(most_adapters, l.num_sms / (p.tiles * sides * splits)));
     const int64_t blocks = static_cast<int64_t>(p.tiles) * sides * splits * p.deal;
     return l.in_dtype == DT_BF16
-               ? launch<__nv_bfloat16>(m, p, static_cast<unsigned>(blocks), splits, LS_RING + 1024, stream)
-               : launch<__half>(m, p, static_cast<unsigned>(blocks), splits, LS_RING + 1024, stream);
+               ? launch<__nv_bfloat16>(m, p, static_cast<unsigned>(blocks), splits, ring + 1024, stream)
+               : launch<__half>(m, p, static_cast<unsigned>(blocks), splits, ring + 1024, stream);
 }
 
 }  // namespace tmmo
