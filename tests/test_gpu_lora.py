@@ -71,6 +71,7 @@ SHAPES = [
     (64, 256, 512, 64, 16, "mixed"), (33, 77, 99, 2, 5, "mixed"), (130, 384, 72, 7, 64, "mixed"),
     (300, 136, 264, 3, 12, "runs"), (513, 520, 1032, 5, 33, "runs"), (257, 264, 136, 2, 128, "one"),
     (129, 128, 64, 2, 256, "mixed"), (200, 264, 136, 3, 16, "none"), (700, 1000, 40, 40, 8, "runs"),
+    (2100, 64, 72, 100, 8, "mixed"), (64, 1000, 328, 30, 24, "mixed"), (1300, 2056, 264, 9, 40, "runs"),
 ]
 
 

@@ -15,7 +15,7 @@ namespace tmmo {
 inline int type_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
 
 // A tensor of up to three dimensions, innermost first, in boxes whose rows are
-// 128 bytes, swizzled; strides in elements.
+// 128, 64 or 32 bytes, swizzled over that length; strides in elements.
 inline bool encode_map(CUtensorMap* map, int dt, const void* base, int rank, const int64_t (&dims)[3],
                        const int64_t (&strides)[2], const uint32_t (&box)[3])
 {
@@ -31,8 +31,12 @@ inline bool encode_map(CUtensorMap* map, int dt, const void* base, int rank, con
     for (int i = 0; i < 2; ++i)
         s[i] = static_cast<cuuint64_t>(strides[i]) * type_bytes(dt);
     const cuuint32_t step[3] = {1, 1, 1};
+    const uint32_t row = box[0] * static_cast<uint32_t>(type_bytes(dt));
     return fn(map, type, rank, const_cast<void*>(base), d, s, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+              : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                          : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -70,6 +70,8 @@ int lora_parts_bytes(int rank, int parts);
 // no size of zero.  Shrink makes the plans and the rank values; of two products, whose rows have the
 // same adapters, in one launch.  Expand may start while a shrink runs.
 cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* second, cudaStream_t stream);
+// Whether a shrink alone leaves room on its SMs for the product's kernel.
+bool lora_shrink_shares(const LoraLaunch& l);
 cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream);
 // The kernel for few output tiles, and whether it is the choice.
 bool lora_small_takes(const LoraLaunch& l);

@@ -51,36 +51,53 @@ struct ExpandLayout {
 };
 
 // The adapters of a pair's 256 rows, ascending, from the plans of its halves.
-struct PairAdapters {
-    const LoraPlan* half[2];
-    int count[2], at[2];
-
-    __device__ PairAdapters(const ExpandParams& p, int mb)
+// What comes next is loaded ahead, so that the tile's shared product hides it.
+class PairAdapters {
+public:
+    __device__ void begin(const ExpandParams& p, int mb)
     {
         const int plans = (p.M + LT_ROWS - 1) / LT_ROWS;
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-            half[h] = p.plan + 2 * mb + h;
-            count[h] = 2 * mb + h < plans ? half[h]->count : 0;
-            at[h] = 0;
+            half_[h] = p.plan + 2 * mb + h;
+            count_[h] = 2 * mb + h < plans ? half_[h]->count : 0;
+            at_[h] = 0;
+            // (the first entry lies in memory even if it is not one)
+            id_[h] = 2 * mb + h < plans ? half_[h]->ids[0] : 0;
+            rows_[h] = 2 * mb + h < plans ? *reinterpret_cast<const uint4*>(half_[h]->rows[0])
+                                          : make_uint4(0, 0, 0, 0);
         }
     }
     // The next adapter, or -1, and (off) the lanes that do not have it.
     __device__ int next(uint32_t (&off)[8])
     {
         int g[2];
+#pragma unroll
         for (int h = 0; h < 2; ++h)
-            g[h] = at[h] < count[h] ? half[h]->ids[at[h]] : 0x7fffffff;
+            g[h] = at_[h] < count_[h] ? id_[h] : 0x7fffffff;
         const int least = min(g[0], g[1]);
         if (least == 0x7fffffff)
             return -1;
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
             const bool has = g[h] == least;
-            for (int w = 0; w < 4; ++w)
-                off[4 * h + w] = has ? ~half[h]->rows[at[h]][w] : ~0u;
-            at[h] += has;
+            off[4 * h] = has ? ~rows_[h].x : ~0u;
+            off[4 * h + 1] = has ? ~rows_[h].y : ~0u;
+            off[4 * h + 2] = has ? ~rows_[h].z : ~0u;
+            off[4 * h + 3] = has ? ~rows_[h].w : ~0u;
+            at_[h] += has;
+            if (has && at_[h] < count_[h]) {
+                id_[h] = half_[h]->ids[at_[h]];
+                rows_[h] = *reinterpret_cast<const uint4*>(half_[h]->rows[at_[h]]);
+            }
         }
         return least;
     }
+
+private:
+    const LoraPlan* half_[2];
+    int count_[2], at_[2], id_[2];
+    uint4 rows_[2];
 };
 
 template <bool ACROSS, typename OutT>
@@ -186,6 +203,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 coords(t, mb, nb);
                 const int row = mb * 256 + static_cast<int>(rank) * TC_BM;
                 const int col = nb * 256 + static_cast<int>(rank) * TC_BM;
+                PairAdapters list;
+                if (waited)
+                    list.begin(p, mb);
                 for (int kb = 0; ok && kb < p.k_blocks; ++kb) {
                     const int k = kb * TC_BK;
                     ok = step(kb == p.fault_skip_kblock, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
@@ -201,10 +221,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if (!ok)
                     break;
                 if (p.adapters) {
-                    if (!waited)
+                    if (!waited) {
                         grid_dep_wait();
+                        list.begin(p, mb);
+                    }
                     waited = true;
-                    PairAdapters list(p, mb);
                     uint32_t off[8];
                     for (int g = list.next(off); ok && g >= 0; g = list.next(off)) {
                         const int z = p.one ? 0 : g;
@@ -277,6 +298,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+                PairAdapters list;
+                if (waited)
+                    list.begin(p, mb);
                 for (int kb = 0; ok && kb < p.k_blocks; ++kb)
                     ok = step([&](uint32_t a0, uint32_t b0) {
 #pragma unroll
@@ -289,10 +313,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if (!ok)
                     break;
                 if (p.adapters) {
-                    if (!waited)
+                    if (!waited) {
                         grid_dep_wait();
+                        list.begin(p, mb);
+                    }
                     waited = true;
-                    PairAdapters list(p, mb);
                     uint32_t off[8];
                     for (int g = list.next(off); ok && g >= 0; g = list.next(off))
                         for (int c = 0; ok && c < p.lay.chunks; ++c)

@@ -21,7 +21,7 @@ namespace {
 
 constexpr int LG_THREADS = 256;  // warps 0: copies, 1: MMA, 2: zeros, 4-7: epilogue
 constexpr int LG_MAX_STAGES = 8;
-constexpr int LG_RING = 192 * 1024;
+constexpr int LG_RING = 192 * 1024;  // beside 23 KiB of plans
 constexpr int LG_CHUNKS = 4;     // chunks of rank values in a tile
 
 struct GradSide {
@@ -65,11 +65,70 @@ __device__ __forceinline__ GradItem grad_item(int t, const GradParams& p)
     return w;
 }
 
+// The plans of all row tiles in shared memory, where they fit: every tile of the
+// gradient searches them (about 2 us a tile from global memory, 0.2 from here).
+constexpr int LG_PLANS = 512;     // row tiles
+constexpr int LG_ENTRIES = 1024;  // adapters of all of them
+struct PlanTable {
+    int first[LG_PLANS + 1];      // entries before each row tile
+    int ids[LG_ENTRIES];
+    alignas(16) uint4 rows[LG_ENTRIES];
+    int whole;                    // whether they fit
+};
+
+// Every thread of the block calls it; it ends in a block barrier.
+__device__ __forceinline__ void load_plans(PlanTable& t, const GradParams& p)
+{
+    if (threadIdx.x == 0)
+        t.whole = 0;
+    if (p.plans <= LG_PLANS) {
+        for (int i = threadIdx.x; i < p.plans; i += LG_THREADS)
+            t.first[i + 1] = p.plan[i].count;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            int sum = 0;
+            for (int base = 0; base < p.plans; base += 32) {
+                const int i = base + threadIdx.x;
+                int v = i < p.plans ? t.first[i + 1] : 0;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int o = __shfl_up_sync(0xffffffffu, v, d);
+                    if (static_cast<int>(threadIdx.x) >= d)
+                        v += o;
+                }
+                if (i < p.plans)
+                    t.first[i + 1] = sum + v;
+                sum += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (threadIdx.x == 0) {
+                t.first[0] = 0;
+                t.whole = sum <= LG_ENTRIES;
+            }
+        }
+        __syncthreads();
+        if (t.whole)
+            for (int e = threadIdx.x; e < t.first[p.plans]; e += LG_THREADS) {
+                int lo = 0, hi = p.plans;  // the tile of entry e
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (t.first[mid] <= e)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                const LoraPlan& plan = p.plan[lo];
+                t.ids[e] = plan.ids[e - t.first[lo]];
+                t.rows[e] = *reinterpret_cast<const uint4*>(plan.rows[e - t.first[lo]]);
+            }
+    }
+    __syncthreads();
+}
+
 // The 64-row blocks that hold rows of adapter g, in order; a whole warp steps
 // through them together.
 class RowBlocks {
 public:
-    __device__ RowBlocks(const GradParams& p, int g) : p_(p), g_(g) {}
+    __device__ RowBlocks(const GradParams& p, const PlanTable& table, int g) : p_(p), table_(table), g_(g) {}
     // The next block and its rows of g (a bit each); false at the end.
     __device__ bool next(int& block, uint64_t& rows)
     {
@@ -91,11 +150,10 @@ public:
             const int src = __ffs(hits_) - 1;
             hits_ &= hits_ - 1;
             tile_ = base_ + src;
-            uint32_t w[4];
-            for (int i = 0; i < 4; ++i)
-                w[i] = __shfl_sync(0xffffffffu, mine_[i], src);
-            lo_ = w[0] | static_cast<uint64_t>(w[1]) << 32;
-            hi_ = w[2] | static_cast<uint64_t>(w[3]) << 32;
+            const uint32_t w0 = __shfl_sync(0xffffffffu, mine_.x, src), w1 = __shfl_sync(0xffffffffu, mine_.y, src);
+            const uint32_t w2 = __shfl_sync(0xffffffffu, mine_.z, src), w3 = __shfl_sync(0xffffffffu, mine_.w, src);
+            lo_ = w0 | static_cast<uint64_t>(w1) << 32;
+            hi_ = w2 | static_cast<uint64_t>(w3) << 32;
             half_ = 0;
         }
     }
@@ -107,33 +165,31 @@ private:
         const int i = base_ + static_cast<int>(lane_id());
         bool found = false;
         if (i < p_.plans) {
-            const LoraPlan& plan = p_.plan[i];
-            int lo = 0, hi = plan.count;  // the first place whose id is not below g
-            const int count = hi;
+            const bool near = table_.whole;
+            const int first = near ? table_.first[i] : 0;
+            const int count = near ? table_.first[i + 1] - first : p_.plan[i].count;
+            const int* ids = near ? table_.ids + first : p_.plan[i].ids;
+            int lo = 0, hi = count;  // the first place whose id is not below g
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (plan.ids[mid] < g_)
+                if (ids[mid] < g_)
                     lo = mid + 1;
                 else
                     hi = mid;
             }
-            found = lo < count && plan.ids[lo] == g_;
-            if (found) {
-                const uint4 v = *reinterpret_cast<const uint4*>(plan.rows[lo]);
-                mine_[0] = v.x;
-                mine_[1] = v.y;
-                mine_[2] = v.z;
-                mine_[3] = v.w;
-            }
+            found = lo < count && ids[lo] == g_;
+            if (found)
+                mine_ = near ? table_.rows[first + lo] : *reinterpret_cast<const uint4*>(p_.plan[i].rows[lo]);
         }
         hits_ = __ballot_sync(0xffffffffu, found);
     }
 
     const GradParams& p_;
+    const PlanTable& table_;
     const int g_;
     int base_ = -32, tile_ = 0, half_ = 2;
     uint32_t hits_ = 0;
-    uint32_t mine_[4] = {};
+    uint4 mine_ = {};
     uint64_t lo_ = 0, hi_ = 0;
 };
 
@@ -141,6 +197,7 @@ struct GradSmem {
     uint64_t full[LG_MAX_STAGES], landed[LG_MAX_STAGES], empty[LG_MAX_STAGES], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int abort_flag;
+    PlanTable plans;
 };
 
 template <typename OutT>
@@ -179,6 +236,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         tmem_alloc<1>(smem_u32(&s.tmem), 512);
         tmem_relinquish<1>();
     }
+    load_plans(s.plans, p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -201,7 +259,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
             const GradItem w = grad_item(t, p);
-            RowBlocks blocks(p, w.g);
+            RowBlocks blocks(p, s.plans, w.g);
             int block;
             uint64_t rows;
             while (ok && blocks.next(block, rows)) {
@@ -249,7 +307,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
             const GradItem w = grad_item(t, p);
-            RowBlocks blocks(p, w.g);
+            RowBlocks blocks(p, s.plans, w.g);
             int block;
             uint64_t rows;
             const int acc = local & 1;
@@ -301,7 +359,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
             const GradItem w = grad_item(t, p);
-            RowBlocks blocks(p, w.g);
+            RowBlocks blocks(p, s.plans, w.g);
             int block;
             uint64_t rows;
             while (ok && blocks.next(block, rows)) {
@@ -337,7 +395,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         for (int t = blockIdx.x; t < p.items; t += gridDim.x) {
             const GradItem w = grad_item(t, p);
             const GradSide& side = p.side[w.which];
-            RowBlocks blocks(p, w.g);
+            RowBlocks blocks(p, s.plans, w.g);
             int block;
             uint64_t rows;
             const bool any = blocks.next(block, rows);

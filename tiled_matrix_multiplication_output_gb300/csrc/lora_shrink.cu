@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "grouped_maps.h"
 #include "lora_tc.cuh"
@@ -22,7 +23,7 @@ namespace {
 constexpr int LS_THREADS = 256;  // warps 0: copies, 1: MMA, 4-7: accumulator
 constexpr int LS_MAX_STAGES = 8;
 constexpr int LS_RING = 192 * 1024;
-constexpr int LS_RING_SHARED = 100 * 1024;  // leaves room for the product's kernel on the SM
+constexpr int LS_RING_SHARED = 88 * 1024;  // leaves room for the product's kernel on the SM
 
 struct ShrinkSide {
     int k_blocks;
@@ -40,7 +41,9 @@ struct ShrinkParams {
     int rows, adapters, rank, cols;  // cols: rank rounded up to 16
     LoraParts lay;
     int tiles, deal;                 // row tiles; clusters that share a tile's adapters
-    int stages, stage_bytes, b_bytes[2];
+    int stages, stage_bytes, a_offset, b_bytes[2];
+    int together;                    // adapters whose factors share a stage
+    int box_rows;                    // rows of X that a copy brings
     uint32_t tmem_cols;
     int* status;
     long long wait_budget;
@@ -50,68 +53,89 @@ struct ShrinkSmem {
     uint64_t full[LS_MAX_STAGES], empty[LS_MAX_STAGES], done;
     uint32_t tmem;
     int abort_flag;
-    int of[LT_ROWS];   // each row's adapter, then its place in the plan
-    int first[LT_ROWS];  // whether the row is the first of its adapter
+    int4 of4[LT_ROWS / 4];     // each row's adapter
+    int4 first4[LT_ROWS / 4];  // the same of its adapter's first row, else INT_MAX
+    int place[LT_ROWS];        // each row's place in the plan
+    float scale[LT_ROWS];      // of each place
     LoraPlan plan;
 };
 
-// The plan of 128 rows from their adapters s.of; every thread calls it.
-__device__ __forceinline__ void make_plan(ShrinkSmem& s, const int32_t* adapter, int row0, int rows, int adapters)
+// The plan of 128 rows from their adapters; every thread calls it.
+__device__ __forceinline__ void make_plan(ShrinkSmem& s, const ShrinkParams& p, int row0)
 {
     const int i = threadIdx.x;
+    int* of = reinterpret_cast<int*>(s.of4);
+    int* first = reinterpret_cast<int*>(s.first4);
+    int g = -1;
     if (i < LT_ROWS) {
-        const int g = row0 + i < rows ? adapter[row0 + i] : -1;
-        s.of[i] = g >= 0 && g < adapters ? g : -1;
+        if (row0 + i < p.rows)
+            g = p.adapter[row0 + i];
+        if (g >= p.adapters)
+            g = -1;
+        of[i] = g;
         for (int w = 0; w < 4; ++w)
             s.plan.rows[i][w] = 0;
     }
     if (i == 0)
         s.plan.count = 0;
     __syncthreads();
-    const int g = i < LT_ROWS ? s.of[i] : -1;
     if (i < LT_ROWS) {
-        bool first = g >= 0;
-        for (int j = 0; j < i; ++j)
-            first = first && s.of[j] != g;
-        s.first[i] = first;
-    }
-    __syncthreads();
-    int place = -1;
-    if (g >= 0) {
-        place = 0;
-        for (int j = 0; j < LT_ROWS; ++j)
-            place += s.first[j] && s.of[j] < g;
-        if (s.first[i]) {
-            s.plan.ids[place] = g;
-            atomicAdd(&s.plan.count, 1);
+        int before = 0;  // earlier rows with the same adapter
+#pragma unroll 4
+        for (int j = 0; j < LT_ROWS / 4; ++j) {
+            const int4 v = s.of4[j];
+            before |= (v.x == g & 4 * j < i) | (v.y == g & 4 * j + 1 < i) | (v.z == g & 4 * j + 2 < i) |
+                      (v.w == g & 4 * j + 3 < i);
         }
-        atomicOr(&s.plan.rows[place][i >> 5], 1u << (i & 31));
+        first[i] = g >= 0 && !before ? g : 0x7fffffff;
     }
     __syncthreads();
-    if (i < LT_ROWS)
-        s.of[i] = place;
+    if (i < LT_ROWS) {
+        int place = -1;
+        if (g >= 0) {
+            place = 0;
+#pragma unroll 4
+            for (int j = 0; j < LT_ROWS / 4; ++j) {
+                const int4 v = s.first4[j];
+                place += (v.x < g) + (v.y < g) + (v.z < g) + (v.w < g);
+            }
+            if (first[i] == g) {
+                s.plan.ids[place] = g;
+                s.scale[place] = p.scale ? p.scale[g] : 1.0f;
+                atomicAdd(&s.plan.count, 1);
+            }
+            atomicOr(&s.plan.rows[place][i >> 5], 1u << (i & 31));
+        }
+        s.place[i] = place;
+    }
     __syncthreads();
 }
 
+// The parts of rank values j .. j + 7 (a multiple of 8) of a row.
 template <typename T>
-__device__ __forceinline__ void store_parts(T* t, float v, const LoraParts& lay, int j)
+__device__ __forceinline__ void store_parts(T* t, float (&left)[8], const LoraParts& lay, int j)
 {
-    t += j / lay.chunk * 64 + j % lay.chunk;
-    float left = v;
-    for (int p = 0; p < lay.parts; ++p) {
-        T h;
-        put(&h, left);
-        t[p * lay.chunk] = h;
-        const float f = to_f32(h);
-        left = isfinite(f) ? left - f : 0.0f;  // an infinity has no remainder
+    t += (j / lay.chunk) * 64 + j % lay.chunk;
+#pragma unroll 1
+    for (int part = 0; part < lay.parts; ++part, t += lay.chunk) {
+        T h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            put(&h[i], left[i]);
+            const float f = to_f32(h[i]);
+            left[i] = isfinite(f) ? left[i] - f : 0.0f;  // an infinity has no remainder
+        }
+        uint4 w;
+        memcpy(&w, h, 16);
+        *reinterpret_cast<uint4*>(t) = w;
     }
 }
 
-template <typename T>
+template <typename T, int SPLITS>
 __global__ void __launch_bounds__(LS_THREADS, 1)
     lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX0, const __grid_constant__ CUtensorMap tmF0,
                           const __grid_constant__ CUtensorMap tmX1, const __grid_constant__ CUtensorMap tmF1,
-                          const ShrinkParams p, int splits)
+                          const ShrinkParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -121,8 +145,8 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
 
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
-    const int split = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    int id = blockIdx.x / splits;
+    const int split = SPLITS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    int id = blockIdx.x / SPLITS;
     const int tile = id % p.tiles;
     id /= p.tiles;
     const int deal = id % p.deal, which = id / p.deal;
@@ -132,6 +156,8 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     const int b_bytes = p.b_bytes[which];
     const int row0 = tile * LT_ROWS;
     const TcWatch watch{&s.abort_flag, p.status, p.wait_budget};
+    const int per = (side.k_blocks + SPLITS - 1) / SPLITS;
+    const int kb0 = min(split * per, side.k_blocks), kb1 = min(kb0 + per, side.k_blocks);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -148,7 +174,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
         tmem_alloc<1>(smem_u32(&s.tmem), p.tmem_cols);
         tmem_relinquish<1>();
     }
-    make_plan(s, p.adapter, row0, p.rows, p.adapters);
+    make_plan(s, p, row0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -160,32 +186,38 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
         for (int i = threadIdx.x; i < words; i += LS_THREADS)
             to[i] = from[i];
     }
-    const int per = (side.k_blocks + splits - 1) / splits;
-    const int kb0 = min(split * per, side.k_blocks), kb1 = min(kb0 + per, side.k_blocks);
     const int mine = s.plan.count > deal ? (s.plan.count - deal + p.deal - 1) / p.deal : 0;
-    const int steps = mine * (kb1 - kb0);
+    const int rounds = (mine + p.together - 1) / p.together;
+    const int steps = rounds * (kb1 - kb0);
+    // the i-th adapter of this CTA, by its place in the plan
+    auto nth = [&](int i) { return deal + i * p.deal; };
 
     if (warp == 0) {
         if (lane == 0) {
             int stage = 0, n = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int a = deal; ok && a < s.plan.count; a += p.deal) {
-                const int g = side.one ? 0 : s.plan.ids[a];
+            for (int i0 = 0; ok && i0 < mine; i0 += p.together) {
+                const int some = min(p.together, mine - i0);
                 for (int kb = kb0; kb < kb1; ++kb, ++n) {
                     if (!tc_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch)) {
                         ok = false;
                         break;
                     }
                     const uint32_t bar = smem_u32(&s.full[stage]);
-                    const uint32_t dA = smem_u32(ring) + stage * p.stage_bytes, dB = dA + 16384;
-                    mbar_arrive_expect_tx(bar, 16384 + b_bytes);
+                    const uint32_t base = smem_u32(ring) + stage * p.stage_bytes;
+                    const uint32_t dA = base + p.a_offset;
+                    mbar_arrive_expect_tx(bar, p.box_rows * 128 + some * b_bytes);
                     tma_load_2d(dA, tmX, bar, kb * TC_BK, row0);
-                    if (side.across) {
-                        for (int b = 0; b * 8192 < b_bytes; ++b)
-                            tma_load_3d(dB + b * 8192, tmF, bar, b * 64, kb * TC_BK, g);
-                    } else {
-                        tma_load_3d(dB, tmF, bar, kb * TC_BK, 0, g);
+                    for (int i = 0; i < some; ++i) {
+                        const int g = side.one ? 0 : s.plan.ids[nth(i0 + i)];
+                        const uint32_t dB = base + i * b_bytes;
+                        if (side.across) {
+                            for (int b = 0; b * 8192 < b_bytes; ++b)
+                                tma_load_3d(dB + b * 8192, tmF, bar, b * 64, kb * TC_BK, g);
+                        } else {
+                            tma_load_3d(dB, tmF, bar, kb * TC_BK, 0, g);
+                        }
                     }
                     if (++stage == p.stages) {
                         stage = 0;
@@ -208,23 +240,27 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int a = deal; ok && a < s.plan.count; a += p.deal) {
-                uint32_t off[4];
-                for (int w = 0; w < 4; ++w)
-                    off[w] = ~s.plan.rows[a][w];
+            for (int i0 = 0; ok && i0 < mine; i0 += p.together) {
+                const int some = min(p.together, mine - i0);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!tc_wait(smem_u32(&s.full[stage]), phase, watch)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(ring) + stage * p.stage_bytes, b0 = a0 + 16384;
+                    const uint32_t base = smem_u32(ring) + stage * p.stage_bytes;
+                    const uint32_t a0 = base + p.a_offset;
+                    for (int i = 0; i < some; ++i) {
+                        const uint32_t b0 = base + i * b_bytes;
+                        const uint4 rows = *reinterpret_cast<const uint4*>(s.plan.rows[nth(i0 + i)]);
+                        const uint32_t off[4] = {~rows.x, ~rows.y, ~rows.z, ~rows.w};
 #pragma unroll
-                    for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
-                        tc_mma_f16_lanes(tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
-                                         side.across ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                                     : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                         side.idesc, kb != kb0 || k != 0, off);
+                        for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
+                            tc_mma_f16_lanes(tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
+                                             side.across ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                         : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                             side.idesc, kb != kb0 || k != 0, off);
+                    }
                     tc_commit(smem_u32(&s.empty[stage]));
                     if (++stage == p.stages) {
                         stage = 0;
@@ -240,7 +276,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     }
     // The sums to shared memory; the ring holds nothing any more.
     __syncwarp();
-    const int pitch = p.cols + 1;
+    const int pitch = p.cols + 4;  // rows 16 bytes apart in the banks
     float* sums = reinterpret_cast<float*>(ring);
     if (warp >= 4) {
         const int row = (warp & 3) * 32 + lane;
@@ -256,8 +292,8 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
                     tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j, v);
                     tmem_wait_ld(v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sums[row * pitch + j + i] = __uint_as_float(v[i]);
+                    for (int i = 0; i < 16; i += 4)
+                        st_shared_v4(smem_u32(sums + row * pitch + j + i), v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
         } else {
@@ -266,59 +302,133 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
         }
         tc_fence_before();
     }
-    if (splits > 1)
+    if constexpr (SPLITS > 1)
         cluster_sync();
     else
         __syncthreads();
     tc_fence_after();
     if (warp == 1)
         tmem_dealloc<1>(tmem, p.tmem_cols);
-    // Each CTA adds up and stores its share of the rows.
+    // Each CTA adds up and stores its share of the rows, eight values of a row a
+    // thread.
     int gave_up = s.abort_flag;
-    for (int k = 0; k < splits && splits > 1; ++k)
-        gave_up |= __float_as_int(ld_cluster_f32(mapa_shared(smem_u32(&s.abort_flag), k)));
-    const int share = LT_ROWS / splits;
-    const int columns = p.lay.columns();
-    T* t = static_cast<T*>(side.t);
-    for (int i = threadIdx.x; i < share * p.cols && !gave_up; i += LS_THREADS) {
-        const int row = split * share + i / p.cols, j = i % p.cols;
-        const int place = s.of[row];
-        if (row0 + row >= p.rows || (place < 0 ? deal != 0 : place % p.deal != deal))
+    if constexpr (SPLITS > 1)
+        for (int k = 0; k < SPLITS; ++k)
+            gave_up |= __float_as_int(ld_cluster_f32(mapa_shared(smem_u32(&s.abort_flag), k)));
+    constexpr int SHARE = LT_ROWS / SPLITS;
+    const int eights = p.cols / 8;
+    const int total = min(SHARE, p.rows - row0 - split * SHARE) * eights;  // none where negative
+    T* t = static_cast<T*>(side.t) + static_cast<int64_t>(row0) * p.lay.columns();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < total && !gave_up; i += LS_THREADS) {
+        const int row = split * SHARE + i / eights, j = i % eights * 8;
+        const int place = s.place[row];
+        if (place < 0 ? deal != 0 : place % p.deal != deal)
             continue;
-        float sum = 0.0f;
-        if (place >= 0 && j < p.rank) {
-            if (splits == 1) {
-                sum = sums[row * pitch + j];
-            } else {
-                const uint32_t at = smem_u32(&sums[row * pitch + j]);
-                for (int k = 0; k < splits; ++k)
-                    sum += ld_cluster_f32(mapa_shared(at, k));
+        float sum[8] = {};
+        if (place >= 0) {
+            const uint32_t at = smem_u32(sums + row * pitch + j);
+            float4 v[SPLITS][2];
+#pragma unroll
+            for (int k = 0; k < SPLITS; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    v[k][h] = ld_cluster_v4(SPLITS > 1 ? mapa_shared(at, k) + 16 * h : at + 16 * h);
+            const float scale = s.scale[place];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 a = v[0][h];
+#pragma unroll
+                for (int k = 1; k < SPLITS; ++k) {
+                    a.x += v[k][h].x;
+                    a.y += v[k][h].y;
+                    a.z += v[k][h].z;
+                    a.w += v[k][h].w;
+                }
+                sum[4 * h] = scale * a.x;
+                sum[4 * h + 1] = scale * a.y;
+                sum[4 * h + 2] = scale * a.z;
+                sum[4 * h + 3] = scale * a.w;
             }
-            if (p.scale)
-                sum *= p.scale[s.plan.ids[place]];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                sum[q] = j + q < p.rank ? sum[q] : 0.0f;
         }
-        store_parts(t + static_cast<int64_t>(row0 + row) * columns, sum, p.lay, j);
+        store_parts(t + static_cast<int64_t>(row) * p.lay.columns(), sum, p.lay, j);
     }
-    if (splits > 1) {
+    if constexpr (SPLITS > 1) {
         __syncwarp();
         cluster_sync();  // nobody leaves while others read its sums
     }
 }
 
-template <typename T>
-cudaError_t launch(const CUtensorMap (&m)[4], const ShrinkParams& p, unsigned blocks, int splits, int smem,
+template <typename T, int SPLITS>
+cudaError_t launch(const CUtensorMap (&m)[4], const ShrinkParams& p, unsigned clusters, int smem,
                    cudaStream_t stream)
 {
     static ClusterCaps caps;
     int cap = 0;
-    const cudaError_t err = cluster_cap(lora_shrink_tc_kernel<T>, caps, 1, LS_THREADS, LS_RING + 1024, 1, &cap);
+    // The SM's memory is laid out for both kernels from the start: it is not
+    // laid out anew while a block runs.
+    cudaError_t err = cudaSuccess;
+    int device = 0;
+    err = cudaGetDevice(&device);
+    if (err == cudaSuccess && device >= 0 && device < kMaxDevices && caps.cap[device] == 0)
+        err = cudaFuncSetAttribute(lora_shrink_tc_kernel<T, SPLITS>,
+                                   cudaFuncAttributePreferredSharedMemoryCarveout,
+                                   cudaSharedmemCarveoutMaxShared);
+    if (err == cudaSuccess)
+        err = cluster_cap(lora_shrink_tc_kernel<T, SPLITS>, caps, 1, LS_THREADS, LS_RING + 1024, 1, &cap);
     if (err != cudaSuccess)
         return err;
-    ClusterLaunch l(blocks, splits, LS_THREADS, smem, stream);
-    return l.run(lora_shrink_tc_kernel<T>, m[0], m[1], m[2], m[3], p, splits);
+    ClusterLaunch l(clusters * SPLITS, SPLITS, LS_THREADS, smem, stream);
+    return l.run(lora_shrink_tc_kernel<T, SPLITS>, m[0], m[1], m[2], m[3], p);
+}
+
+template <typename T>
+cudaError_t launch(const CUtensorMap (&m)[4], const ShrinkParams& p, unsigned clusters, int splits, int smem,
+                   cudaStream_t stream)
+{
+    switch (splits) {
+    case 1:
+        return launch<T, 1>(m, p, clusters, smem, stream);
+    case 2:
+        return launch<T, 2>(m, p, clusters, smem, stream);
+    case 4:
+        return launch<T, 4>(m, p, clusters, smem, stream);
+    default:
+        return launch<T, 8>(m, p, clusters, smem, stream);
+    }
+}
+
+// A stage holds the factors of adapters that a tile has beside each other (two, or
+// as many as 8 KiB hold), and after them X's rows, so that a K step of X is read
+// once for them.
+struct ShrinkRing {
+    int factor, together, a_offset, box_rows, stage_bytes;
+    bool shares;  // four stages leave room for the product's kernel on the SM
+};
+ShrinkRing shrink_ring(const LoraLaunch& l)
+{
+    ShrinkRing r;
+    const int cols = (l.rank + 15) / 16 * 16;
+    r.factor = (l.across ? (cols + 63) / 64 * 64 : cols) * 128;
+    r.together = std::min(std::min(std::max(2, 8192 / r.factor), 32768 / r.factor),
+                          std::min(std::min(l.adapters, LT_ROWS), l.rows));
+    r.a_offset = r.together * r.factor;
+    r.box_rows = std::min(LT_ROWS, (l.rows + 7) / 8 * 8);
+    r.stage_bytes = r.a_offset + (r.box_rows * 128 + 1023) / 1024 * 1024;
+    // The tensor core reads 128 rows of X whatever a copy brings: what follows
+    // lies within the ring too (those lanes are not used).  At the end the
+    // tile's sums lie in it.
+    r.shares = 3 * r.stage_bytes + r.a_offset + 16384 <= LS_RING_SHARED &&
+               LT_ROWS * (cols + 4) * 4 <= LS_RING_SHARED;
+    return r;
 }
 
 }  // namespace
+
+bool lora_shrink_shares(const LoraLaunch& l) { return l.adapters > 0 && shrink_ring(l).shares; }
 
 cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* second, cudaStream_t stream)
 {
@@ -333,6 +443,8 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
     p.cols = (l.rank + 15) / 16 * 16;
     p.lay = lora_parts(l.rank, l.parts);
     p.tiles = (l.rows + LT_ROWS - 1) / LT_ROWS;
+    p.box_rows = std::min(LT_ROWS, (l.rows + 7) / 8 * 8);
+    const uint32_t box_rows = static_cast<uint32_t>(p.box_rows);
     p.tmem_cols = 32;
     while (p.tmem_cols < static_cast<uint32_t>(p.cols))
         p.tmem_cols *= 2;
@@ -350,7 +462,7 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
         most_k = std::max(most_k, p.side[i].k_blocks);
         const int64_t stride = p.side[i].one ? s.ldf : s.stride_f;
         const int64_t stacked = p.side[i].one ? 1 : s.adapters;
-        if (!encode_map(&m[2 * i], s.in_dtype, s.X, 2, {s.K, s.rows, 1}, {s.ldx, 0}, {64, LT_ROWS, 1}) ||
+        if (!encode_map(&m[2 * i], s.in_dtype, s.X, 2, {s.K, s.rows, 1}, {s.ldx, 0}, {64, box_rows, 1}) ||
             !(s.across ? encode_map(&m[2 * i + 1], s.in_dtype, s.F, 3, {s.rank, s.K, stacked}, {s.ldf, stride},
                                     {64, TC_BK, 1})
                        : encode_map(&m[2 * i + 1], s.in_dtype, s.F, 3, {s.K, s.rank, stacked}, {s.ldf, stride},
@@ -361,24 +473,30 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
         m[2] = m[0];
         m[3] = m[1];
     }
-    p.stage_bytes = 16384 + std::max(p.b_bytes[0], p.b_bytes[1]);
-    p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
-    // the sums of a tile lie in the ring at the end
-    const int ring = p.stage_bytes * 4 <= LS_RING_SHARED && LT_ROWS * (p.cols + 1) * 4 <= LS_RING_SHARED
-                         ? LS_RING_SHARED
-                         : LS_RING;
-    p.stages = std::min(LS_MAX_STAGES, ring / p.stage_bytes);
+    const ShrinkRing r = shrink_ring(first);
+    if (second) {
+        const ShrinkRing q = shrink_ring(*second);
+        p.together = std::min(r.together, q.together);
+        p.a_offset = std::max(r.a_offset, q.a_offset);
+        p.stage_bytes = p.a_offset + (r.box_rows * 128 + 1023) / 1024 * 1024;
+    } else {
+        p.together = r.together;
+        p.a_offset = r.a_offset;
+        p.stage_bytes = r.stage_bytes;
+    }
+    const int ring = !second && r.shares ? LS_RING_SHARED : LS_RING;
+    p.stages = std::min(LS_MAX_STAGES, (ring - p.a_offset - 16384) / p.stage_bytes + 1);
+    const int most_adapters = std::min(std::min(l.adapters, LT_ROWS), l.rows);
     // CTAs for every SM: first the contraction is split, then the adapters
     // dealt out.
     int splits = 1;
     while (splits < 8 && 2 * splits <= most_k && p.tiles * sides * splits * 2 <= l.num_sms)
         splits *= 2;
-    const int most_adapters = std::min(std::min(l.adapters, LT_ROWS), l.rows);
     p.deal = std::max(1, std::min(most_adapters, l.num_sms / (p.tiles * sides * splits)));
-    const int64_t blocks = static_cast<int64_t>(p.tiles) * sides * splits * p.deal;
+    const int64_t clusters = static_cast<int64_t>(p.tiles) * sides * p.deal;
     return l.in_dtype == DT_BF16
-               ? launch<__nv_bfloat16>(m, p, static_cast<unsigned>(blocks), splits, ring + 1024, stream)
-               : launch<__half>(m, p, static_cast<unsigned>(blocks), splits, ring + 1024, stream);
+               ? launch<__nv_bfloat16>(m, p, static_cast<unsigned>(clusters), splits, ring + 1024, stream)
+               : launch<__half>(m, p, static_cast<unsigned>(clusters), splits, ring + 1024, stream);
 }
 
 }  // namespace tmmo

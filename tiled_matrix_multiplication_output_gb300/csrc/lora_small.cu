@@ -12,6 +12,7 @@
 // and small enough to share an SM with it: the shared product's weights are read
 // while the rank values are still being summed.
 #include <algorithm>
+#include <cstring>
 
 #include "grouped_maps.h"
 #include "lora_tc.cuh"
@@ -20,10 +21,11 @@
 namespace tmmo {
 namespace {
 
-constexpr int LM_THREADS = 256;  // warps 0: copies, 1: MMA, 4-7: accumulator
+constexpr int LM_THREADS = 256;  // warps 0: copies, 1: MMA, 2: plan, 4-7: accumulator
 constexpr int LM_MAX_STAGES = 8;
-constexpr int LM_RING = 112 * 1024;
-constexpr int LM_PITCH = 129;    // of the sums in shared memory
+constexpr int LM_RING = 200 * 1024;
+constexpr int LM_RING_SHARED = 120 * 1024;  // leaves room for the shrink's kernel on the SM
+constexpr int LM_PITCH = 132;    // of the sums in shared memory: rows 16 bytes apart in the banks
 
 struct SmallParams {
     int M, N, k_blocks, rank;
@@ -35,23 +37,74 @@ struct SmallParams {
     int64_t ldc;
     uint32_t idesc;
     int box_rows;            // rows of X that a copy brings
-    int stages, stage_bytes;
+    int stages, stage_bytes, ring;
+    bool words;              // 16-byte stores
+    int out_dtype;
+    // Adapters of up to 32 rank values: the tile's rank values stay in shared
+    // memory (behind the ring), and a stage holds the factors of several adapters,
+    // rows of 32 or 64 bytes; 0: an adapter a stage, with the rank values.
+    int beside;
     int* status;
     long long wait_budget;
     int fault_skip_kblock;
 };
 
 struct SmallSmem {
-    uint64_t full[LM_MAX_STAGES], empty[LM_MAX_STAGES], done;
+    uint64_t full[LM_MAX_STAGES], empty[LM_MAX_STAGES], planned, done;
     uint32_t tmem;
     int abort_flag;
+    int count, ids[LT_ROWS];  // this CTA's adapters
+    uint4 rows[LT_ROWS];
 };
 
-template <bool ACROSS, typename OutT>
-__global__ void __launch_bounds__(LM_THREADS, 2)
+// Eight values of a row, of which the first n exist; words: p is on a 16-byte
+// boundary.
+template <typename T>
+__device__ __forceinline__ void store_eight(T* p, const float (&v)[8], int n, bool words)
+{
+    alignas(16) T h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        put(&h[i], v[i]);
+    if (words && n >= 8) {
+        uint4 w[sizeof(T) / 2];
+        memcpy(w, h, sizeof h);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+            reinterpret_cast<uint4*>(p)[i] = w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                p[i] = h[i];
+    }
+}
+
+// Descriptor of a K-major operand whose rows are 32, 64 or 128 bytes.
+__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t addr, uint32_t width)
+{
+    const uint64_t mode = width == 128 ? 2 : width == 64 ? 4 : 6;
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | 1ull << 16 |
+           static_cast<uint64_t>(8 * width >> 4) << 32 | 1ull << 46 | mode << 61;
+}
+
+// store(C) with C as a pointer to the output's type.
+template <typename Store>
+__device__ __forceinline__ void with_output(const SmallParams& p, Store&& store)
+{
+    if (p.out_dtype == DT_F32)
+        store(static_cast<float*>(p.C));
+    else if (p.out_dtype == DT_F16)
+        store(static_cast<__half*>(p.C));
+    else
+        store(static_cast<__nv_bfloat16*>(p.C));
+}
+
+template <bool ACROSS, int SPLITS>
+__global__ void __launch_bounds__(LM_THREADS, 1)
     lora_small_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmE,
-                      const __grid_constant__ SmallParams p, int splits)
+                      const __grid_constant__ SmallParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -60,11 +113,11 @@ __global__ void __launch_bounds__(LM_THREADS, 2)
     __shared__ SmallSmem s;
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
-    const int split = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int tile = blockIdx.x / splits;
+    const int split = SPLITS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int tile = blockIdx.x / SPLITS;
     const int mb = tile / p.tiles_n, nb = tile % p.tiles_n;
     const int row0 = mb * LT_ROWS, col0 = nb * 128;
-    const int per = (p.k_blocks + splits - 1) / splits;
+    const int per = (p.k_blocks + SPLITS - 1) / SPLITS;
     const int kb0 = split * per, kb1 = min(kb0 + per, p.k_blocks);
     const TcWatch watch{&s.abort_flag, p.status, p.wait_budget};
     const LoraPlan& plan = p.plan[mb];
@@ -74,6 +127,7 @@ __global__ void __launch_bounds__(LM_THREADS, 2)
             mbar_init(smem_u32(&s.full[i]), 1);
             mbar_init(smem_u32(&s.empty[i]), 1);
         }
+        mbar_init(smem_u32(&s.planned), 1);
         mbar_init(smem_u32(&s.done), 1);
         s.abort_flag = 0;
         fence_mbar_init();
@@ -91,17 +145,18 @@ __global__ void __launch_bounds__(LM_THREADS, 2)
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     const uint32_t a_bytes = p.box_rows * 128;
+    const uint32_t held = ring + p.ring;  // the tile's rank values
 
     if (warp == 0) {
         if (lane == 0) {
             int stage = 0, n = 0;
             uint32_t phase = 0;
-            auto step = [&](bool skip, auto load) {
+            auto step = [&](bool skip, uint32_t bytes, auto load) {
                 if (!tc_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch))
                     return false;
                 if (!skip) {
                     const uint32_t bar = smem_u32(&s.full[stage]);
-                    mbar_arrive_expect_tx(bar, a_bytes + 16384);
+                    mbar_arrive_expect_tx(bar, bytes);
                     load(ring + stage * p.stage_bytes + 16384, ring + stage * p.stage_bytes, bar);
                     ++n;
                 }
@@ -113,7 +168,7 @@ __global__ void __launch_bounds__(LM_THREADS, 2)
             };
             bool ok = true;
             for (int kb = kb0; ok && kb < kb1; ++kb)
-                ok = step(kb == p.fault_skip_kblock, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                ok = step(kb == p.fault_skip_kblock, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
                     if (ACROSS) {
                         tma_load_2d(dB, &tmW, bar, col0, kb * TC_BK);
                         tma_load_2d(dB + 8192, &tmW, bar, col0 + 64, kb * TC_BK);
@@ -124,11 +179,26 @@ __global__ void __launch_bounds__(LM_THREADS, 2)
                 });
             if (ok && p.adapters) {
                 grid_dep_wait();
-                for (int a = split; ok && a < plan.count; a += splits) {
-                    const int z = p.one ? 0 : plan.ids[a];
+                ok = tc_wait(smem_u32(&s.planned), 0, watch);
+                if (!ACROSS && p.beside > 0) {
+                    for (int a = 0; ok && a < s.count; a += p.beside) {
+                        const int some = min(p.beside, s.count - a);
+                        const uint32_t each = p.lay.chunk * 2 * 128;
+                        ok = step(false, (a == 0 ? a_bytes : 0) + some * each,
+                                  [&](uint32_t, uint32_t dB, uint32_t bar) {
+                                      if (a == 0)
+                                          tma_load_2d(held, &tmT, bar, 0, row0);
+                                      for (int i = 0; i < some; ++i)
+                                          tma_load_3d(dB + i * each, &tmE, bar, 0, col0,
+                                                      p.one ? 0 : s.ids[a + i]);
+                                  });
+                    }
+                } else
+                for (int a = 0; ok && a < s.count; ++a) {
+                    const int z = p.one ? 0 : s.ids[a];
                     for (int c = 0; ok && c < p.lay.chunks; ++c) {
                         const int j = c * p.lay.chunk;
-                        ok = step(false, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                        ok = step(false, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
                             if (ACROSS) {
                                 tma_load_3d(dB, &tmE, bar, col0, j, z);
                                 tma_load_3d(dB + 8192, &tmE, bar, col0 + 64, j, z);
@@ -177,11 +247,27 @@ __global__ void __launch_bounds__(LM_THREADS, 2)
                                       p.idesc, kb != kb0 || k != 0);
                 });
             if (ok && p.adapters) {
-                grid_dep_wait();
-                for (int a = split; ok && a < plan.count; a += splits) {
-                    uint32_t off[4];
-                    for (int w = 0; w < 4; ++w)
-                        off[w] = ~plan.rows[a][w];
+                ok = tc_wait(smem_u32(&s.planned), 0, watch);
+                if (!ACROSS && p.beside > 0) {
+                    const uint32_t width = p.lay.chunk * 2;
+                    const int deep = p.lay.deep(0, p.rank);
+                    for (int a = 0; ok && a < s.count; a += p.beside)
+                        ok = step([&](uint32_t, uint32_t b0) {
+                            const int some = min(p.beside, s.count - a);
+                            for (int i = 0; i < some; ++i, b0 += width * 128) {
+                                const uint4 rows = s.rows[a + i];
+                                const uint32_t off[4] = {~rows.x, ~rows.y, ~rows.z, ~rows.w};
+                                for (int part = 0; part < p.lay.parts; ++part)
+                                    for (int k = 0; k < deep; ++k)
+                                        tc_mma_f16_lanes(tmem,
+                                                         smem_desc_sw128(held + part * width + k * 32, 16, 1024),
+                                                         smem_desc_rows(b0 + k * 32, width), p.idesc, 1, off);
+                            }
+                        });
+                } else
+                for (int a = 0; ok && a < s.count; ++a) {
+                    const uint4 rows = s.rows[a];
+                    const uint32_t off[4] = {~rows.x, ~rows.y, ~rows.z, ~rows.w};
                     for (int c = 0; ok && c < p.lay.chunks; ++c)
                         ok = step([&](uint32_t a0, uint32_t b0) {
                             const int deep = p.lay.deep(c, p.rank);
@@ -200,6 +286,19 @@ __global__ void __launch_bounds__(LM_THREADS, 2)
             while (!mbar_try_wait(smem_u32(&s.done), 0) && clock64() - t0 < p.wait_budget) {
             }
         }
+    } else if (warp == 2 && p.adapters) {
+        // this CTA's share of the tile's adapters
+        grid_dep_wait();
+        const int count = plan.count, mine = count > split ? (count - split + SPLITS - 1) / SPLITS : 0;
+        for (int i = lane; i < mine; i += 32) {
+            s.ids[i] = plan.ids[split + i * SPLITS];
+            s.rows[i] = *reinterpret_cast<const uint4*>(plan.rows[split + i * SPLITS]);
+        }
+        if (lane == 0)
+            s.count = mine;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_u32(&s.planned));
     }
     // The sums to shared memory; the ring holds nothing any more.
     __syncwarp();
@@ -213,84 +312,103 @@ __global__ void __launch_bounds__(LM_THREADS, 2)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (ok && q * 32 < rows) {
             tc_fence_after();
-            float* to = sums + (q * 32 + lane) * LM_PITCH;
+            const uint32_t to = smem_u32(sums + (q * 32 + lane) * LM_PITCH);
 #pragma unroll 1
             for (int j = 0; j < 128; j += 32) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + j, v);
                 tmem_wait_ld(v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    to[j + i] = __uint_as_float(v[i]);
+                for (int i = 0; i < 32; i += 4)
+                    st_shared_v4(to + (j + i) * 4, v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
         }
         tc_fence_before();
     }
     if (p.adapters)
         grid_dep_wait();  // this grid must not end before the one it depends on
-    if (splits > 1)
+    if constexpr (SPLITS > 1)
         cluster_sync();
     else
         __syncthreads();
     tc_fence_after();
     if (warp == 1)
         tmem_dealloc<1>(tmem, 128);
+    // (a lane asks each CTA: a loop would wait for one answer after another)
     int gave_up = s.abort_flag;
-    for (int k = 0; k < splits && splits > 1; ++k)
-        gave_up |= __float_as_int(ld_cluster_f32(mapa_shared(smem_u32(&s.abort_flag), k)));
-    // Each CTA adds up and stores its share: two rows at a time, with the
-    // columns along the threads.
-    const int col = threadIdx.x & 127;
-    OutT* out = static_cast<OutT*>(p.C) + row0 * p.ldc + col0 + col;
-    if (!gave_up && col0 + col < p.N)
-        for (int r = 2 * split + (threadIdx.x >> 7); r < rows; r += 2 * splits) {
-            float sum = 0.0f;
-            if (splits == 1) {
-                sum = sums[r * LM_PITCH + col];
-            } else {
-                const uint32_t at = smem_u32(&sums[r * LM_PITCH + col]);
-                float v[8];
+    if (SPLITS > 1 && static_cast<int>(lane) < SPLITS)
+        gave_up = __float_as_int(ld_cluster_f32(mapa_shared(smem_u32(&s.abort_flag), lane)));
+    // Each CTA adds up and stores its share: sixteen rows at a time, eight columns a
+    // thread.
+    const int col = (threadIdx.x & 15) * 8, cols = p.N - col0 - col;
+    uint32_t peer[SPLITS];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    v[k] = k < splits ? ld_cluster_f32(mapa_shared(at, k)) : 0.0f;
+    for (int k = 0; k < SPLITS; ++k) {
+        const uint32_t at = smem_u32(sums + col);
+        peer[k] = SPLITS > 1 ? mapa_shared(at, k) : at;
+    }
+#pragma unroll 1
+    for (int r0 = 16 * split; r0 < rows; r0 += 16 * SPLITS) {
+        const int r = r0 + (threadIdx.x >> 4);  // (rows behind the last: whatever is there)
+        float4 v[SPLITS][2];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    sum += v[k];
+        for (int k = 0; k < SPLITS; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                v[k][h] = ld_cluster_v4(peer[k] + r * LM_PITCH * 4 + 16 * h);
+        if (__any_sync(0xffffffffu, gave_up))
+            break;
+        float sum[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float4 a = v[0][h];
+#pragma unroll
+            for (int k = 1; k < SPLITS; ++k) {
+                a.x += v[k][h].x;
+                a.y += v[k][h].y;
+                a.z += v[k][h].z;
+                a.w += v[k][h].w;
             }
-            put(out + r * p.ldc, sum);
+            sum[4 * h] = a.x;
+            sum[4 * h + 1] = a.y;
+            sum[4 * h + 2] = a.z;
+            sum[4 * h + 3] = a.w;
         }
-    if (splits > 1) {
+        if (r < rows && cols > 0)
+            with_output(p, [&](auto* c) { store_eight(c + (row0 + r) * p.ldc + col0 + col, sum, cols, p.words); });
+    }
+    if constexpr (SPLITS > 1) {
         __syncwarp();
         cluster_sync();  // nobody leaves while others read its sums
     }
 }
 
-template <bool ACROSS, typename OutT>
-cudaError_t launch(const CUtensorMap (&m)[4], const SmallParams& p, int tiles, int splits,
-                   cudaStream_t stream)
+template <bool ACROSS, int SPLITS>
+cudaError_t launch(const CUtensorMap (&m)[4], const SmallParams& p, int tiles, cudaStream_t stream)
 {
     static ClusterCaps caps;
     int cap = 0;
     const cudaError_t err =
-        cluster_cap(lora_small_kernel<ACROSS, OutT>, caps, 1, LM_THREADS, LM_RING + 1024, 1, &cap);
+        cluster_cap(lora_small_kernel<ACROSS, SPLITS>, caps, 1, LM_THREADS, LM_RING + 1024, 1, &cap);
     if (err != cudaSuccess)
         return err;
-    ClusterLaunch l(static_cast<unsigned>(tiles * splits), splits, LM_THREADS, LM_RING + 1024, stream,
-                    p.adapters);
-    return l.run(lora_small_kernel<ACROSS, OutT>, m[0], m[1], m[2], m[3], p, splits);
+    ClusterLaunch l(static_cast<unsigned>(tiles * SPLITS), SPLITS, LM_THREADS,
+                    p.ring + (p.beside ? 16384 : 0) + 1024, stream, p.adapters);
+    return l.run(lora_small_kernel<ACROSS, SPLITS>, m[0], m[1], m[2], m[3], p);
 }
 
 template <bool ACROSS>
-cudaError_t launch(int out_dtype, const CUtensorMap (&m)[4], const SmallParams& p, int tiles, int splits,
-                   cudaStream_t stream)
+cudaError_t launch(const CUtensorMap (&m)[4], const SmallParams& p, int tiles, int splits, cudaStream_t stream)
 {
-    switch (out_dtype) {
-    case DT_F32:
-        return launch<ACROSS, float>(m, p, tiles, splits, stream);
-    case DT_F16:
-        return launch<ACROSS, __half>(m, p, tiles, splits, stream);
+    switch (splits) {
+    case 1:
+        return launch<ACROSS, 1>(m, p, tiles, stream);
+    case 2:
+        return launch<ACROSS, 2>(m, p, tiles, stream);
+    case 4:
+        return launch<ACROSS, 4>(m, p, tiles, stream);
     default:
-        return launch<ACROSS, __nv_bfloat16>(m, p, tiles, splits, stream);
+        return launch<ACROSS, 8>(m, p, tiles, stream);
     }
 }
 
@@ -317,12 +435,16 @@ cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     p.plan = static_cast<const LoraPlan*>(l.plan);
     p.C = l.Y;
     p.ldc = l.ldy;
+    p.out_dtype = l.out_dtype;
+    p.words = aligned_rows(l.Y, l.ldy, l.out_dtype);
     p.idesc = tc_idesc(l.in_dtype == DT_BF16, LT_ROWS, 128, false, l.across);
     p.box_rows = std::min(LT_ROWS, (l.rows + 7) / 8 * 8);
     p.stage_bytes = 16384 + (p.box_rows * 128 + 1023) / 1024 * 1024;
     // The tensor core reads 128 rows of A whatever a copy brings: what follows
     // lies within the ring too (those lanes are not used).
-    p.stages = std::min(LM_MAX_STAGES, (LM_RING - 32768) / p.stage_bytes + 1);
+    p.beside = p.adapters && !l.across && p.lay.chunks == 1 ? 16384 / (p.lay.chunk * 2 * 128) : 0;
+    p.ring = (!l.across && lora_shrink_shares(l) ? LM_RING_SHARED : LM_RING) - (p.beside ? 16384 : 0);
+    p.stages = std::min(LM_MAX_STAGES, (p.ring - 32768) / p.stage_bytes + 1);
     p.status = l.status;
     p.wait_budget = l.wait_budget;
     p.fault_skip_kblock = l.fault_skip_kblock;
@@ -337,7 +459,8 @@ cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream)
         const int64_t stacked = p.one ? 1 : l.adapters, stride = p.one ? l.lde : l.stride_e;
         ok = encode_map(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, box, 1}) &&
              (l.across ? encode_map(&m[3], dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
-                       : encode_map(&m[3], dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride}, {64, 128, 1}));
+                       : encode_map(&m[3], dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride},
+                                    {p.beside ? static_cast<uint32_t>(p.lay.chunk) : 64u, 128, 1}));
     }
     if (!ok)
         return cudaErrorNotSupported;
@@ -350,8 +473,8 @@ cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     };
     while (fits(2 * splits))
         splits *= 2;
-    return l.across ? launch<true>(l.out_dtype, m, p, tiles, splits, stream)
-                    : launch<false>(l.out_dtype, m, p, tiles, splits, stream);
+    return l.across ? launch<true>(m, p, tiles, splits, stream)
+                    : launch<false>(m, p, tiles, splits, stream);
 }
 
 }  // namespace tmmo

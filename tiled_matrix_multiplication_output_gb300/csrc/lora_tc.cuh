@@ -26,7 +26,7 @@ namespace tmmo {
 
 constexpr int LT_ROWS = 128;  // rows of a tile, the lanes of a CTA
 
-struct LoraPlan {
+struct alignas(16) LoraPlan {
     int count;                  // adapters among the tile's rows
     int pad[3];
     int ids[LT_ROWS];           // ascending
@@ -70,6 +70,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
 
 // How the rank values are laid out.
