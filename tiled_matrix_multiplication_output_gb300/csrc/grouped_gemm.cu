@@ -26,15 +26,18 @@ cudaError_t grouped_tc_launch(const GroupedLaunch& l, cudaStream_t stream)
     const int64_t groups = p.one_weight ? 1 : l.by.groups;
     const int64_t stride = p.one_weight ? l.ldw : l.stride_w;
     const uint32_t deep = l.w_t ? TC_BM : TC_BK;
-    CUtensorMap m[4];
-    const bool ok =
-        (p.swap ? encode_map(&m[0], l.in_dtype, l.W, 3, {inner, groups, outer}, {stride, l.ldw}, {64, 1, deep})
-                : encode_map(&m[0], l.in_dtype, l.W, 3, {inner, outer, groups}, {l.ldw, stride}, {64, deep, 1})) &&
-        encode_map(&m[1], l.in_dtype, l.X, 2, {l.K, l.by.rows, 1}, {l.ldx, 0}, {64, TC_BM, 1}) &&
-        encode_map(&m[2], l.in_dtype, l.X, 2, {l.K, l.by.rows, 1}, {l.ldx, 0}, {64, 16, 1});
+    GroupedMaps m;
+    bool ok =
+        (p.swap ? encode_map(&m.a, l.in_dtype, l.W, 3, {inner, groups, outer}, {stride, l.ldw}, {64, 1, deep})
+                : encode_map(&m.a, l.in_dtype, l.W, 3, {inner, outer, groups}, {l.ldw, stride}, {64, deep, 1})) &&
+        encode_map(&m.b, l.in_dtype, l.X, 2, {l.K, l.by.rows, 1}, {l.ldx, 0}, {64, TC_BM, 1});
+    auto rows = [&](CUtensorMap* map, uint32_t n) {
+        return encode_map(map, l.in_dtype, l.X, 2, {l.K, l.by.rows, 1}, {l.ldx, 0}, {64, n, 1});
+    };
+    ok = ok && rows(&m.b64, 64) && rows(&m.b32, 32) && rows(&m.b16, 16);
     if (!ok)
         return cudaErrorNotSupported;
-    m[3] = m[2];
+    m.c = m.b;
     const int64_t most = (l.by.rows / GT_N + static_cast<int64_t>(std::min(l.by.groups, l.by.rows))) * p.tiles_f;
     return l.w_t ? launch_grouped_tc<GROUPED_T>(l.out_dtype, m, p, most, l.num_sms, stream)
                  : launch_grouped_tc<GROUPED_N>(l.out_dtype, m, p, most, l.num_sms, stream);

@@ -12,8 +12,13 @@
 
 namespace tmmo {
 
+// Lanes' side; the other side in boxes of 128 rows and fewer; stored gradients.
+struct GroupedMaps {
+    CUtensorMap a, b, b64, b32, b16, c;
+};
+
 template <int MODE, typename OutT>
-cudaError_t launch_grouped_tc(const CUtensorMap (&maps)[4], const GroupedTcParams& p, int64_t most_work,
+cudaError_t launch_grouped_tc(const GroupedMaps& m, const GroupedTcParams& p, int64_t most_work,
                               int num_sms, cudaStream_t stream)
 {
     using L = GroupedLayout<MODE>;
@@ -25,20 +30,20 @@ cudaError_t launch_grouped_tc(const CUtensorMap (&maps)[4], const GroupedTcParam
         return err;
     const int64_t units = std::min<int64_t>(std::max(cap, 1), std::max<int64_t>(most_work, 1));
     ClusterLaunch l(static_cast<unsigned>(2 * units), 2, L::THREADS, L::SMEM_ALLOC, stream);
-    return l.run(grouped_tc_kernel<MODE, OutT>, maps[0], maps[1], maps[2], maps[3], p);
+    return l.run(grouped_tc_kernel<MODE, OutT>, m.a, m.b, m.b64, m.b32, m.b16, m.c, p);
 }
 
 template <int MODE>
-cudaError_t launch_grouped_tc(int out_dtype, const CUtensorMap (&maps)[4], const GroupedTcParams& p,
+cudaError_t launch_grouped_tc(int out_dtype, const GroupedMaps& m, const GroupedTcParams& p,
                               int64_t most_work, int num_sms, cudaStream_t stream)
 {
     switch (out_dtype) {
     case DT_F32:
-        return launch_grouped_tc<MODE, float>(maps, p, most_work, num_sms, stream);
+        return launch_grouped_tc<MODE, float>(m, p, most_work, num_sms, stream);
     case DT_F16:
-        return launch_grouped_tc<MODE, __half>(maps, p, most_work, num_sms, stream);
+        return launch_grouped_tc<MODE, __half>(m, p, most_work, num_sms, stream);
     default:
-        return launch_grouped_tc<MODE, __nv_bfloat16>(maps, p, most_work, num_sms, stream);
+        return launch_grouped_tc<MODE, __nv_bfloat16>(m, p, most_work, num_sms, stream);
     }
 }
 

@@ -31,6 +31,7 @@
 #include "grouped.cuh"
 #include "ops.cuh"
 #include "simt_tile.cuh"
+#include "warp_roles.cuh"
 
 namespace tmmo {
 
@@ -175,8 +176,9 @@ __device__ __forceinline__ void grouped_strip(const uint32_t (&v)[32], uint32_t 
 template <int MODE, typename OutT>
 __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmB64, const __grid_constant__ CUtensorMap tmB32,
                       const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmC,
-                      const GroupedTcParams p)
+                      const __grid_constant__ GroupedTcParams p)
 {
     using L = GroupedLayout<MODE>;
     constexpr bool WGRAD = L::WGRAD;
@@ -224,7 +226,6 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
-        tma_prefetch_desc(&tmB16);
         tma_prefetch_desc(&tmC);
     }
     if (warp == 1) {
@@ -244,40 +245,37 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        if (lane == 0) {
-            const uint32_t sA = sbase + L::OFF_A;
-            const uint32_t sB = sbase + L::OFF_B;
-            int stage = 0;
-            uint32_t phase = 0;
-            int issued[GT_STAGES], ragged[L::STEPS];
+        const uint32_t sA = sbase + L::OFF_A;
+        const uint32_t sB = sbase + L::OFF_B;
+        int stage = 0;
+        uint32_t phase = 0;
+        int issued[GT_STAGES], ragged[L::STEPS];
 #pragma unroll
-            for (int s = 0; s < GT_STAGES; ++s)
-                issued[s] = 0;
+        for (int s = 0; s < GT_STAGES; ++s)
+            issued[s] = 0;
 #pragma unroll
-            for (int s = 0; s < L::STEPS; ++s)
-                ragged[s] = 0;
-            bool ok = true;
-            for (int t = unit; ok && t < num_work; t += num_units) {
-                const GroupedWork w = grouped_work<MODE>(t, table, p);
-                const int f = w.f0 + static_cast<int>(rank) * TC_BM;
-                const int half = w.n / 2;
-                const int c = w.c0 + static_cast<int>(rank) * half;
-                const int z = p.one_weight ? 0 : w.g;
-                const uint32_t bytes = L::SUB + half * TC_BK * 2;
-                for (int kb0 = 0; kb0 < w.k_blocks; kb0 += GT_KSUB) {
-                    const int nsub = min(GT_KSUB, w.k_blocks - kb0);
-                    if (!tc_wait(empty_bar(stage), phase ^ 1, watch)) {
-                        ok = false;
-                        break;
-                    }
-                    // test hook (-1 in normal use): skip the stage holding that K step
-                    if (p.fault_skip_kblock < kb0 || p.fault_skip_kblock >= kb0 + nsub) {
+        for (int s = 0; s < L::STEPS; ++s)
+            ragged[s] = 0;
+        bool ok = true;
+        for (int t = unit; ok && t < num_work; t += num_units) {
+            const GroupedWork w = grouped_work<MODE>(t, table, p);
+            const int f = w.f0 + static_cast<int>(rank) * TC_BM;
+            const int half = w.n / 2;
+            const int c = w.c0 + static_cast<int>(rank) * half;
+            const int z = p.one_weight ? 0 : w.g;
+            const uint32_t bytes = L::SUB + half * TC_BK * 2;
+            for (int kb0 = 0; kb0 < w.k_blocks; kb0 += GT_KSUB) {
+                const int nsub = min(GT_KSUB, w.k_blocks - kb0);
+                ok = warp_wait(empty_bar(stage), phase ^ 1, watch);
+                if (!ok)
+                    break;
+                // test hook (-1 in normal use): skip the stage holding that K step
+                if (p.fault_skip_kblock < kb0 || p.fault_skip_kblock >= kb0 + nsub) {
+                    if (elect_one()) {
 #pragma unroll
                         for (int j = 0; j < GT_KSUB; ++j) {
                             if (j < nsub && is_ragged(w, kb0 + j)) {
                                 mbar_arrive_expect_tx(tail_bar(stage, j), bytes);
-                                for (int s = 0; s < L::STEPS; ++s)  // (registers: no indexing)
-                                    ragged[s] += s == stage * GT_KSUB + j;
                             } else if (leader) {
                                 if (WGRAD)
                                     mbar_arrive(full_bar(stage, j));
@@ -298,10 +296,12 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                             const uint32_t dB = sB + (stage * GT_KSUB + j) * L::SUB;
                             if constexpr (WGRAD) {
                                 const int row = w.row0 + kb * TC_BK;
+#pragma unroll
                                 for (int b = 0; b < 2; ++b)
                                     tma_load_2d_pair(dA + b * 8192, &tmA, bar, f + 64 * b, row);
-                                for (int b = 0; b < half / 64; ++b)
-                                    tma_load_2d_pair(dB + b * 8192, &tmB, bar, c + 64 * b, row);
+                                tma_load_2d_pair(dB, &tmB, bar, c, row);
+                                if (half > 64)
+                                    tma_load_2d_pair(dB + 8192, &tmB, bar, c + 64, row);
                             } else {
                                 const int k = kb * TC_BK;
                                 auto weights = [&](uint32_t dst, int x, int y) {
@@ -313,43 +313,60 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                                 } else {
                                     weights(dA, k, f);
                                 }
-                                if (half == TC_BM) {
+                                // the tile's rows in boxes of 128, 64, 32 and 16
+                                if (half == 128) {
                                     tma_load_2d_pair(dB, &tmB, bar, k, c);
                                 } else {
-                                    for (int b = 0; b < half; b += 16)
+                                    int b = 0;
+                                    if (half & 64) {
+                                        tma_load_2d_pair(dB, &tmB64, bar, k, c);
+                                        b = 64;
+                                    }
+                                    if (half & 32) {
+                                        tma_load_2d_pair(dB + b * 128, &tmB32, bar, k, c + b);
+                                        b += 32;
+                                    }
+                                    if (half & 16)
                                         tma_load_2d_pair(dB + b * 128, &tmB16, bar, k, c + b);
                                 }
                             }
                         }
-                        ++issued[stage];
                     }
-                    if (++stage == GT_STAGES) {
-                        stage = 0;
-                        phase ^= 1;
+                    __syncwarp();
+#pragma unroll
+                    for (int s = 0; s < GT_STAGES; ++s) {  // (registers: no indexing)
+                        issued[s] += s == stage;
+#pragma unroll
+                        for (int j = 0; j < GT_KSUB; ++j)
+                            ragged[s * GT_KSUB + j] += s == stage && j < nsub && is_ragged(w, kb0 + j);
                     }
                 }
+                if (++stage == GT_STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
-            if (!ok) {
-                // Wait (bounded) for the loads already issued before shared
-                // memory goes away: the leader's barriers cover both CTAs.
-                auto drain = [&](uint32_t bar, int uses) {
-                    const long long t0 = clock64();
-                    while (!mbar_try_wait(bar, static_cast<uint32_t>(uses - 1) & 1u) &&
-                           clock64() - t0 < p.wait_budget) {
-                    }
-                };
-                for (int s = 0; s < GT_STAGES; ++s)
-                    for (int j = 0; j < GT_KSUB; ++j) {
-                        if (leader && issued[s] > 0)
-                            drain(full_bar(s, j), issued[s]);
-                        if (WGRAD && ragged[s * GT_KSUB + j] > 0)
-                            drain(tail_bar(s, j), ragged[s * GT_KSUB + j]);
-                    }
-            }
+        }
+        if (!ok && lane == 0) {
+            // Wait (bounded) for the loads already issued before shared
+            // memory goes away: the leader's barriers cover both CTAs.
+            auto drain = [&](uint32_t bar, int uses) {
+                const long long t0 = clock64();
+                while (!mbar_try_wait(bar, static_cast<uint32_t>(uses - 1) & 1u) &&
+                       clock64() - t0 < p.wait_budget) {
+                }
+            };
+            for (int s = 0; s < GT_STAGES; ++s)
+                for (int j = 0; j < GT_KSUB; ++j) {
+                    if (leader && issued[s] > 0)
+                        drain(full_bar(s, j), issued[s]);
+                    if (WGRAD && ragged[s * GT_KSUB + j] > 0)
+                        drain(tail_bar(s, j), ragged[s * GT_KSUB + j]);
+                }
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (leader && lane == 0) {
+        if (leader) {
             const uint32_t sA = sbase + L::OFF_A;
             const uint32_t sB = sbase + L::OFF_B;
             int stage = 0;
@@ -363,10 +380,9 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                 const int acc = local & 1;
                 const uint32_t acc_phase = (local >> 1) & 1;
                 ++local;
-                if (!tc_wait<true>(tempty_bar(acc), acc_phase ^ 1, watch)) {
-                    ok = false;
+                ok = warp_wait<true>(tempty_bar(acc), acc_phase ^ 1, watch);
+                if (!ok)
                     break;
-                }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * GT_N);
                 const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
@@ -376,43 +392,46 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                     for (int j = 0; j < GT_KSUB; ++j) {
                         if (j >= nsub)
                             break;
-                        const bool landed = WGRAD ? tc_wait<true>(full_bar(stage, j), phase, watch)
-                                                  : tc_wait(full_bar(stage, j), phase, watch);
-                        if (!landed) {
-                            ok = false;
+                        ok = warp_wait<WGRAD>(full_bar(stage, j), phase, watch);
+                        if (!ok)
                             break;
-                        }
                         tc_fence_after();
                         const uint32_t a0 = sA + (stage * GT_KSUB + j) * L::SUB;
                         const uint32_t b0 = sB + (stage * GT_KSUB + j) * L::SUB;
                         // 16-deep instructions; gradient: as many as there are rows
                         const int deep = WGRAD ? min(4, (w.rows - (kb0 + j) * TC_BK + 15) / 16) : 4;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < TC_BK / TC_UMMA_K; ++k) {
-                            if (WGRAD && k >= deep)
-                                break;
-                            const uint64_t adesc = A_MN ? smem_desc_sw128(a0 + k * 2048, 8192, 1024)
-                                                        : smem_desc_sw128(a0 + k * 32, 16, 1024);
-                            const uint64_t bdesc = WGRAD ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                                         : smem_desc_sw128(b0 + k * 32, 16, 1024);
-                            tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, kb0 != 0 || j != 0 || k != 0);
+                            for (int k = 0; k < TC_BK / TC_UMMA_K; ++k) {
+                                if (WGRAD && k >= deep)
+                                    break;
+                                const uint64_t adesc = A_MN ? smem_desc_sw128(a0 + k * 2048, 8192, 1024)
+                                                            : smem_desc_sw128(a0 + k * 32, 16, 1024);
+                                const uint64_t bdesc = WGRAD ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                             : smem_desc_sw128(b0 + k * 32, 16, 1024);
+                                tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, kb0 != 0 || j != 0 || k != 0);
+                            }
+                            if (j == nsub - 1) {
+                                tc_commit_pair(empty_bar(stage), 0x3);
+                                if (kb0 + GT_KSUB >= w.k_blocks)
+                                    tc_commit_pair(tfull_bar(acc), 0x3);
+                            }
                         }
+                        __syncwarp();
                     }
                     if (!ok)
                         break;
-                    tc_commit_pair(empty_bar(stage), 0x3);
                     if (++stage == GT_STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
-                if (!ok)
-                    break;
-                tc_commit_pair(tfull_bar(acc), 0x3);
             }
             // Wait (bounded) until every MMA issued so far has completed, so
             // TMEM and the input stages are no longer in use.
-            tc_commit_self<2>(drain_bar);
+            if (elect_one())
+                tc_commit_self<2>(drain_bar);
+            __syncwarp();
             const long long t0 = clock64();
             while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
             }

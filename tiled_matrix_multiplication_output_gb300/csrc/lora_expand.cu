@@ -24,6 +24,7 @@ constexpr int LE_KSUB = 2;
 struct ExpandParams {
     int M, N, k_blocks, rank;
     int tiles_m, tiles_n;
+    int whole, items;     // tiles of 256 columns first, the others in halves
     bool adapters;        // there are any: plans and rank values are made
     bool one;             // one factor for every adapter
     LoraParts lay;
@@ -31,7 +32,7 @@ struct ExpandParams {
     void* C;
     int64_t ldc;
     bool tma_out;
-    uint32_t idesc, idesc_e;
+    uint32_t idesc;       // with N = 0
     int* status;
     long long wait_budget;
     int fault_skip_kblock;
@@ -100,11 +101,29 @@ private:
     uint4 rows_[2];
 };
 
+// An output tile, or half of one.
+struct Item {
+    int mb, col, n;
+};
+__device__ __forceinline__ Item item(int t, const ExpandParams& p)
+{
+    const int half = t < p.whole ? 0 : (t - p.whole) & 1;
+    const int n = t < p.whole ? 256 : 128;
+    if (t >= p.whole)
+        t = p.whole + (t - p.whole) / 2;
+    // row tiles eight at a time, and within those down the rows first
+    const int band = t / (8 * p.tiles_n) * 8;
+    const int high = min(p.tiles_m - band, 8);
+    const int u = t - band * p.tiles_n;
+    return {band + u % high, u / high * 256 + half * 128, n};
+}
+
 template <bool ACROSS, typename OutT>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     lora_expand_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmE,
-                       const __grid_constant__ CUtensorMap tmC, const ExpandParams p)
+                       const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmW64,
+                       const __grid_constant__ CUtensorMap tmE64, const __grid_constant__ ExpandParams p)
 {
     using L = ExpandLayout;
     extern __shared__ uint8_t smem_raw[];
@@ -125,7 +144,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int unit = blockIdx.x >> 1, num_units = gridDim.x >> 1;
-    const int num_tiles = p.tiles_m * p.tiles_n;
     const TcWatch watch{abort_flag, p.status, p.wait_budget};
 
     if (threadIdx.x == 0) {
@@ -155,123 +173,133 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    // row tiles eight at a time, and within those down the rows first
-    auto coords = [&](int t, int& mb, int& nb) {
-        const int band = t / (8 * p.tiles_n) * 8;
-        const int high = min(p.tiles_m - band, 8);
-        const int u = t - band * p.tiles_n;
-        mb = band + u % high;
-        nb = u / high;
-    };
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        if (lane == 0) {
-            const uint32_t sA = sbase + L::OFF_A, sB = sbase + L::OFF_B;
-            int stage = 0, sub = 0;
-            uint32_t phase = 0;
-            int issued[L::STEPS];
+        const uint32_t sA = sbase + L::OFF_A, sB = sbase + L::OFF_B;
+        int stage = 0, sub = 0;
+        uint32_t phase = 0;
+        int issued[L::STEPS];
 #pragma unroll
-            for (int s = 0; s < L::STEPS; ++s)
-                issued[s] = 0;
-            bool ok = true, waited = false;
-            auto next_stage = [&] {
-                sub = 0;
-                if (++stage == LE_STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            };
-            // One K step: load(A's place, B's place, barrier).
-            auto step = [&](bool skip, auto load) {
-                if (sub == 0 && !tc_wait(empty_bar(stage), phase ^ 1, watch))
-                    return false;
-                if (!skip) {
-                    const int at = stage * LE_KSUB + sub;
+        for (int s = 0; s < L::STEPS; ++s)
+            issued[s] = 0;
+        bool ok = true, waited = false;
+        auto next_stage = [&] {
+            sub = 0;
+            if (++stage == LE_STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+        };
+        auto count = [&](int at) {
+#pragma unroll
+            for (int s = 0; s < L::STEPS; ++s)  // (registers: no indexing)
+                issued[s] += s == at;
+        };
+        // One K step: load(A's place, B's place, barrier).
+        auto step = [&](bool skip, uint32_t bytes, auto load) {
+            if (sub == 0 && !warp_wait(empty_bar(stage), phase ^ 1, watch))
+                return false;
+            if (!skip) {
+                const int at = stage * LE_KSUB + sub;
+                if (elect_one()) {
                     if (leader)
-                        mbar_arrive_expect_tx(full_bar(stage, sub), 4 * L::SUB);
-                    for (int s = 0; s < L::STEPS; ++s)  // (registers: no indexing)
-                        issued[s] += s == at;
+                        mbar_arrive_expect_tx(full_bar(stage, sub), bytes);
                     load(sA + at * L::SUB, sB + at * L::SUB, mapa_shared(full_bar(stage, sub), 0));
                 }
-                if (++sub == LE_KSUB)
-                    next_stage();
-                return true;
+                __syncwarp();
+                count(at);
+            }
+            if (++sub == LE_KSUB)
+                next_stage();
+            return true;
+        };
+        for (int t = unit; ok && t < p.items; t += num_units) {
+            const Item w = item(t, p);
+            const int row = w.mb * 256 + static_cast<int>(rank) * TC_BM;
+            const int col = w.col + static_cast<int>(rank) * w.n / 2;
+            const uint32_t bytes = 2 * (L::SUB + w.n * 64);
+            PairAdapters list;
+            if (waited)
+                list.begin(p, w.mb);
+            // W's or a factor's outputs: boxes of 64 (x) or 128 and 64 (y)
+            auto outputs = [&](auto box, auto box64, uint32_t dB) {
+                if (ACROSS) {
+                    box(dB, col);
+                    if (w.n > 128)
+                        box(dB + 8192, col + 64);
+                } else if (w.n > 128) {
+                    box(dB, col);
+                } else {
+                    box64(dB, col);
+                }
             };
-            for (int t = unit; ok && t < num_tiles; t += num_units) {
-                int mb, nb;
-                coords(t, mb, nb);
-                const int row = mb * 256 + static_cast<int>(rank) * TC_BM;
-                const int col = nb * 256 + static_cast<int>(rank) * TC_BM;
-                PairAdapters list;
-                if (waited)
-                    list.begin(p, mb);
-                for (int kb = 0; ok && kb < p.k_blocks; ++kb) {
-                    const int k = kb * TC_BK;
-                    ok = step(kb == p.fault_skip_kblock, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
-                        tma_load_2d_pair(dA, &tmX, bar, k, row);
-                        if (ACROSS) {
-                            tma_load_2d_pair(dB, &tmW, bar, col, k);
-                            tma_load_2d_pair(dB + 8192, &tmW, bar, col + 64, k);
-                        } else {
-                            tma_load_2d_pair(dB, &tmW, bar, k, col);
-                        }
-                    });
+            for (int kb = 0; ok && kb < p.k_blocks; ++kb) {
+                const int k = kb * TC_BK;
+                ok = step(kb == p.fault_skip_kblock, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                    tma_load_2d_pair(dA, &tmX, bar, k, row);
+                    auto load = [&](const CUtensorMap* map) {
+                        return [=](uint32_t to, int c) {
+                            tma_load_2d_pair(to, map, bar, ACROSS ? c : k, ACROSS ? k : c);
+                        };
+                    };
+                    outputs(load(&tmW), load(&tmW64), dB);
+                });
+            }
+            if (!ok)
+                break;
+            if (p.adapters) {
+                if (!waited) {
+                    grid_dep_wait();
+                    list.begin(p, w.mb);
                 }
-                if (!ok)
-                    break;
-                if (p.adapters) {
-                    if (!waited) {
-                        grid_dep_wait();
-                        list.begin(p, mb);
+                waited = true;
+                uint32_t off[8];
+                for (int g = list.next(off); ok && g >= 0; g = list.next(off)) {
+                    const int z = p.one ? 0 : g;
+                    for (int c = 0; ok && c < p.lay.chunks; ++c) {
+                        const int j = c * p.lay.chunk;
+                        ok = step(false, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                            tma_load_2d_pair(dA, &tmT, bar, c * 64, row);
+                            auto load = [&](const CUtensorMap* map) {
+                                return [=](uint32_t to, int o) {
+                                    tma_load_3d_pair(to, map, bar, ACROSS ? o : j, ACROSS ? j : o, z);
+                                };
+                            };
+                            outputs(load(&tmE), load(&tmE64), dB);
+                        });
                     }
-                    waited = true;
-                    uint32_t off[8];
-                    for (int g = list.next(off); ok && g >= 0; g = list.next(off)) {
-                        const int z = p.one ? 0 : g;
-                        for (int c = 0; ok && c < p.lay.chunks; ++c) {
-                            const int j = c * p.lay.chunk;
-                            ok = step(false, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
-                                tma_load_2d_pair(dA, &tmT, bar, c * 64, row);
-                                if (ACROSS) {
-                                    tma_load_3d_pair(dB, &tmE, bar, col, j, z);
-                                    tma_load_3d_pair(dB + 8192, &tmE, bar, col + 64, j, z);
-                                } else {
-                                    tma_load_3d_pair(dB, &tmE, bar, j, col, z);
-                                }
-                            });
-                        }
-                    }
-                }
-                if (ok && sub != 0) {
-                    if (leader)
-                        mbar_arrive(full_bar(stage, 1));  // the stage's unused step
-                    issued[1] += stage == 0;
-                    issued[3] += stage == 1;
-                    issued[5] += stage == 2;
-                    next_stage();
                 }
             }
-            if (!ok && leader) {
-                // wait (bounded) for the loads already issued, of both CTAs,
-                // before shared memory goes away
-                for (int s = 0; s < L::STEPS; ++s) {
-                    const long long t0 = clock64();
-                    while (issued[s] > 0 && !mbar_try_wait(bar0 + 8u * s, (issued[s] - 1) & 1) &&
-                           clock64() - t0 < p.wait_budget) {
-                    }
+            if (ok && sub != 0) {
+                if (leader && elect_one())
+                    mbar_arrive(full_bar(stage, 1));  // the stage's unused step
+                __syncwarp();
+                count(stage * LE_KSUB + 1);
+                next_stage();
+            }
+        }
+        if (!ok && leader && lane == 0) {
+            // wait (bounded) for the loads already issued, of both CTAs,
+            // before shared memory goes away
+            for (int s = 0; s < L::STEPS; ++s) {
+                const long long t0 = clock64();
+                while (issued[s] > 0 && !mbar_try_wait(bar0 + 8u * s, (issued[s] - 1) & 1) &&
+                       clock64() - t0 < p.wait_budget) {
                 }
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (leader && lane == 0) {
+        if (leader) {
             const uint32_t sA = sbase + L::OFF_A, sB = sbase + L::OFF_B;
             int stage = 0, sub = 0, local = 0;
             uint32_t phase = 0;
             bool ok = true, waited = false;
             auto next_stage = [&] {
-                tc_commit_pair(empty_bar(stage), 0x3);
+                if (elect_one())
+                    tc_commit_pair(empty_bar(stage), 0x3);
+                __syncwarp();
                 sub = 0;
                 if (++stage == LE_STAGES) {
                     stage = 0;
@@ -279,28 +307,29 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 }
             };
             auto step = [&](auto multiply) {
-                if (!tc_wait(full_bar(stage, sub), phase, watch))
+                if (!warp_wait(full_bar(stage, sub), phase, watch))
                     return false;
                 tc_fence_after();
                 const int at = stage * LE_KSUB + sub;
-                multiply(sA + at * L::SUB, sB + at * L::SUB);
+                if (elect_one())
+                    multiply(sA + at * L::SUB, sB + at * L::SUB);
+                __syncwarp();
                 if (++sub == LE_KSUB)
                     next_stage();
                 return true;
             };
-            for (int t = unit; ok && t < num_tiles; t += num_units, ++local) {
-                int mb, nb;
-                coords(t, mb, nb);
+            for (int t = unit; ok && t < p.items; t += num_units, ++local) {
+                const Item w = item(t, p);
                 const int acc = local & 1;
-                if (!tc_wait<true>(tempty_bar(acc), ((local >> 1) & 1) ^ 1, watch)) {
-                    ok = false;
+                ok = warp_wait<true>(tempty_bar(acc), ((local >> 1) & 1) ^ 1, watch);
+                if (!ok)
                     break;
-                }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+                const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
                 PairAdapters list;
                 if (waited)
-                    list.begin(p, mb);
+                    list.begin(p, w.mb);
                 for (int kb = 0; ok && kb < p.k_blocks; ++kb)
                     ok = step([&](uint32_t a0, uint32_t b0) {
 #pragma unroll
@@ -308,14 +337,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                             tc_mma_f16<2>(d_tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
                                           ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
                                                  : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                          p.idesc, kb != 0 || k != 0);
+                                          idesc, kb != 0 || k != 0);
                     });
                 if (!ok)
                     break;
                 if (p.adapters) {
                     if (!waited) {
                         grid_dep_wait();
-                        list.begin(p, mb);
+                        list.begin(p, w.mb);
                     }
                     waited = true;
                     uint32_t off[8];
@@ -330,18 +359,22 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                             smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
                                             ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
                                                    : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                            p.idesc, 1, off);
+                                            idesc, 1, off);
                             });
                 }
                 if (!ok)
                     break;
                 if (sub != 0)
                     next_stage();
-                tc_commit_pair(tfull_bar(acc), 0x3);
+                if (elect_one())
+                    tc_commit_pair(tfull_bar(acc), 0x3);
+                __syncwarp();
             }
             // Wait (bounded) until every MMA issued so far has completed, so
             // TMEM and the input stages are no longer in use.
-            tc_commit_self<2>(drain_bar);
+            if (elect_one())
+                tc_commit_self<2>(drain_bar);
+            __syncwarp();
             const long long t0 = clock64();
             while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
             }
@@ -359,9 +392,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         store.alpha = 1.0f;
         int local = 0;
         uint32_t buf = 0;
-        for (int t = unit; t < num_tiles; t += num_units, ++local) {
-            int mb, nb;
-            coords(t, mb, nb);
+        for (int t = unit; t < p.items; t += num_units, ++local) {
+            const Item w = item(t, p);
             const int acc = local & 1;
             int ok = 1;
             if (lane == 0)
@@ -370,10 +402,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             if (!ok)
                 break;
             tc_fence_after();
-            const int row = mb * 256 + static_cast<int>(rank) * TC_BM + q * 32;
+            const int row = w.mb * 256 + static_cast<int>(rank) * TC_BM + q * 32;
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * 256);
-            const int cols = min(256, p.N - nb * 256);
+            const int cols = min(w.n, p.N - w.col);
             if (row < p.M && p.tma_out) {
                 constexpr int STRIP = TcOut<OutT>::STRIP;
 #pragma unroll 1
@@ -386,7 +418,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_2d(&tmC, stg, nb * 256 + s, row);
+                        tma_store_2d(&tmC, stg, w.col + s, row);
                         bulk_commit_group();
                     }
                     buf ^= 1;
@@ -397,7 +429,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(t_row + s, v);
                     tmem_wait_ld(v);
-                    grouped_strip(v, staging0, lane, out + row * p.ldc + nb * 256 + s, p.ldc,
+                    grouped_strip(v, staging0, lane, out + row * p.ldc + w.col + s, p.ldc,
                                   min(32, p.M - row), cols - s, store);
                 }
             }
@@ -425,7 +457,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 }
 
 template <bool ACROSS, typename OutT>
-cudaError_t launch(const CUtensorMap (&m)[5], const ExpandParams& p, int num_sms, cudaStream_t stream)
+cudaError_t launch(const CUtensorMap (&m)[7], ExpandParams& p, int num_sms, cudaStream_t stream)
 {
     using L = ExpandLayout;
     static ClusterCaps caps;
@@ -434,13 +466,18 @@ cudaError_t launch(const CUtensorMap (&m)[5], const ExpandParams& p, int num_sms
         cluster_cap(lora_expand_kernel<ACROSS, OutT>, caps, 2, TC_THREADS, L::SMEM_ALLOC, num_sms, &cap);
     if (err != cudaSuccess)
         return err;
-    const int64_t units = std::min<int64_t>(std::max(cap, 1), static_cast<int64_t>(p.tiles_m) * p.tiles_n);
+    // The tiles of a last wave that leaves at least half of the pairs idle are
+    // cut in halves: 3.4 waves of tiles take 3.5 instead of 4.
+    const int tiles = p.tiles_m * p.tiles_n, pairs = std::max(cap, 1), rest = tiles % pairs;
+    p.whole = rest > 0 && 2 * rest <= pairs ? tiles - rest : tiles;
+    p.items = p.whole + 2 * (tiles - p.whole);
+    const int units = std::min(pairs, p.items);
     ClusterLaunch l(static_cast<unsigned>(2 * units), 2, TC_THREADS, L::SMEM_ALLOC, stream, p.adapters);
-    return l.run(lora_expand_kernel<ACROSS, OutT>, m[0], m[1], m[2], m[3], m[4], p);
+    return l.run(lora_expand_kernel<ACROSS, OutT>, m[0], m[1], m[2], m[3], m[4], m[5], m[6], p);
 }
 
 template <bool ACROSS>
-cudaError_t launch(int out_dtype, const CUtensorMap (&m)[5], const ExpandParams& p, int num_sms,
+cudaError_t launch(int out_dtype, const CUtensorMap (&m)[7], ExpandParams& p, int num_sms,
                    cudaStream_t stream)
 {
     switch (out_dtype) {
@@ -474,22 +511,27 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     p.plan = static_cast<const LoraPlan*>(l.plan);
     p.C = l.Y;
     p.ldc = l.ldy;
-    p.idesc = tc_idesc(l.in_dtype == DT_BF16, 256, 256, false, l.across);
+    p.idesc = tc_idesc(l.in_dtype == DT_BF16, 256, 0, false, l.across);
     p.status = l.status;
     p.wait_budget = l.wait_budget;
     p.fault_skip_kblock = l.fault_skip_kblock;
-    CUtensorMap m[5];
+    CUtensorMap m[7];
     const int dt = l.in_dtype;
+    auto weights = [&](CUtensorMap* map, uint32_t outputs) {
+        return l.across ? encode_map(map, dt, l.W, 2, {l.N, l.K, 1}, {l.ldw, 0}, {64, TC_BK, 1})
+                        : encode_map(map, dt, l.W, 2, {l.K, l.N, 1}, {l.ldw, 0}, {64, outputs, 1});
+    };
+    const int64_t stacked = p.one ? 1 : l.adapters, stride = p.one ? l.lde : l.stride_e;
+    auto factors = [&](CUtensorMap* map, uint32_t outputs) {
+        return l.across ? encode_map(map, dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
+                        : encode_map(map, dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride}, {64, outputs, 1});
+    };
     bool ok = encode_map(&m[0], dt, l.X, 2, {l.K, l.rows, 1}, {l.ldx, 0}, {64, TC_BM, 1}) &&
-              (l.across ? encode_map(&m[1], dt, l.W, 2, {l.N, l.K, 1}, {l.ldw, 0}, {64, TC_BK, 1})
-                        : encode_map(&m[1], dt, l.W, 2, {l.K, l.N, 1}, {l.ldw, 0}, {64, TC_BM, 1}));
-    m[2] = m[3] = m[4] = m[0];
-    if (ok && p.adapters) {
-        const int64_t stacked = p.one ? 1 : l.adapters, stride = p.one ? l.lde : l.stride_e;
+              weights(&m[1], TC_BM) && weights(&m[5], 64);
+    m[2] = m[3] = m[4] = m[6] = m[0];
+    if (ok && p.adapters)
         ok = encode_map(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, TC_BM, 1}) &&
-             (l.across ? encode_map(&m[3], dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
-                       : encode_map(&m[3], dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride}, {64, TC_BM, 1}));
-    }
+             factors(&m[3], TC_BM) && factors(&m[6], 64);
     if (!ok)
         return cudaErrorNotSupported;
     p.tma_out = aligned_rows(l.Y, l.ldy, l.out_dtype) &&

@@ -242,15 +242,6 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = s.tmem;
 
-    // Roles of whole warps: one lane waits and issues, and the others learn
-    // whether it gave up.
-    auto together = [&](auto f) {
-        int ok = 1;
-        if (lane == 0)
-            ok = f() ? 1 : 0;
-        return __shfl_sync(0xffffffffu, ok, 0) != 0;
-    };
-
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         int stage = 0;
@@ -264,9 +255,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             uint64_t rows;
             while (ok && blocks.next(block, rows)) {
                 const bool whole = rows == ~0ull;
-                ok = together([&] {
-                    if (!tc_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch))
-                        return false;
+                ok = warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch);
+                if (ok && elect_one()) {
                     const uint32_t bar = smem_u32(whole ? &s.full[stage] : &s.landed[stage]);
                     const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 16384;
                     const CUtensorMap* tmP = w.which ? &tmP1 : &tmP0;
@@ -276,8 +266,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                     tma_load_2d(a0 + 8192, tmP, bar, w.c0 + 64, block * 64);
                     for (int c = 0; c < w.chunks; ++c)
                         tma_load_2d(b0 + c * 8192, tmT, bar, (w.chunk0 + c) * 64, block * 64);
-                    return true;
-                });
+                }
+                __syncwarp();
                 if (ok) {
                     ++n_full[stage];  // whichever barrier: full completes once a use
                     n_landed[stage] += !whole;
@@ -315,14 +305,16 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
             bool any = false;
             while (ok && blocks.next(block, rows)) {
-                ok = together([&] {
-                    if (!any && !tc_wait(smem_u32(&s.tempty[acc]), ((local >> 1) & 1) ^ 1, watch))
-                        return false;
-                    if (!tc_wait(smem_u32(&s.full[stage]), phase, watch))
-                        return false;
-                    tc_fence_after();
-                    const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 16384;
+                if (!any)
+                    ok = warp_wait(smem_u32(&s.tempty[acc]), ((local >> 1) & 1) ^ 1, watch);
+                ok = ok && warp_wait(smem_u32(&s.full[stage]), phase, watch);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 16384;
+                if (elect_one()) {
                     bool first = !any;
+#pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (((rows >> (16 * k)) & 0xffff) == 0)
                             continue;
@@ -331,8 +323,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                         first = false;
                     }
                     tc_commit(smem_u32(&s.empty[stage]));
-                    return true;
-                });
+                }
+                __syncwarp();
                 any = true;
                 if (++stage == p.stages) {
                     stage = 0;
@@ -340,14 +332,17 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                 }
             }
             if (ok && any) {
-                if (lane == 0)
+                if (elect_one())
                     tc_commit(smem_u32(&s.tfull[acc]));
+                __syncwarp();
                 ++local;
             }
         }
-        if (lane == 0) {
+        {
             // Wait (bounded) until every MMA issued so far has completed.
-            tc_commit(smem_u32(&s.drain));
+            if (elect_one())
+                tc_commit(smem_u32(&s.drain));
+            __syncwarp();
             const long long t0 = clock64();
             while (!mbar_try_wait(smem_u32(&s.drain), 0) && clock64() - t0 < p.wait_budget) {
             }
@@ -364,9 +359,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             uint64_t rows;
             while (ok && blocks.next(block, rows)) {
                 if (rows != ~0ull) {
-                    ok = together([&] {
-                        return tc_wait(smem_u32(&s.landed[stage]), (parity >> stage) & 1, watch);
-                    });
+                    ok = warp_wait(smem_u32(&s.landed[stage]), (parity >> stage) & 1, watch);
                     if (!ok)
                         break;
                     parity ^= 1u << stage;
@@ -401,7 +394,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             const bool any = blocks.next(block, rows);
             const int acc = local & 1;
             if (any) {
-                if (!together([&] { return tc_wait(smem_u32(&s.tfull[acc]), (local >> 1) & 1, watch); }))
+                if (!warp_wait(smem_u32(&s.tfull[acc]), (local >> 1) & 1, watch))
                     break;
                 ++local;
                 tc_fence_after();

@@ -193,39 +193,41 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     auto nth = [&](int i) { return deal + i * p.deal; };
 
     if (warp == 0) {
-        if (lane == 0) {
+        {
             int stage = 0, n = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int i0 = 0; ok && i0 < mine; i0 += p.together) {
                 const int some = min(p.together, mine - i0);
                 for (int kb = kb0; kb < kb1; ++kb, ++n) {
-                    if (!tc_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch)) {
-                        ok = false;
+                    ok = warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch);
+                    if (!ok)
                         break;
-                    }
                     const uint32_t bar = smem_u32(&s.full[stage]);
                     const uint32_t base = smem_u32(ring) + stage * p.stage_bytes;
                     const uint32_t dA = base + p.a_offset;
-                    mbar_arrive_expect_tx(bar, p.box_rows * 128 + some * b_bytes);
-                    tma_load_2d(dA, tmX, bar, kb * TC_BK, row0);
-                    for (int i = 0; i < some; ++i) {
-                        const int g = side.one ? 0 : s.plan.ids[nth(i0 + i)];
-                        const uint32_t dB = base + i * b_bytes;
-                        if (side.across) {
-                            for (int b = 0; b * 8192 < b_bytes; ++b)
-                                tma_load_3d(dB + b * 8192, tmF, bar, b * 64, kb * TC_BK, g);
-                        } else {
-                            tma_load_3d(dB, tmF, bar, kb * TC_BK, 0, g);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar, p.box_rows * 128 + some * b_bytes);
+                        tma_load_2d(dA, tmX, bar, kb * TC_BK, row0);
+                        for (int i = 0; i < some; ++i) {
+                            const int g = side.one ? 0 : s.plan.ids[nth(i0 + i)];
+                            const uint32_t dB = base + i * b_bytes;
+                            if (side.across) {
+                                for (int b = 0; b * 8192 < b_bytes; ++b)
+                                    tma_load_3d(dB + b * 8192, tmF, bar, b * 64, kb * TC_BK, g);
+                            } else {
+                                tma_load_3d(dB, tmF, bar, kb * TC_BK, 0, g);
+                            }
                         }
                     }
+                    __syncwarp();
                     if (++stage == p.stages) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
             }
-            if (!ok) {  // wait (bounded) for the copies in flight before shared memory goes away
+            if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before shared memory goes away
                 for (int i = 0; i < p.stages; ++i) {
                     const int uses = n / p.stages + (i < n % p.stages);
                     const long long t0 = clock64();
@@ -236,17 +238,16 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && steps > 0) {
+        if (steps > 0) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int i0 = 0; ok && i0 < mine; i0 += p.together) {
                 const int some = min(p.together, mine - i0);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!tc_wait(smem_u32(&s.full[stage]), phase, watch)) {
-                        ok = false;
+                    ok = warp_wait(smem_u32(&s.full[stage]), phase, watch);
+                    if (!ok)
                         break;
-                    }
                     tc_fence_after();
                     const uint32_t base = smem_u32(ring) + stage * p.stage_bytes;
                     const uint32_t a0 = base + p.a_offset;
@@ -254,21 +255,27 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
                         const uint32_t b0 = base + i * b_bytes;
                         const uint4 rows = *reinterpret_cast<const uint4*>(s.plan.rows[nth(i0 + i)]);
                         const uint32_t off[4] = {~rows.x, ~rows.y, ~rows.z, ~rows.w};
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
-                            tc_mma_f16_lanes(tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
-                                             side.across ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                                         : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                             side.idesc, kb != kb0 || k != 0, off);
+                            for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
+                                tc_mma_f16_lanes(tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
+                                                 side.across ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                             : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                                 side.idesc, kb != kb0 || k != 0, off);
+                            if (i == some - 1)
+                                tc_commit(smem_u32(&s.empty[stage]));
+                        }
+                        __syncwarp();
                     }
-                    tc_commit(smem_u32(&s.empty[stage]));
                     if (++stage == p.stages) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
             }
-            tc_commit(smem_u32(&s.done));  // also after giving up: nothing may run on
+            if (elect_one())
+                tc_commit(smem_u32(&s.done));  // also after giving up: nothing may run on
+            __syncwarp();
             const long long t0 = clock64();
             while (!mbar_try_wait(smem_u32(&s.done), 0) && clock64() - t0 < p.wait_budget) {
             }

@@ -148,16 +148,19 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     const uint32_t held = ring + p.ring;  // the tile's rank values
 
     if (warp == 0) {
-        if (lane == 0) {
+        {
             int stage = 0, n = 0;
             uint32_t phase = 0;
             auto step = [&](bool skip, uint32_t bytes, auto load) {
-                if (!tc_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch))
+                if (!warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch))
                     return false;
                 if (!skip) {
                     const uint32_t bar = smem_u32(&s.full[stage]);
-                    mbar_arrive_expect_tx(bar, bytes);
-                    load(ring + stage * p.stage_bytes + 16384, ring + stage * p.stage_bytes, bar);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar, bytes);
+                        load(ring + stage * p.stage_bytes + 16384, ring + stage * p.stage_bytes, bar);
+                    }
+                    __syncwarp();
                     ++n;
                 }
                 if (++stage == p.stages) {
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                 });
             if (ok && p.adapters) {
                 grid_dep_wait();
-                ok = tc_wait(smem_u32(&s.planned), 0, watch);
+                ok = warp_wait(smem_u32(&s.planned), 0, watch);
                 if (!ACROSS && p.beside > 0) {
                     for (int a = 0; ok && a < s.count; a += p.beside) {
                         const int some = min(p.beside, s.count - a);
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     }
                 }
             }
-            if (!ok) {  // wait (bounded) for the copies in flight before shared memory goes away
+            if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before shared memory goes away
                 for (int i = 0; i < p.stages; ++i) {
                     const int uses = n / p.stages + (i < n % p.stages);
                     const long long t0 = clock64();
@@ -221,15 +224,18 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
             int stage = 0;
             uint32_t phase = 0;
             auto step = [&](auto multiply) {
-                if (!tc_wait(smem_u32(&s.full[stage]), phase, watch))
+                if (!warp_wait(smem_u32(&s.full[stage]), phase, watch))
                     return false;
                 tc_fence_after();
-                multiply(ring + stage * p.stage_bytes + 16384, ring + stage * p.stage_bytes);
-                tc_commit(smem_u32(&s.empty[stage]));
+                if (elect_one()) {
+                    multiply(ring + stage * p.stage_bytes + 16384, ring + stage * p.stage_bytes);
+                    tc_commit(smem_u32(&s.empty[stage]));
+                }
+                __syncwarp();
                 if (++stage == p.stages) {
                     stage = 0;
                     phase ^= 1;
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                                       p.idesc, kb != kb0 || k != 0);
                 });
             if (ok && p.adapters) {
-                ok = tc_wait(smem_u32(&s.planned), 0, watch);
+                ok = warp_wait(smem_u32(&s.planned), 0, watch);
                 if (!ACROSS && p.beside > 0) {
                     const uint32_t width = p.lay.chunk * 2;
                     const int deep = p.lay.deep(0, p.rank);
@@ -281,7 +287,9 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                         });
                 }
             }
-            tc_commit(smem_u32(&s.done));  // also after giving up: nothing may run on
+            if (elect_one())
+                tc_commit(smem_u32(&s.done));  // also after giving up: nothing may run on
+            __syncwarp();
             const long long t0 = clock64();
             while (!mbar_try_wait(smem_u32(&s.done), 0) && clock64() - t0 < p.wait_budget) {
             }

@@ -21,6 +21,7 @@
 #include "lora.h"
 #include "ops.cuh"
 #include "simt_tile.cuh"
+#include "warp_roles.cuh"
 
 namespace tmmo {
 

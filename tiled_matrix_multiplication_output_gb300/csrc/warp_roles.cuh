@@ -1,0 +1,32 @@
+// The wait of roles that run on whole warps.
+#pragma once
+
+#include "ops.cuh"
+
+namespace tmmo {
+
+// Bounded wait of a whole converged warp on an mbarrier phase.  The roles that
+// issue copies and MMAs run on whole warps, one elected lane issuing: their
+// operands then live in uniform registers, from which the instructions take
+// them (from a branch of one lane an MMA took about 140 cycles to issue and a
+// copy about 100).
+template <bool CLUSTER_SCOPE = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const TcWatch& w)
+{
+    long long t0 = 0;
+    for (;;) {
+        const bool done = CLUSTER_SCOPE ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, done))
+            return true;
+        const long long now = clock64();
+        if (t0 == 0)
+            t0 = now;
+        const bool late = now - t0 > w.budget;
+        if (late)
+            tc_raise(w);
+        if (__any_sync(0xffffffffu, late || *w.abort_flag))
+            return false;
+    }
+}
+
+}  // namespace tmmo
