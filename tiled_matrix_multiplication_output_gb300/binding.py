@@ -560,7 +560,7 @@ class _Torch:
         # the address of the current stream, 3 us less than building a Stream object
         self.current_stream = torch._C._cuda_getCurrentRawStream
         self.empty = torch.empty
-        self.float32 = torch.float32
+        self.float32, self.int32, self.uint8 = torch.float32, torch.int32, torch.uint8
         self.f8_types = (torch.float8_e4m3fn, torch.float8_e5m2)
         self.f8_codes = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
         self.codes = _dtype_codes()
@@ -836,22 +836,51 @@ def _check_batch(x, what):
 
 # ------------------------------------------------------ products grouped by rows
 
-def _check_typed(x, code, what):
-    """_check_matrix of an operand of the type `code`."""
-    if _cache().codes.get(x.dtype) != code:
-        raise TypeError(f"{what}'s type differs from that of the other operands")
-    return _check_matrix(x, what)
-
-
-def _check_stack(x, what):
-    """(matrices, rows, cols, row stride, matrix stride) of a 3-D tensor with
-    contiguous rows on the current CUDA device."""
+def _begin(x, what):
+    """(type code, dtype, device index) of a call's first operand, which is to be
+    on the current CUDA device."""
+    t = _cached or _cache()
+    dtype = x.dtype
+    code = t.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"{what} must be FP32, FP16 or BF16")
     device = x.get_device()
-    if device < 0 or x.dim() != 3:
-        raise ValueError(f"{what} must be a 3-D CUDA tensor")
-    if device != (_cached or _cache()).current_device():
+    if device < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if device != t.current_device():
         raise ValueError(f"{what} is not on the current device")
-    n, rows, cols = x.shape
+    return code, dtype, device
+
+
+def _rows_of(x, what, dtype, device):
+    """(rows, cols, row stride) of a 2-D operand with contiguous rows; dtype: None
+    for any.  (These checks are most of the host's time in a call: one look at
+    each property.)"""
+    if dtype is not None and x.dtype is not dtype:
+        raise TypeError(f"{what} must have the other operands' dtype")
+    shape = x.shape
+    if x.get_device() != device or len(shape) != 2:
+        raise ValueError(f"{what} must be a 2-D tensor on the operands' device")
+    rows, cols = shape
+    pitch, step = x.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what}'s rows must be contiguous")
+    if rows <= 1:  # a single row has no pitch of its own
+        return rows, cols, (cols + 15) // 16 * 16
+    if pitch < cols:
+        raise ValueError(f"{what}'s rows must not overlap")
+    return rows, cols, pitch
+
+
+def _stack_of(x, what, dtype, device):
+    """(matrices, rows, cols, row stride, matrix stride) of a 3-D operand with
+    contiguous rows."""
+    if dtype is not None and x.dtype is not dtype:
+        raise TypeError(f"{what} must have the other operands' dtype")
+    shape = x.shape
+    if x.get_device() != device or len(shape) != 3:
+        raise ValueError(f"{what} must be a 3-D tensor on the operands' device")
+    n, rows, cols = shape
     stride, pitch, step = x.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what}'s rows must be contiguous")
@@ -864,35 +893,38 @@ def _check_stack(x, what):
     return n, rows, cols, pitch, stride
 
 
-def _check_index(x, like, n, what):
-    """A contiguous int32 vector (of n values, unless None) on `like`'s device."""
-    if x.dim() != 1 or not x.is_contiguous() or x.get_device() != like.get_device():
+def _vector_of(x, what, n, dtype, device):
+    """The address of a contiguous vector (of n values, unless None)."""
+    shape = x.shape
+    if len(shape) != 1 or x.get_device() != device or not x.is_contiguous():
         raise ValueError(f"{what} must be a contiguous 1-D tensor on the operands' device")
-    if x.dtype is not _torch().int32:
-        raise TypeError(f"{what} must be int32")
-    if n is not None and x.shape[0] != n:
+    if x.dtype is not dtype:
+        raise TypeError(f"{what} must be {str(dtype)[6:]}")
+    if n is not None and shape[0] != n:
         raise ValueError(f"{what} must have {n} values")
     return x.data_ptr()
 
 
-def _in_code(x, what):
-    code = (_cached or _cache()).codes.get(x.dtype)
+def _result(out, shape, out_dtype, like, stream):
+    """(the result, its type code): `out`, or a new tensor."""
+    t = _cached or _cache()
+    if out is None:
+        dtype = t.float32 if out_dtype is None else \
+            out_dtype if out_dtype in t.codes else _out_dtype(out_dtype)
+        out = _allocate(stream, _empty, shape, dtype, like.device)
+    elif tuple(out.shape) != shape or (out_dtype is not None and out.dtype != _out_dtype(out_dtype)):
+        raise ValueError(f"out must be a {shape} tensor of the output dtype")
+    code = t.codes.get(out.dtype)
     if code is None:
-        raise TypeError(f"{what} must be FP32, FP16 or BF16")
-    return code
-
-
-def _check_out(out, shape, out_dtype, what="out"):
-    if tuple(out.shape) != shape or (out_dtype is not None and out.dtype != _out_dtype(out_dtype)):
-        raise ValueError(f"{what} must be a {shape} tensor of the output dtype")
-    _in_code(out, what)
+        raise TypeError("results are FP32, FP16 or BF16")
+    return out, code
 
 
 def _workspace(nbytes, x, stream):
     """(address, the tensor that holds it) of device scratch, allocated by PyTorch."""
     if nbytes == 0:
         return None, None
-    w = _allocate(stream, _empty, (nbytes,), _torch().uint8, x.device)
+    w = _allocate(stream, _empty, (nbytes,), (_cached or _cache()).uint8, x.device)
     return w.data_ptr(), w
 
 
@@ -913,31 +945,29 @@ def matmul_grouped(x, w, offsets, op_b="t", out_dtype=None, out=None, alpha=1.0,
     tb = OPS.get(op_b)
     if tb is None:
         raise ValueError("op_b is \"n\" or \"t\"")
-    code = _in_code(x, "x")
-    rows, K, ldx = _check_matrix(x, "x")
-    groups, N, K2, ldw, stride = _check_stack(w, "w")
-    if w.dtype is not x.dtype:
-        raise TypeError("x and w must have the same dtype")
+    code, dtype, device = _begin(x, "x")
+    rows, K, ldx = _rows_of(x, "x", None, device)
+    groups, N, K2, ldw, stride = _stack_of(w, "w", dtype, device)
     if not tb:
         N, K2 = K2, N
     if K != K2:
         raise ValueError("inner dimensions differ")
-    off = _check_index(offsets, x, groups + 1, "offsets")
+    off = _vector_of(offsets, "offsets", groups + 1, _cached.int32, device)
     given = out is not None
-    if not given:
-        if beta != 0.0:
-            raise ValueError("beta != 0 needs out")
-        out = _allocate(stream, _empty, (rows, N), _out_dtype(out_dtype), x.device)
-        ldy = N
-    else:
-        _check_out(out, (rows, N), out_dtype)
-        ldy = _check_matrix(out, "out")[2]
+    if beta != 0.0 and not given:
+        raise ValueError("beta != 0 needs out")
+    out, ocode = _result(out, (rows, N), out_dtype, x, stream)
+    ldy = _rows_of(out, "out", None, device)[2] if given else N
     lib = _lib or load_library()
     px, pw = x.data_ptr(), w.data_ptr()
-    nbytes = lib.gemm_grouped_workspace_size(px, ldx, pw, ldw, stride, rows, groups, N, K, tb, code)
-    ws, _held = _workspace(nbytes, x, stream)
+    ws = _held = None
+    nbytes = 0
+    if code != F32 and (px | pw | 2 * (ldx | ldw | stride)) & 15:
+        nbytes = lib.gemm_grouped_workspace_size(px, ldx, pw, ldw, stride, rows, groups, N, K, tb,
+                                                 code)
+        ws, _held = _workspace(nbytes, x, stream)
     rc = lib.gemm_grouped(px, ldx, pw, ldw, stride, tb, off, out.data_ptr(), ldy, rows, groups, N,
-                          K, alpha, beta, not given, code, dtype_code(out.dtype), ws, nbytes,
+                          K, alpha, beta, not given, code, ocode, ws, nbytes,
                           _stream_ptr(stream, x))
     if rc != OK:
         raise GemmError(rc, "gemm_grouped")
@@ -955,29 +985,29 @@ def matmul_grouped_wgrad(dy, x, offsets, out_dtype=None, out=None, alpha=1.0, be
     beta = 1 to add to it.  out_dtype defaults to FP32, or to out's type.
     Groups without rows give zeros (beta * C).  Returns C without
     synchronizing."""
-    code = _in_code(x, "x")
-    rows, K, ldx = _check_matrix(x, "x")
-    rows2, N, ldd = _check_typed(dy, code, "dy")
+    code, dtype, device = _begin(x, "x")
+    rows, K, ldx = _rows_of(x, "x", None, device)
+    rows2, N, ldd = _rows_of(dy, "dy", dtype, device)
     if rows != rows2:
         raise ValueError("dy and x must have the same number of rows")
-    off = _check_index(offsets, x, None, "offsets")
+    off = _vector_of(offsets, "offsets", None, _cached.int32, device)
     groups = offsets.shape[0] - 1
     if groups < 0:
         raise ValueError("offsets must have at least one value")
-    if out is None:
-        if beta != 0.0:
-            raise ValueError("beta != 0 needs out")
-        out = _allocate(stream, _empty, (groups, N, K), _out_dtype(out_dtype), x.device)
-        ldc, stride = K, N * K
-    else:
-        _check_out(out, (groups, N, K), out_dtype)
-        *_, ldc, stride = _check_stack(out, "out")
+    given = out is not None
+    if beta != 0.0 and not given:
+        raise ValueError("beta != 0 needs out")
+    out, ocode = _result(out, (groups, N, K), out_dtype, x, stream)
+    ldc, stride = _stack_of(out, "out", None, device)[3:] if given else (K, N * K)
     lib = _lib or load_library()
     px, pd = x.data_ptr(), dy.data_ptr()
-    nbytes = lib.gemm_grouped_wgrad_workspace_size(pd, ldd, px, ldx, rows, N, K, code)
-    ws, _held = _workspace(nbytes, x, stream)
+    ws = _held = None
+    nbytes = 0
+    if code != F32 and (px | pd | 2 * (ldx | ldd)) & 15:
+        nbytes = lib.gemm_grouped_wgrad_workspace_size(pd, ldd, px, ldx, rows, N, K, code)
+        ws, _held = _workspace(nbytes, x, stream)
     rc = lib.gemm_grouped_wgrad(pd, ldd, px, ldx, off, out.data_ptr(), ldc, stride, rows, groups,
-                                N, K, alpha, beta, code, dtype_code(out.dtype), ws, nbytes,
+                                N, K, alpha, beta, code, ocode, ws, nbytes,
                                 _stream_ptr(stream, x))
     if rc != OK:
         raise GemmError(rc, "gemm_grouped_wgrad")
@@ -986,32 +1016,21 @@ def matmul_grouped_wgrad(dy, x, offsets, out_dtype=None, out=None, alpha=1.0, be
 
 # --------------------------------------------------------- low-rank adapters
 
-def _lora_operands(a, b, adapter, scale, rows, N, K, code, like):
+def _lora_operands(a, b, adapter, scale, rows, N, K, dtype, device):
     """(the bytes of gemm_lora_t, adapters, rank, the address of the rows' adapters)."""
-    G, r, Ka, lda, stride_a = _check_stack(a, "a")
-    Gb, Nb, rb, ldb, stride_b = _check_stack(b, "b")
-    if a.dtype is not like.dtype or b.dtype is not like.dtype:
-        raise TypeError("a and b must have the other operands' dtype")
-    if (G, r) != (Gb, rb) or Ka != K or Nb != N:
+    G, r, Ka, lda, stride_a = _stack_of(a, "a", dtype, device)
+    Gb, Nb, rb, ldb, stride_b = _stack_of(b, "b", dtype, device)
+    if G != Gb or r != rb or Ka != K or Nb != N:
         raise ValueError(f"a must be (adapters, rank, {K}) and b (adapters, {N}, rank)")
-    index = _check_index(adapter, like, rows, "adapter")
-    ps = None
-    if scale is not None:
-        if scale.dim() != 1 or scale.shape[0] != G or not scale.is_contiguous() \
-                or scale.get_device() != like.get_device():
-            raise ValueError("scale must be a contiguous vector, one value for each adapter, on "
-                             "the operands' device")
-        if scale.dtype is not (_cached or _cache()).float32:
-            raise TypeError("scale must be FP32")
-        ps = scale.data_ptr()
-    return _LORA.pack(a.data_ptr(), lda, stride_a, b.data_ptr(), ldb, stride_b, ps or 0, G,
-                      r), G, r, index
+    index = _vector_of(adapter, "adapter", rows, _cached.int32, device)
+    ps = 0 if scale is None else _vector_of(scale, "scale", G, _cached.float32, device)
+    return _LORA.pack(a.data_ptr(), lda, stride_a, b.data_ptr(), ldb, stride_b, ps, G, r), G, r, \
+        index
 
 
 def matmul_lora(x, w, a, b, adapter, scale=None, out_dtype=None, out=None, stream=None):
     """y_i = x_i @ w^T + scale[g] * (x_i @ a[g]^T) @ b[g]^T with g = adapter[i]:
-    a shared projection with a low-rank adapter of its own for every row, in one
-    pass over the rows.
+    a shared projection with a low-rank adapter of its own for every row.
 
     x: rows x in (FP16, BF16 or FP32; rows contiguous, any row stride); w: out x in;
     a: (adapters, rank, in) and b: (adapters, out, rank); adapter: int32 CUDA
@@ -1020,20 +1039,17 @@ def matmul_lora(x, w, a, b, adapter, scale=None, out_dtype=None, out=None, strea
     rank at most GEMM_MAX_RANK (256).  A row sees nothing of other rows'
     adapters.  out_dtype defaults to FP32, or to out's type.  Returns y
     without synchronizing."""
-    code = _in_code(x, "x")
-    rows, K, ldx = _check_matrix(x, "x")
-    N, K2, ldw = _check_typed(w, code, "w")
+    code, dtype, device = _begin(x, "x")
+    rows, K, ldx = _rows_of(x, "x", None, device)
+    N, K2, ldw = _rows_of(w, "w", dtype, device)
     if K != K2:
         raise ValueError("inner dimensions differ")
-    lora, G, r, index = _lora_operands(a, b, adapter, scale, rows, N, K, code, x)
-    if out is None:
-        out = _allocate(stream, _empty, (rows, N), _out_dtype(out_dtype), x.device)
-        ldy = N
-    else:
-        _check_out(out, (rows, N), out_dtype)
-        ldy = _check_matrix(out, "out")[2]
+    lora, G, r, index = _lora_operands(a, b, adapter, scale, rows, N, K, dtype, device)
+    given = out is not None
+    out, ocode = _result(out, (rows, N), out_dtype, x, stream)
+    ldy = _rows_of(out, "out", None, device)[2] if given else N
     lib = _lib or load_library()
-    px, pw, ocode = x.data_ptr(), w.data_ptr(), dtype_code(out.dtype)
+    px, pw = x.data_ptr(), w.data_ptr()
     nbytes = lib.gemm_lora_workspace_size(px, ldx, pw, ldw, lora, rows, N, K, code, ocode)
     ws, _held = _workspace(nbytes, x, stream)
     rc = lib.gemm_lora(px, ldx, pw, ldw, lora, index, out.data_ptr(), ldy, rows, N, K, code, ocode,
@@ -1053,20 +1069,18 @@ def matmul_lora_backward(dy, x, w, a, b, adapter, scale=None, out_dtype=None, gr
     t_i = scale[g] x_i @ a[g]^T.  Adapters without rows get zeros.  out_dtype is
     dx's type (default FP32), grad_dtype that of da and db (default FP32).
     Returns without synchronizing."""
-    code = _in_code(x, "x")
-    rows, K, ldx = _check_matrix(x, "x")
-    rows2, N, ldd = _check_typed(dy, code, "dy")
-    N2, K2, ldw = _check_typed(w, code, "w")
+    code, dtype, device = _begin(x, "x")
+    rows, K, ldx = _rows_of(x, "x", None, device)
+    rows2, N, ldd = _rows_of(dy, "dy", dtype, device)
+    N2, K2, ldw = _rows_of(w, "w", dtype, device)
     if rows != rows2 or N != N2 or K != K2:
         raise ValueError("dy must be rows x out, x rows x in and w out x in")
-    lora, G, r, index = _lora_operands(a, b, adapter, scale, rows, N, K, code, x)
-    odt, gdt = _out_dtype(out_dtype), _out_dtype(grad_dtype)
-    dx = _allocate(stream, _empty, (rows, K), odt, x.device)
-    da = _allocate(stream, _empty, (G, r, K), gdt, x.device)
-    db = _allocate(stream, _empty, (G, N, r), gdt, x.device)
+    lora, G, r, index = _lora_operands(a, b, adapter, scale, rows, N, K, dtype, device)
+    dx, ocode = _result(None, (rows, K), out_dtype, x, stream)
+    da, gcode = _result(None, (G, r, K), grad_dtype, x, stream)
+    db, _ = _result(None, (G, N, r), grad_dtype, x, stream)
     lib = _lib or load_library()
     pd, px, pw = dy.data_ptr(), x.data_ptr(), w.data_ptr()
-    ocode, gcode = dtype_code(odt), dtype_code(gdt)
     nbytes = lib.gemm_lora_backward_workspace_size(pd, ldd, px, ldx, pw, ldw, lora, rows, N, K, code,
                                                    ocode, gcode)
     ws, _held = _workspace(nbytes, x, stream)
