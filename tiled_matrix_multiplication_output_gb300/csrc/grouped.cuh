@@ -31,11 +31,33 @@ struct GroupTable {
     }
 };
 
-// Builds the table for tiles of `tile_rows` rows; every thread of the block
-// calls it, and it ends in a block barrier.  Offsets are taken as the largest
-// of those up to them, within [0, rows]: whatever they hold, groups neither
-// overlap nor leave the matrix.
-__device__ __forceinline__ GroupTable load_groups(int* smem, const Grouping& by, int tile_rows)
+// The warp's largest value so far in each lane, and of those before the warp.
+__device__ __forceinline__ int warp_max_scan(int v, int before)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (static_cast<int>(threadIdx.x & 31) >= d)
+            v = max(v, o);
+    }
+    return max(v, before);
+}
+__device__ __forceinline__ int warp_sum_scan(int v, int before)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (static_cast<int>(threadIdx.x & 31) >= d)
+            v += o;
+    }
+    return v + before;
+}
+
+// Builds the rows of the table; every thread of the block calls it, and it ends
+// in a block barrier.  Offsets are taken as the largest of those up to them,
+// within [0, rows]: whatever they hold, groups neither overlap nor leave the
+// matrix.
+__device__ __forceinline__ GroupTable load_groups(int* smem, const Grouping& by)
 {
     GroupTable t{smem, smem + kMaxGroups + 1};
     const int n = by.groups + 1;
@@ -43,40 +65,48 @@ __device__ __forceinline__ GroupTable load_groups(int* smem, const Grouping& by,
         t.first[i] = min(max(by.offsets[i], 0), by.rows);
     __syncthreads();
     if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int largest = 0, tiles = 0;
+        int largest = 0;
         for (int base = 0; base < n; base += 32) {
-            const int i = base + lane;
-            int v = i < n ? t.first[i] : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(0xffffffffu, v, d);
-                if (lane >= d)
-                    v = max(v, o);
-            }
-            v = max(v, largest);
-            int before = __shfl_up_sync(0xffffffffu, v, 1);
-            if (lane == 0)
-                before = base == 0 ? v : largest;
-            // tiles of group i - 1, and their sum up to it
-            int c = (v - before) / tile_rows + ((v - before) % tile_rows != 0);
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(0xffffffffu, c, d);
-                if (lane >= d)
-                    c += o;
-            }
-            c += tiles;
-            if (i < n) {
+            const int i = base + threadIdx.x;
+            const int v = warp_max_scan(i < n ? t.first[i] : 0, largest);
+            if (i < n)
                 t.first[i] = v;
-                t.tile[i] = c;
-            }
             largest = __shfl_sync(0xffffffffu, v, 31);
-            tiles = __shfl_sync(0xffffffffu, c, 31);
         }
     }
     __syncthreads();
     return t;
+}
+
+// Tiles of at most `rows` rows in the lane's share of the groups.
+__device__ __forceinline__ int lane_tiles(const GroupTable& t, int groups, int rows)
+{
+    int sum = 0;
+    for (int g = threadIdx.x & 31; g < groups; g += 32)
+        sum += (t.first[g + 1] - t.first[g] + rows - 1) / rows;
+    return sum;
+}
+
+// Builds the tiles of the table, of rows() rows, which the first warp calls; the
+// rest as load_groups.
+template <typename Rows>
+__device__ __forceinline__ void count_tiles(const GroupTable& t, int groups, Rows rows)
+{
+    if (threadIdx.x < 32) {
+        const int tile_rows = rows();
+        int tiles = 0;
+        if (threadIdx.x == 0)
+            t.tile[0] = 0;
+        for (int base = 0; base < groups; base += 32) {
+            const int g = base + threadIdx.x;
+            const int c = warp_sum_scan(
+                g < groups ? (t.first[g + 1] - t.first[g] + tile_rows - 1) / tile_rows : 0, tiles);
+            if (g < groups)
+                t.tile[g + 1] = c;
+            tiles = __shfl_sync(0xffffffffu, c, 31);
+        }
+    }
+    __syncthreads();
 }
 
 // Zeros in this thread's share of the rows that lie before the first group or

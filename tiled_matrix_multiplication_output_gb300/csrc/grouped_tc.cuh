@@ -40,6 +40,7 @@ enum { GROUPED_T = 0, GROUPED_N = 1, GROUPED_WGRAD = 2 };
 constexpr int GT_STAGES = 3;
 constexpr int GT_KSUB = 2;
 constexpr int GT_N = 256;        // the N side of a full tile
+constexpr int GT_SORTED = 256;   // groups, at most, that the gradient sorts
 
 struct GroupedTcParams {
     Grouping by;
@@ -90,8 +91,9 @@ __device__ __forceinline__ GroupedWork grouped_work(int t, const GroupTable& tab
     GroupedWork w;
     if constexpr (MODE == GROUPED_WGRAD) {
         const int per = p.tiles_f * p.tiles_c;
-        w.g = t / per;
-        const int u = t - w.g * per;
+        const int place = t / per;
+        w.g = p.by.groups <= GT_SORTED ? table.tile[place] : place;
+        const int u = t - place * per;
         w.f0 = u / p.tiles_c * 256;
         w.c0 = u % p.tiles_c * GT_N;
         w.count = min(GT_N, p.K - w.c0);
@@ -173,6 +175,46 @@ __device__ __forceinline__ void grouped_strip(const uint32_t (&v)[32], uint32_t 
     __syncwarp();
 }
 
+// How many rows a tile of the products has at most: what is quickest, by the waves
+// of tiles on the pairs and the time of a tile.  A K step of n rows takes about
+// 315 + 1.23 n cycles (630 at 256: operands from L2 set the pace).  5000 rows of 12
+// groups by 1000 outputs are 104 tiles of 256 rows, two waves on 76 pairs, and 132
+// of 192.  One warp calls it.
+__device__ __forceinline__ int tile_rows(const GroupTable& table, int groups, int tiles_f, int pairs)
+{
+    int best = GT_N, least = 0;
+#pragma unroll 1
+    for (int rows = GT_N; rows >= 128; rows -= 32) {
+        const int tiles = __reduce_add_sync(0xffffffffu, lane_tiles(table, groups, rows));
+        const int waves = static_cast<int>((static_cast<int64_t>(tiles) * tiles_f + pairs - 1) / pairs);
+        const int time = min(waves, 1 << 18) * (315 + rows * 5 / 4);
+        if (rows == GT_N || time < least) {
+            best = rows;
+            least = time;
+        }
+        if (waves <= 1)
+            break;  // smaller tiles win nothing
+    }
+    return best;
+}
+
+// Puts the groups into table.tile with the longest first (the gradient has no use
+// for the tiles): the last tiles to start are then the short ones.  Every thread
+// of the block calls it; it ends in a block barrier.
+__device__ __forceinline__ void sort_groups(const GroupTable& table, int groups)
+{
+    for (int g = threadIdx.x; g < groups; g += blockDim.x) {
+        const int rows = table.first[g + 1] - table.first[g];
+        int place = 0;
+        for (int h = 0; h < groups; ++h) {
+            const int other = table.first[h + 1] - table.first[h];
+            place += other > rows || (other == rows && h < g);
+        }
+        table.tile[place] = g;
+    }
+    __syncthreads();
+}
+
 template <int MODE, typename OutT>
 __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -232,7 +274,11 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         tmem_alloc<2>(smem_u32(tmem_slot), L::TMEM_COLS);
         tmem_relinquish<2>();
     }
-    const GroupTable table = load_groups(reinterpret_cast<int*>(smem + L::OFF_TABLE), p.by, GT_N);
+    const GroupTable table = load_groups(reinterpret_cast<int*>(smem + L::OFF_TABLE), p.by);
+    if (!WGRAD)
+        count_tiles(table, p.by.groups, [&] { return tile_rows(table, p.by.groups, p.tiles_f, num_units); });
+    else if (p.by.groups <= GT_SORTED)
+        sort_groups(table, p.by.groups);
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
@@ -485,6 +531,21 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                             tma_store_3d(&tmC, staging, col, f, w.g);
                             bulk_commit_group();
                         }
+                    }
+                } else if (p.tma_out) {
+                    // no rows: one strip of zeros, stored again and again
+                    if (lane == 0)
+                        bulk_wait_group_read<0>();
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        st_shared_v4(staging + lane * 128 + i * 16, 0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && f < p.N) {
+                        for (int col = w.c0; col < min(p.K, w.c0 + GT_N); col += TcOut<OutT>::STRIP)
+                            tma_store_3d(&tmC, staging, col, f, w.g);
+                        bulk_commit_group();
                     }
                 } else {
                     if (lane == 0)

@@ -26,9 +26,10 @@ cudaError_t with_type(int dtype, F f)
     }
 }
 
+// Two blocks for each SM, one hiding the other's latencies.
 inline unsigned simt_blocks(int64_t tiles, int num_sms)
 {
-    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, 8ll * num_sms)));
+    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, 2ll * num_sms)));
 }
 
 }  // namespace tmmo
