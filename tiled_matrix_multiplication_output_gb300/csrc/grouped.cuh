@@ -53,31 +53,6 @@ __device__ __forceinline__ int warp_sum_scan(int v, int before)
     return v + before;
 }
 
-// Builds the rows of the table; every thread of the block calls it, and it ends
-// in a block barrier.  Offsets are taken as the largest of those up to them,
-// within [0, rows]: whatever they hold, groups neither overlap nor leave the
-// matrix.
-__device__ __forceinline__ GroupTable load_groups(int* smem, const Grouping& by)
-{
-    GroupTable t{smem, smem + kMaxGroups + 1};
-    const int n = by.groups + 1;
-    for (int i = threadIdx.x; i < n; i += blockDim.x)
-        t.first[i] = min(max(by.offsets[i], 0), by.rows);
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        int largest = 0;
-        for (int base = 0; base < n; base += 32) {
-            const int i = base + threadIdx.x;
-            const int v = warp_max_scan(i < n ? t.first[i] : 0, largest);
-            if (i < n)
-                t.first[i] = v;
-            largest = __shfl_sync(0xffffffffu, v, 31);
-        }
-    }
-    __syncthreads();
-    return t;
-}
-
 // Tiles of at most `rows` rows in the lane's share of the groups.
 __device__ __forceinline__ int lane_tiles(const GroupTable& t, int groups, int rows)
 {
@@ -87,26 +62,56 @@ __device__ __forceinline__ int lane_tiles(const GroupTable& t, int groups, int r
     return sum;
 }
 
-// Builds the tiles of the table, of rows() rows, which the first warp calls; the
-// rest as load_groups.
-template <typename Rows>
-__device__ __forceinline__ void count_tiles(const GroupTable& t, int groups, Rows rows)
+// Builds the table; every thread of the block calls it, and it ends in a block
+// barrier.  Offsets are taken as the largest of those up to them, within
+// [0, rows]: whatever they hold, groups neither overlap nor leave the matrix.
+// Tiles have at most `rows` rows (0: no tiles are made), or as many as
+// better(table, tiles of `rows` rows) says; meanwhile() is for the other warps while the
+// first one adds up.
+template <typename Better, typename Meanwhile>
+__device__ __forceinline__ GroupTable load_groups(int* smem, const Grouping& by, int rows, Better better,
+                                                  Meanwhile meanwhile)
 {
+    GroupTable t{smem, smem + kMaxGroups + 1};
+    const int n = by.groups + 1;
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        t.first[i] = min(max(by.offsets[i], 0), by.rows);
+    __syncthreads();
     if (threadIdx.x < 32) {
-        const int tile_rows = rows();
-        int tiles = 0;
-        if (threadIdx.x == 0)
-            t.tile[0] = 0;
-        for (int base = 0; base < groups; base += 32) {
-            const int g = base + threadIdx.x;
-            const int c = warp_sum_scan(
-                g < groups ? (t.first[g + 1] - t.first[g] + tile_rows - 1) / tile_rows : 0, tiles);
-            if (g < groups)
-                t.tile[g + 1] = c;
-            tiles = __shfl_sync(0xffffffffu, c, 31);
+        int largest = 0, tiles = 0, made = 0;
+#pragma unroll 1
+        for (;;) {
+#pragma unroll 1
+            for (int base = 0; base < n; base += 32) {
+                const int i = base + threadIdx.x;
+                const int v = warp_max_scan(i < n ? t.first[i] : 0, largest);
+                int before = __shfl_up_sync(0xffffffffu, v, 1);
+                if (threadIdx.x == 0)
+                    before = base == 0 ? v : largest;
+                largest = __shfl_sync(0xffffffffu, v, 31);
+                if (i < n)
+                    t.first[i] = v;
+                if (rows > 0) {  // tiles of the groups before this one
+                    const int c = warp_sum_scan((v - before + rows - 1) / rows, tiles);
+                    tiles = __shfl_sync(0xffffffffu, c, 31);
+                    if (i < n)
+                        t.tile[i] = c;
+                }
+            }
+            if (rows == 0 || made++ > 0)
+                break;
+            __syncwarp();
+            const int other = better(t, tiles);
+            if (other == rows)
+                break;
+            rows = other;  // once more, with tiles of another size
+            largest = tiles = 0;
         }
+    } else {
+        meanwhile();
     }
     __syncthreads();
+    return t;
 }
 
 // Zeros in this thread's share of the rows that lie before the first group or

@@ -15,6 +15,7 @@ cudaError_t grouped_tc_launch(const GroupedLaunch& l, cudaStream_t stream)
     p.alpha = l.alpha;
     p.beta = l.beta;
     p.zero_rest = l.zero_rest;
+    p.unit = row_unit(l.Y, l.ldy * type_bytes(l.out_dtype), 0);
     p.one_weight = l.by.groups == 1 || l.stride_w == 0;
     p.swap = !p.one_weight && l.stride_w < l.ldw;  // matrices interleaved row by row
     p.idesc = tc_idesc(l.in_dtype == DT_BF16, 256, 0, !l.w_t, false);

@@ -13,8 +13,7 @@ __global__ void __launch_bounds__(ST_THREADS) grouped_simt_kernel(const GroupedL
 {
     __shared__ int table[GroupTable::BYTES / sizeof(int)];
     __shared__ SimtSmem s;
-    const GroupTable groups = load_groups(table, l.by);
-    count_tiles(groups, l.by.groups, [] { return ST_M; });
+    const GroupTable groups = load_groups(table, l.by, ST_M, [](const GroupTable&, int) { return ST_M; }, [] {});
     OutT* Y = static_cast<OutT*>(l.Y);
     if (l.zero_rest)
         zero_rest_rows(groups, l.by, Y, l.ldy, l.N,
@@ -42,7 +41,7 @@ __global__ void __launch_bounds__(ST_THREADS) grouped_wgrad_simt_kernel(const Gr
 {
     __shared__ int table[GroupTable::BYTES / sizeof(int)];
     __shared__ SimtSmem s;
-    const GroupTable groups = load_groups(table, l.by);
+    const GroupTable groups = load_groups(table, l.by, 0, [](const GroupTable&, int) { return 0; }, [] {});
     const int tiles_n = (l.N + ST_M - 1) / ST_M, tiles_k = (l.K + ST_N - 1) / ST_N;
     const int64_t per_group = static_cast<int64_t>(tiles_n) * tiles_k;
     for (int64_t t = blockIdx.x; t < per_group * l.by.groups; t += gridDim.x) {

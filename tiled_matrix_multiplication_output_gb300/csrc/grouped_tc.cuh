@@ -30,15 +30,16 @@
 
 #include "grouped.cuh"
 #include "ops.cuh"
-#include "simt_tile.cuh"
+#include "store_rows.cuh"
 #include "warp_roles.cuh"
 
 namespace tmmo {
 
 enum { GROUPED_T = 0, GROUPED_N = 1, GROUPED_WGRAD = 2 };
 
-constexpr int GT_STAGES = 3;
-constexpr int GT_KSUB = 2;
+constexpr int GT_RING = 192 * 1024;
+constexpr int GT_MAX_STAGES = 10;
+constexpr int GT_A_BYTES = TC_BM * TC_BK * 2;  // a K step of the lanes' side
 constexpr int GT_N = 256;        // the N side of a full tile
 constexpr int GT_SORTED = 256;   // groups, at most, that the gradient sorts
 
@@ -52,6 +53,7 @@ struct GroupedTcParams {
     bool zero_rest;
     bool swap;            // the weights' map has its outer dimensions exchanged
     bool one_weight;
+    int unit;             // row_unit of the output
     bool tma_out;         // gradient: stored by TMA
     uint32_t idesc;       // with N = 0
     int* status;
@@ -63,14 +65,11 @@ template <int MODE>
 struct GroupedLayout {
     static constexpr bool WGRAD = MODE == GROUPED_WGRAD;
     static constexpr int THREADS = WGRAD ? 224 : 192;
-    static constexpr int SUB = TC_BM * TC_BK * 2;  // 16 KiB: an operand's K step
-    static constexpr int OFF_A = 0;
-    static constexpr int OFF_B = OFF_A + GT_STAGES * GT_KSUB * SUB;
-    static constexpr int OFF_STAGING = OFF_B + GT_STAGES * GT_KSUB * SUB;
-    static constexpr int OFF_TABLE = OFF_STAGING + (WGRAD ? 4 * TC_STAGING_BYTES : 0);
+    static constexpr int OFF_STAGING = GT_RING;
+    static constexpr int STAGING = WGRAD ? 4096 : 2048;  // of an epilogue warp
+    static constexpr int OFF_TABLE = OFF_STAGING + 4 * STAGING;
     static constexpr int OFF_BAR = OFF_TABLE + (GroupTable::BYTES + 15) / 16 * 16;
-    static constexpr int STEPS = GT_STAGES * GT_KSUB;
-    static constexpr int NUM_BARS = STEPS + GT_STAGES + 5 + (WGRAD ? STEPS : 0);
+    static constexpr int NUM_BARS = 2 * GT_MAX_STAGES + 5 + (WGRAD ? GT_MAX_STAGES : 0);
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
     static constexpr int BYTES = OFF_MISC + 16;
     static constexpr int SMEM_ALLOC = BYTES + 1024;
@@ -123,69 +122,20 @@ __device__ __forceinline__ GroupedWork grouped_work(int t, const GroupTable& tab
     return w;
 }
 
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                                 int32_t x, int32_t y, int32_t z)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
-// p[r * ld] = alpha * v[r] + beta * p[r * ld] for r < rows: what is added to is
-// loaded before anything is stored, so that the loads overlap.
-template <int R, typename OutT>
-__device__ __forceinline__ void grouped_put(OutT* p, int64_t ld, int rows, const float (&v)[R],
-                                            const GroupedTcParams& q)
-{
-    float old[R];
-    if (q.beta != 0.0f) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            old[r] = r < rows ? to_f32(p[r * ld]) : 0.0f;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (r < rows)
-            put(p + r * ld, q.beta != 0.0f ? fmaf(q.beta, old[r], q.alpha * v[r]) : q.alpha * v[r]);
-}
-
-// Strip of 32 rows x 32 FP32 values of a lane-major accumulator (this thread
-// holds a row) to C, through `staging`, in whole lines: any alignment, and
-// with the addition to C.
-template <typename OutT>
-__device__ __forceinline__ void grouped_strip(const uint32_t (&v)[32], uint32_t staging, uint32_t lane,
-                                              OutT* c, int64_t ldc, int rows, int cols,
-                                              const GroupedTcParams& p)
-{
-    const uint32_t at = staging + lane * 128;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)  // column j of row `lane` at j ^ lane: no bank conflicts
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + ((j ^ lane) << 2)), "r"(v[j]) : "memory");
-    __syncwarp();
-    if (static_cast<int>(lane) < cols)
-        for (int r = 0; r < rows; r += 8) {
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = ld_shared_f32(staging + (r + i) * 128 + ((lane ^ (r + i)) << 2));
-            grouped_put(c + r * ldc + lane, ldc, rows - r, f, p);
-        }
-    __syncwarp();
-}
-
 // How many rows a tile of the products has at most: what is quickest, by the waves
 // of tiles on the pairs and the time of a tile.  A K step of n rows takes about
 // 315 + 1.23 n cycles (630 at 256: operands from L2 set the pace).  5000 rows of 12
 // groups by 1000 outputs are 104 tiles of 256 rows, two waves on 76 pairs, and 132
 // of 192.  One warp calls it.
-__device__ __forceinline__ int tile_rows(const GroupTable& table, int groups, int tiles_f, int pairs)
+// largest: receives the rows that a tile then has at most.
+__device__ __forceinline__ int tile_rows(const GroupTable& table, int groups, int tiles, int tiles_f,
+                                         int pairs, int* largest)
 {
     int best = GT_N, least = 0;
 #pragma unroll 1
     for (int rows = GT_N; rows >= 128; rows -= 32) {
-        const int tiles = __reduce_add_sync(0xffffffffu, lane_tiles(table, groups, rows));
+        if (rows != GT_N)
+            tiles = __reduce_add_sync(0xffffffffu, lane_tiles(table, groups, rows));
         const int waves = static_cast<int>((static_cast<int64_t>(tiles) * tiles_f + pairs - 1) / pairs);
         const int time = min(waves, 1 << 18) * (315 + rows * 5 / 4);
         if (rows == GT_N || time < least) {
@@ -195,6 +145,12 @@ __device__ __forceinline__ int tile_rows(const GroupTable& table, int groups, in
         if (waves <= 1)
             break;  // smaller tiles win nothing
     }
+    int most = 0;
+    for (int g = threadIdx.x; g < groups; g += 32)
+        most = max(most, table.first[g + 1] - table.first[g]);
+    most = __reduce_max_sync(0xffffffffu, min(most, best));
+    if (threadIdx.x == 0)
+        *largest = max(32, (most + 31) / 32 * 32);
     return best;
 }
 
@@ -230,17 +186,16 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + L::OFF_BAR;
-    auto full_bar = [&](int s, int j) { return bar0 + 8u * (s * GT_KSUB + j); };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (L::STEPS + s); };
-    auto tfull_bar = [&](int a) { return bar0 + 8u * (L::STEPS + GT_STAGES + a); };
-    auto tempty_bar = [&](int a) { return bar0 + 8u * (L::STEPS + GT_STAGES + 2 + a); };
-    const uint32_t drain_bar = bar0 + 8u * (L::STEPS + GT_STAGES + 4);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (GT_MAX_STAGES + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * GT_MAX_STAGES + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * GT_MAX_STAGES + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * GT_MAX_STAGES + 4);
     // gradient: a group's last K step lands on this CTA's own barrier first
-    auto tail_bar = [&](int s, int j) {
-        return bar0 + 8u * (L::STEPS + GT_STAGES + 5 + s * GT_KSUB + j);
-    };
+    auto tail_bar = [&](int s) { return bar0 + 8u * (2 * GT_MAX_STAGES + 5 + s); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+    int* largest = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);
 
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
@@ -249,15 +204,13 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
     const int unit = blockIdx.x >> 1, num_units = gridDim.x >> 1;
     const TcWatch watch{abort_flag, p.status, p.wait_budget};
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < GT_STAGES; ++s) {
-            for (int j = 0; j < GT_KSUB; ++j) {
-                // gradient: an arrival for each CTA, as either may have to zero
-                mbar_init(full_bar(s, j), WGRAD ? 2 : 1);
-                if (WGRAD)
-                    mbar_init(tail_bar(s, j), 1);
-            }
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < GT_MAX_STAGES; ++s) {
+            // gradient: an arrival for each CTA, as either may have to zero
+            mbar_init(full_bar(s), WGRAD ? 2 : 1);
             mbar_init(empty_bar(s), 1);
+            if (WGRAD)
+                mbar_init(tail_bar(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
@@ -268,21 +221,27 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
-        tma_prefetch_desc(&tmC);
     }
-    if (warp == 1) {
-        tmem_alloc<2>(smem_u32(tmem_slot), L::TMEM_COLS);
-        tmem_relinquish<2>();
-    }
-    const GroupTable table = load_groups(reinterpret_cast<int*>(smem + L::OFF_TABLE), p.by);
-    if (!WGRAD)
-        count_tiles(table, p.by.groups, [&] { return tile_rows(table, p.by.groups, p.tiles_f, num_units); });
-    else if (p.by.groups <= GT_SORTED)
+    // (the first warp makes the table meanwhile)
+    const GroupTable table = load_groups(
+        reinterpret_cast<int*>(smem + L::OFF_TABLE), p.by, WGRAD ? 0 : GT_N,
+        [&](const GroupTable& t, int tiles) { return tile_rows(t, p.by.groups, tiles, p.tiles_f, num_units, largest); },
+        [&] {
+            if (warp == 1) {
+                tmem_alloc<2>(smem_u32(tmem_slot), L::TMEM_COLS);
+                tmem_relinquish<2>();
+            }
+        });
+    if (WGRAD && p.by.groups <= GT_SORTED)
         sort_groups(table, p.by.groups);
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    // The ring: a stage is a K step of both operands, of as many rows as the
+    // largest tile has, so that small tiles have more steps on their way.
+    const int stage_bytes = GT_A_BYTES + (WGRAD ? GT_N : *largest) / 2 * TC_BK * 2;
+    const int stages = min(GT_RING / stage_bytes, GT_MAX_STAGES);
     const int num_work = (WGRAD ? p.by.groups * p.tiles_c : table.tile[p.by.groups]) * p.tiles_f;
     // rows of a group's last K step that the tensor core reads beyond the group
     auto is_ragged = [&](const GroupedWork& w, int kb) {
@@ -291,17 +250,9 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        const uint32_t sA = sbase + L::OFF_A;
-        const uint32_t sB = sbase + L::OFF_B;
-        int stage = 0;
+        int stage = 0, steps = 0;
         uint32_t phase = 0;
-        int issued[GT_STAGES], ragged[L::STEPS];
-#pragma unroll
-        for (int s = 0; s < GT_STAGES; ++s)
-            issued[s] = 0;
-#pragma unroll
-        for (int s = 0; s < L::STEPS; ++s)
-            ragged[s] = 0;
+        uint32_t ragged = 0, ragged_parity = 0;  // of the stages' tail barriers: used, and how often
         bool ok = true;
         for (int t = unit; ok && t < num_work; t += num_units) {
             const GroupedWork w = grouped_work<MODE>(t, table, p);
@@ -309,85 +260,68 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
             const int half = w.n / 2;
             const int c = w.c0 + static_cast<int>(rank) * half;
             const int z = p.one_weight ? 0 : w.g;
-            const uint32_t bytes = L::SUB + half * TC_BK * 2;
-            for (int kb0 = 0; kb0 < w.k_blocks; kb0 += GT_KSUB) {
-                const int nsub = min(GT_KSUB, w.k_blocks - kb0);
+            const uint32_t bytes = GT_A_BYTES + half * TC_BK * 2;
+            for (int kb = 0; kb < w.k_blocks; ++kb) {
                 ok = warp_wait(empty_bar(stage), phase ^ 1, watch);
                 if (!ok)
                     break;
-                // test hook (-1 in normal use): skip the stage holding that K step
-                if (p.fault_skip_kblock < kb0 || p.fault_skip_kblock >= kb0 + nsub) {
+                const bool tail = is_ragged(w, kb);
+                ++steps;
+                if (kb != p.fault_skip_kblock) {  // (test hook, -1 in normal use)
                     if (elect_one()) {
-#pragma unroll
-                        for (int j = 0; j < GT_KSUB; ++j) {
-                            if (j < nsub && is_ragged(w, kb0 + j)) {
-                                mbar_arrive_expect_tx(tail_bar(stage, j), bytes);
-                            } else if (leader) {
-                                if (WGRAD)
-                                    mbar_arrive(full_bar(stage, j));
-                                if (j < nsub)
-                                    mbar_arrive_expect_tx(full_bar(stage, j), 2 * bytes);
-                                else
-                                    mbar_arrive(full_bar(stage, j));  // unused: complete its phase
-                            }
+                        if (tail) {
+                            mbar_arrive_expect_tx(tail_bar(stage), bytes);
+                        } else if (leader) {
+                            if (WGRAD)
+                                mbar_arrive(full_bar(stage));
+                            mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
                         }
-#pragma unroll
-                        for (int j = 0; j < GT_KSUB; ++j) {
-                            if (j >= nsub)
-                                break;
-                            const int kb = kb0 + j;
-                            const uint32_t bar = is_ragged(w, kb) ? mapa_shared(tail_bar(stage, j), rank)
-                                                                  : mapa_shared(full_bar(stage, j), 0);
-                            const uint32_t dA = sA + (stage * GT_KSUB + j) * L::SUB;
-                            const uint32_t dB = sB + (stage * GT_KSUB + j) * L::SUB;
-                            if constexpr (WGRAD) {
-                                const int row = w.row0 + kb * TC_BK;
-#pragma unroll
-                                for (int b = 0; b < 2; ++b)
-                                    tma_load_2d_pair(dA + b * 8192, &tmA, bar, f + 64 * b, row);
-                                tma_load_2d_pair(dB, &tmB, bar, c, row);
-                                if (half > 64)
-                                    tma_load_2d_pair(dB + 8192, &tmB, bar, c + 64, row);
+                        const uint32_t bar = tail ? mapa_shared(tail_bar(stage), rank)
+                                                  : mapa_shared(full_bar(stage), 0);
+                        const uint32_t dA = sbase + stage * stage_bytes, dB = dA + GT_A_BYTES;
+                        if constexpr (WGRAD) {
+                            const int row = w.row0 + kb * TC_BK;
+                            tma_load_2d_pair(dA, &tmA, bar, f, row);
+                            tma_load_2d_pair(dA + 8192, &tmA, bar, f + 64, row);
+                            tma_load_2d_pair(dB, &tmB, bar, c, row);
+                            if (half > 64)
+                                tma_load_2d_pair(dB + 8192, &tmB, bar, c + 64, row);
+                        } else {
+                            const int k = kb * TC_BK;
+                            auto weights = [&](uint32_t dst, int x, int y) {
+                                tma_load_3d_pair(dst, &tmA, bar, x, p.swap ? z : y, p.swap ? y : z);
+                            };
+                            if (A_MN) {
+                                weights(dA, f, k);
+                                weights(dA + 8192, f + 64, k);
                             } else {
-                                const int k = kb * TC_BK;
-                                auto weights = [&](uint32_t dst, int x, int y) {
-                                    tma_load_3d_pair(dst, &tmA, bar, x, p.swap ? z : y, p.swap ? y : z);
-                                };
-                                if (A_MN) {
-                                    weights(dA, f, k);
-                                    weights(dA + 8192, f + 64, k);
-                                } else {
-                                    weights(dA, k, f);
+                                weights(dA, k, f);
+                            }
+                            // the tile's rows in boxes of 128, 64, 32 and 16
+                            if (half == 128) {
+                                tma_load_2d_pair(dB, &tmB, bar, k, c);
+                            } else {
+                                int b = 0;
+                                if (half & 64) {
+                                    tma_load_2d_pair(dB, &tmB64, bar, k, c);
+                                    b = 64;
                                 }
-                                // the tile's rows in boxes of 128, 64, 32 and 16
-                                if (half == 128) {
-                                    tma_load_2d_pair(dB, &tmB, bar, k, c);
-                                } else {
-                                    int b = 0;
-                                    if (half & 64) {
-                                        tma_load_2d_pair(dB, &tmB64, bar, k, c);
-                                        b = 64;
-                                    }
-                                    if (half & 32) {
-                                        tma_load_2d_pair(dB + b * 128, &tmB32, bar, k, c + b);
-                                        b += 32;
-                                    }
-                                    if (half & 16)
-                                        tma_load_2d_pair(dB + b * 128, &tmB16, bar, k, c + b);
+                                if (half & 32) {
+                                    tma_load_2d_pair(dB + b * 128, &tmB32, bar, k, c + b);
+                                    b += 32;
                                 }
+                                if (half & 16)
+                                    tma_load_2d_pair(dB + b * 128, &tmB16, bar, k, c + b);
                             }
                         }
                     }
                     __syncwarp();
-#pragma unroll
-                    for (int s = 0; s < GT_STAGES; ++s) {  // (registers: no indexing)
-                        issued[s] += s == stage;
-#pragma unroll
-                        for (int j = 0; j < GT_KSUB; ++j)
-                            ragged[s * GT_KSUB + j] += s == stage && j < nsub && is_ragged(w, kb0 + j);
+                    if (tail) {
+                        ragged |= 1u << stage;
+                        ragged_parity ^= 1u << stage;
                     }
                 }
-                if (++stage == GT_STAGES) {
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1;
                 }
@@ -396,25 +330,22 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         if (!ok && lane == 0) {
             // Wait (bounded) for the loads already issued before shared
             // memory goes away: the leader's barriers cover both CTAs.
-            auto drain = [&](uint32_t bar, int uses) {
+            auto drain = [&](uint32_t bar, uint32_t parity) {
                 const long long t0 = clock64();
-                while (!mbar_try_wait(bar, static_cast<uint32_t>(uses - 1) & 1u) &&
-                       clock64() - t0 < p.wait_budget) {
+                while (!mbar_try_wait(bar, parity) && clock64() - t0 < p.wait_budget) {
                 }
             };
-            for (int s = 0; s < GT_STAGES; ++s)
-                for (int j = 0; j < GT_KSUB; ++j) {
-                    if (leader && issued[s] > 0)
-                        drain(full_bar(s, j), issued[s]);
-                    if (WGRAD && ragged[s * GT_KSUB + j] > 0)
-                        drain(tail_bar(s, j), ragged[s * GT_KSUB + j]);
-                }
+            for (int s = 0; s < stages; ++s) {
+                const int uses = steps / stages + (s < steps % stages);
+                if (leader && uses > 0)
+                    drain(full_bar(s), (uses - 1) & 1);
+                if (WGRAD && ((ragged >> s) & 1))
+                    drain(tail_bar(s), ((ragged_parity >> s) & 1) ^ 1);
+            }
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
         if (leader) {
-            const uint32_t sA = sbase + L::OFF_A;
-            const uint32_t sB = sbase + L::OFF_B;
             int stage = 0;
             uint32_t phase = 0;
             int local = 0;
@@ -432,42 +363,31 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * GT_N);
                 const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
-                for (int kb0 = 0; kb0 < w.k_blocks; kb0 += GT_KSUB) {
-                    const int nsub = min(GT_KSUB, w.k_blocks - kb0);
-#pragma unroll
-                    for (int j = 0; j < GT_KSUB; ++j) {
-                        if (j >= nsub)
-                            break;
-                        ok = warp_wait<WGRAD>(full_bar(stage, j), phase, watch);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        const uint32_t a0 = sA + (stage * GT_KSUB + j) * L::SUB;
-                        const uint32_t b0 = sB + (stage * GT_KSUB + j) * L::SUB;
-                        // 16-deep instructions; gradient: as many as there are rows
-                        const int deep = WGRAD ? min(4, (w.rows - (kb0 + j) * TC_BK + 15) / 16) : 4;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < TC_BK / TC_UMMA_K; ++k) {
-                                if (WGRAD && k >= deep)
-                                    break;
-                                const uint64_t adesc = A_MN ? smem_desc_sw128(a0 + k * 2048, 8192, 1024)
-                                                            : smem_desc_sw128(a0 + k * 32, 16, 1024);
-                                const uint64_t bdesc = WGRAD ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                                             : smem_desc_sw128(b0 + k * 32, 16, 1024);
-                                tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, kb0 != 0 || j != 0 || k != 0);
-                            }
-                            if (j == nsub - 1) {
-                                tc_commit_pair(empty_bar(stage), 0x3);
-                                if (kb0 + GT_KSUB >= w.k_blocks)
-                                    tc_commit_pair(tfull_bar(acc), 0x3);
-                            }
-                        }
-                        __syncwarp();
-                    }
+                for (int kb = 0; kb < w.k_blocks; ++kb) {
+                    ok = warp_wait<WGRAD>(full_bar(stage), phase, watch);
                     if (!ok)
                         break;
-                    if (++stage == GT_STAGES) {
+                    tc_fence_after();
+                    const uint32_t a0 = sbase + stage * stage_bytes, b0 = a0 + GT_A_BYTES;
+                    // 16-deep instructions; gradient: as many as there are rows
+                    const int deep = WGRAD ? min(4, (w.rows - kb * TC_BK + 15) / 16) : 4;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < TC_BK / TC_UMMA_K; ++k) {
+                            if (WGRAD && k >= deep)
+                                break;
+                            const uint64_t adesc = A_MN ? smem_desc_sw128(a0 + k * 2048, 8192, 1024)
+                                                        : smem_desc_sw128(a0 + k * 32, 16, 1024);
+                            const uint64_t bdesc = WGRAD ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                         : smem_desc_sw128(b0 + k * 32, 16, 1024);
+                            tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, kb != 0 || k != 0);
+                        }
+                        tc_commit_pair(empty_bar(stage), 0x3);
+                        if (kb == w.k_blocks - 1)
+                            tc_commit_pair(tfull_bar(acc), 0x3);
+                    }
+                    __syncwarp();
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1;
                     }
@@ -493,6 +413,7 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                            static_cast<int64_t>(blockIdx.x) * 128 + (threadIdx.x - 64),
                            static_cast<int64_t>(gridDim.x) * 128);
         int local = 0;
+        uint32_t buffer = 0;
         for (int t = unit; t < num_work; t += num_units) {
             const GroupedWork w = grouped_work<MODE>(t, table, p);
             const int acc = local & 1;
@@ -510,75 +431,63 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
             const int f = w.f0 + static_cast<int>(rank) * TC_BM + q * 32;
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * GT_N);
+            const uint32_t staging = sbase + L::OFF_STAGING + q * L::STAGING;
             if constexpr (WGRAD) {
-                const uint32_t staging = sbase + L::OFF_STAGING + q * TC_STAGING_BYTES;
-                if (any && p.tma_out) {
-                    constexpr int STRIP = TcOut<OutT>::STRIP;
-                    TcParams scale{};
-                    scale.alpha = p.alpha;
+                const int row = f + static_cast<int>(lane);
+                OutT* c = out + w.g * p.stride_c + row * p.ldc + w.c0;
+                if (p.tma_out) {
+                    // strips of 64 bytes, through two buffers in turn
+                    constexpr int STRIP = 64 / sizeof(OutT);
+                    if (f < p.N)
 #pragma unroll 1
-                    for (int s = 0; s < w.n / STRIP; ++s) {
-                        const int col = w.c0 + s * STRIP;
-                        if (f >= p.N || col >= p.K)
-                            break;
-                        if (lane == 0)
-                            bulk_wait_group_read<0>();
-                        __syncwarp();
-                        tc_strip_to_smem<OutT>(t_row + s * STRIP, staging, lane, scale, 0, 0);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_3d(&tmC, staging, col, f, w.g);
-                            bulk_commit_group();
+                        for (int s = 0; s < w.count; s += STRIP) {
+                            buffer ^= 2048;
+                            if (lane == 0)
+                                bulk_wait_group_read<1>();
+                            __syncwarp();
+                            strip_to_smem<OutT>(t_row + s, any, staging + buffer, p.alpha);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_3d(&tmC, staging + buffer, w.c0 + s, f, w.g);
+                                bulk_commit_group();
+                            }
                         }
-                    }
-                } else if (p.tma_out) {
-                    // no rows: one strip of zeros, stored again and again
-                    if (lane == 0)
-                        bulk_wait_group_read<0>();
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        st_shared_v4(staging + lane * 128 + i * 16, 0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && f < p.N) {
-                        for (int col = w.c0; col < min(p.K, w.c0 + GT_N); col += TcOut<OutT>::STRIP)
-                            tma_store_3d(&tmC, staging, col, f, w.g);
-                        bulk_commit_group();
-                    }
-                } else {
-                    if (lane == 0)
-                        bulk_wait_group_read<0>();
-                    __syncwarp();
+                } else
 #pragma unroll 1
-                    for (int s = 0; s < w.count; s += 32) {
-                        uint32_t v[32] = {};
-                        if (any) {
-                            tmem_ld_32x32b_x32(t_row + s, v);
-                            tmem_wait_ld(v);
-                        }
-                        if (f < p.N)
-                            grouped_strip(v, staging, lane,
-                                          out + w.g * p.stride_c + f * p.ldc + w.c0 + s, p.ldc,
-                                          min(32, p.N - f), w.count - s, p);
+                for (int s = 0; s < w.count; s += 32) {
+                    uint32_t v[32] = {};
+                    if (any) {
+                        tmem_ld_32x32b_x32(t_row + s, v);
+                        tmem_wait_ld(v);
+                    }
+                    if (p.unit) {
+                        if (row < p.N)
+                            put_row(c + s, v, w.count - s, p.unit, p.alpha, p.beta);
+                    } else if (f < p.N) {
+                        put_strip(v, staging, c - lane * p.ldc + s, p.ldc, min(32, p.N - f), w.count - s,
+                                  p.alpha, p.beta);
                     }
                 }
             } else {
-                const bool mine = f + static_cast<int>(lane) < p.N;
-                OutT* c = out + w.c0 * p.ldc + f + lane;
+                OutT* c = out + w.c0 * p.ldc + f;
 #pragma unroll 1
                 for (int s = 0; s < w.count; s += 32, c += 32 * p.ldc) {
+                    if constexpr (sizeof(OutT) == 2) {
+                        if (p.unit && p.beta == 0.0f) {
+                            put_turned(t_row + s, staging, c, p.ldc, w.count - s, p.N - f, p.alpha);
+                            continue;
+                        }
+                    }
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(t_row + s, v);
                     tmem_wait_ld(v);
-                    const int rows = w.count - s;
-                    if (mine) {
+                    if (f + static_cast<int>(lane) < p.N) {
                         float x[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             x[j] = __uint_as_float(v[j]);
-                        grouped_put(c, p.ldc, rows, x, p);
+                        put_column(c + lane, p.ldc, w.count - s, x, p.alpha, p.beta);
                     }
                 }
             }
@@ -601,31 +510,25 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
             if (w.k_blocks == 0)
                 continue;
             const int last = w.k_blocks - 1;
-            const int s = (stage + last / GT_KSUB) % GT_STAGES, j = last % GT_KSUB;
-            stage = (s + 1) % GT_STAGES;
+            const int s = (stage + last) % stages;
+            stage = (s + 1) % stages;
             if (!is_ragged(w, last))
                 continue;
-            const int step = s * GT_KSUB + j;
-            int ok = 1;
-            if (lane == 0)
-                ok = tc_wait(tail_bar(s, j), (parity >> step) & 1, watch) ? 1 : 0;
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok)
+            if (!warp_wait(tail_bar(s), (parity >> s) & 1, watch))
                 break;
-            parity ^= 1u << step;
+            parity ^= 1u << s;
             // a row of 64 values is 128 contiguous bytes (its swizzle stays within)
             const int from = w.rows - last * TC_BK, to = (from + 15) / 16 * 16;
             const int boxes = 2 + w.n / 128;
-            for (int b = 0; b < boxes; ++b) {
-                const uint32_t box = sbase + (b < 2 ? L::OFF_A + b * 8192 : L::OFF_B + (b - 2) * 8192) +
-                                     step * L::SUB;
+            for (int b = 0; b < boxes; ++b) {  // (A's two boxes, then B's)
+                const uint32_t box = sbase + s * stage_bytes + b * 8192;
                 for (int i = from * 8 + static_cast<int>(lane); i < to * 8; i += 32)
                     st_shared_v4(box + i * 16, 0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_cluster(mapa_shared(full_bar(s, j), 0));
+                mbar_arrive_cluster(mapa_shared(full_bar(s), 0));
         }
     }
 

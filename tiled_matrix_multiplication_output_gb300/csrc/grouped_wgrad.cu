@@ -26,11 +26,12 @@ cudaError_t grouped_wgrad_tc_launch(const GroupedWgradLaunch& l, cudaStream_t st
         !encode_map(&m.b, l.in_dtype, l.X, 2, {l.K, rows, 1}, {l.ldx, 0}, {64, TC_BK, 1}))
         return cudaErrorNotSupported;
     m.b64 = m.b32 = m.b16 = m.c = m.b;
+    const int64_t size = type_bytes(l.out_dtype);
+    p.unit = row_unit(l.C, l.ldc * size, groups > 1 ? l.stride_c * size : 0);
     const int64_t stride = groups > 1 ? l.stride_c : l.N * l.ldc;
-    p.tma_out = l.beta == 0.0f && aligned_rows(l.C, l.ldc, l.out_dtype) &&
-                (groups == 1 || (stride * type_bytes(l.out_dtype)) % 16 == 0) &&
+    p.tma_out = l.beta == 0.0f && p.unit != 0 &&
                 encode_map(&m.c, l.out_dtype, l.C, 3, {l.K, l.N, groups}, {l.ldc, stride},
-                           {128u / type_bytes(l.out_dtype), 32, 1});
+                           {static_cast<uint32_t>(64 / size), 32, 1});
     const int64_t most = groups * p.tiles_f * p.tiles_c;
     return launch_grouped_tc<GROUPED_WGRAD>(l.out_dtype, m, p, most, l.num_sms, stream);
 }

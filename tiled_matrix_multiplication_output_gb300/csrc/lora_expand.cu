@@ -12,8 +12,10 @@
 // waits for them only when the first tile's shared product has been issued.
 #include <algorithm>
 
-#include "grouped_launch.cuh"
+#include "grouped_maps.h"
 #include "lora_tc.cuh"
+#include "persistent.cuh"
+#include "store_rows.cuh"
 
 namespace tmmo {
 namespace {
@@ -31,7 +33,7 @@ struct ExpandParams {
     const LoraPlan* plan;
     void* C;
     int64_t ldc;
-    bool tma_out;
+    int unit;             // row_unit of the output
     uint32_t idesc;       // with N = 0
     int* status;
     long long wait_budget;
@@ -44,7 +46,7 @@ struct ExpandLayout {
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = STEPS * SUB;
     static constexpr int OFF_STAGING = OFF_B + STEPS * SUB;
-    static constexpr int OFF_BAR = OFF_STAGING + 4 * 2 * TC_STAGING_BYTES;
+    static constexpr int OFF_BAR = OFF_STAGING + 4 * 4096;
     static constexpr int NUM_BARS = STEPS + LE_STAGES + 5;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
     static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
@@ -122,8 +124,8 @@ template <bool ACROSS, typename OutT>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     lora_expand_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmE,
-                       const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmW64,
-                       const __grid_constant__ CUtensorMap tmE64, const __grid_constant__ ExpandParams p)
+                       const __grid_constant__ CUtensorMap tmW64, const __grid_constant__ CUtensorMap tmE64,
+                       const __grid_constant__ ExpandParams p)
 {
     using L = ExpandLayout;
     extern __shared__ uint8_t smem_raw[];
@@ -163,7 +165,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmT);
         tma_prefetch_desc(&tmE);
-        tma_prefetch_desc(&tmC);
     }
     if (warp == 1) {
         tmem_alloc<2>(smem_u32(tmem_slot), 512);
@@ -382,16 +383,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     } else {
         // ------------------------------------------------ epilogue
         const int q = warp & 3;  // TMEM lane quarter this warp may access
-        const uint32_t staging0 = sbase + L::OFF_STAGING + q * 2 * TC_STAGING_BYTES;
+        const uint32_t staging = sbase + L::OFF_STAGING + q * 4096;
         const uint32_t leader_tempty0 = mapa_shared(tempty_bar(0), 0);
         const uint32_t leader_tempty1 = mapa_shared(tempty_bar(1), 0);
         OutT* const out = static_cast<OutT*>(p.C);
-        TcParams plain{};
-        plain.alpha = 1.0f;
-        GroupedTcParams store{};
-        store.alpha = 1.0f;
         int local = 0;
-        uint32_t buf = 0;
         for (int t = unit; t < p.items; t += num_units, ++local) {
             const Item w = item(t, p);
             const int acc = local & 1;
@@ -406,41 +402,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * 256);
             const int cols = min(w.n, p.N - w.col);
-            if (row < p.M && p.tma_out) {
-                constexpr int STRIP = TcOut<OutT>::STRIP;
-#pragma unroll 1
-                for (int s = 0; s < cols; s += STRIP) {
-                    const uint32_t stg = staging0 + buf * TC_STAGING_BYTES;
-                    if (lane == 0)
-                        bulk_wait_group_read<1>();
-                    __syncwarp();
-                    tc_strip_to_smem<OutT>(t_row + s, stg, lane, plain, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tmC, stg, w.col + s, row);
-                        bulk_commit_group();
-                    }
-                    buf ^= 1;
-                }
-            } else if (row < p.M) {
+            OutT* c = out + row * p.ldc + w.col;
+            if (row < p.M)
 #pragma unroll 1
                 for (int s = 0; s < cols; s += 32) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(t_row + s, v);
                     tmem_wait_ld(v);
-                    grouped_strip(v, staging0, lane, out + row * p.ldc + w.col + s, p.ldc,
-                                  min(32, p.M - row), cols - s, store);
+                    if (!p.unit)
+                        put_strip(v, staging, c + s, p.ldc, min(32, p.M - row), cols - s, 1.0f, 0.0f);
+                    else if (row + static_cast<int>(lane) < p.M)
+                        put_row(c + lane * p.ldc + s, v, cols - s, p.unit, 1.0f, 0.0f);
                 }
-            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive_cluster(acc ? leader_tempty1 : leader_tempty0);
         }
-        if (lane == 0)
-            bulk_wait_group_read<0>();
-        __syncwarp();
     }
 
     // ---------------------------------------------------- teardown
@@ -457,7 +435,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 }
 
 template <bool ACROSS, typename OutT>
-cudaError_t launch(const CUtensorMap (&m)[7], ExpandParams& p, int num_sms, cudaStream_t stream)
+cudaError_t launch(const CUtensorMap (&m)[6], ExpandParams& p, int num_sms, cudaStream_t stream)
 {
     using L = ExpandLayout;
     static ClusterCaps caps;
@@ -473,11 +451,11 @@ cudaError_t launch(const CUtensorMap (&m)[7], ExpandParams& p, int num_sms, cuda
     p.items = p.whole + 2 * (tiles - p.whole);
     const int units = std::min(pairs, p.items);
     ClusterLaunch l(static_cast<unsigned>(2 * units), 2, TC_THREADS, L::SMEM_ALLOC, stream, p.adapters);
-    return l.run(lora_expand_kernel<ACROSS, OutT>, m[0], m[1], m[2], m[3], m[4], m[5], m[6], p);
+    return l.run(lora_expand_kernel<ACROSS, OutT>, m[0], m[1], m[2], m[3], m[4], m[5], p);
 }
 
 template <bool ACROSS>
-cudaError_t launch(int out_dtype, const CUtensorMap (&m)[7], ExpandParams& p, int num_sms,
+cudaError_t launch(int out_dtype, const CUtensorMap (&m)[6], ExpandParams& p, int num_sms,
                    cudaStream_t stream)
 {
     switch (out_dtype) {
@@ -515,7 +493,7 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     p.status = l.status;
     p.wait_budget = l.wait_budget;
     p.fault_skip_kblock = l.fault_skip_kblock;
-    CUtensorMap m[7];
+    CUtensorMap m[6];
     const int dt = l.in_dtype;
     auto weights = [&](CUtensorMap* map, uint32_t outputs) {
         return l.across ? encode_map(map, dt, l.W, 2, {l.N, l.K, 1}, {l.ldw, 0}, {64, TC_BK, 1})
@@ -527,16 +505,14 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
                         : encode_map(map, dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride}, {64, outputs, 1});
     };
     bool ok = encode_map(&m[0], dt, l.X, 2, {l.K, l.rows, 1}, {l.ldx, 0}, {64, TC_BM, 1}) &&
-              weights(&m[1], TC_BM) && weights(&m[5], 64);
-    m[2] = m[3] = m[4] = m[6] = m[0];
+              weights(&m[1], TC_BM) && weights(&m[4], 64);
+    m[2] = m[3] = m[5] = m[0];
     if (ok && p.adapters)
         ok = encode_map(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, TC_BM, 1}) &&
-             factors(&m[3], TC_BM) && factors(&m[6], 64);
+             factors(&m[3], TC_BM) && factors(&m[5], 64);
     if (!ok)
         return cudaErrorNotSupported;
-    p.tma_out = aligned_rows(l.Y, l.ldy, l.out_dtype) &&
-                encode_map(&m[4], l.out_dtype, l.Y, 2, {l.N, l.rows, 1}, {l.ldy, 0},
-                           {128u / type_bytes(l.out_dtype), 32, 1});
+    p.unit = row_unit(l.Y, l.ldy * type_bytes(l.out_dtype), 0);
     return l.across ? launch<true>(l.out_dtype, m, p, l.num_sms, stream)
                     : launch<false>(l.out_dtype, m, p, l.num_sms, stream);
 }

@@ -1,0 +1,224 @@
+// From an accumulator in tensor memory to rows in global memory, for tiles of
+// any extent.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "ops.cuh"
+#include "simt_tile.cuh"
+
+namespace tmmo {
+
+// p[r * ld] = alpha * v[r] + beta * p[r * ld] for r < rows: what is added to is
+// loaded before anything is stored, so that the loads overlap.
+template <int R, typename OutT>
+__device__ __forceinline__ void put_column(OutT* p, int64_t ld, int rows, const float (&v)[R], float alpha,
+                                           float beta)
+{
+    float old[R];
+    if (beta != 0.0f) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            old[r] = r < rows ? to_f32(p[r * ld]) : 0.0f;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (r < rows)
+            put(p + r * ld, beta != 0.0f ? fmaf(beta, old[r], alpha * v[r]) : alpha * v[r]);
+}
+
+// Strip of 32 rows x 32 FP32 values (this thread holds a row) to C, through 4 KiB
+// of shared memory, in whole lines whatever the alignment.  A whole warp calls it.
+template <typename OutT>
+__device__ __forceinline__ void put_strip(const uint32_t (&v)[32], uint32_t staging, OutT* c, int64_t ldc,
+                                          int rows, int cols, float alpha, float beta)
+{
+    const uint32_t lane = lane_id();
+    const uint32_t at = staging + lane * 128;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)  // column j of row `lane` at j ^ lane: no bank conflicts
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + ((j ^ lane) << 2)), "r"(v[j]) : "memory");
+    __syncwarp();
+    if (static_cast<int>(lane) < cols)
+#pragma unroll 1
+        for (int r = 0; r < rows; r += 8) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                f[i] = ld_shared_f32(staging + (r + i) * 128 + ((lane ^ (r + i)) << 2));
+            put_column(c + r * ldc + lane, ldc, rows - r, f, alpha, beta);
+        }
+    __syncwarp();
+}
+
+// The widest stores that rows allow: 32 or 16 bytes, or 0 for single values.
+inline int row_unit(const void* p, int64_t row_bytes, int64_t matrix_bytes)
+{
+    const uintptr_t low = (reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(row_bytes) |
+                           static_cast<uintptr_t>(matrix_bytes)) & 31u;
+    return low == 0 ? 32 : low == 16 ? 16 : 0;
+}
+
+// p[0 .. n) = alpha * v + beta * p of a row on a boundary of `unit` bytes, at most 32
+// values: each thread its own row.
+template <typename OutT>
+__device__ __forceinline__ void put_row(OutT* p, const uint32_t (&v)[32], int n, int unit, float alpha,
+                                        float beta)
+{
+    constexpr int EACH = 32 / sizeof(OutT);  // values of a store
+#pragma unroll
+    for (int i = 0; i < 32; i += EACH) {
+        if (i + EACH <= n) {
+            alignas(16) OutT h[EACH];
+            uint4 q[2];
+            if (beta != 0.0f) {
+                q[0] = reinterpret_cast<const uint4*>(p + i)[0];
+                q[1] = reinterpret_cast<const uint4*>(p + i)[1];
+                memcpy(h, q, 32);
+            }
+#pragma unroll
+            for (int k = 0; k < EACH; ++k) {
+                const float f = alpha * __uint_as_float(v[i + k]);
+                put(&h[k], beta != 0.0f ? fmaf(beta, to_f32(h[k]), f) : f);
+            }
+            if (unit == 32) {
+                uint32_t w[8];
+                memcpy(w, h, 32);
+                st_global_v8(p + i, w);
+            } else {
+                memcpy(q, h, 32);
+                reinterpret_cast<uint4*>(p + i)[0] = q[0];
+                reinterpret_cast<uint4*>(p + i)[1] = q[1];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+                if (i + k < n) {
+                    const float f = alpha * __uint_as_float(v[i + k]);
+                    put(p + i + k, beta != 0.0f ? fmaf(beta, to_f32(p[i + k]), f) : f);
+                }
+        }
+    }
+}
+
+// 32 lanes x 64 bytes of columns at taddr (zeros where there are no sums) to shared
+// memory as a TMA store of such boxes expects it, 64-byte swizzled: 16-byte unit u
+// of row r at u ^ (r / 2) % 4.  A whole warp calls it.
+template <typename OutT>
+__device__ __forceinline__ void strip_to_smem(uint32_t taddr, bool any, uint32_t to, float alpha)
+{
+    const uint32_t lane = lane_id(), turn = (lane >> 1) & 3;
+    if constexpr (sizeof(OutT) == 4) {
+        uint32_t v[16] = {};
+        if (any) {
+            tmem_ld_32x32b_x16(taddr, v);
+            tmem_wait_ld(v);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = __float_as_uint(alpha * __uint_as_float(v[4 * u + i]));
+            st_shared_v4(to + lane * 64 + ((u ^ turn) << 4), w[0], w[1], w[2], w[3]);
+        }
+    } else {
+        uint32_t v[32] = {};
+        if (any) {
+            tmem_ld_32x32b_x32(taddr, v);
+            tmem_wait_ld(v);
+        }
+        OutT* tag = nullptr;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = pack2(alpha * __uint_as_float(v[8 * u + 2 * i]),
+                             alpha * __uint_as_float(v[8 * u + 2 * i + 1]), tag);
+            st_shared_v4(to + lane * 64 + ((u ^ turn) << 4), w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// ------------------------------------------- tiles that are stored turned
+
+// 16 lanes x 32 columns of 32 bits in the layout of a matrix fragment: for each
+// eight columns 8 i, r[4 i] and r[4 i + 1] are lane l / 4, columns
+// 8 i + 2 (l % 4) and the next one; r[4 i + 2], r[4 i + 3] the same of lane l / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed: lane 8 m + j gives the address
+// of the 16 bytes of column j of matrix m.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+                 "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// 32 lanes x 32 columns of the accumulator at taddr as 32 rows (the columns) of
+// 32 16-bit values (the lanes) to y, through 2 KiB of shared memory; rows of y are on
+// 16-byte boundaries.  n rows and m values of each exist.  A whole warp calls it.
+template <typename OutT>
+__device__ __forceinline__ void put_turned(uint32_t taddr, uint32_t staging, OutT* y, int64_t ldy, int n, int m,
+                                           float alpha)
+{
+    const uint32_t lane = lane_id();
+    uint32_t r[2][16];
+    tmem_ld_16x256b_x4(taddr, r[0]);
+    tmem_ld_16x256b_x4(taddr + (16u << 16), r[1]);
+    tmem_wait_ld(r[0]);
+    tmem_wait_ld(r[1]);
+    OutT* tag = nullptr;
+    // 16-byte unit u of row t at u ^ (t / 2) % 4: no bank conflicts either way
+    const uint32_t at = staging + lane * 64, turn = (lane >> 1) & 3;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {  // eight lanes of the accumulator
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = 4 * i + 2 * (u & 1);
+            w[i] = pack2(alpha * __uint_as_float(r[u >> 1][k]), alpha * __uint_as_float(r[u >> 1][k + 1]), tag);
+        }
+        stmatrix_x4_trans(at + ((u ^ turn) << 4), w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    const int u = lane & 3, left = m - 8 * u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 8 * i + static_cast<int>(lane >> 2);
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(staging + t * 64 + ((u ^ ((t >> 1) & 3)) << 4))
+                     : "memory");
+        OutT* p = y + t * ldy + 8 * u;
+        if (t < n && left >= 8) {
+            *reinterpret_cast<uint4*>(p) = v;
+        } else if (t < n) {
+            OutT h[8];
+            memcpy(h, &v, 16);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < left)
+                    p[k] = h[k];
+        }
+    }
+    __syncwarp();
+}
+
+}  // namespace tmmo

@@ -1,4 +1,4 @@
-// The wait of roles that run on whole warps.
+// The wait of roles that run on whole warps, and copies of 3-D boxes.
 #pragma once
 
 #include "ops.cuh"
@@ -27,6 +27,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const T
         if (__any_sync(0xffffffffu, late || *w.abort_flag))
             return false;
     }
+}
+
+
+// tma_load_2d_pair of a 3-D box.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                 int32_t x, int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
 }
 
 }  // namespace tmmo
