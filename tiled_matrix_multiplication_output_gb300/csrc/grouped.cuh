@@ -53,15 +53,6 @@ __device__ __forceinline__ int warp_sum_scan(int v, int before)
     return v + before;
 }
 
-// Tiles of at most `rows` rows in the lane's share of the groups.
-__device__ __forceinline__ int lane_tiles(const GroupTable& t, int groups, int rows)
-{
-    int sum = 0;
-    for (int g = threadIdx.x & 31; g < groups; g += 32)
-        sum += (t.first[g + 1] - t.first[g] + rows - 1) / rows;
-    return sum;
-}
-
 // Builds the table; every thread of the block calls it, and it ends in a block
 // barrier.  Offsets are taken as the largest of those up to them, within
 // [0, rows]: whatever they hold, groups neither overlap nor leave the matrix.

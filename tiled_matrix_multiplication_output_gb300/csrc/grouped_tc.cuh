@@ -131,19 +131,26 @@ __device__ __forceinline__ GroupedWork grouped_work(int t, const GroupTable& tab
 __device__ __forceinline__ int tile_rows(const GroupTable& table, int groups, int tiles, int tiles_f,
                                          int pairs, int* largest)
 {
-    int best = GT_N, least = 0;
-#pragma unroll 1
-    for (int rows = GT_N; rows >= 128; rows -= 32) {
-        if (rows != GT_N)
-            tiles = __reduce_add_sync(0xffffffffu, lane_tiles(table, groups, rows));
-        const int waves = static_cast<int>((static_cast<int64_t>(tiles) * tiles_f + pairs - 1) / pairs);
-        const int time = min(waves, 1 << 18) * (315 + rows * 5 / 4);
-        if (rows == GT_N || time < least) {
-            best = rows;
-            least = time;
+    constexpr int KINDS = 5;  // 256, 224 .. 128 rows
+    int best = GT_N;
+    if (tiles * static_cast<int64_t>(tiles_f) > pairs) {  // (else smaller tiles win nothing)
+        int n[KINDS] = {};
+        for (int g = threadIdx.x; g < groups; g += 32) {
+            const int rows = table.first[g + 1] - table.first[g];
+#pragma unroll
+            for (int k = 0; k < KINDS; ++k)
+                n[k] += (rows + GT_N - 32 * k - 1) / (GT_N - 32 * k);
         }
-        if (waves <= 1)
-            break;  // smaller tiles win nothing
+        float least = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KINDS; ++k) {
+            const float work = static_cast<float>(__reduce_add_sync(0xffffffffu, n[k])) * tiles_f;
+            const float time = ceilf(__fdividef(work, static_cast<float>(pairs))) * (315 + 1.23f * (GT_N - 32 * k));
+            if (k == 0 || time < least) {
+                best = GT_N - 32 * k;
+                least = time;
+            }
+        }
     }
     int most = 0;
     for (int g = threadIdx.x; g < groups; g += 32)
