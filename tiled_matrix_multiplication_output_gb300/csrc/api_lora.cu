@@ -283,7 +283,7 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
         step(need_u, [&] { return lora_shrink_tc_launch(u, db ? &t : nullptr, s); });
         step(!need_u && db, [&] { return lora_shrink_tc_launch(t, nullptr, s); });
         step(dx, [&] { return lora_expand_tc_launch(u, s); });
-        step(da || db, [&] { return lora_grad_tc_launch({da ? &a : nullptr, db ? &b : nullptr}, s); });
+        step(da || db, [&] { return lora_grad_tc_launch({da ? &a : nullptr, db ? &b : nullptr}, dx, s); });
         return status_of(err);
     }
     if (in_dtype != GEMM_F32) {  // sums of nothing: no operand is read

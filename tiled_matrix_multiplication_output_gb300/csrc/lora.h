@@ -76,8 +76,9 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream);
 // The kernel for few output tiles, and whether it is the choice.
 bool lora_small_takes(const LoraLaunch& l);
 cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream);
-// Two gradients of the same rows in one launch (either may be null).
-cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStream_t stream);
+// Two gradients of the same rows in one launch (either may be null); dependent: the
+// launch before is an expand of the same rank values.
+cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool dependent, cudaStream_t stream);
 
 // On the FP32 units: FP32 operands, and sums of nothing.
 cudaError_t lora_simt_shrink(const LoraLaunch& l, cudaStream_t stream);

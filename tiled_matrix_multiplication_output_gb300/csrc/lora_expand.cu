@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             if (p.adapters) {
                 if (!waited) {
                     grid_dep_wait();
+                    grid_dep_launch_dependents();  // the rank values are there for others, too
                     list.begin(p, w.mb);
                 }
                 waited = true;

@@ -4,11 +4,15 @@
 // One tile is 128 columns of P (the lanes) by up to 256 columns of rank values in
 // parts, whose sums are added at the end.  Both operands lie across the
 // contraction, and an adapter's rows lie anywhere: the tile goes through the
-// 64-row blocks that hold any of them, found from the plans.  In a block that
-// holds other rows as well, a warp zeroes those in shared memory, in both
-// operands, before the block counts as loaded; 16-row slices without a row of
-// the adapter are skipped.  Bound: reading P once for each adapter in a block
+// row tiles (128 rows) that hold any of them, found from the plans.  In one that
+// holds other rows as well, two warps zero those in shared memory, in both
+// operands, before it counts as loaded; 16-row slices without a row of the
+// adapter are skipped.  Bound: reading P once for each adapter in a row tile
 // (once in all where sequences are long), the rank values and the launch.
+//
+// Launched as a programmatic dependent of the product that uses the same rank
+// values, of which it needs nothing: it starts where that one's last tiles leave SMs
+// idle.
 #include <algorithm>
 
 #include "grouped_maps.h"
@@ -19,10 +23,11 @@
 namespace tmmo {
 namespace {
 
-constexpr int LG_THREADS = 256;  // warps 0: copies, 1: MMA, 2: zeros, 4-7: epilogue
+constexpr int LG_THREADS = 256;  // warps 0: copies, 1: MMA, 2 and 3: zeros, 4-7: epilogue
 constexpr int LG_MAX_STAGES = 8;
 constexpr int LG_RING = 192 * 1024;  // beside 23 KiB of plans
 constexpr int LG_CHUNKS = 4;     // chunks of rank values in a tile
+constexpr int LG_BOX = LT_ROWS * 128;  // bytes of 64 columns of a row tile
 
 struct GradSide {
     int tiles_c;       // tiles of P's columns
@@ -76,6 +81,7 @@ struct PlanTable {
     int whole;                    // whether they fit
 };
 
+// (From L2: they are another grid's, and this one does not wait for its end.)
 // Every thread of the block calls it; it ends in a block barrier.
 __device__ __forceinline__ void load_plans(PlanTable& t, const GradParams& p)
 {
@@ -83,7 +89,7 @@ __device__ __forceinline__ void load_plans(PlanTable& t, const GradParams& p)
         t.whole = 0;
     if (p.plans <= LG_PLANS) {
         for (int i = threadIdx.x; i < p.plans; i += LG_THREADS)
-            t.first[i + 1] = p.plan[i].count;
+            t.first[i + 1] = __ldcg(&p.plan[i].count);
         __syncthreads();
         if (threadIdx.x < 32) {
             int sum = 0;
@@ -117,45 +123,35 @@ __device__ __forceinline__ void load_plans(PlanTable& t, const GradParams& p)
                         hi = mid;
                 }
                 const LoraPlan& plan = p.plan[lo];
-                t.ids[e] = plan.ids[e - t.first[lo]];
-                t.rows[e] = *reinterpret_cast<const uint4*>(plan.rows[e - t.first[lo]]);
+                t.ids[e] = __ldcg(&plan.ids[e - t.first[lo]]);
+                t.rows[e] = __ldcg(reinterpret_cast<const uint4*>(plan.rows[e - t.first[lo]]));
             }
     }
     __syncthreads();
 }
 
-// The 64-row blocks that hold rows of adapter g, in order; a whole warp steps
-// through them together.
-class RowBlocks {
+// The row tiles that hold rows of adapter g, in order; a whole warp steps through
+// them together.
+class RowTiles {
 public:
-    __device__ RowBlocks(const GradParams& p, const PlanTable& table, int g) : p_(p), table_(table), g_(g) {}
-    // The next block and its rows of g (a bit each); false at the end.
-    __device__ bool next(int& block, uint64_t& rows)
+    __device__ RowTiles(const GradParams& p, const PlanTable& table, int g) : p_(p), table_(table), g_(g) {}
+    // The next tile and its rows of g (a bit each); false at the end.
+    __device__ bool next(int& tile, uint32_t (&rows)[4])
     {
-        for (;;) {
-            while (half_ < 2) {
-                const uint64_t m = half_ == 0 ? lo_ : hi_;
-                block = 2 * tile_ + half_++;
-                if (m != 0) {
-                    rows = m;
-                    return true;
-                }
-            }
-            while (hits_ == 0) {
-                base_ += 32;
-                if (base_ >= p_.plans)
-                    return false;
-                look();
-            }
-            const int src = __ffs(hits_) - 1;
-            hits_ &= hits_ - 1;
-            tile_ = base_ + src;
-            const uint32_t w0 = __shfl_sync(0xffffffffu, mine_.x, src), w1 = __shfl_sync(0xffffffffu, mine_.y, src);
-            const uint32_t w2 = __shfl_sync(0xffffffffu, mine_.z, src), w3 = __shfl_sync(0xffffffffu, mine_.w, src);
-            lo_ = w0 | static_cast<uint64_t>(w1) << 32;
-            hi_ = w2 | static_cast<uint64_t>(w3) << 32;
-            half_ = 0;
+        while (hits_ == 0) {
+            base_ += 32;
+            if (base_ >= p_.plans)
+                return false;
+            look();
         }
+        const int src = __ffs(hits_) - 1;
+        hits_ &= hits_ - 1;
+        tile = base_ + src;
+        rows[0] = __shfl_sync(0xffffffffu, mine_.x, src);
+        rows[1] = __shfl_sync(0xffffffffu, mine_.y, src);
+        rows[2] = __shfl_sync(0xffffffffu, mine_.z, src);
+        rows[3] = __shfl_sync(0xffffffffu, mine_.w, src);
+        return true;
     }
 
 private:
@@ -167,19 +163,20 @@ private:
         if (i < p_.plans) {
             const bool near = table_.whole;
             const int first = near ? table_.first[i] : 0;
-            const int count = near ? table_.first[i + 1] - first : p_.plan[i].count;
-            const int* ids = near ? table_.ids + first : p_.plan[i].ids;
+            const int count = near ? table_.first[i + 1] - first : __ldcg(&p_.plan[i].count);
+            auto id = [&](int e) { return near ? table_.ids[first + e] : __ldcg(&p_.plan[i].ids[e]); };
             int lo = 0, hi = count;  // the first place whose id is not below g
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (ids[mid] < g_)
+                if (id(mid) < g_)
                     lo = mid + 1;
                 else
                     hi = mid;
             }
-            found = lo < count && ids[lo] == g_;
+            found = lo < count && id(lo) == g_;
             if (found)
-                mine_ = near ? table_.rows[first + lo] : *reinterpret_cast<const uint4*>(p_.plan[i].rows[lo]);
+                mine_ = near ? table_.rows[first + lo]
+                             : __ldcg(reinterpret_cast<const uint4*>(p_.plan[i].rows[lo]));
         }
         hits_ = __ballot_sync(0xffffffffu, found);
     }
@@ -187,11 +184,20 @@ private:
     const GradParams& p_;
     const PlanTable& table_;
     const int g_;
-    int base_ = -32, tile_ = 0, half_ = 2;
+    int base_ = -32;
     uint32_t hits_ = 0;
     uint4 mine_ = {};
-    uint64_t lo_ = 0, hi_ = 0;
 };
+
+__device__ __forceinline__ bool all_rows(const uint32_t (&rows)[4])
+{
+    return (rows[0] & rows[1] & rows[2] & rows[3]) == ~0u;
+}
+// Whether slice k (16 rows) has any.
+__device__ __forceinline__ bool has_slice(const uint32_t (&rows)[4], int k)
+{
+    return (rows[k >> 1] & (k & 1 ? 0xffff0000u : 0xffffu)) != 0;
+}
 
 struct GradSmem {
     uint64_t full[LG_MAX_STAGES], landed[LG_MAX_STAGES], empty[LG_MAX_STAGES], tfull[2], tempty[2], drain;
@@ -216,7 +222,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.full[i]), 2);  // (either of the warps that zero)
             mbar_init(smem_u32(&s.landed[i]), 1);
             mbar_init(smem_u32(&s.empty[i]), 1);
         }
@@ -250,22 +256,24 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
             const GradItem w = grad_item(t, p);
-            RowBlocks blocks(p, s.plans, w.g);
-            int block;
-            uint64_t rows;
-            while (ok && blocks.next(block, rows)) {
-                const bool whole = rows == ~0ull;
+            RowTiles tiles(p, s.plans, w.g);
+            int tile;
+            uint32_t rows[4];
+            while (ok && tiles.next(tile, rows)) {
+                const bool whole = all_rows(rows);
                 ok = warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch);
                 if (ok && elect_one()) {
                     const uint32_t bar = smem_u32(whole ? &s.full[stage] : &s.landed[stage]);
-                    const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 16384;
+                    const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 2 * LG_BOX;
                     const CUtensorMap* tmP = w.which ? &tmP1 : &tmP0;
                     const CUtensorMap* tmT = w.which ? &tmT1 : &tmT0;
-                    mbar_arrive_expect_tx(bar, 16384 + w.chunks * 8192);
-                    tma_load_2d(a0, tmP, bar, w.c0, block * 64);
-                    tma_load_2d(a0 + 8192, tmP, bar, w.c0 + 64, block * 64);
+                    if (whole)
+                        mbar_arrive(bar);
+                    mbar_arrive_expect_tx(bar, (2 + w.chunks) * LG_BOX);
+                    tma_load_2d(a0, tmP, bar, w.c0, tile * LT_ROWS);
+                    tma_load_2d(a0 + LG_BOX, tmP, bar, w.c0 + 64, tile * LT_ROWS);
                     for (int c = 0; c < w.chunks; ++c)
-                        tma_load_2d(b0 + c * 8192, tmT, bar, (w.chunk0 + c) * 64, block * 64);
+                        tma_load_2d(b0 + c * LG_BOX, tmT, bar, (w.chunk0 + c) * 64, tile * LT_ROWS);
                 }
                 __syncwarp();
                 if (ok) {
@@ -297,29 +305,29 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
             const GradItem w = grad_item(t, p);
-            RowBlocks blocks(p, s.plans, w.g);
-            int block;
-            uint64_t rows;
+            RowTiles tiles(p, s.plans, w.g);
+            int tile;
+            uint32_t rows[4];
             const int acc = local & 1;
             const uint32_t d = tmem + acc * 256;
             const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
             bool any = false;
-            while (ok && blocks.next(block, rows)) {
+            while (ok && tiles.next(tile, rows)) {
                 if (!any)
                     ok = warp_wait(smem_u32(&s.tempty[acc]), ((local >> 1) & 1) ^ 1, watch);
                 ok = ok && warp_wait(smem_u32(&s.full[stage]), phase, watch);
                 if (!ok)
                     break;
                 tc_fence_after();
-                const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 16384;
+                const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 2 * LG_BOX;
                 if (elect_one()) {
                     bool first = !any;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (((rows >> (16 * k)) & 0xffff) == 0)
+                    for (int k = 0; k < LT_ROWS / TC_UMMA_K; ++k) {
+                        if (!has_slice(rows, k))
                             continue;
-                        tc_mma_f16<1>(d, smem_desc_sw128(a0 + k * 2048, 8192, 1024),
-                                      smem_desc_sw128(b0 + k * 2048, 8192, 1024), idesc, !first);
+                        tc_mma_f16<1>(d, smem_desc_sw128(a0 + k * 2048, LG_BOX, 1024),
+                                      smem_desc_sw128(b0 + k * 2048, LG_BOX, 1024), idesc, !first);
                         first = false;
                     }
                     tc_commit(smem_u32(&s.empty[stage]));
@@ -347,30 +355,32 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             while (!mbar_try_wait(smem_u32(&s.drain), 0) && clock64() - t0 < p.wait_budget) {
             }
         }
-    } else if (warp == 2) {
+    } else if (warp < 4) {
         // ------------------------------------------------ rows of other adapters
+        const int half = warp - 2;  // of the rows
         int stage = 0;
         uint32_t parity = 0;  // a bit for each stage
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
             const GradItem w = grad_item(t, p);
-            RowBlocks blocks(p, s.plans, w.g);
-            int block;
-            uint64_t rows;
-            while (ok && blocks.next(block, rows)) {
-                if (rows != ~0ull) {
+            RowTiles tiles(p, s.plans, w.g);
+            int tile;
+            uint32_t rows[4];
+            while (ok && tiles.next(tile, rows)) {
+                if (!all_rows(rows)) {
                     ok = warp_wait(smem_u32(&s.landed[stage]), (parity >> stage) & 1, watch);
                     if (!ok)
                         break;
                     parity ^= 1u << stage;
-                    // a row is 128 contiguous bytes of each box (its swizzle stays within)
-                    const uint32_t a0 = ring + stage * p.stage_bytes;
-                    for (int i = lane; i < 512; i += 32) {
-                        const int r = i >> 3;
-                        if (((rows >> r) & 1) || ((rows >> (r & 48)) & 0xffff) == 0)
+                    // a row is 128 contiguous bytes of each box (its swizzle stays
+                    // within): a lane takes 16 of them, of one row in four
+#pragma unroll 1
+                    for (int r = 64 * half + (lane >> 3); r < 64 * half + 64; r += 4) {
+                        if (((rows[r >> 5] >> (r & 31)) & 1) || !has_slice(rows, r >> 4))
                             continue;
-                        for (int b = 0; b < 2 + w.chunks; ++b)
-                            st_shared_v4(a0 + b * 8192 + i * 16, 0, 0, 0, 0);
+                        uint32_t at = ring + stage * p.stage_bytes + r * 128 + (lane & 7) * 16;
+                        for (int b = 0; b < 2 + w.chunks; ++b, at += LG_BOX)
+                            st_shared_v4(at, 0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -388,10 +398,10 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         for (int t = blockIdx.x; t < p.items; t += gridDim.x) {
             const GradItem w = grad_item(t, p);
             const GradSide& side = p.side[w.which];
-            RowBlocks blocks(p, s.plans, w.g);
-            int block;
-            uint64_t rows;
-            const bool any = blocks.next(block, rows);
+            RowTiles tiles(p, s.plans, w.g);
+            int tile;
+            uint32_t rows[4];
+            const bool any = tiles.next(tile, rows);
             const int acc = local & 1;
             if (any) {
                 if (!warp_wait(smem_u32(&s.tfull[acc]), (local >> 1) & 1, watch))
@@ -437,6 +447,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
 
     // ---------------------------------------------------- teardown
     __syncwarp();
+    grid_dep_wait();  // this grid must not end before the one it follows
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -445,7 +456,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
 }
 
 template <typename OutT>
-cudaError_t launch(const CUtensorMap (&m)[4], const GradParams& p, int num_sms, cudaStream_t stream)
+cudaError_t launch(const CUtensorMap (&m)[4], const GradParams& p, int num_sms, bool dependent,
+                   cudaStream_t stream)
 {
     static ClusterCaps caps;
     int cap = 0;
@@ -453,13 +465,14 @@ cudaError_t launch(const CUtensorMap (&m)[4], const GradParams& p, int num_sms, 
         cluster_cap(lora_grad_tc_kernel<OutT>, caps, 1, LG_THREADS, LG_RING + 1024, num_sms, &cap);
     if (err != cudaSuccess)
         return err;
-    ClusterLaunch l(static_cast<unsigned>(std::min(p.items, num_sms)), 1, LG_THREADS, LG_RING + 1024, stream);
+    ClusterLaunch l(static_cast<unsigned>(std::min(p.items, num_sms)), 1, LG_THREADS, LG_RING + 1024, stream,
+                    dependent);
     return l.run(lora_grad_tc_kernel<OutT>, m[0], m[1], m[2], m[3], p);
 }
 
 }  // namespace
 
-cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStream_t stream)
+cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool dependent, cudaStream_t stream)
 {
     const LoraGradLaunch& l = sides[0] ? *sides[0] : *sides[1];
     GradParams p{};
@@ -469,7 +482,7 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStr
     p.plan = static_cast<const LoraPlan*>(l.plan);
     p.lay = lora_parts(l.rank, l.parts);
     p.groups_j = (p.lay.chunks + LG_CHUNKS - 1) / LG_CHUNKS;
-    p.stage_bytes = 16384 + 8192 * std::min(p.lay.chunks, LG_CHUNKS);
+    p.stage_bytes = LG_BOX * (2 + std::min(p.lay.chunks, LG_CHUNKS));
     p.stages = std::min(LG_MAX_STAGES, LG_RING / p.stage_bytes);
     p.idesc = tc_idesc(l.in_dtype == DT_BF16, 128, 0, true, true);
     p.status = l.status;
@@ -482,9 +495,9 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStr
         const LoraGradLaunch& s = *sides[i];
         p.side[i] = {(s.cols + 127) / 128, s.cols, s.G, s.step_c, s.step_j, s.stride_g};
         items[i] = static_cast<int64_t>(p.side[i].tiles_c) * p.groups_j * s.adapters;
-        if (!encode_map(&m[2 * i], s.in_dtype, s.P, 2, {s.cols, s.rows, 1}, {s.ldp, 0}, {64, 64, 1}) ||
+        if (!encode_map(&m[2 * i], s.in_dtype, s.P, 2, {s.cols, s.rows, 1}, {s.ldp, 0}, {64, LT_ROWS, 1}) ||
             !encode_map(&m[2 * i + 1], s.in_dtype, s.t, 2, {p.lay.columns(), s.rows, 1},
-                        {p.lay.columns(), 0}, {64, 64, 1}))
+                        {p.lay.columns(), 0}, {64, LT_ROWS, 1}))
             return cudaErrorNotSupported;
     }
     for (int i = 0; i < 2; ++i)
@@ -497,7 +510,7 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], cudaStr
     p.items0 = static_cast<int>(items[0]);
     p.items = static_cast<int>(items[0] + items[1]);
     return with_type(l.out_dtype, [&](auto out) {
-        return launch<decltype(out)>(m, p, l.num_sms, stream);
+        return launch<decltype(out)>(m, p, l.num_sms, dependent, stream);
     });
 }
 

@@ -297,6 +297,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     } else if (warp == 2 && p.adapters) {
         // this CTA's share of the tile's adapters
         grid_dep_wait();
+        grid_dep_launch_dependents();  // the rank values are there for others, too
         const int count = plan.count, mine = count > split ? (count - split + SPLITS - 1) / SPLITS : 0;
         for (int i = lane; i < mine; i += 32) {
             s.ids[i] = plan.ids[split + i * SPLITS];
