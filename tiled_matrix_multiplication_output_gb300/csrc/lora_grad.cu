@@ -25,7 +25,7 @@ namespace {
 
 constexpr int LG_THREADS = 256;  // warps 0: copies, 1: MMA, 2 and 3: zeros, 4-7: epilogue
 constexpr int LG_MAX_STAGES = 8;
-constexpr int LG_RING = 192 * 1024;  // beside 23 KiB of plans
+constexpr int LG_RING = 192 * 1024;  // beside 25 KiB of plans
 constexpr int LG_CHUNKS = 4;     // chunks of rank values in a tile
 constexpr int LG_BOX = LT_ROWS * 128;  // bytes of 64 columns of a row tile
 
@@ -38,7 +38,7 @@ struct GradSide {
 
 struct GradParams {
     GradSide side[2];
-    int items0, items;   // of the first side, of both
+    int per[2], items;   // of an adapter on each side; of all
     int adapters, rank;
     int plans;
     const LoraPlan* plan;
@@ -55,30 +55,18 @@ struct GradItem {
     int n;  // columns of rank values that the tensor core reads
 };
 
-__device__ __forceinline__ GradItem grad_item(int t, const GradParams& p)
-{
-    GradItem w;
-    w.which = t >= p.items0;
-    t -= w.which ? p.items0 : 0;
-    const int per = p.side[w.which].tiles_c * p.groups_j;
-    w.g = t / per;
-    t -= w.g * per;
-    w.c0 = t / p.groups_j * 128;
-    w.chunk0 = t % p.groups_j * LG_CHUNKS;
-    w.chunks = min(LG_CHUNKS, p.lay.chunks - w.chunk0);
-    w.n = (w.chunks - 1) * 64 + p.lay.parts * p.lay.chunk;
-    return w;
-}
-
 // The plans of all row tiles in shared memory, where they fit: every tile of the
 // gradient searches them (about 2 us a tile from global memory, 0.2 from here).
 constexpr int LG_PLANS = 512;     // row tiles
 constexpr int LG_ENTRIES = 1024;  // adapters of all of them
+constexpr int LG_SORTED = 256;    // adapters, at most, that are sorted
 struct PlanTable {
     int first[LG_PLANS + 1];      // entries before each row tile
     int ids[LG_ENTRIES];
     alignas(16) uint4 rows[LG_ENTRIES];
     int whole;                    // whether they fit
+    int sorted;                   // then: the adapters with the most row tiles first
+    int tiles[LG_SORTED], order[LG_SORTED];
 };
 
 // (From L2: they are another grid's, and this one does not wait for its end.)
@@ -86,7 +74,9 @@ struct PlanTable {
 __device__ __forceinline__ void load_plans(PlanTable& t, const GradParams& p)
 {
     if (threadIdx.x == 0)
-        t.whole = 0;
+        t.whole = t.sorted = 0;
+    if (threadIdx.x < LG_SORTED)
+        t.tiles[threadIdx.x] = 0;
     if (p.plans <= LG_PLANS) {
         for (int i = threadIdx.x; i < p.plans; i += LG_THREADS)
             t.first[i + 1] = __ldcg(&p.plan[i].count);
@@ -109,10 +99,11 @@ __device__ __forceinline__ void load_plans(PlanTable& t, const GradParams& p)
             if (threadIdx.x == 0) {
                 t.first[0] = 0;
                 t.whole = sum <= LG_ENTRIES;
+                t.sorted = t.whole && p.adapters <= LG_SORTED;
             }
         }
         __syncthreads();
-        if (t.whole)
+        if (t.whole) {
             for (int e = threadIdx.x; e < t.first[p.plans]; e += LG_THREADS) {
                 int lo = 0, hi = p.plans;  // the tile of entry e
                 while (hi - lo > 1) {
@@ -125,10 +116,38 @@ __device__ __forceinline__ void load_plans(PlanTable& t, const GradParams& p)
                 const LoraPlan& plan = p.plan[lo];
                 t.ids[e] = __ldcg(&plan.ids[e - t.first[lo]]);
                 t.rows[e] = __ldcg(reinterpret_cast<const uint4*>(plan.rows[e - t.first[lo]]));
+                if (t.sorted)
+                    atomicAdd(&t.tiles[t.ids[e]], 1);
             }
+            __syncthreads();
+            if (t.sorted && static_cast<int>(threadIdx.x) < p.adapters) {
+                const int mine = t.tiles[threadIdx.x];
+                int place = 0;
+                for (int g = 0; g < p.adapters; ++g)
+                    place += t.tiles[g] > mine || (t.tiles[g] == mine && g < static_cast<int>(threadIdx.x));
+                t.order[place] = threadIdx.x;
+            }
+        }
     }
     __syncthreads();
 }
+
+// Tile t of the gradients: adapters in the table's order, and of each both sides.
+__device__ __forceinline__ GradItem grad_item(int t, const GradParams& p, const PlanTable& table)
+{
+    GradItem w;
+    const int per = p.per[0] + p.per[1], place = t / per;
+    t -= place * per;
+    w.g = table.sorted ? table.order[place] : place;
+    w.which = t >= p.per[0];
+    t -= w.which ? p.per[0] : 0;
+    w.c0 = t / p.groups_j * 128;
+    w.chunk0 = t % p.groups_j * LG_CHUNKS;
+    w.chunks = min(LG_CHUNKS, p.lay.chunks - w.chunk0);
+    w.n = (w.chunks - 1) * 64 + p.lay.parts * p.lay.chunk;
+    return w;
+}
+
 
 // The row tiles that hold rows of adapter g, in order; a whole warp steps through
 // them together.
@@ -255,7 +274,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         uint32_t n_full[LG_MAX_STAGES] = {}, n_landed[LG_MAX_STAGES] = {};
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
-            const GradItem w = grad_item(t, p);
+            const GradItem w = grad_item(t, p, s.plans);
             RowTiles tiles(p, s.plans, w.g);
             int tile;
             uint32_t rows[4];
@@ -304,7 +323,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         uint32_t phase = 0;
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
-            const GradItem w = grad_item(t, p);
+            const GradItem w = grad_item(t, p, s.plans);
             RowTiles tiles(p, s.plans, w.g);
             int tile;
             uint32_t rows[4];
@@ -362,7 +381,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         uint32_t parity = 0;  // a bit for each stage
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
-            const GradItem w = grad_item(t, p);
+            const GradItem w = grad_item(t, p, s.plans);
             RowTiles tiles(p, s.plans, w.g);
             int tile;
             uint32_t rows[4];
@@ -396,7 +415,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         const int q = warp & 3;
         int local = 0;
         for (int t = blockIdx.x; t < p.items; t += gridDim.x) {
-            const GradItem w = grad_item(t, p);
+            const GradItem w = grad_item(t, p, s.plans);
             const GradSide& side = p.side[w.which];
             RowTiles tiles(p, s.plans, w.g);
             int tile;
@@ -488,13 +507,13 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
     p.status = l.status;
     p.wait_budget = l.wait_budget;
     CUtensorMap m[4];
-    int64_t items[2] = {0, 0};
+    int64_t per[2] = {0, 0};
     for (int i = 0; i < 2; ++i) {
         if (!sides[i])
             continue;
         const LoraGradLaunch& s = *sides[i];
         p.side[i] = {(s.cols + 127) / 128, s.cols, s.G, s.step_c, s.step_j, s.stride_g};
-        items[i] = static_cast<int64_t>(p.side[i].tiles_c) * p.groups_j * s.adapters;
+        per[i] = static_cast<int64_t>(p.side[i].tiles_c) * p.groups_j;
         if (!encode_map(&m[2 * i], s.in_dtype, s.P, 2, {s.cols, s.rows, 1}, {s.ldp, 0}, {64, LT_ROWS, 1}) ||
             !encode_map(&m[2 * i + 1], s.in_dtype, s.t, 2, {p.lay.columns(), s.rows, 1},
                         {p.lay.columns(), 0}, {64, LT_ROWS, 1}))
@@ -505,10 +524,12 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
             m[2 * i] = m[2 - 2 * i];
             m[2 * i + 1] = m[3 - 2 * i];
         }
-    if (items[0] + items[1] > 0x7fffffff)
+    const int64_t items = (per[0] + per[1]) * l.adapters;
+    if (items > 0x7fffffff)
         return cudaErrorNotSupported;
-    p.items0 = static_cast<int>(items[0]);
-    p.items = static_cast<int>(items[0] + items[1]);
+    p.per[0] = static_cast<int>(per[0]);
+    p.per[1] = static_cast<int>(per[1]);
+    p.items = static_cast<int>(items);
     return with_type(l.out_dtype, [&](auto out) {
         return launch<decltype(out)>(m, p, l.num_sms, dependent, stream);
     });
