@@ -16,10 +16,14 @@
 // 64 rows of a group hold rows of the next one; those among the last 16 that
 // the tensor core reads are zeroed in shared memory by a warp of each CTA,
 // in both operands (a zero against an infinity of another group would be a
-// NaN), before they count as loaded.
+// NaN), before they count as loaded.  The tensor core drops what does not fit when it
+// adds to its accumulator, half a unit in the last place an instruction on
+// average (3e-6 of a sum over 2000 rows), and gradients are often kept in FP32: so
+// every 768 rows the accumulator is added, with rounding, to sums in the epilogue
+// warps' registers.
 //
-// Warps: 0 TMA producer, 1 MMA issuer (of the leader CTA), 2-5 epilogue, and for
-// the gradient 6, which zeroes.  The ring of two 64-deep K steps per stage with a
+// Warps: 0 TMA producer, 1 MMA issuer (of the leader CTA), 2 on epilogue (four; for
+// the gradient eight, and a last warp that zeroes).  The ring of two 64-deep K steps per stage with a
 // barrier each, the bounded waits and the two accumulators in tensor memory
 // are those of tc_gemm_kernel.
 #pragma once
@@ -42,6 +46,7 @@ constexpr int GT_MAX_STAGES = 10;
 constexpr int GT_A_BYTES = TC_BM * TC_BK * 2;  // a K step of the lanes' side
 constexpr int GT_N = 256;        // the N side of a full tile
 constexpr int GT_SORTED = 256;   // groups, at most, that the gradient sorts
+constexpr int GT_SEGMENT = 12;  // K steps of the gradient that one accumulator adds up
 
 struct GroupedTcParams {
     Grouping by;
@@ -64,10 +69,11 @@ struct GroupedTcParams {
 template <int MODE>
 struct GroupedLayout {
     static constexpr bool WGRAD = MODE == GROUPED_WGRAD;
-    static constexpr int THREADS = WGRAD ? 224 : 192;
+    static constexpr int EPI_WARPS = WGRAD ? 8 : 4;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS + (WGRAD ? 32 : 0);
     static constexpr int OFF_STAGING = GT_RING;
-    static constexpr int STAGING = WGRAD ? 4096 : 2048;  // of an epilogue warp
-    static constexpr int OFF_TABLE = OFF_STAGING + 4 * STAGING;
+    static constexpr int STAGING = 2048;  // of an epilogue warp
+    static constexpr int OFF_TABLE = OFF_STAGING + EPI_WARPS * STAGING;
     static constexpr int OFF_BAR = OFF_TABLE + (GroupTable::BYTES + 15) / 16 * 16;
     static constexpr int NUM_BARS = 2 * GT_MAX_STAGES + 5 + (WGRAD ? GT_MAX_STAGES : 0);
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), 8);  // every epilogue warp of the pair
+            mbar_init(tempty_bar(a), 2 * L::EPI_WARPS);  // of the pair
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -361,17 +367,16 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                 const GroupedWork w = grouped_work<MODE>(t, table, p);
                 if (w.k_blocks == 0)
                     continue;
-                const int acc = local & 1;
-                const uint32_t acc_phase = (local >> 1) & 1;
-                ++local;
-                ok = warp_wait<true>(tempty_bar(acc), acc_phase ^ 1, watch);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * GT_N);
                 const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
+                uint32_t d_tmem = 0;
                 for (int kb = 0; kb < w.k_blocks; ++kb) {
-                    ok = warp_wait<WGRAD>(full_bar(stage), phase, watch);
+                    const bool first = WGRAD ? kb % GT_SEGMENT == 0 : kb == 0;
+                    const bool last = kb == w.k_blocks - 1 || (WGRAD && kb % GT_SEGMENT == GT_SEGMENT - 1);
+                    if (first) {
+                        ok = warp_wait<true>(tempty_bar(local & 1), ((local >> 1) & 1) ^ 1, watch);
+                        d_tmem = tmem_base + static_cast<uint32_t>((local & 1) * GT_N);
+                    }
+                    ok = ok && warp_wait<WGRAD>(full_bar(stage), phase, watch);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -387,13 +392,14 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                                                         : smem_desc_sw128(a0 + k * 32, 16, 1024);
                             const uint64_t bdesc = WGRAD ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
                                                          : smem_desc_sw128(b0 + k * 32, 16, 1024);
-                            tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, kb != 0 || k != 0);
+                            tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, !first || k != 0);
                         }
                         tc_commit_pair(empty_bar(stage), 0x3);
-                        if (kb == w.k_blocks - 1)
-                            tc_commit_pair(tfull_bar(acc), 0x3);
+                        if (last)
+                            tc_commit_pair(tfull_bar(local & 1), 0x3);
                     }
                     __syncwarp();
+                    local += last;
                     if (++stage == stages) {
                         stage = 0;
                         phase ^= 1;
@@ -409,85 +415,53 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
             while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
             }
         }
-    } else if (warp < 6) {
+    } else if (warp < 2 + L::EPI_WARPS) {
         // ------------------------------------------------ epilogue
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const uint32_t leader_tempty0 = mapa_shared(tempty_bar(0), 0);
         const uint32_t leader_tempty1 = mapa_shared(tempty_bar(1), 0);
         OutT* const out = static_cast<OutT*>(p.C);
-        if (!WGRAD && p.zero_rest)
-            zero_rest_rows(table, p.by, out, p.ldc, p.N,
-                           static_cast<int64_t>(blockIdx.x) * 128 + (threadIdx.x - 64),
-                           static_cast<int64_t>(gridDim.x) * 128);
+        const uint32_t staging = sbase + L::OFF_STAGING + (warp - 2) * L::STAGING;
+        // waits for the next accumulator; gives it back
         int local = 0;
-        uint32_t buffer = 0;
-        for (int t = unit; t < num_work; t += num_units) {
-            const GroupedWork w = grouped_work<MODE>(t, table, p);
-            const int acc = local & 1;
-            const bool any = w.k_blocks > 0;
-            if (any) {
-                int ok = 1;
-                if (lane == 0)
-                    ok = tc_wait(tfull_bar(acc), (local >> 1) & 1, watch) ? 1 : 0;
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok)
+        auto take = [&] {
+            int ok = 1;
+            if (lane == 0)
+                ok = tc_wait(tfull_bar(local & 1), (local >> 1) & 1, watch) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            tc_fence_after();
+            return ok != 0;
+        };
+        auto give = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(local & 1 ? leader_tempty1 : leader_tempty0);
+            ++local;
+        };
+        const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        if constexpr (!WGRAD) {
+            if (p.zero_rest)
+                zero_rest_rows(table, p.by, out, p.ldc, p.N,
+                               static_cast<int64_t>(blockIdx.x) * 128 + (threadIdx.x - 64),
+                               static_cast<int64_t>(gridDim.x) * 128);
+            for (int t = unit; t < num_work; t += num_units) {
+                const GroupedWork w = grouped_work<MODE>(t, table, p);
+                if (!take())
                     break;
-                ++local;
-                tc_fence_after();
-            }
-            const int f = w.f0 + static_cast<int>(rank) * TC_BM + q * 32;
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                   static_cast<uint32_t>(acc * GT_N);
-            const uint32_t staging = sbase + L::OFF_STAGING + q * L::STAGING;
-            if constexpr (WGRAD) {
-                const int row = f + static_cast<int>(lane);
-                OutT* c = out + w.g * p.stride_c + row * p.ldc + w.c0;
-                if (p.tma_out) {
-                    // strips of 64 bytes, through two buffers in turn
-                    constexpr int STRIP = 64 / sizeof(OutT);
-                    if (f < p.N)
-#pragma unroll 1
-                        for (int s = 0; s < w.count; s += STRIP) {
-                            buffer ^= 2048;
-                            if (lane == 0)
-                                bulk_wait_group_read<1>();
-                            __syncwarp();
-                            strip_to_smem<OutT>(t_row + s, any, staging + buffer, p.alpha);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) {
-                                tma_store_3d(&tmC, staging + buffer, w.c0 + s, f, w.g);
-                                bulk_commit_group();
-                            }
-                        }
-                } else
-#pragma unroll 1
-                for (int s = 0; s < w.count; s += 32) {
-                    uint32_t v[32] = {};
-                    if (any) {
-                        tmem_ld_32x32b_x32(t_row + s, v);
-                        tmem_wait_ld(v);
-                    }
-                    if (p.unit) {
-                        if (row < p.N)
-                            put_row(c + s, v, w.count - s, p.unit, p.alpha, p.beta);
-                    } else if (f < p.N) {
-                        put_strip(v, staging, c - lane * p.ldc + s, p.ldc, min(32, p.N - f), w.count - s,
-                                  p.alpha, p.beta);
-                    }
-                }
-            } else {
+                const int f = w.f0 + static_cast<int>(rank) * TC_BM + q * 32;
+                const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * GT_N);
                 OutT* c = out + w.c0 * p.ldc + f;
 #pragma unroll 1
                 for (int s = 0; s < w.count; s += 32, c += 32 * p.ldc) {
                     if constexpr (sizeof(OutT) == 2) {
                         if (p.unit && p.beta == 0.0f) {
-                            put_turned(t_row + s, staging, c, p.ldc, w.count - s, p.N - f, p.alpha);
+                            put_turned(from + s, staging, c, p.ldc, w.count - s, p.N - f, p.alpha);
                             continue;
                         }
                     }
                     uint32_t v[32];
-                    tmem_ld_32x32b_x32(t_row + s, v);
+                    tmem_ld_32x32b_x32(from + s, v);
                     tmem_wait_ld(v);
                     if (f + static_cast<int>(lane) < p.N) {
                         float x[32];
@@ -497,17 +471,81 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                         put_column(c + lane, p.ldc, w.count - s, x, p.alpha, p.beta);
                     }
                 }
+                give();
             }
-            if (any) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(acc ? leader_tempty1 : leader_tempty0);
+        } else {
+            constexpr int HALF = GT_N / 2, CHUNKS = HALF / 32;
+            const int half = (warp - 2) / 4;  // of the tile's columns
+            bool ok = true;
+            for (int t = unit; t < num_work; t += num_units) {
+                const GroupedWork w = grouped_work<MODE>(t, table, p);
+                float sum[CHUNKS][32] = {};
+                for (int kb = 0; kb < w.k_blocks; kb += GT_SEGMENT) {
+                    ok = take();
+                    if (!ok)
+                        break;
+                    const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * GT_N + half * HALF);
+#pragma unroll
+                    for (int j = 0; j < CHUNKS; ++j)
+                        if (half * HALF + 32 * j < w.count) {
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t v[16];
+                                tmem_ld_32x32b_x16(from + 32 * j + h, v);
+                                tmem_wait_ld(v);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    sum[j][h + i] += __uint_as_float(v[i]);
+                            }
+                        }
+                    give();
+                }
+                if (!ok)
+                    break;
+                const int f = w.f0 + static_cast<int>(rank) * TC_BM + q * 32, row = f + static_cast<int>(lane);
+                if (f >= p.N)
+                    continue;
+#pragma unroll
+                for (int j = 0; j < CHUNKS; ++j) {
+                    const int s = half * HALF + 32 * j, left = w.count - s;
+                    if (left <= 0)
+                        break;
+                    uint32_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __float_as_uint(sum[j][i]);
+                    OutT* c = out + w.g * p.stride_c + row * p.ldc + w.c0 + s;
+                    if (p.tma_out) {
+#pragma unroll
+                        for (int part = 0; part < static_cast<int>(sizeof(OutT)) / 2; ++part) {
+                            if (lane == 0)
+                                bulk_wait_group_read<0>();
+                            __syncwarp();
+                            strip_to_smem<OutT>(v, part, staging, p.alpha);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_3d(&tmC, staging, w.c0 + s + 16 * part, f, w.g);
+                                bulk_commit_group();
+                            }
+                        }
+                    } else if (p.unit && p.beta == 0.0f) {
+#pragma unroll
+                        for (int part = 0; part < static_cast<int>(sizeof(OutT)) / 2; ++part)
+                            put_rows(v, part, staging, c - lane * p.ldc + 16 * part, p.ldc, p.N - f,
+                                     left - 16 * part, p.alpha);
+                    } else if (p.unit) {
+                        if (row < p.N)
+                            put_row(c, v, left, p.unit, p.alpha, p.beta);
+                    } else {
+                        put_strip(v, staging, c - lane * p.ldc, p.ldc, min(32, p.N - f), left, p.alpha, p.beta);
+                    }
+                }
             }
+            if (lane == 0)
+                bulk_wait_group_read<0>();
+            __syncwarp();
         }
-        if (WGRAD && lane == 0)
-            bulk_wait_group_read<0>();
-        __syncwarp();
     } else if constexpr (WGRAD) {
         // ------------------------- rows of other groups in a group's last K step
         int stage = 0;

@@ -410,10 +410,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(t_row + s, v);
                     tmem_wait_ld(v);
-                    if (!p.unit)
+                    if (p.unit) {
+#pragma unroll
+                        for (int part = 0; part < static_cast<int>(sizeof(OutT)) / 2; ++part)
+                            put_rows(v, part, staging, c + s + 16 * part, p.ldc, p.M - row, cols - s - 16 * part,
+                                     1.0f);
+                    } else {
                         put_strip(v, staging, c + s, p.ldc, min(32, p.M - row), cols - s, 1.0f, 0.0f);
-                    else if (row + static_cast<int>(lane) < p.M)
-                        put_row(c + lane * p.ldc + s, v, cols - s, p.unit, 1.0f, 0.0f);
+                    }
                 }
             tc_fence_before();
             __syncwarp();

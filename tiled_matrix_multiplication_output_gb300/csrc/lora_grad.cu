@@ -53,6 +53,7 @@ struct GradParams {
 struct GradItem {
     int which, g, c0, chunk0, chunks;
     int n;  // columns of rank values that the tensor core reads
+    int chains;  // accumulators that row tiles take in turn (see lora_shrink.cu)
 };
 
 // The plans of all row tiles in shared memory, where they fit: every tile of the
@@ -145,6 +146,7 @@ __device__ __forceinline__ GradItem grad_item(int t, const GradParams& p, const 
     w.chunk0 = t % p.groups_j * LG_CHUNKS;
     w.chunks = min(LG_CHUNKS, p.lay.chunks - w.chunk0);
     w.n = (w.chunks - 1) * 64 + p.lay.parts * p.lay.chunk;
+    w.chains = LG_CHUNKS / w.chunks;
     return w;
 }
 
@@ -330,9 +332,9 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             const int acc = local & 1;
             const uint32_t d = tmem + acc * 256;
             const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
-            bool any = false;
+            int steps = 0;
             while (ok && tiles.next(tile, rows)) {
-                if (!any)
+                if (steps == 0)
                     ok = warp_wait(smem_u32(&s.tempty[acc]), ((local >> 1) & 1) ^ 1, watch);
                 ok = ok && warp_wait(smem_u32(&s.full[stage]), phase, watch);
                 if (!ok)
@@ -340,25 +342,26 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                 tc_fence_after();
                 const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 2 * LG_BOX;
                 if (elect_one()) {
-                    bool first = !any;
+                    bool first = steps < w.chains;
+                    const uint32_t to = d + steps % w.chains * w.chunks * 64;
 #pragma unroll
                     for (int k = 0; k < LT_ROWS / TC_UMMA_K; ++k) {
                         if (!has_slice(rows, k))
                             continue;
-                        tc_mma_f16<1>(d, smem_desc_sw128(a0 + k * 2048, LG_BOX, 1024),
+                        tc_mma_f16<1>(to, smem_desc_sw128(a0 + k * 2048, LG_BOX, 1024),
                                       smem_desc_sw128(b0 + k * 2048, LG_BOX, 1024), idesc, !first);
                         first = false;
                     }
                     tc_commit(smem_u32(&s.empty[stage]));
                 }
                 __syncwarp();
-                any = true;
+                ++steps;
                 if (++stage == p.stages) {
                     stage = 0;
                     phase ^= 1;
                 }
             }
-            if (ok && any) {
+            if (ok && steps > 0) {
                 if (elect_one())
                     tc_commit(smem_u32(&s.tfull[acc]));
                 __syncwarp();
@@ -420,7 +423,10 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             RowTiles tiles(p, s.plans, w.g);
             int tile;
             uint32_t rows[4];
-            const bool any = tiles.next(tile, rows);
+            int steps = 0;  // (as many as matter here)
+            while (steps < w.chains && tiles.next(tile, rows))
+                ++steps;
+            const bool any = steps > 0;
             const int acc = local & 1;
             if (any) {
                 if (!warp_wait(smem_u32(&s.tfull[acc]), (local >> 1) & 1, watch))
@@ -439,10 +445,12 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                     if (j >= p.rank)
                         break;
                     float sum[16] = {};
-                    if (any)
+#pragma unroll 1
+                    for (int chain = 0; chain < steps; ++chain)
+#pragma unroll 1
                         for (int part = 0; part < p.lay.parts; ++part) {
                             uint32_t v[16];
-                            tmem_ld_32x32b_x16(from + k * 64 + part * p.lay.chunk + j0, v);
+                            tmem_ld_32x32b_x16(from + (chain * w.chunks + k) * 64 + part * p.lay.chunk + j0, v);
                             tmem_wait_ld(v);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)

@@ -31,28 +31,35 @@ __device__ __forceinline__ void put_column(OutT* p, int64_t ld, int rows, const 
             put(p + r * ld, beta != 0.0f ? fmaf(beta, old[r], alpha * v[r]) : alpha * v[r]);
 }
 
-// Strip of 32 rows x 32 FP32 values (this thread holds a row) to C, through 4 KiB
-// of shared memory, in whole lines whatever the alignment.  A whole warp calls it.
+// Strip of 32 rows x 32 FP32 values (this thread holds a row) to C, through 2 KiB
+// of shared memory, in whole sectors whatever the alignment.  A whole warp calls it.
 template <typename OutT>
 __device__ __forceinline__ void put_strip(const uint32_t (&v)[32], uint32_t staging, OutT* c, int64_t ldc,
                                           int rows, int cols, float alpha, float beta)
 {
-    const uint32_t lane = lane_id();
-    const uint32_t at = staging + lane * 128;
+    const uint32_t lane = lane_id(), col = lane & 15, odd = lane >> 4;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)  // column j of row `lane` at j ^ lane: no bank conflicts
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + ((j ^ lane) << 2)), "r"(v[j]) : "memory");
-    __syncwarp();
-    if (static_cast<int>(lane) < cols)
+    for (int h = 0; h < 32; h += 16) {  // 16 columns at a time, two rows a load
+#pragma unroll
+        for (int j = 0; j < 16; ++j)  // column j of row `lane` at j ^ (lane / 2) % 16
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(staging + lane * 64 + ((j ^ ((lane >> 1) & 15)) << 2)),
+                         "r"(v[h + j])
+                         : "memory");
+        __syncwarp();
+        if (h + static_cast<int>(col) < cols)
 #pragma unroll 1
-        for (int r = 0; r < rows; r += 8) {
-            float f[8];
+            for (int r = 0; r < rows; r += 16) {
+                float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = ld_shared_f32(staging + (r + i) * 128 + ((lane ^ (r + i)) << 2));
-            put_column(c + r * ldc + lane, ldc, rows - r, f, alpha, beta);
-        }
-    __syncwarp();
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t row = r + 2 * i + odd;
+                    f[i] = ld_shared_f32(staging + row * 64 + ((col ^ ((row >> 1) & 15)) << 2));
+                }
+                put_column(c + (r + odd) * ldc + h + col, 2 * ldc, (rows - r - static_cast<int>(odd) + 1) / 2, f,
+                           alpha, beta);
+            }
+        __syncwarp();
+    }
 }
 
 // The widest stores that rows allow: 32 or 16 bytes, or 0 for single values.
@@ -105,44 +112,72 @@ __device__ __forceinline__ void put_row(OutT* p, const uint32_t (&v)[32], int n,
     }
 }
 
-// 32 lanes x 64 bytes of columns at taddr (zeros where there are no sums) to shared
-// memory as a TMA store of such boxes expects it, 64-byte swizzled: 16-byte unit u
-// of row r at u ^ (r / 2) % 4.  A whole warp calls it.
+// The 16-byte unit u of row t of a 64-byte wide strip in shared memory, of which
+// rows rows and cols values a row exist, to its place in rows of c on 16-byte
+// boundaries.
 template <typename OutT>
-__device__ __forceinline__ void strip_to_smem(uint32_t taddr, bool any, uint32_t to, float alpha)
+__device__ __forceinline__ void put_unit(uint32_t at, OutT* c, int64_t ldc, int t, int u, int rows, int cols)
+{
+    constexpr int EACH = 16 / sizeof(OutT);
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    OutT* p = c + t * ldc + EACH * u;
+    const int left = cols - EACH * u;
+    if (t < rows && left >= EACH) {
+        *reinterpret_cast<uint4*>(p) = v;
+    } else if (t < rows) {
+        OutT h[EACH];
+        memcpy(h, &v, 16);
+#pragma unroll
+        for (int k = 0; k < EACH; ++k)
+            if (k < left)
+                p[k] = h[k];
+    }
+}
+
+// alpha * v of 32 rows (this thread holds one), 64 bytes of columns (part: which 16 of
+// the values, for FP32), to shared memory as a TMA store of such boxes expects it,
+// 64-byte swizzled: 16-byte unit u of row r at u ^ (r / 2) % 4, without bank conflicts.
+// A whole warp calls it.
+template <typename OutT>
+__device__ __forceinline__ void strip_to_smem(const uint32_t (&v)[32], int part, uint32_t staging, float alpha)
 {
     const uint32_t lane = lane_id(), turn = (lane >> 1) & 3;
-    if constexpr (sizeof(OutT) == 4) {
-        uint32_t v[16] = {};
-        if (any) {
-            tmem_ld_32x32b_x16(taddr, v);
-            tmem_wait_ld(v);
-        }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            uint32_t w[4];
+    for (int u = 0; u < 4; ++u) {
+        uint32_t w[4];
+        if constexpr (sizeof(OutT) == 4) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                w[i] = __float_as_uint(alpha * __uint_as_float(v[4 * u + i]));
-            st_shared_v4(to + lane * 64 + ((u ^ turn) << 4), w[0], w[1], w[2], w[3]);
-        }
-    } else {
-        uint32_t v[32] = {};
-        if (any) {
-            tmem_ld_32x32b_x32(taddr, v);
-            tmem_wait_ld(v);
-        }
-        OutT* tag = nullptr;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            uint32_t w[4];
+                w[i] = __float_as_uint(alpha * __uint_as_float(v[16 * part + 4 * u + i]));
+        } else {
+            OutT* tag = nullptr;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 w[i] = pack2(alpha * __uint_as_float(v[8 * u + 2 * i]),
                              alpha * __uint_as_float(v[8 * u + 2 * i + 1]), tag);
-            st_shared_v4(to + lane * 64 + ((u ^ turn) << 4), w[0], w[1], w[2], w[3]);
         }
+        st_shared_v4(staging + lane * 64 + ((u ^ turn) << 4), w[0], w[1], w[2], w[3]);
     }
+}
+
+// The same to rows of c on 16-byte boundaries: a store covers 64 bytes of eight rows.
+template <typename OutT>
+__device__ __forceinline__ void put_rows(const uint32_t (&v)[32], int part, uint32_t staging, OutT* c,
+                                         int64_t ldc, int rows, int cols, float alpha)
+{
+    const uint32_t lane = lane_id();
+    strip_to_smem<OutT>(v, part, staging, alpha);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 8 * i + static_cast<int>(lane >> 2), u = lane & 3;
+        put_unit(staging + t * 64 + ((u ^ ((t >> 1) & 3)) << 4), c, ldc, t, u, rows, cols);
+    }
+    __syncwarp();
 }
 
 // ------------------------------------------- tiles that are stored turned
@@ -197,26 +232,10 @@ __device__ __forceinline__ void put_turned(uint32_t taddr, uint32_t staging, Out
         stmatrix_x4_trans(at + ((u ^ turn) << 4), w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
-    const int u = lane & 3, left = m - 8 * u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int t = 8 * i + static_cast<int>(lane >> 2);
-        uint4 v;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(staging + t * 64 + ((u ^ ((t >> 1) & 3)) << 4))
-                     : "memory");
-        OutT* p = y + t * ldy + 8 * u;
-        if (t < n && left >= 8) {
-            *reinterpret_cast<uint4*>(p) = v;
-        } else if (t < n) {
-            OutT h[8];
-            memcpy(h, &v, 16);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < left)
-                    p[k] = h[k];
-        }
+        const int t = 8 * i + static_cast<int>(lane >> 2), k = lane & 3;
+        put_unit(staging + t * 64 + ((k ^ ((t >> 1) & 3)) << 4), y, ldy, t, k, n, m);
     }
     __syncwarp();
 }
