@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "grouped_maps.h"
@@ -54,63 +55,11 @@ struct ShrinkSmem {
     uint64_t full[LS_MAX_STAGES], empty[LS_MAX_STAGES], done;
     uint32_t tmem;
     int abort_flag;
-    int4 of4[LT_ROWS / 4];     // each row's adapter
-    int4 first4[LT_ROWS / 4];  // the same of its adapter's first row, else INT_MAX
+    PlanScratch scratch;
     int place[LT_ROWS];        // each row's place in the plan
     float scale[LT_ROWS];      // of each place
     LoraPlan plan;
 };
-
-// The plan of 128 rows from their adapters; every thread calls it.
-__device__ __forceinline__ void make_plan(ShrinkSmem& s, const ShrinkParams& p, int row0)
-{
-    const int i = threadIdx.x;
-    int* of = reinterpret_cast<int*>(s.of4);
-    int* first = reinterpret_cast<int*>(s.first4);
-    int g = -1;
-    if (i < LT_ROWS) {
-        if (row0 + i < p.rows)
-            g = p.adapter[row0 + i];
-        if (g >= p.adapters)
-            g = -1;
-        of[i] = g;
-        for (int w = 0; w < 4; ++w)
-            s.plan.rows[i][w] = 0;
-    }
-    if (i == 0)
-        s.plan.count = 0;
-    __syncthreads();
-    if (i < LT_ROWS) {
-        int before = 0;  // earlier rows with the same adapter
-#pragma unroll 4
-        for (int j = 0; j < LT_ROWS / 4; ++j) {
-            const int4 v = s.of4[j];
-            before |= (v.x == g & 4 * j < i) | (v.y == g & 4 * j + 1 < i) | (v.z == g & 4 * j + 2 < i) |
-                      (v.w == g & 4 * j + 3 < i);
-        }
-        first[i] = g >= 0 && !before ? g : 0x7fffffff;
-    }
-    __syncthreads();
-    if (i < LT_ROWS) {
-        int place = -1;
-        if (g >= 0) {
-            place = 0;
-#pragma unroll 4
-            for (int j = 0; j < LT_ROWS / 4; ++j) {
-                const int4 v = s.first4[j];
-                place += (v.x < g) + (v.y < g) + (v.z < g) + (v.w < g);
-            }
-            if (first[i] == g) {
-                s.plan.ids[place] = g;
-                s.scale[place] = p.scale ? p.scale[g] : 1.0f;
-                atomicAdd(&s.plan.count, 1);
-            }
-            atomicOr(&s.plan.rows[place][i >> 5], 1u << (i & 31));
-        }
-        s.place[i] = place;
-    }
-    __syncthreads();
-}
 
 // The parts of rank values j .. j + 7 (a multiple of 8) of a row.
 template <typename T>
@@ -156,6 +105,10 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     const CUtensorMap* tmF = which ? &tmF1 : &tmF0;
     const int b_bytes = p.b_bytes[which];
     const int row0 = tile * LT_ROWS;
+    // each row's adapter, asked for before anything else
+    const int g = threadIdx.x >= 128 ? row_adapter(p.adapter, row0 + static_cast<int>(threadIdx.x) - 128, p.rows,
+                                                   p.adapters)
+                                     : -1;
     const TcWatch watch{&s.abort_flag, p.status, p.wait_budget};
     const int per = (side.k_blocks + SPLITS - 1) / SPLITS;
     const int kb0 = min(split * per, side.k_blocks), kb1 = min(kb0 + per, side.k_blocks);
@@ -175,7 +128,14 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
         tmem_alloc<1>(smem_u32(&s.tmem), p.tmem_cols);
         tmem_relinquish<1>();
     }
-    make_plan(s, p, row0);
+    // (128 threads make the plan, as the accumulator's warps are idle)
+    if (threadIdx.x >= 128) {
+        const float scale = p.scale && g >= 0 ? p.scale[g] : 1.0f;
+        const int place = make_plan(s.plan, s.scratch, g, threadIdx.x - 128, [] { bar_sync(1, 128); });
+        s.place[threadIdx.x - 128] = place;
+        if (place >= 0)
+            s.scale[place] = scale;  // (of every row with this adapter: the same)
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -211,13 +171,13 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
                         mbar_arrive_expect_tx(bar, p.box_rows * 128 + some * b_bytes);
                         tma_load_2d(dA, tmX, bar, kb * TC_BK, row0);
                         for (int i = 0; i < some; ++i) {
-                            const int g = side.one ? 0 : s.plan.ids[nth(i0 + i)];
+                            const int z = side.one ? 0 : s.plan.ids[nth(i0 + i)];
                             const uint32_t dB = base + i * b_bytes;
                             if (side.across) {
                                 for (int b = 0; b * 8192 < b_bytes; ++b)
-                                    tma_load_3d(dB + b * 8192, tmF, bar, b * 64, kb * TC_BK, g);
+                                    tma_load_3d(dB + b * 8192, tmF, bar, b * 64, kb * TC_BK, z);
                             } else {
-                                tma_load_3d(dB, tmF, bar, kb * TC_BK, 0, g);
+                                tma_load_3d(dB, tmF, bar, kb * TC_BK, 0, z);
                             }
                         }
                     }
@@ -383,21 +343,33 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     }
 }
 
+// Once for each device: the SM's memory is laid out for this kernel and the
+// product's from the start, as it is not laid out anew while a block runs (a
+// decoding batch took 28 us instead of 25).
+template <typename T, int SPLITS>
+cudaError_t share_sms()
+{
+    static std::atomic<uint64_t> done{0};
+    static_assert(kMaxDevices <= 64, "a bit for each");
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err != cudaSuccess || device < 0 || device >= kMaxDevices || (done.load() >> device & 1))
+        return err;
+    err = cudaFuncSetAttribute(lora_shrink_tc_kernel<T, SPLITS>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (err == cudaSuccess)
+        done.fetch_or(1ull << device);
+    return err;
+}
+
 template <typename T, int SPLITS>
 cudaError_t launch(const CUtensorMap (&m)[4], const ShrinkParams& p, unsigned clusters, int smem,
                    cudaStream_t stream)
 {
     static ClusterCaps caps;
     int cap = 0;
-    // The SM's memory is laid out for both kernels from the start: it is not
-    // laid out anew while a block runs.
-    cudaError_t err = cudaSuccess;
-    int device = 0;
-    err = cudaGetDevice(&device);
-    if (err == cudaSuccess && device >= 0 && device < kMaxDevices && caps.cap[device] == 0)
-        err = cudaFuncSetAttribute(lora_shrink_tc_kernel<T, SPLITS>,
-                                   cudaFuncAttributePreferredSharedMemoryCarveout,
-                                   cudaSharedmemCarveoutMaxShared);
+    cudaError_t err = share_sms<T, SPLITS>();
     if (err == cudaSuccess)
         err = cluster_cap(lora_shrink_tc_kernel<T, SPLITS>, caps, 1, LS_THREADS, LS_RING + 1024, 1, &cap);
     if (err != cudaSuccess)

@@ -10,7 +10,8 @@
 //
 // Launched as a programmatic dependent of the kernel that makes the rank values,
 // and small enough to share an SM with it: the shared product's weights are read
-// while the rank values are still being summed.
+// while the rank values are still being summed, and so are the adapters' factors,
+// as each CTA makes its tile's plan itself.
 #include <algorithm>
 #include <cstring>
 
@@ -21,7 +22,7 @@
 namespace tmmo {
 namespace {
 
-constexpr int LM_THREADS = 256;  // warps 0: copies, 1: MMA, 2: plan, 4-7: accumulator
+constexpr int LM_THREADS = 256;  // warps 0: copies, 1: MMA, 2: rank values, 4-7: plan, accumulator
 constexpr int LM_MAX_STAGES = 8;
 constexpr int LM_RING = 200 * 1024;
 constexpr int LM_RING_SHARED = 120 * 1024;  // leaves room for the shrink's kernel on the SM
@@ -30,9 +31,10 @@ constexpr int LM_PITCH = 132;    // of the sums in shared memory: rows 16 bytes 
 struct SmallParams {
     int M, N, k_blocks, rank;
     int tiles_n;
-    bool adapters, one;
+    bool one;
+    int adapters;
     LoraParts lay;
-    const LoraPlan* plan;
+    const int32_t* adapter;
     void* C;
     int64_t ldc;
     uint32_t idesc;
@@ -50,11 +52,11 @@ struct SmallParams {
 };
 
 struct SmallSmem {
-    uint64_t full[LM_MAX_STAGES], empty[LM_MAX_STAGES], planned, done;
+    uint64_t full[LM_MAX_STAGES], empty[LM_MAX_STAGES], planned, held, done;
     uint32_t tmem;
     int abort_flag;
-    int count, ids[LT_ROWS];  // this CTA's adapters
-    uint4 rows[LT_ROWS];
+    PlanScratch scratch;
+    LoraPlan plan;
 };
 
 // Eight values of a row, of which the first n exist; words: p is on a 16-byte
@@ -120,14 +122,17 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     const int per = (p.k_blocks + SPLITS - 1) / SPLITS;
     const int kb0 = split * per, kb1 = min(kb0 + per, p.k_blocks);
     const TcWatch watch{&s.abort_flag, p.status, p.wait_budget};
-    const LoraPlan& plan = p.plan[mb];
+    // each row's adapter, asked for before anything else
+    const int g = warp >= 4 ? row_adapter(p.adapter, row0 + static_cast<int>(threadIdx.x) - 128, p.M, p.adapters)
+                            : -1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(smem_u32(&s.full[i]), 1);
             mbar_init(smem_u32(&s.empty[i]), 1);
         }
-        mbar_init(smem_u32(&s.planned), 1);
+        mbar_init(smem_u32(&s.planned), 128);
+        mbar_init(smem_u32(&s.held), 1);
         mbar_init(smem_u32(&s.done), 1);
         s.abort_flag = 0;
         fence_mbar_init();
@@ -180,36 +185,34 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     }
                     tma_load_2d(dA, &tmX, bar, kb * TC_BK, row0);
                 });
-            if (ok && p.adapters) {
-                grid_dep_wait();
+            if (ok && p.adapters > 0) {
                 ok = warp_wait(smem_u32(&s.planned), 0, watch);
                 if (!ACROSS && p.beside > 0) {
-                    for (int a = 0; ok && a < s.count; a += p.beside) {
-                        const int some = min(p.beside, s.count - a);
+                    for (int a = split; ok && a < s.plan.count; a += p.beside * SPLITS) {
+                        const int some = min(p.beside, (s.plan.count - a + SPLITS - 1) / SPLITS);
                         const uint32_t each = p.lay.chunk * 2 * 128;
-                        ok = step(false, (a == 0 ? a_bytes : 0) + some * each,
-                                  [&](uint32_t, uint32_t dB, uint32_t bar) {
-                                      if (a == 0)
-                                          tma_load_2d(held, &tmT, bar, 0, row0);
-                                      for (int i = 0; i < some; ++i)
-                                          tma_load_3d(dB + i * each, &tmE, bar, 0, col0,
-                                                      p.one ? 0 : s.ids[a + i]);
-                                  });
-                    }
-                } else
-                for (int a = 0; ok && a < s.count; ++a) {
-                    const int z = p.one ? 0 : s.ids[a];
-                    for (int c = 0; ok && c < p.lay.chunks; ++c) {
-                        const int j = c * p.lay.chunk;
-                        ok = step(false, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
-                            if (ACROSS) {
-                                tma_load_3d(dB, &tmE, bar, col0, j, z);
-                                tma_load_3d(dB + 8192, &tmE, bar, col0 + 64, j, z);
-                            } else {
-                                tma_load_3d(dB, &tmE, bar, j, col0, z);
-                            }
-                            tma_load_2d(dA, &tmT, bar, c * 64, row0);
+                        ok = step(false, some * each, [&](uint32_t, uint32_t dB, uint32_t bar) {
+                            for (int i = 0; i < some; ++i)
+                                tma_load_3d(dB + i * each, &tmE, bar, 0, col0,
+                                            p.one ? 0 : s.plan.ids[a + i * SPLITS]);
                         });
+                    }
+                } else {
+                    grid_dep_wait();  // the rank values come with the factors
+                    for (int a = split; ok && a < s.plan.count; a += SPLITS) {
+                        const int z = p.one ? 0 : s.plan.ids[a];
+                        for (int c = 0; ok && c < p.lay.chunks; ++c) {
+                            const int j = c * p.lay.chunk;
+                            ok = step(false, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                                if (ACROSS) {
+                                    tma_load_3d(dB, &tmE, bar, col0, j, z);
+                                    tma_load_3d(dB + 8192, &tmE, bar, col0 + 64, j, z);
+                                } else {
+                                    tma_load_3d(dB, &tmE, bar, j, col0, z);
+                                }
+                                tma_load_2d(dA, &tmT, bar, c * 64, row0);
+                            });
+                        }
                     }
                 }
             }
@@ -252,17 +255,25 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                                              : smem_desc_sw128(b0 + k * 32, 16, 1024),
                                       p.idesc, kb != kb0 || k != 0);
                 });
-            if (ok && p.adapters) {
+            if (ok && p.adapters > 0) {
                 ok = warp_wait(smem_u32(&s.planned), 0, watch);
+                auto others = [&](int a, uint32_t (&off)[4]) {
+                    const uint4 rows = *reinterpret_cast<const uint4*>(s.plan.rows[a]);
+                    off[0] = ~rows.x;
+                    off[1] = ~rows.y;
+                    off[2] = ~rows.z;
+                    off[3] = ~rows.w;
+                };
                 if (!ACROSS && p.beside > 0) {
                     const uint32_t width = p.lay.chunk * 2;
                     const int deep = p.lay.deep(0, p.rank);
-                    for (int a = 0; ok && a < s.count; a += p.beside)
+                    ok = ok && warp_wait(smem_u32(&s.held), 0, watch);
+                    for (int a = split; ok && a < s.plan.count; a += p.beside * SPLITS)
                         ok = step([&](uint32_t, uint32_t b0) {
-                            const int some = min(p.beside, s.count - a);
+                            const int some = min(p.beside, (s.plan.count - a + SPLITS - 1) / SPLITS);
                             for (int i = 0; i < some; ++i, b0 += width * 128) {
-                                const uint4 rows = s.rows[a + i];
-                                const uint32_t off[4] = {~rows.x, ~rows.y, ~rows.z, ~rows.w};
+                                uint32_t off[4];
+                                others(a + i * SPLITS, off);
                                 for (int part = 0; part < p.lay.parts; ++part)
                                     for (int k = 0; k < deep; ++k)
                                         tc_mma_f16_lanes(tmem,
@@ -270,21 +281,22 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                                                          smem_desc_rows(b0 + k * 32, width), p.idesc, 1, off);
                             }
                         });
-                } else
-                for (int a = 0; ok && a < s.count; ++a) {
-                    const uint4 rows = s.rows[a];
-                    const uint32_t off[4] = {~rows.x, ~rows.y, ~rows.z, ~rows.w};
-                    for (int c = 0; ok && c < p.lay.chunks; ++c)
-                        ok = step([&](uint32_t a0, uint32_t b0) {
-                            const int deep = p.lay.deep(c, p.rank);
-                            for (int part = 0; part < p.lay.parts; ++part)
-                                for (int k = 0; k < deep; ++k)
-                                    tc_mma_f16_lanes(
-                                        tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
-                                        ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                               : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                        p.idesc, 1, off);
-                        });
+                } else {
+                    for (int a = split; ok && a < s.plan.count; a += SPLITS) {
+                        uint32_t off[4];
+                        others(a, off);
+                        for (int c = 0; ok && c < p.lay.chunks; ++c)
+                            ok = step([&](uint32_t a0, uint32_t b0) {
+                                const int deep = p.lay.deep(c, p.rank);
+                                for (int part = 0; part < p.lay.parts; ++part)
+                                    for (int k = 0; k < deep; ++k)
+                                        tc_mma_f16_lanes(
+                                            tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
+                                            ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                   : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                            p.idesc, 1, off);
+                            });
+                    }
                 }
             }
             if (elect_one())
@@ -294,20 +306,21 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             while (!mbar_try_wait(smem_u32(&s.done), 0) && clock64() - t0 < p.wait_budget) {
             }
         }
-    } else if (warp == 2 && p.adapters) {
-        // this CTA's share of the tile's adapters
+    } else if (warp == 2 && p.adapters > 0) {
         grid_dep_wait();
         grid_dep_launch_dependents();  // the rank values are there for others, too
-        const int count = plan.count, mine = count > split ? (count - split + SPLITS - 1) / SPLITS : 0;
-        for (int i = lane; i < mine; i += 32) {
-            s.ids[i] = plan.ids[split + i * SPLITS];
-            s.rows[i] = *reinterpret_cast<const uint4*>(plan.rows[split + i * SPLITS]);
+        if (!ACROSS && p.beside > 0) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(smem_u32(&s.held), a_bytes);
+                tma_load_2d(held, &tmT, smem_u32(&s.held), 0, row0);
+            }
+            __syncwarp();
+            // (also after the others gave up: nothing may land when this CTA is gone)
+            warp_wait(smem_u32(&s.held), 0, watch);
         }
-        if (lane == 0)
-            s.count = mine;
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(smem_u32(&s.planned));
+    } else if (warp >= 4 && p.adapters > 0) {
+        make_plan(s.plan, s.scratch, g, threadIdx.x - 128, [] { bar_sync(1, 128); });
+        mbar_arrive(smem_u32(&s.planned));
     }
     // The sums to shared memory; the ring holds nothing any more.
     __syncwarp();
@@ -334,7 +347,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         }
         tc_fence_before();
     }
-    if (p.adapters)
+    if (p.adapters > 0)
         grid_dep_wait();  // this grid must not end before the one it depends on
     if constexpr (SPLITS > 1)
         cluster_sync();
@@ -402,7 +415,7 @@ cudaError_t launch(const CUtensorMap (&m)[4], const SmallParams& p, int tiles, c
     if (err != cudaSuccess)
         return err;
     ClusterLaunch l(static_cast<unsigned>(tiles * SPLITS), SPLITS, LM_THREADS,
-                    p.ring + (p.beside ? 16384 : 0) + 1024, stream, p.adapters);
+                    p.ring + (p.beside ? 16384 : 0) + 1024, stream, p.adapters > 0);
     return l.run(lora_small_kernel<ACROSS, SPLITS>, m[0], m[1], m[2], m[3], p);
 }
 
@@ -438,10 +451,10 @@ cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     p.k_blocks = (l.K + TC_BK - 1) / TC_BK;
     p.rank = l.rank;
     p.tiles_n = (l.N + 127) / 128;
-    p.adapters = l.adapters > 0;
+    p.adapters = l.adapters;
     p.one = l.adapters == 1 || l.stride_e == 0;
     p.lay = lora_parts(l.rank, l.parts);
-    p.plan = static_cast<const LoraPlan*>(l.plan);
+    p.adapter = l.adapter;
     p.C = l.Y;
     p.ldc = l.ldy;
     p.out_dtype = l.out_dtype;
@@ -464,7 +477,7 @@ cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream)
               (l.across ? encode_map(&m[1], dt, l.W, 2, {l.N, l.K, 1}, {l.ldw, 0}, {64, TC_BK, 1})
                         : encode_map(&m[1], dt, l.W, 2, {l.K, l.N, 1}, {l.ldw, 0}, {64, 128, 1}));
     m[2] = m[3] = m[0];
-    if (ok && p.adapters) {
+    if (ok && p.adapters > 0) {
         const int64_t stacked = p.one ? 1 : l.adapters, stride = p.one ? l.lde : l.stride_e;
         ok = encode_map(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, box, 1}) &&
              (l.across ? encode_map(&m[3], dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})

@@ -35,6 +35,57 @@ struct alignas(16) LoraPlan {
 };
 static_assert(sizeof(LoraPlan) == LORA_PLAN_BYTES, "size of a plan in the workspace");
 
+// The adapter of a row, or -1.
+__device__ __forceinline__ int row_adapter(const int32_t* adapter, int row, int rows, int adapters)
+{
+    const int g = row < rows ? adapter[row] : -1;
+    return g >= 0 && g < adapters ? g : -1;
+}
+
+struct PlanScratch {
+    int4 of[LT_ROWS / 4];     // each row's adapter
+    int4 first[LT_ROWS / 4];  // the same of its adapter's first row, else INT_MAX
+};
+
+// The plan of a tile's rows: 128 threads call it, each (i) with its row's adapter g,
+// with a barrier sync() of theirs, in which it ends.  Returns the row's place in the
+// plan, or -1.
+template <typename Sync>
+__device__ __forceinline__ int make_plan(LoraPlan& plan, PlanScratch& s, int g, int i, Sync sync)
+{
+    int* first = reinterpret_cast<int*>(s.first);
+    reinterpret_cast<int*>(s.of)[i] = g;
+    *reinterpret_cast<uint4*>(plan.rows[i]) = make_uint4(0, 0, 0, 0);
+    if (i == 0)
+        plan.count = 0;
+    sync();
+    int before = 0;  // earlier rows with the same adapter
+#pragma unroll 4
+    for (int j = 0; j < LT_ROWS / 4; ++j) {
+        const int4 v = s.of[j];
+        before |= (v.x == g & 4 * j < i) | (v.y == g & 4 * j + 1 < i) | (v.z == g & 4 * j + 2 < i) |
+                  (v.w == g & 4 * j + 3 < i);
+    }
+    first[i] = g >= 0 && !before ? g : 0x7fffffff;
+    sync();
+    int place = -1;
+    if (g >= 0) {
+        place = 0;
+#pragma unroll 4
+        for (int j = 0; j < LT_ROWS / 4; ++j) {
+            const int4 v = s.first[j];
+            place += (v.x < g) + (v.y < g) + (v.z < g) + (v.w < g);
+        }
+        if (!before) {
+            plan.ids[place] = g;
+            atomicAdd(&plan.count, 1);
+        }
+        atomicOr(&plan.rows[place][i >> 5], 1u << (i & 31));
+    }
+    sync();
+    return place;
+}
+
 // D[tmem] (+)= A B for the lanes whose bit of `off` is clear.
 __device__ __forceinline__ void tc_mma_f16_lanes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                                  uint32_t idesc, uint32_t accumulate,
