@@ -7,6 +7,7 @@
 
 #include "api_checks.h"
 #include "device.h"
+#include "grouped_maps.h"
 #include "launch.h"
 #include "lora.h"
 #include "pack.h"
@@ -99,7 +100,8 @@ int parts_for(int in_dtype, bool f32_result)
 
 // The input's direction: rank values from X and A, or (across) from D and B.
 LoraLaunch make_launch(const Operands& o, bool across, const gemm_lora_t& lora, const int32_t* adapter,
-                       int64_t rows, int64_t N, int64_t K, int in_dtype, const DeviceInfo& d)
+                       int64_t rows, int64_t N, int64_t K, int in_dtype, const DeviceInfo& d,
+                       TensorMaps* maps)
 {
     const PackMatrix &in = across ? o.d : o.x, &f = across ? o.b : o.a, &e = across ? o.a : o.b;
     LoraLaunch l{};
@@ -114,6 +116,7 @@ LoraLaunch make_launch(const Operands& o, bool across, const gemm_lora_t& lora, 
     l.lde = e.ld;
     l.stride_e = e.stride;
     l.across = across;
+    l.maps = maps;
     l.scale = lora.scale;
     l.adapter = adapter;
     l.rows = static_cast<int>(rows);
@@ -162,7 +165,8 @@ extern "C" int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw,
         return GEMM_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t err = o.packing.run(ws.copy(workspace), d.num_sms, s);
-    LoraLaunch l = make_launch(o, false, *lora, adapter, rows, N, K, in_dtype, d);
+    TensorMaps maps;
+    LoraLaunch l = make_launch(o, false, *lora, adapter, rows, N, K, in_dtype, d, &maps);
     l.Y = Y;
     l.ldy = ldy;
     l.out_dtype = out_dtype;
@@ -232,14 +236,15 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t err = o.packing.run(ws.copy(workspace), dev.num_sms, s);
 
-    LoraLaunch u = make_launch(o, true, *lora, adapter, rows, N, K, in_dtype, dev);  // scale * D B
+    TensorMaps maps;
+    LoraLaunch u = make_launch(o, true, *lora, adapter, rows, N, K, in_dtype, dev, &maps);  // scale * D B
     u.Y = DX;
     u.ldy = lddx;
     u.out_dtype = out_dtype;
     u.parts = parts;
     u.t = ws.side(workspace, 0);
     u.plan = ws.plan(workspace);
-    LoraLaunch t = make_launch(o, false, *lora, adapter, rows, N, K, in_dtype, dev);  // scale * X A^T
+    LoraLaunch t = make_launch(o, false, *lora, adapter, rows, N, K, in_dtype, dev, &maps);  // scale * X A^T
     t.parts = parts;
     t.t = ws.side(workspace, 1);
     t.plan = u.plan;
@@ -250,6 +255,7 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
     a.t = u.t;
     a.parts = parts;
     a.plan = u.plan;
+    a.maps = &maps;
     a.G = DA;
     a.step_c = 1;
     a.step_j = ldda;

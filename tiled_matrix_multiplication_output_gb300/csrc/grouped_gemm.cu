@@ -30,12 +30,18 @@ cudaError_t grouped_tc_launch(const GroupedLaunch& l, cudaStream_t stream)
     GroupedMaps m;
     bool ok =
         (p.swap ? encode_map(&m.a, l.in_dtype, l.W, 3, {inner, groups, outer}, {stride, l.ldw}, {64, 1, deep})
-                : encode_map(&m.a, l.in_dtype, l.W, 3, {inner, outer, groups}, {l.ldw, stride}, {64, deep, 1})) &&
-        encode_map(&m.b, l.in_dtype, l.X, 2, {l.K, l.by.rows, 1}, {l.ldx, 0}, {64, TC_BM, 1});
+                : encode_map(&m.a, l.in_dtype, l.W, 3, {inner, outer, groups}, {l.ldw, stride}, {64, deep, 1}));
+    // The boxes that half of the largest possible tile is made of; a kernel asks
+    // for no other.
+    const int64_t half = (std::min<int64_t>(l.by.rows, GT_N) + 31) / 32 * 16;
     auto rows = [&](CUtensorMap* map, uint32_t n) {
+        if (half < static_cast<int64_t>(n)) {
+            *map = m.b16;
+            return true;
+        }
         return encode_map(map, l.in_dtype, l.X, 2, {l.K, l.by.rows, 1}, {l.ldx, 0}, {64, n, 1});
     };
-    ok = ok && rows(&m.b64, 64) && rows(&m.b32, 32) && rows(&m.b16, 16);
+    ok = ok && rows(&m.b16, 16) && rows(&m.b32, 32) && rows(&m.b64, 64) && rows(&m.b, TC_BM);
     if (!ok)
         return cudaErrorNotSupported;
     m.c = m.b;

@@ -20,6 +20,8 @@ namespace tmmo {
 
 constexpr int kMaxRank = 256;
 
+class TensorMaps;
+
 struct LoraLaunch {
     const void* X;        // rows x K
     int64_t ldx;
@@ -39,6 +41,7 @@ struct LoraLaunch {
     void* t;              // the rank values: FP32, rows x rank, or in parts (lora_tc.cuh)
     int parts;
     void* plan;           // one for each 128 rows
+    TensorMaps* maps;     // the call's
     int num_sms;
     int* status;
     long long wait_budget;
@@ -52,6 +55,7 @@ struct LoraGradLaunch {
     const void* t;        // as LoraLaunch has them
     int parts;
     const void* plan;
+    TensorMaps* maps;
     void* G;              // adapters; element (c, j) at c * step_c + j * step_j
     int64_t step_c, step_j, stride_g;
     const int32_t* adapter;

@@ -501,19 +501,19 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     CUtensorMap m[6];
     const int dt = l.in_dtype;
     auto weights = [&](CUtensorMap* map, uint32_t outputs) {
-        return l.across ? encode_map(map, dt, l.W, 2, {l.N, l.K, 1}, {l.ldw, 0}, {64, TC_BK, 1})
-                        : encode_map(map, dt, l.W, 2, {l.K, l.N, 1}, {l.ldw, 0}, {64, outputs, 1});
+        return l.across ? l.maps->get(map, dt, l.W, 2, {l.N, l.K, 1}, {l.ldw, 0}, {64, TC_BK, 1})
+                        : l.maps->get(map, dt, l.W, 2, {l.K, l.N, 1}, {l.ldw, 0}, {64, outputs, 1});
     };
     const int64_t stacked = p.one ? 1 : l.adapters, stride = p.one ? l.lde : l.stride_e;
     auto factors = [&](CUtensorMap* map, uint32_t outputs) {
-        return l.across ? encode_map(map, dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
-                        : encode_map(map, dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride}, {64, outputs, 1});
+        return l.across ? l.maps->get(map, dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
+                        : l.maps->get(map, dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride}, {64, outputs, 1});
     };
-    bool ok = encode_map(&m[0], dt, l.X, 2, {l.K, l.rows, 1}, {l.ldx, 0}, {64, TC_BM, 1}) &&
+    bool ok = l.maps->get(&m[0], dt, l.X, 2, {l.K, l.rows, 1}, {l.ldx, 0}, {64, TC_BM, 1}) &&
               weights(&m[1], TC_BM) && weights(&m[4], 64);
     m[2] = m[3] = m[5] = m[0];
     if (ok && p.adapters)
-        ok = encode_map(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, TC_BM, 1}) &&
+        ok = l.maps->get(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, TC_BM, 1}) &&
              factors(&m[3], TC_BM) && factors(&m[5], 64);
     if (!ok)
         return cudaErrorNotSupported;

@@ -45,6 +45,7 @@ struct GradParams {
     LoraParts lay;
     int groups_j;        // tiles of rank values
     int stages, stage_bytes;
+    int box_rows;        // rows that a copy brings (what lies behind is zeroed, as others' rows)
     uint32_t idesc;      // with N = 0
     int* status;
     long long wait_budget;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                     const CUtensorMap* tmT = w.which ? &tmT1 : &tmT0;
                     if (whole)
                         mbar_arrive(bar);
-                    mbar_arrive_expect_tx(bar, (2 + w.chunks) * LG_BOX);
+                    mbar_arrive_expect_tx(bar, (2 + w.chunks) * p.box_rows * 128);
                     tma_load_2d(a0, tmP, bar, w.c0, tile * LT_ROWS);
                     tma_load_2d(a0 + LG_BOX, tmP, bar, w.c0 + 64, tile * LT_ROWS);
                     for (int c = 0; c < w.chunks; ++c)
@@ -514,6 +515,8 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
     p.idesc = tc_idesc(l.in_dtype == DT_BF16, 128, 0, true, true);
     p.status = l.status;
     p.wait_budget = l.wait_budget;
+    p.box_rows = std::min(LT_ROWS, (l.rows + 7) / 8 * 8);
+    const uint32_t box_rows = static_cast<uint32_t>(p.box_rows);
     CUtensorMap m[4];
     int64_t per[2] = {0, 0};
     for (int i = 0; i < 2; ++i) {
@@ -522,9 +525,9 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
         const LoraGradLaunch& s = *sides[i];
         p.side[i] = {(s.cols + 127) / 128, s.cols, s.G, s.step_c, s.step_j, s.stride_g};
         per[i] = static_cast<int64_t>(p.side[i].tiles_c) * p.groups_j;
-        if (!encode_map(&m[2 * i], s.in_dtype, s.P, 2, {s.cols, s.rows, 1}, {s.ldp, 0}, {64, LT_ROWS, 1}) ||
-            !encode_map(&m[2 * i + 1], s.in_dtype, s.t, 2, {p.lay.columns(), s.rows, 1},
-                        {p.lay.columns(), 0}, {64, LT_ROWS, 1}))
+        if (!s.maps->get(&m[2 * i], s.in_dtype, s.P, 2, {s.cols, s.rows, 1}, {s.ldp, 0}, {64, box_rows, 1}) ||
+            !s.maps->get(&m[2 * i + 1], s.in_dtype, s.t, 2, {p.lay.columns(), s.rows, 1},
+                        {p.lay.columns(), 0}, {64, box_rows, 1}))
             return cudaErrorNotSupported;
     }
     for (int i = 0; i < 2; ++i)

@@ -459,10 +459,10 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
         most_k = std::max(most_k, p.side[i].k_blocks);
         const int64_t stride = p.side[i].one ? s.ldf : s.stride_f;
         const int64_t stacked = p.side[i].one ? 1 : s.adapters;
-        if (!encode_map(&m[2 * i], s.in_dtype, s.X, 2, {s.K, s.rows, 1}, {s.ldx, 0}, {64, box_rows, 1}) ||
-            !(s.across ? encode_map(&m[2 * i + 1], s.in_dtype, s.F, 3, {s.rank, s.K, stacked}, {s.ldf, stride},
+        if (!s.maps->get(&m[2 * i], s.in_dtype, s.X, 2, {s.K, s.rows, 1}, {s.ldx, 0}, {64, box_rows, 1}) ||
+            !(s.across ? s.maps->get(&m[2 * i + 1], s.in_dtype, s.F, 3, {s.rank, s.K, stacked}, {s.ldf, stride},
                                     {64, TC_BK, 1})
-                       : encode_map(&m[2 * i + 1], s.in_dtype, s.F, 3, {s.K, s.rank, stacked}, {s.ldf, stride},
+                       : s.maps->get(&m[2 * i + 1], s.in_dtype, s.F, 3, {s.K, s.rank, stacked}, {s.ldf, stride},
                                     {64, cols, 1})))
             return cudaErrorNotSupported;
     }

@@ -473,15 +473,15 @@ cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     CUtensorMap m[4];
     const int dt = l.in_dtype;
     const uint32_t box = static_cast<uint32_t>(p.box_rows);
-    bool ok = encode_map(&m[0], dt, l.X, 2, {l.K, l.rows, 1}, {l.ldx, 0}, {64, box, 1}) &&
-              (l.across ? encode_map(&m[1], dt, l.W, 2, {l.N, l.K, 1}, {l.ldw, 0}, {64, TC_BK, 1})
-                        : encode_map(&m[1], dt, l.W, 2, {l.K, l.N, 1}, {l.ldw, 0}, {64, 128, 1}));
+    bool ok = l.maps->get(&m[0], dt, l.X, 2, {l.K, l.rows, 1}, {l.ldx, 0}, {64, box, 1}) &&
+              (l.across ? l.maps->get(&m[1], dt, l.W, 2, {l.N, l.K, 1}, {l.ldw, 0}, {64, TC_BK, 1})
+                        : l.maps->get(&m[1], dt, l.W, 2, {l.K, l.N, 1}, {l.ldw, 0}, {64, 128, 1}));
     m[2] = m[3] = m[0];
     if (ok && p.adapters > 0) {
         const int64_t stacked = p.one ? 1 : l.adapters, stride = p.one ? l.lde : l.stride_e;
-        ok = encode_map(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, box, 1}) &&
-             (l.across ? encode_map(&m[3], dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
-                       : encode_map(&m[3], dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride},
+        ok = l.maps->get(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, box, 1}) &&
+             (l.across ? l.maps->get(&m[3], dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
+                       : l.maps->get(&m[3], dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride},
                                     {p.beside ? static_cast<uint32_t>(p.lay.chunk) : 64u, 128, 1}));
     }
     if (!ok)
