@@ -85,8 +85,9 @@ def parse_args():
                          "unaligned 16-bit products in every operand layout, one JSON line each")
     ap.add_argument("--operators", action="store_true",
                     help="instead of the benchmark line: time the 8-bit products, their "
-                         "quantisation and the orthogonalisation on the cases of "
-                         "perf/operators.py, one JSON line each")
+                         "quantisation, the orthogonalisation, the products grouped by "
+                         "rows and the adapters on the cases of perf/operators.py and "
+                         "perf/more_operators.py, one JSON line each")
     ap.add_argument("--kernel-only", action="store_true",
                     help="time only the GEMM launches (no e2e, cuBLAS context or CPU "
                          "baseline); used for profiler captures")
@@ -979,26 +980,28 @@ def operator_floor_us(op, work, peaks):
     """The least time of a case at the measured rates: its compulsory bytes at
     the copy bandwidth or its operations at the burst rate of 16-bit products
     (twice that for 8-bit ones), whichever is longer."""
-    rate = {"quant": math.inf, "product": 2.0, "orth": 1.0}[op] * peaks["bf16_tflops"] * 1e12
+    rate = {"quant": math.inf, "product": 2.0}.get(op, 1.0) * peaks["bf16_tflops"] * 1e12
     return 1e6 * max(work["bytes"] / (peaks["hbm_gbs"] * 1e9), work["flops"] / rate)
 
 
 def run_operators(passes=60):
-    """Times the listed cases of perf/operators.py through the package: on the
-    device alone (a CUDA graph of the calls, over three sets of inputs in
-    turn) and as Python calls one after another."""
+    """Times the listed cases of perf/operators.py and perf/more_operators.py
+    through the package: on the device alone (a CUDA graph of the calls, over
+    three sets of inputs in turn) and as Python calls one after another."""
     import importlib.util
     import torch
     import tiled_matrix_multiplication_output_gb300 as tg
     tg.load_library(build_if_missing=True)
     torch.cuda.set_device(0)
-    spec = importlib.util.spec_from_file_location("operators",
-                                                  os.path.join(ROOT, "perf", "operators.py"))
-    ops = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(ops)
-    ops.own = True
     peaks, _ = load_peaks()
-    for case in ops.listed():
+    cases = []
+    for name in ("operators", "more_operators"):
+        spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
+        ops = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ops)
+        ops.own = True
+        cases += [(ops, case) for case in ops.listed()]
+    for ops, case in cases:
         states = [ops.prepare(case, seed) for seed in range(3)]
         for state in states * 2:
             ops.run(state)

@@ -123,3 +123,56 @@ def test_cpu_tensors_are_rejected():
                  lambda: tg.matmul_lora_backward(x, x, x, w, w, of)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_bench_floor_of_the_routed_operators():
+    import bench
+    peaks = {"hbm_gbs": 6800.0, "bf16_tflops": 1876.6}
+    for op in ("grouped", "wgrad", "lora", "lora_backward"):
+        assert bench.operator_floor_us(op, {"bytes": 6.8e9, "flops": 1.0}, peaks) == pytest.approx(1000.0)
+        assert bench.operator_floor_us(op, {"bytes": 1, "flops": 1.8766e12}, peaks) == pytest.approx(1000.0)
+
+
+def test_row_stacks_and_vectors_are_checked_before_the_library():
+    """The binding's own checks, on tensors that say they are on a device."""
+    from tiled_matrix_multiplication_output_gb300 import binding
+
+    class T:
+        def __init__(self, shape, stride, dtype=torch.bfloat16, device=0, contiguous=True):
+            self.shape, self._s, self.dtype, self._d, self._c = shape, stride, dtype, device, contiguous
+
+        def stride(self):
+            return self._s
+
+        def get_device(self):
+            return self._d
+
+        def is_contiguous(self):
+            return self._c
+
+        def data_ptr(self):
+            return 64
+
+    bf16, i32 = torch.bfloat16, torch.int32
+    assert binding._rows_of(T((4, 8), (10, 1)), "x", bf16, 0) == (4, 8, 10)
+    assert binding._rows_of(T((1, 9), (3, 1)), "x", bf16, 0) == (1, 9, 16)
+    assert binding._rows_of(T((4, 1), (5, 7)), "x", None, 0) == (4, 1, 5)
+    for bad in (T((4, 8), (7, 1)), T((4, 8), (16, 2)), T((4, 8, 2), (16, 2, 1)), T((4, 8), (8, 1), device=1)):
+        with pytest.raises(ValueError):
+            binding._rows_of(bad, "x", bf16, 0)
+    with pytest.raises(TypeError):
+        binding._rows_of(T((4, 8), (8, 1)), "x", torch.float16, 0)
+    assert binding._stack_of(T((3, 4, 8), (32, 8, 1)), "w", bf16, 0) == (3, 4, 8, 8, 32)
+    assert binding._stack_of(T((3, 4, 8), (0, 8, 1)), "w", bf16, 0) == (3, 4, 8, 8, 0)
+    assert binding._stack_of(T((1, 4, 8), (7, 8, 1)), "w", bf16, 0) == (1, 4, 8, 8, 32)
+    for bad in (T((3, 4, 8), (32, 8, 2)), T((3, 4, 8), (32, 7, 1)), T((4, 8), (8, 1)),
+                T((3, 4, 8), (32, 8, 1), device=-1)):
+        with pytest.raises(ValueError):
+            binding._stack_of(bad, "w", bf16, 0)
+    assert binding._vector_of(T((5,), (1,), i32), "o", 5, i32, 0) == 64
+    for bad in (T((4,), (1,), i32), T((5,), (2,), i32, contiguous=False), T((5, 1), (1, 1), i32),
+                T((5,), (1,), i32, device=2)):
+        with pytest.raises(ValueError):
+            binding._vector_of(bad, "o", 5, i32, 0)
+    with pytest.raises(TypeError):
+        binding._vector_of(T((5,), (1,), torch.int64), "o", 5, i32, 0)
