@@ -558,8 +558,9 @@ int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int64_t ldx,
  * adapter to the next, in elements).  The rows of different adapters may come
  * in any order; a row whose adapter[i] lies outside [0, adapters) has none.  No
  * row sees anything of another row's adapter, not even of one that is not
- * finite.  scale: device memory, one for each adapter, or null for 1.  rank
- * at most GEMM_MAX_RANK.  The pages have no counterpart.
+ * finite.  scale: device memory, one for each adapter, or null for 1.  At most
+ * GEMM_MAX_ADAPTERS adapters, of a rank up to GEMM_MAX_RANK.  The pages have no
+ * counterpart.
  *
  * The rank values scale * X_i A^T are FP32 sums.  On the tensor cores they
  * enter the second product in parts of the operands' type that together hold
@@ -569,6 +570,7 @@ int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int64_t ldx,
  * to run.  Types, alignment and pitches as gemm_grouped.
  */
 #define GEMM_MAX_RANK 256
+#define GEMM_MAX_ADAPTERS 65535
 
 typedef struct {
     const void* A;     /* adapters of rank x K */
@@ -583,10 +585,11 @@ typedef struct {
  * gemm_lora -- the forward product above.  X is rows x K, Y rows x N.
  *
  * workspace: gemm_lora_workspace_size() bytes of device memory for these very
- * operands; 256-byte aligned, not shared by calls that overlap in time.  Returns GEMM_OK, GEMM_ERR_INVALID_VALUE (null pointer
- * where data is needed, bad size, pitch, stride or enum, workspace missing,
- * misaligned or too small), GEMM_ERR_UNSUPPORTED (rank above GEMM_MAX_RANK)
- * or GEMM_ERR_CUDA.
+ * operands; 256-byte aligned, not shared by calls that overlap in time.
+ * Without adapters, or with rank 0, neither `adapter` nor A and B are read.
+ * Returns GEMM_OK, GEMM_ERR_INVALID_VALUE (null pointer where data is needed,
+ * bad size, pitch, stride or enum, workspace missing, misaligned or too
+ * small), GEMM_ERR_UNSUPPORTED (rank above GEMM_MAX_RANK) or GEMM_ERR_CUDA.
  */
 size_t gemm_lora_workspace_size(const void* X, int64_t ldx, const void* W, int64_t ldw,
                                 const gemm_lora_t* lora, int64_t rows, int64_t N, int64_t K,

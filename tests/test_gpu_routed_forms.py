@@ -213,3 +213,25 @@ def test_backward_captured_beside_an_eager_graph():
     torch.cuda.synchronize()
     assert torch.equal(y, eager.detach()) and torch.equal(da, want)
     assert torch.equal(torch.autograd.grad(eager, a, c.dy.float())[0], want)
+
+
+@pytest.mark.parametrize("dtype", [tg.F32, tg.BF16])
+@pytest.mark.parametrize("rows", [3, 300, 5000])
+@pytest.mark.parametrize("adapters, rank", [(0, 8), (4, 0), (0, 0)])
+def test_no_adapters_reads_no_pointer_of_theirs(dtype, rows, adapters, rank):
+    """Small, large and FP32 forms with every adapter pointer null."""
+    N, K = 1304, 136
+    name = "f32" if dtype == tg.F32 else "bf16"
+    x, w, dy = _ints(1, name, rows, K), _ints(2, name, N, K), _ints(3, name, rows, N)
+    lora = tg.LoraAdapters(None, 0, 0, None, 0, 0, None, adapters, rank)
+    y, dx = torch.empty(rows, N, device="cuda"), torch.empty(rows, K, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert tg.gemm_lora_workspace_size(x.data_ptr(), K, w.data_ptr(), K, lora, rows, N, K, dtype,
+                                       tg.F32) == 0
+    assert tg.gemm_lora(x.data_ptr(), K, w.data_ptr(), K, lora, None, y.data_ptr(), N, rows, N, K,
+                        dtype, tg.F32, None, 0, stream) == tg.binding.OK
+    assert tg.gemm_lora_backward(dy.data_ptr(), N, None, 0, w.data_ptr(), K, lora, None, dx.data_ptr(),
+                                 K, None, 0, 0, None, 0, 0, rows, N, K, dtype, tg.F32, tg.F32, None, 0,
+                                 stream) == tg.binding.OK
+    assert torch.equal(y.double(), x.double() @ w.double().T)
+    assert torch.equal(dx.double(), dy.double() @ w.double())

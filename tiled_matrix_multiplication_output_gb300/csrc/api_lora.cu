@@ -19,8 +19,6 @@ static_assert(kMaxRank == GEMM_MAX_RANK, "the largest rank");
 
 namespace {
 
-constexpr int64_t kMaxAdapters = 65535;
-
 size_t round256(int64_t n) { return static_cast<size_t>((n + 255) / 256 * 256); }
 
 // Whether there is an adapter that can change anything.
@@ -29,7 +27,7 @@ bool has_adapters(const gemm_lora_t& a) { return a.adapters > 0 && a.rank > 0; }
 int check_sizes(const gemm_lora_t* a, int64_t rows, int64_t N, int64_t K, int in_dtype, int out_dtype)
 {
     if (!a || !valid_size(rows) || !valid_size(N) || !valid_size(K) || a->adapters < 0 || a->rank < 0 ||
-        a->adapters > kMaxAdapters || !valid_dtype(in_dtype) || !valid_dtype(out_dtype))
+        a->adapters > GEMM_MAX_ADAPTERS || !valid_dtype(in_dtype) || !valid_dtype(out_dtype))
         return GEMM_ERR_INVALID_VALUE;
     return a->rank > GEMM_MAX_RANK ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
 }

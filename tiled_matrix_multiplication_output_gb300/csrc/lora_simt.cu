@@ -15,7 +15,7 @@ __device__ __forceinline__ void load_adapters(int (&s)[ST_M], const int32_t* ada
     __syncthreads();
     if (threadIdx.x < ST_M) {
         const int i = row0 + threadIdx.x;
-        const int g = i < rows ? adapter[i] : -1;
+        const int g = adapters > 0 && i < rows ? adapter[i] : -1;
         s[threadIdx.x] = g >= 0 && g < adapters ? g : -1;
     }
     __syncthreads();

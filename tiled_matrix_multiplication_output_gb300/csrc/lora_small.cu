@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     const int kb0 = split * per, kb1 = min(kb0 + per, p.k_blocks);
     const TcWatch watch{&s.abort_flag, p.status, p.wait_budget};
     // each row's adapter, asked for before anything else
-    const int g = warp >= 4 ? row_adapter(p.adapter, row0 + static_cast<int>(threadIdx.x) - 128, p.M, p.adapters)
-                            : -1;
+    const int g = warp >= 4 && p.adapters > 0
+                      ? row_adapter(p.adapter, row0 + static_cast<int>(threadIdx.x) - 128, p.M, p.adapters)
+                      : -1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -153,158 +154,156 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     const uint32_t held = ring + p.ring;  // the tile's rank values
 
     if (warp == 0) {
-        {
-            int stage = 0, n = 0;
-            uint32_t phase = 0;
-            auto step = [&](bool skip, uint32_t bytes, auto load) {
-                if (!warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch))
-                    return false;
-                if (!skip) {
-                    const uint32_t bar = smem_u32(&s.full[stage]);
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, bytes);
-                        load(ring + stage * p.stage_bytes + 16384, ring + stage * p.stage_bytes, bar);
-                    }
-                    __syncwarp();
-                    ++n;
+        int stage = 0, n = 0;
+        uint32_t phase = 0;
+        auto step = [&](bool skip, uint32_t bytes, auto load) {
+            if (!warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch))
+                return false;
+            if (!skip) {
+                const uint32_t bar = smem_u32(&s.full[stage]);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, bytes);
+                    load(ring + stage * p.stage_bytes + 16384, ring + stage * p.stage_bytes, bar);
                 }
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-                return true;
-            };
-            bool ok = true;
-            for (int kb = kb0; ok && kb < kb1; ++kb)
-                ok = step(kb == p.fault_skip_kblock, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
-                    if (ACROSS) {
-                        tma_load_2d(dB, &tmW, bar, col0, kb * TC_BK);
-                        tma_load_2d(dB + 8192, &tmW, bar, col0 + 64, kb * TC_BK);
-                    } else {
-                        tma_load_2d(dB, &tmW, bar, kb * TC_BK, col0);
-                    }
-                    tma_load_2d(dA, &tmX, bar, kb * TC_BK, row0);
-                });
-            if (ok && p.adapters > 0) {
-                ok = warp_wait(smem_u32(&s.planned), 0, watch);
-                if (!ACROSS && p.beside > 0) {
-                    for (int a = split; ok && a < s.plan.count; a += p.beside * SPLITS) {
-                        const int some = min(p.beside, (s.plan.count - a + SPLITS - 1) / SPLITS);
-                        const uint32_t each = p.lay.chunk * 2 * 128;
-                        ok = step(false, some * each, [&](uint32_t, uint32_t dB, uint32_t bar) {
-                            for (int i = 0; i < some; ++i)
-                                tma_load_3d(dB + i * each, &tmE, bar, 0, col0,
-                                            p.one ? 0 : s.plan.ids[a + i * SPLITS]);
-                        });
-                    }
-                } else {
-                    grid_dep_wait();  // the rank values come with the factors
-                    for (int a = split; ok && a < s.plan.count; a += SPLITS) {
-                        const int z = p.one ? 0 : s.plan.ids[a];
-                        for (int c = 0; ok && c < p.lay.chunks; ++c) {
-                            const int j = c * p.lay.chunk;
-                            ok = step(false, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
-                                if (ACROSS) {
-                                    tma_load_3d(dB, &tmE, bar, col0, j, z);
-                                    tma_load_3d(dB + 8192, &tmE, bar, col0 + 64, j, z);
-                                } else {
-                                    tma_load_3d(dB, &tmE, bar, j, col0, z);
-                                }
-                                tma_load_2d(dA, &tmT, bar, c * 64, row0);
-                            });
-                        }
-                    }
-                }
+                __syncwarp();
+                ++n;
             }
-            if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before shared memory goes away
-                for (int i = 0; i < p.stages; ++i) {
-                    const int uses = n / p.stages + (i < n % p.stages);
-                    const long long t0 = clock64();
-                    while (uses > 0 && !mbar_try_wait(smem_u32(&s.full[i]), (uses - 1) & 1) &&
-                           clock64() - t0 < p.wait_budget) {
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+            return true;
+        };
+        bool ok = true;
+        for (int kb = kb0; ok && kb < kb1; ++kb)
+            ok = step(kb == p.fault_skip_kblock, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                if (ACROSS) {
+                    tma_load_2d(dB, &tmW, bar, col0, kb * TC_BK);
+                    tma_load_2d(dB + 8192, &tmW, bar, col0 + 64, kb * TC_BK);
+                } else {
+                    tma_load_2d(dB, &tmW, bar, kb * TC_BK, col0);
+                }
+                tma_load_2d(dA, &tmX, bar, kb * TC_BK, row0);
+            });
+        if (ok && p.adapters > 0) {
+            ok = warp_wait(smem_u32(&s.planned), 0, watch);
+            if (!ACROSS && p.beside > 0) {
+                for (int a = split; ok && a < s.plan.count; a += p.beside * SPLITS) {
+                    const int some = min(p.beside, (s.plan.count - a + SPLITS - 1) / SPLITS);
+                    const uint32_t each = p.lay.chunk * 2 * 128;
+                    ok = step(false, some * each, [&](uint32_t, uint32_t dB, uint32_t bar) {
+                        for (int i = 0; i < some; ++i)
+                            tma_load_3d(dB + i * each, &tmE, bar, 0, col0,
+                                        p.one ? 0 : s.plan.ids[a + i * SPLITS]);
+                    });
+                }
+            } else {
+                grid_dep_wait();  // the rank values come with the factors
+                for (int a = split; ok && a < s.plan.count; a += SPLITS) {
+                    const int z = p.one ? 0 : s.plan.ids[a];
+                    for (int c = 0; ok && c < p.lay.chunks; ++c) {
+                        const int j = c * p.lay.chunk;
+                        ok = step(false, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                            if (ACROSS) {
+                                tma_load_3d(dB, &tmE, bar, col0, j, z);
+                                tma_load_3d(dB + 8192, &tmE, bar, col0 + 64, j, z);
+                            } else {
+                                tma_load_3d(dB, &tmE, bar, j, col0, z);
+                            }
+                            tma_load_2d(dA, &tmT, bar, c * 64, row0);
+                        });
                     }
                 }
             }
         }
+        if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before shared memory goes away
+            for (int i = 0; i < p.stages; ++i) {
+                const int uses = n / p.stages + (i < n % p.stages);
+                const long long t0 = clock64();
+                while (uses > 0 && !mbar_try_wait(smem_u32(&s.full[i]), (uses - 1) & 1) &&
+                       clock64() - t0 < p.wait_budget) {
+                }
+            }
+        }
     } else if (warp == 1) {
-        {
-            int stage = 0;
-            uint32_t phase = 0;
-            auto step = [&](auto multiply) {
-                if (!warp_wait(smem_u32(&s.full[stage]), phase, watch))
-                    return false;
-                tc_fence_after();
-                if (elect_one()) {
-                    multiply(ring + stage * p.stage_bytes + 16384, ring + stage * p.stage_bytes);
-                    tc_commit(smem_u32(&s.empty[stage]));
-                }
-                __syncwarp();
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-                return true;
-            };
-            bool ok = true;
-            for (int kb = kb0; ok && kb < kb1; ++kb)
-                ok = step([&](uint32_t a0, uint32_t b0) {
-#pragma unroll
-                    for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
-                        tc_mma_f16<1>(tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
-                                      ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                             : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                      p.idesc, kb != kb0 || k != 0);
-                });
-            if (ok && p.adapters > 0) {
-                ok = warp_wait(smem_u32(&s.planned), 0, watch);
-                auto others = [&](int a, uint32_t (&off)[4]) {
-                    const uint4 rows = *reinterpret_cast<const uint4*>(s.plan.rows[a]);
-                    off[0] = ~rows.x;
-                    off[1] = ~rows.y;
-                    off[2] = ~rows.z;
-                    off[3] = ~rows.w;
-                };
-                if (!ACROSS && p.beside > 0) {
-                    const uint32_t width = p.lay.chunk * 2;
-                    const int deep = p.lay.deep(0, p.rank);
-                    ok = ok && warp_wait(smem_u32(&s.held), 0, watch);
-                    for (int a = split; ok && a < s.plan.count; a += p.beside * SPLITS)
-                        ok = step([&](uint32_t, uint32_t b0) {
-                            const int some = min(p.beside, (s.plan.count - a + SPLITS - 1) / SPLITS);
-                            for (int i = 0; i < some; ++i, b0 += width * 128) {
-                                uint32_t off[4];
-                                others(a + i * SPLITS, off);
-                                for (int part = 0; part < p.lay.parts; ++part)
-                                    for (int k = 0; k < deep; ++k)
-                                        tc_mma_f16_lanes(tmem,
-                                                         smem_desc_sw128(held + part * width + k * 32, 16, 1024),
-                                                         smem_desc_rows(b0 + k * 32, width), p.idesc, 1, off);
-                            }
-                        });
-                } else {
-                    for (int a = split; ok && a < s.plan.count; a += SPLITS) {
-                        uint32_t off[4];
-                        others(a, off);
-                        for (int c = 0; ok && c < p.lay.chunks; ++c)
-                            ok = step([&](uint32_t a0, uint32_t b0) {
-                                const int deep = p.lay.deep(c, p.rank);
-                                for (int part = 0; part < p.lay.parts; ++part)
-                                    for (int k = 0; k < deep; ++k)
-                                        tc_mma_f16_lanes(
-                                            tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
-                                            ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                                   : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                            p.idesc, 1, off);
-                            });
-                    }
-                }
+        int stage = 0;
+        uint32_t phase = 0;
+        auto step = [&](auto multiply) {
+            if (!warp_wait(smem_u32(&s.full[stage]), phase, watch))
+                return false;
+            tc_fence_after();
+            if (elect_one()) {
+                multiply(ring + stage * p.stage_bytes + 16384, ring + stage * p.stage_bytes);
+                tc_commit(smem_u32(&s.empty[stage]));
             }
-            if (elect_one())
-                tc_commit(smem_u32(&s.done));  // also after giving up: nothing may run on
             __syncwarp();
-            const long long t0 = clock64();
-            while (!mbar_try_wait(smem_u32(&s.done), 0) && clock64() - t0 < p.wait_budget) {
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1;
             }
+            return true;
+        };
+        bool ok = true;
+        for (int kb = kb0; ok && kb < kb1; ++kb)
+            ok = step([&](uint32_t a0, uint32_t b0) {
+#pragma unroll
+                for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
+                    tc_mma_f16<1>(tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
+                                  ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                         : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                  p.idesc, kb != kb0 || k != 0);
+            });
+        if (ok && p.adapters > 0) {
+            ok = warp_wait(smem_u32(&s.planned), 0, watch);
+            auto others = [&](int a, uint32_t (&off)[4]) {
+                const uint4 rows = *reinterpret_cast<const uint4*>(s.plan.rows[a]);
+                off[0] = ~rows.x;
+                off[1] = ~rows.y;
+                off[2] = ~rows.z;
+                off[3] = ~rows.w;
+            };
+            if (!ACROSS && p.beside > 0) {
+                const uint32_t width = p.lay.chunk * 2;
+                const int deep = p.lay.deep(0, p.rank);
+                grid_dep_wait();  // (so that no wait spans the kernel before)
+                ok = ok && warp_wait(smem_u32(&s.held), 0, watch);
+                for (int a = split; ok && a < s.plan.count; a += p.beside * SPLITS)
+                    ok = step([&](uint32_t, uint32_t b0) {
+                        const int some = min(p.beside, (s.plan.count - a + SPLITS - 1) / SPLITS);
+                        for (int i = 0; i < some; ++i, b0 += width * 128) {
+                            uint32_t off[4];
+                            others(a + i * SPLITS, off);
+                            for (int part = 0; part < p.lay.parts; ++part)
+                                for (int k = 0; k < deep; ++k)
+                                    tc_mma_f16_lanes(tmem,
+                                                     smem_desc_sw128(held + part * width + k * 32, 16, 1024),
+                                                     smem_desc_rows(b0 + k * 32, width), p.idesc, 1, off);
+                        }
+                    });
+            } else {
+                grid_dep_wait();
+                for (int a = split; ok && a < s.plan.count; a += SPLITS) {
+                    uint32_t off[4];
+                    others(a, off);
+                    for (int c = 0; ok && c < p.lay.chunks; ++c)
+                        ok = step([&](uint32_t a0, uint32_t b0) {
+                            const int deep = p.lay.deep(c, p.rank);
+                            for (int part = 0; part < p.lay.parts; ++part)
+                                for (int k = 0; k < deep; ++k)
+                                    tc_mma_f16_lanes(
+                                        tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
+                                        ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                               : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                        p.idesc, 1, off);
+                        });
+                }
+            }
+        }
+        if (elect_one())
+            tc_commit(smem_u32(&s.done));  // also after giving up: nothing may run on
+        __syncwarp();
+        const long long t0 = clock64();
+        while (!mbar_try_wait(smem_u32(&s.done), 0) && clock64() - t0 < p.wait_budget) {
         }
     } else if (warp == 2 && p.adapters > 0) {
         grid_dep_wait();
@@ -328,9 +327,11 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     float* sums = reinterpret_cast<float*>(base);
     if (warp >= 4) {
         const int q = warp & 3;
+        if (p.adapters > 0)
+            grid_dep_wait();  // (so that no wait spans the kernel before)
         int ok = 1;
         if (lane == 0)
-            ok = tc_wait(smem_u32(&s.done), 0, watch) ? 1 : 0;
+            ok = tc_wait(smem_u32(&s.done), 0, patient(watch, p.k_blocks)) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (ok && q * 32 < rows) {
             tc_fence_after();

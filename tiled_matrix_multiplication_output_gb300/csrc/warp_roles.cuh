@@ -29,6 +29,13 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const T
     }
 }
 
+// For a wait that spans `steps` K steps (a whole tile's): a step takes well below
+// 2^-18 of the budget.
+__device__ __forceinline__ TcWatch patient(TcWatch w, int steps)
+{
+    w.budget *= 1 + (steps >> 18);
+    return w;
+}
 
 // tma_load_2d_pair of a 3-D box.
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
