@@ -47,7 +47,8 @@ public:
     bool get(CUtensorMap* map, int dt, const void* base, int rank, const int64_t (&dims)[3],
              const int64_t (&strides)[2], const uint32_t (&box)[3])
     {
-        const Key key{base, {dims[0], dims[1], dims[2]}, {strides[0], strides[1]}, {box[0], box[1], box[2]}, dt, rank};
+        const Key key{base, {dims[0], dims[1], dims[2]}, {strides[0], strides[1]}, {box[0], box[1], box[2]},
+                      dt, rank};
         for (int i = 0; i < n_; ++i)
             if (key == keys_[i]) {
                 *map = maps_[i];

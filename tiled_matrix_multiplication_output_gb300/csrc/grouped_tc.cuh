@@ -23,9 +23,8 @@
 // warps' registers.
 //
 // Warps: 0 TMA producer, 1 MMA issuer (of the leader CTA), 2 on epilogue (four; for
-// the gradient eight, and a last warp that zeroes).  The ring of two 64-deep K steps per stage with a
-// barrier each, the bounded waits and the two accumulators in tensor memory
-// are those of tc_gemm_kernel.
+// the gradient eight, and a last warp that zeroes).  A ring of K steps, bounded waits
+// and two accumulators in tensor memory, as in tc_gemm_kernel.
 #pragma once
 
 #include <cuda.h>
@@ -46,7 +45,7 @@ constexpr int GT_MAX_STAGES = 10;
 constexpr int GT_A_BYTES = TC_BM * TC_BK * 2;  // a K step of the lanes' side
 constexpr int GT_N = 256;        // the N side of a full tile
 constexpr int GT_SORTED = 256;   // groups, at most, that the gradient sorts
-constexpr int GT_SEGMENT = 12;  // K steps of the gradient that one accumulator adds up
+constexpr int GT_SEGMENT = 12;   // K steps of the gradient that one accumulator adds up
 
 struct GroupedTcParams {
     Grouping by;
@@ -424,10 +423,10 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         const uint32_t staging = sbase + L::OFF_STAGING + (warp - 2) * L::STAGING;
         // waits for the next accumulator; gives it back
         int local = 0;
-        auto take = [&] {
+        auto take = [&](int steps) {
             int ok = 1;
             if (lane == 0)
-                ok = tc_wait(tfull_bar(local & 1), (local >> 1) & 1, watch) ? 1 : 0;
+                ok = tc_wait(tfull_bar(local & 1), (local >> 1) & 1, patient(watch, steps)) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             tc_fence_after();
             return ok != 0;
@@ -447,7 +446,7 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                                static_cast<int64_t>(gridDim.x) * 128);
             for (int t = unit; t < num_work; t += num_units) {
                 const GroupedWork w = grouped_work<MODE>(t, table, p);
-                if (!take())
+                if (!take(w.k_blocks))
                     break;
                 const int f = w.f0 + static_cast<int>(rank) * TC_BM + q * 32;
                 const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * GT_N);
@@ -481,7 +480,7 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                 const GroupedWork w = grouped_work<MODE>(t, table, p);
                 float sum[CHUNKS][32] = {};
                 for (int kb = 0; kb < w.k_blocks; kb += GT_SEGMENT) {
-                    ok = take();
+                    ok = take(GT_SEGMENT);
                     if (!ok)
                         break;
                     const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * GT_N + half * HALF);

@@ -71,8 +71,9 @@ constexpr int LORA_PLAN_BYTES = 2576;
 int lora_parts_bytes(int rank, int parts);
 
 // On the tensor cores: 16-bit operands with rows on 16-byte boundaries (pack.h),
-// no size of zero.  Shrink makes the plans and the rank values; of two products, whose rows have the
-// same adapters, in one launch.  Expand may start while a shrink runs.
+// no size of zero.  Shrink makes the plans and the rank values; of two products,
+// whose rows have the same adapters, in one launch.  Expand may start while a
+// shrink runs.
 cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* second, cudaStream_t stream);
 // Whether a shrink alone leaves room on its SMs for the product's kernel.
 bool lora_shrink_shares(const LoraLaunch& l);

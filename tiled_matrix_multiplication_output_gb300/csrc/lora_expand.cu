@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
     } else {
         // ------------------------------------------------ epilogue
+        if (p.adapters)
+            grid_dep_wait();  // (the first tile ends no sooner: its wait begins here)
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const uint32_t staging = sbase + L::OFF_STAGING + q * 4096;
         const uint32_t leader_tempty0 = mapa_shared(tempty_bar(0), 0);
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const int acc = local & 1;
             int ok = 1;
             if (lane == 0)
-                ok = tc_wait(tfull_bar(acc), (local >> 1) & 1, watch) ? 1 : 0;
+                ok = tc_wait(tfull_bar(acc), (local >> 1) & 1, patient(watch, p.k_blocks)) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok)
                 break;

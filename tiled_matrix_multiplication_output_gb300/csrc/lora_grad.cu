@@ -151,7 +151,6 @@ __device__ __forceinline__ GradItem grad_item(int t, const GradParams& p, const 
     return w;
 }
 
-
 // The row tiles that hold rows of adapter g, in order; a whole warp steps through
 // them together.
 class RowTiles {
@@ -369,14 +368,12 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                 ++local;
             }
         }
-        {
-            // Wait (bounded) until every MMA issued so far has completed.
-            if (elect_one())
-                tc_commit(smem_u32(&s.drain));
-            __syncwarp();
-            const long long t0 = clock64();
-            while (!mbar_try_wait(smem_u32(&s.drain), 0) && clock64() - t0 < p.wait_budget) {
-            }
+        // Wait (bounded) until every MMA issued so far has completed.
+        if (elect_one())
+            tc_commit(smem_u32(&s.drain));
+        __syncwarp();
+        const long long t0 = clock64();
+        while (!mbar_try_wait(smem_u32(&s.drain), 0) && clock64() - t0 < p.wait_budget) {
         }
     } else if (warp < 4) {
         // ------------------------------------------------ rows of other adapters
@@ -430,7 +427,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             const bool any = steps > 0;
             const int acc = local & 1;
             if (any) {
-                if (!warp_wait(smem_u32(&s.tfull[acc]), (local >> 1) & 1, watch))
+                if (!warp_wait(smem_u32(&s.tfull[acc]), (local >> 1) & 1, patient(watch, 2 * p.plans)))
                     break;
                 ++local;
                 tc_fence_after();

@@ -154,47 +154,45 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     auto nth = [&](int i) { return deal + i * p.deal; };
 
     if (warp == 0) {
-        {
-            int stage = 0, n = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int i0 = 0; ok && i0 < mine; i0 += p.together) {
-                const int some = min(p.together, mine - i0);
-                for (int kb = kb0; kb < kb1; ++kb, ++n) {
-                    ok = warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch);
-                    if (!ok)
-                        break;
-                    const uint32_t bar = smem_u32(&s.full[stage]);
-                    const uint32_t base = smem_u32(ring) + stage * p.stage_bytes;
-                    const uint32_t dA = base + p.a_offset;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, p.box_rows * 128 + some * b_bytes);
-                        tma_load_2d(dA, tmX, bar, kb * TC_BK, row0);
-                        for (int i = 0; i < some; ++i) {
-                            const int z = side.one ? 0 : s.plan.ids[nth(i0 + i)];
-                            const uint32_t dB = base + i * b_bytes;
-                            if (side.across) {
-                                for (int b = 0; b * 8192 < b_bytes; ++b)
-                                    tma_load_3d(dB + b * 8192, tmF, bar, b * 64, kb * TC_BK, z);
-                            } else {
-                                tma_load_3d(dB, tmF, bar, kb * TC_BK, 0, z);
-                            }
+        int stage = 0, n = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int i0 = 0; ok && i0 < mine; i0 += p.together) {
+            const int some = min(p.together, mine - i0);
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                ok = warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch);
+                if (!ok)
+                    break;
+                const uint32_t bar = smem_u32(&s.full[stage]);
+                const uint32_t base = smem_u32(ring) + stage * p.stage_bytes;
+                const uint32_t dA = base + p.a_offset;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, p.box_rows * 128 + some * b_bytes);
+                    tma_load_2d(dA, tmX, bar, kb * TC_BK, row0);
+                    for (int i = 0; i < some; ++i) {
+                        const int z = side.one ? 0 : s.plan.ids[nth(i0 + i)];
+                        const uint32_t dB = base + i * b_bytes;
+                        if (side.across) {
+                            for (int b = 0; b * 8192 < b_bytes; ++b)
+                                tma_load_3d(dB + b * 8192, tmF, bar, b * 64, kb * TC_BK, z);
+                        } else {
+                            tma_load_3d(dB, tmF, bar, kb * TC_BK, 0, z);
                         }
                     }
-                    __syncwarp();
-                    if (++stage == p.stages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before shared memory goes away
-                for (int i = 0; i < p.stages; ++i) {
-                    const int uses = n / p.stages + (i < n % p.stages);
-                    const long long t0 = clock64();
-                    while (uses > 0 && !mbar_try_wait(smem_u32(&s.full[i]), (uses - 1) & 1) &&
-                           clock64() - t0 < p.wait_budget) {
-                    }
+        }
+        if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before shared memory goes away
+            for (int i = 0; i < p.stages; ++i) {
+                const int uses = n / p.stages + (i < n % p.stages);
+                const long long t0 = clock64();
+                while (uses > 0 && !mbar_try_wait(smem_u32(&s.full[i]), (uses - 1) & 1) &&
+                       clock64() - t0 < p.wait_budget) {
                 }
             }
         }
@@ -252,7 +250,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
         if (steps > 0) {
             int ok = 1;
             if (lane == 0)
-                ok = tc_wait(smem_u32(&s.done), 0, watch) ? 1 : 0;
+                ok = tc_wait(smem_u32(&s.done), 0, patient(watch, steps)) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (ok) {
                 tc_fence_after();
@@ -453,8 +451,8 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
     for (int i = 0; i < sides; ++i) {
         const LoraLaunch& s = i ? *second : first;
         const uint32_t cols = static_cast<uint32_t>(p.cols);
-        p.side[i] = {(s.K + TC_BK - 1) / TC_BK, s.across, s.adapters == 1 || s.stride_f == 0, tc_idesc(s.in_dtype == DT_BF16, LT_ROWS, p.cols, false, s.across),
-                     s.t};
+        p.side[i] = {(s.K + TC_BK - 1) / TC_BK, s.across, s.adapters == 1 || s.stride_f == 0,
+                     tc_idesc(s.in_dtype == DT_BF16, LT_ROWS, p.cols, false, s.across), s.t};
         p.b_bytes[i] = (s.across ? (p.cols + 63) / 64 * 64 : p.cols) * 128;
         most_k = std::max(most_k, p.side[i].k_blocks);
         const int64_t stride = p.side[i].one ? s.ldf : s.stride_f;
