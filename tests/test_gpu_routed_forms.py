@@ -133,17 +133,20 @@ def _grouped_calls():
     x, dy = _ints(9, "bf16", 1040, 320), _ints(10, "bf16", 1040, 264)
     w = _ints(11, "bf16", 4, 264, 320)
     few, many = Case(60, 264, 320, 5, 16, "bf16", ints=True), Case(2100, 2056, 320, 5, 16, "bf16", ints=True)
+    each = Case(60, 264, 320, 60, 16, "bf16", ints=True)
     return {
         "t": lambda: (tg.matmul_grouped(x, w, off),),
         "n": lambda: (tg.matmul_grouped(dy, w, off, op_b="n"),),
         "wgrad": lambda: (tg.matmul_grouped_wgrad(dy, x, off),),
         "lora few tiles": lambda: (few.forward(),),
+        "lora many adapters": lambda: (each.forward(),),
         "lora many tiles": lambda: (many.forward(),),
         "lora backward": lambda: many.backward(),
     }
 
 
-@pytest.mark.parametrize("name", ["t", "n", "wgrad", "lora few tiles", "lora many tiles", "lora backward"])
+@pytest.mark.parametrize("name", ["t", "n", "wgrad", "lora few tiles", "lora many adapters", "lora many tiles",
+                                  "lora backward"])
 def test_a_wait_that_runs_out_is_reported(name):
     """The producer skips one K step (10 ms a wait): the status says so, the context stays
     usable, and the next call is right."""
@@ -235,3 +238,56 @@ def test_no_adapters_reads_no_pointer_of_theirs(dtype, rows, adapters, rank):
                                  stream) == tg.binding.OK
     assert torch.equal(y.double(), x.double() @ w.double().T)
     assert torch.equal(dx.double(), dy.double() @ w.double())
+
+
+# rows, N, K, adapters, rank: one kernel makes the rank values (cases with up to 32
+# adapters x K steps of a CTA), on clusters of 1, 2, 4 and 8, with the factors of more
+# adapters than come beside W, several tiles of rows, K steps that wrap the ring
+OWN = [
+    (1, 8, 8, 1, 1), (1, 136, 4096, 1, 16), (5, 1000, 2048, 4, 8), (40, 136, 64, 20, 16), (40, 136, 128, 30, 5),
+    (90, 264, 130, 10, 32), (128, 2048, 1024, 3, 8), (128, 2432, 520, 2, 17), (130, 4744, 1024, 2, 12),
+    (300, 500, 4000, 3, 16), (1000, 1000, 960, 2, 24), (77, 131, 515, 6, 7), (2000, 200, 400, 16, 16),
+]
+
+
+@pytest.mark.parametrize("case", OWN, ids=str)
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_rank_values_made_by_the_products_kernel(case, dtype):
+    rows, N, K, G, r = case
+    for out in (DT[dtype], torch.float32):
+        c = Case(rows, N, K, G, r, dtype, seed=rows + r)
+        y = c.forward(out_dtype=out)
+        c.check_forward(y)
+        assert torch.equal(c.forward(out_dtype=out), y)  # identical run to run
+        c = Case(rows, N, K, G, r, dtype, ints=True)
+        want = c.x.double() @ c.w.double().T
+        for g in range(G):
+            of = c.adapter == g
+            t = c.scale[g].double() * (c.x[of].double() @ c.a[g].double().T)
+            want[of] += t @ c.b[g].double().T
+        assert torch.equal(c.forward(out_dtype=out).double(), want.to(out).double())
+
+
+def test_few_adapters_need_one_launch_and_no_workspace():
+    c = Case(5, 1000, 2048, 4, 8, "bf16")
+    lora = tg.LoraAdapters(c.a.data_ptr(), 2048, 8 * 2048, c.b.data_ptr(), 8, 8000, None, 4, 8)
+    assert tg.gemm_lora_workspace_size(c.x.data_ptr(), 2048, c.w.data_ptr(), 2048, lora, 5, 1000, 2048,
+                                       tg.BF16, tg.BF16) == 0
+    c.forward()
+    n = tg.gemm_launch_count()
+    c.forward()
+    assert tg.gemm_launch_count() == n + 1
+
+
+@pytest.mark.parametrize("rows", [1, 30, 200])
+def test_one_kernel_keeps_infinities_of_other_adapters_away(rows):
+    c = Case(rows, 264, 520, 3, 12, "bf16", seed=3)
+    c.adapter.copy_(torch.arange(rows) % 4 - 1)
+    clean = c.forward()
+    c.a[1] = float("inf")
+    c.b[2] = float("nan")
+    y = c.forward()
+    keep = (c.adapter != 1) & (c.adapter != 2)
+    assert torch.equal(y[keep], clean[keep]) and not torch.isfinite(y[~keep]).any()
+    c.x[0] = float("inf")  # an infinity in a row stays in it
+    assert torch.equal(c.forward()[keep][1:], clean[keep][1:])

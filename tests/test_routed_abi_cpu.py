@@ -77,7 +77,7 @@ def _lora(X=P, ldx=64, W=P, ldw=64, lora=None, of=P, Y=P, ldy=32, rows=10, N=32,
 
 
 def test_lora_rejects_bad_arguments():
-    def size(rows, r=8, G=3, dt=tg.BF16, ldx=64):
+    def size(rows, r=40, G=3, dt=tg.BF16, ldx=64):
         return tg.gemm_lora_workspace_size(P, ldx, P, 64, _adapters(G=G, r=r), rows, 32, 64, dt, tg.F32)
 
     assert 0 < size(10) < size(1000) < size(1000, r=200)
@@ -87,7 +87,7 @@ def test_lora_rejects_bad_arguments():
     for bad in (dict(X=None), dict(W=None), dict(Y=None), dict(of=None), dict(ldx=63), dict(ldw=63),
                 dict(ldy=31), dict(rows=-1), dict(N=BIG + 1), dict(K=-1), dict(dt=3), dict(out=-1),
                 dict(ws=None), dict(ws=P + 16), dict(nbytes=need - 1)):
-        assert _lora(**bad) == INV, bad
+        assert _lora(lora=_adapters(r=40, ldb=40, sb=32 * 40), **bad) == INV, bad
     for bad in (dict(A=None), dict(B=None), dict(lda=63), dict(ldb=7), dict(sa=-1), dict(sb=-1),
                 dict(G=-1), dict(G=65536), dict(r=-1)):
         assert _lora(lora=_adapters(**bad)) == INV, bad

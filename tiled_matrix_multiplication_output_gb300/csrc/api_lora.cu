@@ -76,10 +76,11 @@ struct Operands {
 struct Workspace {
     size_t values, plans, copies;
     int sides;
+    // sides 0: the copies alone
     Workspace(int sides_, const gemm_lora_t& l, int64_t rows, int parts, const Operands& o)
         : values(0), plans(0), copies(o.packing.bytes()), sides(sides_)
     {
-        if (!has_adapters(l))
+        if (!has_adapters(l) || sides == 0)
             return;
         values = round256(rows * (o.tc ? lora_parts_bytes(static_cast<int>(l.rank), parts) : l.rank * 4));
         plans = o.tc ? round256((rows + 127) / 128 * LORA_PLAN_BYTES) : 0;
@@ -94,6 +95,14 @@ struct Workspace {
 int parts_for(int in_dtype, bool f32_result)
 {
     return in_dtype == GEMM_BF16 && f32_result ? 3 : 2;
+}
+
+// Whether one kernel makes the rank values and the product (on the current device).
+bool one_kernel(const Operands& o, const gemm_lora_t& l, int64_t rows, int64_t N, int64_t K, int parts)
+{
+    DeviceInfo d;
+    return o.tc && has_adapters(l) && device_info(&d) == cudaSuccess &&
+           lora_alone_takes(rows, N, K, l.adapters, static_cast<int>(l.rank), parts, d.num_sms);
 }
 
 // The input's direction: rank values from X and A, or (across) from D and B.
@@ -139,7 +148,8 @@ extern "C" size_t gemm_lora_workspace_size(const void* X, int64_t ldx, const voi
     if (check_sizes(lora, rows, N, K, in_dtype, out_dtype) != GEMM_OK || rows == 0 || N == 0)
         return 0;
     const Operands o(X, ldx, nullptr, 0, W, ldw, *lora, rows, N, K, in_dtype);
-    return Workspace(1, *lora, rows, parts_for(in_dtype, out_dtype == GEMM_F32), o).bytes();
+    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32);
+    return Workspace(one_kernel(o, *lora, rows, N, K, parts) ? 0 : 1, *lora, rows, parts, o).bytes();
 }
 
 extern "C" int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw,
@@ -155,7 +165,8 @@ extern "C" int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw,
         return GEMM_ERR_INVALID_VALUE;
     Operands o(X, ldx, nullptr, 0, W, ldw, *lora, rows, N, K, in_dtype);
     const int parts = parts_for(in_dtype, out_dtype == GEMM_F32);
-    const Workspace ws(1, *lora, rows, parts, o);
+    const bool alone = one_kernel(o, *lora, rows, N, K, parts);
+    const Workspace ws(alone ? 0 : 1, *lora, rows, parts, o);
     if (bad_workspace(workspace, workspace_bytes, ws.bytes()))
         return GEMM_ERR_INVALID_VALUE;
     DeviceInfo d;
@@ -173,6 +184,8 @@ extern "C" int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw,
     l.plan = ws.plan(workspace);
     if (!o.tc && K == 0)
         l.adapters = 0;
+    if (alone)
+        return status_of(err == cudaSuccess ? lora_alone_tc_launch(l, s) : err);
     if (err == cudaSuccess && l.adapters > 0)
         err = o.tc ? lora_shrink_tc_launch(l, nullptr, s) : lora_simt_shrink(l, s);
     if (err == cudaSuccess)

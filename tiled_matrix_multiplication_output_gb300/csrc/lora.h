@@ -81,6 +81,10 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream);
 // The kernel for few output tiles, and whether it is the choice.
 bool lora_small_takes(const LoraLaunch& l);
 cudaError_t lora_small_tc_launch(const LoraLaunch& l, cudaStream_t stream);
+// The same kernel that makes the rank values too (of the forward direction), and
+// whether it is the choice: it needs no shrink, no plans and no rank values in memory.
+bool lora_alone_takes(int64_t rows, int64_t N, int64_t K, int64_t adapters, int rank, int parts, int num_sms);
+cudaError_t lora_alone_tc_launch(const LoraLaunch& l, cudaStream_t stream);
 // Two gradients of the same rows in one launch (either may be null); dependent: the
 // launch before is an expand of the same rank values.
 cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool dependent, cudaStream_t stream);

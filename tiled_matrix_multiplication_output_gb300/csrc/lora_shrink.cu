@@ -12,7 +12,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cstring>
 
 #include "grouped_maps.h"
 #include "lora_tc.cuh"
@@ -66,19 +65,9 @@ template <typename T>
 __device__ __forceinline__ void store_parts(T* t, float (&left)[8], const LoraParts& lay, int j)
 {
     t += (j / lay.chunk) * 64 + j % lay.chunk;
-#pragma unroll 1
-    for (int part = 0; part < lay.parts; ++part, t += lay.chunk) {
-        T h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            put(&h[i], left[i]);
-            const float f = to_f32(h[i]);
-            left[i] = isfinite(f) ? left[i] - f : 0.0f;  // an infinity has no remainder
-        }
-        uint4 w;
-        memcpy(&w, h, 16);
-        *reinterpret_cast<uint4*>(t) = w;
-    }
+    each_part<T>(left, lay.parts, [&](int part, const uint4& w) {
+        *reinterpret_cast<uint4*>(t + part * lay.chunk) = w;
+    });
 }
 
 template <typename T, int SPLITS>
@@ -361,31 +350,58 @@ cudaError_t share_sms()
     return err;
 }
 
+// Sets the kernel up, once; how many of its clusters run at a time, with the
+// smaller ring (shared) or the larger.
+template <typename T, int SPLITS>
+cudaError_t most_clusters(bool shared, int num_sms, int* cap)
+{
+    static ClusterCaps caps[2];
+    cudaError_t err = share_sms<T, SPLITS>();
+    int n[2] = {};
+    for (int i = 0; i < 2 && err == cudaSuccess; ++i)  // (the larger last: it stays the kernel's limit)
+        err = cluster_cap(lora_shrink_tc_kernel<T, SPLITS>, caps[i], SPLITS, LS_THREADS,
+                          (i ? LS_RING : LS_RING_SHARED) + 1024, num_sms, &n[i]);
+    *cap = n[shared ? 0 : 1];
+    return err;
+}
+
 template <typename T, int SPLITS>
 cudaError_t launch(const CUtensorMap (&m)[4], const ShrinkParams& p, unsigned clusters, int smem,
                    cudaStream_t stream)
 {
-    static ClusterCaps caps;
-    int cap = 0;
-    cudaError_t err = share_sms<T, SPLITS>();
-    if (err == cudaSuccess)
-        err = cluster_cap(lora_shrink_tc_kernel<T, SPLITS>, caps, 1, LS_THREADS, LS_RING + 1024, 1, &cap);
-    if (err != cudaSuccess)
-        return err;
     ClusterLaunch l(clusters * SPLITS, SPLITS, LS_THREADS, smem, stream);
     return l.run(lora_shrink_tc_kernel<T, SPLITS>, m[0], m[1], m[2], m[3], p);
 }
 
+// CTAs for every SM, in clusters that run all at once: first the contraction is
+// split, then the adapters are dealt out.
 template <typename T>
-cudaError_t launch(const CUtensorMap (&m)[4], const ShrinkParams& p, unsigned clusters, int splits, int smem,
-                   cudaStream_t stream)
+cudaError_t launch(const CUtensorMap (&m)[4], ShrinkParams& p, int sides, int most_k, int most_adapters,
+                   bool shared, int num_sms, cudaStream_t stream)
 {
-    switch (splits) {
-    case 1:
+    static SplitCaps known[2];
+    const int* most = nullptr;
+    const cudaError_t err = split_caps(known[shared], [&](int i, int* n) {
+        return i == 0   ? most_clusters<T, 1>(shared, num_sms, n)
+               : i == 1 ? most_clusters<T, 2>(shared, num_sms, n)
+               : i == 2 ? most_clusters<T, 4>(shared, num_sms, n)
+                        : most_clusters<T, 8>(shared, num_sms, n);
+    }, &most);
+    if (err != cudaSuccess)
+        return err;
+    auto cap = [&](int i) { return std::min(most[i], num_sms >> i); };  // (one an SM)
+    int i = 0;
+    while (i < 3 && 2 << i <= most_k && p.tiles * sides <= cap(i + 1))
+        ++i;
+    p.deal = std::max(1, std::min(most_adapters, cap(i) / (p.tiles * sides)));
+    const unsigned clusters = static_cast<unsigned>(p.tiles) * sides * p.deal;
+    const int smem = (shared ? LS_RING_SHARED : LS_RING) + 1024;
+    switch (i) {
+    case 0:
         return launch<T, 1>(m, p, clusters, smem, stream);
-    case 2:
+    case 1:
         return launch<T, 2>(m, p, clusters, smem, stream);
-    case 4:
+    case 2:
         return launch<T, 4>(m, p, clusters, smem, stream);
     default:
         return launch<T, 8>(m, p, clusters, smem, stream);
@@ -479,19 +495,13 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
         p.a_offset = r.a_offset;
         p.stage_bytes = r.stage_bytes;
     }
-    const int ring = !second && r.shares ? LS_RING_SHARED : LS_RING;
-    p.stages = std::min(LS_MAX_STAGES, (ring - p.a_offset - 16384) / p.stage_bytes + 1);
+    const bool shared = !second && r.shares;
+    p.stages = std::min(LS_MAX_STAGES,
+                        ((shared ? LS_RING_SHARED : LS_RING) - p.a_offset - 16384) / p.stage_bytes + 1);
     const int most_adapters = std::min(std::min(l.adapters, LT_ROWS), l.rows);
-    // CTAs for every SM: first the contraction is split, then the adapters
-    // dealt out.
-    int splits = 1;
-    while (splits < 8 && 2 * splits <= most_k && p.tiles * sides * splits * 2 <= l.num_sms)
-        splits *= 2;
-    p.deal = std::max(1, std::min(most_adapters, l.num_sms / (p.tiles * sides * splits)));
-    const int64_t clusters = static_cast<int64_t>(p.tiles) * sides * p.deal;
     return l.in_dtype == DT_BF16
-               ? launch<__nv_bfloat16>(m, p, static_cast<unsigned>(clusters), splits, ring + 1024, stream)
-               : launch<__half>(m, p, static_cast<unsigned>(clusters), splits, ring + 1024, stream);
+               ? launch<__nv_bfloat16>(m, p, sides, most_k, most_adapters, shared, l.num_sms, stream)
+               : launch<__half>(m, p, sides, most_k, most_adapters, shared, l.num_sms, stream);
 }
 
 }  // namespace tmmo

@@ -18,6 +18,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cstring>
+
 #include "lora.h"
 #include "ops.cuh"
 #include "simt_tile.cuh"
@@ -149,6 +151,25 @@ inline LoraParts lora_parts(int rank, int parts)
 {
     const int chunk = rank <= 16 || parts == 3 ? 16 : 32;
     return {parts, chunk, (rank + chunk - 1) / chunk};
+}
+
+// Eight rank values in parts: store(part, its eight values).
+template <typename T, typename Store>
+__device__ __forceinline__ void each_part(float (&left)[8], int parts, Store store)
+{
+#pragma unroll 1
+    for (int part = 0; part < parts; ++part) {
+        T h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            put(&h[i], left[i]);
+            const float f = to_f32(h[i]);
+            left[i] = isfinite(f) ? left[i] - f : 0.0f;  // an infinity has no remainder
+        }
+        uint4 w;
+        memcpy(&w, h, 16);
+        store(part, w);
+    }
 }
 
 }  // namespace tmmo

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <cstdint>
 #include <mutex>
 
 #include "device.h"
@@ -87,6 +89,37 @@ cudaError_t cluster_cap(Kernel kern, ClusterCaps& caps, int size, int threads, i
         caps.cap[dev] = clusters > 0 ? clusters : -1;
     }
     *cap = caps.cap[dev];
+    return cudaSuccess;
+}
+
+// The same of a kernel's forms for clusters of 1, 2, 4 and 8 blocks, for every
+// device: asked for once.
+struct SplitCaps {
+    std::mutex mu;
+    std::atomic<uint64_t> known{0};  // a bit for each device
+    int cap[kMaxDevices][4];
+};
+static_assert(kMaxDevices <= 64, "a bit for each");
+
+// ask(i, &cap) gives the number for clusters of 2^i blocks.
+template <typename Ask>
+cudaError_t split_caps(SplitCaps& c, Ask ask, const int** caps)
+{
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess)
+        return err;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    if (!(c.known.load(std::memory_order_acquire) >> dev & 1)) {
+        std::lock_guard<std::mutex> lock(c.mu);
+        for (int i = 0; i < 4 && err == cudaSuccess; ++i)
+            err = ask(i, &c.cap[dev][i]);
+        if (err != cudaSuccess)
+            return err;
+        c.known.fetch_or(1ull << dev, std::memory_order_release);
+    }
+    *caps = c.cap[dev];
     return cudaSuccess;
 }
 

@@ -1,4 +1,5 @@
-// The wait of roles that run on whole warps, and copies of 3-D boxes.
+// The wait of roles that run on whole warps, the halves of a cluster's barrier, and
+// copies of 3-D boxes.
 #pragma once
 
 #include "ops.cuh"
@@ -27,6 +28,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const T
         if (__any_sync(0xffffffffu, late || *w.abort_flag))
             return false;
     }
+}
+
+// The two halves of cluster_sync(), each by every thread of the cluster.
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // For a wait that spans `steps` K steps (a whole tile's): a step takes well below
