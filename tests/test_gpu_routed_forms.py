@@ -291,3 +291,24 @@ def test_one_kernel_keeps_infinities_of_other_adapters_away(rows):
     assert torch.equal(y[keep], clean[keep]) and not torch.isfinite(y[~keep]).any()
     c.x[0] = float("inf")  # an infinity in a row stays in it
     assert torch.equal(c.forward()[keep][1:], clean[keep][1:])
+
+
+@pytest.mark.parametrize("rank", [8, 40, 72, 128])
+@pytest.mark.parametrize("runs", [(40, 128, 300, 17, 640), (1, 700), (129, 127, 384, 60)])
+def test_gradients_where_whole_and_shared_row_tiles_alternate(rank, runs):
+    """Row tiles of one adapter beside row tiles of several, in rings of every length."""
+    c = Case(5000, 264, 136, 3, rank, "bf16", ints=True)
+    of, i = [], 0
+    while len(of) < 5000:
+        of += [(i * 7 // 3) % 4 - 1] * runs[i % len(runs)]
+        i += 1
+    c.adapter.copy_(torch.tensor(of[:5000], dtype=torch.int32))
+    _, da, db = c.backward(grad_dtype=torch.float32)
+    for g in range(3):
+        rows = c.adapter == g
+        u = c.scale[g].double() * (c.dy[rows].double() @ c.b[g].double())
+        t = c.scale[g].double() * (c.x[rows].double() @ c.a[g].double().T)
+        for got, want, size in ((da[g], u.T @ c.x[rows].double(), u.abs().T @ c.x[rows].double().abs()),
+                                (db[g], c.dy[rows].double().T @ t, c.dy[rows].double().abs().T @ t.abs())):
+            # sums of integers: exact while no partial sum needs more than 24 bits
+            assert size.max() < 2 ** 24 and torch.equal(got.double(), want)

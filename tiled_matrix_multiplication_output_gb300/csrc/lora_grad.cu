@@ -14,6 +14,7 @@
 // values, of which it needs nothing: it starts where that one's last tiles leave SMs
 // idle.
 #include <algorithm>
+#include <cstring>
 
 #include "grouped_maps.h"
 #include "lora_tc.cuh"
@@ -23,7 +24,9 @@
 namespace tmmo {
 namespace {
 
-constexpr int LG_THREADS = 256;  // warps 0: copies, 1: MMA, 2 and 3: zeros, 4-7: epilogue
+constexpr int LG_TEAMS = 4;      // pairs of warps that zero, each in its stages of the ring
+// warps 0: copies, 1: MMA, 4-7: epilogue, the others: zeros
+constexpr int LG_THREADS = 32 * (6 + 2 * LG_TEAMS);
 constexpr int LG_MAX_STAGES = 8;
 constexpr int LG_RING = 192 * 1024;  // beside 25 KiB of plans
 constexpr int LG_CHUNKS = 4;     // chunks of rank values in a tile
@@ -34,6 +37,7 @@ struct GradSide {
     int cols;
     void* G;
     int64_t step_c, step_j, stride_g;
+    bool words;        // rank values next to each other, rows on 16-byte boundaries
 };
 
 struct GradParams {
@@ -220,6 +224,30 @@ __device__ __forceinline__ bool has_slice(const uint32_t (&rows)[4], int k)
     return (rows[k >> 1] & (k & 1 ? 0xffff0000u : 0xffffu)) != 0;
 }
 
+// p[0 .. n) = v, of 16 values at most, on a 16-byte boundary.
+template <typename OutT>
+__device__ __forceinline__ void put_words(OutT* p, const float (&v)[16], int n)
+{
+    constexpr int EACH = 16 / sizeof(OutT);
+    alignas(16) OutT h[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        put(&h[i], v[i]);
+#pragma unroll
+    for (int i = 0; i < 16; i += EACH) {
+        if (i + EACH <= n) {
+            uint4 w;
+            memcpy(&w, h + i, 16);
+            *reinterpret_cast<uint4*>(p + i) = w;
+        } else {
+#pragma unroll
+            for (int k = i; k < i + EACH; ++k)
+                if (k < n)
+                    p[k] = h[k];
+        }
+    }
+}
+
 struct GradSmem {
     uint64_t full[LG_MAX_STAGES], landed[LG_MAX_STAGES], empty[LG_MAX_STAGES], tfull[2], tempty[2], drain;
     uint32_t tmem;
@@ -375,9 +403,10 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         const long long t0 = clock64();
         while (!mbar_try_wait(smem_u32(&s.drain), 0) && clock64() - t0 < p.wait_budget) {
         }
-    } else if (warp < 4) {
+    } else if (warp < 4 || warp >= 8) {
         // ------------------------------------------------ rows of other adapters
-        const int half = warp - 2;  // of the rows
+        const int half = warp & 1;  // of the rows
+        const int team = warp < 4 ? 0 : (warp - 6) / 2;
         int stage = 0;
         uint32_t parity = 0;  // a bit for each stage
         bool ok = true;
@@ -387,7 +416,9 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             int tile;
             uint32_t rows[4];
             while (ok && tiles.next(tile, rows)) {
-                if (!all_rows(rows)) {
+                // (a stage's steps are always the same team's: a barrier whose phases another
+                // team waited for would tell this one nothing)
+                if (stage % LG_TEAMS == team && !all_rows(rows)) {
                     ok = warp_wait(smem_u32(&s.landed[stage]), (parity >> stage) & 1, watch);
                     if (!ok)
                         break;
@@ -411,7 +442,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                     stage = 0;
             }
         }
-    } else if (warp >= 4) {
+    } else {
         // ------------------------------------------------ epilogue
         const int q = warp & 3;
         int local = 0;
@@ -454,7 +485,9 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                             for (int i = 0; i < 16; ++i)
                                 sum[i] += __uint_as_float(v[i]);
                         }
-                    if (c < side.cols) {
+                    if (c < side.cols && side.words) {
+                        put_words(out + j, sum, p.rank - j);
+                    } else if (c < side.cols) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (j + i < p.rank)
@@ -520,7 +553,9 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
         if (!sides[i])
             continue;
         const LoraGradLaunch& s = *sides[i];
-        p.side[i] = {(s.cols + 127) / 128, s.cols, s.G, s.step_c, s.step_j, s.stride_g};
+        const int64_t size = type_bytes(s.out_dtype);
+        p.side[i] = {(s.cols + 127) / 128, s.cols, s.G, s.step_c, s.step_j, s.stride_g,
+                     s.step_j == 1 && aligned16(s.G) && s.step_c * size % 16 == 0 && s.stride_g * size % 16 == 0};
         per[i] = static_cast<int64_t>(p.side[i].tiles_c) * p.groups_j;
         if (!s.maps->get(&m[2 * i], s.in_dtype, s.P, 2, {s.cols, s.rows, 1}, {s.ldp, 0}, {64, box_rows, 1}) ||
             !s.maps->get(&m[2 * i + 1], s.in_dtype, s.t, 2, {p.lay.columns(), s.rows, 1},
