@@ -94,14 +94,16 @@ __device__ __forceinline__ int simt_col() { return 4 * (threadIdx.x % 16); }
 // values a thread the loads from shared memory, not the multiply-adds, set the
 // pace.  The tile is small because an SM that gets one more than others takes as
 // much longer: 999 rows of eight groups by 512 x 768 took 63 us in 160 tiles of
-// 64 x 64, three of which met on one SM, and take 35 so (22 TFLOP/s).
+// 64 x 64, three of which met on one SM, and take 33 so (24 TFLOP/s).
 template <typename KeepA, typename KeepB>
 __device__ __forceinline__ void simt_accumulate(SimtValues& acc, SimtSmem& smem, const View& a, const View& b,
                                                 int k0, int k1, KeepA keep_a, KeepB keep_b)
 {
     constexpr int WARPS = ST_THREADS / 32, DEPTH = ST_K / WARPS;
     const int warp = threadIdx.x / 32;
-    const int r8 = 8 * (threadIdx.x % 32 / 8), c8 = 8 * (threadIdx.x % 8);
+    // a thread's rows r4 .. r4 + 3 and 16 behind, its columns c4 .. c4 + 3 and 32 behind:
+    // eight threads read 128 contiguous bytes
+    const int r4 = 4 * (threadIdx.x % 32 / 8), c4 = 4 * (threadIdx.x % 8);
     SimtLoader<ST_M> la(a, k0);
     SimtLoader<ST_N> lb(b, k0);
     auto load = [&](int stage, int k) {
@@ -128,8 +130,8 @@ __device__ __forceinline__ void simt_accumulate(SimtValues& acc, SimtSmem& smem,
             float x[8], y[8];
 #pragma unroll
             for (int h = 0; h < 8; h += 4) {
-                *reinterpret_cast<float4*>(x + h) = *reinterpret_cast<const float4*>(&s.a[kk][r8 + h]);
-                *reinterpret_cast<float4*>(y + h) = *reinterpret_cast<const float4*>(&s.b[kk][c8 + h]);
+                *reinterpret_cast<float4*>(x + h) = *reinterpret_cast<const float4*>(&s.a[kk][r4 + 4 * h]);
+                *reinterpret_cast<float4*>(y + h) = *reinterpret_cast<const float4*>(&s.b[kk][c4 + 8 * h]);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -146,12 +148,12 @@ __device__ __forceinline__ void simt_accumulate(SimtValues& acc, SimtSmem& smem,
     for (int w = 0; w < WARPS; w += 2) {
         __syncthreads();
         if (warp == w || warp == w + 1) {
-            float* to = sums + (warp - w) * ST_M * PITCH + r8 * PITCH + c8;
+            float* to = sums + (warp - w) * ST_M * PITCH + r4 * PITCH + c4;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int h = 0; h < 8; h += 4)
-                    *reinterpret_cast<float4*>(to + i * PITCH + h) =
+                    *reinterpret_cast<float4*>(to + (i % 4 + i / 4 * 16) * PITCH + 8 * h) =
                         make_float4(part[i][h], part[i][h + 1], part[i][h + 2], part[i][h + 3]);
         }
         __syncthreads();
