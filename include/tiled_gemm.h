@@ -585,7 +585,8 @@ typedef struct {
  * gemm_lora -- the forward product above.  X is rows x K, Y rows x N.
  *
  * workspace: gemm_lora_workspace_size() bytes of device memory for these very
- * operands; 256-byte aligned, not shared by calls that overlap in time.
+ * operands on the current device, 0 where none is needed; 256-byte aligned, not
+ * shared by calls that overlap in time.
  * Without adapters, or with rank 0, neither `adapter` nor A and B are read.
  * Returns GEMM_OK, GEMM_ERR_INVALID_VALUE (null pointer where data is needed,
  * bad size, pitch, stride or enum, workspace missing, misaligned or too

