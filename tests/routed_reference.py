@@ -98,6 +98,10 @@ def _beside(x, w, down, up, adapter, scale, dtype, out_dtype):
         d = tm @ up[g].abs()
         mag[rows] += d
         err[rows] += (sums_bound(x.shape[1]) + 2.0 ** -23 + parts_bound(dtype, out_dtype)) * d
+        if dtype == torch.float16:
+            # the second part is a multiple of FP16's least step, 2^-24: it leaves up to half
+            # of that of a rank value, however small the value is
+            err[rows] += 2.0 ** -25 * up[g].abs().sum(0)
     return out, err + mag * sums_bound(x.shape[1] + 3 * r)
 
 

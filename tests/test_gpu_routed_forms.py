@@ -347,3 +347,19 @@ def test_few_rows_of_very_many_outputs(rows, rank):
         of = c.adapter == g
         want[of] += (c.scale[g].double() * (c.x[of].double() @ c.a[g].double().T)) @ c.b[g].double().T
     assert torch.equal(c.forward().double(), want)
+
+
+@pytest.mark.parametrize("rank", [4, 12, 40, 128])
+@pytest.mark.parametrize("size", [1e-2, 1e-3, 1e-4])
+def test_fp16_gradients_from_small_values(rank, size):
+    """Rank values of 1e-3 down to 1e-7, below what FP16 holds: their gradients keep
+    the precision of larger ones."""
+    c = Case(300, 136, 264, 3, rank, "f16", seed=rank)
+    c.dy.mul_(size)
+    c.x.mul_(size)
+    c.a.mul_(size)
+    c.b.mul_(size)
+    want = ref.lora_backward(c.dy, c.x, c.w, c.a, c.b, c.adapter, c.scale, torch.float32)
+    _, da, db = c.backward(grad_dtype=torch.float32)
+    ref.check(da, *want[1])
+    ref.check(db, *want[2])

@@ -91,10 +91,11 @@ struct Workspace {
     void* copy(void* p) const { return static_cast<char*>(plan(p)) + plans; }
 };
 
-// How many parts hold a rank value: all bits of an FP32 sum for an FP32 result.
-int parts_for(int in_dtype, bool f32_result)
+// How many parts hold a rank value: all bits of an FP32 sum for an FP32 result, and
+// for gradients from FP16 operands, which may be far below what two FP16 parts hold.
+int parts_for(int in_dtype, bool f32_result, bool gradients)
 {
-    return in_dtype == GEMM_BF16 && f32_result ? 3 : 2;
+    return (in_dtype == GEMM_BF16 && f32_result) || (in_dtype == GEMM_F16 && gradients) ? 3 : 2;
 }
 
 // Whether one kernel makes the rank values and the product (on the current device).
@@ -148,7 +149,7 @@ extern "C" size_t gemm_lora_workspace_size(const void* X, int64_t ldx, const voi
     if (check_sizes(lora, rows, N, K, in_dtype, out_dtype) != GEMM_OK || rows == 0 || N == 0)
         return 0;
     const Operands o(X, ldx, nullptr, 0, W, ldw, *lora, rows, N, K, in_dtype);
-    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32);
+    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32, false);
     return Workspace(one_kernel(o, *lora, rows, N, K, parts) ? 0 : 1, *lora, rows, parts, o).bytes();
 }
 
@@ -164,7 +165,7 @@ extern "C" int gemm_lora(const void* X, int64_t ldx, const void* W, int64_t ldw,
     if (!Y || ldy < N || (K > 0 && (!X || !W || ldx < K || ldw < K)))
         return GEMM_ERR_INVALID_VALUE;
     Operands o(X, ldx, nullptr, 0, W, ldw, *lora, rows, N, K, in_dtype);
-    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32);
+    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32, false);
     const bool alone = one_kernel(o, *lora, rows, N, K, parts);
     const Workspace ws(alone ? 0 : 1, *lora, rows, parts, o);
     if (bad_workspace(workspace, workspace_bytes, ws.bytes()))
@@ -204,7 +205,7 @@ extern "C" size_t gemm_lora_backward_workspace_size(const void* D, int64_t ldd, 
         return 0;
     const Operands o(X, ldx, D, ldd, W, ldw, *lora, rows, N, K, in_dtype);
     const bool f32 = out_dtype == GEMM_F32 || grad_dtype == GEMM_F32;
-    return Workspace(2, *lora, rows, parts_for(in_dtype, f32), o).bytes();
+    return Workspace(2, *lora, rows, parts_for(in_dtype, f32, true), o).bytes();
 }
 
 extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int64_t ldx,
@@ -237,7 +238,7 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
     if (db && (lddb < lora->rank || (lora->adapters > 1 && !apart(stride_db, N, lddb, lora->rank))))
         return GEMM_ERR_INVALID_VALUE;
     Operands o(X, ldx, D, ldd, W, ldw, *lora, rows, N, K, in_dtype);
-    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32 || grad_dtype == GEMM_F32);
+    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32 || grad_dtype == GEMM_F32, true);
     const Workspace ws(2, *lora, rows, parts, o);
     if (bad_workspace(workspace, workspace_bytes, ws.bytes()))
         return GEMM_ERR_INVALID_VALUE;

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         for (int c = 0; ok && c < p.lay.chunks; ++c)
                             ok = step([&](uint32_t a0, uint32_t b0) {
                                 const int deep = p.lay.deep(c, p.rank);
-                                for (int part = 0; part < p.lay.parts; ++part)
+                                for (int part = 0; part < p.lay.plain; ++part)
                                     for (int k = 0; k < deep; ++k)
                                         tc_mma_f16_lanes(
                                             d_tmem,
@@ -478,7 +478,7 @@ cudaError_t launch(int out_dtype, const CUtensorMap (&m)[6], ExpandParams& p, in
 
 }  // namespace
 
-int lora_parts_bytes(int rank, int parts) { return 2 * lora_parts(rank, parts).columns(); }
+int lora_parts_bytes(int rank, int parts) { return 2 * lora_parts(rank, parts, DT_BF16).columns(); }
 
 cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
 {
@@ -493,7 +493,7 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     p.tiles_n = (l.N + 255) / 256;
     p.adapters = l.adapters > 0;
     p.one = l.adapters == 1 || l.stride_e == 0;
-    p.lay = lora_parts(l.rank, l.parts);
+    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);
     p.plan = static_cast<const LoraPlan*>(l.plan);
     p.C = l.Y;
     p.ldc = l.ldy;

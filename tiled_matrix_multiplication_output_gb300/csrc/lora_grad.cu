@@ -487,7 +487,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                             tmem_wait_ld(v);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                sum[i] += __uint_as_float(v[i]);
+                                sum[i] = fmaf(part < p.lay.plain ? 1.0f : 1.0f / LT_FINE, __uint_as_float(v[i]),
+                                              sum[i]);
                         }
                     if (c < side.cols && side.words) {
                         put_words(out + j, sum, p.rank - j);
@@ -542,7 +543,7 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
     p.rank = l.rank;
     p.plans = (l.rows + LT_ROWS - 1) / LT_ROWS;
     p.plan = static_cast<const LoraPlan*>(l.plan);
-    p.lay = lora_parts(l.rank, l.parts);
+    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);
     p.groups_j = (p.lay.chunks + LG_CHUNKS - 1) / LG_CHUNKS;
     p.stage_bytes = LG_BOX * (2 + std::min(p.lay.chunks, LG_CHUNKS));
     p.stages = std::min(LG_MAX_STAGES, LG_RING / p.stage_bytes);

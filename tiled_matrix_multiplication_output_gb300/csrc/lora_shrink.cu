@@ -67,7 +67,7 @@ template <typename T>
 __device__ __forceinline__ void store_parts(T* t, float (&left)[8], const LoraParts& lay, int j)
 {
     t += (j / lay.chunk) * 64 + j % lay.chunk;
-    each_part<T>(left, lay.parts, [&](int part, const uint4& w) {
+    each_part<T>(left, lay, [&](int part, const uint4& w) {
         *reinterpret_cast<uint4*>(t + part * lay.chunk) = w;
     });
 }
@@ -450,7 +450,7 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
     p.adapters = l.adapters;
     p.rank = l.rank;
     p.cols = (l.rank + 15) / 16 * 16;
-    p.lay = lora_parts(l.rank, l.parts);
+    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);
     p.tiles = (l.rows + LT_ROWS - 1) / LT_ROWS;
     p.box_rows = std::min(LT_ROWS, (l.rows + 7) / 8 * 8);
     const uint32_t box_rows = static_cast<uint32_t>(p.box_rows);

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                         for (int i = 0; i < some; ++i, b0 += width * 128) {
                             uint32_t off[4];
                             others(a + i * SPLITS, off);
-                            for (int part = 0; part < p.lay.parts; ++part)
+                            for (int part = 0; part < p.lay.plain; ++part)
                                 for (int k = 0; k < deep; ++k)
                                     tc_mma_f16_lanes(tmem,
                                                      smem_desc_sw128(held + part * width + k * 32, 16, 1024),
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     for (int c = 0; ok && c < p.lay.chunks; ++c)
                         ok = step([&](uint32_t a0, uint32_t b0) {
                             const int deep = p.lay.deep(c, p.rank);
-                            for (int part = 0; part < p.lay.parts; ++part)
+                            for (int part = 0; part < p.lay.plain; ++part)
                                 for (int k = 0; k < deep; ++k)
                                     tc_mma_f16_lanes(
                                         tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
@@ -503,9 +503,9 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                         st_shared_v4(held + row * 128 + ((at ^ (row & 7)) << 4), w.x, w.y, w.z, w.w);
                     };
                     if (p.bf16)
-                        each_part<__nv_bfloat16>(sum, p.lay.parts, store);
+                        each_part<__nv_bfloat16>(sum, p.lay, store);
                     else
-                        each_part<__half>(sum, p.lay.parts, store);
+                        each_part<__half>(sum, p.lay, store);
                 }
             }
             fence_proxy_async_smem();
@@ -678,7 +678,7 @@ cudaError_t launch_small(const LoraLaunch& l, bool own, cudaStream_t stream)
     p.tiles_n = (l.N + 127) / 128;
     p.adapters = l.adapters;
     p.one = l.adapters == 1 || l.stride_e == 0;
-    p.lay = lora_parts(l.rank, l.parts);
+    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);
     p.adapter = l.adapter;
     p.C = l.Y;
     p.ldc = l.ldy;
@@ -747,7 +747,7 @@ bool lora_small_takes(const LoraLaunch& l) { return small_tiles(l.rows, l.N) <= 
 bool lora_alone_takes(int64_t rows, int64_t N, int64_t K, int64_t adapters, int rank, int parts, int num_sms)
 {
     const int64_t tiles = small_tiles(rows, N), k_blocks = (K + TC_BK - 1) / TC_BK;
-    if (adapters == 0 || tiles > num_sms || lora_parts(rank, parts).chunks > 1)
+    if (adapters == 0 || tiles > num_sms || lora_parts(rank, parts, DT_BF16).chunks > 1)
         return false;
     int splits = 1;
     if (small_splits<false, true>(tiles, k_blocks, num_sms, &splits) != cudaSuccess)

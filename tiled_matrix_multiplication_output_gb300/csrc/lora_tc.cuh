@@ -9,9 +9,12 @@
 // The rank values t are FP32 sums that enter a second product as operands of 16
 // bits, in parts: t = p0 + p1 (+ p2), each the rounding of what the ones before
 // leave, multiplied by the same factor.  Two parts hold 16 bits of a BF16 value
-// and 22 of an FP16 one, three hold 24.  They lie in chunks of `chunk` rank
-// values, 64 columns (128 bytes, a swizzle row) a chunk: part p of value j at
-// column (j / chunk) * 64 + p * chunk + j % chunk.
+// and 22 of an FP16 one, three hold 24.  An FP16 part is no finer than 2^-24, which
+// a product may leave out beside the shared one, but not a gradient that is nothing
+// but rank values times rows (its values may be 1e-6): its third part is of 2^20
+// times what the two leave, and has an accumulator of its own.  They lie in chunks of
+// `chunk` rank values, 64 columns (128 bytes, a swizzle row) a chunk: part p of value
+// j at column (j / chunk) * 64 + p * chunk + j % chunk.
 #pragma once
 
 #include <cuda.h>
@@ -20,6 +23,7 @@
 
 #include <cstring>
 
+#include "launch.h"
 #include "lora.h"
 #include "ops.cuh"
 #include "simt_tile.cuh"
@@ -28,6 +32,7 @@
 namespace tmmo {
 
 constexpr int LT_ROWS = 128;  // rows of a tile, the lanes of a CTA
+constexpr float LT_FINE = 1048576.0f;  // 2^20: a remainder of 2^-8 at most stays below 65504
 
 struct alignas(16) LoraPlan {
     int count;                  // adapters among the tile's rows
@@ -139,6 +144,7 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
 // How the rank values are laid out.
 struct LoraParts {
     int parts, chunk, chunks;
+    int plain;    // parts to the scale of 1; one behind them is to that of LT_FINE
     __host__ __device__ int columns() const { return 64 * chunks; }
     // 16-deep instructions of each part in chunk c
     __host__ __device__ int deep(int c, int rank) const
@@ -147,19 +153,24 @@ struct LoraParts {
         return ((left < chunk ? left : chunk) + 15) / 16;
     }
 };
-inline LoraParts lora_parts(int rank, int parts)
+inline LoraParts lora_parts(int rank, int parts, int dtype)
 {
     const int chunk = rank <= 16 || parts == 3 ? 16 : 32;
-    return {parts, chunk, (rank + chunk - 1) / chunk};
+    return {parts, chunk, (rank + chunk - 1) / chunk, dtype == DT_F16 ? 2 : parts};
 }
 
 // Eight rank values in parts: store(part, its eight values).
 template <typename T, typename Store>
-__device__ __forceinline__ void each_part(float (&left)[8], int parts, Store store)
+__device__ __forceinline__ void each_part(float (&left)[8], const LoraParts& lay, Store store)
 {
 #pragma unroll 1
-    for (int part = 0; part < parts; ++part) {
+    for (int part = 0; part < lay.parts; ++part) {
         T h[8];
+        if (part == lay.plain) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                left[i] *= LT_FINE;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             put(&h[i], left[i]);
