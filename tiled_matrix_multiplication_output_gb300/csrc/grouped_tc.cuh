@@ -28,9 +28,10 @@
 // by 4096 x 2048 150 us (6.6 TB/s), the gradient of 16384 rows of 8 groups, 4096 x
 // 2048, FP32, 176 us (1.56 PFLOP/s).
 //
-// Warps: 0 TMA producer, 1 MMA issuer (of the leader CTA), 2 on epilogue (four; for
-// the gradient eight, and a last warp that zeroes).  A ring of K steps, bounded waits
-// and two accumulators in tensor memory, as in tc_gemm_kernel.
+// Warps: 0 TMA producer, 1 MMA issuer (of the leader CTA), 2 to 9 epilogue (with four,
+// 4148 rows of 17 groups by 1360 x 152 took 13.7 us, with eight 12.4; 16384 of 16 by
+// 4096 x 4096 300 and 303), for the gradient a last warp that zeroes.  A ring of K
+// steps, bounded waits and two accumulators in tensor memory, as in tc_gemm_kernel.
 #pragma once
 
 #include <cuda.h>
@@ -74,7 +75,7 @@ struct GroupedTcParams {
 template <int MODE>
 struct GroupedLayout {
     static constexpr bool WGRAD = MODE == GROUPED_WGRAD;
-    static constexpr int EPI_WARPS = WGRAD ? 8 : 4;
+    static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS + (WGRAD ? 32 : 0);
     static constexpr int OFF_STAGING = GT_RING;
     static constexpr int STAGING = 2048;  // of an epilogue warp
@@ -448,17 +449,18 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         if constexpr (!WGRAD) {
             if (p.zero_rest)
                 zero_rest_rows(table, p.by, out, p.ldc, p.N,
-                               static_cast<int64_t>(blockIdx.x) * 128 + (threadIdx.x - 64),
-                               static_cast<int64_t>(gridDim.x) * 128);
+                               static_cast<int64_t>(blockIdx.x) * (32 * L::EPI_WARPS) + (threadIdx.x - 64),
+                               static_cast<int64_t>(gridDim.x) * (32 * L::EPI_WARPS));
+            const int half = (warp - 2) / 4;  // these warps' strips: every other one
             for (int t = unit; t < num_work; t += num_units) {
                 const GroupedWork w = grouped_work<MODE>(t, table, p);
                 if (!take(w.k_blocks))
                     break;
                 const int f = w.f0 + static_cast<int>(rank) * TC_BM + q * 32;
                 const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * GT_N);
-                OutT* c = out + w.c0 * p.ldc + f;
+                OutT* c = out + (w.c0 + 32 * half) * p.ldc + f;
 #pragma unroll 1
-                for (int s = 0; s < w.count; s += 32, c += 32 * p.ldc) {
+                for (int s = 32 * half; s < w.count; s += 64, c += 64 * p.ldc) {
                     if constexpr (sizeof(OutT) == 2) {
                         if (p.unit && p.beta == 0.0f) {
                             put_turned(from + s, staging, c, p.ldc, w.count - s, p.N - f, p.alpha);
