@@ -1,0 +1,42 @@
+"""The grouped products and the adapters at the limits of their sizes, waits and
+ranges: groups of nearly 2^31 rows, waits behind long sums, sums of one sign, FP16
+values far from one."""
+import pytest
+import torch
+
+import tiled_matrix_multiplication_output_gb300 as tg
+from tests import routed_reference as ref
+from tests.test_gpu_grouped import _dev, _ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    tg.load_library(build_if_missing=True)
+
+
+@pytest.fixture(autouse=True)
+def _restore():
+    tg.gemm_debug_config(0, -1)
+    yield
+    tg.gemm_debug_config(0, -1)
+    assert tg.gemm_device_status(torch.cuda.current_stream().cuda_stream) == tg.binding.OK
+
+
+@pytest.mark.parametrize("op", ["t", "n"])
+def test_a_group_of_the_most_rows(op):
+    """One group of GEMM_MAX_DIM rows: the rows and the tiles that they give do not fit
+    32 bits together."""
+    rows = tg.binding.MAX_DIM
+    blocks = rows // 256
+    x = torch.empty(rows, 8, dtype=torch.bfloat16, device="cuda")
+    x.view(blocks, 256, 8).copy_(_ints(1, "bf16", 256, 8))
+    x.view(blocks, 256, 8)[:, :, 0] = (torch.arange(blocks, device="cuda") % 61 - 30)[:, None]
+    w = _ints(2, "bf16", 1, 8, 8)
+    y = tg.matmul_grouped(x, w, _dev([0, rows]), op_b=op, out_dtype=torch.bfloat16)
+    m = (w[0].t() if op == "t" else w[0]).float()
+    for r in range(0, rows, 1 << 25):
+        assert torch.equal(y[r:r + (1 << 25)].float(), (x[r:r + (1 << 25)].float() @ m).bfloat16().float())

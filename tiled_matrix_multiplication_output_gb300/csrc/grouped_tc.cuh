@@ -116,7 +116,8 @@ __device__ __forceinline__ GroupedWork grouped_work(int t, const GroupTable& tab
         w.g = table.group_of(t / p.tiles_f, p.by.groups);
         const int tiles = table.tile[w.g + 1] - table.tile[w.g];
         const int begin = table.first[w.g], rows = table.first[w.g + 1] - begin;
-        const int each = ((rows + tiles - 1) / tiles + 31) / 32 * 32;
+        // (rounded up to 32; rows + tiles may not fit 32 bits)
+        const int each = ((rows - 1) / tiles + 32) / 32 * 32;
         // row tiles eight at a time, and within those down the rows first: the
         // tiles that run together share weights and rows in L2
         int u = t - table.tile[w.g] * p.tiles_f;
