@@ -40,3 +40,17 @@ def test_a_group_of_the_most_rows(op):
     m = (w[0].t() if op == "t" else w[0]).float()
     for r in range(0, rows, 1 << 25):
         assert torch.equal(y[r:r + (1 << 25)].float(), (x[r:r + (1 << 25)].float() @ m).bfloat16().float())
+
+
+@pytest.mark.parametrize("counts", [[64 * 40_000 + 5], [64 * 10_000] * 76 + [5, 3]])
+def test_wgrad_waits_behind_long_sums(counts):
+    """The warp that zeroes the rows behind a ragged end waits for it through all K steps
+    before, of its tile and of the even ones that its pair had before: ten times as long
+    as a wait may be (0.5 and 1 ms here) while nothing moves."""
+    rows = sum(counts)
+    dy, x = (torch.ones(rows, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    off = _dev([0] + torch.tensor(counts).cumsum(0).tolist())
+    tg.gemm_debug_config(1_000_000 if len(counts) == 1 else 2_000_000, -1)
+    c = tg.matmul_grouped_wgrad(dy, x, off)
+    assert tg.gemm_device_status(torch.cuda.current_stream().cuda_stream) == tg.binding.OK
+    assert torch.equal(c, torch.tensor(counts, dtype=torch.float32, device="cuda")[:, None, None].expand_as(c))

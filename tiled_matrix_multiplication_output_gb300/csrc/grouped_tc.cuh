@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
     int* largest = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);
+    volatile int* progress = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 12);  // K steps copied
 
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
+        *progress = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
@@ -287,6 +289,8 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                     break;
                 const bool tail = is_ragged(w, kb);
                 ++steps;
+                if (WGRAD && lane == 0)
+                    *progress = steps;
                 if (kb != p.fault_skip_kblock) {  // (test hook, -1 in normal use)
                     if (elect_one()) {
                         if (tail) {
@@ -567,7 +571,8 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
             stage = (s + 1) % stages;
             if (!is_ragged(w, last))
                 continue;
-            if (!warp_wait(tail_bar(s), (parity >> s) & 1, watch))
+            // (the steps before, of this tile and of ones that end evenly, are not waited for)
+            if (!warp_wait_behind(tail_bar(s), (parity >> s) & 1, watch, progress))
                 break;
             parity ^= 1u << s;
             // a row of 64 values is 128 contiguous bytes (its swizzle stays within)

@@ -30,6 +30,30 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const T
     }
 }
 
+// warp_wait for what may lie any number of K steps ahead: the budget counts anew
+// whenever *progress, which the block's copies move on, has changed.
+__device__ __forceinline__ bool warp_wait_behind(uint32_t bar, uint32_t parity, const TcWatch& w,
+                                                 const volatile int* progress)
+{
+    long long t0 = clock64();
+    int seen = *progress;
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+            return true;
+        const long long now = clock64();
+        const int at = *progress;
+        if (at != seen) {
+            seen = at;
+            t0 = now;
+        }
+        const bool late = now - t0 > w.budget;
+        if (late)
+            tc_raise(w);
+        if (__any_sync(0xffffffffu, late || *w.abort_flag))
+            return false;
+    }
+}
+
 // The two halves of cluster_sync(), each by every thread of the cluster.
 __device__ __forceinline__ void cluster_arrive()
 {
