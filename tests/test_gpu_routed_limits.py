@@ -54,3 +54,16 @@ def test_wgrad_waits_behind_long_sums(counts):
     c = tg.matmul_grouped_wgrad(dy, x, off)
     assert tg.gemm_device_status(torch.cuda.current_stream().cuda_stream) == tg.binding.OK
     assert torch.equal(c, torch.tensor(counts, dtype=torch.float32, device="cuda")[:, None, None].expand_as(c))
+
+
+def test_adapter_gradients_wait_behind_long_sums():
+    """The warps that zero other adapters' rows in the last row tile, and the epilogue, wait
+    for it through ten thousand whole ones (0.5 ms a wait here)."""
+    rows = 128 * 10_000 + 5
+    dy, x = (torch.ones(rows, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w, a, b = (torch.ones(s, dtype=torch.bfloat16, device="cuda") for s in ((8, 8), (1, 8, 8), (1, 8, 8)))
+    adapter = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    tg.gemm_debug_config(1_000_000, -1)
+    _, da, db = tg.matmul_lora_backward(dy, x, w, a, b, adapter)
+    assert tg.gemm_device_status(torch.cuda.current_stream().cuda_stream) == tg.binding.OK
+    assert (da == 8 * rows).all() and (db == 8 * rows).all()

@@ -256,6 +256,7 @@ struct GradSmem {
     uint64_t full[LG_MAX_STAGES], landed[LG_MAX_STAGES], empty[LG_MAX_STAGES], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int abort_flag;
+    int progress;  // row tiles copied
     PlanTable plans;
 };
 
@@ -272,6 +273,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
     const TcWatch watch{&s.abort_flag, p.status, p.wait_budget};
+    volatile int* const progress = &s.progress;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         }
         mbar_init(smem_u32(&s.drain), 1);
         s.abort_flag = 0;
+        s.progress = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmP0);
         tma_prefetch_desc(&tmT0);
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        int stage = 0;
+        int stage = 0, steps = 0;
         uint32_t phase = 0;
         uint32_t n_full[LG_MAX_STAGES] = {}, n_landed[LG_MAX_STAGES] = {};
         bool ok = true;
@@ -329,6 +332,9 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                         tma_load_2d(b0 + c * LG_BOX, tmT, bar, (w.chunk0 + c) * 64, tile * LT_ROWS);
                 }
                 __syncwarp();
+                ++steps;
+                if (lane == 0)
+                    *progress = steps;
                 if (ok) {
                     ++n_full[stage];  // whichever barrier: full completes once a use
                     n_landed[stage] += !whole;
@@ -423,7 +429,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                 // (a stage's steps are always the same team's: a barrier whose phases another
                 // team waited for would tell this one nothing)
                 if (stage % LG_TEAMS == team && !all_rows(rows)) {
-                    ok = warp_wait(smem_u32(&s.landed[stage]), (parity >> stage) & 1, watch);
+                    // (whole row tiles before it, and other teams', are not waited for)
+                    ok = warp_wait_behind(smem_u32(&s.landed[stage]), (parity >> stage) & 1, watch, progress);
                     if (!ok)
                         break;
                     parity ^= 1u << stage;
@@ -462,7 +469,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             const bool any = steps > 0;
             const int acc = local & 1;
             if (any) {
-                if (!warp_wait(smem_u32(&s.tfull[acc]), (local >> 1) & 1, patient(watch, 2 * p.plans)))
+                if (!warp_wait_behind(smem_u32(&s.tfull[acc]), (local >> 1) & 1, watch, progress))
                     break;
                 ++local;
                 tc_fence_after();
