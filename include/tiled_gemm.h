@@ -564,8 +564,8 @@ int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int64_t ldx,
  *
  * The rank values scale * X_i A^T are FP32 sums.  On the tensor cores they
  * enter the second product in parts of the operands' type that together hold
- * 16 bits of them for BF16 operands (24 where a result of the call is F32) and
- * 22 for FP16 ones, with which they must stay within FP16's range: none below
+ * 16 bits of them for BF16 operands (24 for an F32 result, and in the backward
+ * pass) and 22 for FP16 ones, with which they must stay within FP16's range: none below
  * 2^-25 counts beside the shared product, none below 2^-45 in DA and DB.  All sums are
  * FP32, with one rounding to the output's type.  Results are identical run
  * to run.  Types, alignment and pitches as gemm_grouped.

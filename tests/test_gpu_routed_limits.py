@@ -7,6 +7,7 @@ import torch
 import tiled_matrix_multiplication_output_gb300 as tg
 from tests import routed_reference as ref
 from tests.test_gpu_grouped import _dev, _ints
+from tests.test_gpu_lora import Case
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,14 @@ def test_adapter_gradients_wait_behind_long_sums():
     _, da, db = tg.matmul_lora_backward(dy, x, w, a, b, adapter)
     assert tg.gemm_device_status(torch.cuda.current_stream().cuda_stream) == tg.binding.OK
     assert (da == 8 * rows).all() and (db == 8 * rows).all()
+
+
+@pytest.mark.parametrize("rank", [8, 24])
+def test_bf16_gradients_do_not_depend_on_the_other_results_types(rank):
+    """BF16 gradients have the same bits beside a BF16 dx as beside an FP32 one: rank values
+    of 16 bits would move about one in 300 of them over its rounding's border."""
+    c = Case(12, 1000, 1032, 2, rank, "bf16")
+    wide = c.backward(out_dtype=torch.float32, grad_dtype=torch.bfloat16)
+    narrow = c.backward(out_dtype=torch.bfloat16, grad_dtype=torch.bfloat16)
+    assert torch.equal(wide[0].bfloat16(), narrow[0])
+    assert torch.equal(wide[1], narrow[1]) and torch.equal(wide[2], narrow[2])

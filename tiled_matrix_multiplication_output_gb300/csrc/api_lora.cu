@@ -91,11 +91,12 @@ struct Workspace {
     void* copy(void* p) const { return static_cast<char*>(plan(p)) + plans; }
 };
 
-// How many parts hold a rank value: all bits of an FP32 sum for an FP32 result, and
-// for gradients from FP16 operands, which may be far below what two FP16 parts hold.
-int parts_for(int in_dtype, bool f32_result, bool gradients)
+// How many parts hold a rank value.  All bits of an FP32 sum in the backward pass, so
+// that no gradient depends on the other results' types, and for an FP32 result of BF16
+// operands; two parts are 2^-16 off, a 128th of a BF16 result's rounding.
+int parts_for(int in_dtype, bool f32_result, bool backward)
 {
-    return (in_dtype == GEMM_BF16 && f32_result) || (in_dtype == GEMM_F16 && gradients) ? 3 : 2;
+    return backward || (in_dtype == GEMM_BF16 && f32_result) ? 3 : 2;
 }
 
 // Whether one kernel makes the rank values and the product (on the current device).
@@ -204,8 +205,7 @@ extern "C" size_t gemm_lora_backward_workspace_size(const void* D, int64_t ldd, 
     if (check_sizes(lora, rows, N, K, in_dtype, out_dtype) != GEMM_OK || !valid_dtype(grad_dtype))
         return 0;
     const Operands o(X, ldx, D, ldd, W, ldw, *lora, rows, N, K, in_dtype);
-    const bool f32 = out_dtype == GEMM_F32 || grad_dtype == GEMM_F32;
-    return Workspace(2, *lora, rows, parts_for(in_dtype, f32, true), o).bytes();
+    return Workspace(2, *lora, rows, parts_for(in_dtype, false, true), o).bytes();
 }
 
 extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int64_t ldx,
@@ -238,7 +238,7 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
     if (db && (lddb < lora->rank || (lora->adapters > 1 && !apart(stride_db, N, lddb, lora->rank))))
         return GEMM_ERR_INVALID_VALUE;
     Operands o(X, ldx, D, ldd, W, ldw, *lora, rows, N, K, in_dtype);
-    const int parts = parts_for(in_dtype, out_dtype == GEMM_F32 || grad_dtype == GEMM_F32, true);
+    const int parts = parts_for(in_dtype, false, true);
     const Workspace ws(2, *lora, rows, parts, o);
     if (bad_workspace(workspace, workspace_bytes, ws.bytes()))
         return GEMM_ERR_INVALID_VALUE;
