@@ -79,3 +79,26 @@ def test_bf16_gradients_do_not_depend_on_the_other_results_types(rank):
     narrow = c.backward(out_dtype=torch.bfloat16, grad_dtype=torch.bfloat16)
     assert torch.equal(wide[0].bfloat16(), narrow[0])
     assert torch.equal(wide[1], narrow[1]) and torch.equal(wide[2], narrow[2])
+
+
+def _positive(seed, dtype, *shape):
+    g = torch.Generator().manual_seed(seed)
+    return (0.25 + torch.rand(*shape, generator=g)).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rank", [16, 32, 48, 64, 72, 128, 256])
+def test_adapter_gradients_of_long_sums_keep_fp32(rank, dtype):
+    """Sums over 8000 rows of one sign, for every number of accumulators.  A matrix
+    instruction drops less than a unit in the last place (2^-23), and an accumulator takes 48
+    of them: 96 half units (2^-24) at most; eleven segments of three parts are added
+    with a rounding each: 33; a rank value is four instructions, a rounding for the scale
+    and one for the parts: 10.  One accumulator for all rows would drop up to 1000."""
+    x, dy = _positive(1, dtype, 8000, 64), _positive(2, dtype, 8000, 64)
+    a, b = _positive(3, dtype, 2, rank, 64), _positive(4, dtype, 2, 64, rank)
+    adapter = torch.zeros(8000, dtype=torch.int32, device="cuda")
+    _, da, db = tg.matmul_lora_backward(dy, x, x[:64], a, b, adapter)
+    u, t = dy.double() @ b[0].double(), x.double() @ a[0].double().t()
+    for got, want in ((da, u.t() @ x.double()), (db, dy.double().t() @ t)):
+        assert ((got[0].double() - want).abs() <= 140 * 2.0 ** -24 * want).all()
+        assert not got[1].any()

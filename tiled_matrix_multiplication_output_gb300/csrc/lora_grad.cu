@@ -33,7 +33,8 @@ constexpr int LG_TEAMS = 4;      // pairs of warps that zero, each in its stages
 constexpr int LG_THREADS = 32 * (6 + 2 * LG_TEAMS);
 constexpr int LG_MAX_STAGES = 8;
 constexpr int LG_RING = 192 * 1024;  // beside 25 KiB of plans
-constexpr int LG_CHUNKS = 4;     // chunks of rank values in a tile
+constexpr int LG_CHUNKS = 4;     // chunks of 16 rank values in a tile
+constexpr int LG_SEGMENT = 6;    // row tiles that one accumulator adds up
 constexpr int LG_BOX = LT_ROWS * 128;  // bytes of 64 columns of a row tile
 
 struct GradSide {
@@ -62,7 +63,11 @@ struct GradParams {
 struct GradItem {
     int which, g, c0, chunk0, chunks;
     int n;  // columns of rank values that the tensor core reads
-    int chains;  // accumulators that row tiles take in turn (see lora_shrink.cu)
+    int chains;  // accumulators that row tiles take in turn
+    // row tiles after which they are added, with rounding, to FP32 sums in the epilogue
+    // warps' registers (the tensor core drops what does not fit when it adds: over 8000 rows
+    // of one sign 3e-5 in one accumulator)
+    __device__ int segment() const { return LG_SEGMENT * chains; }
 };
 
 // The plans of all row tiles in shared memory, where they fit: every tile of the
@@ -367,21 +372,21 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             RowTiles tiles(p, s.plans, w.g);
             int tile;
             uint32_t rows[4];
-            const int acc = local & 1;
-            const uint32_t d = tmem + acc * 256;
             const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
-            int steps = 0;
+            int n = 0;  // row tiles of the segment
             while (ok && tiles.next(tile, rows)) {
-                if (steps == 0)
+                const int acc = local & 1;
+                if (n == 0)
                     ok = warp_wait(smem_u32(&s.tempty[acc]), ((local >> 1) & 1) ^ 1, watch);
                 ok = ok && warp_wait(smem_u32(&s.full[stage]), phase, watch);
                 if (!ok)
                     break;
                 tc_fence_after();
                 const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 2 * LG_BOX;
+                const bool last = n == w.segment() - 1;
                 if (elect_one()) {
-                    bool first = steps < w.chains;
-                    const uint32_t to = d + steps % w.chains * w.chunks * 64;
+                    bool first = n < w.chains;
+                    const uint32_t to = tmem + acc * 256 + n % w.chains * w.chunks * 64;
 #pragma unroll
                     for (int k = 0; k < LT_ROWS / TC_UMMA_K; ++k) {
                         if (!has_slice(rows, k))
@@ -391,17 +396,20 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                         first = false;
                     }
                     tc_commit(smem_u32(&s.empty[stage]));
+                    if (last)
+                        tc_commit(smem_u32(&s.tfull[acc]));
                 }
                 __syncwarp();
-                ++steps;
+                n = last ? 0 : n + 1;
+                local += last;
                 if (++stage == p.stages) {
                     stage = 0;
                     phase ^= 1;
                 }
             }
-            if (ok && steps > 0) {
+            if (ok && n > 0) {
                 if (elect_one())
-                    tc_commit(smem_u32(&s.tfull[acc]));
+                    tc_commit(smem_u32(&s.tfull[local & 1]));
                 __syncwarp();
                 ++local;
             }
@@ -463,54 +471,59 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             RowTiles tiles(p, s.plans, w.g);
             int tile;
             uint32_t rows[4];
-            int steps = 0;  // (as many as matter here)
-            while (steps < w.chains && tiles.next(tile, rows))
-                ++steps;
-            const bool any = steps > 0;
-            const int acc = local & 1;
-            if (any) {
-                if (!warp_wait_behind(smem_u32(&s.tfull[acc]), (local >> 1) & 1, watch, progress))
+            float sum[LG_CHUNKS][16] = {};
+            bool ok = true;
+            for (bool more = tiles.next(tile, rows); more;) {
+                int n = 0;  // row tiles of the segment
+                do {
+                    ++n;
+                    more = tiles.next(tile, rows);
+                } while (more && n < w.segment());
+                const int acc = local & 1;
+                ok = warp_wait_behind(smem_u32(&s.tfull[acc]), (local >> 1) & 1, watch, progress);
+                if (!ok)
                     break;
-                ++local;
                 tc_fence_after();
-            }
-            const int c = w.c0 + q * 32 + static_cast<int>(lane);
-            OutT* out = static_cast<OutT*>(side.G) + w.g * side.stride_g + c * side.step_c;
-            const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-#pragma unroll 1
-            for (int k = 0; k < w.chunks; ++k)
-#pragma unroll 1
-                for (int j0 = 0; j0 < p.lay.chunk; j0 += 16) {
-                    const int j = (w.chunk0 + k) * p.lay.chunk + j0;
-                    if (j >= p.rank)
-                        break;
-                    float sum[16] = {};
-#pragma unroll 1
-                    for (int chain = 0; chain < steps; ++chain)
-#pragma unroll 1
-                        for (int part = 0; part < p.lay.parts; ++part) {
-                            uint32_t v[16];
-                            tmem_ld_32x32b_x16(from + (chain * w.chunks + k) * 64 + part * p.lay.chunk + j0, v);
-                            tmem_wait_ld(v);
+                const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+                const int chains = min(n, w.chains);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                sum[i] = fmaf(part < p.lay.plain ? 1.0f : 1.0f / LT_FINE, __uint_as_float(v[i]),
-                                              sum[i]);
-                        }
-                    if (c < side.cols && side.words) {
-                        put_words(out + j, sum, p.rank - j);
-                    } else if (c < side.cols) {
+                for (int k = 0; k < LG_CHUNKS; ++k)
+                    if (k < w.chunks)
+#pragma unroll 1
+                        for (int chain = 0; chain < chains; ++chain)
+#pragma unroll 1
+                            for (int part = 0; part < p.lay.parts; ++part) {
+                                uint32_t v[16];
+                                tmem_ld_32x32b_x16(from + (chain * w.chunks + k) * 64 + part * 16, v);
+                                tmem_wait_ld(v);
+                                const float scale = part < p.lay.plain ? 1.0f : 1.0f / LT_FINE;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (j + i < p.rank)
-                                put(out + (j + i) * side.step_j, sum[i]);
-                    }
-                }
-            if (any) {
+                                for (int i = 0; i < 16; ++i)
+                                    sum[k][i] = fmaf(scale, __uint_as_float(v[i]), sum[k][i]);
+                            }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_u32(&s.tempty[acc]));
+                ++local;
+            }
+            if (!ok)
+                break;
+            const int c = w.c0 + q * 32 + static_cast<int>(lane);
+            OutT* out = static_cast<OutT*>(side.G) + w.g * side.stride_g + c * side.step_c;
+#pragma unroll
+            for (int k = 0; k < LG_CHUNKS; ++k) {
+                const int j = (w.chunk0 + k) * 16;
+                if (k >= w.chunks || c >= side.cols)
+                    continue;
+                if (side.words) {
+                    put_words(out + j, sum[k], p.rank - j);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (j + i < p.rank)
+                            put(out + (j + i) * side.step_j, sum[k][i]);
+                }
             }
         }
     }
@@ -550,7 +563,7 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
     p.rank = l.rank;
     p.plans = (l.rows + LT_ROWS - 1) / LT_ROWS;
     p.plan = static_cast<const LoraPlan*>(l.plan);
-    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);
+    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);  // (of three parts: chunks of 16)
     p.groups_j = (p.lay.chunks + LG_CHUNKS - 1) / LG_CHUNKS;
     p.stage_bytes = LG_BOX * (2 + std::min(p.lay.chunks, LG_CHUNKS));
     p.stages = std::min(LG_MAX_STAGES, LG_RING / p.stage_bytes);
