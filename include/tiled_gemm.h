@@ -563,10 +563,13 @@ int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int64_t ldx,
  * counterpart.
  *
  * The rank values scale * X_i A^T are FP32 sums.  On the tensor cores they
- * enter the second product in parts of the operands' type that together hold
- * 16 bits of them for BF16 operands (24 for an F32 result, and in the backward
- * pass) and 22 for FP16 ones, with which they must stay within FP16's range: none below
- * 2^-25 counts beside the shared product, none below 2^-45 in DA and DB.  All sums are
+ * enter the second product in parts of BF16, which have FP32's range and
+ * together hold 16 bits of them for BF16 operands (24 for an F32 result, and in
+ * the backward pass) and 24 for FP16 ones, whose factors become two BF16 values
+ * each, without loss.  In DA and DB rank values of FP16 operands enter in parts
+ * of FP16: there they must stay within FP16's range, and none below 2^-45
+ * counts.  Where an infinity is among the operands of a row's own sums, its
+ * result may be a NaN though the formula has an infinity.  All sums are
  * FP32, with one rounding to the output's type.  Results are identical run
  * to run.  Types, alignment and pitches as gemm_grouped.
  */

@@ -102,3 +102,26 @@ def test_adapter_gradients_of_long_sums_keep_fp32(rank, dtype):
     for got, want in ((da, u.t() @ x.double()), (db, dy.double().t() @ t)):
         assert ((got[0].double() - want).abs() <= 140 * 2.0 ** -24 * want).all()
         assert not got[1].any()
+
+
+@pytest.mark.parametrize("rows,N,K,G,order", [(20, 136, 264, 3, "mixed"), (100, 264, 520, 90, "mixed"),
+                                              (300, 1000, 264, 3, "runs"), (1300, 2056, 264, 9, "mixed"),
+                                              (130, 40008, 72, 2, "mixed")])
+@pytest.mark.parametrize("rank", [4, 16, 40, 128])
+@pytest.mark.parametrize("size", [1e-4, 1e-2, 1.0, 300.0, 20000.0])
+def test_fp16_products_with_rank_values_of_any_size(rows, N, K, G, order, rank, size):
+    """Rank values from 1e-8 to 1e9, far below FP16's least step and above its largest
+    value, in every form of the product and its input's gradient: rank values keep 24 bits
+    (the bound is that of BF16 operands, with no absolute term)."""
+    c = Case(rows, N, K, G, rank, "f16", order, seed=rank)
+    small = min(size, 1.0)
+    for t, by in ((c.x, size), (c.dy, size), (c.w, small), (c.a, min(size, 300.0)), (c.b, min(size, 300.0))):
+        t.copy_((t.float() * by).clamp(-60000, 60000))
+    y, dx = c.forward(), c.backward()[0]
+    x, dy, w, a, b = (t.double() for t in (c.x, c.dy, c.w, c.a, c.b))
+    full = (torch.bfloat16, torch.float32)
+    ref.check(y, *ref._beside(x, w.t(), a, b.transpose(1, 2), c.adapter, c.scale, *full))
+    ref.check(dx, *ref._beside(dy, w, b.transpose(1, 2), a, c.adapter, c.scale, *full))
+    if size == 1.0:
+        half = c.forward(out_dtype=torch.float16)
+        ref.check(half, *ref._beside(x, w.t(), a, b.transpose(1, 2), c.adapter, c.scale, *full))

@@ -93,11 +93,15 @@ struct Workspace {
 
 // How many parts hold a rank value.  All bits of an FP32 sum in the backward pass, so
 // that no gradient depends on the other results' types, and for an FP32 result of BF16
-// operands; two parts are 2^-16 off, a 128th of a BF16 result's rounding.
+// operands, and for FP16 operands, whose results are finer; two parts are 2^-16 off, a
+// 128th of a BF16 result's rounding.
 int parts_for(int in_dtype, bool f32_result, bool backward)
 {
-    return backward || (in_dtype == GEMM_BF16 && f32_result) ? 3 : 2;
+    return backward || in_dtype == GEMM_F16 || f32_result ? 3 : 2;
 }
+// How many sets of rank values the backward pass keeps: towards DX and DA, and DB; from FP16
+// operands those towards DA are apart (lora_tc.cuh).
+int backward_sides(int in_dtype) { return in_dtype == GEMM_F16 ? 3 : 2; }
 
 // Whether one kernel makes the rank values and the product (on the current device).
 bool one_kernel(const Operands& o, const gemm_lora_t& l, int64_t rows, int64_t N, int64_t K, int parts)
@@ -205,7 +209,7 @@ extern "C" size_t gemm_lora_backward_workspace_size(const void* D, int64_t ldd, 
     if (check_sizes(lora, rows, N, K, in_dtype, out_dtype) != GEMM_OK || !valid_dtype(grad_dtype))
         return 0;
     const Operands o(X, ldx, D, ldd, W, ldw, *lora, rows, N, K, in_dtype);
-    return Workspace(2, *lora, rows, parts_for(in_dtype, false, true), o).bytes();
+    return Workspace(backward_sides(in_dtype), *lora, rows, parts_for(in_dtype, false, true), o).bytes();
 }
 
 extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int64_t ldx,
@@ -239,7 +243,7 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
         return GEMM_ERR_INVALID_VALUE;
     Operands o(X, ldx, D, ldd, W, ldw, *lora, rows, N, K, in_dtype);
     const int parts = parts_for(in_dtype, false, true);
-    const Workspace ws(2, *lora, rows, parts, o);
+    const Workspace ws(backward_sides(in_dtype), *lora, rows, parts, o);
     if (bad_workspace(workspace, workspace_bytes, ws.bytes()))
         return GEMM_ERR_INVALID_VALUE;
     DeviceInfo dev;
@@ -256,15 +260,18 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
     u.parts = parts;
     u.t = ws.side(workspace, 0);
     u.plan = ws.plan(workspace);
+    const bool f16 = in_dtype == GEMM_F16;
+    if (f16)
+        u.t_grad = ws.side(workspace, 2);
     LoraLaunch t = make_launch(o, false, *lora, adapter, rows, N, K, in_dtype, dev, &maps);  // scale * X A^T
     t.parts = parts;
-    t.t = ws.side(workspace, 1);
+    (f16 ? t.t_grad : t.t) = ws.side(workspace, 1);
     t.plan = u.plan;
 
     LoraGradLaunch a{};  // dA from X and u
     a.P = o.x.p;
     a.ldp = o.x.ld;
-    a.t = u.t;
+    a.t = f16 ? u.t_grad : u.t;
     a.parts = parts;
     a.plan = u.plan;
     a.maps = &maps;
@@ -285,7 +292,7 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
     LoraGradLaunch b = a;  // dB from D and t
     b.P = o.d.p;
     b.ldp = o.d.ld;
-    b.t = t.t;
+    b.t = f16 ? t.t_grad : t.t;
     b.G = DB;
     b.step_c = lddb;
     b.step_j = 1;
@@ -297,6 +304,10 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
             err = launch();
     };
     const bool need_u = adapters && (dx || da);
+    if (f16 && !dx)
+        u.t = nullptr;
+    if (f16 && !da)
+        u.t_grad = nullptr;
     if (o.tc) {
         step(need_u, [&] { return lora_shrink_tc_launch(u, db ? &t : nullptr, s); });
         step(!need_u && db, [&] { return lora_shrink_tc_launch(t, nullptr, s); });

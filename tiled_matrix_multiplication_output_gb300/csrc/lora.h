@@ -40,6 +40,8 @@ struct LoraLaunch {
     int in_dtype, out_dtype;  // DT_*
     void* t;              // the rank values: FP32, rows x rank, or in parts (lora_tc.cuh)
     int parts;
+    void* t_grad;         // of FP16 operands: the same in FP16 parts, for the gradients (or null,
+                          // as may then be t)
     void* plan;           // one for each 128 rows
     TensorMaps* maps;     // the call's
     int num_sms;
@@ -52,7 +54,7 @@ struct LoraLaunch {
 struct LoraGradLaunch {
     const void* P;        // rows x cols
     int64_t ldp;
-    const void* t;        // as LoraLaunch has them
+    const void* t;        // as LoraLaunch has them (of FP16 operands: t_grad)
     int parts;
     const void* plan;
     TensorMaps* maps;

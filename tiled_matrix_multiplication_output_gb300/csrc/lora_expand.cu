@@ -9,6 +9,9 @@
 // once.  Bound by the tensor cores as the shared product alone: 8192 rows of 12
 // adapters of rank 64 by 4096 x 4096, BF16, 151 us (1.86 PFLOP/s).
 //
+// Of FP16 operands, a warp of each CTA splits its half of a factor in two in shared
+// memory (lora_tc.cuh) before the step counts as loaded.
+//
 // Launched as a programmatic dependent of the kernel that makes the rank values: it
 // waits for them only when the first tile's shared product has been issued.
 #include <algorithm>
@@ -23,6 +26,7 @@ namespace {
 
 constexpr int LE_STAGES = 3;
 constexpr int LE_KSUB = 2;
+constexpr int LE_THREADS = TC_THREADS + 32;  // a last warp splits factors
 
 struct ExpandParams {
     int M, N, k_blocks, rank;
@@ -36,6 +40,8 @@ struct ExpandParams {
     int64_t ldc;
     int unit;             // row_unit of the output
     uint32_t idesc;       // with N = 0
+    bool split;           // FP16 factors, split in two
+    uint32_t idesc_e;     // of the adapters' products: BF16
     int* status;
     long long wait_budget;
     int fault_skip_kblock;
@@ -48,7 +54,7 @@ struct ExpandLayout {
     static constexpr int OFF_B = STEPS * SUB;
     static constexpr int OFF_STAGING = OFF_B + STEPS * SUB;
     static constexpr int OFF_BAR = OFF_STAGING + 4 * 4096;
-    static constexpr int NUM_BARS = STEPS + LE_STAGES + 5;
+    static constexpr int NUM_BARS = 2 * STEPS + LE_STAGES + 5;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
     static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
     static_assert(SMEM_ALLOC <= 232448, "exceeds 227 KiB of dynamic shared memory");
@@ -122,7 +128,7 @@ __device__ __forceinline__ Item item(int t, const ExpandParams& p)
 }
 
 template <bool ACROSS, typename OutT>
-__global__ void __launch_bounds__(TC_THREADS, 1)
+__global__ void __launch_bounds__(LE_THREADS, 1)
     lora_expand_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmE,
                        const __grid_constant__ CUtensorMap tmW64, const __grid_constant__ CUtensorMap tmE64,
@@ -139,8 +145,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     auto tfull_bar = [&](int a) { return bar0 + 8u * (L::STEPS + LE_STAGES + a); };
     auto tempty_bar = [&](int a) { return bar0 + 8u * (L::STEPS + LE_STAGES + 2 + a); };
     const uint32_t drain_bar = bar0 + 8u * (L::STEPS + LE_STAGES + 4);
+    // a step whose factor is to be split lands on this CTA's own barrier first
+    auto landed_bar = [&](int at) { return bar0 + 8u * (L::STEPS + LE_STAGES + 5 + at); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+    volatile int* progress = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 8);  // steps copied
 
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
@@ -152,15 +161,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < LE_STAGES; ++s) {
             for (int j = 0; j < LE_KSUB; ++j)
-                mbar_init(full_bar(s, j), 1);
+                mbar_init(full_bar(s, j), p.split ? 2 : 1);  // (either CTA's factor)
             mbar_init(empty_bar(s), 1);
         }
+        for (int at = 0; at < L::STEPS; ++at)
+            mbar_init(landed_bar(at), 1);
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
             mbar_init(tempty_bar(a), 8);  // every epilogue warp of the pair
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
+        *progress = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmW);
@@ -185,6 +197,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll
         for (int s = 0; s < L::STEPS; ++s)
             issued[s] = 0;
+        uint32_t to_split = 0, parity = 0;  // steps that last landed on their own barrier; how often
+        int steps = 0;
         bool ok = true, waited = false;
         auto next_stage = [&] {
             sub = 0;
@@ -198,19 +212,30 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             for (int s = 0; s < L::STEPS; ++s)  // (registers: no indexing)
                 issued[s] += s == at;
         };
-        // One K step: load(A's place, B's place, barrier).
-        auto step = [&](bool skip, uint32_t bytes, auto load) {
+        // One K step: load(A's place, B's place, barrier); split: its factor is to be split.
+        auto step = [&](bool skip, bool split, uint32_t bytes, auto load) {
             if (sub == 0 && !warp_wait(empty_bar(stage), phase ^ 1, watch))
                 return false;
+            ++steps;
+            if (p.split && lane == 0)
+                *progress = steps;
             if (!skip) {
                 const int at = stage * LE_KSUB + sub;
                 if (elect_one()) {
-                    if (leader)
+                    if (split) {
+                        mbar_arrive_expect_tx(landed_bar(at), bytes / 2);
+                    } else if (leader) {
+                        if (p.split)
+                            mbar_arrive(full_bar(stage, sub));
                         mbar_arrive_expect_tx(full_bar(stage, sub), bytes);
-                    load(sA + at * L::SUB, sB + at * L::SUB, mapa_shared(full_bar(stage, sub), 0));
+                    }
+                    load(sA + at * L::SUB, sB + at * L::SUB,
+                         split ? mapa_shared(landed_bar(at), rank) : mapa_shared(full_bar(stage, sub), 0));
                 }
                 __syncwarp();
                 count(at);
+                to_split = split ? to_split | 1u << at : to_split & ~(1u << at);
+                parity ^= static_cast<uint32_t>(split) << at;
             }
             if (++sub == LE_KSUB)
                 next_stage();
@@ -238,7 +263,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             };
             for (int kb = 0; ok && kb < p.k_blocks; ++kb) {
                 const int k = kb * TC_BK;
-                ok = step(kb == p.fault_skip_kblock, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                ok = step(kb == p.fault_skip_kblock, false, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
                     tma_load_2d_pair(dA, &tmX, bar, k, row);
                     auto load = [&](const CUtensorMap* map) {
                         return [=](uint32_t to, int c) {
@@ -262,7 +287,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     const int z = p.one ? 0 : g;
                     for (int c = 0; ok && c < p.lay.chunks; ++c) {
                         const int j = c * p.lay.chunk;
-                        ok = step(false, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                        ok = step(false, p.split, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
                             tma_load_2d_pair(dA, &tmT, bar, c * 64, row);
                             auto load = [&](const CUtensorMap* map) {
                                 return [=](uint32_t to, int o) {
@@ -275,19 +300,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 }
             }
             if (ok && sub != 0) {
-                if (leader && elect_one())
-                    mbar_arrive(full_bar(stage, 1));  // the stage's unused step
+                if (leader && elect_one()) {  // the stage's unused step
+                    mbar_arrive(full_bar(stage, 1));
+                    if (p.split)
+                        mbar_arrive(full_bar(stage, 1));
+                }
                 __syncwarp();
                 count(stage * LE_KSUB + 1);
+                to_split &= ~(1u << (stage * LE_KSUB + 1));
                 next_stage();
             }
         }
-        if (!ok && leader && lane == 0) {
-            // wait (bounded) for the loads already issued, of both CTAs,
-            // before shared memory goes away
+        if (!ok && lane == 0) {
+            // wait (bounded) for the loads already issued (those of both CTAs, but each CTA
+            // its own factors to be split) before shared memory goes away
             for (int s = 0; s < L::STEPS; ++s) {
+                const bool own = (to_split >> s) & 1;
+                const uint32_t bar = own ? landed_bar(s) : bar0 + 8u * s;
+                const uint32_t phase_of = own ? ((parity >> s) & 1) ^ 1 : (issued[s] - 1) & 1;
                 const long long t0 = clock64();
-                while (issued[s] > 0 && !mbar_try_wait(bar0 + 8u * s, (issued[s] - 1) & 1) &&
+                while ((own || (leader && issued[s] > 0)) && !mbar_try_wait(bar, phase_of) &&
                        clock64() - t0 < p.wait_budget) {
                 }
             }
@@ -310,7 +342,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 }
             };
             auto step = [&](auto multiply) {
-                if (!warp_wait(full_bar(stage, sub), phase, watch))
+                if (!(p.split ? warp_wait<true>(full_bar(stage, sub), phase, watch)
+                              : warp_wait(full_bar(stage, sub), phase, watch)))
                     return false;
                 tc_fence_after();
                 const int at = stage * LE_KSUB + sub;
@@ -354,15 +387,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     for (int g = list.next(off); ok && g >= 0; g = list.next(off))
                         for (int c = 0; ok && c < p.lay.chunks; ++c)
                             ok = step([&](uint32_t a0, uint32_t b0) {
-                                const int deep = p.lay.deep(c, p.rank);
-                                for (int part = 0; part < p.lay.plain; ++part)
-                                    for (int k = 0; k < deep; ++k)
-                                        tc_mma_f16_lanes(
-                                            d_tmem,
-                                            smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
-                                            ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                                   : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                            idesc, 1, off);
+                                const uint32_t idesc_e = p.idesc_e | static_cast<uint32_t>(w.n >> 3) << 17;
+                                each_product(p.lay, p.lay.deep(c, p.rank), p.split, [&](int part, int pair, int k) {
+                                    const int b = pair * p.lay.chunk / 16 + k;
+                                    tc_mma_f16_lanes(
+                                        d_tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
+                                        ACROSS ? smem_desc_sw128(b0 + b * 2048, 8192, 1024)
+                                               : smem_desc_sw128(b0 + b * 32, 16, 1024),
+                                        idesc_e, 1, off);
+                                });
                             });
                 }
                 if (!ok)
@@ -380,6 +413,40 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             __syncwarp();
             const long long t0 = clock64();
             while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
+            }
+        }
+    } else if (warp == LE_THREADS / 32 - 1) {
+        // ------------------------------------------------ factors in two
+        if (p.split && p.adapters) {
+            grid_dep_wait();
+            int at = 0;           // the step's place
+            uint32_t parity = 0;  // a bit for each
+            bool ok = true;
+            for (int t = unit; ok && t < p.items; t += num_units) {
+                const Item w = item(t, p);
+                PairAdapters list;
+                list.begin(p, w.mb);
+                at = (at + p.k_blocks) % L::STEPS;
+                uint32_t off[8];
+                for (int g = list.next(off); ok && g >= 0; g = list.next(off))
+                    for (int c = 0; ok && c < p.lay.chunks; ++c) {
+                        // (the steps of the shared product are not waited for)
+                        ok = warp_wait_behind(landed_bar(at), (parity >> at) & 1, watch, progress);
+                        if (!ok)
+                            break;
+                        parity ^= 1u << at;
+                        const uint32_t tile = sbase + L::OFF_B + at * L::SUB;
+                        if (ACROSS)
+                            split_across(tile, w.n / 128);
+                        else
+                            split_rows(tile, w.n / 2, 128);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_cluster(mapa_shared(bar0 + 8u * at, 0));
+                        at = (at + 1) % L::STEPS;
+                    }
+                at = (at + at % LE_KSUB) % L::STEPS;  // (behind a stage's unused step)
             }
         }
     } else {
@@ -449,7 +516,7 @@ cudaError_t launch(const CUtensorMap (&m)[6], ExpandParams& p, int num_sms, cuda
     static ClusterCaps caps;
     int cap = 0;
     const cudaError_t err =
-        cluster_cap(lora_expand_kernel<ACROSS, OutT>, caps, 2, TC_THREADS, L::SMEM_ALLOC, num_sms, &cap);
+        cluster_cap(lora_expand_kernel<ACROSS, OutT>, caps, 2, LE_THREADS, L::SMEM_ALLOC, num_sms, &cap);
     if (err != cudaSuccess)
         return err;
     // The tiles of a last wave that leaves at least half of the pairs idle are
@@ -458,7 +525,7 @@ cudaError_t launch(const CUtensorMap (&m)[6], ExpandParams& p, int num_sms, cuda
     p.whole = rest > 0 && 2 * rest <= pairs ? tiles - rest : tiles;
     p.items = p.whole + 2 * (tiles - p.whole);
     const int units = std::min(pairs, p.items);
-    ClusterLaunch l(static_cast<unsigned>(2 * units), 2, TC_THREADS, L::SMEM_ALLOC, stream, p.adapters);
+    ClusterLaunch l(static_cast<unsigned>(2 * units), 2, LE_THREADS, L::SMEM_ALLOC, stream, p.adapters);
     return l.run(lora_expand_kernel<ACROSS, OutT>, m[0], m[1], m[2], m[3], m[4], m[5], p);
 }
 
@@ -478,7 +545,7 @@ cudaError_t launch(int out_dtype, const CUtensorMap (&m)[6], ExpandParams& p, in
 
 }  // namespace
 
-int lora_parts_bytes(int rank, int parts) { return 2 * lora_parts(rank, parts, DT_BF16).columns(); }
+int lora_parts_bytes(int rank, int parts) { return 2 * lora_parts(rank, parts).columns(); }
 
 cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
 {
@@ -493,11 +560,13 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     p.tiles_n = (l.N + 255) / 256;
     p.adapters = l.adapters > 0;
     p.one = l.adapters == 1 || l.stride_e == 0;
-    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);
+    p.lay = lora_parts(l.rank, l.parts);
     p.plan = static_cast<const LoraPlan*>(l.plan);
     p.C = l.Y;
     p.ldc = l.ldy;
-    p.idesc = tc_idesc(l.in_dtype == DT_BF16, 256, 0, false, l.across);
+    p.split = l.in_dtype == DT_F16;
+    p.idesc = tc_idesc(!p.split, 256, 0, false, l.across);
+    p.idesc_e = tc_idesc(true, 256, 0, false, l.across);
     p.status = l.status;
     p.wait_budget = l.wait_budget;
     p.fault_skip_kblock = l.fault_skip_kblock;
@@ -516,7 +585,7 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
               weights(&m[1], TC_BM) && weights(&m[4], 64);
     m[2] = m[3] = m[5] = m[0];
     if (ok && p.adapters)
-        ok = l.maps->get(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, TC_BM, 1}) &&
+        ok = l.maps->get(&m[2], DT_BF16, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0}, {64, TC_BM, 1}) &&
              factors(&m[3], TC_BM) && factors(&m[5], 64);
     if (!ok)
         return cudaErrorNotSupported;

@@ -52,6 +52,7 @@ struct GradParams {
     int plans;
     const LoraPlan* plan;
     LoraParts lay;
+    bool f16;            // parts of FP16
     int groups_j;        // tiles of rank values
     int stages, stage_bytes;
     int box_rows;        // rows that a copy brings (what lies behind is zeroed, as others' rows)
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                                 uint32_t v[16];
                                 tmem_ld_32x32b_x16(from + (chain * w.chunks + k) * 64 + part * 16, v);
                                 tmem_wait_ld(v);
-                                const float scale = part < p.lay.plain ? 1.0f : 1.0f / LT_FINE;
+                                const float scale = p.f16 && part == 2 ? 1.0f / LT_FINE : 1.0f;
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
                                     sum[k][i] = fmaf(scale, __uint_as_float(v[i]), sum[k][i]);
@@ -563,7 +564,8 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
     p.rank = l.rank;
     p.plans = (l.rows + LT_ROWS - 1) / LT_ROWS;
     p.plan = static_cast<const LoraPlan*>(l.plan);
-    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);  // (of three parts: chunks of 16)
+    p.lay = lora_parts(l.rank, l.parts);  // (of three parts: chunks of 16)
+    p.f16 = l.in_dtype == DT_F16;
     p.groups_j = (p.lay.chunks + LG_CHUNKS - 1) / LG_CHUNKS;
     p.stage_bytes = LG_BOX * (2 + std::min(p.lay.chunks, LG_CHUNKS));
     p.stages = std::min(LG_MAX_STAGES, LG_RING / p.stage_bytes);

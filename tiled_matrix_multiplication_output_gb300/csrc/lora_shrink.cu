@@ -32,7 +32,8 @@ struct ShrinkSide {
     int across;
     int one;  // one factor for every adapter
     uint32_t idesc;
-    void* t;  // parts, rows x columns()
+    void* t;       // BF16 parts, rows x columns()
+    void* t_grad;  // FP16 parts, laid out the same (either may be null)
 };
 
 struct ShrinkParams {
@@ -62,17 +63,14 @@ struct ShrinkSmem {
     LoraPlan plan;
 };
 
-// The parts of rank values j .. j + 7 (a multiple of 8) of a row.
-template <typename T>
-__device__ __forceinline__ void store_parts(T* t, float (&left)[8], const LoraParts& lay, int j)
+// The place of rank values j .. j + 7 (a multiple of 8) of a row in parts: that of the
+// first part, and how far each next one lies behind (16-byte words).
+__device__ __forceinline__ uint4* parts_at(void* t, int64_t row, const LoraParts& lay, int j)
 {
-    t += (j / lay.chunk) * 64 + j % lay.chunk;
-    each_part<T>(left, lay, [&](int part, const uint4& w) {
-        *reinterpret_cast<uint4*>(t + part * lay.chunk) = w;
-    });
+    return static_cast<uint4*>(t) + (row * lay.columns() + j / lay.chunk * 64 + j % lay.chunk) / 8;
 }
 
-template <typename T, int SPLITS>
+template <int SPLITS>
 __global__ void __launch_bounds__(LS_THREADS, 1)
     lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX0, const __grid_constant__ CUtensorMap tmF0,
                           const __grid_constant__ CUtensorMap tmX1, const __grid_constant__ CUtensorMap tmF1,
@@ -288,7 +286,6 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     constexpr int SHARE = LT_ROWS / SPLITS;
     const int eights = p.cols / 8;
     const int total = min(SHARE, p.rows - row0 - split * SHARE) * eights;  // none where negative
-    T* t = static_cast<T*>(side.t) + static_cast<int64_t>(row0) * p.lay.columns();
 #pragma unroll 1
     for (int i = threadIdx.x; i < total && !gave_up; i += LS_THREADS) {
         const int row = split * SHARE + i / eights, j = i % eights * 8;
@@ -324,7 +321,19 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
             for (int q = 0; q < 8; ++q)
                 sum[q] = j + q < p.rank ? sum[q] : 0.0f;
         }
-        store_parts(t + static_cast<int64_t>(row) * p.lay.columns(), sum, p.lay, j);
+        const int next = p.lay.chunk / 8;
+        if (side.t_grad) {
+            float left[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                left[q] = sum[q];
+            uint4* to = parts_at(side.t_grad, row0 + row, p.lay, j);
+            each_f16_part(left, [&](int part, const uint4& w) { to[part * next] = w; });
+        }
+        if (side.t) {
+            uint4* to = parts_at(side.t, row0 + row, p.lay, j);
+            each_part(sum, p.lay.parts, [&](int part, const uint4& w) { to[part * next] = w; });
+        }
     }
     if constexpr (SPLITS > 1) {
         __syncwarp();
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
 // Once for each device: the SM's memory is laid out for this kernel and the
 // product's from the start, as it is not laid out anew while a block runs (a
 // decoding batch took 28 us instead of 25).
-template <typename T, int SPLITS>
+template <int SPLITS>
 cudaError_t share_sms()
 {
     static std::atomic<uint64_t> done{0};
@@ -344,7 +353,7 @@ cudaError_t share_sms()
     cudaError_t err = cudaGetDevice(&device);
     if (err != cudaSuccess || device < 0 || device >= kMaxDevices || (done.load() >> device & 1))
         return err;
-    err = cudaFuncSetAttribute(lora_shrink_tc_kernel<T, SPLITS>,
+    err = cudaFuncSetAttribute(lora_shrink_tc_kernel<SPLITS>,
                                cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (err == cudaSuccess)
@@ -354,40 +363,39 @@ cudaError_t share_sms()
 
 // Sets the kernel up, once; how many of its clusters run at a time, with the
 // smaller ring (shared) or the larger.
-template <typename T, int SPLITS>
+template <int SPLITS>
 cudaError_t most_clusters(bool shared, int num_sms, int* cap)
 {
     static ClusterCaps caps[2];
-    cudaError_t err = share_sms<T, SPLITS>();
+    cudaError_t err = share_sms<SPLITS>();
     int n[2] = {};
     for (int i = 0; i < 2 && err == cudaSuccess; ++i)  // (the larger last: it stays the kernel's limit)
-        err = cluster_cap(lora_shrink_tc_kernel<T, SPLITS>, caps[i], SPLITS, LS_THREADS,
+        err = cluster_cap(lora_shrink_tc_kernel<SPLITS>, caps[i], SPLITS, LS_THREADS,
                           (i ? LS_RING : LS_RING_SHARED) + 1024, num_sms, &n[i]);
     *cap = n[shared ? 0 : 1];
     return err;
 }
 
-template <typename T, int SPLITS>
+template <int SPLITS>
 cudaError_t launch(const CUtensorMap (&m)[4], const ShrinkParams& p, unsigned clusters, int smem,
                    cudaStream_t stream)
 {
     ClusterLaunch l(clusters * SPLITS, SPLITS, LS_THREADS, smem, stream);
-    return l.run(lora_shrink_tc_kernel<T, SPLITS>, m[0], m[1], m[2], m[3], p);
+    return l.run(lora_shrink_tc_kernel<SPLITS>, m[0], m[1], m[2], m[3], p);
 }
 
 // CTAs for every SM, in clusters that run all at once: first the contraction is
 // split, then the adapters are dealt out.
-template <typename T>
 cudaError_t launch(const CUtensorMap (&m)[4], ShrinkParams& p, int sides, int most_k, int most_adapters,
                    bool shared, int num_sms, cudaStream_t stream)
 {
     static SplitCaps known[2];
     const int* most = nullptr;
     const cudaError_t err = split_caps(known[shared], [&](int i, int* n) {
-        return i == 0   ? most_clusters<T, 1>(shared, num_sms, n)
-               : i == 1 ? most_clusters<T, 2>(shared, num_sms, n)
-               : i == 2 ? most_clusters<T, 4>(shared, num_sms, n)
-                        : most_clusters<T, 8>(shared, num_sms, n);
+        return i == 0   ? most_clusters<1>(shared, num_sms, n)
+               : i == 1 ? most_clusters<2>(shared, num_sms, n)
+               : i == 2 ? most_clusters<4>(shared, num_sms, n)
+                        : most_clusters<8>(shared, num_sms, n);
     }, &most);
     if (err != cudaSuccess)
         return err;
@@ -400,13 +408,13 @@ cudaError_t launch(const CUtensorMap (&m)[4], ShrinkParams& p, int sides, int mo
     const int smem = (shared ? LS_RING_SHARED : LS_RING) + 1024;
     switch (i) {
     case 0:
-        return launch<T, 1>(m, p, clusters, smem, stream);
+        return launch<1>(m, p, clusters, smem, stream);
     case 1:
-        return launch<T, 2>(m, p, clusters, smem, stream);
+        return launch<2>(m, p, clusters, smem, stream);
     case 2:
-        return launch<T, 4>(m, p, clusters, smem, stream);
+        return launch<4>(m, p, clusters, smem, stream);
     default:
-        return launch<T, 8>(m, p, clusters, smem, stream);
+        return launch<8>(m, p, clusters, smem, stream);
     }
 }
 
@@ -450,7 +458,7 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
     p.adapters = l.adapters;
     p.rank = l.rank;
     p.cols = (l.rank + 15) / 16 * 16;
-    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);
+    p.lay = lora_parts(l.rank, l.parts);
     p.tiles = (l.rows + LT_ROWS - 1) / LT_ROWS;
     p.box_rows = std::min(LT_ROWS, (l.rows + 7) / 8 * 8);
     const uint32_t box_rows = static_cast<uint32_t>(p.box_rows);
@@ -470,7 +478,7 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
         const LoraLaunch& s = i ? *second : first;
         const uint32_t cols = static_cast<uint32_t>(p.cols);
         p.side[i] = {(s.K + TC_BK - 1) / TC_BK, s.across, s.adapters == 1 || s.stride_f == 0,
-                     tc_idesc(s.in_dtype == DT_BF16, LT_ROWS, p.cols, false, s.across), s.t};
+                     tc_idesc(s.in_dtype == DT_BF16, LT_ROWS, p.cols, false, s.across), s.t, s.t_grad};
         p.b_bytes[i] = (s.across ? (p.cols + 63) / 64 * 64 : p.cols) * 128;
         most_k = std::max(most_k, p.side[i].k_blocks);
         const int64_t stride = p.side[i].one ? s.ldf : s.stride_f;
@@ -501,9 +509,7 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
     p.stages = std::min(LS_MAX_STAGES,
                         ((shared ? LS_RING_SHARED : LS_RING) - p.a_offset - 16384) / p.stage_bytes + 1);
     const int most_adapters = std::min(std::min(l.adapters, LT_ROWS), l.rows);
-    return l.in_dtype == DT_BF16
-               ? launch<__nv_bfloat16>(m, p, sides, most_k, most_adapters, shared, l.num_sms, stream)
-               : launch<__half>(m, p, sides, most_k, most_adapters, shared, l.num_sms, stream);
+    return launch(m, p, sides, most_k, most_adapters, shared, l.num_sms, stream);
 }
 
 }  // namespace tmmo

@@ -34,7 +34,8 @@
 namespace tmmo {
 namespace {
 
-constexpr int LM_THREADS = 256;  // warps 0: copies, 1: MMA, 2: rank values, 4-7: plan, accumulators
+// warps 0: copies, 1: MMA, 2: rank values, 3: FP16 factors in two, 4-7: plan, accumulators
+constexpr int LM_THREADS = 256;
 constexpr int LM_MAX_STAGES = 8;
 constexpr int LM_RING = 200 * 1024;
 constexpr int LM_RING_SHARED = 120 * 1024;  // leaves room for the shrink's kernel on the SM
@@ -58,13 +59,16 @@ struct SmallParams {
     int stages, stage_bytes, ring;
     bool words;              // 16-byte stores
     int out_dtype;
-    // Adapters of up to 32 rank values: the tile's rank values stay in shared
+    // Adapters of one chunk of rank values: the tile's rank values stay in shared
     // memory (behind the ring), and a stage holds the factors of several adapters,
-    // rows of 32 or 64 bytes; 0: an adapter a stage, with the rank values.
+    // rows of 32 or 64 bytes (width); 0: an adapter a stage, with the rank values.
     int beside;
+    uint32_t width;
+    bool split;              // FP16 factors, split in two (lora_tc.cuh)
+    uint32_t idesc_e;        // of the adapters' products: BF16
     // Where the kernel makes the rank values: rows of X times the factors F
     const float* scale;
-    bool one_f, bf16;
+    bool one_f;
     int together;            // adapters whose factors come with a K step of W
     int extra;               // further ones share a stage of X and factors
     int w_bytes;             // of a stage before X: W, factors
@@ -77,8 +81,10 @@ struct SmallParams {
 
 struct SmallSmem {
     uint64_t full[LM_MAX_STAGES], empty[LM_MAX_STAGES], planned, held, done, thin, thin_all;
+    uint64_t landed[LM_MAX_STAGES];  // of steps whose factors are to be split
     uint32_t tmem;
     int abort_flag;
+    int progress;  // steps copied
     PlanScratch scratch;
     LoraPlan plan;
 };
@@ -156,6 +162,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(smem_u32(&s.full[i]), OWN ? 2 : 1);
             mbar_init(smem_u32(&s.empty[i]), 1);
+            mbar_init(smem_u32(&s.landed[i]), 1);
         }
         mbar_init(smem_u32(&s.planned), 128);
         mbar_init(smem_u32(&s.held), OWN ? 4 : 1);
@@ -163,6 +170,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         mbar_init(smem_u32(&s.thin), 1);
         mbar_init(smem_u32(&s.thin_all), 4 * SPLITS);
         s.abort_flag = 0;
+        s.progress = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmW);
@@ -182,17 +190,24 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     const uint32_t a_bytes = p.box_rows * 128;
     const uint32_t held = ring + p.ring;  // the tile's rank values
     float* const thin = reinterpret_cast<float*>(base + p.ring + LM_HELD);  // shares of their sums
+    volatile int* const progress = &s.progress;
 
     if (warp == 0) {
         int stage = 0, n = 0;
         uint32_t phase = 0;
-        auto step = [&](bool skip, uint32_t bytes, auto load) {
+        uint32_t to_split = 0, parity = 0;  // stages that last landed on their own barrier; how often
+        // split_e: the step's factors are to be split
+        auto step = [&](bool skip, bool split_e, uint32_t bytes, auto load) {
             if (!warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch))
                 return false;
+            if (p.split && lane == 0)
+                *progress = n + 1;
+            to_split = split_e ? to_split | 1u << stage : to_split & ~(1u << stage);
+            parity ^= static_cast<uint32_t>(split_e) << stage;
             if (!skip) {
-                const uint32_t bar = smem_u32(&s.full[stage]);
+                const uint32_t bar = smem_u32(split_e ? &s.landed[stage] : &s.full[stage]);
                 if (elect_one()) {
-                    if (OWN)
+                    if (OWN && !split_e)
                         mbar_arrive(bar);
                     mbar_arrive_expect_tx(bar, bytes);
                     load(ring + stage * p.stage_bytes + p.w_bytes, ring + stage * p.stage_bytes, bar);
@@ -248,7 +263,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             stage = ahead % p.stages;
             phase = ahead / p.stages;
             for (int kb = kb0 + ahead; ok && kb < kb1; ++kb)
-                ok = step(kb == p.fault_skip_kblock, a_bytes + 16384 + some * each,
+                ok = step(kb == p.fault_skip_kblock, false, a_bytes + 16384 + some * each,
                           [&](uint32_t dA, uint32_t dB, uint32_t bar) {
                               shared_product(kb, dA, dB, bar);
                               factors(0, some, kb, dB + 16384, bar);
@@ -256,24 +271,23 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             for (int a = p.together; ok && a < s.plan.count; a += p.extra) {
                 const int more = min(p.extra, s.plan.count - a);
                 for (int kb = kb0; ok && kb < kb1; ++kb)
-                    ok = step(false, a_bytes + more * each, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                    ok = step(false, false, a_bytes + more * each, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
                         tma_load_2d(dA, &tmX, bar, kb * TC_BK, row0);
                         factors(a, more, kb, dB, bar);
                     });
             }
         } else {
             for (int kb = kb0; ok && kb < kb1; ++kb)
-                ok = step(kb == p.fault_skip_kblock, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
-                    shared_product(kb, dA, dB, bar);
-                });
+                ok = step(kb == p.fault_skip_kblock, false, a_bytes + 16384,
+                          [&](uint32_t dA, uint32_t dB, uint32_t bar) { shared_product(kb, dA, dB, bar); });
         }
         if (ok && p.adapters > 0) {
             ok = warp_wait(smem_u32(&s.planned), 0, watch);
             if (!ACROSS && p.beside > 0) {
                 for (int a = split; ok && a < s.plan.count; a += p.beside * SPLITS) {
                     const int some = min(p.beside, (s.plan.count - a + SPLITS - 1) / SPLITS);
-                    const uint32_t each = p.lay.chunk * 2 * 128;
-                    ok = step(false, some * each, [&](uint32_t, uint32_t dB, uint32_t bar) {
+                    const uint32_t each = p.width * 128;
+                    ok = step(false, p.split, some * each, [&](uint32_t, uint32_t dB, uint32_t bar) {
                         for (int i = 0; i < some; ++i)
                             tma_load_3d(dB + i * each, &tmE, bar, 0, col0,
                                         p.one ? 0 : s.plan.ids[a + i * SPLITS]);
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     const int z = p.one ? 0 : s.plan.ids[a];
                     for (int c = 0; ok && c < p.lay.chunks; ++c) {
                         const int j = c * p.lay.chunk;
-                        ok = step(false, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                        ok = step(false, p.split, a_bytes + 16384, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
                             if (ACROSS) {
                                 tma_load_3d(dB, &tmE, bar, col0, j, z);
                                 tma_load_3d(dB + 8192, &tmE, bar, col0 + 64, j, z);
@@ -301,9 +315,11 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before shared memory goes away
             for (int i = 0; i < p.stages; ++i) {
                 const int uses = n / p.stages + (i < n % p.stages);
+                const bool own = (to_split >> i) & 1;
+                const uint32_t bar = smem_u32(own ? &s.landed[i] : &s.full[i]);
+                const uint32_t phase_of = own ? ((parity >> i) & 1) ^ 1 : (uses - 1) & 1;
                 const long long t0 = clock64();
-                while (uses > 0 && !mbar_try_wait(smem_u32(&s.full[i]), (uses - 1) & 1) &&
-                       clock64() - t0 < p.wait_budget) {
+                while (uses > 0 && !mbar_try_wait(bar, phase_of) && clock64() - t0 < p.wait_budget) {
                 }
             }
         }
@@ -375,21 +391,21 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         if (ok && p.adapters > 0) {
             ok = warp_wait(smem_u32(&s.planned), 0, watch);
             if (!ACROSS && p.beside > 0) {
-                const uint32_t width = p.lay.chunk * 2;
                 const int deep = p.lay.deep(0, p.rank);
                 grid_dep_wait();  // (so that no wait spans the kernel before)
                 ok = ok && warp_wait(smem_u32(&s.held), 0, watch);
                 for (int a = split; ok && a < s.plan.count; a += p.beside * SPLITS)
                     ok = step([&](uint32_t, uint32_t b0) {
                         const int some = min(p.beside, (s.plan.count - a + SPLITS - 1) / SPLITS);
-                        for (int i = 0; i < some; ++i, b0 += width * 128) {
+                        for (int i = 0; i < some; ++i, b0 += p.width * 128) {
                             uint32_t off[4];
                             others(a + i * SPLITS, off);
-                            for (int part = 0; part < p.lay.plain; ++part)
-                                for (int k = 0; k < deep; ++k)
-                                    tc_mma_f16_lanes(tmem,
-                                                     smem_desc_sw128(held + part * width + k * 32, 16, 1024),
-                                                     smem_desc_rows(b0 + k * 32, width), p.idesc, 1, off);
+                            each_product(p.lay, deep, p.split, [&](int part, int pair, int k) {
+                                const int b = pair * p.lay.chunk / 16 + k;
+                                tc_mma_f16_lanes(
+                                    tmem, smem_desc_sw128(held + part * p.lay.chunk * 2 + k * 32, 16, 1024),
+                                    smem_desc_rows(b0 + b * 32, p.width), p.idesc_e, 1, off);
+                            });
                         }
                     });
             } else {
@@ -399,14 +415,14 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     others(a, off);
                     for (int c = 0; ok && c < p.lay.chunks; ++c)
                         ok = step([&](uint32_t a0, uint32_t b0) {
-                            const int deep = p.lay.deep(c, p.rank);
-                            for (int part = 0; part < p.lay.plain; ++part)
-                                for (int k = 0; k < deep; ++k)
-                                    tc_mma_f16_lanes(
-                                        tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
-                                        ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                               : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                        p.idesc, 1, off);
+                            each_product(p.lay, p.lay.deep(c, p.rank), p.split, [&](int part, int pair, int k) {
+                                const int b = pair * p.lay.chunk / 16 + k;
+                                tc_mma_f16_lanes(
+                                    tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
+                                    ACROSS ? smem_desc_sw128(b0 + b * 2048, 8192, 1024)
+                                           : smem_desc_sw128(b0 + b * 32, 16, 1024),
+                                    p.idesc_e, 1, off);
+                            });
                         });
                 }
             }
@@ -428,6 +444,46 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             __syncwarp();
             // (also after the others gave up: nothing may land when this CTA is gone)
             warp_wait(smem_u32(&s.held), 0, watch);
+        }
+    } else if (warp == 3 && p.adapters > 0 && p.split) {
+        grid_dep_wait();  // (so that no wait spans the kernel before)
+        bool ok = warp_wait(smem_u32(&s.planned), 0, watch);
+        const int count = ok ? s.plan.count : 0;
+        int n = kb1 - kb0;  // steps before
+        if (OWN && count > p.together)
+            n += (count - p.together + p.extra - 1) / p.extra * (kb1 - kb0);
+        uint32_t parity = 0;  // a bit for each stage
+        // split(tile) of the next step's factors
+        auto step = [&](auto split_tile) {
+            const int stage = n++ % p.stages;
+            // (the steps before are not waited for)
+            if (!warp_wait_behind(smem_u32(&s.landed[stage]), (parity >> stage) & 1, watch, progress))
+                return false;
+            parity ^= 1u << stage;
+            split_tile(ring + stage * p.stage_bytes);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&s.full[stage]));
+                if (OWN)
+                    mbar_arrive(smem_u32(&s.full[stage]));
+            }
+            return true;
+        };
+        if (!ACROSS && p.beside > 0) {
+            for (int a = split; ok && a < count; a += p.beside * SPLITS)
+                ok = step([&](uint32_t tile) {
+                    split_rows(tile, 128 * min(p.beside, (count - a + SPLITS - 1) / SPLITS), p.width);
+                });
+        } else {
+            for (int a = split; a < count; a += SPLITS)
+                for (int c = 0; ok && c < p.lay.chunks; ++c)
+                    ok = step([&](uint32_t tile) {
+                        if (ACROSS)
+                            split_across(tile, 2);
+                        else
+                            split_rows(tile, 128, 128);
+                    });
         }
     } else if (warp >= 4 && p.adapters > 0) {
         const int place = make_plan(s.plan, s.scratch, g, threadIdx.x - 128, [] { bar_sync(1, 128); });
@@ -502,10 +558,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                         const uint32_t at = (part * p.lay.chunk + j) / 8;
                         st_shared_v4(held + row * 128 + ((at ^ (row & 7)) << 4), w.x, w.y, w.z, w.w);
                     };
-                    if (p.bf16)
-                        each_part<__nv_bfloat16>(sum, p.lay, store);
-                    else
-                        each_part<__half>(sum, p.lay, store);
+                    each_part(sum, p.lay.parts, store);
                 }
             }
             fence_proxy_async_smem();
@@ -678,7 +731,7 @@ cudaError_t launch_small(const LoraLaunch& l, bool own, cudaStream_t stream)
     p.tiles_n = (l.N + 127) / 128;
     p.adapters = l.adapters;
     p.one = l.adapters == 1 || l.stride_e == 0;
-    p.lay = lora_parts(l.rank, l.parts, l.in_dtype);
+    p.lay = lora_parts(l.rank, l.parts);
     p.adapter = l.adapter;
     p.C = l.Y;
     p.ldc = l.ldy;
@@ -687,13 +740,15 @@ cudaError_t launch_small(const LoraLaunch& l, bool own, cudaStream_t stream)
     const bool bf16 = l.in_dtype == DT_BF16;
     p.idesc = tc_idesc(bf16, LT_ROWS, 128, false, l.across);
     p.box_rows = std::min(LT_ROWS, (l.rows + 7) / 8 * 8);
-    p.beside = p.adapters && !l.across && p.lay.chunks == 1 ? 16384 / (p.lay.chunk * 2 * 128) : 0;
+    p.split = !bf16;
+    p.idesc_e = tc_idesc(true, LT_ROWS, 128, false, l.across);
+    p.width = static_cast<uint32_t>(p.lay.chunk * (p.split ? 4 : 2));
+    p.beside = p.adapters && !l.across && p.lay.chunks == 1 ? static_cast<int>(16384 / (p.width * 128)) : 0;
     p.w_bytes = 16384;
     if (own) {
         const int each = p.lay.chunk * 128;
         p.scale = l.scale;
         p.one_f = l.adapters == 1 || l.stride_f == 0;
-        p.bf16 = bf16;
         p.together = std::min(std::min(l.adapters, l.rows), LM_FACTORS / each);
         p.w_bytes += p.together * each;
         p.extra = p.w_bytes / each;
@@ -720,11 +775,11 @@ cudaError_t launch_small(const LoraLaunch& l, bool own, cudaStream_t stream)
         const int64_t stacked = p.one ? 1 : l.adapters, stride = p.one ? l.lde : l.stride_e;
         ok = (own ? l.maps->get(&m[2], dt, l.F, 3, {l.K, l.rank, p.one_f ? 1 : l.adapters},
                                 {l.ldf, p.one_f ? l.ldf : l.stride_f}, {64, chunk, 1})
-                  : l.maps->get(&m[2], dt, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0},
+                  : l.maps->get(&m[2], DT_BF16, l.t, 2, {p.lay.columns(), l.rows, 1}, {p.lay.columns(), 0},
                                 {64, box, 1})) &&
              (l.across ? l.maps->get(&m[3], dt, l.E, 3, {l.N, l.rank, stacked}, {l.lde, stride}, {64, TC_BK, 1})
                        : l.maps->get(&m[3], dt, l.E, 3, {l.rank, l.N, stacked}, {l.lde, stride},
-                                    {p.beside ? chunk : 64u, 128, 1}));
+                                    {p.beside ? p.width / 2 : 64u, 128, 1}));
     }
     if (!ok)
         return cudaErrorNotSupported;
@@ -747,7 +802,7 @@ bool lora_small_takes(const LoraLaunch& l) { return small_tiles(l.rows, l.N) <= 
 bool lora_alone_takes(int64_t rows, int64_t N, int64_t K, int64_t adapters, int rank, int parts, int num_sms)
 {
     const int64_t tiles = small_tiles(rows, N), k_blocks = (K + TC_BK - 1) / TC_BK;
-    if (adapters == 0 || tiles > num_sms || lora_parts(rank, parts, DT_BF16).chunks > 1)
+    if (adapters == 0 || tiles > num_sms || lora_parts(rank, parts).chunks > 1)
         return false;
     int splits = 1;
     if (small_splits<false, true>(tiles, k_blocks, num_sms, &splits) != cudaSuccess)

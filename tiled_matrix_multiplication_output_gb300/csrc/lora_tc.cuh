@@ -7,14 +7,19 @@
 // ascending, with the rows of each.
 //
 // The rank values t are FP32 sums that enter a second product as operands of 16
-// bits, in parts: t = p0 + p1 (+ p2), each the rounding of what the ones before
-// leave, multiplied by the same factor.  Two parts hold 16 bits of a BF16 value
-// and 22 of an FP16 one, three hold 24.  An FP16 part is no finer than 2^-24, which
-// a product may leave out beside the shared one, but not a gradient that is nothing
-// but rank values times rows (its values may be 1e-6): its third part is of 2^20
-// times what the two leave, and has an accumulator of its own.  They lie in chunks of
-// `chunk` rank values, 64 columns (128 bytes, a swizzle row) a chunk: part p of value
-// j at column (j / chunk) * 64 + p * chunk + j % chunk.
+// bits, in BF16 parts, which have FP32's range: t = p0 + p1 (+ p2), each the rounding
+// of what the ones before leave, multiplied by the same factor.  Two parts hold 16
+// bits, three 24.  A matrix instruction takes both operands in one type: a factor
+// in FP16 is split in shared memory into two BF16 values, which hold all of
+// its 11 bits.  (FP16 parts would lose what is below 2^-25, 1e-6 of a young
+// adapter's gradients being 3 % off, and turn what is above 65504 into infinities.)
+//
+// The gradients multiply rank values by rows instead, which in FP16 are not worth
+// splitting: there the parts are FP16, the third of 2^20 times what the two leave, with an
+// accumulator of its own.
+//
+// Parts lie in chunks of `chunk` rank values, 64 columns (128 bytes, a swizzle row) a
+// chunk: part p of value j at column (j / chunk) * 64 + p * chunk + j % chunk.
 #pragma once
 
 #include <cuda.h>
@@ -144,7 +149,6 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
 // How the rank values are laid out.
 struct LoraParts {
     int parts, chunk, chunks;
-    int plain;    // parts to the scale of 1; one behind them is to that of LT_FINE
     __host__ __device__ int columns() const { return 64 * chunks; }
     // 16-deep instructions of each part in chunk c
     __host__ __device__ int deep(int c, int rank) const
@@ -153,34 +157,107 @@ struct LoraParts {
         return ((left < chunk ? left : chunk) + 15) / 16;
     }
 };
-inline LoraParts lora_parts(int rank, int parts, int dtype)
+inline LoraParts lora_parts(int rank, int parts)
 {
     const int chunk = rank <= 16 || parts == 3 ? 16 : 32;
-    return {parts, chunk, (rank + chunk - 1) / chunk, dtype == DT_F16 ? 2 : parts};
+    return {parts, chunk, (rank + chunk - 1) / chunk};
 }
 
-// Eight rank values in parts: store(part, its eight values).
-template <typename T, typename Store>
-__device__ __forceinline__ void each_part(float (&left)[8], const LoraParts& lay, Store store)
+// The rounding of eight values; what it leaves of them stays.
+template <typename T>
+__device__ __forceinline__ uint4 take_part(float (&left)[8])
+{
+    T h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        put(&h[i], left[i]);
+        const float f = to_f32(h[i]);
+        left[i] = isfinite(f) ? left[i] - f : 0.0f;  // an infinity has no remainder
+    }
+    uint4 w;
+    memcpy(&w, h, 16);
+    return w;
+}
+
+// Eight rank values in BF16 parts: store(part, its eight values).
+template <typename Store>
+__device__ __forceinline__ void each_part(float (&left)[8], int parts, Store store)
 {
 #pragma unroll 1
-    for (int part = 0; part < lay.parts; ++part) {
-        T h[8];
-        if (part == lay.plain) {
+    for (int part = 0; part < parts; ++part)
+        store(part, take_part<__nv_bfloat16>(left));
+}
+
+// The same in FP16 parts, for the gradients: two to the scale of 1, one to that of LT_FINE.
+constexpr int LT_F16_PARTS = 3;
+template <typename Store>
+__device__ __forceinline__ void each_f16_part(float (&left)[8], Store store)
+{
+    store(0, take_part<__half>(left));
+    store(1, take_part<__half>(left));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                left[i] *= LT_FINE;
-        }
+    for (int i = 0; i < 8; ++i)
+        left[i] *= LT_FINE;
+    store(2, take_part<__half>(left));
+}
+
+// Eight FP16 values at `at` in shared memory as pairs of BF16 ones: the first of each in
+// their place, the second at `rest`.
+__device__ __forceinline__ void split_eight(uint32_t at, uint32_t rest)
+{
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(at)
+                 : "memory");
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t first[4], second[4];
+    __nv_bfloat16* const tag = nullptr;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            put(&h[i], left[i]);
-            const float f = to_f32(h[i]);
-            left[i] = isfinite(f) ? left[i] - f : 0.0f;  // an infinity has no remainder
-        }
-        uint4 w;
-        memcpy(&w, h, 16);
-        store(part, w);
+    for (int i = 0; i < 4; ++i) {
+        __half2 h;
+        memcpy(&h, &in[i], 4);
+        const float2 f = __half22float2(h);
+        first[i] = pack2(f.x, f.y, tag);
+        second[i] = pack2(f.x - __uint_as_float(first[i] << 16), f.y - __uint_as_float(first[i] & 0xffff0000u), tag);
     }
+    st_shared_v4(at, first[0], first[1], first[2], first[3]);
+    st_shared_v4(rest, second[0], second[1], second[2], second[3]);
+}
+
+// Splits a factor's tile of one chunk (16 rank values), a whole warp's work.  K-major: n
+// rows of 64 or 128 bytes, swizzled over them; the second values lie in the 16 columns
+// behind the first.
+__device__ __forceinline__ void split_rows(uint32_t tile, int n, uint32_t width)
+{
+#pragma unroll 8
+    for (int i = lane_id(); i < 2 * n; i += 32) {
+        const uint32_t r = i >> 1, u = i & 1, turn = width == 128 ? r & 7 : (r >> 1) & 3;
+        const uint32_t row = tile + r * width;
+        split_eight(row + ((u ^ turn) << 4), row + (((u + 2) ^ turn) << 4));
+    }
+}
+// Across: boxes of 64 outputs, a row of 128 bytes for each rank value; the second values
+// lie in the 16 rows behind the first (with the same swizzle).
+__device__ __forceinline__ void split_across(uint32_t tile, int boxes)
+{
+#pragma unroll 8
+    for (int i = lane_id(); i < 128 * boxes; i += 32) {
+        const uint32_t at = tile + (i >> 7) * 8192 + (i & 127) * 16;
+        split_eight(at, at + 2048);
+    }
+}
+
+// The products of a chunk's parts: multiply(part, pair, k) for each 16-deep instruction,
+// pair being 1 for the second values of a factor in two (of which the third part's
+// product is below 2^-24 of the sum).
+template <typename Multiply>
+__device__ __forceinline__ void each_product(const LoraParts& lay, int deep, bool split, Multiply multiply)
+{
+    for (int part = 0; part < lay.parts; ++part)
+        for (int pair = 0; pair <= static_cast<int>(split && part < 2); ++pair)
+            for (int k = 0; k < deep; ++k)
+                multiply(part, pair, k);
 }
 
 }  // namespace tmmo
