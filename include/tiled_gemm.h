@@ -566,9 +566,9 @@ int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int64_t ldx,
  * enter the second product in parts of BF16, which have FP32's range and
  * together hold 16 bits of them for BF16 operands (24 for an F32 result, and in
  * the backward pass) and 24 for FP16 ones, whose factors become two BF16 values
- * each, without loss.  In DA and DB rank values of FP16 operands enter in parts
- * of FP16: there they must stay within FP16's range, and none below 2^-45
- * counts.  Where an infinity is among the operands of a row's own sums, its
+ * each, without loss.  In DA and DB rank values of FP16 operands enter in FP16
+ * parts of four scales: there they must stay below 2.7e11, keep 23 bits down to
+ * 2^-13 and 11 at 2^-25, and do not count below 2^-45.  Where an infinity is among the operands of a row's own sums, its
  * result may be a NaN though the formula has an infinity.  All sums are
  * FP32, with one rounding to the output's type.  Results are identical run
  * to run.  Types, alignment and pitches as gemm_grouped.

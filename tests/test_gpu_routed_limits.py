@@ -125,3 +125,20 @@ def test_fp16_products_with_rank_values_of_any_size(rows, N, K, G, order, rank, 
     if size == 1.0:
         half = c.forward(out_dtype=torch.float16)
         ref.check(half, *ref._beside(x, w.t(), a, b.transpose(1, 2), c.adapter, c.scale, *full))
+
+
+@pytest.mark.parametrize("rank", [4, 16, 40, 128])
+@pytest.mark.parametrize("order", ["mixed", "runs"])
+@pytest.mark.parametrize("size", [1.0, 30.0, 300.0, 2000.0])
+def test_fp16_gradients_with_rank_values_above_fp16(size, order, rank):
+    """Rank values from 10 to 3e8, most of them above 65504 at the larger sizes, beside
+    others that are not: sums of the same relative precision."""
+    c = Case(700, 136, 264, 3, rank, "f16", order, seed=rank)
+    for t in (c.x, c.dy, c.a, c.b):
+        t.copy_((t.float() * size).clamp(-60000, 60000))
+    c.scale.copy_(torch.tensor([1.0, 0.01, -0.5]))
+    _, da, db = c.backward()
+    want = ref.lora_backward(c.dy, c.x, c.w, c.a, c.b, c.adapter, c.scale, torch.float32)
+    assert torch.isfinite(da).all() and torch.isfinite(db).all()
+    ref.check(da, *want[1])
+    ref.check(db, *want[2])

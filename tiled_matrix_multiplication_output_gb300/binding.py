@@ -1068,7 +1068,8 @@ def matmul_lora_backward(dy, x, w, a, b, adapter, scale=None, out_dtype=None, gr
     dy_i^T t_i over the rows of adapter g, with u_i = scale[g] dy_i @ b[g] and
     t_i = scale[g] x_i @ a[g]^T.  Adapters without rows get zeros.  out_dtype is
     dx's type (default FP32), grad_dtype that of da and db (default FP32).
-    Returns without synchronizing."""
+    With FP16 operands u_i and t_i must stay below 2.7e11 (beyond, da and db are
+    not finite).  Returns without synchronizing."""
     code, dtype, device = _begin(x, "x")
     rows, K, ldx = _rows_of(x, "x", None, device)
     rows2, N, ldd = _rows_of(dy, "dy", dtype, device)

@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                                 uint32_t v[16];
                                 tmem_ld_32x32b_x16(from + (chain * w.chunks + k) * 64 + part * 16, v);
                                 tmem_wait_ld(v);
-                                const float scale = p.f16 && part == 2 ? 1.0f / LT_FINE : 1.0f;
+                                const float scale = p.f16 ? f16_part_scale(part) : 1.0f;
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
                                     sum[k][i] = fmaf(scale, __uint_as_float(v[i]), sum[k][i]);
@@ -564,8 +564,8 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
     p.rank = l.rank;
     p.plans = (l.rows + LT_ROWS - 1) / LT_ROWS;
     p.plan = static_cast<const LoraPlan*>(l.plan);
-    p.lay = lora_parts(l.rank, l.parts);  // (of three parts: chunks of 16)
     p.f16 = l.in_dtype == DT_F16;
+    p.lay = lora_parts(l.rank, p.f16 ? LT_F16_PARTS : l.parts);  // (of three or four parts: chunks of 16)
     p.groups_j = (p.lay.chunks + LG_CHUNKS - 1) / LG_CHUNKS;
     p.stage_bytes = LG_BOX * (2 + std::min(p.lay.chunks, LG_CHUNKS));
     p.stages = std::min(LG_MAX_STAGES, LG_RING / p.stage_bytes);

@@ -15,8 +15,8 @@
 // adapter's gradients being 3 % off, and turn what is above 65504 into infinities.)
 //
 // The gradients multiply rank values by rows instead, which in FP16 are not worth
-// splitting: there the parts are FP16, the third of 2^20 times what the two leave, with an
-// accumulator of its own.
+// splitting: there the parts are FP16, each to a scale and with an accumulator of its own:
+// t = 2^22 h0 + 2^11 h1 + h2 + 2^-20 h3, from 2^-45 to 2.7e11.
 //
 // Parts lie in chunks of `chunk` rank values, 64 columns (128 bytes, a swizzle row) a
 // chunk: part p of value j at column (j / chunk) * 64 + p * chunk + j % chunk.
@@ -37,7 +37,7 @@
 namespace tmmo {
 
 constexpr int LT_ROWS = 128;  // rows of a tile, the lanes of a CTA
-constexpr float LT_FINE = 1048576.0f;  // 2^20: a remainder of 2^-8 at most stays below 65504
+constexpr int LT_F16_PARTS = 4;
 
 struct alignas(16) LoraPlan {
     int count;                  // adapters among the tile's rows
@@ -159,7 +159,7 @@ struct LoraParts {
 };
 inline LoraParts lora_parts(int rank, int parts)
 {
-    const int chunk = rank <= 16 || parts == 3 ? 16 : 32;
+    const int chunk = rank <= 16 || parts > 2 ? 16 : 32;
     return {parts, chunk, (rank + chunk - 1) / chunk};
 }
 
@@ -188,17 +188,38 @@ __device__ __forceinline__ void each_part(float (&left)[8], int parts, Store sto
         store(part, take_part<__nv_bfloat16>(left));
 }
 
-// The same in FP16 parts, for the gradients: two to the scale of 1, one to that of LT_FINE.
-constexpr int LT_F16_PARTS = 3;
+// What an FP16 part counts for.
+__device__ __forceinline__ float f16_part_scale(int part)
+{
+    return part == 0 ? 0x1p22f : part == 1 ? 0x1p11f : part == 2 ? 1.0f : 0x1p-20f;
+}
+// The same in FP16 parts, for the gradients.  A part of 2^11 or 2^22 takes what is too
+// large to leave less than 2^-5 to the parts of 1 and of 2^-20: rank values below 2^7 have
+// the last two, those below 2^26 two or three, 23 bits at least.
 template <typename Store>
 __device__ __forceinline__ void each_f16_part(float (&left)[8], Store store)
 {
-    store(0, take_part<__half>(left));
-    store(1, take_part<__half>(left));
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        left[i] *= LT_FINE;
+    for (int part = 0; part < 2; ++part) {
+        const float least = part == 0 ? 0x1p26f : 0x1p7f, scale = f16_part_scale(part);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = fabsf(left[i]) >= least ? left[i] * (1.0f / scale) : 0.0f;
+        float rest[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            rest[i] = v[i];
+        store(part, take_part<__half>(rest));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            left[i] = v[i] != 0.0f ? rest[i] * scale : left[i];
+    }
     store(2, take_part<__half>(left));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // (more is left of rank values above 2^19 alone: 2^-23 of them at most)
+        left[i] = fabsf(left[i]) <= 0x1p-5f ? left[i] * 0x1p20f : 0.0f;
+    store(3, take_part<__half>(left));
 }
 
 // Eight FP16 values at `at` in shared memory as pairs of BF16 ones: the first of each in
