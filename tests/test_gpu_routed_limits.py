@@ -142,3 +142,36 @@ def test_fp16_gradients_with_rank_values_above_fp16(size, order, rank):
     assert torch.isfinite(da).all() and torch.isfinite(db).all()
     ref.check(da, *want[1])
     ref.check(db, *want[2])
+
+
+# rows, K, the skipped step: of the rank values' 16 K steps (three row tiles); of the
+# gradients' 12 row tiles (two K steps), a whole one and the ragged one
+@pytest.mark.parametrize("rows,K,skip", [(300, 1024, 8), (1500, 128, 5), (1500, 128, 11)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_waits_of_rank_values_and_gradients_that_run_out_are_reported(rows, K, skip, dtype):
+    """The kernels' copies leave out a step (10 ms a wait): the status says so, the context
+    stays usable, and the next call is right.  Only B's gradient is asked for, so that no
+    product has a step of that number."""
+    c = Case(rows, 136, K, 1, 8, dtype, "one", ints=True)
+    code = tg.BF16 if dtype == "bf16" else tg.F16
+    lora = tg.LoraAdapters(c.a.data_ptr(), K, 8 * K, c.b.data_ptr(), 8, 136 * 8, c.scale.data_ptr(), 1, 8)
+    db = torch.empty(136, 8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call():
+        args = (c.dy.data_ptr(), 136, c.x.data_ptr(), K, c.w.data_ptr(), K, lora)
+        size = tg.gemm_lora_backward_workspace_size(*args, rows, 136, K, code, tg.F32, tg.F32)
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        assert tg.gemm_lora_backward(*args, c.adapter.data_ptr(), None, K, None, K, 8 * K, db.data_ptr(), 8,
+                                     136 * 8, rows, 136, K, code, tg.F32, tg.F32, ws.data_ptr(), size,
+                                     stream) == tg.binding.OK
+        return tg.gemm_device_status(stream)
+
+    assert call() == tg.binding.OK
+    want = db.clone()
+    tg.gemm_debug_config(20_000_000, skip)
+    assert call() == tg.binding.ERR_TIMEOUT
+    tg.gemm_debug_config(0, -1)
+    assert call() == tg.binding.OK
+    t = c.scale[0].double() * (c.x.double() @ c.a[0].double().T)
+    assert torch.equal(db, want) and torch.equal(db.double(), c.dy.double().T @ t)

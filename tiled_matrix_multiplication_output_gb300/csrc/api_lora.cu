@@ -289,6 +289,7 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
     a.num_sms = u.num_sms;
     a.status = u.status;
     a.wait_budget = u.wait_budget;
+    a.fault_skip_kblock = u.fault_skip_kblock;
     LoraGradLaunch b = a;  // dB from D and t
     b.P = o.d.p;
     b.ldp = o.d.ld;

@@ -66,6 +66,7 @@ struct LoraGradLaunch {
     int num_sms;
     int* status;
     long long wait_budget;
+    int fault_skip_kblock;  // (of an adapter's row tiles)
 };
 
 // Bytes of a row tile's plan, and of rank values in parts for a row.

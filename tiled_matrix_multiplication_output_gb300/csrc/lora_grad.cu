@@ -59,6 +59,7 @@ struct GradParams {
     uint32_t idesc;      // with N = 0
     int* status;
     long long wait_budget;
+    int fault_skip_kblock;
 };
 
 struct GradItem {
@@ -319,12 +320,13 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         for (int t = blockIdx.x; ok && t < p.items; t += gridDim.x) {
             const GradItem w = grad_item(t, p, s.plans);
             RowTiles tiles(p, s.plans, w.g);
-            int tile;
+            int tile, step = 0;
             uint32_t rows[4];
             while (ok && tiles.next(tile, rows)) {
                 const bool whole = all_rows(rows);
+                const bool skip = step++ == p.fault_skip_kblock;  // (test hook, -1 in normal use)
                 ok = warp_wait(smem_u32(&s.empty[stage]), phase ^ 1, watch);
-                if (ok && elect_one()) {
+                if (ok && !skip && elect_one()) {
                     const uint32_t bar = smem_u32(whole ? &s.full[stage] : &s.landed[stage]);
                     const uint32_t a0 = ring + stage * p.stage_bytes, b0 = a0 + 2 * LG_BOX;
                     const CUtensorMap* tmP = w.which ? &tmP1 : &tmP0;
@@ -342,8 +344,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
                 if (lane == 0)
                     *progress = steps;
                 if (ok) {
-                    ++n_full[stage];  // whichever barrier: full completes once a use
-                    n_landed[stage] += !whole;
+                    n_full[stage] += !skip;  // whichever barrier: full completes once a use
+                    n_landed[stage] += !skip && !whole;
                     if (++stage == p.stages) {
                         stage = 0;
                         phase ^= 1;
@@ -572,6 +574,7 @@ cudaError_t lora_grad_tc_launch(const LoraGradLaunch* const (&sides)[2], bool de
     p.idesc = tc_idesc(l.in_dtype == DT_BF16, 128, 0, true, true);
     p.status = l.status;
     p.wait_budget = l.wait_budget;
+    p.fault_skip_kblock = l.fault_skip_kblock;
     p.box_rows = std::min(LT_ROWS, (l.rows + 7) / 8 * 8);
     const uint32_t box_rows = static_cast<uint32_t>(p.box_rows);
     CUtensorMap m[4];

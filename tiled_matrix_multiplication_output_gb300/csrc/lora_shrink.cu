@@ -51,6 +51,7 @@ struct ShrinkParams {
     uint32_t tmem_cols;
     int* status;
     long long wait_budget;
+    int fault_skip_kblock;
 };
 
 struct ShrinkSmem {
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
                 const uint32_t bar = smem_u32(&s.full[stage]);
                 const uint32_t base = smem_u32(ring) + stage * p.stage_bytes;
                 const uint32_t dA = base + p.a_offset;
-                if (elect_one()) {
+                if (kb != p.fault_skip_kblock && elect_one()) {  // (test hook, -1 in normal use)
                     mbar_arrive_expect_tx(bar, p.box_rows * 128 + some * b_bytes);
                     tma_load_2d(dA, tmX, bar, kb * TC_BK, row0);
                     for (int i = 0; i < some; ++i) {
@@ -471,6 +472,7 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
         p.tmem_cols *= 2;
     p.status = l.status;
     p.wait_budget = l.wait_budget;
+    p.fault_skip_kblock = l.fault_skip_kblock;
     CUtensorMap m[4];
     const int sides = second ? 2 : 1;
     int most_k = 1;
