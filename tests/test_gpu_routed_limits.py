@@ -175,3 +175,49 @@ def test_waits_of_rank_values_and_gradients_that_run_out_are_reported(rows, K, s
     assert call() == tg.binding.OK
     t = c.scale[0].double() * (c.x.double() @ c.a[0].double().T)
     assert torch.equal(db, want) and torch.equal(db.double(), c.dy.double().T @ t)
+
+
+# What sums of one sign over K values may lose where an accumulator takes 64 matrix
+# instructions, each of which drops less than a unit (two half units, 2^-24) of what it
+# adds up to, and K / 1024 accumulators are added with a rounding each; two more roundings
+def _segments(K):
+    return (128 + K / 1024 + 2) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("op", ["t", "n"])
+@pytest.mark.parametrize("K", [1024, 1032, 8192, 20_000])
+def test_grouped_products_of_long_sums_keep_fp32(K, op):
+    """One accumulator for all of K dropped 3e-5 of 8192 values of one sign."""
+    off = [0, 300, 300, 333, 360]
+    x = _positive(1, torch.bfloat16, 360, K)
+    w = _positive(2, torch.bfloat16, 4, *((264, K) if op == "t" else (K, 264)))
+    y = tg.matmul_grouped(x, w, _dev(off), op_b=op)
+    want = ref.grouped(x, w, off, op == "t")[0]
+    assert ((y.double() - want).abs() <= _segments(K) * want).all()
+    y0 = torch.rand(360, 264, device="cuda")
+    added = tg.matmul_grouped(x, w, _dev(off), op_b=op, out=y0.clone(), alpha=0.5, beta=2.0)
+    want = 0.5 * want + 2.0 * y0.double()
+    assert ((added.double() - want).abs() <= _segments(K) * want).all()
+    # results of 16 bits, through either store: the rounding of the same sums
+    for pitch in (264, 265):
+        for dtype in (torch.bfloat16, torch.float16):
+            out = torch.empty(360, pitch, dtype=dtype, device="cuda")[:, :264]
+            tg.matmul_grouped(x, w, _dev(off), op_b=op, out=out, alpha=0.5)
+            assert torch.equal(out, (0.5 * y).to(dtype))
+
+
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("name", ["forward", "backward"])
+def test_fp16_waits_that_run_out_are_reported(name, few):
+    """As BF16's, with the warp that splits factors behind the copies."""
+    for c in ([Case(60, 264, 320, 5, 16, "f16", ints=True), Case(60, 264, 320, 60, 40, "f16", ints=True)] if few else
+              [Case(2100, 2056, 320, 5, 16, "f16", ints=True)]):
+        call = (lambda: (c.forward(),)) if name == "forward" else c.backward
+        want = call()
+        stream = torch.cuda.current_stream().cuda_stream
+        assert tg.gemm_device_status(stream) == tg.binding.OK
+        tg.gemm_debug_config(20_000_000, 1)
+        call()
+        assert tg.gemm_device_status(stream) == tg.binding.ERR_TIMEOUT
+        tg.gemm_debug_config(0, -1)
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))

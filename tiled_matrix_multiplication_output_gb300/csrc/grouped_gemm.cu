@@ -11,6 +11,11 @@ cudaError_t grouped_tc_launch(const GroupedLaunch& l, cudaStream_t stream)
     p.ldc = l.ldy;
     p.N = l.N;
     p.K = l.K;
+    // (in even shares, so that a segment's sums are taken while the next one is made)
+    const int k_blocks = (l.K + TC_BK - 1) / TC_BK;
+    p.segments = (k_blocks + GT_SEGMENT_PRODUCT - 1) / GT_SEGMENT_PRODUCT;
+    p.segment = (k_blocks + p.segments - 1) / p.segments;
+    p.segments = (k_blocks + p.segment - 1) / p.segment;
     p.tiles_f = (l.N + 255) / 256;
     p.alpha = l.alpha;
     p.beta = l.beta;

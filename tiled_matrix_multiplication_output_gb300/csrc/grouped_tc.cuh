@@ -16,11 +16,13 @@
 // 64 rows of a group hold rows of the next one; those among the last 16 that
 // the tensor core reads are zeroed in shared memory by a warp of each CTA,
 // in both operands (a zero against an infinity of another group would be a
-// NaN), before they count as loaded.  The tensor core drops what does not fit when it
-// adds to its accumulator, half a unit in the last place an instruction on
-// average (3e-6 of a sum over 2000 rows), and gradients are often kept in FP32: so
-// every 768 rows the accumulator is added, with rounding, to sums in the epilogue
-// warps' registers.
+// NaN), before they count as loaded.
+//
+// The tensor core drops what does not fit when it adds to its accumulator, half a unit in
+// the last place an instruction on average (3e-6 of a sum over 2000 products of one
+// sign, 3e-5 over 8000).  So every 768 rows of the gradient, every 1024 inputs of a
+// product, the accumulator is added, with rounding, to sums in the epilogue warps'
+// registers.
 //
 // Both are bound by the operands' way from L2 (a K step of a full tile takes 630
 // cycles, its MMAs 512) or, with few rows, by reading the weights from HBM.  BF16:
@@ -28,9 +30,9 @@
 // by 4096 x 2048 150 us (6.6 TB/s), the gradient of 16384 rows of 8 groups, 4096 x
 // 2048, FP32, 176 us (1.56 PFLOP/s).
 //
-// Warps: 0 TMA producer, 1 MMA issuer (of the leader CTA), 2 to 9 epilogue (with four,
-// 4148 rows of 17 groups by 1360 x 152 took 13.7 us, with eight 12.4; 16384 of 16 by
-// 4096 x 4096 300 and 303), for the gradient a last warp that zeroes.  A ring of K
+// Warps: 0 TMA producer, 1 MMA issuer (of the leader CTA), 2 for the gradient one that
+// zeroes, 4 to 11 epilogue (with four, 4148 rows of 17 groups by 1360 x 152 took
+// 13.7 us, with eight 12.4; 16384 of 16 by 4096 x 4096 300 and 303).  A ring of K
 // steps, bounded waits and two accumulators in tensor memory, as in tc_gemm_kernel.
 #pragma once
 
@@ -53,12 +55,14 @@ constexpr int GT_A_BYTES = TC_BM * TC_BK * 2;  // a K step of the lanes' side
 constexpr int GT_N = 256;        // the N side of a full tile
 constexpr int GT_SORTED = 256;   // groups, at most, that the gradient sorts
 constexpr int GT_SEGMENT = 12;   // K steps of the gradient that one accumulator adds up
+constexpr int GT_SEGMENT_PRODUCT = 16;  // the same of a product, at most
 
 struct GroupedTcParams {
     Grouping by;
     void* C;              // Y, or the gradients
     int64_t ldc, stride_c;
     int N, K;             // outputs and inputs of a weight
+    int segments, segment;  // products: how many parts of K, and their K steps
     int tiles_f, tiles_c; // 256-wide tiles of the lanes' axis; gradient: of the other one
     float alpha, beta;
     bool zero_rest;
@@ -76,7 +80,12 @@ template <int MODE>
 struct GroupedLayout {
     static constexpr bool WGRAD = MODE == GROUPED_WGRAD;
     static constexpr int EPI_WARPS = 8;
-    static constexpr int THREADS = 64 + 32 * EPI_WARPS + (WGRAD ? 32 : 0);
+    static constexpr int EPI_WARP0 = 4;
+    static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+    // Of the 168 registers a thread that the block is launched with, the first warps
+    // need few and the epilogue's sums many.
+    static constexpr int REGS_FEW = 88, REGS_EPI = 208;
+    static_assert(4 * REGS_FEW + EPI_WARPS * REGS_EPI <= (4 + EPI_WARPS) * 168, "of the block's registers");
     static constexpr int OFF_STAGING = GT_RING;
     static constexpr int STAGING = 2048;  // of an epilogue warp
     static constexpr int OFF_TABLE = OFF_STAGING + EPI_WARPS * STAGING;
@@ -270,175 +279,212 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         return WGRAD && kb == w.k_blocks - 1 && (w.rows & 15) != 0;
     };
 
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer
-        int stage = 0, steps = 0;
-        uint32_t phase = 0;
-        uint32_t ragged = 0, ragged_parity = 0;  // of the stages' tail barriers: used, and how often
-        bool ok = true;
-        for (int t = unit; ok && t < num_work; t += num_units) {
-            const GroupedWork w = grouped_work<MODE>(t, table, p);
-            const int f = w.f0 + static_cast<int>(rank) * TC_BM;
-            const int half = w.n / 2;
-            const int c = w.c0 + static_cast<int>(rank) * half;
-            const int z = p.one_weight ? 0 : w.g;
-            const uint32_t bytes = GT_A_BYTES + half * TC_BK * 2;
-            for (int kb = 0; kb < w.k_blocks; ++kb) {
-                ok = warp_wait(empty_bar(stage), phase ^ 1, watch);
-                if (!ok)
-                    break;
-                const bool tail = is_ragged(w, kb);
-                ++steps;
-                if (WGRAD && lane == 0)
-                    *progress = steps;
-                if (kb != p.fault_skip_kblock) {  // (test hook, -1 in normal use)
-                    if (elect_one()) {
-                        if (tail) {
-                            mbar_arrive_expect_tx(tail_bar(stage), bytes);
-                        } else if (leader) {
-                            if (WGRAD)
-                                mbar_arrive(full_bar(stage));
-                            mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
-                        }
-                        const uint32_t bar = tail ? mapa_shared(tail_bar(stage), rank)
-                                                  : mapa_shared(full_bar(stage), 0);
-                        const uint32_t dA = sbase + stage * stage_bytes, dB = dA + GT_A_BYTES;
-                        if constexpr (WGRAD) {
-                            const int row = w.row0 + kb * TC_BK;
-                            tma_load_2d_pair(dA, &tmA, bar, f, row);
-                            tma_load_2d_pair(dA + 8192, &tmA, bar, f + 64, row);
-                            tma_load_2d_pair(dB, &tmB, bar, c, row);
-                            if (half > 64)
-                                tma_load_2d_pair(dB + 8192, &tmB, bar, c + 64, row);
-                        } else {
-                            const int k = kb * TC_BK;
-                            auto weights = [&](uint32_t dst, int x, int y) {
-                                tma_load_3d_pair(dst, &tmA, bar, x, p.swap ? z : y, p.swap ? y : z);
-                            };
-                            if (A_MN) {
-                                weights(dA, f, k);
-                                weights(dA + 8192, f + 64, k);
-                            } else {
-                                weights(dA, k, f);
-                            }
-                            // the tile's rows in boxes of 128, 64, 32 and 16
-                            if (half == 128) {
-                                tma_load_2d_pair(dB, &tmB, bar, k, c);
-                            } else {
-                                int b = 0;
-                                if (half & 64) {
-                                    tma_load_2d_pair(dB, &tmB64, bar, k, c);
-                                    b = 64;
-                                }
-                                if (half & 32) {
-                                    tma_load_2d_pair(dB + b * 128, &tmB32, bar, k, c + b);
-                                    b += 32;
-                                }
-                                if (half & 16)
-                                    tma_load_2d_pair(dB + b * 128, &tmB16, bar, k, c + b);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                    if (tail) {
-                        ragged |= 1u << stage;
-                        ragged_parity ^= 1u << stage;
-                    }
-                }
-                if (++stage == stages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        if (!ok && lane == 0) {
-            // Wait (bounded) for the loads already issued before shared
-            // memory goes away: the leader's barriers cover both CTAs.
-            auto drain = [&](uint32_t bar, uint32_t parity) {
-                const long long t0 = clock64();
-                while (!mbar_try_wait(bar, parity) && clock64() - t0 < p.wait_budget) {
-                }
-            };
-            for (int s = 0; s < stages; ++s) {
-                const int uses = steps / stages + (s < steps % stages);
-                if (leader && uses > 0)
-                    drain(full_bar(s), (uses - 1) & 1);
-                if (WGRAD && ((ragged >> s) & 1))
-                    drain(tail_bar(s), ((ragged_parity >> s) & 1) ^ 1);
-            }
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer
-        if (leader) {
-            int stage = 0;
+    if (warp < L::EPI_WARP0) {
+        set_max_regs_dec<L::REGS_FEW>();
+        if (warp == 0) {
+            // ------------------------------------------------ TMA producer
+            int stage = 0, steps = 0;
             uint32_t phase = 0;
-            int local = 0;
+            uint32_t ragged = 0, ragged_parity = 0;  // of the stages' tail barriers: used, and how often
             bool ok = true;
             for (int t = unit; ok && t < num_work; t += num_units) {
                 const GroupedWork w = grouped_work<MODE>(t, table, p);
-                if (w.k_blocks == 0)
-                    continue;
-                const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
-                uint32_t d_tmem = 0;
+                const int f = w.f0 + static_cast<int>(rank) * TC_BM;
+                const int half = w.n / 2;
+                const int c = w.c0 + static_cast<int>(rank) * half;
+                const int z = p.one_weight ? 0 : w.g;
+                const uint32_t bytes = GT_A_BYTES + half * TC_BK * 2;
                 for (int kb = 0; kb < w.k_blocks; ++kb) {
-                    const bool first = WGRAD ? kb % GT_SEGMENT == 0 : kb == 0;
-                    const bool last = kb == w.k_blocks - 1 || (WGRAD && kb % GT_SEGMENT == GT_SEGMENT - 1);
-                    if (first) {
-                        ok = warp_wait<true>(tempty_bar(local & 1), ((local >> 1) & 1) ^ 1, watch);
-                        d_tmem = tmem_base + static_cast<uint32_t>((local & 1) * GT_N);
-                    }
-                    ok = ok && warp_wait<WGRAD>(full_bar(stage), phase, watch);
+                    ok = warp_wait(empty_bar(stage), phase ^ 1, watch);
                     if (!ok)
                         break;
-                    tc_fence_after();
-                    const uint32_t a0 = sbase + stage * stage_bytes, b0 = a0 + GT_A_BYTES;
-                    // 16-deep instructions; gradient: as many as there are rows
-                    const int deep = WGRAD ? min(4, (w.rows - kb * TC_BK + 15) / 16) : 4;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < TC_BK / TC_UMMA_K; ++k) {
-                            if (WGRAD && k >= deep)
-                                break;
-                            const uint64_t adesc = A_MN ? smem_desc_sw128(a0 + k * 2048, 8192, 1024)
-                                                        : smem_desc_sw128(a0 + k * 32, 16, 1024);
-                            const uint64_t bdesc = WGRAD ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                                         : smem_desc_sw128(b0 + k * 32, 16, 1024);
-                            tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, !first || k != 0);
+                    const bool tail = is_ragged(w, kb);
+                    ++steps;
+                    if (WGRAD && lane == 0)
+                        *progress = steps;
+                    if (kb != p.fault_skip_kblock) {  // (test hook, -1 in normal use)
+                        if (elect_one()) {
+                            if (tail) {
+                                mbar_arrive_expect_tx(tail_bar(stage), bytes);
+                            } else if (leader) {
+                                if (WGRAD)
+                                    mbar_arrive(full_bar(stage));
+                                mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+                            }
+                            const uint32_t bar = tail ? mapa_shared(tail_bar(stage), rank)
+                                                      : mapa_shared(full_bar(stage), 0);
+                            const uint32_t dA = sbase + stage * stage_bytes, dB = dA + GT_A_BYTES;
+                            if constexpr (WGRAD) {
+                                const int row = w.row0 + kb * TC_BK;
+                                tma_load_2d_pair(dA, &tmA, bar, f, row);
+                                tma_load_2d_pair(dA + 8192, &tmA, bar, f + 64, row);
+                                tma_load_2d_pair(dB, &tmB, bar, c, row);
+                                if (half > 64)
+                                    tma_load_2d_pair(dB + 8192, &tmB, bar, c + 64, row);
+                            } else {
+                                const int k = kb * TC_BK;
+                                auto weights = [&](uint32_t dst, int x, int y) {
+                                    tma_load_3d_pair(dst, &tmA, bar, x, p.swap ? z : y, p.swap ? y : z);
+                                };
+                                if (A_MN) {
+                                    weights(dA, f, k);
+                                    weights(dA + 8192, f + 64, k);
+                                } else {
+                                    weights(dA, k, f);
+                                }
+                                // the tile's rows in boxes of 128, 64, 32 and 16
+                                if (half == 128) {
+                                    tma_load_2d_pair(dB, &tmB, bar, k, c);
+                                } else {
+                                    int b = 0;
+                                    if (half & 64) {
+                                        tma_load_2d_pair(dB, &tmB64, bar, k, c);
+                                        b = 64;
+                                    }
+                                    if (half & 32) {
+                                        tma_load_2d_pair(dB + b * 128, &tmB32, bar, k, c + b);
+                                        b += 32;
+                                    }
+                                    if (half & 16)
+                                        tma_load_2d_pair(dB + b * 128, &tmB16, bar, k, c + b);
+                                }
+                            }
                         }
-                        tc_commit_pair(empty_bar(stage), 0x3);
-                        if (last)
-                            tc_commit_pair(tfull_bar(local & 1), 0x3);
+                        __syncwarp();
+                        if (tail) {
+                            ragged |= 1u << stage;
+                            ragged_parity ^= 1u << stage;
+                        }
                     }
-                    __syncwarp();
-                    local += last;
                     if (++stage == stages) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
             }
-            // Wait (bounded) until every MMA issued so far has completed, so
-            // TMEM and the input stages are no longer in use.
-            if (elect_one())
-                tc_commit_self<2>(drain_bar);
-            __syncwarp();
-            const long long t0 = clock64();
-            while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
+            if (!ok && lane == 0) {
+                // Wait (bounded) for the loads already issued before shared
+                // memory goes away: the leader's barriers cover both CTAs.
+                auto drain = [&](uint32_t bar, uint32_t parity) {
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait(bar, parity) && clock64() - t0 < p.wait_budget) {
+                    }
+                };
+                for (int s = 0; s < stages; ++s) {
+                    const int uses = steps / stages + (s < steps % stages);
+                    if (leader && uses > 0)
+                        drain(full_bar(s), (uses - 1) & 1);
+                    if (WGRAD && ((ragged >> s) & 1))
+                        drain(tail_bar(s), ((ragged_parity >> s) & 1) ^ 1);
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMA issuer
+            if (leader) {
+                int stage = 0;
+                uint32_t phase = 0;
+                int local = 0;
+                bool ok = true;
+                for (int t = unit; ok && t < num_work; t += num_units) {
+                    const GroupedWork w = grouped_work<MODE>(t, table, p);
+                    if (w.k_blocks == 0)
+                        continue;
+                    const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
+                    uint32_t d_tmem = 0;
+                    int of_segment = 0;
+                    for (int kb = 0; kb < w.k_blocks; ++kb) {
+                        const bool first = of_segment == 0;
+                        const bool last = kb == w.k_blocks - 1 ||
+                                          of_segment == (WGRAD ? GT_SEGMENT : p.segment) - 1;
+                        of_segment = last ? 0 : of_segment + 1;
+                        if (first) {
+                            ok = warp_wait<true>(tempty_bar(local & 1), ((local >> 1) & 1) ^ 1, watch);
+                            d_tmem = tmem_base + static_cast<uint32_t>((local & 1) * GT_N);
+                        }
+                        ok = ok && warp_wait<WGRAD>(full_bar(stage), phase, watch);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const uint32_t a0 = sbase + stage * stage_bytes, b0 = a0 + GT_A_BYTES;
+                        // 16-deep instructions; gradient: as many as there are rows
+                        const int deep = WGRAD ? min(4, (w.rows - kb * TC_BK + 15) / 16) : 4;
+                        if (elect_one()) {
+    #pragma unroll
+                            for (int k = 0; k < TC_BK / TC_UMMA_K; ++k) {
+                                if (WGRAD && k >= deep)
+                                    break;
+                                const uint64_t adesc = A_MN ? smem_desc_sw128(a0 + k * 2048, 8192, 1024)
+                                                            : smem_desc_sw128(a0 + k * 32, 16, 1024);
+                                const uint64_t bdesc = WGRAD ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                             : smem_desc_sw128(b0 + k * 32, 16, 1024);
+                                tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, !first || k != 0);
+                            }
+                            tc_commit_pair(empty_bar(stage), 0x3);
+                            if (last)
+                                tc_commit_pair(tfull_bar(local & 1), 0x3);
+                        }
+                        __syncwarp();
+                        local += last;
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+                // Wait (bounded) until every MMA issued so far has completed, so
+                // TMEM and the input stages are no longer in use.
+                if (elect_one())
+                    tc_commit_self<2>(drain_bar);
+                __syncwarp();
+                const long long t0 = clock64();
+                while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
+                }
+            }
+        } else if (WGRAD && warp == 2) {
+            // ------------------------- rows of other groups in a group's last K step
+            int stage = 0;
+            uint32_t parity = 0;  // a bit for each step's barrier
+            for (int t = unit; t < num_work; t += num_units) {
+                const GroupedWork w = grouped_work<MODE>(t, table, p);
+                if (w.k_blocks == 0)
+                    continue;
+                const int last = w.k_blocks - 1;
+                const int s = (stage + last) % stages;
+                stage = (s + 1) % stages;
+                if (!is_ragged(w, last))
+                    continue;
+                // (the steps before, of this tile and of ones that end evenly, are not waited for)
+                if (!warp_wait_behind(tail_bar(s), (parity >> s) & 1, watch, progress))
+                    break;
+                parity ^= 1u << s;
+                // a row of 64 values is 128 contiguous bytes (its swizzle stays within)
+                const int from = w.rows - last * TC_BK, to = (from + 15) / 16 * 16;
+                const int boxes = 2 + w.n / 128;
+                for (int b = 0; b < boxes; ++b) {  // (A's two boxes, then B's)
+                    const uint32_t box = sbase + s * stage_bytes + b * 8192;
+                    for (int i = from * 8 + static_cast<int>(lane); i < to * 8; i += 32)
+                        st_shared_v4(box + i * 16, 0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(mapa_shared(full_bar(s), 0));
             }
         }
-    } else if (warp < 2 + L::EPI_WARPS) {
+    } else {
+        set_max_regs_inc<L::REGS_EPI>();
         // ------------------------------------------------ epilogue
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const uint32_t leader_tempty0 = mapa_shared(tempty_bar(0), 0);
         const uint32_t leader_tempty1 = mapa_shared(tempty_bar(1), 0);
         OutT* const out = static_cast<OutT*>(p.C);
-        const uint32_t staging = sbase + L::OFF_STAGING + (warp - 2) * L::STAGING;
-        // waits for the next accumulator; gives it back
+        const uint32_t staging = sbase + L::OFF_STAGING + (warp - L::EPI_WARP0) * L::STAGING;
+        // waits for the next accumulator, of a segment; gives it back
         int local = 0;
-        auto take = [&](int steps) {
+        auto take = [&] {
             int ok = 1;
             if (lane == 0)
-                ok = tc_wait(tfull_bar(local & 1), (local >> 1) & 1, patient(watch, steps)) ? 1 : 0;
+                ok = tc_wait(tfull_bar(local & 1), (local >> 1) & 1, watch) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             tc_fence_after();
             return ok != 0;
@@ -454,46 +500,93 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
         if constexpr (!WGRAD) {
             if (p.zero_rest)
                 zero_rest_rows(table, p.by, out, p.ldc, p.N,
-                               static_cast<int64_t>(blockIdx.x) * (32 * L::EPI_WARPS) + (threadIdx.x - 64),
+                               static_cast<int64_t>(blockIdx.x) * (32 * L::EPI_WARPS) + threadIdx.x -
+                                   32 * L::EPI_WARP0,
                                static_cast<int64_t>(gridDim.x) * (32 * L::EPI_WARPS));
-            const int half = (warp - 2) / 4;  // these warps' strips: every other one
+            const int half = (warp - L::EPI_WARP0) / 4;  // these warps' strips: every other one
+            constexpr int STRIPS = GT_N / 64;
+            const bool turned = sizeof(OutT) == 2 && p.unit && p.beta == 0.0f;
+            bool ok = true;
             for (int t = unit; t < num_work; t += num_units) {
                 const GroupedWork w = grouped_work<MODE>(t, table, p);
-                if (!take(w.k_blocks))
-                    break;
                 const int f = w.f0 + static_cast<int>(rank) * TC_BM + q * 32;
-                const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * GT_N);
-                OutT* c = out + (w.c0 + 32 * half) * p.ldc + f;
-#pragma unroll 1
-                for (int s = 32 * half; s < w.count; s += 64, c += 64 * p.ldc) {
+                auto store = [&](const auto& v, int s) {
+                    OutT* c = out + (w.c0 + s) * p.ldc + f;
                     if constexpr (sizeof(OutT) == 2) {
-                        if (p.unit && p.beta == 0.0f) {
-                            put_turned(from + s, staging, c, p.ldc, w.count - s, p.N - f, p.alpha);
-                            continue;
+                        if (turned) {
+                            put_turned(v, staging, c, p.ldc, w.count - s, p.N - f, p.alpha);
+                            return;
                         }
                     }
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(from + s, v);
+                    if (f + static_cast<int>(lane) < p.N)
+                        put_column(c + lane, p.ldc, w.count - s, v, p.alpha, p.beta);
+                };
+                // 16 of the lanes (turned: see put_turned()) or columns of a strip
+                auto load = [&](uint32_t from, int h, uint32_t (&v)[16]) {
+                    if (turned)
+                        tmem_ld_16x256b_x4(from + (static_cast<uint32_t>(h) << 16), v);
+                    else
+                        tmem_ld_32x32b_x16(from + h, v);
                     tmem_wait_ld(v);
-                    if (f + static_cast<int>(lane) < p.N) {
+                };
+                if (p.segments == 1) {
+                    ok = take();
+                    if (!ok)
+                        break;
+                    const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * GT_N);
+#pragma unroll 1
+                    for (int s = 32 * half; s < w.count; s += 64) {
                         float x[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            x[j] = __uint_as_float(v[j]);
-                        put_column(c + lane, p.ldc, w.count - s, x, p.alpha, p.beta);
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t v[16];
+                            load(from + s, h, v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                x[h + i] = __uint_as_float(v[i]);
+                        }
+                        store(x, s);
                     }
+                    give();
+                    continue;
                 }
-                give();
+                float sum[STRIPS][32] = {};
+#pragma unroll 1
+                for (int segment = 0; segment < p.segments; ++segment) {
+                    ok = take();
+                    if (!ok)
+                        break;
+                    const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * GT_N + 32 * half);
+#pragma unroll
+                    for (int j = 0; j < STRIPS; ++j)
+                        if (32 * half + 64 * j < w.count) {
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t v[16];
+                                load(from + 64 * j, h, v);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    sum[j][h + i] += __uint_as_float(v[i]);
+                            }
+                        }
+                    give();  // (before the stores: the next tile's segments take both accumulators)
+                }
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int j = 0; j < STRIPS; ++j)
+                    if (32 * half + 64 * j < w.count)
+                        store(sum[j], 32 * half + 64 * j);
             }
         } else {
             constexpr int HALF = GT_N / 2, CHUNKS = HALF / 32;
-            const int half = (warp - 2) / 4;  // of the tile's columns
+            const int half = (warp - L::EPI_WARP0) / 4;  // of the tile's columns
             bool ok = true;
             for (int t = unit; t < num_work; t += num_units) {
                 const GroupedWork w = grouped_work<MODE>(t, table, p);
                 float sum[CHUNKS][32] = {};
                 for (int kb = 0; kb < w.k_blocks; kb += GT_SEGMENT) {
-                    ok = take(GT_SEGMENT);
+                    ok = take();
                     if (!ok)
                         break;
                     const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * GT_N + half * HALF);
@@ -557,36 +650,6 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
             if (lane == 0)
                 bulk_wait_group_read<0>();
             __syncwarp();
-        }
-    } else if constexpr (WGRAD) {
-        // ------------------------- rows of other groups in a group's last K step
-        int stage = 0;
-        uint32_t parity = 0;  // a bit for each step's barrier
-        for (int t = unit; t < num_work; t += num_units) {
-            const GroupedWork w = grouped_work<MODE>(t, table, p);
-            if (w.k_blocks == 0)
-                continue;
-            const int last = w.k_blocks - 1;
-            const int s = (stage + last) % stages;
-            stage = (s + 1) % stages;
-            if (!is_ragged(w, last))
-                continue;
-            // (the steps before, of this tile and of ones that end evenly, are not waited for)
-            if (!warp_wait_behind(tail_bar(s), (parity >> s) & 1, watch, progress))
-                break;
-            parity ^= 1u << s;
-            // a row of 64 values is 128 contiguous bytes (its swizzle stays within)
-            const int from = w.rows - last * TC_BK, to = (from + 15) / 16 * 16;
-            const int boxes = 2 + w.n / 128;
-            for (int b = 0; b < boxes; ++b) {  // (A's two boxes, then B's)
-                const uint32_t box = sbase + s * stage_bytes + b * 8192;
-                for (int i = from * 8 + static_cast<int>(lane); i < to * 8; i += 32)
-                    st_shared_v4(box + i * 16, 0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_cluster(mapa_shared(full_bar(s), 0));
         }
     }
 

@@ -205,19 +205,15 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                  : "memory");
 }
 
-// 32 lanes x 32 columns of the accumulator at taddr as 32 rows (the columns) of
-// 32 16-bit values (the lanes) to y, through 2 KiB of shared memory; rows of y are on
-// 16-byte boundaries.  n rows and m values of each exist.  A whole warp calls it.
+// 32 lanes x 32 columns, as tmem_ld_16x256b_x4 gives lanes 0 to 15 and 16 to 31, as 32
+// rows (the columns) of 32 16-bit values (the lanes) to y, through 2 KiB of shared
+// memory; rows of y are on 16-byte boundaries.  n rows and m values of each exist.  A
+// whole warp calls it.
 template <typename OutT>
-__device__ __forceinline__ void put_turned(uint32_t taddr, uint32_t staging, OutT* y, int64_t ldy, int n, int m,
-                                           float alpha)
+__device__ __forceinline__ void put_turned(const float (&v)[32], uint32_t staging, OutT* y, int64_t ldy,
+                                           int n, int m, float alpha)
 {
     const uint32_t lane = lane_id();
-    uint32_t r[2][16];
-    tmem_ld_16x256b_x4(taddr, r[0]);
-    tmem_ld_16x256b_x4(taddr + (16u << 16), r[1]);
-    tmem_wait_ld(r[0]);
-    tmem_wait_ld(r[1]);
     OutT* tag = nullptr;
     // 16-byte unit u of row t at u ^ (t / 2) % 4: no bank conflicts either way
     const uint32_t at = staging + lane * 64, turn = (lane >> 1) & 3;
@@ -226,8 +222,8 @@ __device__ __forceinline__ void put_turned(uint32_t taddr, uint32_t staging, Out
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int k = 4 * i + 2 * (u & 1);
-            w[i] = pack2(alpha * __uint_as_float(r[u >> 1][k]), alpha * __uint_as_float(r[u >> 1][k + 1]), tag);
+            const int k = 16 * (u >> 1) + 4 * i + 2 * (u & 1);
+            w[i] = pack2(alpha * v[k], alpha * v[k + 1], tag);
         }
         stmatrix_x4_trans(at + ((u ^ turn) << 4), w[0], w[1], w[2], w[3]);
     }
