@@ -221,3 +221,38 @@ def test_fp16_waits_that_run_out_are_reported(name, few):
         assert tg.gemm_device_status(stream) == tg.binding.ERR_TIMEOUT
         tg.gemm_debug_config(0, -1)
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
+# the product on CTA pairs
+LONG_SUMS = [(2100, 2056, 8192, 3), (2100, 2056, 1088, 3)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,N,K,G", LONG_SUMS)
+def test_adapted_products_of_long_sums_keep_fp32(rows, N, K, G, dtype):
+    """The product and its input's gradient, FP32 results of values of one sign.  Rank values
+    are summed as the shared product is, with up to eight accumulators (8 more roundings),
+    a scale and parts (2), and enter the last accumulator by six instructions (12)."""
+    x, w = _positive(1, dtype, rows, K), _positive(2, dtype, N, K)
+    a, b = _positive(3, dtype, G, 16, K), _positive(4, dtype, G, N, 16)
+    adapter = (torch.arange(rows) * 7 % (G + 1) - 1).to(torch.int32).cuda()
+    limit = _segments(K) + 22 * 2.0 ** -24
+
+    def want(x, w, f, e):
+        y = x.double() @ w.double()
+        for g in range(G):
+            mine = adapter == g
+            y[mine] += (x[mine].double() @ f[g].double()) @ e[g].double()
+        return y
+
+    y = tg.matmul_lora(x, w, a, b, adapter)
+    ref_y = want(x, w.t(), a.transpose(1, 2), b.transpose(1, 2))
+    assert ((y.double() - ref_y).abs() <= limit * ref_y).all()
+    half = tg.matmul_lora(x, w, a, b, adapter, out_dtype=dtype)
+    if dtype == torch.float16:
+        assert torch.equal(half, y.half())
+    # the same product as an input's gradient: from w, and a and b exchanged, turned
+    none = torch.zeros(rows, N, dtype=dtype, device="cuda")
+    dx = tg.matmul_lora_backward(x, none, w.t().contiguous(), b.transpose(1, 2).contiguous(),
+                                 a.transpose(1, 2).contiguous(), adapter)[0]
+    assert ((dx.double() - ref_y).abs() <= limit * ref_y).all()

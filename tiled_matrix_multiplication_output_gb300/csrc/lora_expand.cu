@@ -26,10 +26,19 @@ namespace {
 
 constexpr int LE_STAGES = 3;
 constexpr int LE_KSUB = 2;
-constexpr int LE_THREADS = TC_THREADS + 32;  // a last warp splits factors
+// Warps 0: copies, 1: MMA, 2: FP16 factors in two, 4 to 11: epilogue, to which the first
+// ones leave registers of the 168 that a thread is launched with.
+constexpr int LE_EPI_WARP0 = 4;
+constexpr int LE_EPI_WARPS = 8;
+constexpr int LE_THREADS = 32 * (LE_EPI_WARP0 + LE_EPI_WARPS);
+constexpr int LE_REGS_FEW = 88, LE_REGS_EPI = 208;
+static_assert(LE_EPI_WARP0 * LE_REGS_FEW + LE_EPI_WARPS * LE_REGS_EPI <= LE_THREADS / 32 * 168,
+              "of the block's registers");
+constexpr int LE_SEGMENT = 16;  // K steps that one accumulator adds up, at most (see grouped_tc.cuh)
 
 struct ExpandParams {
     int M, N, k_blocks, rank;
+    int segments, segment;  // parts of K, and their K steps
     int tiles_m, tiles_n;
     int whole, items;     // tiles of 256 columns first, the others in halves
     bool adapters;        // there are any: plans and rank values are made
@@ -53,7 +62,7 @@ struct ExpandLayout {
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = STEPS * SUB;
     static constexpr int OFF_STAGING = OFF_B + STEPS * SUB;
-    static constexpr int OFF_BAR = OFF_STAGING + 4 * 4096;
+    static constexpr int OFF_BAR = OFF_STAGING + LE_EPI_WARPS * 2048;
     static constexpr int NUM_BARS = 2 * STEPS + LE_STAGES + 5;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
     static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
@@ -168,7 +177,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
             mbar_init(landed_bar(at), 1);
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), 8);  // every epilogue warp of the pair
+            mbar_init(tempty_bar(a), 2 * LE_EPI_WARPS);  // of the pair
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -188,311 +197,374 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer
-        const uint32_t sA = sbase + L::OFF_A, sB = sbase + L::OFF_B;
-        int stage = 0, sub = 0;
-        uint32_t phase = 0;
-        int issued[L::STEPS];
-#pragma unroll
-        for (int s = 0; s < L::STEPS; ++s)
-            issued[s] = 0;
-        uint32_t to_split = 0, parity = 0;  // steps that last landed on their own barrier; how often
-        int steps = 0;
-        bool ok = true, waited = false;
-        auto next_stage = [&] {
-            sub = 0;
-            if (++stage == LE_STAGES) {
-                stage = 0;
-                phase ^= 1;
-            }
-        };
-        auto count = [&](int at) {
-#pragma unroll
-            for (int s = 0; s < L::STEPS; ++s)  // (registers: no indexing)
-                issued[s] += s == at;
-        };
-        // One K step: load(A's place, B's place, barrier); split: its factor is to be split.
-        auto step = [&](bool skip, bool split, uint32_t bytes, auto load) {
-            if (sub == 0 && !warp_wait(empty_bar(stage), phase ^ 1, watch))
-                return false;
-            ++steps;
-            if (p.split && lane == 0)
-                *progress = steps;
-            if (!skip) {
-                const int at = stage * LE_KSUB + sub;
-                if (elect_one()) {
-                    if (split) {
-                        mbar_arrive_expect_tx(landed_bar(at), bytes / 2);
-                    } else if (leader) {
-                        if (p.split)
-                            mbar_arrive(full_bar(stage, sub));
-                        mbar_arrive_expect_tx(full_bar(stage, sub), bytes);
-                    }
-                    load(sA + at * L::SUB, sB + at * L::SUB,
-                         split ? mapa_shared(landed_bar(at), rank) : mapa_shared(full_bar(stage, sub), 0));
-                }
-                __syncwarp();
-                count(at);
-                to_split = split ? to_split | 1u << at : to_split & ~(1u << at);
-                parity ^= static_cast<uint32_t>(split) << at;
-            }
-            if (++sub == LE_KSUB)
-                next_stage();
-            return true;
-        };
-        for (int t = unit; ok && t < p.items; t += num_units) {
-            const Item w = item(t, p);
-            const int row = w.mb * 256 + static_cast<int>(rank) * TC_BM;
-            const int col = w.col + static_cast<int>(rank) * w.n / 2;
-            const uint32_t bytes = 2 * (L::SUB + w.n * 64);
-            PairAdapters list;
-            if (waited)
-                list.begin(p, w.mb);
-            // W's or a factor's outputs: boxes of 64 (x) or 128 and 64 (y)
-            auto outputs = [&](auto box, auto box64, uint32_t dB) {
-                if (ACROSS) {
-                    box(dB, col);
-                    if (w.n > 128)
-                        box(dB + 8192, col + 64);
-                } else if (w.n > 128) {
-                    box(dB, col);
-                } else {
-                    box64(dB, col);
-                }
-            };
-            for (int kb = 0; ok && kb < p.k_blocks; ++kb) {
-                const int k = kb * TC_BK;
-                ok = step(kb == p.fault_skip_kblock, false, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
-                    tma_load_2d_pair(dA, &tmX, bar, k, row);
-                    auto load = [&](const CUtensorMap* map) {
-                        return [=](uint32_t to, int c) {
-                            tma_load_2d_pair(to, map, bar, ACROSS ? c : k, ACROSS ? k : c);
-                        };
-                    };
-                    outputs(load(&tmW), load(&tmW64), dB);
-                });
-            }
-            if (!ok)
-                break;
-            if (p.adapters) {
-                if (!waited) {
-                    grid_dep_wait();
-                    grid_dep_launch_dependents();  // the rank values are there for others, too
-                    list.begin(p, w.mb);
-                }
-                waited = true;
-                uint32_t off[8];
-                for (int g = list.next(off); ok && g >= 0; g = list.next(off)) {
-                    const int z = p.one ? 0 : g;
-                    for (int c = 0; ok && c < p.lay.chunks; ++c) {
-                        const int j = c * p.lay.chunk;
-                        ok = step(false, p.split, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
-                            tma_load_2d_pair(dA, &tmT, bar, c * 64, row);
-                            auto load = [&](const CUtensorMap* map) {
-                                return [=](uint32_t to, int o) {
-                                    tma_load_3d_pair(to, map, bar, ACROSS ? o : j, ACROSS ? j : o, z);
-                                };
-                            };
-                            outputs(load(&tmE), load(&tmE64), dB);
-                        });
-                    }
-                }
-            }
-            if (ok && sub != 0) {
-                if (leader && elect_one()) {  // the stage's unused step
-                    mbar_arrive(full_bar(stage, 1));
-                    if (p.split)
-                        mbar_arrive(full_bar(stage, 1));
-                }
-                __syncwarp();
-                count(stage * LE_KSUB + 1);
-                to_split &= ~(1u << (stage * LE_KSUB + 1));
-                next_stage();
-            }
-        }
-        if (!ok && lane == 0) {
-            // wait (bounded) for the loads already issued (those of both CTAs, but each CTA
-            // its own factors to be split) before shared memory goes away
-            for (int s = 0; s < L::STEPS; ++s) {
-                const bool own = (to_split >> s) & 1;
-                const uint32_t bar = own ? landed_bar(s) : bar0 + 8u * s;
-                const uint32_t phase_of = own ? ((parity >> s) & 1) ^ 1 : (issued[s] - 1) & 1;
-                const long long t0 = clock64();
-                while ((own || (leader && issued[s] > 0)) && !mbar_try_wait(bar, phase_of) &&
-                       clock64() - t0 < p.wait_budget) {
-                }
-            }
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer
-        if (leader) {
+    if (warp < LE_EPI_WARP0) {
+        set_max_regs_dec<LE_REGS_FEW>();
+        if (warp == 0) {
+            // ------------------------------------------------ TMA producer
             const uint32_t sA = sbase + L::OFF_A, sB = sbase + L::OFF_B;
-            int stage = 0, sub = 0, local = 0;
+            int stage = 0, sub = 0;
             uint32_t phase = 0;
+            int issued[L::STEPS];
+    #pragma unroll
+            for (int s = 0; s < L::STEPS; ++s)
+                issued[s] = 0;
+            uint32_t to_split = 0, parity = 0;  // steps that last landed on their own barrier; how often
+            int steps = 0;
             bool ok = true, waited = false;
             auto next_stage = [&] {
-                if (elect_one())
-                    tc_commit_pair(empty_bar(stage), 0x3);
-                __syncwarp();
                 sub = 0;
                 if (++stage == LE_STAGES) {
                     stage = 0;
                     phase ^= 1;
                 }
             };
-            auto step = [&](auto multiply) {
-                if (!(p.split ? warp_wait<true>(full_bar(stage, sub), phase, watch)
-                              : warp_wait(full_bar(stage, sub), phase, watch)))
+            auto count = [&](int at) {
+    #pragma unroll
+                for (int s = 0; s < L::STEPS; ++s)  // (registers: no indexing)
+                    issued[s] += s == at;
+            };
+            // One K step: load(A's place, B's place, barrier); split: its factor is to be split.
+            auto step = [&](bool skip, bool split, uint32_t bytes, auto load) {
+                if (sub == 0 && !warp_wait(empty_bar(stage), phase ^ 1, watch))
                     return false;
-                tc_fence_after();
-                const int at = stage * LE_KSUB + sub;
-                if (elect_one())
-                    multiply(sA + at * L::SUB, sB + at * L::SUB);
-                __syncwarp();
+                ++steps;
+                if (p.split && lane == 0)
+                    *progress = steps;
+                if (!skip) {
+                    const int at = stage * LE_KSUB + sub;
+                    if (elect_one()) {
+                        if (split) {
+                            mbar_arrive_expect_tx(landed_bar(at), bytes / 2);
+                        } else if (leader) {
+                            if (p.split)
+                                mbar_arrive(full_bar(stage, sub));
+                            mbar_arrive_expect_tx(full_bar(stage, sub), bytes);
+                        }
+                        load(sA + at * L::SUB, sB + at * L::SUB,
+                             split ? mapa_shared(landed_bar(at), rank) : mapa_shared(full_bar(stage, sub), 0));
+                    }
+                    __syncwarp();
+                    count(at);
+                    to_split = split ? to_split | 1u << at : to_split & ~(1u << at);
+                    parity ^= static_cast<uint32_t>(split) << at;
+                }
                 if (++sub == LE_KSUB)
                     next_stage();
                 return true;
             };
-            for (int t = unit; ok && t < p.items; t += num_units, ++local) {
+            for (int t = unit; ok && t < p.items; t += num_units) {
                 const Item w = item(t, p);
-                const int acc = local & 1;
-                ok = warp_wait<true>(tempty_bar(acc), ((local >> 1) & 1) ^ 1, watch);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-                const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
+                const int row = w.mb * 256 + static_cast<int>(rank) * TC_BM;
+                const int col = w.col + static_cast<int>(rank) * w.n / 2;
+                const uint32_t bytes = 2 * (L::SUB + w.n * 64);
                 PairAdapters list;
                 if (waited)
                     list.begin(p, w.mb);
-                for (int kb = 0; ok && kb < p.k_blocks; ++kb)
-                    ok = step([&](uint32_t a0, uint32_t b0) {
-#pragma unroll
-                        for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
-                            tc_mma_f16<2>(d_tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
-                                          ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                                 : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                          idesc, kb != 0 || k != 0);
+                // W's or a factor's outputs: boxes of 64 (x) or 128 and 64 (y)
+                auto outputs = [&](auto box, auto box64, uint32_t dB) {
+                    if (ACROSS) {
+                        box(dB, col);
+                        if (w.n > 128)
+                            box(dB + 8192, col + 64);
+                    } else if (w.n > 128) {
+                        box(dB, col);
+                    } else {
+                        box64(dB, col);
+                    }
+                };
+                for (int kb = 0; ok && kb < p.k_blocks; ++kb) {
+                    const int k = kb * TC_BK;
+                    ok = step(kb == p.fault_skip_kblock, false, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                        tma_load_2d_pair(dA, &tmX, bar, k, row);
+                        auto load = [&](const CUtensorMap* map) {
+                            return [=](uint32_t to, int c) {
+                                tma_load_2d_pair(to, map, bar, ACROSS ? c : k, ACROSS ? k : c);
+                            };
+                        };
+                        outputs(load(&tmW), load(&tmW64), dB);
                     });
+                }
                 if (!ok)
                     break;
                 if (p.adapters) {
                     if (!waited) {
                         grid_dep_wait();
+                        grid_dep_launch_dependents();  // the rank values are there for others, too
                         list.begin(p, w.mb);
                     }
                     waited = true;
                     uint32_t off[8];
-                    for (int g = list.next(off); ok && g >= 0; g = list.next(off))
-                        for (int c = 0; ok && c < p.lay.chunks; ++c)
-                            ok = step([&](uint32_t a0, uint32_t b0) {
-                                const uint32_t idesc_e = p.idesc_e | static_cast<uint32_t>(w.n >> 3) << 17;
-                                each_product(p.lay, p.lay.deep(c, p.rank), p.split, [&](int part, int pair, int k) {
-                                    const int b = pair * p.lay.chunk / 16 + k;
-                                    tc_mma_f16_lanes(
-                                        d_tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
-                                        ACROSS ? smem_desc_sw128(b0 + b * 2048, 8192, 1024)
-                                               : smem_desc_sw128(b0 + b * 32, 16, 1024),
-                                        idesc_e, 1, off);
-                                });
+                    for (int g = list.next(off); ok && g >= 0; g = list.next(off)) {
+                        const int z = p.one ? 0 : g;
+                        for (int c = 0; ok && c < p.lay.chunks; ++c) {
+                            const int j = c * p.lay.chunk;
+                            ok = step(false, p.split, bytes, [&](uint32_t dA, uint32_t dB, uint32_t bar) {
+                                tma_load_2d_pair(dA, &tmT, bar, c * 64, row);
+                                auto load = [&](const CUtensorMap* map) {
+                                    return [=](uint32_t to, int o) {
+                                        tma_load_3d_pair(to, map, bar, ACROSS ? o : j, ACROSS ? j : o, z);
+                                    };
+                                };
+                                outputs(load(&tmE), load(&tmE64), dB);
                             });
+                        }
+                    }
                 }
-                if (!ok)
-                    break;
-                if (sub != 0)
+                if (ok && sub != 0) {
+                    if (leader && elect_one()) {  // the stage's unused step
+                        mbar_arrive(full_bar(stage, 1));
+                        if (p.split)
+                            mbar_arrive(full_bar(stage, 1));
+                    }
+                    __syncwarp();
+                    count(stage * LE_KSUB + 1);
+                    to_split &= ~(1u << (stage * LE_KSUB + 1));
                     next_stage();
-                if (elect_one())
-                    tc_commit_pair(tfull_bar(acc), 0x3);
-                __syncwarp();
+                }
             }
-            // Wait (bounded) until every MMA issued so far has completed, so
-            // TMEM and the input stages are no longer in use.
-            if (elect_one())
-                tc_commit_self<2>(drain_bar);
-            __syncwarp();
-            const long long t0 = clock64();
-            while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
+            if (!ok && lane == 0) {
+                // wait (bounded) for the loads already issued (those of both CTAs, but each CTA
+                // its own factors to be split) before shared memory goes away
+                for (int s = 0; s < L::STEPS; ++s) {
+                    const bool own = (to_split >> s) & 1;
+                    const uint32_t bar = own ? landed_bar(s) : bar0 + 8u * s;
+                    const uint32_t phase_of = own ? ((parity >> s) & 1) ^ 1 : (issued[s] - 1) & 1;
+                    const long long t0 = clock64();
+                    while ((own || (leader && issued[s] > 0)) && !mbar_try_wait(bar, phase_of) &&
+                           clock64() - t0 < p.wait_budget) {
+                    }
+                }
             }
-        }
-    } else if (warp == LE_THREADS / 32 - 1) {
-        // ------------------------------------------------ factors in two
-        if (p.split && p.adapters) {
-            grid_dep_wait();
-            int at = 0;           // the step's place
-            uint32_t parity = 0;  // a bit for each
-            bool ok = true;
-            for (int t = unit; ok && t < p.items; t += num_units) {
-                const Item w = item(t, p);
-                PairAdapters list;
-                list.begin(p, w.mb);
-                at = (at + p.k_blocks) % L::STEPS;
-                uint32_t off[8];
-                for (int g = list.next(off); ok && g >= 0; g = list.next(off))
-                    for (int c = 0; ok && c < p.lay.chunks; ++c) {
-                        // (the steps of the shared product are not waited for)
-                        ok = warp_wait_behind(landed_bar(at), (parity >> at) & 1, watch, progress);
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMA issuer
+            if (leader) {
+                const uint32_t sA = sbase + L::OFF_A, sB = sbase + L::OFF_B;
+                int stage = 0, sub = 0, local = 0;
+                uint32_t phase = 0;
+                bool ok = true, waited = false;
+                auto next_stage = [&] {
+                    if (elect_one())
+                        tc_commit_pair(empty_bar(stage), 0x3);
+                    __syncwarp();
+                    sub = 0;
+                    if (++stage == LE_STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                };
+                auto step = [&](auto multiply) {
+                    if (!(p.split ? warp_wait<true>(full_bar(stage, sub), phase, watch)
+                                  : warp_wait(full_bar(stage, sub), phase, watch)))
+                        return false;
+                    tc_fence_after();
+                    const int at = stage * LE_KSUB + sub;
+                    if (elect_one())
+                        multiply(sA + at * L::SUB, sB + at * L::SUB);
+                    __syncwarp();
+                    if (++sub == LE_KSUB)
+                        next_stage();
+                    return true;
+                };
+                for (int t = unit; ok && t < p.items; t += num_units) {
+                    const Item w = item(t, p);
+                    uint32_t d_tmem = 0;
+                    const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
+                    PairAdapters list;
+                    if (waited)
+                        list.begin(p, w.mb);
+                    for (int kb = 0; ok && kb < p.k_blocks;) {
+                        ok = warp_wait<true>(tempty_bar(local & 1), ((local >> 1) & 1) ^ 1, watch);
                         if (!ok)
                             break;
-                        parity ^= 1u << at;
-                        const uint32_t tile = sbase + L::OFF_B + at * L::SUB;
-                        if (ACROSS)
-                            split_across(tile, w.n / 128);
-                        else
-                            split_rows(tile, w.n / 2, 128);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_cluster(mapa_shared(bar0 + 8u * at, 0));
-                        at = (at + 1) % L::STEPS;
+                        tc_fence_after();
+                        d_tmem = tmem_base + static_cast<uint32_t>((local & 1) * 256);
+                        const int begin = kb, end = min(kb + p.segment, p.k_blocks);
+                        for (; ok && kb < end; ++kb)
+                            ok = step([&](uint32_t a0, uint32_t b0) {
+#pragma unroll
+                                for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
+                                    tc_mma_f16<2>(d_tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
+                                                  ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                         : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                                  idesc, kb != begin || k != 0);
+                            });
+                        if (ok && kb < p.k_blocks) {
+                            if (elect_one())
+                                tc_commit_pair(tfull_bar(local & 1), 0x3);
+                            __syncwarp();
+                            ++local;
+                        }
                     }
-                at = (at + at % LE_KSUB) % L::STEPS;  // (behind a stage's unused step)
+                    if (!ok)
+                        break;
+                    if (p.adapters) {  // (of the last segment)
+                        if (!waited) {
+                            grid_dep_wait();
+                            list.begin(p, w.mb);
+                        }
+                        waited = true;
+                        uint32_t off[8];
+                        for (int g = list.next(off); ok && g >= 0; g = list.next(off))
+                            for (int c = 0; ok && c < p.lay.chunks; ++c)
+                                ok = step([&](uint32_t a0, uint32_t b0) {
+                                    const uint32_t idesc_e = p.idesc_e | static_cast<uint32_t>(w.n >> 3) << 17;
+                                    each_product(p.lay, p.lay.deep(c, p.rank), p.split, [&](int part, int pair, int k) {
+                                        const int b = pair * p.lay.chunk / 16 + k;
+                                        tc_mma_f16_lanes(
+                                            d_tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
+                                            ACROSS ? smem_desc_sw128(b0 + b * 2048, 8192, 1024)
+                                                   : smem_desc_sw128(b0 + b * 32, 16, 1024),
+                                            idesc_e, 1, off);
+                                    });
+                                });
+                    }
+                    if (!ok)
+                        break;
+                    if (sub != 0)
+                        next_stage();
+                    if (elect_one())
+                        tc_commit_pair(tfull_bar(local & 1), 0x3);
+                    __syncwarp();
+                    ++local;
+                }
+                // Wait (bounded) until every MMA issued so far has completed, so
+                // TMEM and the input stages are no longer in use.
+                if (elect_one())
+                    tc_commit_self<2>(drain_bar);
+                __syncwarp();
+                const long long t0 = clock64();
+                while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < p.wait_budget) {
+                }
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------ factors in two
+            if (p.split && p.adapters) {
+                grid_dep_wait();
+                int at = 0;           // the step's place
+                uint32_t parity = 0;  // a bit for each
+                bool ok = true;
+                for (int t = unit; ok && t < p.items; t += num_units) {
+                    const Item w = item(t, p);
+                    PairAdapters list;
+                    list.begin(p, w.mb);
+                    at = (at + p.k_blocks) % L::STEPS;
+                    uint32_t off[8];
+                    for (int g = list.next(off); ok && g >= 0; g = list.next(off))
+                        for (int c = 0; ok && c < p.lay.chunks; ++c) {
+                            // (the steps of the shared product are not waited for)
+                            ok = warp_wait_behind(landed_bar(at), (parity >> at) & 1, watch, progress);
+                            if (!ok)
+                                break;
+                            parity ^= 1u << at;
+                            const uint32_t tile = sbase + L::OFF_B + at * L::SUB;
+                            if (ACROSS)
+                                split_across(tile, w.n / 128);
+                            else
+                                split_rows(tile, w.n / 2, 128);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive_cluster(mapa_shared(bar0 + 8u * at, 0));
+                            at = (at + 1) % L::STEPS;
+                        }
+                    at = (at + at % LE_KSUB) % L::STEPS;  // (behind a stage's unused step)
+                }
             }
         }
     } else {
         // ------------------------------------------------ epilogue
+        set_max_regs_inc<LE_REGS_EPI>();
         if (p.adapters)
             grid_dep_wait();  // (the first tile ends no sooner: its wait begins here)
         const int q = warp & 3;  // TMEM lane quarter this warp may access
-        const uint32_t staging = sbase + L::OFF_STAGING + q * 4096;
+        const int half = (warp - LE_EPI_WARP0) / 4;  // of the tile's columns
+        const uint32_t staging = sbase + L::OFF_STAGING + (warp - LE_EPI_WARP0) * 2048;
         const uint32_t leader_tempty0 = mapa_shared(tempty_bar(0), 0);
         const uint32_t leader_tempty1 = mapa_shared(tempty_bar(1), 0);
         OutT* const out = static_cast<OutT*>(p.C);
+        const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        constexpr int STRIPS = 128 / 32;
         int local = 0;
-        for (int t = unit; t < p.items; t += num_units, ++local) {
-            const Item w = item(t, p);
-            const int acc = local & 1;
+        // waits for the next accumulator, of a segment; gives it back
+        auto take = [&] {
             int ok = 1;
             if (lane == 0)
-                ok = tc_wait(tfull_bar(acc), (local >> 1) & 1, patient(watch, p.k_blocks)) ? 1 : 0;
+                ok = tc_wait(tfull_bar(local & 1), (local >> 1) & 1, watch) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok)
-                break;
             tc_fence_after();
-            const int row = w.mb * 256 + static_cast<int>(rank) * TC_BM + q * 32;
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                   static_cast<uint32_t>(acc * 256);
-            const int cols = min(w.n, p.N - w.col);
-            OutT* c = out + row * p.ldc + w.col;
-            if (row < p.M)
-#pragma unroll 1
-                for (int s = 0; s < cols; s += 32) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(t_row + s, v);
-                    tmem_wait_ld(v);
-                    if (p.unit) {
-#pragma unroll
-                        for (int part = 0; part < static_cast<int>(sizeof(OutT)) / 2; ++part)
-                            put_rows(v, part, staging, c + s + 16 * part, p.ldc, p.M - row, cols - s - 16 * part,
-                                     1.0f);
-                    } else {
-                        put_strip(v, staging, c + s, p.ldc, min(32, p.M - row), cols - s, 1.0f, 0.0f);
-                    }
-                }
+            return ok != 0;
+        };
+        auto give = [&] {
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_cluster(acc ? leader_tempty1 : leader_tempty0);
+                mbar_arrive_cluster(local & 1 ? leader_tempty1 : leader_tempty0);
+            ++local;
+        };
+        bool ok = true;
+        for (int t = unit; t < p.items; t += num_units) {
+            const Item w = item(t, p);
+            const int row = w.mb * 256 + static_cast<int>(rank) * TC_BM + q * 32;
+            const int first = half * w.n / 2;  // of these warps' columns, and behind the last
+            const int cols = row < p.M ? min(first + w.n / 2, p.N - w.col) : 0;
+            OutT* c = out + row * p.ldc + w.col;
+            auto store = [&](const uint32_t (&v)[32], int s) {
+                if (p.unit) {
+#pragma unroll
+                    for (int part = 0; part < static_cast<int>(sizeof(OutT)) / 2; ++part)
+                        put_rows(v, part, staging, c + s + 16 * part, p.ldc, p.M - row, cols - s - 16 * part, 1.0f);
+                } else {
+                    put_strip(v, staging, c + s, p.ldc, min(32, p.M - row), cols - s, 1.0f, 0.0f);
+                }
+            };
+            if (p.segments == 1) {
+                ok = take();
+                if (!ok)
+                    break;
+                const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * 256);
+#pragma unroll 1
+                for (int s = first; s < cols; s += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(from + s, v);
+                    tmem_wait_ld(v);
+                    store(v, s);
+                }
+                give();
+                continue;
+            }
+            float sum[STRIPS][32] = {};
+#pragma unroll 1
+            for (int segment = 0; segment < p.segments; ++segment) {
+                ok = take();
+                if (!ok)
+                    break;
+                const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * 256 + first);
+#pragma unroll
+                for (int j = 0; j < STRIPS; ++j)
+                    if (first + 32 * j < cols) {
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t v[16];
+                            tmem_ld_32x32b_x16(from + 32 * j + h, v);
+                            tmem_wait_ld(v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                sum[j][h + i] += __uint_as_float(v[i]);
+                        }
+                    }
+                give();  // (before the stores: the next tile's segments take both accumulators)
+            }
+            if (!ok)
+                break;
+#pragma unroll
+            for (int j = 0; j < STRIPS; ++j)
+                if (first + 32 * j < cols) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __float_as_uint(sum[j][i]);
+                    store(v, first + 32 * j);
+                }
         }
     }
 
@@ -555,6 +627,9 @@ cudaError_t lora_expand_tc_launch(const LoraLaunch& l, cudaStream_t stream)
     p.M = l.rows;
     p.N = l.N;
     p.k_blocks = (l.K + TC_BK - 1) / TC_BK;
+    p.segments = (p.k_blocks + LE_SEGMENT - 1) / LE_SEGMENT;
+    p.segment = (p.k_blocks + p.segments - 1) / p.segments;
+    p.segments = (p.k_blocks + p.segment - 1) / p.segment;
     p.rank = l.rank;
     p.tiles_m = (l.rows + 255) / 256;
     p.tiles_n = (l.N + 255) / 256;
