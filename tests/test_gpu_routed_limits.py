@@ -223,8 +223,10 @@ def test_fp16_waits_that_run_out_are_reported(name, few):
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
 
 
-# the product on CTA pairs
-LONG_SUMS = [(2100, 2056, 8192, 3), (2100, 2056, 1088, 3)]
+# the product on CTA pairs; few tiles, in clusters of one CTA and of several; the kernel that
+# makes the rank values too
+LONG_SUMS = [(2100, 2056, 8192, 3), (2100, 2056, 1088, 3), (1300, 1300, 8192, 3), (300, 1000, 8192, 3),
+             (300, 1000, 8200, 90), (1300, 1300, 2048, 1)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])

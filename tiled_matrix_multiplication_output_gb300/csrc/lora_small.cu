@@ -43,10 +43,14 @@ constexpr int LM_PITCH = 132;    // of the sums in shared memory: rows 16 bytes 
 constexpr int LM_HELD = 16384;   // a tile's rank values in parts, of one chunk
 constexpr int LM_FACTORS = 16384;  // factors of F beside a K step of W, at most
 constexpr int LM_OWN_STEPS = 32;
+static_assert(LM_OWN_STEPS <= 2 * LT_SEGMENT, "two accumulators");
+constexpr int LM_OWN_SECOND = 384;  // OWN: tensor memory of a second accumulator
 constexpr int LM_THIN = LT_ROWS * (32 + 4) * 4;  // a CTA's share of their sums
 
 struct SmallParams {
     int M, N, k_blocks, rank;
+    int segment;             // K steps that one accumulator adds up
+    int tmem_cols;
     int tiles_n;
     bool one;
     int adapters;
@@ -82,6 +86,7 @@ struct SmallParams {
 struct SmallSmem {
     uint64_t full[LM_MAX_STAGES], empty[LM_MAX_STAGES], planned, held, done, thin, thin_all;
     uint64_t landed[LM_MAX_STAGES];  // of steps whose factors are to be split
+    uint64_t segment, taken;         // a segment's sums are there, are added
     uint32_t tmem;
     int abort_flag;
     int progress;  // steps copied
@@ -167,6 +172,8 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         mbar_init(smem_u32(&s.planned), 128);
         mbar_init(smem_u32(&s.held), OWN ? 4 : 1);
         mbar_init(smem_u32(&s.done), 1);
+        mbar_init(smem_u32(&s.segment), 1);
+        mbar_init(smem_u32(&s.taken), 4);
         mbar_init(smem_u32(&s.thin), 1);
         mbar_init(smem_u32(&s.thin_all), 4 * SPLITS);
         s.abort_flag = 0;
@@ -178,7 +185,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         tma_prefetch_desc(&tmE);
     }
     if (warp == 1) {
-        tmem_alloc<1>(smem_u32(&s.tmem), OWN ? 512 : 128);
+        tmem_alloc<1>(smem_u32(&s.tmem), p.tmem_cols);
         tmem_relinquish<1>();
     }
     tc_fence_before();
@@ -188,6 +195,11 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         cluster_arrive();  // (waited for before another CTA's barrier is touched)
     const uint32_t tmem = s.tmem;
     const uint32_t a_bytes = p.box_rows * 128;
+    // The contraction goes in segments.  Their sums are added in tensor memory, behind
+    // the accumulator; the kernel that makes the rank values too, whose warps are not free for
+    // that, has two at most, in accumulators of their own.
+    const int segments = (kb1 - kb0 + p.segment - 1) / p.segment;
+    const uint32_t second = tmem + (OWN ? LM_OWN_SECOND : 128);
     const uint32_t held = ring + p.ring;  // the tile's rank values
     float* const thin = reinterpret_cast<float*>(base + p.ring + LM_HELD);  // shares of their sums
     volatile int* const progress = &s.progress;
@@ -367,17 +379,30 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             ok = warp_wait(smem_u32(&s.planned), 0, watch);
             some = min(p.together, s.plan.count);
         }
-        for (int kb = kb0; ok && kb < kb1; ++kb)
-            ok = step([&](uint32_t a0, uint32_t b0) {
+        uint32_t acc = tmem;
+        for (int n = 0; ok && n < segments; ++n) {
+            if (OWN && n > 0)
+                acc = second;
+            if (!OWN && n > 0) {
+                if (elect_one())
+                    tc_commit(smem_u32(&s.segment));
+                __syncwarp();
+                ok = warp_wait(smem_u32(&s.taken), (n - 1) & 1, watch);
+                tc_fence_after();
+            }
+            const int begin = kb0 + n * p.segment, end = min(begin + p.segment, kb1);
+            for (int kb = begin; ok && kb < end; ++kb)
+                ok = step([&](uint32_t a0, uint32_t b0) {
 #pragma unroll
-                for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
-                    tc_mma_f16<1>(tmem, smem_desc_sw128(a0 + k * 32, 16, 1024),
-                                  ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                         : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                  p.idesc, kb != kb0 || k != 0);
-                if constexpr (OWN)
-                    rank_values(0, some, kb, a0, b0 + 16384);
-            });
+                    for (int k = 0; k < TC_BK / TC_UMMA_K; ++k)
+                        tc_mma_f16<1>(acc, smem_desc_sw128(a0 + k * 32, 16, 1024),
+                                      ACROSS ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                             : smem_desc_sw128(b0 + k * 32, 16, 1024),
+                                      p.idesc, kb != begin || k != 0);
+                    if constexpr (OWN)
+                        rank_values(0, some, kb, a0, b0 + 16384);
+                });
+        }
         if constexpr (OWN) {
             for (int a = p.together; ok && a < s.plan.count; a += p.extra)
                 for (int kb = kb0; ok && kb < kb1; ++kb)
@@ -403,7 +428,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                             each_product(p.lay, deep, p.split, [&](int part, int pair, int k) {
                                 const int b = pair * p.lay.chunk / 16 + k;
                                 tc_mma_f16_lanes(
-                                    tmem, smem_desc_sw128(held + part * p.lay.chunk * 2 + k * 32, 16, 1024),
+                                    acc, smem_desc_sw128(held + part * p.lay.chunk * 2 + k * 32, 16, 1024),
                                     smem_desc_rows(b0 + b * 32, p.width), p.idesc_e, 1, off);
                             });
                         }
@@ -418,7 +443,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                             each_product(p.lay, p.lay.deep(c, p.rank), p.split, [&](int part, int pair, int k) {
                                 const int b = pair * p.lay.chunk / 16 + k;
                                 tc_mma_f16_lanes(
-                                    tmem, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
+                                    acc, smem_desc_sw128(a0 + part * p.lay.chunk * 2 + k * 32, 16, 1024),
                                     ACROSS ? smem_desc_sw128(b0 + b * 2048, 8192, 1024)
                                            : smem_desc_sw128(b0 + b * 32, 16, 1024),
                                     p.idesc_e, 1, off);
@@ -574,9 +599,20 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     float* sums = reinterpret_cast<float*>(base);
     if (warp >= 4) {
         const int q = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+        int ok = 1;
+        for (int n = 0; !OWN && n + 1 < segments; ++n) {
+            if (!warp_wait(smem_u32(&s.segment), n & 1, watch))
+                break;
+            tc_fence_after();
+            add_to_sums(tmem + lanes, 1, second + lanes, 128, n == 0, true);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&s.taken));
+        }
         if (p.adapters > 0)
             grid_dep_wait();  // (so that no wait spans the kernel before)
-        int ok = 1;
         if (lane == 0)
             ok = tc_wait(smem_u32(&s.done), 0, patient(watch, p.k_blocks)) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -586,8 +622,16 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
 #pragma unroll 1
             for (int j = 0; j < 128; j += 32) {
                 uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + j, v);
+                tmem_ld_32x32b_x32(tmem + lanes + j, v);
                 tmem_wait_ld(v);
+                if (segments > 1) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(second + lanes + j, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(v[i]));
+                }
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
                     st_shared_v4(to + (j + i) * 4, v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -606,7 +650,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         __syncthreads();
     tc_fence_after();
     if (warp == 1)
-        tmem_dealloc<1>(tmem, OWN ? 512 : 128);
+        tmem_dealloc<1>(tmem, p.tmem_cols);
     // (a lane asks each CTA: a loop would wait for one answer after another)
     int gave_up = s.abort_flag;
     if (SPLITS > 1 && static_cast<int>(lane) < SPLITS)
@@ -790,6 +834,9 @@ cudaError_t launch_small(const LoraLaunch& l, bool own, cudaStream_t stream)
                                      : small_splits<false, false>(tiles, p.k_blocks, l.num_sms, &splits);
     if (err != cudaSuccess)
         return err;
+    const int per = (p.k_blocks + splits - 1) / splits, segments = (per + LT_SEGMENT - 1) / LT_SEGMENT;
+    p.segment = (per + segments - 1) / segments;
+    p.tmem_cols = own ? 512 : segments > 1 ? 256 : 128;
     return l.across ? launch<true, false>(m, p, tiles, splits, stream)
            : own    ? launch<false, true>(m, p, tiles, splits, stream)
                     : launch<false, false>(m, p, tiles, splits, stream);

@@ -146,6 +146,55 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
     return v;
 }
 
+// 32 lanes x 16 columns of 32 bits to tensor memory, and the wait for such stores.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// K steps that one accumulator adds up, at most: 64 instructions (see grouped_tc.cuh).
+// Where a CTA has more, the accumulators are added to FP32 sums, with rounding, and begin
+// anew; the sums lie in tensor memory.
+constexpr int LT_SEGMENT = 16;
+
+// Adds `chains` accumulators of cols columns (a multiple of 16), one behind the other from
+// acc, to the sums of this warp's lanes: of those lanes that are mine, whose first addition
+// it may be.
+__device__ __forceinline__ void add_to_sums(uint32_t acc, int chains, uint32_t sums, int cols, bool first,
+                                            bool mine)
+{
+#pragma unroll 1
+    for (int j = 0; j < cols; j += 16) {
+        uint32_t v[16], o[16];
+        tmem_ld_32x32b_x16(acc + j, v);
+        tmem_wait_ld(v);
+#pragma unroll 1
+        for (int c = 1; c < chains; ++c) {
+            tmem_ld_32x32b_x16(acc + c * cols + j, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(o[i]));
+        }
+        tmem_ld_32x32b_x16(sums + j, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (!first)
+                v[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(v[i]));
+            v[i] = mine ? v[i] : o[i];
+        }
+        tmem_st_32x32b_x16(sums + j, v);
+    }
+    tmem_wait_st();
+}
+
 // How the rank values are laid out.
 struct LoraParts {
     int parts, chunk, chunks;
