@@ -258,3 +258,24 @@ def test_adapted_products_of_long_sums_keep_fp32(rows, N, K, G, dtype):
     dx = tg.matmul_lora_backward(x, none, w.t().contiguous(), b.transpose(1, 2).contiguous(),
                                  a.transpose(1, 2).contiguous(), adapter)[0]
     assert ((dx.double() - ref_y).abs() <= limit * ref_y).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,G,rank", [(10_000, 1, 256), (10_000, 3, 128), (10_000, 2, 200), (300, 3, 256),
+                                         (10_000, 40, 32), (1000, 100, 48), (10_000, 130, 16)])
+def test_rank_values_of_long_sums_keep_fp32(rows, G, rank, dtype):
+    """Of every number of accumulators and of rounds over a tile's adapters: 32768 values of
+    one sign.  Rank values add up as _segments() has it, with eight accumulators' roundings, a
+    scale and parts (10); in the product up to six instructions for 16 of them, in one
+    accumulator, each dropping two half units at most."""
+    K = 32_768
+    x = _positive(1, dtype, rows, K)
+    a, b = _positive(2, dtype, G, rank, K), _positive(3, dtype, G, 24, rank)
+    w = torch.zeros(24, K, dtype=dtype, device="cuda")
+    adapter = (torch.arange(rows) * 7 % G).to(torch.int32).cuda()
+    y = tg.matmul_lora(x, w, a, b, adapter)
+    limit = _segments(K) + (10 + 2 * 6 * ((rank + 15) // 16)) * 2.0 ** -24
+    for g in range(G):
+        mine = adapter == g
+        want = (x[mine].double() @ a[g].double().t()) @ b[g].double().t()
+        assert ((y[mine].double() - want).abs() <= limit * want).all()

@@ -47,7 +47,7 @@ struct ShrinkParams {
     int stages, stage_bytes, a_offset, b_bytes[2];
     int together;                    // adapters whose factors share a stage
     int box_rows;                    // rows of X that a copy brings
-    int chains;                      // accumulators that K steps take in turn
+    int chains;                      // accumulators that K steps take in turn; behind them, sums
     uint32_t tmem_cols;
     int* status;
     long long wait_budget;
@@ -56,6 +56,7 @@ struct ShrinkParams {
 
 struct ShrinkSmem {
     uint64_t full[LS_MAX_STAGES], empty[LS_MAX_STAGES], done;
+    uint64_t segment, taken;  // accumulators are to be added to the sums, are added
     uint32_t tmem;
     int abort_flag;
     PlanScratch scratch;
@@ -109,6 +110,8 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
             mbar_init(smem_u32(&s.empty[i]), 1);
         }
         mbar_init(smem_u32(&s.done), 1);
+        mbar_init(smem_u32(&s.segment), 1);
+        mbar_init(smem_u32(&s.taken), 4);
         s.abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(tmX);
@@ -140,6 +143,11 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     const int mine = s.plan.count > deal ? (s.plan.count - deal + p.deal - 1) / p.deal : 0;
     const int rounds = (mine + p.together - 1) / p.together;
     const int steps = rounds * (kb1 - kb0);
+    // A round's K steps go in segments, after each of which but the last the accumulators of
+    // its adapters' rows are added to the rows' sums.
+    const int segment = LT_SEGMENT * p.chains;
+    const int segments = (kb1 - kb0 + segment - 1) / segment;
+    const uint32_t sums_at = tmem + p.chains * p.cols;
     // the i-th adapter of this CTA, by its place in the plan
     auto nth = [&](int i) { return deal + i * p.deal; };
 
@@ -189,18 +197,28 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     } else if (warp == 1) {
         if (steps > 0) {
             int stage = 0;
-            uint32_t phase = 0;
+            uint32_t phase = 0, added = 0;
             bool ok = true;
             for (int i0 = 0; ok && i0 < mine; i0 += p.together) {
                 const int some = min(p.together, mine - i0);
-                for (int kb = kb0; kb < kb1; ++kb) {
+                int n = 0;  // K step of the segment
+                for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                    if (n == segment) {
+                        if (elect_one())
+                            tc_commit(smem_u32(&s.segment));
+                        __syncwarp();
+                        ok = warp_wait(smem_u32(&s.taken), added++ & 1, watch);
+                        if (!ok)
+                            break;
+                        n = 0;
+                    }
                     ok = warp_wait(smem_u32(&s.full[stage]), phase, watch);
                     if (!ok)
                         break;
                     tc_fence_after();
                     const uint32_t base = smem_u32(ring) + stage * p.stage_bytes;
                     const uint32_t a0 = base + p.a_offset;
-                    const uint32_t d = tmem + (kb - kb0) % p.chains * p.cols;
+                    const uint32_t d = tmem + n % p.chains * p.cols;
                     for (int i = 0; i < some; ++i) {
                         const uint32_t b0 = base + i * b_bytes;
                         const uint4 rows = *reinterpret_cast<const uint4*>(s.plan.rows[nth(i0 + i)]);
@@ -211,7 +229,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
                                 tc_mma_f16_lanes(d, smem_desc_sw128(a0 + k * 32, 16, 1024),
                                                  side.across ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
                                                              : smem_desc_sw128(b0 + k * 32, 16, 1024),
-                                                 side.idesc, kb - kb0 >= p.chains || k != 0, off);
+                                                 side.idesc, n >= p.chains || k != 0, off);
                             if (i == some - 1)
                                 tc_commit(smem_u32(&s.empty[stage]));
                         }
@@ -237,6 +255,23 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
     float* sums = reinterpret_cast<float*>(ring);
     if (warp >= 4) {
         const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int place = s.place[row];
+        const int round = place >= 0 && place % p.deal == deal ? place / p.deal / p.together : -1;
+        bool all = true;
+        uint32_t added = 0;
+        for (int r = 0; all && r < rounds; ++r)
+            for (int n = 1; all && n < segments; ++n) {
+                all = warp_wait(smem_u32(&s.segment), added++ & 1, watch);
+                if (!all)
+                    break;
+                tc_fence_after();
+                add_to_sums(tmem + lanes, p.chains, sums_at + lanes, p.cols, n == 1, r == round);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&s.taken));
+            }
         if (steps > 0) {
             int ok = 1;
             if (lane == 0)
@@ -244,15 +279,18 @@ __global__ void __launch_bounds__(LS_THREADS, 1)
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (ok) {
                 tc_fence_after();
-                const int chains = min(p.chains, kb1 - kb0);
+                const int chains = min(p.chains, kb1 - kb0 - (segments - 1) * segment);
 #pragma unroll 1
                 for (int j = 0; j < p.cols; j += 16) {
-                    const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j;
+                    const uint32_t from = tmem + lanes + j;
                     uint32_t v[16];
                     tmem_ld_32x32b_x16(from, v);
                     tmem_wait_ld(v);
+                    // (the sums lie behind the last accumulator)
+                    const int others = chains + (segments > 1);
 #pragma unroll 1
-                    for (int c = 1; c < chains; ++c) {
+                    for (int k = 1; k < others; ++k) {
+                        const int c = k < chains ? k : p.chains;
                         uint32_t o[16];
                         tmem_ld_32x32b_x16(from + c * p.cols, o);
                         tmem_wait_ld(o);
@@ -463,13 +501,6 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
     p.tiles = (l.rows + LT_ROWS - 1) / LT_ROWS;
     p.box_rows = std::min(LT_ROWS, (l.rows + 7) / 8 * 8);
     const uint32_t box_rows = static_cast<uint32_t>(p.box_rows);
-    p.tmem_cols = 32;
-    // The tensor core drops what does not fit when it adds a step to an accumulator,
-    // half a unit in the last place on average: 2000 deep sums were 3e-6 short.  The
-    // steps take up to eight accumulators in turn, added with rounding at the end.
-    p.chains = std::max(1, std::min(8, 256 / p.cols));
-    while (p.tmem_cols < static_cast<uint32_t>(p.chains * p.cols))
-        p.tmem_cols *= 2;
     p.status = l.status;
     p.wait_budget = l.wait_budget;
     p.fault_skip_kblock = l.fault_skip_kblock;
@@ -508,6 +539,15 @@ cudaError_t lora_shrink_tc_launch(const LoraLaunch& first, const LoraLaunch* sec
         p.stage_bytes = r.stage_bytes;
     }
     const bool shared = !second && r.shares;
+    // The tensor core drops what does not fit when it adds a step to an accumulator,
+    // half a unit in the last place on average: 2000 deep sums were 3e-6 short.  The
+    // steps take up to eight accumulators in turn, added with rounding every
+    // LT_SEGMENT steps of each and at the end.  The product's kernel has 256 columns of a
+    // shared SM's tensor memory.
+    p.chains = std::max(1, std::min(8, (shared ? 256 : 512) / p.cols - 1));
+    p.tmem_cols = 32;
+    while (p.tmem_cols < static_cast<uint32_t>((p.chains + 1) * p.cols))
+        p.tmem_cols *= 2;
     p.stages = std::min(LS_MAX_STAGES,
                         ((shared ? LS_RING_SHARED : LS_RING) - p.a_offset - 16384) / p.stage_bytes + 1);
     const int most_adapters = std::min(std::min(l.adapters, LT_ROWS), l.rows);
