@@ -534,9 +534,10 @@ int gemm_grouped(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t
  * output's gradient D and the input X.
  *
  * D is rows x N (pitch ldd), X rows x K (pitch ldx), C[g] N x K (pitch ldc)
- * and stride_c elements behind C[g - 1] (matrices must not overlap).  A group
- * without rows gives beta * C[g] (zeros for beta == 0).  Workspace, alignment
- * and errors as gemm_grouped.
+ * and stride_c elements behind C[g - 1] (matrices must not overlap: one lies
+ * behind the other, or they are interleaved row by row).  A group without rows
+ * gives beta * C[g] (zeros for beta == 0).  Workspace, alignment and errors as
+ * gemm_grouped.
  */
 size_t gemm_grouped_wgrad_workspace_size(const void* D, int64_t ldd, const void* X, int64_t ldx,
                                          int64_t rows, int64_t N, int64_t K,

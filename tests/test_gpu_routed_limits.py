@@ -6,7 +6,7 @@ import torch
 
 import tiled_matrix_multiplication_output_gb300 as tg
 from tests import routed_reference as ref
-from tests.test_gpu_grouped import _dev, _ints
+from tests.test_gpu_grouped import _dev, _ints, _offsets
 from tests.test_gpu_lora import Case
 
 pytestmark = pytest.mark.gpu
@@ -279,3 +279,22 @@ def test_rank_values_of_long_sums_keep_fp32(rows, G, rank, dtype):
         mine = adapter == g
         want = (x[mine].double() @ a[g].double().t()) @ b[g].double().t()
         assert ((y[mine].double() - want).abs() <= limit * want).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("K,pad", [(200, 0), (200, 8), (77, 3)])
+def test_wgrad_results_interleaved_row_by_row(K, pad, dtype, out):
+    """As matmul_grouped takes its weights: (out, groups, in) in memory."""
+    off = _offsets([70, 0, 33, 200])
+    dy, x = _ints(1, dtype, off[-1], 136), _ints(2, dtype, off[-1], K)
+    want = ref.wgrad(dy, x, off)[0]
+    buf = torch.full((136, 4, K + pad), 7.0, dtype=ref.DT[out], device="cuda")
+    c = buf[:, :, :K].transpose(0, 1)
+    tg.matmul_grouped_wgrad(dy, x, _dev(off), out=c)
+    assert torch.equal(c.double(), want.to(ref.DT[out]).double()) and (buf[:, :, K:] == 7).all()
+    tg.matmul_grouped_wgrad(dy, x, _dev(off), out=c, alpha=0.0, beta=1.0)
+    assert torch.equal(c.double(), want.to(ref.DT[out]).double()) and (buf[:, :, K:] == 7).all()
+    with pytest.raises(tg.GemmError):  # each row begins within the one before
+        tg.matmul_grouped_wgrad(dy, x, _dev(off), out=torch.zeros(9999999, dtype=ref.DT[out], device="cuda")
+                                .as_strided((4, 136, K), (K - 1, 4 * K, 1)))

@@ -176,3 +176,10 @@ def test_row_stacks_and_vectors_are_checked_before_the_library():
             binding._vector_of(bad, "o", 5, i32, 0)
     with pytest.raises(TypeError):
         binding._vector_of(T((5,), (1,), torch.int64), "o", 5, i32, 0)
+
+
+def test_interleaved_results_that_overlap_are_rejected():
+    """Results may be interleaved row by row (the pitch holds a row of each); rows that
+    reach into the next are not accepted."""
+    for stride, ldc in ((7, 24), (8, 23), (9, 25), (31, 8), (0, 24), (-8, 24), (2 ** 62, 2 ** 62)):
+        assert _wgrad(stride=stride, ldc=ldc, N=4, K=8, ldx=8) == INV, (stride, ldc)

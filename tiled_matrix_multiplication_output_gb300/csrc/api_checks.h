@@ -14,11 +14,13 @@ namespace tmmo {
 inline bool valid_size(int64_t n) { return n >= 0 && n <= GEMM_MAX_DIM; }
 inline bool valid_dtype(int t) { return t == GEMM_F32 || t == GEMM_F16 || t == GEMM_BF16; }
 
-// Whether matrices of rows x cols (pitch ld >= cols), `stride` elements after
-// each other, do not overlap.
-inline bool apart(int64_t stride, int64_t rows, int64_t ld, int64_t cols)
+// Whether `count` matrices of rows x cols (pitch ld >= cols), `stride` elements after
+// each other, do not overlap: one behind the other, or interleaved row by row.
+inline bool apart(int64_t count, int64_t stride, int64_t rows, int64_t ld, int64_t cols)
 {
-    return stride >= 0 && static_cast<__int128>(stride) >= static_cast<__int128>(rows - 1) * ld + cols;
+    const __int128 step = stride;
+    return count <= 1 || step >= static_cast<__int128>(rows - 1) * ld + cols ||
+           (step >= cols && ld >= (count - 1) * step + cols);
 }
 
 // Whether `need` bytes of workspace are not there.

@@ -136,7 +136,7 @@ extern "C" int gemm_grouped_wgrad(const void* D, int64_t ldd, const void* X, int
     const int rc = check_grouping(rows, groups, N, K, in_dtype, out_dtype);
     if (rc != GEMM_OK || groups == 0 || N == 0 || K == 0)
         return rc;
-    if (!offsets || !C || ldc < K || (groups > 1 && !apart(stride_c, N, ldc, K)))
+    if (!offsets || !C || ldc < K || !apart(groups, stride_c, N, ldc, K))
         return GEMM_ERR_INVALID_VALUE;
     if (rows > 0 && (!D || !X || ldd < N || ldx < K))
         return GEMM_ERR_INVALID_VALUE;

@@ -237,9 +237,9 @@ extern "C" int gemm_lora_backward(const void* D, int64_t ldd, const void* X, int
         return GEMM_ERR_INVALID_VALUE;
     if (dx && (lddx < K || (N > 0 && (!W || ldw < K))))
         return GEMM_ERR_INVALID_VALUE;
-    if (da && (ldda < K || (lora->adapters > 1 && !apart(stride_da, lora->rank, ldda, K))))
+    if (da && (ldda < K || !apart(lora->adapters, stride_da, lora->rank, ldda, K)))
         return GEMM_ERR_INVALID_VALUE;
-    if (db && (lddb < lora->rank || (lora->adapters > 1 && !apart(stride_db, N, lddb, lora->rank))))
+    if (db && (lddb < lora->rank || !apart(lora->adapters, stride_db, N, lddb, lora->rank)))
         return GEMM_ERR_INVALID_VALUE;
     Operands o(X, ldx, D, ldd, W, ldw, *lora, rows, N, K, in_dtype);
     const int parts = parts_for(in_dtype, false, true);

@@ -29,7 +29,7 @@ cudaError_t grouped_wgrad_tc_launch(const GroupedWgradLaunch& l, cudaStream_t st
     const int64_t size = type_bytes(l.out_dtype);
     p.unit = row_unit(l.C, l.ldc * size, groups > 1 ? l.stride_c * size : 0);
     const int64_t stride = groups > 1 ? l.stride_c : l.N * l.ldc;
-    p.tma_out = l.beta == 0.0f && p.unit != 0 &&
+    p.tma_out = l.beta == 0.0f && p.unit != 0 && stride >= l.ldc &&  // (not interleaved row by row)
                 encode_map(&m.c, l.out_dtype, l.C, 3, {l.K, l.N, groups}, {l.ldc, stride},
                            {static_cast<uint32_t>(64 / size), 32, 1});
     const int64_t most = groups * p.tiles_f * p.tiles_c;
