@@ -298,3 +298,26 @@ def test_wgrad_results_interleaved_row_by_row(K, pad, dtype, out):
     with pytest.raises(tg.GemmError):  # each row begins within the one before
         tg.matmul_grouped_wgrad(dy, x, _dev(off), out=torch.zeros(9999999, dtype=ref.DT[out], device="cuda")
                                 .as_strided((4, 136, K), (K - 1, 4 * K, 1)))
+
+
+@pytest.mark.parametrize("rows,N,K,G,rank", [(20, 136, 264, 3, 12), (150, 264, 200, 6, 16), (150, 264, 200, 6, 40),
+                                             (1300, 2056, 264, 6, 24)])
+def test_fp16_rows_see_nothing_of_other_adapters(rows, N, K, G, rank):
+    """Factors, rows and gradients that are not finite stay with their adapters and rows,
+    though factors are split in two and rank values go in parts."""
+    c = Case(rows, N, K, G, rank, "f16", seed=5)
+    y, (dx, da, db) = c.forward(), c.backward()
+    c.a[1], c.b[2] = float("nan"), float("inf")
+    c.x[7], c.dy[9] = float("inf"), float("nan")
+    y2, (dx2, da2, db2) = c.forward(), c.backward()
+    of = c.adapter
+    clean = (of != 1) & (of != 2)
+    keep = clean.clone()
+    keep[7] = False
+    assert torch.equal(y2[keep], y[keep]) and not torch.isfinite(y2[of == 1]).any()
+    keep = clean.clone()
+    keep[9] = False
+    assert torch.equal(dx2[keep], dx[keep])
+    ok = [g for g in range(G) if g not in (1, 2, int(of[7]), int(of[9]))]
+    assert torch.equal(da2[ok], da[ok]) and torch.equal(db2[ok], db[ok])
+    assert ok or G == 3

@@ -27,7 +27,6 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 struct View {
     const float* p;
     int64_t outer, inner;
-    __device__ float at(int i, int k) const { return p[i * outer + k * inner]; }
 };
 
 struct alignas(16) SimtStep {  // read as float4
