@@ -321,3 +321,34 @@ def test_fp16_rows_see_nothing_of_other_adapters(rows, N, K, G, rank):
     ok = [g for g in range(G) if g not in (1, 2, int(of[7]), int(of[9]))]
     assert torch.equal(da2[ok], da[ok]) and torch.equal(db2[ok], db[ok])
     assert ok or G == 3
+
+
+@pytest.mark.parametrize("dtype,rows,N,K,G,rank", [("f16", 60, 264, 320, 5, 16), ("f16", 60, 264, 320, 60, 40),
+                                                   ("f16", 2100, 2056, 320, 5, 24), ("bf16", 2100, 2056, 2600, 5, 136),
+                                                   ("bf16", 1300, 1300, 4200, 3, 200)])
+def test_split_factors_and_segments_repeat(dtype, rows, N, K, G, rank):
+    """The same bits call by call, on another stream beside the first, and from a graph whose
+    adapters change between replays."""
+    c = Case(rows, N, K, G, rank, dtype, "runs")
+    first = c.forward(), *c.backward()
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(first, (c.forward(), *c.backward())))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    here, there = [], []
+    for _ in range(3):
+        there.append((c.forward(stream=s), *c.backward(stream=s)))
+        here.append((c.forward(), *c.backward()))
+    torch.cuda.synchronize()
+    for got in here + there:
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = c.forward(), *c.backward()
+    adapters = c.adapter.clone()
+    for of in (adapters.flip(0), torch.full_like(adapters, -1), adapters):
+        c.adapter.copy_(of)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, (c.forward(), *c.backward())))
+    assert all(torch.equal(a, b) for a, b in zip(first, held))
