@@ -474,8 +474,6 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
     } else {
         // ------------------------------------------------ epilogue
         set_max_regs_inc<LE_REGS_EPI>();
-        if (p.adapters)
-            grid_dep_wait();  // (the first tile ends no sooner: its wait begins here)
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const int half = (warp - LE_EPI_WARP0) / 4;  // of the tile's columns
         const uint32_t staging = sbase + L::OFF_STAGING + (warp - LE_EPI_WARP0) * 2048;
@@ -485,8 +483,13 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
         const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         constexpr int STRIPS = 128 / 32;
         int local = 0;
-        // waits for the next accumulator, of a segment; gives it back
-        auto take = [&] {
+        // waits for the next accumulator, of a segment (whether of a tile's last one); gives it back
+        bool waited = !p.adapters;
+        auto take = [&](bool last) {
+            if (last && !waited) {
+                grid_dep_wait();  // (the first tile ends no sooner: its wait begins here)
+                waited = true;
+            }
             int ok = 1;
             if (lane == 0)
                 ok = tc_wait(tfull_bar(local & 1), (local >> 1) & 1, watch) ? 1 : 0;
@@ -518,7 +521,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
                 }
             };
             if (p.segments == 1) {
-                ok = take();
+                ok = take(true);
                 if (!ok)
                     break;
                 const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * 256);
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
             float sum[STRIPS][32] = {};
 #pragma unroll 1
             for (int segment = 0; segment < p.segments; ++segment) {
-                ok = take();
+                ok = take(segment == p.segments - 1);
                 if (!ok)
                     break;
                 const uint32_t from = t_lane + static_cast<uint32_t>((local & 1) * 256 + first);
