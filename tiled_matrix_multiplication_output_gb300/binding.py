@@ -981,8 +981,8 @@ def matmul_grouped_wgrad(dy, x, offsets, out_dtype=None, out=None, alpha=1.0, be
     w (stored out x in).
 
     dy: rows x out, x: rows x in, as matmul_grouped's x; offsets: int32 CUDA
-    tensor of groups + 1 values.  `out` may supply C (groups, out, in), with
-    beta = 1 to add to it.  out_dtype defaults to FP32, or to out's type.
+    tensor of groups + 1 values.  `out` may supply C (groups, out, in; matrices
+    one behind the other or interleaved row by row), with beta = 1 to add to it.  out_dtype defaults to FP32, or to out's type.
     Groups without rows give zeros (beta * C).  Returns C without
     synchronizing."""
     code, dtype, device = _begin(x, "x")

@@ -25,10 +25,11 @@
 // registers.
 //
 // Both are bound by the operands' way from L2 (a K step of a full tile takes 630
-// cycles, its MMAs 512) or, with few rows, by reading the weights from HBM.  BF16:
-// 16384 rows of 16 groups by 4096 x 4096 302 us (1.82 PFLOP/s), 256 rows of 64 groups
-// by 4096 x 2048 150 us (6.6 TB/s), the gradient of 16384 rows of 8 groups, 4096 x
-// 2048, FP32, 176 us (1.56 PFLOP/s).
+// cycles, its MMAs 512) or, with few rows, by reading the weights from HBM.  BF16, on the
+// device, GPU not power-capped: 16384 rows of 16 groups by 4096 x 4096 319 us (1.72
+// PFLOP/s; one accumulator for all of K 316), 256 rows of 64 groups by 4096 x 2048 153
+// us (6.5 TB/s), the gradient of 16384 rows of 8 groups, 4096 x 2048, FP32, 180 us (1.53
+// PFLOP/s).  Capped, the large ones take up to 370 and 205.
 //
 // Warps: 0 TMA producer, 1 MMA issuer (of the leader CTA), 2 for the gradient one that
 // zeroes, 4 to 11 epilogue (with four, 4148 rows of 17 groups by 1360 x 152 took

@@ -5,12 +5,16 @@
 // stage) whose contraction goes on, for each adapter among the tile's rows, over
 // its rank values: A is then t in parts, B the adapter's factor, and the lanes
 // of other adapters' rows are masked out.  An adapter of rank 64 costs two more
-// K steps (of 64 at K = 4096) in the tiles that have it, and Y is written
-// once.  Bound by the tensor cores as the shared product alone: 8192 rows of 12
-// adapters of rank 64 by 4096 x 4096, BF16, 151 us (1.86 PFLOP/s).
+// K steps (of 64 at K = 4096; four with rank values in three parts) in the tiles that
+// have it, and Y is written once.  Every 1024 inputs the accumulator is added to sums in
+// the epilogue's registers (see grouped_tc.cuh; 171 us without, 174 so, rank values
+// included).  Bound by the tensor cores as the shared product alone: 8192 rows of 12
+// adapters of rank 64 by 4096 x 4096, BF16, not power-capped, 159 us (1.77 PFLOP/s).
 //
 // Of FP16 operands, a warp of each CTA splits its half of a factor in two in shared
-// memory (lora_tc.cuh) before the step counts as loaded.
+// memory (lora_tc.cuh) before the step counts as loaded: 210 us for the same call of
+// 174 (five instructions for 16 rank values instead of two, and four steps of rank 64
+// instead of two).
 //
 // Launched as a programmatic dependent of the kernel that makes the rank values: it
 // waits for them only when the first tile's shared product has been issued.

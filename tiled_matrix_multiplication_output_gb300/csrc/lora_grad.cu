@@ -12,7 +12,7 @@
 // sequences are short, the zeroing, 0.8 us a step for two warps, so that four pairs of
 // them work on the stages of the ring (3237 rows in runs of 59 by 1248 and 472 columns:
 // a call 42 us with one pair, 34 with four).  4096 rows of 6 adapters, rank 16, both
-// gradients of 4096 columns: 27 us, 10 of them HBM's.
+// gradients of 4096 columns: 26 us, 10 of them HBM's.
 //
 // Launched as a programmatic dependent of the product that uses the same rank
 // values, of which it needs nothing: it starts where that one's last tiles leave SMs

@@ -12,8 +12,8 @@
 // makes the rank values, and small enough to share an SM with it: the shared
 // product's weights are read while the rank values are still being summed, and so
 // are the adapters' factors, as each CTA makes its tile's plan itself.  64 rows of
-// 64 adapters (4096 x 4096, rank 16, BF16): 21 us for both, 16 of them this kernel,
-// for 43 MB.
+// 64 adapters (4096 x 4096, rank 16, BF16): 22 us for both, 16 of them this kernel,
+// for 43 MB (FP16, whose factors a warp splits in two: 26 to 29).
 //
 // For few it makes the rank values itself (OWN): the first factors F of up to eight
 // adapters come with the K steps of W, and X is multiplied by both; the shares of a
