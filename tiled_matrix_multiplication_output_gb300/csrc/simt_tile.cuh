@@ -93,7 +93,8 @@ __device__ __forceinline__ int simt_col() { return 4 * (threadIdx.x % 16); }
 // values a thread the loads from shared memory, not the multiply-adds, set the
 // pace.  The tile is small because an SM that gets one more than others takes as
 // much longer: 999 rows of eight groups by 512 x 768 took 63 us in 160 tiles of
-// 64 x 64, three of which met on one SM, and take 33 so (24 TFLOP/s).
+// 64 x 64, three of which met on one SM, and take 33 so (24 TFLOP/s; 8192 rows of eight
+// by 2048 x 2048, where a larger tile would do better, 33).
 template <typename KeepA, typename KeepB>
 __device__ __forceinline__ void simt_accumulate(SimtValues& acc, SimtSmem& smem, const View& a, const View& b,
                                                 int k0, int k1, KeepA keep_a, KeepB keep_b)
