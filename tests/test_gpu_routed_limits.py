@@ -352,3 +352,36 @@ def test_split_factors_and_segments_repeat(dtype, rows, N, K, G, rank):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, (c.forward(), *c.backward())))
     assert all(torch.equal(a, b) for a, b in zip(first, held))
+
+
+@pytest.mark.parametrize("rows,N,K", [(200, 136, 264), (2100, 2056, 264)])
+@pytest.mark.parametrize("rank", [16, 40])
+def test_fp16_parts_of_the_gradients_alone(rows, N, K, rank):
+    """From C, any of the three results may be left out, and with it one of the two sets of
+    rank values towards the input."""
+    c = Case(rows, N, K, 3, rank, "f16", "mixed")
+    want = c.backward()
+    lora = tg.LoraAdapters(c.a.data_ptr(), K, rank * K, c.b.data_ptr(), rank, N * rank, c.scale.data_ptr(), 3, rank)
+    args = (c.dy.data_ptr(), N, c.x.data_ptr(), K, c.w.data_ptr(), K, lora)
+    size = tg.gemm_lora_backward_workspace_size(*args, rows, N, K, tg.F16, tg.F32, tg.F32)
+    for keep in ([0], [1], [2], [1, 2], [0, 2], [0, 1]):
+        got = [torch.full_like(t, 9.0) for t in want]
+        p = [t.data_ptr() if i in keep else None for i, t in enumerate(got)]
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        rc = tg.gemm_lora_backward(*args, c.adapter.data_ptr(), p[0], K, p[1], K, rank * K, p[2], rank, N * rank, rows,
+                                   N, K, tg.F16, tg.F32, tg.F32, ws.data_ptr(), size,
+                                   torch.cuda.current_stream().cuda_stream)
+        assert rc == tg.binding.OK
+        for i, t in enumerate(got):
+            assert torch.equal(t, want[i]) if i in keep else (t == 9.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [20, 200, 1400])
+def test_one_pair_of_factors_for_every_adapter(dtype, rows):
+    """Expanded factors (no stride from one adapter to the next), with scales of their own."""
+    N, K = 1304, 264
+    c = Case(rows, N, K, 5, 24, dtype, "mixed")
+    c.a, c.b = c.a[:1].expand(5, 24, K), c.b[:1].expand(5, N, 24)
+    c.check_forward(c.forward())
+    c.check_backward(c.backward())

@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(ST_THREADS) lora_expand_kernel(const LoraLaunc
 
 // Sixteen rows at a time, so that rows of other adapters between cost a look only: no
 // copy is ahead of its use here, and the warps' sums are added for every sixteen.
-// (1000 rows of four adapters by 1024 and 768 columns, rank 16: most of the backward
-// pass's 270 us.)
+// (1000 rows of four adapters by 1024 and 768 columns, rank 16: the backward pass 270
+// us, the forward one 131.)
 template <typename OutT>
 __global__ void __launch_bounds__(ST_THREADS) lora_grad_kernel(const LoraGradLaunch l)
 {
