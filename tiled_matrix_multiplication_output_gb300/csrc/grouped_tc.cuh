@@ -391,45 +391,40 @@ __global__ void __launch_bounds__(GroupedLayout<MODE>::THREADS, 1)
                     if (w.k_blocks == 0)
                         continue;
                     const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
-                    uint32_t d_tmem = 0;
-                    int of_segment = 0;
-                    for (int kb = 0; kb < w.k_blocks; ++kb) {
-                        const bool first = of_segment == 0;
-                        const bool last = kb == w.k_blocks - 1 ||
-                                          of_segment == (WGRAD ? GT_SEGMENT : p.segment) - 1;
-                        of_segment = last ? 0 : of_segment + 1;
-                        if (first) {
-                            ok = warp_wait<true>(tempty_bar(local & 1), ((local >> 1) & 1) ^ 1, watch);
-                            d_tmem = tmem_base + static_cast<uint32_t>((local & 1) * GT_N);
-                        }
-                        ok = ok && warp_wait<WGRAD>(full_bar(stage), phase, watch);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        const uint32_t a0 = sbase + stage * stage_bytes, b0 = a0 + GT_A_BYTES;
-                        // 16-deep instructions; gradient: as many as there are rows
-                        const int deep = WGRAD ? min(4, (w.rows - kb * TC_BK + 15) / 16) : 4;
-                        if (elect_one()) {
-    #pragma unroll
-                            for (int k = 0; k < TC_BK / TC_UMMA_K; ++k) {
-                                if (WGRAD && k >= deep)
-                                    break;
-                                const uint64_t adesc = A_MN ? smem_desc_sw128(a0 + k * 2048, 8192, 1024)
-                                                            : smem_desc_sw128(a0 + k * 32, 16, 1024);
-                                const uint64_t bdesc = WGRAD ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
-                                                             : smem_desc_sw128(b0 + k * 32, 16, 1024);
-                                tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, !first || k != 0);
+                    for (int kb = 0; ok && kb < w.k_blocks;) {  // by segments: a loop with one accumulator
+                        ok = warp_wait<true>(tempty_bar(local & 1), ((local >> 1) & 1) ^ 1, watch);
+                        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((local & 1) * GT_N);
+                        const int begin = kb, end = min(kb + (WGRAD ? GT_SEGMENT : p.segment), w.k_blocks);
+                        for (; ok && kb < end; ++kb) {
+                            ok = warp_wait<WGRAD>(full_bar(stage), phase, watch);
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                            const uint32_t a0 = sbase + stage * stage_bytes, b0 = a0 + GT_A_BYTES;
+                            // 16-deep instructions; gradient: as many as there are rows
+                            const int deep = WGRAD ? min(4, (w.rows - kb * TC_BK + 15) / 16) : 4;
+                            if (elect_one()) {
+#pragma unroll
+                                for (int k = 0; k < TC_BK / TC_UMMA_K; ++k) {
+                                    if (WGRAD && k >= deep)
+                                        break;
+                                    const uint64_t adesc = A_MN ? smem_desc_sw128(a0 + k * 2048, 8192, 1024)
+                                                                : smem_desc_sw128(a0 + k * 32, 16, 1024);
+                                    const uint64_t bdesc = WGRAD ? smem_desc_sw128(b0 + k * 2048, 8192, 1024)
+                                                                 : smem_desc_sw128(b0 + k * 32, 16, 1024);
+                                    tc_mma_f16<2>(d_tmem, adesc, bdesc, idesc, kb != begin || k != 0);
+                                }
+                                tc_commit_pair(empty_bar(stage), 0x3);
+                                if (kb == end - 1)
+                                    tc_commit_pair(tfull_bar(local & 1), 0x3);
                             }
-                            tc_commit_pair(empty_bar(stage), 0x3);
-                            if (last)
-                                tc_commit_pair(tfull_bar(local & 1), 0x3);
+                            __syncwarp();
+                            if (++stage == stages) {
+                                stage = 0;
+                                phase ^= 1;
+                            }
                         }
-                        __syncwarp();
-                        local += last;
-                        if (++stage == stages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+                        ++local;
                     }
                 }
                 // Wait (bounded) until every MMA issued so far has completed, so

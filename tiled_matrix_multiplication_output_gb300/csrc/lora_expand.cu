@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
             int stage = 0, sub = 0;
             uint32_t phase = 0;
             int issued[L::STEPS];
-    #pragma unroll
+#pragma unroll
             for (int s = 0; s < L::STEPS; ++s)
                 issued[s] = 0;
             uint32_t to_split = 0, parity = 0;  // steps that last landed on their own barrier; how often
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
                 }
             };
             auto count = [&](int at) {
-    #pragma unroll
+#pragma unroll
                 for (int s = 0; s < L::STEPS; ++s)  // (registers: no indexing)
                     issued[s] += s == at;
             };
